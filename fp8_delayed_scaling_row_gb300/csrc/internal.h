@@ -172,4 +172,17 @@ bool ln_linear_small_fits(int64_t M, int64_t K, int64_t N);
 lnfp8_status ln_linear_small_launch(const SmallLinearArgs& a, int dtype, cudaStream_t st);
 lnfp8_status selftest_timeout_launch(int64_t limit_ns, cudaStream_t st);
 
+// 16/32-bit operators (arguments checked and strides filled in by ops_api.cu).
+int64_t layernorm_max_d();
+int64_t layernorm_bwd_ws_bytes(int64_t M, int64_t D);
+lnfp8_status layernorm_fwd_launch(const lnfp8_layernorm_fwd_args* a, cudaStream_t st);
+lnfp8_status layernorm_bwd_launch(const lnfp8_layernorm_bwd_args* a, cudaStream_t st);
+lnfp8_status act_ckpt_save_launch(const void* x, int elem, int64_t rows, int64_t cols, int64_t ldx, const lnfp8_ckpt& c,
+                                  cudaStream_t st);
+lnfp8_status act_ckpt_restore_launch(const lnfp8_ckpt& c, int64_t rows, int64_t cols, int act, const void* gamma,
+                                     const void* beta, int param_elem, void* out, int elem, int64_t ldo, cudaStream_t st);
+// Column sums of n partial rows of `cols` floats in a fixed order; column c goes to a[c], or
+// from `split` on to b[c - split].
+lnfp8_status colsum_launch(const float* part, int n, int cols, int split, float* a, float* b, cudaStream_t st);
+
 }  // namespace lnfp8

@@ -1,0 +1,141 @@
+// Element types, 8-bit checkpoint blocks and activations shared by the 16/32-bit
+// row kernels (layernorm_rows.cu, act_ckpt.cu) and the linear layer (linear.cu).
+//
+// A checkpoint keeps each 32 consecutive columns of a row as FP8 codes and one
+// scale byte b: value = code * 2^(b - 127), with b the least byte for which the
+// block's largest magnitude, divided by 2^(b - 127), does not pass the format's
+// largest value. The scale is a power of two, so dividing and multiplying by it
+// is exact and the code's own rounding (half a step, 2^-4 relative for E4M3,
+// 2^-3 for E5M2) is the only one. A block with an Inf or NaN has b = 255 and
+// restores as NaN throughout.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace lnfp8 {
+
+template <int ELEM>
+struct ElemSize {
+  static constexpr int value = ELEM == LNFP8_FP32 ? 4 : 2;
+};
+
+template <int ELEM>
+__device__ __forceinline__ float load_elem(const void* p, int64_t i) {
+  if constexpr (ELEM == LNFP8_FP32) return reinterpret_cast<const float*>(p)[i];
+  else if constexpr (ELEM == LNFP8_FP16) return __half2float(reinterpret_cast<const __half*>(p)[i]);
+  else return bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(p)[i]);
+}
+
+// Parameter vectors (gamma, beta) come in a type of their own, read a few times per block.
+__device__ __forceinline__ float load_elem_rt(const void* p, int elem, int64_t i) {
+  if (elem == LNFP8_FP32) return load_elem<LNFP8_FP32>(p, i);
+  if (elem == LNFP8_FP16) return load_elem<LNFP8_FP16>(p, i);
+  return load_elem<LNFP8_BF16>(p, i);
+}
+
+template <int ELEM>
+__device__ __forceinline__ void store_elem(void* p, int64_t i, float v) {
+  if constexpr (ELEM == LNFP8_FP32) reinterpret_cast<float*>(p)[i] = v;
+  else if constexpr (ELEM == LNFP8_FP16) reinterpret_cast<__half*>(p)[i] = __float2half_rn(v);
+  else reinterpret_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+}
+
+// v as it is after being stored in the type (nearest even) and read back.
+template <int ELEM>
+__device__ __forceinline__ float round_elem(float v) {
+  if constexpr (ELEM == LNFP8_FP32) return v;
+  else if constexpr (ELEM == LNFP8_FP16) return __half2float(__float2half_rn(v));
+  else return __bfloat162float(__float2bfloat16_rn(v));
+}
+
+// The largest finite value of the type.
+template <int ELEM>
+__device__ __forceinline__ float elem_max() {
+  if constexpr (ELEM == LNFP8_FP32) return __uint_as_float(0x7F7FFFFFu);
+  else if constexpr (ELEM == LNFP8_FP16) return 65504.0f;
+  else return __uint_as_float(0x7F7F0000u);
+}
+
+// ------------------------------------------------------------ checkpoint blocks
+// The scale byte of a block whose largest |v| has these fp32 bits (NaN > Inf > finite):
+// the largest value of the format is 1.75 * 2^top, top = 8 (E4M3) or 15 (E5M2).
+template <int DT>
+__device__ __forceinline__ uint32_t ckpt_byte(uint32_t amax_bits) {
+  constexpr int top = DT == LNFP8_E4M3 ? 8 : 15;
+  const int e = (int)(amax_bits >> 23);
+  if (e == 255) return 255u;
+  const int b = e - top + ((amax_bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return b < 0 ? 0u : (uint32_t)b;
+}
+
+// 2^(127 - b), the factor of the codes (b <= 247 unless the block is not finite: then NaN).
+__device__ __forceinline__ float ckpt_inv_scale(uint32_t b) {
+  return __uint_as_float(b == 255u ? 0x7FFFFFFFu : (254u - b) << 23);
+}
+
+// 2^(b - 127); b = 0 is the fp32 subnormal 2^-127, b = 255 NaN.
+__device__ __forceinline__ float ckpt_scale(uint32_t b) {
+  return __uint_as_float(b == 0u ? 0x00400000u : b == 255u ? 0x7FFFFFFFu : b << 23);
+}
+
+// Two codes (low byte first) -> two fp32, exactly (both formats are subsets of fp16).
+template <int DT>
+__device__ __forceinline__ float2 fp8x2_to_f32(uint32_t codes) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, DT == LNFP8_E4M3 ? __NV_E4M3 : __NV_E5M2);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// A restored value: code * 2^e, kept inside the type (a block whose largest value
+// rounded up past the type's range saturates; NaN stays).
+template <int ELEM>
+__device__ __forceinline__ float ckpt_clamp(float v) {
+  const float m = elem_max<ELEM>();
+  return v > m ? m : v < -m ? -m : v;
+}
+
+// ------------------------------------------------------------ activations
+// GELU is the tanh form, written with the logistic function s(u) = 1/(1 + e^-u):
+//   gelu(z) = z s(u), u = 2 sqrt(2/pi) (z + c z^3);  gelu'(z) = s + z s (1 - s) u'
+// silu(z) = z s(z); silu'(z) = s + z s (1 - s). ex2.approx and rcp.approx keep
+// s to about 2^-22 relative, also in the tails, where 1 + tanh would cancel.
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kGelu2K = 1.5957691216057308f;  // 2 sqrt(2/pi)
+constexpr float kGelu2KC = kGelu2K * 0.044715f;
+
+__device__ __forceinline__ float ex2_fast(float x) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// s(u) from -u log2(e)
+__device__ __forceinline__ float logistic_neg2(float nu) { return rcp_fast(1.0f + ex2_fast(nu)); }
+
+__device__ __forceinline__ float act_fwd(float z, int act) {
+  if (act == LNFP8_ACT_GELU) return z * logistic_neg2(z * (-kLog2e * kGelu2K - kLog2e * kGelu2KC * (z * z)));
+  if (act == LNFP8_ACT_SILU) return z * logistic_neg2(-kLog2e * z);
+  if (act == LNFP8_ACT_RELU) return z > 0.f ? z : (z != z ? z : 0.f);
+  return z;
+}
+
+__device__ __forceinline__ float act_slope(float z, int act) {
+  if (act == LNFP8_ACT_GELU) {
+    const float z2 = fminf(z * z, 1e30f);  // finite, so that the vanished s (1 - s) wins far out
+    const float s = logistic_neg2(z * (-kLog2e * kGelu2K - kLog2e * kGelu2KC * z2));
+    return s + z * (s * (1.0f - s)) * (kGelu2K + 3.0f * kGelu2KC * z2);
+  }
+  if (act == LNFP8_ACT_SILU) {
+    const float s = logistic_neg2(-kLog2e * z);
+    return s + z * (s * (1.0f - s));
+  }
+  if (act == LNFP8_ACT_RELU) return z > 0.f ? 1.0f : 0.f;
+  return 1.0f;
+}
+
+}  // namespace lnfp8

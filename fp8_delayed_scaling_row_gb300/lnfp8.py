@@ -6,7 +6,8 @@ the shared library has not been built, importing this module raises.
 
 Names follow the C ABI: lnfp8_meta_init, amax_history_update, fp8_quantize,
 ln_fwd_cast, ln_bwd, fp8_gemm, ln_linear_fwd / ln_linear_bwd,
-ln_mlp_fwd / ln_mlp_bwd.
+ln_mlp_fwd / ln_mlp_bwd; and, for what a model keeps in 16 or 32 bits,
+layernorm_fwd / layernorm_bwd and act_ckpt_save / act_ckpt_restore.
 """
 from __future__ import annotations
 
@@ -33,7 +34,8 @@ EXPORTED = [
     "fp8_quantize", "fp8_weight_quantize", "ln_fwd_cast", "ln_bwd", "fp8_gemm", "ln_linear_fwd", "ln_linear_bwd",
     "ln_linear_bwd_noalloc", "ln_mlp_fwd", "ln_mlp_bwd", "lnfp8_gemm_workspace_size",
     "lnfp8_ln_linear_bwd_workspace_size", "lnfp8_ln_mlp_bwd_workspace_size", "lnfp8_ln_mlp_fwd_workspace_size",
-    "lnfp8_ctx_bytes", "lnfp8_ctx_offsets",
+    "lnfp8_ctx_bytes", "lnfp8_ctx_offsets", "lnfp8_act_ckpt_scale_pitch", "act_ckpt_save", "act_ckpt_restore",
+    "layernorm_fwd", "layernorm_bwd", "lnfp8_layernorm_bwd_workspace_size",
 ]
 OP_LN_LINEAR, OP_LINEAR, OP_LN_MLP = 0, 1, 2
 
@@ -92,6 +94,23 @@ class CLnMlpBwd(C.Structure):
                 ("defer_update", C.c_int), ("dh_debug", _P), ("gemm_ws", _P), ("gemm_ws_bytes", _I64)]
 
 
+class CCkpt(C.Structure):
+    _fields_ = [("codes", _P), ("scales", _P), ("dtype", C.c_int)]
+
+
+class CLayerNormFwd(C.Structure):
+    _fields_ = [("M", _I64), ("D", _I64), ("elem", C.c_int), ("param_elem", C.c_int), ("x", _P), ("residual", _P),
+                ("gamma", _P), ("beta", _P), ("y", _P), ("x_sum", _P), ("mu", _P), ("rsigma", _P), ("ckpt", CCkpt),
+                ("ldx", _I64), ("ld_residual", _I64), ("ldy", _I64), ("eps", C.c_float)]
+
+
+class CLayerNormBwd(C.Structure):
+    _fields_ = [("M", _I64), ("D", _I64), ("elem", C.c_int), ("param_elem", C.c_int), ("dy", _P), ("x", _P), ("mu", _P),
+                ("rsigma", _P), ("ckpt", CCkpt), ("gamma", _P), ("dresidual", _P), ("dx", _P), ("dgamma", _P),
+                ("dbeta", _P), ("workspace", _P), ("workspace_bytes", _I64), ("ld_dy", _I64), ("ldx", _I64),
+                ("ld_dresidual", _I64), ("ld_dx", _I64)]
+
+
 def _sig(name, args, res=C.c_int):
     f = getattr(_lib, name)
     f.argtypes = args
@@ -131,6 +150,12 @@ _c_lin_bwd = _sig("ln_linear_bwd", [C.POINTER(CLnLinearBwd), _P])
 _c_lin_bwd_noalloc = _sig("ln_linear_bwd_noalloc", [C.POINTER(CLnLinearBwd), _P])
 _c_mlp_fwd = _sig("ln_mlp_fwd", [C.POINTER(CLnMlpFwd), _P])
 _c_mlp_bwd = _sig("ln_mlp_bwd", [C.POINTER(CLnMlpBwd), _P])
+_c_ckpt_save = _sig("act_ckpt_save", [_P, C.c_int, _I64, _I64, _I64, C.POINTER(CCkpt), _P])
+_c_ckpt_restore = _sig("act_ckpt_restore", [C.POINTER(CCkpt), _I64, _I64, C.c_int, _P, _P, C.c_int, _P, C.c_int, _I64, _P])
+_c_ckpt_pitch = _sig("lnfp8_act_ckpt_scale_pitch", [_I64], C.c_int64)
+_c_layernorm_fwd = _sig("layernorm_fwd", [C.POINTER(CLayerNormFwd), _P])
+_c_layernorm_bwd = _sig("layernorm_bwd", [C.POINTER(CLayerNormBwd), _P])
+_c_layernorm_bwd_ws = _sig("lnfp8_layernorm_bwd_workspace_size", [_I64, _I64], C.c_int64)
 
 
 def _check(st: int) -> None:
@@ -599,4 +624,217 @@ def ln_mlp_bwd(dy, x, gamma, ctx: MlpCtx, meta: ScalingMeta, recipe: Recipe, *, 
                   defer_update=int(defer_update), dh_debug=_ptr(g.dh_debug), gemm_ws=_ptr(g.gemm_ws),
                   gemm_ws_bytes=g.gemm_ws.numel() if g.gemm_ws is not None else 0)
     _check(_c_mlp_bwd(C.byref(a), _stream(stream)))
+    return g
+
+
+# ------------------------------------------------------------------ 16- and 32-bit operators
+_ELEM = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+ACTS = {"none": 0, "gelu": 1, "relu": 2, "silu": 3}
+_NO_CKPT = CCkpt(None, None, 0)
+
+
+def _elem(t, name, kinds=_ELEM) -> int:
+    e = kinds.get(t.dtype)
+    if e is None:
+        raise TypeError(f"{name} is {t.dtype}: expected one of {', '.join(str(k) for k in kinds)}")
+    return e
+
+
+def _act(act) -> int:
+    if act not in ACTS:
+        raise ValueError(f"unknown activation {act!r}: one of {', '.join(ACTS)}")
+    return ACTS[act]
+
+
+def _here(t, name) -> None:
+    if not t.is_cuda:
+        raise TypeError(f"{name} is not a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _rows(t, name, rows, cols, dtype) -> int:
+    """Checks a [rows, cols] tensor whose rows are contiguous; returns its row stride."""
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}: expected ({rows}, {cols})")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} is {t.dtype}: expected {dtype}")
+    _here(t, name)
+    s0, s1 = t.stride()
+    if (cols > 1 and s1 != 1) or (rows > 1 and s0 < cols):
+        raise ValueError(f"{name} has strides {(s0, s1)}: rows must be contiguous and not overlap")
+    return s0 if rows > 1 else cols
+
+
+def _flat(t, name, shape, dtype) -> None:
+    """Checks a contiguous tensor of the given shape and type."""
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}: expected {shape}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} is {t.dtype}: expected {dtype}")
+    _here(t, name)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+
+
+class _On:
+    """Allocations of a call belong to the stream that it runs on."""
+
+    def __init__(self, stream):
+        self.ctx = torch.cuda.stream(stream) if stream is not None else None
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+@dataclass
+class ActCkpt:
+    """An 8-bit checkpoint of a [rows, cols] tensor: FP8 codes [rows, cols] uint8 and, per 32
+    columns of a row, a scale byte b (value = code * 2^(b - 127)) in scales [rows, 4 ceil(cols / 128)]."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    dtype: int = E4M3
+
+    @property
+    def shape(self):
+        return self.codes.shape
+
+    def c(self, rows, cols, name="ckpt") -> CCkpt:
+        _flat(self.codes, name + ".codes", (rows, cols), torch.uint8)
+        _flat(self.scales, name + ".scales", (rows, (cols + 127) // 128 * 4), torch.uint8)
+        return CCkpt(self.codes.data_ptr(), self.scales.data_ptr(), self.dtype)
+
+
+def act_ckpt_scale_pitch(cols) -> int:
+    return int(_c_ckpt_pitch(cols))
+
+
+def act_ckpt(rows, cols, *, dtype=E4M3, device="cuda") -> ActCkpt:
+    """An uninitialised checkpoint of a [rows, cols] tensor."""
+    return ActCkpt(_e((rows, cols), torch.uint8, device), _e((rows, (cols + 127) // 128 * 4), torch.uint8, device), dtype)
+
+
+def act_ckpt_save(x, *, dtype=E4M3, ckpt: ActCkpt | None = None, stream=None) -> ActCkpt:
+    """Saves a 2-D bf16, fp16 or fp32 tensor as an 8-bit checkpoint (into `ckpt` if given, in its format)."""
+    elem = _elem(x, "x")
+    if x.dim() != 2:
+        raise ValueError(f"x has shape {tuple(x.shape)}: expected two dimensions")
+    rows, cols = x.shape
+    ldx = _rows(x, "x", rows, cols, x.dtype)
+    with _On(stream):
+        ckpt = ckpt if ckpt is not None else act_ckpt(rows, cols, dtype=dtype, device=x.device)
+        _check(_c_ckpt_save(x.data_ptr(), elem, rows, cols, ldx, C.byref(ckpt.c(rows, cols)), _stream(stream)))
+    return ckpt
+
+
+def act_ckpt_restore(ckpt: ActCkpt, *, out_dtype=torch.bfloat16, act="none", gamma=None, beta=None, out=None,
+                     stream=None) -> torch.Tensor:
+    """The checkpoint's values, or act(values), or values * gamma + beta per column (a LayerNorm's
+    output from its checkpointed rows). Values beyond the type's range saturate."""
+    rows, cols = ckpt.codes.shape
+    cc = ckpt.c(rows, cols)
+    pe = 0
+    if gamma is not None and beta is not None:
+        pe = _elem(gamma, "gamma")
+        _flat(gamma, "gamma", (cols,), gamma.dtype)
+        _flat(beta, "beta", (cols,), gamma.dtype)
+    with _On(stream):
+        out = out if out is not None else _e((rows, cols), out_dtype, ckpt.codes.device)
+        elem = _elem(out, "out")
+        ldo = _rows(out, "out", rows, cols, out.dtype)
+        _check(_c_ckpt_restore(C.byref(cc), rows, cols, _act(act), _ptr(gamma), _ptr(beta), pe, out.data_ptr(), elem,
+                               ldo, _stream(stream)))
+    return out
+
+
+@dataclass
+class LayerNormCtx:
+    """What a LayerNorm's backward needs: rsigma, and the normalised input x (the sum, after a
+    fused residual) with mu, or the checkpoint of the normalised rows."""
+    x: torch.Tensor | None
+    mu: torch.Tensor | None
+    rsigma: torch.Tensor
+    ckpt: ActCkpt | None = None
+
+
+def layernorm_fwd(x, gamma, beta, *, eps=1e-5, residual=None, ckpt=False, y=None, stream=None):
+    """LayerNorm of a 2-D bf16, fp16 or fp32 tensor, output of the same type; returns (y, ctx).
+    gamma and beta are of one type, any of the three. residual: h = x + residual (rounded to the
+    type) is normalised and returned as ctx.x. ckpt: True (E4M3) or an ActCkpt to fill; the
+    normalised rows are kept in 8 bits and the backward reads those, so x may be dropped."""
+    elem, pe = _elem(x, "x"), _elem(gamma, "gamma")
+    if x.dim() != 2:
+        raise ValueError(f"x has shape {tuple(x.shape)}: expected two dimensions")
+    M, D = x.shape
+    dt, dev = x.dtype, x.device
+    ldx = _rows(x, "x", M, D, dt)
+    _flat(gamma, "gamma", (D,), gamma.dtype)
+    _flat(beta, "beta", (D,), gamma.dtype)
+    ldr = _rows(residual, "residual", M, D, dt) if residual is not None else 0
+    with _On(stream):
+        y = y if y is not None else _e((M, D), dt, dev)
+        ldy = _rows(y, "y", M, D, dt)
+        mu, rs = _e((M,), torch.float32, dev), _e((M,), torch.float32, dev)
+        h = _e((M, D), dt, dev) if residual is not None else x
+        if ckpt is True:
+            ckpt = act_ckpt(M, D, device=dev)
+        elif ckpt is False:
+            ckpt = None
+        a = CLayerNormFwd(M, D, elem, pe, x.data_ptr(), _ptr(residual), gamma.data_ptr(), beta.data_ptr(), y.data_ptr(),
+                          h.data_ptr() if residual is not None else None, mu.data_ptr(), rs.data_ptr(),
+                          ckpt.c(M, D) if ckpt is not None else _NO_CKPT, ldx, ldr, ldy, eps)
+        _check(_c_layernorm_fwd(C.byref(a), _stream(stream)))
+    return y, LayerNormCtx(h, mu, rs, ckpt)
+
+
+@dataclass
+class LayerNormGrads:
+    dx: torch.Tensor
+    dgamma: torch.Tensor
+    dbeta: torch.Tensor
+    workspace: torch.Tensor | None = None
+
+
+def layernorm_bwd_workspace_size(M, D) -> int:
+    return int(_c_layernorm_bwd_ws(M, D))
+
+
+def layernorm_grads(M, D, *, dtype=torch.bfloat16, device="cuda") -> LayerNormGrads:
+    return LayerNormGrads(_e((M, D), dtype, device), _e((D,), torch.float32, device), _e((D,), torch.float32, device),
+                          _e((layernorm_bwd_workspace_size(M, D),), torch.uint8, device))
+
+
+def layernorm_bwd(dy, ctx: LayerNormCtx, gamma, *, dresidual=None, grads: LayerNormGrads | None = None,
+                  stream=None) -> LayerNormGrads:
+    """Gradients of layernorm_fwd: dx (plus dresidual, the residual stream's own gradient), and
+    dgamma, dbeta in fp32 (summed in a fixed order). Reads ctx.ckpt if there is one, else ctx.x."""
+    elem, pe = _elem(dy, "dy"), _elem(gamma, "gamma")
+    if dy.dim() != 2:
+        raise ValueError(f"dy has shape {tuple(dy.shape)}: expected two dimensions")
+    M, D = dy.shape
+    dt = dy.dtype
+    lddy = _rows(dy, "dy", M, D, dt)
+    _flat(gamma, "gamma", (D,), gamma.dtype)
+    _flat(ctx.rsigma, "ctx.rsigma", (M,), torch.float32)
+    if ctx.ckpt is not None:
+        ck, x, mu, ldx = ctx.ckpt.c(M, D), None, None, 0
+    else:
+        ck, x, mu = _NO_CKPT, ctx.x.data_ptr(), ctx.mu.data_ptr()
+        ldx = _rows(ctx.x, "ctx.x", M, D, dt)
+        _flat(ctx.mu, "ctx.mu", (M,), torch.float32)
+    lddr = _rows(dresidual, "dresidual", M, D, dt) if dresidual is not None else 0
+    with _On(stream):
+        g = grads if grads is not None else layernorm_grads(M, D, dtype=dt, device=dy.device)
+        lddx = _rows(g.dx, "grads.dx", M, D, dt)
+        _flat(g.dgamma, "grads.dgamma", (D,), torch.float32)
+        _flat(g.dbeta, "grads.dbeta", (D,), torch.float32)
+        a = CLayerNormBwd(M, D, elem, pe, dy.data_ptr(), x, mu, ctx.rsigma.data_ptr(), ck, gamma.data_ptr(),
+                          _ptr(dresidual), g.dx.data_ptr(), g.dgamma.data_ptr(), g.dbeta.data_ptr(), _ptr(g.workspace),
+                          g.workspace.numel() if g.workspace is not None else 0, lddy, ldx, lddr, lddx)
+        _check(_c_layernorm_bwd(C.byref(a), _stream(stream)))
     return g

@@ -520,6 +520,107 @@ int64_t lnfp8_ctx_bytes(int op, int64_t M, int64_t D, int64_t F);
  * that number plus one. */
 int lnfp8_ctx_offsets(int op, int64_t M, int64_t D, int64_t F, int64_t* offsets, int max_offsets);
 
+/* 16- and 32-bit operators beside the FP8 modules ---------------------------
+ * What a model keeps outside the FP8 modules (TE tutorial, code block 1 module
+ * tour: te.LayerNorm, te.Linear; code block 2: the MiniGPT's final norm and
+ * head): a LayerNorm with 16- or 32-bit output, 8-bit checkpoints of
+ * activations, and a linear layer with bias, activation and residual in its
+ * epilogue, each with its backward.
+ *
+ * Tensors are typed (lnfp8_elem) and row-major; every [rows, cols] tensor that
+ * has an ld argument may have a row stride of its own, in elements (0: cols).
+ * Checkpoints, mu, rsigma, x_sum, h, w, dw and vectors are contiguous. Outputs
+ * must not overlap inputs or each other. Row tensors and vectors of layernorm_*
+ * and act_ckpt_* need the alignment of their element only, and any width;
+ * rows that are multiples of 16 bytes on 16-byte boundaries run faster.
+ * linear_act_* moves its tiles with TMA: 16-byte aligned pointers, K and N
+ * multiples of 8, row strides multiples of 8 elements.
+ * NaN and Inf pass through the arithmetic as IEEE gives them. */
+typedef enum { LNFP8_BF16 = 0, LNFP8_FP16 = 1, LNFP8_FP32 = 2 } lnfp8_elem;
+
+/* Activations: GELU is the tanh form, SILU is z / (1 + e^-z). */
+typedef enum { LNFP8_ACT_NONE = 0, LNFP8_ACT_GELU = 1, LNFP8_ACT_RELU = 2, LNFP8_ACT_SILU = 3 } lnfp8_act;
+
+/* An 8-bit checkpoint of a [rows, cols] tensor: codes [rows, cols], and for each
+ * 32 consecutive columns of a row (the last block of a row may be shorter) one
+ * scale byte b in scales [rows, pitch], pitch = lnfp8_act_ckpt_scale_pitch(cols);
+ * value = code * 2^(b - 127). b is the least byte with max|v| <= fp8_max * 2^(b - 127)
+ * over the block; codes round to nearest even. A block that holds an Inf or NaN
+ * has b = 255 and restores as NaN throughout. The bytes of a scale row past the
+ * last block are neither read nor defined. codes == NULL: no checkpoint.
+ * scales must be 4-byte aligned. */
+typedef struct {
+  uint8_t* codes;
+  uint8_t* scales;
+  int dtype; /* lnfp8_dtype of the codes */
+} lnfp8_ckpt;
+
+/* Bytes per row of a checkpoint's scales: 4 * ceil(cols / 128); -1 for negative cols. */
+int64_t lnfp8_act_ckpt_scale_pitch(int64_t cols);
+
+/* Saves x [rows, cols] (elem, row stride ldx) as a checkpoint. cols >= 1, rows >= 0. */
+lnfp8_status act_ckpt_save(const void* x, int elem, int64_t rows, int64_t cols, int64_t ldx, const lnfp8_ckpt* ckpt,
+                           lnfp8_stream stream);
+
+/* out [rows, cols] (elem, row stride ldo) = f(checkpoint), f one of
+ *   act      the activation (LNFP8_ACT_NONE: the values themselves)
+ *   gamma    with gamma and beta ([cols], param_elem): v * gamma[c] + beta[c]
+ *            (a LayerNorm's output from its checkpointed rows); act must be NONE.
+ * Values beyond the largest finite one of elem saturate; NaN stays. */
+lnfp8_status act_ckpt_restore(const lnfp8_ckpt* ckpt, int64_t rows, int64_t cols, int act, const void* gamma,
+                              const void* beta, int param_elem, void* out, int elem, int64_t ldo, lnfp8_stream stream);
+
+typedef struct {
+  int64_t M, D;          /* rows >= 0, columns 1..16384 */
+  int elem;              /* lnfp8_elem of x, residual, y, x_sum */
+  int param_elem;        /* lnfp8_elem of gamma, beta */
+  const void* x;         /* [M, D] */
+  const void* residual;  /* [M, D] or NULL; then h = T(x + residual) is normalised and written to x_sum */
+  const void* gamma;     /* [D] */
+  const void* beta;      /* [D] */
+  void* y;               /* out [M, D] */
+  void* x_sum;           /* out [M, D] (required with residual) */
+  float* mu;             /* out [M] */
+  float* rsigma;         /* out [M] */
+  lnfp8_ckpt ckpt;       /* out, optional: the normalised rows (h - mu) * rsigma */
+  int64_t ldx, ld_residual, ldy;
+  float eps;             /* >= 0 */
+} lnfp8_layernorm_fwd_args;
+
+/* LayerNorm forward: mu = mean(h), rsigma = 1/sqrt(mean((h - mu)^2) + eps),
+ * y = T((h - mu) * rsigma * gamma + beta), statistics in fp32. */
+lnfp8_status layernorm_fwd(const lnfp8_layernorm_fwd_args* args, lnfp8_stream stream);
+
+typedef struct {
+  int64_t M, D;
+  int elem;               /* of dy, x, dresidual, dx */
+  int param_elem;         /* of gamma */
+  const void* dy;         /* [M, D] */
+  const void* x;          /* [M, D] the normalised input (x, or x_sum); NULL with a checkpoint */
+  const float* mu;        /* [M]; NULL with a checkpoint */
+  const float* rsigma;    /* [M] */
+  lnfp8_ckpt ckpt;        /* the forward's checkpoint instead of x and mu */
+  const void* gamma;      /* [D] */
+  const void* dresidual;  /* [M, D] or NULL: the residual stream's own gradient, added to dx */
+  void* dx;               /* out [M, D] */
+  float* dgamma;          /* out [D] */
+  float* dbeta;           /* out [D] */
+  void* workspace;        /* lnfp8_layernorm_bwd_workspace_size(M, D) bytes, 16-byte aligned */
+  int64_t workspace_bytes;
+  int64_t ld_dy, ldx, ld_dresidual, ld_dx;
+} lnfp8_layernorm_bwd_args;
+
+/* LayerNorm backward: with g = dy * gamma and xhat the normalised rows,
+ * dx = T(rsigma * (g - mean(g) - xhat * mean(g * xhat)) + dresidual),
+ * dgamma = sum_rows dy * xhat, dbeta = sum_rows dy. The column sums are added in
+ * a fixed order: the same call gives the same bits. The workspace need not be
+ * initialised, and may be used for something else once the call has completed
+ * on the stream. */
+lnfp8_status layernorm_bwd(const lnfp8_layernorm_bwd_args* args, lnfp8_stream stream);
+
+/* Bytes of layernorm_bwd's workspace on the current device; -1 for a negative size. */
+int64_t lnfp8_layernorm_bwd_workspace_size(int64_t M, int64_t D);
+
 #ifdef __cplusplus
 }
 #endif
