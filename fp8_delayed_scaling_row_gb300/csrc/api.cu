@@ -331,6 +331,9 @@ lnfp8_status lnfp8_sync_status(lnfp8_stream stream) {
   clear_error();
   unsigned int word = 0;
   TRY(status_read_clear((cudaStream_t)stream, &word));
+  unsigned int lin_word = 0;
+  TRY(lin_status_read_clear(&lin_word));
+  word |= lin_word;
   if (word & kStatusTimeout) return set_error(LNFP8_ERR_TIMEOUT, "a bounded device wait gave up");
   return LNFP8_OK;
 }

@@ -185,4 +185,31 @@ lnfp8_status act_ckpt_restore_launch(const lnfp8_ckpt& c, int64_t rows, int64_t 
 // from `split` on to b[c - split].
 lnfp8_status colsum_launch(const float* part, int n, int cols, int split, float* a, float* b, cudaStream_t st);
 
+// One product of 16-bit matrices on the tensor cores (linear.cu):
+//   out[M, N] = T(act(z) + resid), z = sum_k a[m, k] b[n, k] + bias[n]
+// a_mn / b_mn false: stored [rows, K] (K contiguous); true: stored [K, rows].
+struct LinGemm {
+  int64_t M, N, K;
+  int elem;
+  const void* a;
+  int64_t lda;
+  bool a_mn;
+  const void* b;
+  int64_t ldb;
+  bool b_mn;
+  void* out;
+  int64_t ldo;
+  const void* bias;   // optional from here on
+  int act;
+  const void* resid;
+  int64_t ldr;
+  void* h;            // [M, N] contiguous: T(z)
+  lnfp8_ckpt ckpt;    // z as a checkpoint
+};
+lnfp8_status lin_gemm_launch(const LinGemm& g, cudaStream_t st);
+lnfp8_status lin_status_read_clear(unsigned int* word);
+lnfp8_status linear_act_fwd_launch(const lnfp8_linear_act_fwd_args* a, cudaStream_t st);
+int64_t linear_act_bwd_ws_bytes(int64_t M, int64_t K, int64_t N, bool has_act, bool x_from_ckpt);
+lnfp8_status linear_act_bwd_launch(const lnfp8_linear_act_bwd_args* a, cudaStream_t st);
+
 }  // namespace lnfp8

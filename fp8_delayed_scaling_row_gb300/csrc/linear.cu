@@ -1,0 +1,600 @@
+// The 16-bit linear layer with bias, activation and residual in its epilogue, and
+// its backward (te.Linear outside fp8_autocast, TE tutorial, code blocks 1 and 2:
+// projections and head in 16 bits beside the FP8 modules):
+//   forward   z = x w^T + b, y = T(act(z) + r); z kept as T(z) or as an 8-bit checkpoint
+//   backward  dz = dy act'(h), db = sum_rows dz, dx = T(dz w), dw = T(dz^T x)
+// The products run on the tensor cores (tcgen05, 16-bit operands staged by TMA,
+// fp32 accumulators in tensor memory); the backward reads dz, w and x in the
+// layouts they have (operands may be K-major or MN-major), so nothing is transposed.
+#include <cudaTypedefs.h>
+
+#include "common.cuh"
+#include "internal.h"
+#include "rowmath.cuh"
+#include "tc.cuh"
+
+namespace lnfp8 {
+
+lnfp8_status lin_status_read_clear(unsigned int* word) {
+  const unsigned int zero = 0;
+  if (cudaMemcpyFromSymbol(word, g_tc_status, sizeof(unsigned int)) != cudaSuccess ||
+      (*word && cudaMemcpyToSymbol(g_tc_status, &zero, sizeof(unsigned int)) != cudaSuccess))
+    return check_launch("lnfp8_sync_status: the linear layer's status word");
+  return LNFP8_OK;
+}
+
+namespace {
+
+constexpr int BK = 64;  // 16-bit elements of K per pipeline stage: 128-byte rows
+
+struct EpiParams {
+  int M, N, f16, act, ck;  // ck: -1 none, else the checkpoint's lnfp8_dtype
+  void* out;
+  int64_t ldo;
+  const void* bias;
+  const void* resid;
+  int64_t ldr;
+  void* h;
+  uint8_t* codes;
+  uint8_t* scales;
+  int64_t pitch;
+};
+
+__device__ __forceinline__ uint32_t pack16(float a, float b, int f16) {
+  if (f16) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return pack_bf16x2(a, b);
+}
+__device__ __forceinline__ float2 unpack16(uint32_t w, int f16) {
+  if (f16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint4 pack16x8(const float* v, int f16) {
+  return make_uint4(pack16(v[0], v[1], f16), pack16(v[2], v[3], f16), pack16(v[4], v[5], f16), pack16(v[6], v[7], f16));
+}
+__device__ __forceinline__ void add16x8(float* v, uint4 u, int f16) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = unpack16(w[i], f16);
+    v[2 * i] += p.x;
+    v[2 * i + 1] += p.y;
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ uint2 encode8(const float* v, float inv) {
+  return cvt_fp8x8<DT>(v, inv);
+}
+
+// The epilogue of 8 columns n.. of row m. The four lanes of a checkpoint block (32 columns)
+// are neighbours; every lane of the warp calls it (`ok`: inside the tensor).
+__device__ __forceinline__ void epilogue8(const EpiParams& p, float* v, int m, int n, bool ok) {
+  const int64_t row = m;
+  if (p.bias && ok) add16x8(v, *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.bias) + n), p.f16);
+  if (p.h && ok)
+    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.h) + row * p.N + n) = pack16x8(v, p.f16);
+  if (p.ck >= 0) {
+    uint32_t am = 0;
+    if (ok)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) am = max(am, abs_bits(v[i]));
+    am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
+    am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
+    const uint32_t b = p.ck == LNFP8_E4M3 ? ckpt_byte<LNFP8_E4M3>(am) : ckpt_byte<LNFP8_E5M2>(am);
+    const float inv = ckpt_inv_scale(b);
+    if (ok) {
+      const uint2 c = p.ck == LNFP8_E4M3 ? encode8<LNFP8_E4M3>(v, inv) : encode8<LNFP8_E5M2>(v, inv);
+      *reinterpret_cast<uint2*>(p.codes + row * p.N + n) = c;
+      if ((n & 31) == 0) p.scales[row * p.pitch + (n >> 5)] = (uint8_t)b;
+    }
+  }
+  if (p.act != LNFP8_ACT_NONE)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = act_fwd(v[i], p.act);
+  if (ok) {
+    if (p.resid) add16x8(v, *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.resid) + row * p.ldr + n), p.f16);
+    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + row * p.ldo + n) = pack16x8(v, p.f16);
+  }
+}
+
+// ------------------------------------------------------------ one tile per cluster
+// A cluster of S CTAs computes one tile, each CTA a piece of K with the 1-SM MMA
+// (128 x BN x 16), then the pieces' fp32 sums are read from one another's shared
+// memory and added in rank order, each CTA finishing 1/S of the tile's rows: K is
+// split over S SMs without a workspace, and the result does not depend on timing.
+// SWAP: the 128 accumulator lanes are output features and the BN columns tokens, so
+// that few tokens fill the instruction; else lanes are tokens.
+template <int BN>
+struct TileCfg {
+  static constexpr int P_BYTES = 128 * BK * 2;
+  static constexpr int Q_BYTES = BN * BK * 2;
+  static constexpr int STAGE = P_BYTES + Q_BYTES;
+  static constexpr int STAGES = 196608 / STAGE > 8 ? 8 : 196608 / STAGE;
+  static constexpr int SMEM = 1024 + STAGES * STAGE + 256;
+  static constexpr int TMEM_COLS = BN < 32 ? 32 : BN;
+  static_assert(SMEM <= 232448, "shared memory budget");
+  static_assert(128 * (BN + 4) * 4 <= STAGES * STAGE && BN * 132 * 4 <= STAGES * STAGE, "the fp32 tile reuses the ring");
+};
+
+struct TileParams {
+  EpiParams e;
+  int num_p, num_kb, splits, kb_per_split;
+  uint32_t idesc;
+};
+
+constexpr int kTileThreads = 256;
+
+template <int BN, bool P_MN, bool Q_MN, bool SWAP>
+__global__ void __launch_bounds__(kTileThreads, 1)
+lin_tile_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ, const TileParams p) {
+  using C = TileCfg<BN>;
+  constexpr int STAGES = C::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t ring = smem_u32(smem);
+  const uint32_t bars = ring + STAGES * C::STAGE;  // full[STAGES], empty[STAGES], done
+  volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + STAGES * C::STAGE + 8 * (2 * STAGES + 1));
+  volatile uint32_t* abort_flag = misc;
+  auto full_bar = [&](int s) { return bars + 8u * s; };
+  auto empty_bar = [&](int s) { return bars + 8u * (STAGES + s); };
+  const uint32_t done_bar = bars + 8u * (2 * STAGES);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    mbar_init(done_bar, 1);
+    *abort_flag = 0;
+    mbar_init_fence();
+    tma_prefetch_map(&tmP);
+    tma_prefetch_map(&tmQ);
+  }
+  if (warp == 1) tmem_alloc<false>(smem_u32((const void*)(misc + 1)), C::TMEM_COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc[1];
+  pdl_wait();
+  pdl_launch_dependents();
+
+  const int S = p.splits;
+  const int rank = S > 1 ? (int)cluster_rank() : 0;
+  const int tile = blockIdx.x / S;
+  const int p0 = (tile % p.num_p) * 128, q0 = (tile / p.num_p) * BN;
+  const int kb0 = rank * p.kb_per_split, kb1 = min(p.num_kb, kb0 + p.kb_per_split);
+
+  if (warp == 0 && lane == 0) {
+    int stage = 0;
+    uint32_t phase = 0;
+    int issued = 0;
+    bool ok = true;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!mbar_wait(empty_bar(stage), phase ^ 1, abort_flag)) { ok = false; break; }
+      const uint32_t fb = full_bar(stage), pd = ring + stage * C::STAGE, qd = pd + C::P_BYTES;
+      mbar_expect_tx(fb, C::STAGE);
+      if constexpr (!P_MN) tma_load(pd, &tmP, kb * BK, p0, fb);
+      else {
+        tma_load(pd, &tmP, p0, kb * BK, fb);
+        tma_load(pd + 8192, &tmP, p0 + 64, kb * BK, fb);
+      }
+      if constexpr (!Q_MN) tma_load(qd, &tmQ, kb * BK, q0, fb);
+      else
+#pragma unroll
+        for (int j = 0; j < BN / 64; ++j) tma_load(qd + j * 8192, &tmQ, q0 + 64 * j, kb * BK, fb);
+      ++issued;
+      if (++stage == STAGES) { stage = 0; phase ^= 1; }
+    }
+    if (!ok)
+      for (int i = min(issued, STAGES); i > 0; --i) {  // copies in flight land before the CTA leaves
+        if (--stage < 0) { stage = STAGES - 1; phase ^= 1; }
+        mbar_drain(full_bar(stage), phase);
+      }
+  } else if (warp == 1 && lane == 0) {
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!mbar_wait(full_bar(stage), phase, abort_flag)) break;
+      tc_fence_after();
+      const uint32_t pb = ring + stage * C::STAGE, qb = pb + C::P_BYTES;
+#pragma unroll
+      for (int kk = 0; kk < BK / 16; ++kk) {
+        const uint64_t pd = P_MN ? mat_desc(pb + kk * 2048, 8192, 1024) : mat_desc(pb + kk * 32, 16, 1024);
+        const uint64_t qd = Q_MN ? mat_desc(qb + kk * 2048, 8192, 1024) : mat_desc(qb + kk * 32, 16, 1024);
+        mma_16bit<false>(tmem, pd, qd, p.idesc, kb != kb0 || kk != 0);
+      }
+      mma_commit<false>(empty_bar(stage));
+      if (++stage == STAGES) { stage = 0; phase ^= 1; }
+    }
+    mma_commit<false>(done_bar);  // after an abort too: no MMA outlives the CTA
+  }
+
+  // the fp32 tile, tokens by features, over the ring (every copy and MMA has completed)
+  constexpr int ROWS = SWAP ? BN : 128, COLS = SWAP ? 128 : BN, PITCH = COLS + 4;
+  float* tile_f = reinterpret_cast<float*>(smem);
+  if (warp >= 4) {
+    uint32_t never = 0;
+    mbar_wait(done_bar, 0, &never);
+    tc_fence_after();
+    const int quarter = warp & 3;
+    const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16);
+#pragma unroll 1
+    for (int c = 0; c < BN; c += 16) {
+      uint32_t r[16];
+      if (kb1 > kb0) tmem_ld16(t0 + c, r);
+      else
+#pragma unroll
+        for (int i = 0; i < 16; ++i) r[i] = 0u;
+      if constexpr (SWAP) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) tile_f[(c + i) * PITCH + quarter * 32 + lane] = __uint_as_float(r[i]);
+      } else {
+        uint4* dst = reinterpret_cast<uint4*>(tile_f + (quarter * 32 + lane) * PITCH + c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dst[i] = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+      }
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (S > 1) cluster_sync_all();
+
+  const int rows = ROWS / S;  // of this CTA; a multiple of 32 items in all
+  constexpr int CH = COLS / 8;
+  for (int i = threadIdx.x; i < rows * CH; i += kTileThreads) {
+    const int r = rank * rows + i / CH, c = (i % CH) * 8;
+    float v[8];
+    const uint32_t at = ring + (uint32_t)(r * PITCH + c) * 4u;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = 0.f;
+    for (int s = 0; s < S; ++s) {
+      float4 a, b;
+      if (S > 1) {
+        const uint32_t ra = map_to_rank(at, s);
+        a = ld_cluster_f4(ra);
+        b = ld_cluster_f4(ra + 16);
+      } else {
+        a = *reinterpret_cast<const float4*>(tile_f + r * PITCH + c);
+        b = *reinterpret_cast<const float4*>(tile_f + r * PITCH + c + 4);
+      }
+      v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+      v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+    }
+    const int m = (SWAP ? q0 : p0) + r, n = (SWAP ? p0 : q0) + c;
+    epilogue8(p.e, v, m, n, m < p.e.M && n < p.e.N);
+  }
+  __syncthreads();
+  if (S > 1) cluster_sync_all();  // nobody leaves while its tile may still be read
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_free<false>(tmem, C::TMEM_COLS);
+  }
+}
+
+// ------------------------------------------------------------ dz = dy act'(h), db
+// A block takes 256 columns (32 threads of 8) and `rows_per_block` rows, 8 at a time; each
+// thread keeps the sums of its columns, added over the 8 row lanes at the end.
+struct DactParams {
+  const void* dy;
+  const void* h;
+  const uint8_t* codes;
+  const uint8_t* scales;
+  void* dz;      // NULL: no activation, only the column sums
+  float* part;   // [row blocks][N] or NULL
+  int64_t M, lddy, pitch;
+  int N, act, rows_per_block;
+};
+
+template <int ELEM, int SRC>  // SRC: -2 no activation, -1 h as a tensor, else the checkpoint's format
+__global__ void __launch_bounds__(256) lin_dact_kernel(const DactParams p) {
+  __shared__ float red[8][32][9];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int cl = threadIdx.x & 31, rl = threadIdx.x >> 5;
+  const int c = (blockIdx.x * 32 + cl) * 8;
+  const bool ok = c < p.N;
+  const int64_t r0 = (int64_t)blockIdx.y * p.rows_per_block;
+  const int64_t r1 = min64(p.M, r0 + p.rows_per_block);
+  constexpr int f16 = ELEM == LNFP8_FP16;
+  float acc[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+  if (ok) {
+#pragma unroll 4
+    for (int64_t r = r0 + rl; r < r1; r += 8) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.f;
+      add16x8(v, *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.dy) + r * p.lddy + c), f16);
+      if constexpr (SRC >= -1) {
+        float z[8];
+        if constexpr (SRC == -1) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) z[i] = 0.f;
+          add16x8(z, *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.h) + r * p.N + c), f16);
+        } else {
+          const uint2 q = *reinterpret_cast<const uint2*>(p.codes + r * p.N + c);
+          const float s = ckpt_scale(p.scales[r * p.pitch + (c >> 5)]);
+          const uint32_t w[4] = {q.x & 0xFFFFu, q.x >> 16, q.y & 0xFFFFu, q.y >> 16};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 t = fp8x2_to_f32<SRC>(w[i]);
+            z[2 * i] = t.x * s;
+            z[2 * i + 1] = t.y * s;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= act_slope(z[i], p.act);
+        *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.dz) + r * p.N + c) = pack16x8(v, f16);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] += v[i];
+    }
+  }
+  if (p.part == nullptr) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) red[rl][cl][i] = acc[i];
+  __syncthreads();
+  const int col = threadIdx.x;  // 256 columns
+  float s = 0.f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) s += red[k][col >> 3][col & 7];
+  if (blockIdx.x * 256 + col < p.N) p.part[(int64_t)blockIdx.y * p.N + blockIdx.x * 256 + col] = s;
+}
+
+// ------------------------------------------------------------ host side
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      ptr = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  }();
+  return fn;
+}
+
+// 2-D map over a row-major [outer, inner] tensor of 16-bit elements, row stride ld elements.
+bool make_map(CUtensorMap* tm, const void* base, int64_t inner, int64_t outer, int64_t ld, int box_inner, int box_outer,
+              CUtensorMapSwizzle swz) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
+  cuuint64_t strides[1] = {(cuuint64_t)(ld * 2)};
+  cuuint32_t box[2] = {(cuuint32_t)box_inner, (cuuint32_t)box_outer};
+  cuuint32_t estr[2] = {1u, 1u};
+  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+// An operand of `rows` rows/columns over K: `box_rows` of them per box when K-major, 64 when MN-major.
+bool operand_map(CUtensorMap* tm, const void* base, bool mn, int64_t rows, int64_t K, int64_t ld, int box_rows) {
+  return mn ? make_map(tm, base, rows, K, ld, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B)
+            : make_map(tm, base, K, rows, ld, BK, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// kind::f16: fp32 accumulator, both operands bf16 (1) or fp16 (0).
+uint32_t make_idesc(int elem, int m_mma, int n_mma, bool a_mn, bool b_mn) {
+  const uint32_t t = elem == LNFP8_BF16 ? 1u : 0u;
+  return (1u << 4) | (t << 7) | (t << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+         ((uint32_t)(n_mma >> 3) << 17) | ((uint32_t)(m_mma >> 4) << 24);
+}
+
+EpiParams epi_params(const LinGemm& g) {
+  EpiParams e;
+  e.M = (int)g.M;
+  e.N = (int)g.N;
+  e.f16 = g.elem == LNFP8_FP16;
+  e.act = g.act;
+  e.ck = g.ckpt.codes ? g.ckpt.dtype : -1;
+  e.out = g.out;
+  e.ldo = g.ldo;
+  e.bias = g.bias;
+  e.resid = g.resid;
+  e.ldr = g.ldr;
+  e.h = g.h;
+  e.codes = g.ckpt.codes;
+  e.scales = g.ckpt.scales;
+  e.pitch = lnfp8_act_ckpt_scale_pitch(g.N);
+  return e;
+}
+
+template <int BN, bool P_MN, bool Q_MN, bool SWAP>
+lnfp8_status tile_launch(const LinGemm& g, cudaStream_t st) {
+  using C = TileCfg<BN>;
+  auto k = lin_tile_kernel<BN, P_MN, Q_MN, SWAP>;
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+    return check_launch("linear: shared memory attribute");
+  const int64_t prow = SWAP ? g.N : g.M, qrow = SWAP ? g.M : g.N;
+  const int64_t num_p = (prow + 127) / 128, num_q = (qrow + BN - 1) / BN;
+  TileParams p;
+  p.e = epi_params(g);
+  p.num_p = (int)num_p;
+  p.num_kb = (int)((g.K + BK - 1) / BK);
+  // K pieces: while they run on SMs that would idle and each keeps a few K blocks
+  int S = 1;
+  while (S < 8 && num_p * num_q * S * 2 <= num_sms() && p.num_kb >= S * 2 * 2) S *= 2;
+  p.splits = S;
+  p.kb_per_split = (p.num_kb + S - 1) / S;
+  if (num_p * num_q * S > 0x7FFFFFFF) return set_error(LNFP8_ERR_UNSUPPORTED_SHAPE, "linear: too many tiles");
+  p.idesc = make_idesc(g.elem, 128, BN, P_MN, Q_MN);
+  CUtensorMap tp, tq;
+  const bool ok = SWAP ? operand_map(&tp, g.b, P_MN, g.N, g.K, g.ldb, 128) && operand_map(&tq, g.a, Q_MN, g.M, g.K, g.lda, BN)
+                       : operand_map(&tp, g.a, P_MN, g.M, g.K, g.lda, 128) && operand_map(&tq, g.b, Q_MN, g.N, g.K, g.ldb, BN);
+  if (!ok) return set_error(LNFP8_ERR_CUDA, "linear: cuTensorMapEncodeTiled failed (driver entry point or arguments)");
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = S;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)(num_p * num_q * S));
+  cfg.blockDim = dim3(kTileThreads);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  LaunchScope ls("linear_tile", st);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, tp, tq, p);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return set_error(LNFP8_ERR_CUDA, "linear launch: %s", cudaGetErrorString(e));
+  }
+  return check_launch("linear");
+}
+
+// Rows of the dz pass per block: enough blocks for about four per SM.
+int64_t dact_rows_per_block(int64_t M, int64_t N) {
+  const int64_t col_blocks = (N + 255) / 256;
+  const int64_t row_blocks = max64(1, (int64_t)num_sms() * 4 / col_blocks);
+  const int64_t rows = (M + row_blocks - 1) / row_blocks;
+  return max64(32, (rows + 7) / 8 * 8);
+}
+int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
+
+}  // namespace
+
+lnfp8_status lin_gemm_launch(const LinGemm& g, cudaStream_t st) {
+  if (g.M == 0 || g.N == 0) return LNFP8_OK;
+  const bool swap = g.M <= 64 && !g.a_mn;
+  if (swap && !g.b_mn) {
+    if (g.M <= 16) return tile_launch<16, false, false, true>(g, st);
+    if (g.M <= 32) return tile_launch<32, false, false, true>(g, st);
+    return tile_launch<64, false, false, true>(g, st);
+  }
+  if (swap) {
+    if (g.M <= 16) return tile_launch<16, true, false, true>(g, st);
+    if (g.M <= 32) return tile_launch<32, true, false, true>(g, st);
+    return tile_launch<64, true, false, true>(g, st);
+  }
+  if (!g.a_mn) return g.b_mn ? tile_launch<128, false, true, false>(g, st) : tile_launch<128, false, false, false>(g, st);
+  return tile_launch<128, true, true, false>(g, st);
+}
+
+lnfp8_status linear_act_fwd_launch(const lnfp8_linear_act_fwd_args* a, cudaStream_t st) {
+  LinGemm g = {};
+  g.M = a->M;
+  g.N = a->N;
+  g.K = a->K;
+  g.elem = a->elem;
+  g.a = a->x;
+  g.lda = a->ldx;
+  g.b = a->w;
+  g.ldb = a->K;
+  g.out = a->y;
+  g.ldo = a->ldy;
+  g.bias = a->bias;
+  g.act = a->act;
+  g.resid = a->residual;
+  g.ldr = a->ld_residual;
+  g.h = a->h;
+  g.ckpt = a->ckpt;
+  return lin_gemm_launch(g, st);
+}
+
+// dz [M, N], the restored x [M, K] and the column partials of db, each from a multiple of 256 on.
+int64_t linear_act_bwd_ws_bytes(int64_t M, int64_t K, int64_t N, bool has_act, bool x_from_ckpt) {
+  if (M == 0 || N == 0) return 0;
+  const int64_t rpb = dact_rows_per_block(M, N);
+  return (has_act ? up256(M * N * 2) : 0) + (x_from_ckpt ? up256(M * K * 2) : 0) + up256((M + rpb - 1) / rpb * N * 4);
+}
+
+lnfp8_status linear_act_bwd_launch(const lnfp8_linear_act_bwd_args* a, cudaStream_t st) {
+  if (a->M == 0) {
+    if ((a->dw && cudaMemsetAsync(a->dw, 0, a->N * a->K * 2, st) != cudaSuccess) ||
+        (a->dbias && cudaMemsetAsync(a->dbias, 0, a->N * sizeof(float), st) != cudaSuccess))
+      return check_launch("linear_act_bwd: clearing dw/dbias");
+    return LNFP8_OK;
+  }
+  const bool has_act = a->act != LNFP8_ACT_NONE, xck = a->x_ckpt.codes != nullptr;
+  uint8_t* ws = static_cast<uint8_t*>(a->workspace);
+  void* dz_ws = ws;
+  if (has_act) ws += up256(a->M * a->N * 2);
+  void* x_ws = ws;
+  if (xck) ws += up256(a->M * a->K * 2);
+  const void* dz = has_act ? dz_ws : a->dy;
+  const int64_t lddz = has_act ? a->N : a->ld_dy;
+
+  if (has_act || a->dbias) {
+    DactParams p;
+    p.dy = a->dy;
+    p.h = a->h;
+    p.codes = a->h_ckpt.codes;
+    p.scales = a->h_ckpt.scales;
+    p.dz = dz_ws;
+    p.part = a->dbias ? reinterpret_cast<float*>(ws) : nullptr;
+    p.M = a->M;
+    p.lddy = a->ld_dy;
+    p.pitch = lnfp8_act_ckpt_scale_pitch(a->N);
+    p.N = (int)a->N;
+    p.act = a->act;
+    p.rows_per_block = (int)dact_rows_per_block(a->M, a->N);
+    const int64_t row_blocks = (a->M + p.rows_per_block - 1) / p.rows_per_block;
+    auto go = [&](auto kernel) {
+      LaunchScope ls("linear_dact", st);
+      if (launch_pdl(kernel, dim3((unsigned)((a->N + 255) / 256), (unsigned)row_blocks), dim3(256), 0, st, p) != cudaSuccess)
+        return check_launch("linear_act_bwd launch");
+      return check_launch("linear_act_bwd: dz");
+    };
+    auto pick = [&](auto elem) {
+      constexpr int E = decltype(elem)::value;
+      if (!has_act) return go(lin_dact_kernel<E, -2>);
+      if (!p.codes) return go(lin_dact_kernel<E, -1>);
+      return a->h_ckpt.dtype == LNFP8_E4M3 ? go(lin_dact_kernel<E, LNFP8_E4M3>) : go(lin_dact_kernel<E, LNFP8_E5M2>);
+    };
+    lnfp8_status s = a->elem == LNFP8_BF16 ? pick(std::integral_constant<int, LNFP8_BF16>()) : pick(std::integral_constant<int, LNFP8_FP16>());
+    if (s != LNFP8_OK) return s;
+    if (a->dbias) {
+      s = colsum_launch(p.part, (int)row_blocks, p.N, p.N, a->dbias, nullptr, st);
+      if (s != LNFP8_OK) return s;
+    }
+  }
+  LinGemm g = {};
+  g.elem = a->elem;
+  if (a->dx) {  // [M, K] = dz [M, N] . w, contracted over N
+    g.M = a->M;
+    g.N = a->K;
+    g.K = a->N;
+    g.a = dz;
+    g.lda = lddz;
+    g.b = a->w;
+    g.ldb = a->K;
+    g.b_mn = true;
+    g.out = a->dx;
+    g.ldo = a->ld_dx;
+    const lnfp8_status s = lin_gemm_launch(g, st);
+    if (s != LNFP8_OK) return s;
+  }
+  if (a->dw) {  // [N, K] = dz^T . x, contracted over the tokens
+    const void* x = a->x;
+    int64_t ldx = a->ldx;
+    if (xck) {
+      const lnfp8_status s = act_ckpt_restore_launch(a->x_ckpt, a->M, a->K, a->x_act, a->x_gamma, a->x_beta, a->elem, x_ws, a->elem, a->K, st);
+      if (s != LNFP8_OK) return s;
+      x = x_ws;
+      ldx = a->K;
+    }
+    g.M = a->N;
+    g.N = a->K;
+    g.K = a->M;
+    g.a = dz;
+    g.lda = lddz;
+    g.a_mn = true;
+    g.b = x;
+    g.ldb = ldx;
+    g.b_mn = true;
+    g.out = a->dw;
+    g.ldo = a->K;
+    return lin_gemm_launch(g, st);
+  }
+  return LNFP8_OK;
+}
+
+}  // namespace lnfp8

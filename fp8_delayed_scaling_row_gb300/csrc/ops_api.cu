@@ -34,6 +34,10 @@ lnfp8_status check_elem(int e, const char* name, const char* who) {
   if (e < LNFP8_BF16 || e > LNFP8_FP32) return set_error(LNFP8_ERR_INVALID_ARG, "%s: bad %s %d", who, name, e);
   return LNFP8_OK;
 }
+lnfp8_status check_elem16(int e, const char* who) {
+  if (e != LNFP8_BF16 && e != LNFP8_FP16) return set_error(LNFP8_ERR_INVALID_ARG, "%s: elem %d (bf16 or fp16)", who, e);
+  return LNFP8_OK;
+}
 lnfp8_status check_act(int act, const char* name, const char* who) {
   if (act < LNFP8_ACT_NONE || act > LNFP8_ACT_SILU) return set_error(LNFP8_ERR_INVALID_ARG, "%s: bad %s %d", who, name, act);
   return LNFP8_OK;
@@ -53,6 +57,17 @@ lnfp8_status fill_ld(int64_t* ld, int64_t cols, const char* name, const char* wh
   if (*ld == 0) *ld = cols;
   if (*ld < cols || *ld > (1ll << 40))
     return set_error(LNFP8_ERR_INVALID_ARG, "%s: %s = %lld, rows have %lld columns", who, name, (long long)*ld, (long long)cols);
+  return LNFP8_OK;
+}
+// Feature sizes and row strides of the tensor-core products: 16-byte rows.
+lnfp8_status check_feature(int64_t v, const char* name, const char* who) {
+  if (v < 8 || v % 8 != 0 || v > kMaxCols)
+    return set_error(LNFP8_ERR_UNSUPPORTED_SHAPE, "%s: %s = %lld must be a positive multiple of 8", who, name, (long long)v);
+  return LNFP8_OK;
+}
+lnfp8_status fill_ld8(int64_t* ld, int64_t cols, const char* name, const char* who) {
+  TRY(fill_ld(ld, cols, name, who));
+  if (*ld % 8 != 0) return set_error(LNFP8_ERR_INVALID_ARG, "%s: %s = %lld is not a multiple of 8", who, name, (long long)*ld);
   return LNFP8_OK;
 }
 lnfp8_status check_ckpt(const lnfp8_ckpt& c, int code_align, const char* name, const char* who) {
@@ -178,6 +193,90 @@ lnfp8_status layernorm_bwd(const lnfp8_layernorm_bwd_args* args, lnfp8_stream st
                        (long long)layernorm_bwd_ws_bytes(a.M, a.D));
   }
   return layernorm_bwd_launch(&a, (cudaStream_t)stream);
+}
+
+lnfp8_status linear_act_fwd(const lnfp8_linear_act_fwd_args* args, lnfp8_stream stream) {
+  const char* who = "linear_act_fwd";
+  clear_error();
+  if (!args) return set_error(LNFP8_ERR_INVALID_ARG, "%s: args is NULL", who);
+  lnfp8_linear_act_fwd_args a = *args;
+  TRY(check_elem16(a.elem, who));
+  TRY(check_act(a.act, "act", who));
+  TRY(check_rows(a.M, "M", who));
+  TRY(check_feature(a.K, "K", who));
+  TRY(check_feature(a.N, "N", who));
+  TRY(fill_ld8(&a.ldx, a.K, "ldx", who));
+  TRY(fill_ld8(&a.ld_residual, a.N, "ld_residual", who));
+  TRY(fill_ld8(&a.ldy, a.N, "ldy", who));
+  TRY(need(a.w, 16, "w", who));
+  TRY(maybe(a.bias, 16, "bias", who));
+  if (a.M > 0) {
+    TRY(need(a.x, 16, "x", who));
+    TRY(need(a.y, 16, "y", who));
+    TRY(maybe(a.residual, 16, "residual", who));
+    TRY(maybe(a.h, 16, "h", who));
+    if (a.ckpt.codes || a.ckpt.scales) {
+      TRY(check_ckpt(a.ckpt, 8, "ckpt", who));
+      if (a.h) return set_error(LNFP8_ERR_INVALID_ARG, "%s: h and a checkpoint", who);
+    }
+  }
+  return linear_act_fwd_launch(&a, (cudaStream_t)stream);
+}
+
+int64_t lnfp8_linear_act_bwd_workspace_size(int64_t M, int64_t K, int64_t N, int has_act, int x_from_ckpt) {
+  return M < 0 || K < 0 || N < 0 ? -1 : linear_act_bwd_ws_bytes(M, K, N, has_act != 0, x_from_ckpt != 0);
+}
+
+lnfp8_status linear_act_bwd(const lnfp8_linear_act_bwd_args* args, lnfp8_stream stream) {
+  const char* who = "linear_act_bwd";
+  clear_error();
+  if (!args) return set_error(LNFP8_ERR_INVALID_ARG, "%s: args is NULL", who);
+  lnfp8_linear_act_bwd_args a = *args;
+  TRY(check_elem16(a.elem, who));
+  TRY(check_act(a.act, "act", who));
+  TRY(check_act(a.x_act, "x_act", who));
+  TRY(check_rows(a.M, "M", who));
+  TRY(check_feature(a.K, "K", who));
+  TRY(check_feature(a.N, "N", who));
+  TRY(fill_ld8(&a.ld_dy, a.N, "ld_dy", who));
+  TRY(fill_ld8(&a.ldx, a.K, "ldx", who));
+  TRY(fill_ld8(&a.ld_dx, a.K, "ld_dx", who));
+  TRY(maybe(a.dw, 16, "dw", who));
+  TRY(maybe(a.dbias, 4, "dbias", who));
+  const bool xck = a.x_ckpt.codes || a.x_ckpt.scales, hck = a.h_ckpt.codes || a.h_ckpt.scales;
+  if (a.M > 0) {
+    TRY(need(a.dy, 16, "dy", who));
+    TRY(maybe(a.dx, 16, "dx", who));
+    if (a.dx) TRY(need(a.w, 16, "w", who));
+    if (a.act != LNFP8_ACT_NONE) {
+      if (hck) TRY(check_ckpt(a.h_ckpt, 8, "h_ckpt", who));
+      else TRY(need(a.h, 16, "h", who));
+    }
+    if (a.dw) {
+      if (xck) {
+        TRY(check_ckpt(a.x_ckpt, 8, "x_ckpt", who));
+        if (a.x) return set_error(LNFP8_ERR_INVALID_ARG, "%s: x and a checkpoint of x", who);
+        if ((a.x_gamma == nullptr) != (a.x_beta == nullptr))
+          return set_error(LNFP8_ERR_INVALID_ARG, "%s: x_gamma and x_beta come together", who);
+        if (a.x_gamma && a.x_act != LNFP8_ACT_NONE)
+          return set_error(LNFP8_ERR_UNSUPPORTED, "%s: x_act and x_gamma, x_beta in one call", who);
+        TRY(maybe(a.x_gamma, 16, "x_gamma", who));
+        TRY(maybe(a.x_beta, 16, "x_beta", who));
+      } else {
+        TRY(need(a.x, 16, "x", who));
+        if (a.x_act != LNFP8_ACT_NONE || a.x_gamma || a.x_beta)
+          return set_error(LNFP8_ERR_INVALID_ARG, "%s: x_act, x_gamma, x_beta restore a checkpoint", who);
+      }
+    }
+    const int64_t want = linear_act_bwd_ws_bytes(a.M, a.K, a.N, a.act != LNFP8_ACT_NONE, xck);
+    if (want > 0) {
+      TRY(need(a.workspace, 16, "workspace", who));
+      if (a.workspace_bytes < want)
+        return set_error(LNFP8_ERR_INVALID_ARG, "%s: workspace of %lld bytes, %lld needed", who, (long long)a.workspace_bytes,
+                         (long long)want);
+    }
+  }
+  return linear_act_bwd_launch(&a, (cudaStream_t)stream);
 }
 
 }  // extern "C"

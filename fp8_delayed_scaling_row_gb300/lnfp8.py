@@ -7,7 +7,8 @@ the shared library has not been built, importing this module raises.
 Names follow the C ABI: lnfp8_meta_init, amax_history_update, fp8_quantize,
 ln_fwd_cast, ln_bwd, fp8_gemm, ln_linear_fwd / ln_linear_bwd,
 ln_mlp_fwd / ln_mlp_bwd; and, for what a model keeps in 16 or 32 bits,
-layernorm_fwd / layernorm_bwd and act_ckpt_save / act_ckpt_restore.
+layernorm_fwd / layernorm_bwd, act_ckpt_save / act_ckpt_restore and
+linear_act_fwd / linear_act_bwd.
 """
 from __future__ import annotations
 
@@ -35,7 +36,8 @@ EXPORTED = [
     "ln_linear_bwd_noalloc", "ln_mlp_fwd", "ln_mlp_bwd", "lnfp8_gemm_workspace_size",
     "lnfp8_ln_linear_bwd_workspace_size", "lnfp8_ln_mlp_bwd_workspace_size", "lnfp8_ln_mlp_fwd_workspace_size",
     "lnfp8_ctx_bytes", "lnfp8_ctx_offsets", "lnfp8_act_ckpt_scale_pitch", "act_ckpt_save", "act_ckpt_restore",
-    "layernorm_fwd", "layernorm_bwd", "lnfp8_layernorm_bwd_workspace_size",
+    "layernorm_fwd", "layernorm_bwd", "lnfp8_layernorm_bwd_workspace_size", "linear_act_fwd", "linear_act_bwd",
+    "lnfp8_linear_act_bwd_workspace_size",
 ]
 OP_LN_LINEAR, OP_LINEAR, OP_LN_MLP = 0, 1, 2
 
@@ -111,6 +113,19 @@ class CLayerNormBwd(C.Structure):
                 ("ld_dresidual", _I64), ("ld_dx", _I64)]
 
 
+class CLinearActFwd(C.Structure):
+    _fields_ = [("M", _I64), ("K", _I64), ("N", _I64), ("elem", C.c_int), ("act", C.c_int), ("x", _P), ("w", _P),
+                ("bias", _P), ("residual", _P), ("y", _P), ("h", _P), ("ckpt", CCkpt), ("ldx", _I64),
+                ("ld_residual", _I64), ("ldy", _I64)]
+
+
+class CLinearActBwd(C.Structure):
+    _fields_ = [("M", _I64), ("K", _I64), ("N", _I64), ("elem", C.c_int), ("act", C.c_int), ("dy", _P), ("x", _P),
+                ("x_ckpt", CCkpt), ("x_act", C.c_int), ("x_gamma", _P), ("x_beta", _P), ("w", _P), ("h", _P),
+                ("h_ckpt", CCkpt), ("dx", _P), ("dw", _P), ("dbias", _P), ("workspace", _P), ("workspace_bytes", _I64),
+                ("ld_dy", _I64), ("ldx", _I64), ("ld_dx", _I64)]
+
+
 def _sig(name, args, res=C.c_int):
     f = getattr(_lib, name)
     f.argtypes = args
@@ -155,6 +170,9 @@ _c_ckpt_restore = _sig("act_ckpt_restore", [C.POINTER(CCkpt), _I64, _I64, C.c_in
 _c_ckpt_pitch = _sig("lnfp8_act_ckpt_scale_pitch", [_I64], C.c_int64)
 _c_layernorm_fwd = _sig("layernorm_fwd", [C.POINTER(CLayerNormFwd), _P])
 _c_layernorm_bwd = _sig("layernorm_bwd", [C.POINTER(CLayerNormBwd), _P])
+_c_linear_act_fwd = _sig("linear_act_fwd", [C.POINTER(CLinearActFwd), _P])
+_c_linear_act_bwd = _sig("linear_act_bwd", [C.POINTER(CLinearActBwd), _P])
+_c_linear_act_bwd_ws = _sig("lnfp8_linear_act_bwd_workspace_size", [_I64, _I64, _I64, C.c_int, C.c_int], C.c_int64)
 _c_layernorm_bwd_ws = _sig("lnfp8_layernorm_bwd_workspace_size", [_I64, _I64], C.c_int64)
 
 
@@ -837,4 +855,120 @@ def layernorm_bwd(dy, ctx: LayerNormCtx, gamma, *, dresidual=None, grads: LayerN
                           _ptr(dresidual), g.dx.data_ptr(), g.dgamma.data_ptr(), g.dbeta.data_ptr(), _ptr(g.workspace),
                           g.workspace.numel() if g.workspace is not None else 0, lddy, ldx, lddr, lddx)
         _check(_c_layernorm_bwd(C.byref(a), _stream(stream)))
+    return g
+
+
+_ELEM16 = {torch.bfloat16: 0, torch.float16: 1}
+
+
+@dataclass
+class LinearActCtx:
+    """What linear_act_bwd needs of its forward besides x and w: the activation and the
+    pre-activation, as a tensor or as a checkpoint (neither for act "none")."""
+    act: str = "none"
+    h: torch.Tensor | None = None
+    ckpt: ActCkpt | None = None
+
+
+def linear_act_fwd(x, w, bias=None, *, act="none", residual=None, save="none", y=None, ctx: LinearActCtx | None = None,
+                   stream=None):
+    """act(x w^T + bias) + residual of bf16 or fp16 tensors, x [M, K], w [N, K]; returns (y, ctx).
+    act: "none", "gelu" (tanh form), "relu" or "silu". save: what the backward reads of the
+    pre-activation, "h" (a tensor), "ckpt" (8 bits) or "none"; the buffers of `ctx` are used if it has them."""
+    elem, ia = _elem(x, "x", _ELEM16), _act(act)
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError(f"x and w have shapes {tuple(x.shape)} and {tuple(w.shape)}: expected two dimensions")
+    if save not in ("none", "h", "ckpt"):
+        raise ValueError(f"unknown save {save!r}: one of none, h, ckpt")
+    M, K = x.shape
+    N = w.shape[0]
+    dt, dev = x.dtype, x.device
+    ldx = _rows(x, "x", M, K, dt)
+    _flat(w, "w", (N, K), dt)
+    if bias is not None:
+        _flat(bias, "bias", (N,), dt)
+    ldr = _rows(residual, "residual", M, N, dt) if residual is not None else 0
+    with _On(stream):
+        y = y if y is not None else _e((M, N), dt, dev)
+        ldy = _rows(y, "y", M, N, dt)
+        ctx = ctx if ctx is not None else LinearActCtx()
+        ctx.act = act
+        h, ck = None, _NO_CKPT
+        if save == "h":
+            ctx.ckpt = None
+            ctx.h = ctx.h if ctx.h is not None else _e((M, N), dt, dev)
+            _flat(ctx.h, "ctx.h", (M, N), dt)
+            h = ctx.h.data_ptr()
+        elif save == "ckpt":
+            ctx.h = None
+            ctx.ckpt = ctx.ckpt if ctx.ckpt is not None else act_ckpt(M, N, device=dev)
+            ck = ctx.ckpt.c(M, N, "ctx.ckpt")
+        a = CLinearActFwd(M, K, N, elem, ia, x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual), y.data_ptr(), h, ck,
+                          ldx, ldr, ldy)
+        _check(_c_linear_act_fwd(C.byref(a), _stream(stream)))
+    return y, ctx
+
+
+@dataclass
+class LinearActGrads:
+    dx: torch.Tensor | None
+    dw: torch.Tensor | None
+    dbias: torch.Tensor | None
+    workspace: torch.Tensor | None = None
+
+
+def linear_act_bwd_workspace_size(M, K, N, *, has_act, x_from_ckpt) -> int:
+    return int(_c_linear_act_bwd_ws(M, K, N, int(has_act), int(x_from_ckpt)))
+
+
+def linear_act_grads(M, K, N, *, act="none", x_from_ckpt=False, dx=True, dw=True, bias=True, dtype=torch.bfloat16,
+                     device="cuda") -> LinearActGrads:
+    """Gradients and workspace of one linear_act_bwd; dx, dw, bias=False leave theirs out."""
+    ws = linear_act_bwd_workspace_size(M, K, N, has_act=act != "none", x_from_ckpt=x_from_ckpt)
+    return LinearActGrads(_e((M, K), dtype, device) if dx else None, _e((N, K), dtype, device) if dw else None,
+                          _e((N,), torch.float32, device) if bias else None, _e((ws,), torch.uint8, device))
+
+
+def linear_act_bwd(dy, x, w, ctx: LinearActCtx, *, x_act="none", x_gamma=None, x_beta=None,
+                   grads: LinearActGrads | None = None, stream=None) -> LinearActGrads:
+    """Gradients of linear_act_fwd (the residual's is dy). x: the forward's input, or an ActCkpt from
+    which it is restored as x_act(values) or values * x_gamma + x_beta. Gradients that `grads` leaves
+    None are not computed; x may be None without dw."""
+    elem, ia = _elem(dy, "dy", _ELEM16), _act(ctx.act)
+    if dy.dim() != 2 or w.dim() != 2:
+        raise ValueError(f"dy and w have shapes {tuple(dy.shape)} and {tuple(w.shape)}: expected two dimensions")
+    M, N = dy.shape
+    K = w.shape[1]
+    dt = dy.dtype
+    lddy = _rows(dy, "dy", M, N, dt)
+    _flat(w, "w", (N, K), dt)
+    h, hck, xp, xck, ldx = None, _NO_CKPT, None, _NO_CKPT, 0
+    if ia:
+        if ctx.ckpt is not None:
+            hck = ctx.ckpt.c(M, N, "ctx.ckpt")
+        elif ctx.h is not None:
+            _flat(ctx.h, "ctx.h", (M, N), dt)
+            h = ctx.h.data_ptr()
+        else:
+            raise ValueError(f"the forward with act {ctx.act!r} saved no pre-activation")
+    if isinstance(x, ActCkpt):
+        xck = x.c(M, K, "x")
+    elif x is not None:
+        ldx = _rows(x, "x", M, K, dt)
+        xp = x.data_ptr()
+    for t, name in ((x_gamma, "x_gamma"), (x_beta, "x_beta")):
+        if t is not None:
+            _flat(t, name, (K,), dt)
+    with _On(stream):
+        g = grads if grads is not None else linear_act_grads(M, K, N, act=ctx.act, x_from_ckpt=xck is not _NO_CKPT,
+                                                             dw=x is not None, dtype=dt, device=dy.device)
+        lddx = _rows(g.dx, "grads.dx", M, K, dt) if g.dx is not None else 0
+        if g.dw is not None:
+            _flat(g.dw, "grads.dw", (N, K), dt)
+        if g.dbias is not None:
+            _flat(g.dbias, "grads.dbias", (N,), torch.float32)
+        a = CLinearActBwd(M, K, N, elem, ia, dy.data_ptr(), xp, xck, _act(x_act), _ptr(x_gamma), _ptr(x_beta), w.data_ptr(),
+                          h, hck, _ptr(g.dx), _ptr(g.dw), _ptr(g.dbias), _ptr(g.workspace),
+                          g.workspace.numel() if g.workspace is not None else 0, lddy, ldx, lddx)
+        _check(_c_linear_act_bwd(C.byref(a), _stream(stream)))
     return g

@@ -621,6 +621,57 @@ lnfp8_status layernorm_bwd(const lnfp8_layernorm_bwd_args* args, lnfp8_stream st
 /* Bytes of layernorm_bwd's workspace on the current device; -1 for a negative size. */
 int64_t lnfp8_layernorm_bwd_workspace_size(int64_t M, int64_t D);
 
+typedef struct {
+  int64_t M, K, N;        /* rows (tokens) >= 0, in_features, out_features (multiples of 8) */
+  int elem;               /* LNFP8_BF16 or LNFP8_FP16, of every tensor */
+  int act;                /* lnfp8_act */
+  const void* x;          /* [M, K] */
+  const void* w;          /* [N, K] */
+  const void* bias;       /* [N] or NULL */
+  const void* residual;   /* [M, N] or NULL, added after the activation */
+  void* y;                /* out [M, N] */
+  void* h;                /* out [M, N] or NULL: the pre-activation z, for the backward */
+  lnfp8_ckpt ckpt;        /* out, optional: z as an 8-bit checkpoint instead (codes 8-byte aligned) */
+  int64_t ldx, ld_residual, ldy;
+} lnfp8_linear_act_fwd_args;
+
+/* Linear layer with its epilogue: z = x . w^T + bias (fp32), y = T(act(z) + residual);
+ * h = T(z), or z as a checkpoint, saved on request. */
+lnfp8_status linear_act_fwd(const lnfp8_linear_act_fwd_args* args, lnfp8_stream stream);
+
+typedef struct {
+  int64_t M, K, N;
+  int elem;               /* LNFP8_BF16 or LNFP8_FP16, of every tensor but dbias */
+  int act;                /* of the forward */
+  const void* dy;         /* [M, N] */
+  const void* x;          /* [M, K] the forward's input; NULL with x_ckpt or without dw */
+  lnfp8_ckpt x_ckpt;      /* a checkpoint to restore x from: x = x_act(v), or v * x_gamma + x_beta */
+  int x_act;              /* lnfp8_act: e.g. the previous layer's activation of its checkpointed pre-activation */
+  const void* x_gamma;    /* [K] or NULL: a LayerNorm's gamma and beta with its checkpointed rows */
+  const void* x_beta;
+  const void* w;          /* [N, K]; may be NULL without dx */
+  const void* h;          /* [M, N] the forward's h; NULL with h_ckpt or without activation */
+  lnfp8_ckpt h_ckpt;      /* the forward's checkpoint of z (codes 8-byte aligned) */
+  void* dx;               /* out [M, K] or NULL */
+  void* dw;               /* out [N, K] or NULL */
+  float* dbias;           /* out [N] or NULL */
+  void* workspace;        /* lnfp8_linear_act_bwd_workspace_size bytes, 16-byte aligned */
+  int64_t workspace_bytes;
+  int64_t ld_dy, ldx, ld_dx;
+} lnfp8_linear_act_bwd_args;
+
+/* Backward of linear_act_fwd: dz = dy * act'(h) (fp32; rounded to the type for the
+ * products), dbias = sum_rows dz (before that rounding, added in a fixed order),
+ * dx = T(dz . w), dw = T(dz^T . x). The residual's gradient is dy itself. With M = 0,
+ * dw and dbias are zero. The same call gives the same bits. The workspace need
+ * not be initialised. */
+lnfp8_status linear_act_bwd(const lnfp8_linear_act_bwd_args* args, lnfp8_stream stream);
+
+/* Bytes of linear_act_bwd's workspace on the current device, for a forward with
+ * (has_act) or without activation, x given as a tensor or restored from a
+ * checkpoint (x_from_ckpt); -1 for a negative size. */
+int64_t lnfp8_linear_act_bwd_workspace_size(int64_t M, int64_t K, int64_t N, int has_act, int x_from_ckpt);
+
 #ifdef __cplusplus
 }
 #endif

@@ -105,7 +105,61 @@ def test_layernorm_bwd_refuses_both_sources(L):
     assert L._c_layernorm_bwd(ctypes.byref(a), None) == 1 and "checkpoint" in L.last_error()
 
 
-STRUCTS = {"lnfp8_ckpt": "CCkpt", "lnfp8_layernorm_fwd_args": "CLayerNormFwd", "lnfp8_layernorm_bwd_args": "CLayerNormBwd"}
+@pytest.mark.parametrize("args,status,needle", [
+    (dict(elem=2), 1, "elem"), (dict(act=9), 1, "act"), (dict(K=12), 2, "multiple of 8"), (dict(N=0), 2, "N"), (dict(M=-1), 1, "M"),
+    (dict(x=FAKE + 8), 1, "x is not 16-byte"), (dict(bias=FAKE + 2), 1, "bias"), (dict(ldx=66), 1, "ldx"), (dict(ldy=32), 1, "ldy"),
+    (dict(w=None), 1, "w is NULL"), (dict(y=None), 1, "y is NULL"), (dict(residual=FAKE + 4), 1, "residual"),
+])
+def test_linear_act_fwd_refuses(L, args, status, needle):
+    a = L.CLinearActFwd(M=4, K=64, N=64, x=FAKE, w=FAKE, y=FAKE)
+    for k, v in args.items():
+        setattr(a, k, v)
+    assert L._c_linear_act_fwd(ctypes.byref(a), None) == status
+    assert needle in L.last_error()
+
+
+def test_linear_act_fwd_refuses_checkpoints(L):
+    a = L.CLinearActFwd(M=4, K=64, N=64, x=FAKE, w=FAKE, y=FAKE, h=FAKE, ckpt=ck(L))
+    assert L._c_linear_act_fwd(ctypes.byref(a), None) == 1 and "checkpoint" in L.last_error()
+    a = L.CLinearActFwd(M=4, K=64, N=64, x=FAKE, w=FAKE, y=FAKE, ckpt=ck(L, codes=FAKE + 4))
+    assert L._c_linear_act_fwd(ctypes.byref(a), None) == 1 and "8-byte" in L.last_error()
+    a = L.CLinearActFwd(M=0, K=64, N=64, w=FAKE)
+    assert L._c_linear_act_fwd(ctypes.byref(a), None) == 0
+
+
+@pytest.mark.parametrize("args,status,needle", [
+    (dict(elem=2), 1, "elem"), (dict(act=1, h=None), 1, "h is NULL"), (dict(x=None), 1, "x is NULL"), (dict(x_act=1), 1, "checkpoint"),
+    (dict(x_act=8), 1, "x_act"), (dict(workspace=None), 1, "workspace"), (dict(workspace_bytes=8), 1, "workspace"),
+    (dict(w=None), 1, "w is NULL"), (dict(ld_dy=60), 1, "ld_dy"), (dict(dw=FAKE + 2), 1, "dw"), (dict(x_gamma=FAKE), 1, "checkpoint"),
+    (dict(N=4), 2, "multiple of 8"), (dict(dbias=FAKE + 2), 1, "dbias"),
+])
+def test_linear_act_bwd_refuses(L, args, status, needle):
+    a = L.CLinearActBwd(M=4, K=64, N=64, dy=FAKE, x=FAKE, w=FAKE, h=FAKE, dx=FAKE, dw=FAKE, dbias=FAKE, workspace=FAKE,
+                        workspace_bytes=1 << 40)
+    for k, v in args.items():
+        setattr(a, k, v)
+    assert L._c_linear_act_bwd(ctypes.byref(a), None) == status
+    assert needle in L.last_error()
+
+
+def test_linear_act_bwd_refuses_checkpoint_mixes(L):
+    def call(**kw):
+        a = L.CLinearActBwd(M=4, K=64, N=64, dy=FAKE, x=None, w=FAKE, dx=FAKE, dw=FAKE, x_ckpt=ck(L), workspace=FAKE,
+                            workspace_bytes=1 << 40)
+        for k, v in kw.items():
+            setattr(a, k, v)
+        return L._c_linear_act_bwd(ctypes.byref(a), None)
+
+    assert call(x=FAKE) == 1 and "checkpoint" in L.last_error()
+    assert call(x_gamma=FAKE) == 1 and "together" in L.last_error()
+    assert call(x_gamma=FAKE, x_beta=FAKE, x_act=1) == 5
+    assert L.linear_act_bwd_workspace_size(-1, 8, 8, has_act=True, x_from_ckpt=False) == -1
+    small, big = (L.linear_act_bwd_workspace_size(100, 64, 96, has_act=a, x_from_ckpt=a) for a in (False, True))
+    assert small >= 96 * 4 and big >= small + 100 * (64 + 96) * 2
+
+
+STRUCTS = {"lnfp8_ckpt": "CCkpt", "lnfp8_layernorm_fwd_args": "CLayerNormFwd", "lnfp8_layernorm_bwd_args": "CLayerNormBwd",
+           "lnfp8_linear_act_fwd_args": "CLinearActFwd", "lnfp8_linear_act_bwd_args": "CLinearActBwd"}
 
 
 def test_struct_layouts_match_the_header(L, tmp_path):
