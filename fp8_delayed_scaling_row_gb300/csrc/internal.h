@@ -205,6 +205,10 @@ struct LinGemm {
   int64_t ldr;
   void* h;            // [M, N] contiguous: T(z)
   lnfp8_ckpt ckpt;    // z as a checkpoint
+  // or, without any of the above: out = T(acc * cscale[col] + rvec[row] * cvec[col])
+  const void* cscale;  // [N] elem
+  const void* cvec;    // [N] elem
+  const float* rvec;   // [M]
 };
 lnfp8_status lin_gemm_launch(const LinGemm& g, cudaStream_t st);
 lnfp8_status lin_status_read_clear(unsigned int* word);

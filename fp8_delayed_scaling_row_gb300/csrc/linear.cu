@@ -38,6 +38,9 @@ struct EpiParams {
   uint8_t* codes;
   uint8_t* scales;
   int64_t pitch;
+  const void* cscale;
+  const void* cvec;
+  const float* rvec;
 };
 
 __device__ __forceinline__ uint32_t pack16(float a, float b, int f16) {
@@ -73,6 +76,14 @@ __device__ __forceinline__ uint2 encode8(const float* v, float inv) {
 // are neighbours; every lane of the warp calls it (`ok`: inside the tensor).
 __device__ __forceinline__ void epilogue8(const EpiParams& p, float* v, int m, int n, bool ok) {
   const int64_t row = m;
+  if (p.cscale && ok) {
+    float cs[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, cv[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    add16x8(cs, *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.cscale) + n), p.f16);
+    add16x8(cv, *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.cvec) + n), p.f16);
+    const float rv = p.rvec[m];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = fmaf(v[i], cs[i], rv * cv[i]);
+  }
   if (p.bias && ok) add16x8(v, *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.bias) + n), p.f16);
   if (p.h && ok)
     *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.h) + row * p.N + n) = pack16x8(v, p.f16);
@@ -284,7 +295,8 @@ struct DactParams {
   const uint8_t* codes;
   const uint8_t* scales;
   void* dz;      // NULL: no activation, only the column sums
-  float* part;   // [row blocks][N] or NULL
+  float* part;   // [row blocks][N] or NULL; with `both` [row blocks][2][N]: the sums of dz, then of dz as rounded
+  int both;
   int64_t M, lddy, pitch;
   int N, act, rows_per_block;
 };
@@ -300,9 +312,9 @@ __global__ void __launch_bounds__(256) lin_dact_kernel(const DactParams p) {
   const int64_t r0 = (int64_t)blockIdx.y * p.rows_per_block;
   const int64_t r1 = min64(p.M, r0 + p.rows_per_block);
   constexpr int f16 = ELEM == LNFP8_FP16;
-  float acc[8];
+  float acc[8], accr[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+  for (int i = 0; i < 8; ++i) acc[i] = accr[i] = 0.f;
   if (ok) {
 #pragma unroll 4
     for (int64_t r = r0 + rl; r < r1; r += 8) {
@@ -329,21 +341,26 @@ __global__ void __launch_bounds__(256) lin_dact_kernel(const DactParams p) {
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] *= act_slope(z[i], p.act);
-        *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.dz) + r * p.N + c) = pack16x8(v, f16);
+        const uint4 w = pack16x8(v, f16);
+        *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.dz) + r * p.N + c) = w;
+        if (p.both) add16x8(accr, w, f16);
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[i] += v[i];
     }
   }
   if (p.part == nullptr) return;
+  for (int k = 0; k <= p.both; ++k) {
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) red[rl][cl][i] = acc[i];
-  __syncthreads();
-  const int col = threadIdx.x;  // 256 columns
-  float s = 0.f;
+    for (int i = 0; i < 8; ++i) red[rl][cl][i] = k ? accr[i] : acc[i];
+    __syncthreads();
+    const int col = threadIdx.x;  // 256 columns
+    float s = 0.f;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) s += red[k][col >> 3][col & 7];
-  if (blockIdx.x * 256 + col < p.N) p.part[(int64_t)blockIdx.y * p.N + blockIdx.x * 256 + col] = s;
+    for (int q = 0; q < 8; ++q) s += red[q][col >> 3][col & 7];
+    if (blockIdx.x * 256 + col < p.N) p.part[((int64_t)blockIdx.y * (1 + p.both) + k) * p.N + blockIdx.x * 256 + col] = s;
+  }
 }
 
 // ------------------------------------------------------------ host side
@@ -401,6 +418,9 @@ EpiParams epi_params(const LinGemm& g) {
   e.codes = g.ckpt.codes;
   e.scales = g.ckpt.scales;
   e.pitch = lnfp8_act_ckpt_scale_pitch(g.N);
+  e.cscale = g.cscale;
+  e.cvec = g.cvec;
+  e.rvec = g.rvec;
   return e;
 }
 
@@ -450,6 +470,8 @@ lnfp8_status tile_launch(const LinGemm& g, cudaStream_t st) {
   return check_launch("linear");
 }
 
+#include "linear_pair.cuh"
+
 // Rows of the dz pass per block: enough blocks for about four per SM.
 int64_t dact_rows_per_block(int64_t M, int64_t N) {
   const int64_t col_blocks = (N + 255) / 256;
@@ -473,6 +495,11 @@ lnfp8_status lin_gemm_launch(const LinGemm& g, cudaStream_t st) {
     if (g.M <= 16) return tile_launch<16, true, false, true>(g, st);
     if (g.M <= 32) return tile_launch<32, true, false, true>(g, st);
     return tile_launch<64, true, false, true>(g, st);
+  }
+  if (((g.M + 255) / 256) * ((g.N + 255) / 256) * 4 >= num_sms()) {
+    if (!g.a_mn && !g.b_mn) return pair_launch<256, false, false, LIN_FULL>(g, st);
+    if (!g.a_mn) return pair_launch<256, false, true, LIN_PLAIN>(g, st);
+    return g.cscale ? pair_launch<256, true, true, LIN_AFFINE>(g, st) : pair_launch<256, true, true, LIN_PLAIN>(g, st);
   }
   if (!g.a_mn) return g.b_mn ? tile_launch<128, false, true, false>(g, st) : tile_launch<128, false, false, false>(g, st);
   return tile_launch<128, true, true, false>(g, st);
@@ -499,11 +526,13 @@ lnfp8_status linear_act_fwd_launch(const lnfp8_linear_act_fwd_args* a, cudaStrea
   return lin_gemm_launch(g, st);
 }
 
-// dz [M, N], the restored x [M, K] and the column partials of db, each from a multiple of 256 on.
+// dz [M, N], the restored x [M, K], two column sums for the affine input, and the columns' partial
+// sums, each from a multiple of 256 on.
 int64_t linear_act_bwd_ws_bytes(int64_t M, int64_t K, int64_t N, bool has_act, bool x_from_ckpt) {
   if (M == 0 || N == 0) return 0;
   const int64_t rpb = dact_rows_per_block(M, N);
-  return (has_act ? up256(M * N * 2) : 0) + (x_from_ckpt ? up256(M * K * 2) : 0) + up256((M + rpb - 1) / rpb * N * 4);
+  return (has_act ? up256(M * N * 2) : 0) + (x_from_ckpt ? up256(M * K * 2) + 2 * up256(N * 4) : 0) +
+         up256((M + rpb - 1) / rpb * N * 4 * (has_act && x_from_ckpt ? 2 : 1));
 }
 
 lnfp8_status linear_act_bwd_launch(const lnfp8_linear_act_bwd_args* a, cudaStream_t st) {
@@ -519,17 +548,31 @@ lnfp8_status linear_act_bwd_launch(const lnfp8_linear_act_bwd_args* a, cudaStrea
   if (has_act) ws += up256(a->M * a->N * 2);
   void* x_ws = ws;
   if (xck) ws += up256(a->M * a->K * 2);
+  // x = v gamma + beta from a checkpoint's values v: dw = (dz^T v) gamma + (sum dz) beta, applied in the
+  // product's epilogue. v has four significant bits, so the 16-bit operand is exact and x is never rounded. The
+  // sum is of dz as rounded for the product, so that where v gamma and beta cancel, dw does too.
+  const bool affine = a->dw && xck && a->x_gamma;
+  float* db = a->dbias;
+  float* dbr = nullptr;
+  if (xck) {
+    if (affine) {
+      if (!db) db = reinterpret_cast<float*>(ws);
+      dbr = has_act ? reinterpret_cast<float*>(ws + up256(a->N * 4)) : db;
+    }
+    ws += 2 * up256(a->N * 4);
+  }
   const void* dz = has_act ? dz_ws : a->dy;
   const int64_t lddz = has_act ? a->N : a->ld_dy;
 
-  if (has_act || a->dbias) {
+  if (has_act || db) {
     DactParams p;
     p.dy = a->dy;
     p.h = a->h;
     p.codes = a->h_ckpt.codes;
     p.scales = a->h_ckpt.scales;
     p.dz = dz_ws;
-    p.part = a->dbias ? reinterpret_cast<float*>(ws) : nullptr;
+    p.part = db ? reinterpret_cast<float*>(ws) : nullptr;
+    p.both = affine && has_act;
     p.M = a->M;
     p.lddy = a->ld_dy;
     p.pitch = lnfp8_act_ckpt_scale_pitch(a->N);
@@ -551,8 +594,8 @@ lnfp8_status linear_act_bwd_launch(const lnfp8_linear_act_bwd_args* a, cudaStrea
     };
     lnfp8_status s = a->elem == LNFP8_BF16 ? pick(std::integral_constant<int, LNFP8_BF16>()) : pick(std::integral_constant<int, LNFP8_FP16>());
     if (s != LNFP8_OK) return s;
-    if (a->dbias) {
-      s = colsum_launch(p.part, (int)row_blocks, p.N, p.N, a->dbias, nullptr, st);
+    if (db) {
+      s = colsum_launch(p.part, (int)row_blocks, p.N * (1 + p.both), p.N, db, dbr, st);
       if (s != LNFP8_OK) return s;
     }
   }
@@ -576,7 +619,7 @@ lnfp8_status linear_act_bwd_launch(const lnfp8_linear_act_bwd_args* a, cudaStrea
     const void* x = a->x;
     int64_t ldx = a->ldx;
     if (xck) {
-      const lnfp8_status s = act_ckpt_restore_launch(a->x_ckpt, a->M, a->K, a->x_act, a->x_gamma, a->x_beta, a->elem, x_ws, a->elem, a->K, st);
+      const lnfp8_status s = act_ckpt_restore_launch(a->x_ckpt, a->M, a->K, a->x_act, nullptr, nullptr, a->elem, x_ws, a->elem, a->K, st);
       if (s != LNFP8_OK) return s;
       x = x_ws;
       ldx = a->K;
@@ -592,6 +635,11 @@ lnfp8_status linear_act_bwd_launch(const lnfp8_linear_act_bwd_args* a, cudaStrea
     g.b_mn = true;
     g.out = a->dw;
     g.ldo = a->K;
+    if (affine) {
+      g.cscale = a->x_gamma;
+      g.cvec = a->x_beta;
+      g.rvec = dbr;
+    }
     return lin_gemm_launch(g, st);
   }
   return LNFP8_OK;

@@ -1,0 +1,449 @@
+// Included by linear.cu: the persistent kernel for large products.
+//
+// A pair of CTAs (a cluster of 2) computes 256 x BN tiles with the 2-SM MMA
+// (256 x BN x 16 per instruction): each CTA loads its 128 rows of A and half of the
+// B tile by TMA into its own ring and signals the leader's barrier; the leader's one
+// thread issues the MMAs for both. Two accumulators (2 x BN tensor-memory columns)
+// alternate, so that the epilogue of one tile runs under the MMAs of the next.
+//   warp 0      TMA producer          warp 1   tensor memory, MMA issuer (leader)
+//   warps 2-3   idle                  warps 4-19  epilogue, 8 per accumulator
+// An epilogue warp takes 32 rows (its tensor-memory lanes) and half of the tile's
+// columns, 32 x 32 at a time: a thread holds 32 columns of one row, which is one
+// checkpoint block, so the scale needs no exchange between threads.
+
+enum LinEpi {
+  LIN_PLAIN = 0,   // out = T(acc)
+  LIN_FULL = 1,    // bias, saved pre-activation, activation, residual
+  LIN_AFFINE = 2,  // out = T(acc * cscale[col] + rvec[row] * cvec[col])
+};
+
+constexpr int kPairEpiWarps = 16;
+constexpr int kPairThreads = 128 + 32 * kPairEpiWarps;
+
+template <int BN, int EPI>
+struct PairCfg {
+  static constexpr int A_BYTES = 128 * BK * 2;
+  static constexpr int B_BYTES = BN / 2 * BK * 2;
+  static constexpr int STAGE = A_BYTES + B_BYTES;
+  // per epilogue warp: 32 x 32 16-bit boxes (2 KB) for the output and, with the full epilogue,
+  // for the saved pre-activation and the residual
+  static constexpr int BOXES = EPI == LIN_FULL ? 3 : 1;
+  static constexpr int BOX_BYTES = kPairEpiWarps * BOXES * 2048;
+  static constexpr int STAGES = (232448 - 1024 - 512 - BOX_BYTES) / STAGE;
+  static constexpr int BOX_OFF = STAGES * STAGE;
+  static constexpr int BAR_OFF = BOX_OFF + BOX_BYTES;
+  static constexpr int SMEM = 1024 + BAR_OFF + 512;
+  static constexpr int TMEM_COLS = 512;
+  static_assert(STAGES >= 4 && SMEM <= 232448, "shared memory budget");
+};
+
+struct PairParams {
+  int M, N, num_m2, num_n, num_kb, group_m;
+  uint32_t idesc;
+  int f16, act, ck, has_resid, has_h, codes16;
+  const void* bias;     // FULL; AFFINE: cscale
+  const void* cvec;     // AFFINE
+  const float* rvec;    // AFFINE
+  uint8_t* codes;
+  uint8_t* scales;
+  int64_t pitch;
+};
+
+// Tile t of a [num_m2 x num_n] grid: M fastest inside groups of G, then N, then the next
+// group; G panels of A stay in L2 while the group's columns pass.
+__device__ __forceinline__ int2 pair_tile(int t, int num_m2, int num_n, int G) {
+  const int span = G * num_n, grp = t / span, r = t - grp * span, m0 = grp * G;
+  const int gs = min(G, num_m2 - m0);
+  return make_int2(m0 + r % gs, r / gs);
+}
+
+// Row r, 16-byte chunk j of a 32 x 32 16-bit box with the 64-byte swizzle.
+__device__ __forceinline__ uint32_t box_at(int r, int j) { return (uint32_t)(r * 64 + ((j ^ ((r >> 1) & 3)) << 4)); }
+
+// The activation of 32 values held as 16 pairs.
+template <int ACT>
+__device__ __forceinline__ void act_pairs(uint64_t* z) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    if constexpr (ACT == LNFP8_ACT_RELU) {
+      const float2 v = up(z[i]);
+      z[i] = f2(act_fwd(v.x, ACT), act_fwd(v.y, ACT));
+    } else {
+      uint64_t nu;
+      if constexpr (ACT == LNFP8_ACT_GELU) {
+        const uint64_t c0 = f2(-kLog2e * kGelu2K, -kLog2e * kGelu2K), c1 = f2(-kLog2e * kGelu2KC, -kLog2e * kGelu2KC);
+        nu = mul2(z[i], fma2(mul2(z[i], z[i]), c1, c0));
+      } else {
+        nu = mul2(z[i], f2(-kLog2e, -kLog2e));
+      }
+      const float2 n = up(nu);
+      const float2 d = up(add2(f2(ex2_fast(n.x), ex2_fast(n.y)), f2(1.0f, 1.0f)));
+      z[i] = mul2(z[i], f2(rcp_fast(d.x), rcp_fast(d.y)));
+    }
+  }
+}
+
+template <int BN, bool A_MN, bool B_MN, int EPI>
+__global__ void __launch_bounds__(kPairThreads, 1)
+lin_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmR,
+                const __grid_constant__ CUtensorMap tmH, const PairParams p) {
+  using C = PairCfg<BN, EPI>;
+  constexpr int STAGES = C::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t ring = smem_u32(smem);
+  const uint32_t bar0 = ring + C::BAR_OFF;
+  // full[STAGES], empty[STAGES], tfull[2], tempty[2], drain, rload[kPairEpiWarps]
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+  auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + a); };
+  auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + 2 + a); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 4);
+  auto rload_bar = [&](int w) { return bar0 + 8u * (2 * STAGES + 5 + w); };
+  static_assert(8 * (2 * STAGES + 5 + kPairEpiWarps) + 8 <= 512, "barrier space");
+  volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + C::BAR_OFF + 8 * (2 * STAGES + 5 + kPairEpiWarps));
+  volatile uint32_t* abort_flag = misc;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), kPairEpiWarps);  // the 8 warps of this buffer in both CTAs
+    }
+    mbar_init(drain_bar, 1);
+    for (int w = 0; w < kPairEpiWarps; ++w) mbar_init(rload_bar(w), 1);
+    *abort_flag = 0;
+    mbar_init_fence();
+    tma_prefetch_map(&tmA);
+    tma_prefetch_map(&tmB);
+  }
+  cluster_sync_all();  // the peer signals this CTA's barriers
+  if (warp == 1) tmem_alloc<true>(smem_u32((const void*)(misc + 1)), C::TMEM_COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc[1];
+  pdl_wait();
+  pdl_launch_dependents();
+
+  const int rank = (int)cluster_rank();
+  const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
+  const int tiles = p.num_m2 * p.num_n;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int64_t issued = 0;
+      bool ok = true;
+      for (int t = cid; t < tiles && ok; t += ncl) {
+        const int2 mn = pair_tile(t, p.num_m2, p.num_n, p.group_m);
+        const int m0 = mn.x * 256 + rank * 128, n0 = mn.y * BN + rank * (BN / 2);
+        for (int kb = 0; kb < p.num_kb; ++kb) {
+          if (!mbar_wait(empty_bar(stage), phase ^ 1, abort_flag)) { ok = false; break; }
+          const uint32_t fb = map_to_rank(full_bar(stage), 0);
+          const uint32_t ad = ring + stage * C::STAGE, bd = ad + C::A_BYTES;
+          if (rank == 0) mbar_expect_tx(full_bar(stage), 2 * C::STAGE);
+          if constexpr (!A_MN) tma_load_pair(ad, &tmA, kb * BK, m0, fb);
+          else {
+            tma_load_pair(ad, &tmA, m0, kb * BK, fb);
+            tma_load_pair(ad + 8192, &tmA, m0 + 64, kb * BK, fb);
+          }
+          if constexpr (!B_MN) tma_load_pair(bd, &tmB, kb * BK, n0, fb);
+          else
+#pragma unroll
+            for (int j = 0; j < BN / 128; ++j) tma_load_pair(bd + j * 8192, &tmB, n0 + 64 * j, kb * BK, fb);
+          ++issued;
+          if (++stage == STAGES) { stage = 0; phase ^= 1; }
+        }
+      }
+      if (!ok && rank == 0)
+        for (int64_t i = min64(issued, STAGES); i > 0; --i) {
+          if (--stage < 0) { stage = STAGES - 1; phase ^= 1; }
+          mbar_drain(full_bar(stage), phase);
+        }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int t = cid; t < tiles && ok; t += ncl) {
+        if (!mbar_wait(tempty_bar(acc), acc_phase ^ 1, abort_flag)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(acc * BN);
+        for (int kb = 0; kb < p.num_kb; ++kb) {
+          if (!mbar_wait(full_bar(stage), phase, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t ab = ring + stage * C::STAGE, bb = ab + C::A_BYTES;
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk) {
+            const uint64_t ad = A_MN ? mat_desc(ab + kk * 2048, 8192, 1024) : mat_desc(ab + kk * 32, 16, 1024);
+            const uint64_t bd = B_MN ? mat_desc(bb + kk * 2048, 8192, 1024) : mat_desc(bb + kk * 32, 16, 1024);
+            mma_16bit<true>(d, ad, bd, p.idesc, kb != 0 || kk != 0);
+          }
+          mma_commit<true>(empty_bar(stage));
+          if (++stage == STAGES) { stage = 0; phase ^= 1; }
+        }
+        if (!ok) break;
+        mma_commit<true>(tfull_bar(acc));
+        if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+      }
+      if (!ok) {  // no MMA may still write tensor memory when it is freed
+        mma_commit<true>(drain_bar, 1);
+        mbar_drain(drain_bar, 0);
+      }
+    }
+  } else if (warp >= 4) {
+    const int ew = warp - 4, acc = ew >> 3, quarter = warp & 3, half = (ew >> 2) & 1;
+    constexpr int HALF = BN / 2, CHUNKS = HALF / 32;
+    uint8_t* box_o = smem + C::BOX_OFF + ew * C::BOXES * 2048;
+    uint8_t* box_h = box_o + 2048;
+    uint8_t* box_r = box_o + 4096;
+    const uint32_t rbar = rload_bar(ew);
+    uint32_t rphase = 0, acc_phase = 0;
+    bool r_pending = false;
+    const uint32_t tempty = map_to_rank(tempty_bar(acc), 0);
+    auto tile_at = [&](int t) { return pair_tile(t, p.num_m2, p.num_n, p.group_m); };
+    auto load_resid = [&](int t, int ch) {  // the 32 x 32 residual block of (tile, chunk)
+      if (lane == 0) {
+        const int2 mn = tile_at(t);
+        mbar_expect_tx(rbar, 2048);
+        tma_load(smem_u32(box_r), &tmR, mn.y * BN + half * HALF + ch * 32, mn.x * 256 + rank * 128 + quarter * 32, rbar);
+      }
+      r_pending = true;
+    };
+    const int t0 = cid + acc * ncl;
+    if constexpr (EPI == LIN_FULL)
+      if (p.has_resid && t0 < tiles) load_resid(t0, 0);
+    for (int t = t0; t < tiles; t += 2 * ncl) {
+      const int2 mn = tile_at(t);
+      const int m = mn.x * 256 + rank * 128 + quarter * 32 + lane;
+      const int nh = mn.y * BN + half * HALF;  // this warp's first column
+      // four columns of the per-column vectors per lane, asked for before the accumulator is waited for
+      uint2 cb = make_uint2(0u, 0u), cv = make_uint2(0u, 0u);
+      float rv = 0.f;
+      const int lc = nh + lane * 4;
+      if constexpr (EPI != LIN_PLAIN) {
+        if (p.bias && lane * 4 < HALF && lc < p.N) cb = __ldg(reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(p.bias) + lc));
+      }
+      if constexpr (EPI == LIN_AFFINE) {
+        if (lane * 4 < HALF && lc < p.N) cv = __ldg(reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(p.cvec) + lc));
+        if (m < p.M) rv = __ldg(p.rvec + m);
+      }
+      if (!mbar_wait(tfull_bar(acc), acc_phase, abort_flag)) break;
+      tc_fence_after();
+      bool aborted = false;
+      uint32_t scale_word = 0;
+#pragma unroll 1
+      for (int ch = 0; ch < CHUNKS; ++ch) {
+        const int n0 = nh + ch * 32;
+        uint32_t rr[32];
+        tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * BN + half * HALF + ch * 32), rr);
+        if (ch == CHUNKS - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(tempty);
+        }
+        uint64_t z[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) z[i] = f2(__uint_as_float(rr[2 * i]), __uint_as_float(rr[2 * i + 1]));
+        if constexpr (EPI != LIN_PLAIN) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {  // columns 2i, 2i + 1 of the chunk sit in lane 8 ch + i / 2
+            const float2 b = unpack16(__shfl_sync(0xFFFFFFFFu, i & 1 ? cb.y : cb.x, ch * 8 + (i >> 1)), p.f16);
+            if constexpr (EPI == LIN_FULL) z[i] = add2(z[i], f2(b.x, b.y));
+            else {
+              const float2 v = unpack16(__shfl_sync(0xFFFFFFFFu, i & 1 ? cv.y : cv.x, ch * 8 + (i >> 1)), p.f16);
+              z[i] = fma2(z[i], f2(b.x, b.y), mul2(f2(rv, rv), f2(v.x, v.y)));
+            }
+          }
+        }
+        uint4 res[4];
+        if constexpr (EPI == LIN_FULL) {
+          if (p.has_resid) {
+            if (!mbar_wait(rbar, rphase, abort_flag)) { aborted = true; break; }
+            rphase ^= 1;
+            r_pending = false;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) res[j] = *reinterpret_cast<const uint4*>(box_r + box_at(lane, j));
+            fence_async_smem();
+            __syncwarp();
+            if (ch + 1 < CHUNKS) load_resid(t, ch + 1);
+            else if (t + 2 * ncl < tiles) load_resid(t + 2 * ncl, 0);
+          }
+        }
+        if (lane == 0) bulk_wait_read();  // the previous chunk's stores have read their boxes
+        __syncwarp();
+        if constexpr (EPI == LIN_FULL) {
+          if (p.has_h) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float2 v = up(z[4 * j + i]);
+                w[i] = pack16(v.x, v.y, p.f16);
+              }
+              *reinterpret_cast<uint4*>(box_h + box_at(lane, j)) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+          if (p.ck >= 0) {
+            // columns past N are zero (no operand, no bias) and do not move the block's maximum
+            uint32_t am = 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 v = up(z[i]);
+              am = max(am, max(abs_bits(v.x), abs_bits(v.y)));
+            }
+            const uint32_t b = p.ck == LNFP8_E4M3 ? ckpt_byte<LNFP8_E4M3>(am) : ckpt_byte<LNFP8_E5M2>(am);
+            const float inv = ckpt_inv_scale(b);
+            const uint64_t i2 = f2(inv, inv);
+            scale_word |= b << (8 * ch);
+            uint32_t q[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float2 u = up(mul2(z[2 * i], i2)), v = up(mul2(z[2 * i + 1], i2));
+              q[i] = p.ck == LNFP8_E4M3 ? (uint32_t)cvt_fp8x2<LNFP8_E4M3>(u.x, u.y) | ((uint32_t)cvt_fp8x2<LNFP8_E4M3>(v.x, v.y) << 16)
+                                        : (uint32_t)cvt_fp8x2<LNFP8_E5M2>(u.x, u.y) | ((uint32_t)cvt_fp8x2<LNFP8_E5M2>(v.x, v.y) << 16);
+            }
+            if (m < p.M) {
+              uint8_t* dst = p.codes + (int64_t)m * p.N + n0;
+              if (p.codes16 && n0 + 32 <= p.N) {
+                reinterpret_cast<uint4*>(dst)[0] = make_uint4(q[0], q[1], q[2], q[3]);
+                reinterpret_cast<uint4*>(dst)[1] = make_uint4(q[4], q[5], q[6], q[7]);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  if (n0 + 8 * j < p.N) reinterpret_cast<uint2*>(dst)[j] = make_uint2(q[2 * j], q[2 * j + 1]);
+              }
+            }
+          }
+          if (p.act == LNFP8_ACT_GELU) act_pairs<LNFP8_ACT_GELU>(z);
+          else if (p.act == LNFP8_ACT_SILU) act_pairs<LNFP8_ACT_SILU>(z);
+          else if (p.act == LNFP8_ACT_RELU) act_pairs<LNFP8_ACT_RELU>(z);
+          if (p.has_resid) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t w[4] = {res[j].x, res[j].y, res[j].z, res[j].w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float2 v = unpack16(w[i], p.f16);
+                z[4 * j + i] = add2(z[4 * j + i], f2(v.x, v.y));
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 v = up(z[4 * j + i]);
+            w[i] = pack16(v.x, v.y, p.f16);
+          }
+          *reinterpret_cast<uint4*>(box_o + box_at(lane, j)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          const int y = mn.x * 256 + rank * 128 + quarter * 32;
+          if (y < p.M && n0 < p.N) {  // TMA clips the rest of a box at the tensor's edge
+            tma_store(&tmO, smem_u32(box_o), n0, y);
+            if constexpr (EPI == LIN_FULL)
+              if (p.has_h) tma_store(&tmH, smem_u32(box_h), n0, y);
+          }
+          bulk_commit();
+        }
+      }
+      if (aborted) break;
+      if constexpr (EPI == LIN_FULL) {
+        if (p.ck >= 0 && m < p.M && nh < p.N) {  // the four (or, at the edge, fewer) blocks' bytes, one word of the row
+          if constexpr (CHUNKS == 4) *reinterpret_cast<uint32_t*>(p.scales + (int64_t)m * p.pitch + (nh >> 5)) = scale_word;
+          else *reinterpret_cast<uint16_t*>(p.scales + (int64_t)m * p.pitch + (nh >> 5)) = (uint16_t)scale_word;
+        }
+      }
+      acc_phase ^= 1;
+    }
+    if (r_pending) {  // a residual block still on its way
+      if (lane == 0) mbar_drain(rbar, rphase);
+      __syncwarp();
+    }
+    if (lane == 0) bulk_wait();
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // both CTAs are done with the pair's tensor memory
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_free<true>(tmem, C::TMEM_COLS);
+  }
+  cluster_sync_all();  // nobody leaves while the peer may still signal its barriers
+}
+
+template <int BN, bool A_MN, bool B_MN, int EPI>
+lnfp8_status pair_launch(const LinGemm& g, cudaStream_t st) {
+  using C = PairCfg<BN, EPI>;
+  auto k = lin_pair_kernel<BN, A_MN, B_MN, EPI>;
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+    return check_launch("linear: shared memory attribute");
+  PairParams p = {};
+  p.M = (int)g.M;
+  p.N = (int)g.N;
+  p.num_m2 = (int)((g.M + 255) / 256);
+  p.num_n = (int)((g.N + BN - 1) / BN);
+  p.num_kb = (int)((g.K + BK - 1) / BK);
+  if ((int64_t)p.num_m2 * p.num_n > 0x7FFFFFFF) return set_error(LNFP8_ERR_UNSUPPORTED_SHAPE, "linear: too many tiles");
+  // A panels (256 rows x K) of a raster group: what fits in 48 MB of L2
+  const int64_t panel = 512 * max64(g.K, 1);
+  p.group_m = (int)max64(1, min64((48ll << 20) / panel, p.num_m2));
+  p.idesc = make_idesc(g.elem, 256, BN, A_MN, B_MN);
+  p.f16 = g.elem == LNFP8_FP16;
+  p.act = g.act;
+  p.ck = g.ckpt.codes ? g.ckpt.dtype : -1;
+  p.has_resid = g.resid != nullptr;
+  p.has_h = g.h != nullptr;
+  p.bias = EPI == LIN_AFFINE ? g.cscale : g.bias;
+  p.cvec = g.cvec;
+  p.rvec = g.rvec;
+  p.codes = g.ckpt.codes;
+  p.scales = g.ckpt.scales;
+  p.codes16 = g.N % 16 == 0 && reinterpret_cast<uintptr_t>(g.ckpt.codes) % 16 == 0;
+  p.pitch = lnfp8_act_ckpt_scale_pitch(g.N);
+  CUtensorMap ta, tb, to, tr, th;
+  bool ok = operand_map(&ta, g.a, A_MN, g.M, g.K, g.lda, 128) && operand_map(&tb, g.b, B_MN, g.N, g.K, g.ldb, BN / 2) &&
+            make_map(&to, g.out, g.N, g.M, g.ldo, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  tr = th = to;
+  if (ok && g.resid) ok = make_map(&tr, g.resid, g.N, g.M, g.ldr, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  if (ok && g.h) ok = make_map(&th, g.h, g.N, g.M, g.N, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  if (!ok) return set_error(LNFP8_ERR_CUDA, "linear: cuTensorMapEncodeTiled failed (driver entry point or arguments)");
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  const int64_t tiles = (int64_t)p.num_m2 * p.num_n, pairs = num_sms() / 2;
+  cfg.gridDim = dim3((unsigned)(2 * max64(1, min64(tiles, pairs))));
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  LaunchScope ls("linear_pair", st);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, ta, tb, to, tr, th, p);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return set_error(LNFP8_ERR_CUDA, "linear launch: %s", cudaGetErrorString(e));
+  }
+  return check_launch("linear");
+}

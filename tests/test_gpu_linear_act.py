@@ -13,7 +13,8 @@ pytestmark = pytest.mark.gpu
 DTYPES = [torch.bfloat16, torch.float16]
 # tokens, in, out: single tokens, the borders of the few-token forms, ragged and long ones
 SHAPES = [(1, 64, 64), (1, 2048, 1024), (7, 72, 200), (16, 512, 136), (17, 256, 8), (33, 8, 256), (64, 640, 320), (65, 128, 128),
-          (129, 200, 264), (300, 1032, 520), (513, 768, 768), (2048, 264, 1024), (700, 2048, 2056)]
+          (129, 200, 264), (300, 1032, 520), (513, 768, 768), (2048, 264, 1024), (700, 2048, 2056), (1500, 1800, 2056), (2600, 2568, 2560),
+          (2049, 2048, 4104)]
 
 
 @pytest.fixture(scope="module")
