@@ -50,6 +50,76 @@ __device__ __forceinline__ float round_elem(float v) {
   else return __bfloat162float(__float2bfloat16_rn(v));
 }
 
+// Eight neighbouring elements: one (16-bit types) or two (fp32) 16-byte words.
+template <int ELEM>
+__device__ __forceinline__ void unpack8(const uint4* u, float* v) {
+  if constexpr (ELEM == LNFP8_FP32) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      v[4 * k] = __uint_as_float(u[k].x);
+      v[4 * k + 1] = __uint_as_float(u[k].y);
+      v[4 * k + 2] = __uint_as_float(u[k].z);
+      v[4 * k + 3] = __uint_as_float(u[k].w);
+    }
+  } else {
+    const uint32_t w[4] = {u->x, u->y, u->z, u->w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (ELEM == LNFP8_FP16) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+        v[2 * k] = f.x;
+        v[2 * k + 1] = f.y;
+      } else {
+        v[2 * k] = __uint_as_float(w[k] << 16);
+        v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+      }
+    }
+  }
+}
+template <int ELEM>
+__device__ __forceinline__ void pack8(const float* v, uint4* u) {
+  if constexpr (ELEM == LNFP8_FP32) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      u[k] = make_uint4(__float_as_uint(v[4 * k]), __float_as_uint(v[4 * k + 1]), __float_as_uint(v[4 * k + 2]), __float_as_uint(v[4 * k + 3]));
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (ELEM == LNFP8_FP16) {
+        const __half2 h = __floats2half2_rn(v[2 * k], v[2 * k + 1]);
+        w[k] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        w[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
+      }
+    }
+    *u = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+template <int ELEM>
+__device__ __forceinline__ void load8(const void* p, int64_t i, float* v) {
+  constexpr int W = ELEM == LNFP8_FP32 ? 2 : 1;
+  const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(p) + i * ElemSize<ELEM>::value);
+  uint4 u[W];
+#pragma unroll
+  for (int k = 0; k < W; ++k) u[k] = q[k];
+  unpack8<ELEM>(u, v);
+}
+__device__ __forceinline__ void load8_rt(const void* p, int elem, int64_t i, float* v) {
+  if (elem == LNFP8_FP32) load8<LNFP8_FP32>(p, i, v);
+  else if (elem == LNFP8_FP16) load8<LNFP8_FP16>(p, i, v);
+  else load8<LNFP8_BF16>(p, i, v);
+}
+template <int ELEM>
+__device__ __forceinline__ void store8(void* p, int64_t i, const float* v) {
+  constexpr int W = ELEM == LNFP8_FP32 ? 2 : 1;
+  uint4* q = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p) + i * ElemSize<ELEM>::value);
+  uint4 u[W];
+  pack8<ELEM>(v, u);
+#pragma unroll
+  for (int k = 0; k < W; ++k) q[k] = u[k];
+}
+
 // The largest finite value of the type.
 template <int ELEM>
 __device__ __forceinline__ float elem_max() {
@@ -85,6 +155,26 @@ template <int DT>
 __device__ __forceinline__ float2 fp8x2_to_f32(uint32_t codes) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, DT == LNFP8_E4M3 ? __NV_E4M3 : __NV_E5M2);
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// Eight codes (a uint2, low byte first) times their block's scale.
+template <int DT>
+__device__ __forceinline__ void decode8(uint2 q, float scale, float* v) {
+  const uint32_t w[4] = {q.x & 0xFFFFu, q.x >> 16, q.y & 0xFFFFu, q.y >> 16};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 f = fp8x2_to_f32<DT>(w[k]);
+    v[2 * k] = f.x * scale;
+    v[2 * k + 1] = f.y * scale;
+  }
+}
+// Largest |v| bits of 8 values, then over the 4 neighbouring lanes that hold a block.
+__device__ __forceinline__ uint32_t block_amax8(const float* v) {
+  uint32_t am = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) am = max(am, abs_bits(v[k]));
+  am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
+  return max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
 }
 
 // A restored value: code * 2^e, kept inside the type (a block whose largest value
