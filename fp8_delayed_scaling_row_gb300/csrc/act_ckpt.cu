@@ -8,6 +8,8 @@
 #include "internal.h"
 #include "rowmath.cuh"
 
+#include <type_traits>
+
 namespace lnfp8 {
 namespace {
 
@@ -19,7 +21,7 @@ struct SaveParams {
   uint8_t* codes;
   uint8_t* scales;
   int64_t rows, ldx, pitch, units;  // units: rows * ceil(blocks per row / kBlocksPerWarp)
-  int cols, upr;                    // upr: units per row
+  int cols, upr, dt;                // upr: units per row; dt: the lnfp8_dtype of the codes
 };
 
 struct RestoreParams {
@@ -29,11 +31,11 @@ struct RestoreParams {
   const void* beta;
   void* out;
   int64_t rows, ldo, pitch, units;
-  int cols, upr, act, param_elem;
+  int cols, upr, act, param_elem, dt;
 };
 
 // Any width and alignment: a warp takes kBlocksPerWarp blocks of a row, lane = column.
-template <int ELEM, int DT>
+template <int ELEM>
 __global__ void __launch_bounds__(kThreads) save_any_kernel(const SaveParams p) {
   pdl_wait();
   pdl_launch_dependents();
@@ -48,8 +50,8 @@ __global__ void __launch_bounds__(kThreads) save_any_kernel(const SaveParams p) 
 #pragma unroll
     for (int i = 0; i < kBlocksPerWarp; ++i) {
       const int c = c0 + 32 * i;
-      const uint32_t b = ckpt_byte<DT>(warp_max_u32(abs_bits(v[i])));
-      const uint16_t code = cvt_fp8x2<DT>(v[i] * ckpt_inv_scale(b), 0.f);
+      const uint32_t b = ckpt_byte(warp_max_u32(abs_bits(v[i])), p.dt);
+      const uint32_t code = fp8x2(v[i] * ckpt_inv_scale(b), 0.f, p.dt);
       if (c < p.cols) {
         p.codes[row * p.cols + c] = (uint8_t)code;
         if (lane == 0) p.scales[row * p.pitch + (c >> 5)] = (uint8_t)b;
@@ -58,7 +60,7 @@ __global__ void __launch_bounds__(kThreads) save_any_kernel(const SaveParams p) 
   }
 }
 
-template <int ELEM, int DT>
+template <int ELEM>
 __global__ void __launch_bounds__(kThreads) restore_any_kernel(const RestoreParams p) {
   pdl_wait();
   pdl_launch_dependents();
@@ -78,11 +80,114 @@ __global__ void __launch_bounds__(kThreads) restore_any_kernel(const RestorePara
     for (int i = 0; i < kBlocksPerWarp; ++i) {
       const int c = c0 + 32 * i;
       if (c >= p.cols) continue;
-      float v = fp8x2_to_f32<DT>(code[i]).x * ckpt_scale(byte[i]);
+      float v = fp8x2_to_f32(code[i], p.dt).x * ckpt_scale(byte[i]);
       if (p.gamma) v = fmaf(v, load_elem_rt(p.gamma, p.param_elem, c), load_elem_rt(p.beta, p.param_elem, c));
       store_elem<ELEM>(p.out, row * p.ldo + c, ckpt_clamp<ELEM>(act_fwd(v, p.act)));
     }
   }
+}
+
+// Rows of whole 8-element chunks on 16-byte boundaries: a thread takes kChunks chunks of 8, a warp's
+// lanes neighbouring ones, so that four lanes hold a block. Chunks are counted over the rows with
+// each row's last block padded to 32 columns (cpr chunks a row), which keeps blocks inside four lanes.
+// HBM-bound: kChunks independent 16-byte loads a thread cover the latency.
+constexpr int kChunks = 4;
+
+struct ChunkPlace {
+  int64_t row;
+  int c;
+};
+__device__ __forceinline__ ChunkPlace place(int64_t chunk, uint32_t cpr) {
+  int64_t row;
+  if (chunk <= 0xFFFFFFFFll) row = (uint32_t)chunk / cpr;  // the 64-bit division costs several times this
+  else row = chunk / cpr;
+  return {row, (int)(chunk - row * cpr) * 8};
+}
+
+template <int ELEM>
+__global__ void __launch_bounds__(kThreads) save_vec_kernel(const SaveParams p) {
+  constexpr int W = ELEM == LNFP8_FP32 ? 2 : 1;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t total = p.rows * p.upr, step = (int64_t)gridDim.x * kThreads;  // upr: chunks per row here
+  const int64_t tail = (total + 31) / 32 * 32;                                  // whole warps reach the shuffles
+  for (int64_t i0 = (int64_t)blockIdx.x * kThreads + threadIdx.x; i0 < tail; i0 += step * kChunks) {
+    uint4 u[kChunks][W];
+    ChunkPlace at[kChunks];
+    bool ok[kChunks];
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) {
+      const int64_t i = i0 + k * step;
+      at[k] = place(i, p.upr);
+      ok[k] = i < total && at[k].c < p.cols;
+#pragma unroll
+      for (int w = 0; w < W; ++w) u[k][w] = make_uint4(0u, 0u, 0u, 0u);
+      if (ok[k]) {
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.x) + (at[k].row * p.ldx + at[k].c) * ElemSize<ELEM>::value);
+#pragma unroll
+        for (int w = 0; w < W; ++w) u[k][w] = __ldcs(src + w);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) {
+      if (i0 + k * step >= tail) break;  // uniform over the warp
+      float v[8];
+      unpack8<ELEM>(u[k], v);
+      const uint32_t b = ckpt_byte(block_amax8(v), p.dt);
+      if (ok[k]) {
+        *reinterpret_cast<uint2*>(p.codes + at[k].row * p.cols + at[k].c) = encode8(v, ckpt_inv_scale(b), p.dt);
+        if ((at[k].c & 31) == 0) p.scales[at[k].row * p.pitch + (at[k].c >> 5)] = (uint8_t)b;
+      }
+    }
+  }
+}
+
+template <int ELEM, int ACT, bool AFFINE>
+__global__ void __launch_bounds__(kThreads) restore_vec_kernel(const RestoreParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t total = p.rows * p.upr, step = (int64_t)gridDim.x * kThreads;
+  for (int64_t i0 = (int64_t)blockIdx.x * kThreads + threadIdx.x; i0 < total; i0 += step * kChunks) {
+    uint2 q[kChunks];
+    uint32_t b[kChunks];
+    ChunkPlace at[kChunks];
+    bool ok[kChunks];
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) {
+      const int64_t i = i0 + k * step;
+      at[k] = place(i, p.upr);
+      ok[k] = i < total && at[k].c < p.cols;
+      q[k] = make_uint2(0u, 0u);
+      b[k] = 0u;
+      if (ok[k]) {
+        q[k] = __ldcs(reinterpret_cast<const uint2*>(p.codes + at[k].row * p.cols + at[k].c));
+        b[k] = __ldg(p.scales + at[k].row * p.pitch + (at[k].c >> 5));
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) {
+      if (!ok[k]) continue;
+      float v[8];
+      decode8(q[k], ckpt_scale(b[k]), p.dt, v);
+      if constexpr (AFFINE) {
+        float ga[8], be[8];
+        load8_rt(p.gamma, p.param_elem, at[k].c, ga);
+        load8_rt(p.beta, p.param_elem, at[k].c, be);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = fmaf(v[e], ga[e], be[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = ckpt_clamp<ELEM>(act_fwd(v[e], ACT));
+      store8<ELEM>(p.out, at[k].row * p.ldo + at[k].c, v);
+    }
+  }
+}
+
+bool al(const void* p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+unsigned vec_grid(int64_t chunks) {
+  const int64_t blocks = (chunks + kThreads * kChunks - 1) / (kThreads * kChunks);
+  return (unsigned)max64(1, min64(blocks, (int64_t)num_sms() * 8));
 }
 
 unsigned grid_for(int64_t warps_of_work) {
@@ -102,6 +207,7 @@ lnfp8_status act_ckpt_save_launch(const void* x, int elem, int64_t rows, int64_t
   p.rows = rows;
   p.ldx = ldx;
   p.pitch = lnfp8_act_ckpt_scale_pitch(cols);
+  p.dt = c.dtype;
   p.cols = (int)cols;
   p.upr = (int)((cols + kBlocksPerWarp * 32 - 1) / (kBlocksPerWarp * 32));
   p.units = rows * p.upr;
@@ -110,10 +216,18 @@ lnfp8_status act_ckpt_save_launch(const void* x, int elem, int64_t rows, int64_t
     if (launch_pdl(kernel, dim3(grid_for(p.units)), dim3(kThreads), 0, st, p) != cudaSuccess) return check_launch("act_ckpt_save launch");
     return check_launch("act_ckpt_save");
   };
-  const bool e4 = c.dtype == LNFP8_E4M3;
-  if (elem == LNFP8_BF16) return e4 ? go(save_any_kernel<LNFP8_BF16, LNFP8_E4M3>) : go(save_any_kernel<LNFP8_BF16, LNFP8_E5M2>);
-  if (elem == LNFP8_FP16) return e4 ? go(save_any_kernel<LNFP8_FP16, LNFP8_E4M3>) : go(save_any_kernel<LNFP8_FP16, LNFP8_E5M2>);
-  return e4 ? go(save_any_kernel<LNFP8_FP32, LNFP8_E4M3>) : go(save_any_kernel<LNFP8_FP32, LNFP8_E5M2>);
+  // 16-byte rows take the vector kernel
+  if (cols % 8 == 0 && al(x, 16) && ldx * (elem == LNFP8_FP32 ? 4 : 2) % 16 == 0 && al(c.codes, 8)) {
+    p.upr = (int)((cols + 31) / 32 * 4);
+    auto vec = [&](auto kernel) {
+      if (launch_pdl(kernel, dim3(vec_grid(rows * p.upr)), dim3(kThreads), 0, st, p) != cudaSuccess) return check_launch("act_ckpt_save launch");
+      return check_launch("act_ckpt_save");
+    };
+    if (elem == LNFP8_BF16) return vec(save_vec_kernel<LNFP8_BF16>);
+    return elem == LNFP8_FP16 ? vec(save_vec_kernel<LNFP8_FP16>) : vec(save_vec_kernel<LNFP8_FP32>);
+  }
+  if (elem == LNFP8_BF16) return go(save_any_kernel<LNFP8_BF16>);
+  return elem == LNFP8_FP16 ? go(save_any_kernel<LNFP8_FP16>) : go(save_any_kernel<LNFP8_FP32>);
 }
 
 lnfp8_status act_ckpt_restore_launch(const lnfp8_ckpt& c, int64_t rows, int64_t cols, int act, const void* gamma,
@@ -128,6 +242,7 @@ lnfp8_status act_ckpt_restore_launch(const lnfp8_ckpt& c, int64_t rows, int64_t 
   p.rows = rows;
   p.ldo = ldo;
   p.pitch = lnfp8_act_ckpt_scale_pitch(cols);
+  p.dt = c.dtype;
   p.cols = (int)cols;
   p.upr = (int)((cols + kBlocksPerWarp * 32 - 1) / (kBlocksPerWarp * 32));
   p.units = rows * p.upr;
@@ -138,10 +253,25 @@ lnfp8_status act_ckpt_restore_launch(const lnfp8_ckpt& c, int64_t rows, int64_t 
     if (launch_pdl(kernel, dim3(grid_for(p.units)), dim3(kThreads), 0, st, p) != cudaSuccess) return check_launch("act_ckpt_restore launch");
     return check_launch("act_ckpt_restore");
   };
-  const bool e4 = c.dtype == LNFP8_E4M3;
-  if (elem == LNFP8_BF16) return e4 ? go(restore_any_kernel<LNFP8_BF16, LNFP8_E4M3>) : go(restore_any_kernel<LNFP8_BF16, LNFP8_E5M2>);
-  if (elem == LNFP8_FP16) return e4 ? go(restore_any_kernel<LNFP8_FP16, LNFP8_E4M3>) : go(restore_any_kernel<LNFP8_FP16, LNFP8_E5M2>);
-  return e4 ? go(restore_any_kernel<LNFP8_FP32, LNFP8_E4M3>) : go(restore_any_kernel<LNFP8_FP32, LNFP8_E5M2>);
+  if (cols % 8 == 0 && al(out, 16) && ldo * (elem == LNFP8_FP32 ? 4 : 2) % 16 == 0 && al(c.codes, 8) &&
+      (!gamma || (al(gamma, 16) && al(beta, 16)))) {
+    p.upr = (int)((cols + 31) / 32 * 4);
+    auto vec = [&](auto kernel) {
+      if (launch_pdl(kernel, dim3(vec_grid(rows * p.upr)), dim3(kThreads), 0, st, p) != cudaSuccess) return check_launch("act_ckpt_restore launch");
+      return check_launch("act_ckpt_restore");
+    };
+    auto by_act = [&](auto e) {
+      constexpr int E = decltype(e)::value;
+      if (gamma) return vec(restore_vec_kernel<E, LNFP8_ACT_NONE, true>);
+      if (act == LNFP8_ACT_GELU) return vec(restore_vec_kernel<E, LNFP8_ACT_GELU, false>);
+      if (act == LNFP8_ACT_SILU) return vec(restore_vec_kernel<E, LNFP8_ACT_SILU, false>);
+      return act == LNFP8_ACT_RELU ? vec(restore_vec_kernel<E, LNFP8_ACT_RELU, false>) : vec(restore_vec_kernel<E, LNFP8_ACT_NONE, false>);
+    };
+    if (elem == LNFP8_BF16) return by_act(std::integral_constant<int, LNFP8_BF16>());
+    return elem == LNFP8_FP16 ? by_act(std::integral_constant<int, LNFP8_FP16>()) : by_act(std::integral_constant<int, LNFP8_FP32>());
+  }
+  if (elem == LNFP8_BF16) return go(restore_any_kernel<LNFP8_BF16>);
+  return elem == LNFP8_FP16 ? go(restore_any_kernel<LNFP8_FP16>) : go(restore_any_kernel<LNFP8_FP32>);
 }
 
 }  // namespace lnfp8

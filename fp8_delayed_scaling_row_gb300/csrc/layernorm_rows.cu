@@ -63,7 +63,7 @@ struct LnFwdParams {
   uint8_t* codes;
   uint8_t* scales;
   int64_t M, ldx, ldr, ldy, pitch;
-  int D, param_elem;
+  int D, param_elem, dt;  // dt: the lnfp8_dtype of the codes
   float eps;
 };
 
@@ -79,13 +79,13 @@ struct LnBwdParams {
   void* dx;
   float* part;  // [blocks][2][D] column partials
   int64_t M, lddy, ldx, lddres, lddx, pitch;
-  int D, param_elem;
+  int D, param_elem, dt;
 };
 
 // ------------------------------------------------------------ any width, any alignment
 // A group of TPR threads owns a row; thread t holds columns t, t + TPR, ... (so that
 // a warp reads 32 neighbours and a checkpoint block is one warp's value i).
-template <int ELEM, int TPR, int NE, int CK>  // CK: -1 none, else the lnfp8_dtype of the codes
+template <int ELEM, int TPR, int NE, bool CK>  // CK: with a checkpoint
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
 ln_fwd_any_kernel(const LnFwdParams p) {
   constexpr int kThreads = TPR < 256 ? 256 : TPR;
@@ -132,9 +132,9 @@ ln_fwd_any_kernel(const LnFwdParams p) {
         const float ga = load_elem_rt(p.gamma, p.param_elem, c), be = load_elem_rt(p.beta, p.param_elem, c);
         store_elem<ELEM>(p.y, row * p.ldy + c, fmaf(xh, ga, be));
       }
-      if constexpr (CK >= 0) {
-        const uint32_t b = ckpt_byte<CK>(warp_max_u32(in ? abs_bits(xh) : 0u));
-        const uint16_t code = cvt_fp8x2<CK>(xh * ckpt_inv_scale(b), 0.f);
+      if constexpr (CK) {
+        const uint32_t b = ckpt_byte(warp_max_u32(in ? abs_bits(xh) : 0u), p.dt);
+        const uint32_t code = fp8x2(xh * ckpt_inv_scale(b), 0.f, p.dt);
         if (in) p.codes[row * p.D + c] = (uint8_t)code;
         if ((threadIdx.x & 31) == 0 && in) p.scales[row * p.pitch + (c >> 5)] = (uint8_t)b;
       }
@@ -146,7 +146,7 @@ ln_fwd_any_kernel(const LnFwdParams p) {
   }
 }
 
-template <int ELEM, int TPR, int NE, int CK>
+template <int ELEM, int TPR, int NE, bool CK>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
 ln_bwd_any_kernel(const LnBwdParams p) {
   constexpr int kThreads = TPR < 256 ? 256 : TPR;
@@ -165,7 +165,7 @@ ln_bwd_any_kernel(const LnBwdParams p) {
     const int64_t row = row0 + g;
     const bool active = row < p.M;
     const float rs = active ? p.rs[row] : 0.f;
-    const float mu = active && CK < 0 ? p.mu[row] : 0.f;
+    const float mu = active && !CK ? p.mu[row] : 0.f;
     float xh[NE], gg[NE];
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
@@ -174,8 +174,8 @@ ln_bwd_any_kernel(const LnBwdParams p) {
       xh[i] = gg[i] = 0.f;
       if (active && c < p.D) {
         const float d = load_elem<ELEM>(p.dy, row * p.lddy + c);
-        if constexpr (CK >= 0)
-          xh[i] = fp8x2_to_f32<CK>(p.codes[row * p.D + c]).x * ckpt_scale(p.scales[row * p.pitch + (c >> 5)]);
+        if constexpr (CK)
+          xh[i] = fp8x2_to_f32(p.codes[row * p.D + c], p.dt).x * ckpt_scale(p.scales[row * p.pitch + (c >> 5)]);
         else
           xh[i] = (load_elem<ELEM>(p.x, row * p.ldx + c) - mu) * rs;
         accg[i] = fmaf(d, xh[i], accg[i]);
@@ -254,7 +254,7 @@ struct FwdShape {
   static constexpr size_t SMEM = (size_t)RING * WORDS * THREADS * 16;
 };
 
-template <int ELEM, int TPR, int NV, int CK, bool RES>
+template <int ELEM, int TPR, int NV, bool CK, bool RES>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
 ln_fwd_vec_kernel(const LnFwdParams p) {
   using S = FwdShape<ELEM, TPR, NV, RES>;
@@ -358,10 +358,10 @@ ln_fwd_vec_kernel(const LnFwdParams p) {
         for (int k = 0; k < 8; ++k) y[k] = fmaf(v[j][k], ga[j][k], be[j][k]);
         store8<ELEM>(p.y, row * p.ldy + c, y);
       }
-      if constexpr (CK >= 0) {
-        const uint32_t b = ckpt_byte<CK>(block_amax8(v[j]));  // columns past D hold zeros
+      if constexpr (CK) {
+        const uint32_t b = ckpt_byte(block_amax8(v[j]), p.dt);  // columns past D hold zeros
         if (in) {
-          *reinterpret_cast<uint2*>(p.codes + row * p.D + c) = cvt_fp8x8<CK>(v[j], ckpt_inv_scale(b));
+          *reinterpret_cast<uint2*>(p.codes + row * p.D + c) = encode8(v[j], ckpt_inv_scale(b), p.dt);
           if ((t & 3) == 0) p.scales[row * p.pitch + (c >> 5)] = (uint8_t)b;
         }
       }
@@ -374,20 +374,20 @@ ln_fwd_vec_kernel(const LnFwdParams p) {
   cp_wait<0>();
 }
 
-template <int ELEM, int TPR, int NV, int CK, bool RES>
+template <int ELEM, int TPR, int NV, bool CK, bool RES>
 struct BwdShape {
   static constexpr int THREADS = TPR < 256 ? 256 : TPR;
   static constexpr int W = ELEM == LNFP8_FP32 ? 2 : 1;
   // 16-byte words per thread and row: dy, dres, x or the codes (8 bytes a chunk), then one word of
   // scalars (mu, rs) and the scale words
-  static constexpr int X_WORDS = CK >= 0 ? (NV + 1) / 2 : NV * W;
+  static constexpr int X_WORDS = CK ? (NV + 1) / 2 : NV * W;
   static constexpr int WORDS = NV * W * (RES ? 2 : 1) + X_WORDS + 1;
   static constexpr int RING = WORDS <= 6 ? 4 : 3 * WORDS * THREADS * 16 <= 224 * 1024 ? 3 : 2;
   static constexpr size_t SMEM = (size_t)RING * WORDS * THREADS * 16;
   static_assert(SMEM <= 224 * 1024, "shared memory budget");
 };
 
-template <int ELEM, int TPR, int NV, int CK, bool RES>
+template <int ELEM, int TPR, int NV, bool CK, bool RES>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR < 512 ? 2 : 1)
 ln_bwd_vec_kernel(const LnBwdParams p) {
   using S = BwdShape<ELEM, TPR, NV, CK, RES>;
@@ -406,7 +406,7 @@ ln_bwd_vec_kernel(const LnBwdParams p) {
     if (r < p.M) {
       uint32_t* sc = reinterpret_cast<uint32_t*>(at(slot, S0));
       cp4(sc, p.rs + r);
-      if constexpr (CK < 0) cp4(sc + 1, p.mu + r);
+      if constexpr (!CK) cp4(sc + 1, p.mu + r);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int c = (t + TPR * j) * 8;
@@ -414,10 +414,10 @@ ln_bwd_vec_kernel(const LnBwdParams p) {
 #pragma unroll
           for (int k = 0; k < W; ++k) {
             cp16(at(slot, j * W + k), static_cast<const uint8_t*>(p.dy) + (r * p.lddy + c) * ES + 16 * k);
-            if constexpr (CK < 0) cp16(at(slot, X0 + j * W + k), static_cast<const uint8_t*>(p.x) + (r * p.ldx + c) * ES + 16 * k);
+            if constexpr (!CK) cp16(at(slot, X0 + j * W + k), static_cast<const uint8_t*>(p.x) + (r * p.ldx + c) * ES + 16 * k);
             if constexpr (RES) cp16(at(slot, R0 + j * W + k), static_cast<const uint8_t*>(p.dres) + (r * p.lddres + c) * ES + 16 * k);
           }
-          if constexpr (CK >= 0) {
+          if constexpr (CK) {
             cp8(reinterpret_cast<uint2*>(at(slot, X0)) + j, p.codes + r * p.D + c);
             cp4(sc + 2 + j, p.scales + r * p.pitch + ((c >> 7) << 2));
           }
@@ -457,9 +457,9 @@ ln_bwd_vec_kernel(const LnBwdParams p) {
 #pragma unroll
         for (int k = 0; k < W; ++k) u[k] = *at(slot, j * W + k);
         unpack8<ELEM>(u, d);
-        if constexpr (CK >= 0) {
+        if constexpr (CK) {
           const uint4 sc = *at(slot, S0);
-          decode8<CK>(reinterpret_cast<const uint2*>(at(slot, X0))[j], ckpt_scale(((j ? sc.w : sc.z) >> (((c >> 5) & 3) * 8)) & 0xFFu), xh[j]);
+          decode8(reinterpret_cast<const uint2*>(at(slot, X0))[j], ckpt_scale(((j ? sc.w : sc.z) >> (((c >> 5) & 3) * 8)) & 0xFFu), p.dt, xh[j]);
         } else {
           const float mu = __uint_as_float(at(slot, S0)->y);
 #pragma unroll
@@ -566,7 +566,7 @@ lnfp8_status allow_smem(K kernel, size_t smem, const char* who) {
   return LNFP8_OK;
 }
 
-template <int ELEM, int CK>
+template <int ELEM, bool CK>
 lnfp8_status fwd_any(const LnFwdParams& p, cudaStream_t st) {
   auto go = [&](auto kernel, int tpr) {
     const int threads = tpr < 256 ? 256 : tpr, gpb = threads / tpr;
@@ -580,7 +580,7 @@ lnfp8_status fwd_any(const LnFwdParams& p, cudaStream_t st) {
   return go(ln_fwd_any_kernel<ELEM, 1024, 16, CK>, 1024);
 }
 
-template <int ELEM, int CK>
+template <int ELEM, bool CK>
 lnfp8_status bwd_any(const LnBwdParams& p, int* blocks_out, cudaStream_t st) {
   auto go = [&](auto kernel, int tpr) {
     const int threads = tpr < 256 ? 256 : tpr, gpb = threads / tpr;
@@ -606,7 +606,7 @@ int blocks_per_sm(K kernel, int threads, size_t smem) {
   return n;
 }
 
-template <int ELEM, int CK, bool RES>
+template <int ELEM, bool CK, bool RES>
 lnfp8_status fwd_vec(const LnFwdParams& p, cudaStream_t st) {
   auto go = [&](auto kernel, auto shape, int tpr) {
     using S = decltype(shape);
@@ -627,7 +627,7 @@ lnfp8_status fwd_vec(const LnFwdParams& p, cudaStream_t st) {
 #undef FWD
 }
 
-template <int ELEM, int CK, bool RES>
+template <int ELEM, bool CK, bool RES>
 lnfp8_status bwd_vec(const LnBwdParams& p, int* blocks_out, cudaStream_t st) {
   auto go = [&](auto kernel, auto shape, int tpr) {
     using S = decltype(shape);
@@ -653,19 +653,19 @@ lnfp8_status bwd_vec(const LnBwdParams& p, int* blocks_out, cudaStream_t st) {
 // Rows of 16-byte words up to 8192 columns take the vector kernels (beyond, and for any other
 // width or alignment, the kernels above).
 bool row_aligned(const void* p, int64_t ld, int es) { return al(p, 16) && ld * es % 16 == 0; }
-template <int ELEM, int CK>
+template <int ELEM, bool CK>
 lnfp8_status fwd(const LnFwdParams& p, cudaStream_t st) {
   constexpr int es = ElemSize<ELEM>::value;
   const bool vec = p.D % 8 == 0 && p.D <= 8192 && row_aligned(p.x, p.ldx, es) && row_aligned(p.y, p.ldy, es) && al(p.gamma, 16) && al(p.beta, 16) &&
-                   (!p.resid || (row_aligned(p.resid, p.ldr, es) && al(p.xsum, 16))) && (CK < 0 || al(p.codes, 8));
+                   (!p.resid || (row_aligned(p.resid, p.ldr, es) && al(p.xsum, 16))) && (!CK || al(p.codes, 8));
   if (!vec) return fwd_any<ELEM, CK>(p, st);
   return p.resid ? fwd_vec<ELEM, CK, true>(p, st) : fwd_vec<ELEM, CK, false>(p, st);
 }
-template <int ELEM, int CK>
+template <int ELEM, bool CK>
 lnfp8_status bwd(const LnBwdParams& p, int* blocks_out, cudaStream_t st) {
   constexpr int es = ElemSize<ELEM>::value;
   const bool vec = p.D % 8 == 0 && p.D <= 8192 && row_aligned(p.dy, p.lddy, es) && row_aligned(p.dx, p.lddx, es) && al(p.gamma, 16) &&
-                   (!p.dres || row_aligned(p.dres, p.lddres, es)) && (CK < 0 ? row_aligned(p.x, p.ldx, es) : al(p.codes, 8));
+                   (!p.dres || row_aligned(p.dres, p.lddres, es)) && (!CK ? row_aligned(p.x, p.ldx, es) : al(p.codes, 8));
   if (!vec) return bwd_any<ELEM, CK>(p, blocks_out, st);
   return p.dres ? bwd_vec<ELEM, CK, true>(p, blocks_out, st) : bwd_vec<ELEM, CK, false>(p, blocks_out, st);
 }
@@ -686,9 +686,7 @@ lnfp8_status colsum_launch(const float* part, int n, int cols, int split, float*
   return check_launch("column sums");
 }
 
-#define BY_CKPT(ELEM, FN, ...)                                                                   \
-  (ck < 0 ? FN<ELEM, -1>(__VA_ARGS__)                                                            \
-          : ck == LNFP8_E4M3 ? FN<ELEM, LNFP8_E4M3>(__VA_ARGS__) : FN<ELEM, LNFP8_E5M2>(__VA_ARGS__))
+#define BY_CKPT(ELEM, FN, ...) (a->ckpt.codes ? FN<ELEM, true>(__VA_ARGS__) : FN<ELEM, false>(__VA_ARGS__))
 #define BY_ELEM(FN, ...)                                                                         \
   (a->elem == LNFP8_BF16 ? BY_CKPT(LNFP8_BF16, FN, __VA_ARGS__)                                  \
                          : a->elem == LNFP8_FP16 ? BY_CKPT(LNFP8_FP16, FN, __VA_ARGS__) : BY_CKPT(LNFP8_FP32, FN, __VA_ARGS__))
@@ -714,7 +712,7 @@ lnfp8_status layernorm_fwd_launch(const lnfp8_layernorm_fwd_args* a, cudaStream_
   p.D = (int)a->D;
   p.param_elem = a->param_elem;
   p.eps = a->eps;
-  const int ck = a->ckpt.codes ? a->ckpt.dtype : -1;
+  p.dt = a->ckpt.dtype;
   LaunchScope ls("layernorm_fwd", st);
   return BY_ELEM(fwd, p, st);
 }
@@ -745,7 +743,7 @@ lnfp8_status layernorm_bwd_launch(const lnfp8_layernorm_bwd_args* a, cudaStream_
   p.pitch = lnfp8_act_ckpt_scale_pitch(a->D);
   p.D = (int)a->D;
   p.param_elem = a->param_elem;
-  const int ck = a->ckpt.codes ? a->ckpt.dtype : -1;
+  p.dt = a->ckpt.dtype;
   int blocks = 0;
   lnfp8_status s;
   {

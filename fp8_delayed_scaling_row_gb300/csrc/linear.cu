@@ -67,11 +67,6 @@ __device__ __forceinline__ void add16x8(float* v, uint4 u, int f16) {
   }
 }
 
-template <int DT>
-__device__ __forceinline__ uint2 encode8(const float* v, float inv) {
-  return cvt_fp8x8<DT>(v, inv);
-}
-
 // The epilogue of 8 columns n.. of row m. The four lanes of a checkpoint block (32 columns)
 // are neighbours; every lane of the warp calls it (`ok`: inside the tensor).
 __device__ __forceinline__ void epilogue8(const EpiParams& p, float* v, int m, int n, bool ok) {
@@ -88,17 +83,10 @@ __device__ __forceinline__ void epilogue8(const EpiParams& p, float* v, int m, i
   if (p.h && ok)
     *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.h) + row * p.N + n) = pack16x8(v, p.f16);
   if (p.ck >= 0) {
-    uint32_t am = 0;
-    if (ok)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) am = max(am, abs_bits(v[i]));
-    am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
-    am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
-    const uint32_t b = p.ck == LNFP8_E4M3 ? ckpt_byte<LNFP8_E4M3>(am) : ckpt_byte<LNFP8_E5M2>(am);
-    const float inv = ckpt_inv_scale(b);
+    // columns past N hold zeros (no operand, no bias)
+    const uint32_t b = ckpt_byte(block_amax8(v), p.ck);
     if (ok) {
-      const uint2 c = p.ck == LNFP8_E4M3 ? encode8<LNFP8_E4M3>(v, inv) : encode8<LNFP8_E5M2>(v, inv);
-      *reinterpret_cast<uint2*>(p.codes + row * p.N + n) = c;
+      *reinterpret_cast<uint2*>(p.codes + row * p.N + n) = encode8(v, ckpt_inv_scale(b), p.ck);
       if ((n & 31) == 0) p.scales[row * p.pitch + (n >> 5)] = (uint8_t)b;
     }
   }
@@ -298,10 +286,11 @@ struct DactParams {
   float* part;   // [row blocks][N] or NULL; with `both` [row blocks][2][N]: the sums of dz, then of dz as rounded
   int both;
   int64_t M, lddy, pitch;
-  int N, act, rows_per_block;
+  int N, act, dt, rows_per_block;  // dt: the lnfp8_dtype of the codes
 };
 
-template <int ELEM, int SRC>  // SRC: -2 no activation, -1 h as a tensor, else the checkpoint's format
+enum DactSource { DACT_NONE, DACT_TENSOR, DACT_CKPT };  // no activation; h as a tensor; h as a checkpoint
+template <int ELEM, int SRC>
 __global__ void __launch_bounds__(256) lin_dact_kernel(const DactParams p) {
   __shared__ float red[8][32][9];
   pdl_wait();
@@ -322,22 +311,16 @@ __global__ void __launch_bounds__(256) lin_dact_kernel(const DactParams p) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = 0.f;
       add16x8(v, *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.dy) + r * p.lddy + c), f16);
-      if constexpr (SRC >= -1) {
+      if constexpr (SRC != DACT_NONE) {
         float z[8];
-        if constexpr (SRC == -1) {
+        if constexpr (SRC == DACT_TENSOR) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) z[i] = 0.f;
           add16x8(z, *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.h) + r * p.N + c), f16);
         } else {
           const uint2 q = *reinterpret_cast<const uint2*>(p.codes + r * p.N + c);
           const float s = ckpt_scale(p.scales[r * p.pitch + (c >> 5)]);
-          const uint32_t w[4] = {q.x & 0xFFFFu, q.x >> 16, q.y & 0xFFFFu, q.y >> 16};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 t = fp8x2_to_f32<SRC>(w[i]);
-            z[2 * i] = t.x * s;
-            z[2 * i + 1] = t.y * s;
-          }
+          decode8(q, s, p.dt, z);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] *= act_slope(z[i], p.act);
@@ -578,6 +561,7 @@ lnfp8_status linear_act_bwd_launch(const lnfp8_linear_act_bwd_args* a, cudaStrea
     p.pitch = lnfp8_act_ckpt_scale_pitch(a->N);
     p.N = (int)a->N;
     p.act = a->act;
+    p.dt = a->h_ckpt.dtype;
     p.rows_per_block = (int)dact_rows_per_block(a->M, a->N);
     const int64_t row_blocks = (a->M + p.rows_per_block - 1) / p.rows_per_block;
     auto go = [&](auto kernel) {
@@ -588,9 +572,8 @@ lnfp8_status linear_act_bwd_launch(const lnfp8_linear_act_bwd_args* a, cudaStrea
     };
     auto pick = [&](auto elem) {
       constexpr int E = decltype(elem)::value;
-      if (!has_act) return go(lin_dact_kernel<E, -2>);
-      if (!p.codes) return go(lin_dact_kernel<E, -1>);
-      return a->h_ckpt.dtype == LNFP8_E4M3 ? go(lin_dact_kernel<E, LNFP8_E4M3>) : go(lin_dact_kernel<E, LNFP8_E5M2>);
+      if (!has_act) return go(lin_dact_kernel<E, DACT_NONE>);
+      return p.codes ? go(lin_dact_kernel<E, DACT_CKPT>) : go(lin_dact_kernel<E, DACT_TENSOR>);
     };
     lnfp8_status s = a->elem == LNFP8_BF16 ? pick(std::integral_constant<int, LNFP8_BF16>()) : pick(std::integral_constant<int, LNFP8_FP16>());
     if (s != LNFP8_OK) return s;

@@ -301,7 +301,7 @@ lin_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
               const float2 v = up(z[i]);
               am = max(am, max(abs_bits(v.x), abs_bits(v.y)));
             }
-            const uint32_t b = p.ck == LNFP8_E4M3 ? ckpt_byte<LNFP8_E4M3>(am) : ckpt_byte<LNFP8_E5M2>(am);
+            const uint32_t b = ckpt_byte(am, p.ck);
             const float inv = ckpt_inv_scale(b);
             const uint64_t i2 = f2(inv, inv);
             scale_word |= b << (8 * ch);
@@ -309,8 +309,7 @@ lin_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const float2 u = up(mul2(z[2 * i], i2)), v = up(mul2(z[2 * i + 1], i2));
-              q[i] = p.ck == LNFP8_E4M3 ? (uint32_t)cvt_fp8x2<LNFP8_E4M3>(u.x, u.y) | ((uint32_t)cvt_fp8x2<LNFP8_E4M3>(v.x, v.y) << 16)
-                                        : (uint32_t)cvt_fp8x2<LNFP8_E5M2>(u.x, u.y) | ((uint32_t)cvt_fp8x2<LNFP8_E5M2>(v.x, v.y) << 16);
+              q[i] = fp8x2(u.x, u.y, p.ck) | (fp8x2(v.x, v.y, p.ck) << 16);
             }
             if (m < p.M) {
               uint8_t* dst = p.codes + (int64_t)m * p.N + n0;

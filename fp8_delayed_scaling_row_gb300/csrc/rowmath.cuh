@@ -131,9 +131,8 @@ __device__ __forceinline__ float elem_max() {
 // ------------------------------------------------------------ checkpoint blocks
 // The scale byte of a block whose largest |v| has these fp32 bits (NaN > Inf > finite):
 // the largest value of the format is 1.75 * 2^top, top = 8 (E4M3) or 15 (E5M2).
-template <int DT>
-__device__ __forceinline__ uint32_t ckpt_byte(uint32_t amax_bits) {
-  constexpr int top = DT == LNFP8_E4M3 ? 8 : 15;
+__device__ __forceinline__ uint32_t ckpt_byte(uint32_t amax_bits, int dt) {
+  const int top = dt == LNFP8_E4M3 ? 8 : 15;
   const int e = (int)(amax_bits >> 23);
   if (e == 255) return 255u;
   const int b = e - top + ((amax_bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
@@ -150,20 +149,27 @@ __device__ __forceinline__ float ckpt_scale(uint32_t b) {
   return __uint_as_float(b == 0u ? 0x00400000u : b == 255u ? 0x7FFFFFFFu : b << 23);
 }
 
+// The codes' format is a run-time argument: it selects one of two conversions, uniformly.
+__device__ __forceinline__ uint32_t fp8x2(float a, float b, int dt) {
+  return dt == LNFP8_E4M3 ? cvt_fp8x2<LNFP8_E4M3>(a, b) : cvt_fp8x2<LNFP8_E5M2>(a, b);
+}
+// Eight values times inv -> eight codes.
+__device__ __forceinline__ uint2 encode8(const float* v, float inv, int dt) {
+  return dt == LNFP8_E4M3 ? cvt_fp8x8<LNFP8_E4M3>(v, inv) : cvt_fp8x8<LNFP8_E5M2>(v, inv);
+}
 // Two codes (low byte first) -> two fp32, exactly (both formats are subsets of fp16).
-template <int DT>
-__device__ __forceinline__ float2 fp8x2_to_f32(uint32_t codes) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, DT == LNFP8_E4M3 ? __NV_E4M3 : __NV_E5M2);
+__device__ __forceinline__ float2 fp8x2_to_f32(uint32_t codes, int dt) {
+  const __half2_raw h = dt == LNFP8_E4M3 ? __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3)
+                                         : __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E5M2);
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
 // Eight codes (a uint2, low byte first) times their block's scale.
-template <int DT>
-__device__ __forceinline__ void decode8(uint2 q, float scale, float* v) {
+__device__ __forceinline__ void decode8(uint2 q, float scale, int dt, float* v) {
   const uint32_t w[4] = {q.x & 0xFFFFu, q.x >> 16, q.y & 0xFFFFu, q.y >> 16};
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const float2 f = fp8x2_to_f32<DT>(w[k]);
+    const float2 f = fp8x2_to_f32(w[k], dt);
     v[2 * k] = f.x * scale;
     v[2 * k + 1] = f.y * scale;
   }
