@@ -20,22 +20,36 @@ namespace {
 
 constexpr int kMaxD = 16384;
 
+// Sums of two values over a warp in 6 shuffles: the halves of the warp first swap, so that each
+// goes on with one of the two.
+__device__ __forceinline__ float2 warp_sum2(float a, float b) {
+  const bool hi = (threadIdx.x & 16) != 0;
+  float v = (hi ? b : a) + __shfl_xor_sync(0xFFFFFFFFu, hi ? a : b, 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  const float w = __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+  return hi ? make_float2(w, v) : make_float2(v, w);
+}
+
 // Sum over the TPR threads of a row group; every thread gets the result. `xch`
 // holds two buffers of 32 floats per group, used in turn (`turn` counts the sums),
 // so that one barrier per sum is enough.
 template <int TPR>
+__device__ __forceinline__ void group_sync() {
+  if constexpr (TPR == 1024) __syncthreads();
+  else asm volatile("bar.sync %0, %1;" ::"r"((int)threadIdx.x / TPR + 1), "r"(TPR) : "memory");
+}
+template <int TPR>
 __device__ __forceinline__ float2 row_sum2(float a, float b, float2* xch, int& turn) {
-  a = warp_sum(a);
-  b = warp_sum(b);
+  const float2 s = warp_sum2(a, b);
   if constexpr (TPR == 32) {
-    return make_float2(a, b);
+    return s;
   } else {
     constexpr int W = TPR / 32;
     const int group = threadIdx.x / TPR, w = (threadIdx.x % TPR) / 32, lane = threadIdx.x & 31;
     float2* buf = xch + (group * 2 + (turn++ & 1)) * W;
-    if (lane == 0) buf[w] = make_float2(a, b);
-    if constexpr (TPR == 1024) __syncthreads();
-    else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(TPR) : "memory");
+    if (lane == 0) buf[w] = s;
+    group_sync<TPR>();
     if constexpr (W <= 8) {
       float sa = 0.f, sb = 0.f;
 #pragma unroll
@@ -46,7 +60,28 @@ __device__ __forceinline__ float2 row_sum2(float a, float b, float2* xch, int& t
       return make_float2(sa, sb);
     } else {
       const float2 v = lane < W ? buf[lane] : make_float2(0.f, 0.f);
-      return make_float2(warp_sum(v.x), warp_sum(v.y));
+      return warp_sum2(v.x, v.y);
+    }
+  }
+}
+template <int TPR>
+__device__ __forceinline__ float row_sum(float a, float2* xch, int& turn) {
+  a = warp_sum(a);
+  if constexpr (TPR == 32) {
+    return a;
+  } else {
+    constexpr int W = TPR / 32;
+    const int group = threadIdx.x / TPR, w = (threadIdx.x % TPR) / 32, lane = threadIdx.x & 31;
+    float* buf = reinterpret_cast<float*>(xch + (group * 2 + (turn++ & 1)) * W);
+    if (lane == 0) buf[w] = a;
+    group_sync<TPR>();
+    if constexpr (W <= 8) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < W; ++i) s += buf[i];
+      return s;
+    } else {
+      return warp_sum(lane < W ? buf[lane] : 0.f);
     }
   }
 }
@@ -64,6 +99,7 @@ struct LnFwdParams {
   uint8_t* scales;
   int64_t M, ldx, ldr, ldy, pitch;
   int D, param_elem, dt;  // dt: the lnfp8_dtype of the codes
+  int64_t step, xstep, rstep, ystep, hstep, cstep, sstep;  // rows a group moves on by; the same in bytes of each tensor
   float eps;
 };
 
@@ -80,6 +116,7 @@ struct LnBwdParams {
   float* part;  // [blocks][2][D] column partials
   int64_t M, lddy, ldx, lddres, lddx, pitch;
   int D, param_elem, dt;
+  int64_t step, dstep, xstep, rstep, ostep, cstep, sstep;
 };
 
 // ------------------------------------------------------------ any width, any alignment
@@ -114,14 +151,14 @@ ln_fwd_any_kernel(const LnFwdParams p) {
       }
       s += v[i];
     }
-    const float mu = row_sum2<TPR>(s, 0.f, xch, turn).x * inv_d;
+    const float mu = row_sum<TPR>(s, xch, turn) * inv_d;
     float q = 0.f;
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
       v[i] -= mu;
       if (t + TPR * i < p.D) q = fmaf(v[i], v[i], q);
     }
-    const float rs = 1.0f / sqrtf(row_sum2<TPR>(q, 0.f, xch, turn).x * inv_d + p.eps);
+    const float rs = rsqrt_nr(row_sum<TPR>(q, xch, turn) * inv_d + p.eps);
     if (!active) continue;  // uniform over the row group; the barriers above are behind it
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
@@ -230,14 +267,29 @@ ln_bwd_any_kernel(const LnBwdParams p) {
 // bound by HBM: each thread copies (cp.async) the chunks of its next RING - 1 rows into its own
 // slots of a shared-memory ring, so the bytes in flight cost no registers, and a slot is
 // refilled one row after it was read. Four neighbouring lanes hold a checkpoint block.
-__device__ __forceinline__ void cp16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp8(void* dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+__device__ __forceinline__ void cp8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp4(void* dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds4(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -264,30 +316,33 @@ ln_fwd_vec_kernel(const LnFwdParams p) {
   const int g = threadIdx.x / TPR, t = threadIdx.x % TPR;
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t stride = (int64_t)gridDim.x * GPB;
   constexpr int ES = ElemSize<ELEM>::value;
-  auto issue = [&](int64_t r, int slot) {
+  constexpr uint32_t WB = T * 16, SB = S::WORDS * WB;  // bytes of a word of all threads, of a slot
+  const uint32_t mine = (uint32_t)__cvta_generic_to_shared(ring) + threadIdx.x * 16;
+  int64_t row = (int64_t)blockIdx.x * GPB + g;
+  // this thread's first chunk in the row to be loaded next: the pointers run ahead of `row`
+  const uint8_t* xp = static_cast<const uint8_t*>(p.x) + (row * p.ldx + t * 8) * ES;
+  const uint8_t* rp = RES ? static_cast<const uint8_t*>(p.resid) + (row * p.ldr + t * 8) * ES : nullptr;
+  auto issue = [&](int64_t r, uint32_t slot) {
     if (r < p.M) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int c = (t + TPR * j) * 8;
-        if (c < p.D) {
+        if ((t + TPR * j) * 8 < p.D) {
 #pragma unroll
           for (int k = 0; k < W; ++k) {
-            cp16(&ring[(slot * S::WORDS + j * W + k) * T + threadIdx.x], static_cast<const uint8_t*>(p.x) + (r * p.ldx + c) * ES + 16 * k);
-            if constexpr (RES)
-              cp16(&ring[(slot * S::WORDS + (NV + j) * W + k) * T + threadIdx.x],
-                   static_cast<const uint8_t*>(p.resid) + (r * p.ldr + c) * ES + 16 * k);
+            cp16(slot + (j * W + k) * WB, xp + TPR * j * 8 * ES + 16 * k);
+            if constexpr (RES) cp16(slot + ((NV + j) * W + k) * WB, rp + TPR * j * 8 * ES + 16 * k);
           }
         }
       }
+      xp += p.xstep;
+      if constexpr (RES) rp += p.rstep;
     }
     cp_commit();
   };
-  int64_t row = (int64_t)blockIdx.x * GPB + g;
 #pragma unroll
-  for (int k = 0; k < P; ++k) issue(row + k * stride, k);
-  float ga[NV][8], be[NV][8];
+  for (int k = 0; k < P; ++k) issue(row + k * p.step, mine + k * SB);
+  uint64_t ga[NV][4], be[NV][4];  // pairs of columns
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int c = (t + TPR * j) * 8;
@@ -297,78 +352,94 @@ ln_fwd_vec_kernel(const LnFwdParams p) {
     }
   }
   const float inv_d = 1.0f / (float)p.D;
-  int turn = 0, slot = 0;
-  for (; row - g < p.M; row += stride) {  // the same trip count for every group of the block
-    issue(row + P * stride, slot == 0 ? RING - 1 : slot - 1);
+  int turn = 0;
+  uint32_t slot = mine, last = mine + P * SB;  // the row's slot; the one read before it, filled next
+  // the chunk's place in the outputs, advanced row by row
+  uint8_t* yp = static_cast<uint8_t*>(p.y) + (row * p.ldy + t * 8) * ES;
+  uint8_t* hp = RES ? static_cast<uint8_t*>(p.xsum) + (row * p.D + t * 8) * ES : nullptr;
+  uint8_t* cp = CK ? p.codes + row * p.D + t * 8 : nullptr;
+  uint8_t* sp8 = CK ? p.scales + row * p.pitch + (t >> 2) : nullptr;
+  for (; row - g < p.M; row += p.step) {  // the same trip count for every group of the block
+    issue(row + P * p.step, last);
     cp_wait<P>();
     const bool active = row < p.M;
-    float v[NV][8];
-    float s = 0.f;
+    uint64_t v[NV][4];
+    uint64_t s2 = 0;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (t + TPR * j) * 8;
-      const bool ok = active && c < p.D;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[j][k] = 0.f;
-      if (ok) {
+      for (int k = 0; k < 4; ++k) v[j][k] = 0;
+      if (active && c < p.D) {
         uint4 u[W];
 #pragma unroll
-        for (int k = 0; k < W; ++k) u[k] = ring[(slot * S::WORDS + j * W + k) * T + threadIdx.x];
+        for (int k = 0; k < W; ++k) u[k] = lds16(slot + (j * W + k) * WB);
         unpack8<ELEM>(u, v[j]);
         if constexpr (RES) {
-          float r[8];
+          uint64_t r[4];
 #pragma unroll
-          for (int k = 0; k < W; ++k) u[k] = ring[(slot * S::WORDS + (NV + j) * W + k) * T + threadIdx.x];
+          for (int k = 0; k < W; ++k) u[k] = lds16(slot + ((NV + j) * W + k) * WB);
           unpack8<ELEM>(u, r);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) v[j][k] += r[k];
+          for (int k = 0; k < 4; ++k) v[j][k] = add_2(v[j][k], r[k]);
           pack8<ELEM>(v[j], u);
           unpack8<ELEM>(u, v[j]);  // normalised as it is kept
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.xsum) + (row * p.D + c) * ES);
+          uint4* dst = reinterpret_cast<uint4*>(hp + TPR * j * 8 * ES);
 #pragma unroll
           for (int k = 0; k < W; ++k) dst[k] = u[k];
         }
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) s += v[j][k];
+      for (int k = 0; k < 4; ++k) s2 = add_2(s2, v[j][k]);
     }
-    slot = slot + 1 == RING ? 0 : slot + 1;
-    const float mu = row_sum2<TPR>(s, 0.f, xch, turn).x * inv_d;
-    float q = 0.f;
+    last = slot;
+    slot = slot == mine + P * SB ? mine : slot + SB;
+    const float2 sp = upk(s2);
+    const float mu = row_sum<TPR>(sp.x + sp.y, xch, turn) * inv_d;
+    const uint64_t mu2 = pk(mu, mu);
+    uint64_t q2 = 0;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
       if ((t + TPR * j) * 8 < p.D) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          v[j][k] -= mu;
-          q = fmaf(v[j][k], v[j][k], q);
+        for (int k = 0; k < 4; ++k) {
+          v[j][k] = sub_2(v[j][k], mu2);
+          q2 = fma_2(v[j][k], v[j][k], q2);
         }
       }
-    const float rs = 1.0f / sqrtf(row_sum2<TPR>(q, 0.f, xch, turn).x * inv_d + p.eps);
+    const float2 qp = upk(q2);
+    const float rs = rsqrt_nr(row_sum<TPR>(qp.x + qp.y, xch, turn) * inv_d + p.eps);
     if (!active) continue;  // uniform over the row group
+    const uint64_t rs2 = pk(rs, rs);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (t + TPR * j) * 8;
       const bool in = c < p.D;
-      float y[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[j][k] *= rs;
+      for (int k = 0; k < 4; ++k) v[j][k] = mul_2(v[j][k], rs2);
       if (in) {
+        uint64_t y[4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] = fmaf(v[j][k], ga[j][k], be[j][k]);
-        store8<ELEM>(p.y, row * p.ldy + c, y);
+        for (int k = 0; k < 4; ++k) y[k] = fma_2(v[j][k], ga[j][k], be[j][k]);
+        store8<ELEM>(yp, TPR * j * 8, y);
       }
       if constexpr (CK) {
         const uint32_t b = ckpt_byte(block_amax8(v[j]), p.dt);  // columns past D hold zeros
         if (in) {
-          *reinterpret_cast<uint2*>(p.codes + row * p.D + c) = encode8(v[j], ckpt_inv_scale(b), p.dt);
-          if ((t & 3) == 0) p.scales[row * p.pitch + (c >> 5)] = (uint8_t)b;
+          *reinterpret_cast<uint2*>(cp + TPR * j * 8) = encode8(v[j], ckpt_inv_scale(b), p.dt);
+          if ((t & 3) == 0) sp8[TPR / 4 * j] = (uint8_t)b;
         }
       }
     }
     if (t == 0) {
       p.mu[row] = mu;
       p.rs[row] = rs;
+    }
+    yp += p.ystep;
+    if constexpr (RES) hp += p.hstep;
+    if constexpr (CK) {
+      cp += p.cstep;
+      sp8 += p.sstep;
     }
   }
   cp_wait<0>();
@@ -378,12 +449,12 @@ template <int ELEM, int TPR, int NV, bool CK, bool RES>
 struct BwdShape {
   static constexpr int THREADS = TPR < 256 ? 256 : TPR;
   static constexpr int W = ELEM == LNFP8_FP32 ? 2 : 1;
-  // 16-byte words per thread and row: dy, dres, x or the codes (8 bytes a chunk), then one word of
-  // scalars (mu, rs) and the scale words
-  static constexpr int X_WORDS = CK ? (NV + 1) / 2 : NV * W;
-  static constexpr int WORDS = NV * W * (RES ? 2 : 1) + X_WORDS + 1;
-  static constexpr int RING = WORDS <= 6 ? 4 : 3 * WORDS * THREADS * 16 <= 224 * 1024 ? 3 : 2;
-  static constexpr size_t SMEM = (size_t)RING * WORDS * THREADS * 16;
+  // bytes per thread and row, each kind an array over the threads (so that a warp's accesses fill whole
+  // lines of banks): dy, x or the codes, dres, then rsigma and mu or the scale words
+  static constexpr int X_OFF = NV * W * 16, R_OFF = X_OFF + (CK ? NV * 8 : NV * W * 16);
+  static constexpr int S_OFF = R_OFF + (RES ? NV * W * 16 : 0), BYTES = S_OFF + 4 + (CK ? NV * 4 : 4);
+  static constexpr int RING = 4 * BYTES * THREADS <= 104 * 1024 ? 4 : 3 * BYTES * THREADS <= 224 * 1024 ? 3 : 2;
+  static constexpr size_t SMEM = (size_t)RING * BYTES * THREADS;
   static_assert(SMEM <= 224 * 1024, "shared memory budget");
 };
 
@@ -392,115 +463,133 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR < 512 ? 2 : 1)
 ln_bwd_vec_kernel(const LnBwdParams p) {
   using S = BwdShape<ELEM, TPR, NV, CK, RES>;
   constexpr int T = S::THREADS, GPB = T / TPR, W = S::W, RING = S::RING, P = RING - 1;
-  constexpr int X0 = NV * W, R0 = X0 + S::X_WORDS, S0 = S::WORDS - 1;  // word offsets in a slot: dy, x, dres, scalars
-  static_assert(NV <= 2, "two scale words beside mu and rsigma");
   __shared__ float2 xch[2 * T / 32];
-  extern __shared__ uint4 ring[];
+  extern __shared__ uint4 ring[];  // [RING][BYTES * T]
   const int g = threadIdx.x / TPR, t = threadIdx.x % TPR;
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t stride = (int64_t)gridDim.x * GPB;
   constexpr int ES = ElemSize<ELEM>::value;
-  auto at = [&](int slot, int w) { return &ring[(slot * S::WORDS + w) * T + threadIdx.x]; };
-  auto issue = [&](int64_t r, int slot) {
+  constexpr uint32_t SB = S::BYTES * T;
+  const uint32_t base = (uint32_t)__cvta_generic_to_shared(ring);
+  const uint32_t t16 = threadIdx.x * 16, t8 = S::X_OFF * T + threadIdx.x * 8, t4 = S::S_OFF * T + threadIdx.x * 4;
+  int64_t row = (int64_t)blockIdx.x * GPB + g;
+  // this thread's first chunk in the row to be loaded next: the pointers run ahead of `row`
+  const uint8_t* dp = static_cast<const uint8_t*>(p.dy) + (row * p.lddy + t * 8) * ES;
+  const uint8_t* xp = CK ? p.codes + row * p.D + t * 8 : static_cast<const uint8_t*>(p.x) + (row * p.ldx + t * 8) * ES;
+  const uint8_t* bp = CK ? p.scales + row * p.pitch + ((t >> 4) << 2) : nullptr;  // the word of this chunk's scale byte
+  const uint8_t* rp = RES ? static_cast<const uint8_t*>(p.dres) + (row * p.lddres + t * 8) * ES : nullptr;
+  const float* mp = p.mu + row;
+  const float* sp = p.rs + row;
+  auto issue = [&](int64_t r, uint32_t slot) {
     if (r < p.M) {
-      uint32_t* sc = reinterpret_cast<uint32_t*>(at(slot, S0));
-      cp4(sc, p.rs + r);
-      if constexpr (!CK) cp4(sc + 1, p.mu + r);
+      cp4(slot + t4, sp);
+      if constexpr (!CK) cp4(slot + t4 + 4 * T, mp);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int c = (t + TPR * j) * 8;
-        if (c < p.D) {
+        if ((t + TPR * j) * 8 < p.D) {
 #pragma unroll
           for (int k = 0; k < W; ++k) {
-            cp16(at(slot, j * W + k), static_cast<const uint8_t*>(p.dy) + (r * p.lddy + c) * ES + 16 * k);
-            if constexpr (!CK) cp16(at(slot, X0 + j * W + k), static_cast<const uint8_t*>(p.x) + (r * p.ldx + c) * ES + 16 * k);
-            if constexpr (RES) cp16(at(slot, R0 + j * W + k), static_cast<const uint8_t*>(p.dres) + (r * p.lddres + c) * ES + 16 * k);
+            cp16(slot + t16 + (j * W + k) * 16 * T, dp + TPR * j * 8 * ES + 16 * k);
+            if constexpr (!CK) cp16(slot + t16 + (S::X_OFF + (j * W + k) * 16) * T, xp + TPR * j * 8 * ES + 16 * k);
+            if constexpr (RES) cp16(slot + t16 + (S::R_OFF + (j * W + k) * 16) * T, rp + TPR * j * 8 * ES + 16 * k);
           }
           if constexpr (CK) {
-            cp8(reinterpret_cast<uint2*>(at(slot, X0)) + j, p.codes + r * p.D + c);
-            cp4(sc + 2 + j, p.scales + r * p.pitch + ((c >> 7) << 2));
+            cp8(slot + t8 + j * 8 * T, xp + TPR * j * 8);
+            cp4(slot + t4 + (4 + 4 * j) * T, bp + TPR / 16 * j * 4);
           }
         }
       }
+      dp += p.dstep;
+      xp += CK ? p.cstep : p.xstep;
+      if constexpr (CK) bp += p.sstep;
+      if constexpr (RES) rp += p.rstep;
+      if constexpr (!CK) mp += p.step;
+      sp += p.step;
     }
     cp_commit();
   };
-  int64_t row = (int64_t)blockIdx.x * GPB + g;
 #pragma unroll
-  for (int k = 0; k < P; ++k) issue(row + k * stride, k);
-  float ga[NV][8], accg[NV][8], accb[NV][8];
+  for (int k = 0; k < P; ++k) issue(row + k * p.step, base + k * SB);
+  uint64_t ga[NV][4], accg[NV][4], accb[NV][4];  // pairs of columns
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) ga[j][k] = accg[j][k] = accb[j][k] = 0.f;
+    for (int k = 0; k < 4; ++k) ga[j][k] = accg[j][k] = accb[j][k] = 0;
     const int c = (t + TPR * j) * 8;
     if (c < p.D) load8_rt(p.gamma, p.param_elem, c, ga[j]);
   }
   const float inv_d = 1.0f / (float)p.D;
-  int turn = 0, slot = 0;
-  for (; row - g < p.M; row += stride) {
-    issue(row + P * stride, slot == 0 ? RING - 1 : slot - 1);
+  int turn = 0;
+  uint32_t slot = base, last = base + P * SB;
+  const int byte = ((t >> 2) & 3) * 8;  // of this thread's scale in its word, the same in every chunk (TPR is a multiple of 16)
+  uint8_t* op = static_cast<uint8_t*>(p.dx) + (row * p.lddx + t * 8) * ES;
+  for (; row - g < p.M; row += p.step) {
+    issue(row + P * p.step, last);
     cp_wait<P>();
     const bool active = row < p.M;
-    float xh[NV][8], gg[NV][8];
-    float rs = 0.f, s1 = 0.f, s2 = 0.f;
-    if (active) rs = __uint_as_float(at(slot, S0)->x);
+    uint64_t xh[NV][4], gg[NV][4];
+    uint64_t a1 = 0, a2 = 0;
+    const float rs = active ? __uint_as_float(lds4(slot + t4)) : 0.f;
+    const uint64_t rs2 = pk(rs, rs);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (t + TPR * j) * 8;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) xh[j][k] = gg[j][k] = 0.f;
+      for (int k = 0; k < 4; ++k) xh[j][k] = gg[j][k] = 0;
       if (active && c < p.D) {
         uint4 u[W];
-        float d[8];
+        uint64_t d[4];
 #pragma unroll
-        for (int k = 0; k < W; ++k) u[k] = *at(slot, j * W + k);
+        for (int k = 0; k < W; ++k) u[k] = lds16(slot + t16 + (j * W + k) * 16 * T);
         unpack8<ELEM>(u, d);
         if constexpr (CK) {
-          const uint4 sc = *at(slot, S0);
-          decode8(reinterpret_cast<const uint2*>(at(slot, X0))[j], ckpt_scale(((j ? sc.w : sc.z) >> (((c >> 5) & 3) * 8)) & 0xFFu), p.dt, xh[j]);
+          decode8(lds8(slot + t8 + j * 8 * T), ckpt_scale((lds4(slot + t4 + (4 + 4 * j) * T) >> byte) & 0xFFu), p.dt, xh[j]);
         } else {
-          const float mu = __uint_as_float(at(slot, S0)->y);
+          const float mu = __uint_as_float(lds4(slot + t4 + 4 * T));
+          const uint64_t mu2 = pk(mu, mu);
 #pragma unroll
-          for (int k = 0; k < W; ++k) u[k] = *at(slot, X0 + j * W + k);
+          for (int k = 0; k < W; ++k) u[k] = lds16(slot + t16 + (S::X_OFF + (j * W + k) * 16) * T);
           unpack8<ELEM>(u, xh[j]);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) xh[j][k] = (xh[j][k] - mu) * rs;
+          for (int k = 0; k < 4; ++k) xh[j][k] = mul_2(sub_2(xh[j][k], mu2), rs2);
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          gg[j][k] = d[k] * ga[j][k];
-          accg[j][k] = fmaf(d[k], xh[j][k], accg[j][k]);
-          accb[j][k] += d[k];
-          s1 += gg[j][k];
-          s2 = fmaf(gg[j][k], xh[j][k], s2);
+        for (int k = 0; k < 4; ++k) {
+          gg[j][k] = mul_2(d[k], ga[j][k]);
+          accg[j][k] = fma_2(d[k], xh[j][k], accg[j][k]);
+          accb[j][k] = add_2(accb[j][k], d[k]);
+          a1 = add_2(a1, gg[j][k]);
+          a2 = fma_2(gg[j][k], xh[j][k], a2);
         }
       }
     }
-    const float2 sums = row_sum2<TPR>(s1, s2, xch, turn);
+    const float2 p1 = upk(a1), p2 = upk(a2);
+    const float2 sums = row_sum2<TPR>(p1.x + p1.y, p2.x + p2.y, xch, turn);
     const float mg = sums.x * inv_d, nmx = -sums.y * inv_d;
     if (active) {
+      const uint64_t mg2 = pk(mg, mg), nmx2 = pk(nmx, nmx);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int c = (t + TPR * j) * 8;
         if (c >= p.D) continue;
-        float o[8];
+        uint64_t o[4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) o[k] = fmaf(nmx, xh[j][k], gg[j][k] - mg) * rs;
+        for (int k = 0; k < 4; ++k) o[k] = mul_2(fma_2(nmx2, xh[j][k], sub_2(gg[j][k], mg2)), rs2);
         if constexpr (RES) {
           uint4 u[W];
-          float r[8];
+          uint64_t r[4];
 #pragma unroll
-          for (int k = 0; k < W; ++k) u[k] = *at(slot, R0 + j * W + k);
+          for (int k = 0; k < W; ++k) u[k] = lds16(slot + t16 + (S::R_OFF + (j * W + k) * 16) * T);
           unpack8<ELEM>(u, r);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) o[k] += r[k];
+          for (int k = 0; k < 4; ++k) o[k] = add_2(o[k], r[k]);
         }
-        store8<ELEM>(p.dx, row * p.lddx + c, o);
+        store8<ELEM>(op, TPR * j * 8, o);
       }
     }
-    slot = slot + 1 == RING ? 0 : slot + 1;
+    op += p.ostep;
+    last = slot;
+    slot = slot == base + P * SB ? base : slot + SB;
   }
   cp_wait<0>();
   // column partials: the row groups add theirs in turn in the ring's memory
@@ -516,9 +605,10 @@ ln_bwd_vec_kernel(const LnBwdParams p) {
       if (c >= p.D) continue;
 #pragma unroll
       for (int h = 0; h < 4; ++h) {  // dgamma then dbeta, 4 columns at a time
-        float* acc = h < 2 ? accg[j] + 4 * h : accb[j] + 4 * (h - 2);
+        const uint64_t* acc = h < 2 ? accg[j] + 2 * h : accb[j] + 2 * (h - 2);
         const int at_c = (h < 2 ? 0 : p.D) + c + 4 * (h & 1);
-        float4 v = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        const float2 lo = upk(acc[0]), hi = upk(acc[1]);
+        float4 v = make_float4(lo.x, lo.y, hi.x, hi.y);
         if (turn_g > 0) {
           const float4 o = *reinterpret_cast<const float4*>(red + at_c);
           v = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
@@ -530,28 +620,29 @@ ln_bwd_vec_kernel(const LnBwdParams p) {
   }
 }
 
-// dst[c] = sum over n partial rows of part[i][c], c < cols, in a fixed order: 32 columns
-// per block, 8 warps each adding every eighth row, then the warps' sums in order.
-__global__ void __launch_bounds__(256) colsum_kernel(const float* __restrict__ part, int n, int cols, int split,
-                                                     float* __restrict__ a, float* __restrict__ b) {
-  __shared__ float red[8][33];
+// Sums over n partial rows of `cols` floats in a fixed order: 32 columns per block, warp w adds rows
+// w, w + 32, ..., then the warps' sums are added over the lanes of a warp. A few hundred rows leave
+// each thread about ten loads, all in flight at once: with 8 warps a block it took 9.9 us for
+// 304 x 1536, cold, against 5.
+__global__ void __launch_bounds__(1024) colsum_kernel(const float* __restrict__ part, int n, int cols, int split,
+                                                      float* __restrict__ a, float* __restrict__ b) {
+  __shared__ float red[32][33];
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float s = 0.f;
   if (c < cols) {
-#pragma unroll 8
-    for (int i = w; i < n; i += 8) s += part[(int64_t)i * cols + c];
+#pragma unroll 10
+    for (int i = w; i < n; i += 32) s += __ldcs(part + (int64_t)i * cols + c);
   }
   red[w][lane] = s;
   __syncthreads();
-  if (w == 0 && c < cols) {
-    s = red[0][lane];
-#pragma unroll
-    for (int k = 1; k < 8; ++k) s += red[k][lane];
-    if (c < split) a[c] = s;
-    else b[c - split] = s;
+  s = warp_sum(red[lane][w]);  // warp w: column w of the block
+  const int cw = blockIdx.x * 32 + w;
+  if (lane == 0 && cw < cols) {
+    if (cw < split) a[cw] = s;
+    else b[cw - split] = s;
   }
 }
 
@@ -614,7 +705,16 @@ lnfp8_status fwd_vec(const LnFwdParams& p, cudaStream_t st) {
       return check_launch("layernorm_fwd: shared memory");
     const int gpb = S::THREADS / tpr;
     const int64_t blocks = min64((p.M + gpb - 1) / gpb, (int64_t)num_sms() * blocks_per_sm(kernel, S::THREADS, S::SMEM));
-    if (launch_pdl(kernel, dim3((unsigned)blocks), dim3(S::THREADS), S::SMEM, st, p) != cudaSuccess) return check_launch("layernorm_fwd launch");
+    constexpr int es = ElemSize<ELEM>::value;
+    LnFwdParams q = p;
+    q.step = blocks * gpb;
+    q.xstep = q.step * p.ldx * es;
+    q.rstep = q.step * p.ldr * es;
+    q.ystep = q.step * p.ldy * es;
+    q.hstep = q.step * p.D * es;
+    q.cstep = q.step * p.D;
+    q.sstep = q.step * p.pitch;
+    if (launch_pdl(kernel, dim3((unsigned)blocks), dim3(S::THREADS), S::SMEM, st, q) != cudaSuccess) return check_launch("layernorm_fwd launch");
     return check_launch("layernorm_fwd");
   };
 #define FWD(TPR, NV) go(ln_fwd_vec_kernel<ELEM, TPR, NV, CK, RES>, FwdShape<ELEM, TPR, NV, RES>(), TPR)
@@ -637,7 +737,16 @@ lnfp8_status bwd_vec(const LnBwdParams& p, int* blocks_out, cudaStream_t st) {
       return check_launch("layernorm_bwd: shared memory");
     const int64_t blocks = min64((p.M + gpb - 1) / gpb, (int64_t)num_sms() * std::min(kBwdBlocksPerSm, blocks_per_sm(kernel, S::THREADS, smem)));
     *blocks_out = (int)blocks;
-    if (launch_pdl(kernel, dim3((unsigned)blocks), dim3(S::THREADS), smem, st, p) != cudaSuccess) return check_launch("layernorm_bwd launch");
+    constexpr int es = ElemSize<ELEM>::value;
+    LnBwdParams q = p;
+    q.step = blocks * gpb;
+    q.dstep = q.step * p.lddy * es;
+    q.xstep = q.step * p.ldx * es;
+    q.rstep = q.step * p.lddres * es;
+    q.ostep = q.step * p.lddx * es;
+    q.cstep = q.step * p.D;
+    q.sstep = q.step * p.pitch;
+    if (launch_pdl(kernel, dim3((unsigned)blocks), dim3(S::THREADS), smem, st, q) != cudaSuccess) return check_launch("layernorm_bwd launch");
     return check_launch("layernorm_bwd");
   };
 #define BWD(TPR, NV) go(ln_bwd_vec_kernel<ELEM, TPR, NV, CK, RES>, BwdShape<ELEM, TPR, NV, CK, RES>(), TPR)
@@ -681,7 +790,7 @@ int64_t layernorm_bwd_ws_bytes(int64_t M, int64_t D) {
 
 lnfp8_status colsum_launch(const float* part, int n, int cols, int split, float* a, float* b, cudaStream_t st) {
   LaunchScope ls("colsum", st);
-  if (launch_pdl(colsum_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(256), 0, st, part, n, cols, split, a, b) != cudaSuccess)
+  if (launch_pdl(colsum_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(1024), 0, st, part, n, cols, split, a, b) != cudaSuccess)
     return check_launch("column sums launch");
   return check_launch("column sums");
 }

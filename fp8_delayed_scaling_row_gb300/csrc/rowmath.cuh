@@ -50,6 +50,38 @@ __device__ __forceinline__ float round_elem(float v) {
   else return __bfloat162float(__float2bfloat16_rn(v));
 }
 
+// Packed fp32 pairs: the f32x2 instructions give two IEEE round-to-nearest results each.
+__device__ __forceinline__ uint64_t pk(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 upk(uint64_t r) {
+  float2 v;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(r));
+  return v;
+}
+__device__ __forceinline__ uint64_t fma_2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul_2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t sub_2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // Eight neighbouring elements: one (16-bit types) or two (fp32) 16-byte words.
 template <int ELEM>
 __device__ __forceinline__ void unpack8(const uint4* u, float* v) {
@@ -96,6 +128,25 @@ __device__ __forceinline__ void pack8(const float* v, uint4* u) {
     *u = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
+// The same as four pairs.
+template <int ELEM>
+__device__ __forceinline__ void unpack8(const uint4* u, uint64_t* v) {
+  float f[8];
+  unpack8<ELEM>(u, f);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = pk(f[2 * k], f[2 * k + 1]);
+}
+template <int ELEM>
+__device__ __forceinline__ void pack8(const uint64_t* v, uint4* u) {
+  float f[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 t = upk(v[k]);
+    f[2 * k] = t.x;
+    f[2 * k + 1] = t.y;
+  }
+  pack8<ELEM>(f, u);
+}
 template <int ELEM>
 __device__ __forceinline__ void load8(const void* p, int64_t i, float* v) {
   constexpr int W = ELEM == LNFP8_FP32 ? 2 : 1;
@@ -110,8 +161,14 @@ __device__ __forceinline__ void load8_rt(const void* p, int elem, int64_t i, flo
   else if (elem == LNFP8_FP16) load8<LNFP8_FP16>(p, i, v);
   else load8<LNFP8_BF16>(p, i, v);
 }
-template <int ELEM>
-__device__ __forceinline__ void store8(void* p, int64_t i, const float* v) {
+__device__ __forceinline__ void load8_rt(const void* p, int elem, int64_t i, uint64_t* v) {
+  float f[8];
+  load8_rt(p, elem, i, f);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = pk(f[2 * k], f[2 * k + 1]);
+}
+template <int ELEM, typename V>  // float[8] or uint64_t[4]
+__device__ __forceinline__ void store8(void* p, int64_t i, const V* v) {
   constexpr int W = ELEM == LNFP8_FP32 ? 2 : 1;
   uint4* q = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p) + i * ElemSize<ELEM>::value);
   uint4 u[W];
@@ -126,6 +183,14 @@ __device__ __forceinline__ float elem_max() {
   if constexpr (ELEM == LNFP8_FP32) return __uint_as_float(0x7F7FFFFFu);
   else if constexpr (ELEM == LNFP8_FP16) return 65504.0f;
   else return __uint_as_float(0x7F7F0000u);
+}
+
+// 1/sqrt(x) of a variance: the approximation (2 ulp) with one Newton step, within 2 ulp; x = 0
+// (a constant row with eps 0) is Inf as by division, x = Inf 0, NaN stays.
+__device__ __forceinline__ float rsqrt_nr(float x) {
+  const float r = rsqrtf(x);
+  const float s = r * fmaf(-0.5f * x * r, r, 1.5f);
+  return x > 0.f && x < __uint_as_float(0x7F800000u) ? s : r;
 }
 
 // ------------------------------------------------------------ checkpoint blocks
@@ -174,13 +239,48 @@ __device__ __forceinline__ void decode8(uint2 q, float scale, int dt, float* v) 
     v[2 * k + 1] = f.y * scale;
   }
 }
+__device__ __forceinline__ uint2 encode8(const uint64_t* v, float inv, int dt) {
+  const uint64_t i2 = pk(inv, inv);
+  uint32_t c[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 f = upk(mul_2(v[k], i2));
+    c[k] = fp8x2(f.x, f.y, dt);
+  }
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+__device__ __forceinline__ void decode8(uint2 q, float scale, int dt, uint64_t* v) {
+  const uint32_t w[4] = {q.x & 0xFFFFu, q.x >> 16, q.y & 0xFFFFu, q.y >> 16};
+  const uint64_t s2 = pk(scale, scale);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 f = fp8x2_to_f32(w[k], dt);
+    v[k] = mul_2(pk(f.x, f.y), s2);
+  }
+}
+// max(|a|, |b|, |c|), NaN if one is (sm_100 and later)
+__device__ __forceinline__ float amax3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 // Largest |v| bits of 8 values, then over the 4 neighbouring lanes that hold a block.
 __device__ __forceinline__ uint32_t block_amax8(const float* v) {
-  uint32_t am = 0;
-#pragma unroll
-  for (int k = 0; k < 8; ++k) am = max(am, abs_bits(v[k]));
+  const float m = amax3(amax3(amax3(v[0], v[1], v[2]), v[3], v[4]), amax3(v[5], v[6], v[7]), 0.f);
+  uint32_t am = abs_bits(m);
   am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
   return max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
+}
+
+__device__ __forceinline__ uint32_t block_amax8(const uint64_t* v) {
+  float f[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 t = upk(v[k]);
+    f[2 * k] = t.x;
+    f[2 * k + 1] = t.y;
+  }
+  return block_amax8(f);
 }
 
 // A restored value: code * 2^e, kept inside the type (a block whose largest value
