@@ -11,6 +11,7 @@
 // (the mean first, then the centred squares, so a large mean loses nothing).
 #include "common.cuh"
 #include "internal.h"
+#include "kernel_setup.cuh"
 #include "rowmath.cuh"
 
 #include <algorithm>
@@ -649,14 +650,6 @@ __global__ void __launch_bounds__(1024) colsum_kernel(const float* __restrict__ 
 // Blocks of the backward's row pass: the partial rows it leaves are summed afterwards.
 constexpr int kBwdBlocksPerSm = 2;
 
-template <typename K>
-lnfp8_status allow_smem(K kernel, size_t smem, const char* who) {
-  if (smem > 40 * 1024 &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return check_launch(who);
-  return LNFP8_OK;
-}
-
 template <int ELEM, bool CK>
 lnfp8_status fwd_any(const LnFwdParams& p, cudaStream_t st) {
   auto go = [&](auto kernel, int tpr) {
@@ -689,74 +682,68 @@ lnfp8_status bwd_any(const LnBwdParams& p, int* blocks_out, cudaStream_t st) {
 
 bool al(const void* p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
-// Resident blocks per SM, looked up once per kernel (the devices of a process are alike).
-template <typename K>
-int blocks_per_sm(K kernel, int threads, size_t smem) {
-  int n = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess || n < 1) n = 1;
-  return n;
+template <int ELEM, int TPR, int NV, bool CK, bool RES>
+lnfp8_status fwd_vec_launch(const LnFwdParams& p, cudaStream_t st) {
+  using S = FwdShape<ELEM, TPR, NV, RES>;
+  constexpr auto kernel = ln_fwd_vec_kernel<ELEM, TPR, NV, CK, RES>;
+  int bps = 1;
+  const lnfp8_status s = kernel_setup<kernel>(S::THREADS, S::SMEM, &bps, "layernorm_fwd: kernel set-up");
+  if (s != LNFP8_OK) return s;
+  constexpr int gpb = S::THREADS / TPR, es = ElemSize<ELEM>::value;
+  const int64_t blocks = min64((p.M + gpb - 1) / gpb, (int64_t)num_sms() * bps);
+  LnFwdParams q = p;
+  q.step = blocks * gpb;
+  q.xstep = q.step * p.ldx * es;
+  q.rstep = q.step * p.ldr * es;
+  q.ystep = q.step * p.ldy * es;
+  q.hstep = q.step * p.D * es;
+  q.cstep = q.step * p.D;
+  q.sstep = q.step * p.pitch;
+  if (launch_pdl(kernel, dim3((unsigned)blocks), dim3(S::THREADS), S::SMEM, st, q) != cudaSuccess) return check_launch("layernorm_fwd launch");
+  return check_launch("layernorm_fwd");
 }
 
 template <int ELEM, bool CK, bool RES>
 lnfp8_status fwd_vec(const LnFwdParams& p, cudaStream_t st) {
-  auto go = [&](auto kernel, auto shape, int tpr) {
-    using S = decltype(shape);
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::SMEM) != cudaSuccess)
-      return check_launch("layernorm_fwd: shared memory");
-    const int gpb = S::THREADS / tpr;
-    const int64_t blocks = min64((p.M + gpb - 1) / gpb, (int64_t)num_sms() * blocks_per_sm(kernel, S::THREADS, S::SMEM));
-    constexpr int es = ElemSize<ELEM>::value;
-    LnFwdParams q = p;
-    q.step = blocks * gpb;
-    q.xstep = q.step * p.ldx * es;
-    q.rstep = q.step * p.ldr * es;
-    q.ystep = q.step * p.ldy * es;
-    q.hstep = q.step * p.D * es;
-    q.cstep = q.step * p.D;
-    q.sstep = q.step * p.pitch;
-    if (launch_pdl(kernel, dim3((unsigned)blocks), dim3(S::THREADS), S::SMEM, st, q) != cudaSuccess) return check_launch("layernorm_fwd launch");
-    return check_launch("layernorm_fwd");
-  };
-#define FWD(TPR, NV) go(ln_fwd_vec_kernel<ELEM, TPR, NV, CK, RES>, FwdShape<ELEM, TPR, NV, RES>(), TPR)
-  if (p.D <= 256) return FWD(32, 1);
-  if (p.D <= 512) return FWD(32, 2);
-  if (p.D <= 1024) return FWD(64, 2);
-  if (p.D <= 2048) return FWD(128, 2);
-  if (p.D <= 4096) return FWD(256, 2);
-  return FWD(512, 2);
-#undef FWD
+  if (p.D <= 256) return fwd_vec_launch<ELEM, 32, 1, CK, RES>(p, st);
+  if (p.D <= 512) return fwd_vec_launch<ELEM, 32, 2, CK, RES>(p, st);
+  if (p.D <= 1024) return fwd_vec_launch<ELEM, 64, 2, CK, RES>(p, st);
+  if (p.D <= 2048) return fwd_vec_launch<ELEM, 128, 2, CK, RES>(p, st);
+  if (p.D <= 4096) return fwd_vec_launch<ELEM, 256, 2, CK, RES>(p, st);
+  return fwd_vec_launch<ELEM, 512, 2, CK, RES>(p, st);
+}
+
+template <int ELEM, int TPR, int NV, bool CK, bool RES>
+lnfp8_status bwd_vec_launch(const LnBwdParams& p, int* blocks_out, cudaStream_t st) {
+  using S = BwdShape<ELEM, TPR, NV, CK, RES>;
+  static_assert(S::SMEM >= TPR * NV * 8 * 2 * sizeof(float), "the column partials reuse the ring");
+  constexpr auto kernel = ln_bwd_vec_kernel<ELEM, TPR, NV, CK, RES>;
+  int bps = 1;
+  const lnfp8_status s = kernel_setup<kernel>(S::THREADS, S::SMEM, &bps, "layernorm_bwd: kernel set-up");
+  if (s != LNFP8_OK) return s;
+  constexpr int gpb = S::THREADS / TPR, es = ElemSize<ELEM>::value;
+  const int64_t blocks = min64((p.M + gpb - 1) / gpb, (int64_t)num_sms() * std::min(kBwdBlocksPerSm, bps));
+  *blocks_out = (int)blocks;
+  LnBwdParams q = p;
+  q.step = blocks * gpb;
+  q.dstep = q.step * p.lddy * es;
+  q.xstep = q.step * p.ldx * es;
+  q.rstep = q.step * p.lddres * es;
+  q.ostep = q.step * p.lddx * es;
+  q.cstep = q.step * p.D;
+  q.sstep = q.step * p.pitch;
+  if (launch_pdl(kernel, dim3((unsigned)blocks), dim3(S::THREADS), S::SMEM, st, q) != cudaSuccess) return check_launch("layernorm_bwd launch");
+  return check_launch("layernorm_bwd");
 }
 
 template <int ELEM, bool CK, bool RES>
 lnfp8_status bwd_vec(const LnBwdParams& p, int* blocks_out, cudaStream_t st) {
-  auto go = [&](auto kernel, auto shape, int tpr) {
-    using S = decltype(shape);
-    const int gpb = S::THREADS / tpr;
-    const size_t smem = gpb > 1 ? std::max<size_t>(S::SMEM, 2 * (size_t)p.D * sizeof(float)) : S::SMEM;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-      return check_launch("layernorm_bwd: shared memory");
-    const int64_t blocks = min64((p.M + gpb - 1) / gpb, (int64_t)num_sms() * std::min(kBwdBlocksPerSm, blocks_per_sm(kernel, S::THREADS, smem)));
-    *blocks_out = (int)blocks;
-    constexpr int es = ElemSize<ELEM>::value;
-    LnBwdParams q = p;
-    q.step = blocks * gpb;
-    q.dstep = q.step * p.lddy * es;
-    q.xstep = q.step * p.ldx * es;
-    q.rstep = q.step * p.lddres * es;
-    q.ostep = q.step * p.lddx * es;
-    q.cstep = q.step * p.D;
-    q.sstep = q.step * p.pitch;
-    if (launch_pdl(kernel, dim3((unsigned)blocks), dim3(S::THREADS), smem, st, q) != cudaSuccess) return check_launch("layernorm_bwd launch");
-    return check_launch("layernorm_bwd");
-  };
-#define BWD(TPR, NV) go(ln_bwd_vec_kernel<ELEM, TPR, NV, CK, RES>, BwdShape<ELEM, TPR, NV, CK, RES>(), TPR)
-  if (p.D <= 256) return BWD(32, 1);
-  if (p.D <= 512) return BWD(32, 2);
-  if (p.D <= 1024) return BWD(64, 2);
-  if (p.D <= 2048) return BWD(128, 2);
-  if (p.D <= 4096) return BWD(256, 2);
-  return BWD(512, 2);
-#undef BWD
+  if (p.D <= 256) return bwd_vec_launch<ELEM, 32, 1, CK, RES>(p, blocks_out, st);
+  if (p.D <= 512) return bwd_vec_launch<ELEM, 32, 2, CK, RES>(p, blocks_out, st);
+  if (p.D <= 1024) return bwd_vec_launch<ELEM, 64, 2, CK, RES>(p, blocks_out, st);
+  if (p.D <= 2048) return bwd_vec_launch<ELEM, 128, 2, CK, RES>(p, blocks_out, st);
+  if (p.D <= 4096) return bwd_vec_launch<ELEM, 256, 2, CK, RES>(p, blocks_out, st);
+  return bwd_vec_launch<ELEM, 512, 2, CK, RES>(p, blocks_out, st);
 }
 
 // Rows of 16-byte words up to 8192 columns take the vector kernels (beyond, and for any other

@@ -10,6 +10,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "kernel_setup.cuh"
 #include "rowmath.cuh"
 #include "tc.cuh"
 
@@ -410,9 +411,9 @@ EpiParams epi_params(const LinGemm& g) {
 template <int BN, bool P_MN, bool Q_MN, bool SWAP>
 lnfp8_status tile_launch(const LinGemm& g, cudaStream_t st) {
   using C = TileCfg<BN>;
-  auto k = lin_tile_kernel<BN, P_MN, Q_MN, SWAP>;
-  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
-    return check_launch("linear: shared memory attribute");
+  constexpr auto k = lin_tile_kernel<BN, P_MN, Q_MN, SWAP>;
+  const lnfp8_status set = kernel_setup<k>(kTileThreads, C::SMEM, nullptr, "linear: kernel set-up");
+  if (set != LNFP8_OK) return set;
   const int64_t prow = SWAP ? g.N : g.M, qrow = SWAP ? g.M : g.N;
   const int64_t num_p = (prow + 127) / 128, num_q = (qrow + BN - 1) / BN;
   TileParams p;

@@ -390,9 +390,9 @@ lin_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 template <int BN, bool A_MN, bool B_MN, int EPI>
 lnfp8_status pair_launch(const LinGemm& g, cudaStream_t st) {
   using C = PairCfg<BN, EPI>;
-  auto k = lin_pair_kernel<BN, A_MN, B_MN, EPI>;
-  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
-    return check_launch("linear: shared memory attribute");
+  constexpr auto k = lin_pair_kernel<BN, A_MN, B_MN, EPI>;
+  const lnfp8_status set = kernel_setup<k>(kPairThreads, C::SMEM, nullptr, "linear: kernel set-up");
+  if (set != LNFP8_OK) return set;
   PairParams p = {};
   p.M = (int)g.M;
   p.N = (int)g.N;

@@ -664,41 +664,60 @@ def _act(act) -> int:
     return ACTS[act]
 
 
-def _here(t, name) -> None:
+def _where(t, name) -> None:
+    """Says why a tensor is not on the current CUDA device."""
     if not t.is_cuda:
         raise TypeError(f"{name} is not a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
 
 
-def _rows(t, name, rows, cols, dtype) -> int:
+def _dev(t, name) -> int:
+    """The index of the current CUDA device, on which the tensor must be."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        _where(t, name)
+    return dev
+
+
+def _rows(t, name, rows, cols, dtype, dev) -> int:
     """Checks a [rows, cols] tensor whose rows are contiguous; returns its row stride."""
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} has shape {tuple(t.shape)}: expected ({rows}, {cols})")
     if t.dtype is not dtype:
         raise TypeError(f"{name} is {t.dtype}: expected {dtype}")
-    _here(t, name)
+    if t.get_device() != dev:
+        _where(t, name)
+    if t.is_contiguous():
+        return cols
     s0, s1 = t.stride()
     if (cols > 1 and s1 != 1) or (rows > 1 and s0 < cols):
         raise ValueError(f"{name} has strides {(s0, s1)}: rows must be contiguous and not overlap")
     return s0 if rows > 1 else cols
 
 
-def _flat(t, name, shape, dtype) -> None:
+def _flat(t, name, shape, dtype, dev) -> None:
     """Checks a contiguous tensor of the given shape and type."""
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}: expected {shape}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} is {t.dtype}: expected {dtype}")
-    _here(t, name)
+    if t.get_device() != dev:
+        _where(t, name)
     if not t.is_contiguous():
         raise ValueError(f"{name} is not contiguous")
+
+
+# The current stream's handle without the Stream object around it (4 us less per call where
+# this PyTorch offers it).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 class _On:
     """Allocations of a call belong to the stream that it runs on."""
 
-    def __init__(self, stream):
+    def __init__(self, stream, dev):
+        if stream is not None and stream.device.index != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on cuda:{dev}")
         self.ctx = torch.cuda.stream(stream) if stream is not None else None
 
     def __enter__(self):
@@ -722,9 +741,9 @@ class ActCkpt:
     def shape(self):
         return self.codes.shape
 
-    def c(self, rows, cols, name="ckpt") -> CCkpt:
-        _flat(self.codes, name + ".codes", (rows, cols), torch.uint8)
-        _flat(self.scales, name + ".scales", (rows, (cols + 127) // 128 * 4), torch.uint8)
+    def c(self, rows, cols, dev, name="ckpt") -> CCkpt:
+        _flat(self.codes, name + ".codes", (rows, cols), torch.uint8, dev)
+        _flat(self.scales, name + ".scales", (rows, (cols + 127) // 128 * 4), torch.uint8, dev)
         return CCkpt(self.codes.data_ptr(), self.scales.data_ptr(), self.dtype)
 
 
@@ -743,10 +762,11 @@ def act_ckpt_save(x, *, dtype=E4M3, ckpt: ActCkpt | None = None, stream=None) ->
     if x.dim() != 2:
         raise ValueError(f"x has shape {tuple(x.shape)}: expected two dimensions")
     rows, cols = x.shape
-    ldx = _rows(x, "x", rows, cols, x.dtype)
-    with _On(stream):
-        ckpt = ckpt if ckpt is not None else act_ckpt(rows, cols, dtype=dtype, device=x.device)
-        _check(_c_ckpt_save(x.data_ptr(), elem, rows, cols, ldx, C.byref(ckpt.c(rows, cols)), _stream(stream)))
+    dev = _dev(x, "x")
+    ldx = _rows(x, "x", rows, cols, x.dtype, dev)
+    with _On(stream, dev):
+        ckpt = ckpt if ckpt is not None else act_ckpt(rows, cols, dtype=dtype, device=dev)
+        _check(_c_ckpt_save(x.data_ptr(), elem, rows, cols, ldx, C.byref(ckpt.c(rows, cols, dev)), _raw_stream(dev)))
     return ckpt
 
 
@@ -755,18 +775,19 @@ def act_ckpt_restore(ckpt: ActCkpt, *, out_dtype=torch.bfloat16, act="none", gam
     """The checkpoint's values, or act(values), or values * gamma + beta per column (a LayerNorm's
     output from its checkpointed rows). Values beyond the type's range saturate."""
     rows, cols = ckpt.codes.shape
-    cc = ckpt.c(rows, cols)
+    dev = _dev(ckpt.codes, "ckpt.codes")
+    cc = ckpt.c(rows, cols, dev)
     pe = 0
     if gamma is not None and beta is not None:
         pe = _elem(gamma, "gamma")
-        _flat(gamma, "gamma", (cols,), gamma.dtype)
-        _flat(beta, "beta", (cols,), gamma.dtype)
-    with _On(stream):
-        out = out if out is not None else _e((rows, cols), out_dtype, ckpt.codes.device)
+        _flat(gamma, "gamma", (cols,), gamma.dtype, dev)
+        _flat(beta, "beta", (cols,), gamma.dtype, dev)
+    with _On(stream, dev):
+        out = out if out is not None else _e((rows, cols), out_dtype, dev)
         elem = _elem(out, "out")
-        ldo = _rows(out, "out", rows, cols, out.dtype)
+        ldo = _rows(out, "out", rows, cols, out.dtype, dev)
         _check(_c_ckpt_restore(C.byref(cc), rows, cols, _act(act), _ptr(gamma), _ptr(beta), pe, out.data_ptr(), elem,
-                               ldo, _stream(stream)))
+                               ldo, _raw_stream(dev)))
     return out
 
 
@@ -789,14 +810,14 @@ def layernorm_fwd(x, gamma, beta, *, eps=1e-5, residual=None, ckpt=False, y=None
     if x.dim() != 2:
         raise ValueError(f"x has shape {tuple(x.shape)}: expected two dimensions")
     M, D = x.shape
-    dt, dev = x.dtype, x.device
-    ldx = _rows(x, "x", M, D, dt)
-    _flat(gamma, "gamma", (D,), gamma.dtype)
-    _flat(beta, "beta", (D,), gamma.dtype)
-    ldr = _rows(residual, "residual", M, D, dt) if residual is not None else 0
-    with _On(stream):
+    dt, dev = x.dtype, _dev(x, "x")
+    ldx = _rows(x, "x", M, D, dt, dev)
+    _flat(gamma, "gamma", (D,), gamma.dtype, dev)
+    _flat(beta, "beta", (D,), gamma.dtype, dev)
+    ldr = _rows(residual, "residual", M, D, dt, dev) if residual is not None else 0
+    with _On(stream, dev):
         y = y if y is not None else _e((M, D), dt, dev)
-        ldy = _rows(y, "y", M, D, dt)
+        ldy = _rows(y, "y", M, D, dt, dev)
         mu, rs = _e((M,), torch.float32, dev), _e((M,), torch.float32, dev)
         h = _e((M, D), dt, dev) if residual is not None else x
         if ckpt is True:
@@ -805,8 +826,8 @@ def layernorm_fwd(x, gamma, beta, *, eps=1e-5, residual=None, ckpt=False, y=None
             ckpt = None
         a = CLayerNormFwd(M, D, elem, pe, x.data_ptr(), _ptr(residual), gamma.data_ptr(), beta.data_ptr(), y.data_ptr(),
                           h.data_ptr() if residual is not None else None, mu.data_ptr(), rs.data_ptr(),
-                          ckpt.c(M, D) if ckpt is not None else _NO_CKPT, ldx, ldr, ldy, eps)
-        _check(_c_layernorm_fwd(C.byref(a), _stream(stream)))
+                          ckpt.c(M, D, dev) if ckpt is not None else _NO_CKPT, ldx, ldr, ldy, eps)
+        _check(_c_layernorm_fwd(C.byref(a), _raw_stream(dev)))
     return y, LayerNormCtx(h, mu, rs, ckpt)
 
 
@@ -835,26 +856,26 @@ def layernorm_bwd(dy, ctx: LayerNormCtx, gamma, *, dresidual=None, grads: LayerN
     if dy.dim() != 2:
         raise ValueError(f"dy has shape {tuple(dy.shape)}: expected two dimensions")
     M, D = dy.shape
-    dt = dy.dtype
-    lddy = _rows(dy, "dy", M, D, dt)
-    _flat(gamma, "gamma", (D,), gamma.dtype)
-    _flat(ctx.rsigma, "ctx.rsigma", (M,), torch.float32)
+    dt, dev = dy.dtype, _dev(dy, "dy")
+    lddy = _rows(dy, "dy", M, D, dt, dev)
+    _flat(gamma, "gamma", (D,), gamma.dtype, dev)
+    _flat(ctx.rsigma, "ctx.rsigma", (M,), torch.float32, dev)
     if ctx.ckpt is not None:
-        ck, x, mu, ldx = ctx.ckpt.c(M, D), None, None, 0
+        ck, x, mu, ldx = ctx.ckpt.c(M, D, dev), None, None, 0
     else:
         ck, x, mu = _NO_CKPT, ctx.x.data_ptr(), ctx.mu.data_ptr()
-        ldx = _rows(ctx.x, "ctx.x", M, D, dt)
-        _flat(ctx.mu, "ctx.mu", (M,), torch.float32)
-    lddr = _rows(dresidual, "dresidual", M, D, dt) if dresidual is not None else 0
-    with _On(stream):
-        g = grads if grads is not None else layernorm_grads(M, D, dtype=dt, device=dy.device)
-        lddx = _rows(g.dx, "grads.dx", M, D, dt)
-        _flat(g.dgamma, "grads.dgamma", (D,), torch.float32)
-        _flat(g.dbeta, "grads.dbeta", (D,), torch.float32)
+        ldx = _rows(ctx.x, "ctx.x", M, D, dt, dev)
+        _flat(ctx.mu, "ctx.mu", (M,), torch.float32, dev)
+    lddr = _rows(dresidual, "dresidual", M, D, dt, dev) if dresidual is not None else 0
+    with _On(stream, dev):
+        g = grads if grads is not None else layernorm_grads(M, D, dtype=dt, device=dev)
+        lddx = _rows(g.dx, "grads.dx", M, D, dt, dev)
+        _flat(g.dgamma, "grads.dgamma", (D,), torch.float32, dev)
+        _flat(g.dbeta, "grads.dbeta", (D,), torch.float32, dev)
         a = CLayerNormBwd(M, D, elem, pe, dy.data_ptr(), x, mu, ctx.rsigma.data_ptr(), ck, gamma.data_ptr(),
                           _ptr(dresidual), g.dx.data_ptr(), g.dgamma.data_ptr(), g.dbeta.data_ptr(), _ptr(g.workspace),
                           g.workspace.numel() if g.workspace is not None else 0, lddy, ldx, lddr, lddx)
-        _check(_c_layernorm_bwd(C.byref(a), _stream(stream)))
+        _check(_c_layernorm_bwd(C.byref(a), _raw_stream(dev)))
     return g
 
 
@@ -882,30 +903,30 @@ def linear_act_fwd(x, w, bias=None, *, act="none", residual=None, save="none", y
         raise ValueError(f"unknown save {save!r}: one of none, h, ckpt")
     M, K = x.shape
     N = w.shape[0]
-    dt, dev = x.dtype, x.device
-    ldx = _rows(x, "x", M, K, dt)
-    _flat(w, "w", (N, K), dt)
+    dt, dev = x.dtype, _dev(x, "x")
+    ldx = _rows(x, "x", M, K, dt, dev)
+    _flat(w, "w", (N, K), dt, dev)
     if bias is not None:
-        _flat(bias, "bias", (N,), dt)
-    ldr = _rows(residual, "residual", M, N, dt) if residual is not None else 0
-    with _On(stream):
+        _flat(bias, "bias", (N,), dt, dev)
+    ldr = _rows(residual, "residual", M, N, dt, dev) if residual is not None else 0
+    with _On(stream, dev):
         y = y if y is not None else _e((M, N), dt, dev)
-        ldy = _rows(y, "y", M, N, dt)
+        ldy = _rows(y, "y", M, N, dt, dev)
         ctx = ctx if ctx is not None else LinearActCtx()
         ctx.act = act
         h, ck = None, _NO_CKPT
         if save == "h":
             ctx.ckpt = None
             ctx.h = ctx.h if ctx.h is not None else _e((M, N), dt, dev)
-            _flat(ctx.h, "ctx.h", (M, N), dt)
+            _flat(ctx.h, "ctx.h", (M, N), dt, dev)
             h = ctx.h.data_ptr()
         elif save == "ckpt":
             ctx.h = None
             ctx.ckpt = ctx.ckpt if ctx.ckpt is not None else act_ckpt(M, N, device=dev)
-            ck = ctx.ckpt.c(M, N, "ctx.ckpt")
+            ck = ctx.ckpt.c(M, N, dev, "ctx.ckpt")
         a = CLinearActFwd(M, K, N, elem, ia, x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual), y.data_ptr(), h, ck,
                           ldx, ldr, ldy)
-        _check(_c_linear_act_fwd(C.byref(a), _stream(stream)))
+        _check(_c_linear_act_fwd(C.byref(a), _raw_stream(dev)))
     return y, ctx
 
 
@@ -939,36 +960,36 @@ def linear_act_bwd(dy, x, w, ctx: LinearActCtx, *, x_act="none", x_gamma=None, x
         raise ValueError(f"dy and w have shapes {tuple(dy.shape)} and {tuple(w.shape)}: expected two dimensions")
     M, N = dy.shape
     K = w.shape[1]
-    dt = dy.dtype
-    lddy = _rows(dy, "dy", M, N, dt)
-    _flat(w, "w", (N, K), dt)
+    dt, dev = dy.dtype, _dev(dy, "dy")
+    lddy = _rows(dy, "dy", M, N, dt, dev)
+    _flat(w, "w", (N, K), dt, dev)
     h, hck, xp, xck, ldx = None, _NO_CKPT, None, _NO_CKPT, 0
     if ia:
         if ctx.ckpt is not None:
-            hck = ctx.ckpt.c(M, N, "ctx.ckpt")
+            hck = ctx.ckpt.c(M, N, dev, "ctx.ckpt")
         elif ctx.h is not None:
-            _flat(ctx.h, "ctx.h", (M, N), dt)
+            _flat(ctx.h, "ctx.h", (M, N), dt, dev)
             h = ctx.h.data_ptr()
         else:
             raise ValueError(f"the forward with act {ctx.act!r} saved no pre-activation")
     if isinstance(x, ActCkpt):
-        xck = x.c(M, K, "x")
+        xck = x.c(M, K, dev, "x")
     elif x is not None:
-        ldx = _rows(x, "x", M, K, dt)
+        ldx = _rows(x, "x", M, K, dt, dev)
         xp = x.data_ptr()
     for t, name in ((x_gamma, "x_gamma"), (x_beta, "x_beta")):
         if t is not None:
-            _flat(t, name, (K,), dt)
-    with _On(stream):
+            _flat(t, name, (K,), dt, dev)
+    with _On(stream, dev):
         g = grads if grads is not None else linear_act_grads(M, K, N, act=ctx.act, x_from_ckpt=xck is not _NO_CKPT,
-                                                             dw=x is not None, dtype=dt, device=dy.device)
-        lddx = _rows(g.dx, "grads.dx", M, K, dt) if g.dx is not None else 0
+                                                             dw=x is not None, dtype=dt, device=dev)
+        lddx = _rows(g.dx, "grads.dx", M, K, dt, dev) if g.dx is not None else 0
         if g.dw is not None:
-            _flat(g.dw, "grads.dw", (N, K), dt)
+            _flat(g.dw, "grads.dw", (N, K), dt, dev)
         if g.dbias is not None:
-            _flat(g.dbias, "grads.dbias", (N,), torch.float32)
+            _flat(g.dbias, "grads.dbias", (N,), torch.float32, dev)
         a = CLinearActBwd(M, K, N, elem, ia, dy.data_ptr(), xp, xck, _act(x_act), _ptr(x_gamma), _ptr(x_beta), w.data_ptr(),
                           h, hck, _ptr(g.dx), _ptr(g.dw), _ptr(g.dbias), _ptr(g.workspace),
                           g.workspace.numel() if g.workspace is not None else 0, lddy, ldx, lddx)
-        _check(_c_linear_act_bwd(C.byref(a), _stream(stream)))
+        _check(_c_linear_act_bwd(C.byref(a), _raw_stream(dev)))
     return g
