@@ -167,17 +167,24 @@ __global__ void __launch_bounds__(kThreads) restore_vec_kernel(const RestorePara
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) {
       if (!ok[k]) continue;
-      float v[8];
+      uint64_t v[4];
       decode8(q[k], ckpt_scale(b[k]), p.dt, v);
       if constexpr (AFFINE) {
-        float ga[8], be[8];
+        uint64_t ga[4], be[4];
         load8_rt(p.gamma, p.param_elem, at[k].c, ga);
         load8_rt(p.beta, p.param_elem, at[k].c, be);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = fmaf(v[e], ga[e], be[e]);
+        for (int e = 0; e < 4; ++e) v[e] = fma_2(v[e], ga[e], be[e]);
       }
+      act8<ACT>(v);
+      // values past the type's range: with gamma and beta anywhere, else in blocks of large scales only
+      if (AFFINE || b[k] >= (ELEM == LNFP8_FP16 ? 127u : 239u)) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = ckpt_clamp<ELEM>(act_fwd(v[e], ACT));
+        for (int e = 0; e < 4; ++e) {
+          const float2 t = upk(v[e]);
+          v[e] = pk(ckpt_clamp<ELEM>(t.x), ckpt_clamp<ELEM>(t.y));
+        }
+      }
       store8<ELEM>(p.out, at[k].row * p.ldo + at[k].c, v);
     }
   }

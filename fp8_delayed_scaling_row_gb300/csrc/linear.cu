@@ -287,12 +287,15 @@ struct DactParams {
   float* part;   // [row blocks][N] or NULL; with `both` [row blocks][2][N]: the sums of dz, then of dz as rounded
   int both;
   int64_t M, lddy, pitch;
-  int N, act, dt, rows_per_block;  // dt: the lnfp8_dtype of the codes
+  int N, dt, rows_per_block;  // dt: the lnfp8_dtype of the codes
 };
 
 enum DactSource { DACT_NONE, DACT_TENSOR, DACT_CKPT };  // no activation; h as a tensor; h as a checkpoint
-template <int ELEM, int SRC>
-__global__ void __launch_bounds__(256) lin_dact_kernel(const DactParams p) {
+constexpr int kDactRows = 4;       // rows a thread has in flight
+constexpr int kDactBlocksPerSm = 3;
+
+template <int ELEM, int SRC, int ACT>
+__global__ void __launch_bounds__(256, kDactBlocksPerSm) lin_dact_kernel(const DactParams p) {
   __shared__ float red[8][32][9];
   pdl_wait();
   pdl_launch_dependents();
@@ -301,43 +304,66 @@ __global__ void __launch_bounds__(256) lin_dact_kernel(const DactParams p) {
   const bool ok = c < p.N;
   const int64_t r0 = (int64_t)blockIdx.y * p.rows_per_block;
   const int64_t r1 = min64(p.M, r0 + p.rows_per_block);
-  constexpr int f16 = ELEM == LNFP8_FP16;
-  float acc[8], accr[8];
+  uint64_t acc[4], accr[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = accr[i] = 0.f;
+  for (int k = 0; k < 4; ++k) acc[k] = accr[k] = 0;
   if (ok) {
-#pragma unroll 4
-    for (int64_t r = r0 + rl; r < r1; r += 8) {
-      float v[8];
+    for (int64_t rb = r0 + rl; rb < r1; rb += 8 * kDactRows) {
+      uint4 dy[kDactRows], h[kDactRows];
+      uint32_t sb[kDactRows];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.f;
-      add16x8(v, *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.dy) + r * p.lddy + c), f16);
-      if constexpr (SRC != DACT_NONE) {
-        float z[8];
-        if constexpr (SRC == DACT_TENSOR) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) z[i] = 0.f;
-          add16x8(z, *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.h) + r * p.N + c), f16);
-        } else {
-          const uint2 q = *reinterpret_cast<const uint2*>(p.codes + r * p.N + c);
-          const float s = ckpt_scale(p.scales[r * p.pitch + (c >> 5)]);
-          decode8(q, s, p.dt, z);
+      for (int i = 0; i < kDactRows; ++i) {
+        const int64_t r = rb + 8 * i;
+        dy[i] = h[i] = make_uint4(0u, 0u, 0u, 0u);
+        sb[i] = 127u;
+        if (r < r1) {
+          dy[i] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.dy) + r * p.lddy + c);
+          if constexpr (SRC == DACT_TENSOR) h[i] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.h) + r * p.N + c);
+          if constexpr (SRC == DACT_CKPT) {
+            const uint2 q = *reinterpret_cast<const uint2*>(p.codes + r * p.N + c);
+            h[i].x = q.x;
+            h[i].y = q.y;
+            sb[i] = p.scales[r * p.pitch + (c >> 5)];
+          }
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= act_slope(z[i], p.act);
-        const uint4 w = pack16x8(v, f16);
-        *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.dz) + r * p.N + c) = w;
-        if (p.both) add16x8(accr, w, f16);
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] += v[i];
+      for (int i = 0; i < kDactRows; ++i) {
+        const int64_t r = rb + 8 * i;
+        if (r >= r1) break;
+        uint64_t v[4];
+        unpack8<ELEM>(&dy[i], v);
+        if constexpr (SRC != DACT_NONE) {
+          uint64_t z[4], sl[4];
+          if constexpr (SRC == DACT_TENSOR) unpack8<ELEM>(&h[i], z);
+          else decode8(make_uint2(h[i].x, h[i].y), ckpt_scale(sb[i]), p.dt, z);
+          slope8<ACT>(z, sl);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] = mul_2(v[k], sl[k]);
+          uint4 w;
+          pack8<ELEM>(v, &w);
+          *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.dz) + r * p.N + c) = w;
+          if (p.both) {
+            uint64_t u[4];
+            unpack8<ELEM>(&w, u);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) accr[k] = add_2(accr[k], u[k]);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[k] = add_2(acc[k], v[k]);
+      }
     }
   }
   if (p.part == nullptr) return;
   for (int k = 0; k <= p.both; ++k) {
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) red[rl][cl][i] = k ? accr[i] : acc[i];
+    for (int i = 0; i < 4; ++i) {
+      const float2 t = upk(k ? accr[i] : acc[i]);
+      red[rl][cl][2 * i] = t.x;
+      red[rl][cl][2 * i + 1] = t.y;
+    }
     __syncthreads();
     const int col = threadIdx.x;  // 256 columns
     float s = 0.f;
@@ -456,10 +482,10 @@ lnfp8_status tile_launch(const LinGemm& g, cudaStream_t st) {
 
 #include "linear_pair.cuh"
 
-// Rows of the dz pass per block: enough blocks for about four per SM.
+// Rows of the dz pass per block: one wave of resident blocks.
 int64_t dact_rows_per_block(int64_t M, int64_t N) {
   const int64_t col_blocks = (N + 255) / 256;
-  const int64_t row_blocks = max64(1, (int64_t)num_sms() * 4 / col_blocks);
+  const int64_t row_blocks = max64(1, (int64_t)num_sms() * kDactBlocksPerSm / col_blocks);
   const int64_t rows = (M + row_blocks - 1) / row_blocks;
   return max64(32, (rows + 7) / 8 * 8);
 }
@@ -561,7 +587,6 @@ lnfp8_status linear_act_bwd_launch(const lnfp8_linear_act_bwd_args* a, cudaStrea
     p.lddy = a->ld_dy;
     p.pitch = lnfp8_act_ckpt_scale_pitch(a->N);
     p.N = (int)a->N;
-    p.act = a->act;
     p.dt = a->h_ckpt.dtype;
     p.rows_per_block = (int)dact_rows_per_block(a->M, a->N);
     const int64_t row_blocks = (a->M + p.rows_per_block - 1) / p.rows_per_block;
@@ -573,8 +598,12 @@ lnfp8_status linear_act_bwd_launch(const lnfp8_linear_act_bwd_args* a, cudaStrea
     };
     auto pick = [&](auto elem) {
       constexpr int E = decltype(elem)::value;
-      if (!has_act) return go(lin_dact_kernel<E, DACT_NONE>);
-      return p.codes ? go(lin_dact_kernel<E, DACT_CKPT>) : go(lin_dact_kernel<E, DACT_TENSOR>);
+      if (!has_act) return go(lin_dact_kernel<E, DACT_NONE, LNFP8_ACT_NONE>);
+      if (p.codes)
+        return a->act == LNFP8_ACT_GELU ? go(lin_dact_kernel<E, DACT_CKPT, LNFP8_ACT_GELU>)
+               : a->act == LNFP8_ACT_SILU ? go(lin_dact_kernel<E, DACT_CKPT, LNFP8_ACT_SILU>) : go(lin_dact_kernel<E, DACT_CKPT, LNFP8_ACT_RELU>);
+      return a->act == LNFP8_ACT_GELU ? go(lin_dact_kernel<E, DACT_TENSOR, LNFP8_ACT_GELU>)
+             : a->act == LNFP8_ACT_SILU ? go(lin_dact_kernel<E, DACT_TENSOR, LNFP8_ACT_SILU>) : go(lin_dact_kernel<E, DACT_TENSOR, LNFP8_ACT_RELU>);
     };
     lnfp8_status s = a->elem == LNFP8_BF16 ? pick(std::integral_constant<int, LNFP8_BF16>()) : pick(std::integral_constant<int, LNFP8_FP16>());
     if (s != LNFP8_OK) return s;

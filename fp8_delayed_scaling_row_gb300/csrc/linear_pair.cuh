@@ -64,23 +64,7 @@ __device__ __forceinline__ uint32_t box_at(int r, int j) { return (uint32_t)(r *
 template <int ACT>
 __device__ __forceinline__ void act_pairs(uint64_t* z) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    if constexpr (ACT == LNFP8_ACT_RELU) {
-      const float2 v = up(z[i]);
-      z[i] = f2(act_fwd(v.x, ACT), act_fwd(v.y, ACT));
-    } else {
-      uint64_t nu;
-      if constexpr (ACT == LNFP8_ACT_GELU) {
-        const uint64_t c0 = f2(-kLog2e * kGelu2K, -kLog2e * kGelu2K), c1 = f2(-kLog2e * kGelu2KC, -kLog2e * kGelu2KC);
-        nu = mul2(z[i], fma2(mul2(z[i], z[i]), c1, c0));
-      } else {
-        nu = mul2(z[i], f2(-kLog2e, -kLog2e));
-      }
-      const float2 n = up(nu);
-      const float2 d = up(add2(f2(ex2_fast(n.x), ex2_fast(n.y)), f2(1.0f, 1.0f)));
-      z[i] = mul2(z[i], f2(rcp_fast(d.x), rcp_fast(d.y)));
-    }
-  }
+  for (int i = 0; i < 16; i += 4) act8<ACT>(z + i);
 }
 
 template <int BN, bool A_MN, bool B_MN, int EPI>
@@ -252,15 +236,15 @@ lin_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         }
         uint64_t z[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) z[i] = f2(__uint_as_float(rr[2 * i]), __uint_as_float(rr[2 * i + 1]));
+        for (int i = 0; i < 16; ++i) z[i] = pk(__uint_as_float(rr[2 * i]), __uint_as_float(rr[2 * i + 1]));
         if constexpr (EPI != LIN_PLAIN) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) {  // columns 2i, 2i + 1 of the chunk sit in lane 8 ch + i / 2
             const float2 b = unpack16(__shfl_sync(0xFFFFFFFFu, i & 1 ? cb.y : cb.x, ch * 8 + (i >> 1)), p.f16);
-            if constexpr (EPI == LIN_FULL) z[i] = add2(z[i], f2(b.x, b.y));
+            if constexpr (EPI == LIN_FULL) z[i] = add_2(z[i], pk(b.x, b.y));
             else {
               const float2 v = unpack16(__shfl_sync(0xFFFFFFFFu, i & 1 ? cv.y : cv.x, ch * 8 + (i >> 1)), p.f16);
-              z[i] = fma2(z[i], f2(b.x, b.y), mul2(f2(rv, rv), f2(v.x, v.y)));
+              z[i] = fma_2(z[i], pk(b.x, b.y), mul_2(pk(rv, rv), pk(v.x, v.y)));
             }
           }
         }
@@ -287,7 +271,7 @@ lin_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
               uint32_t w[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const float2 v = up(z[4 * j + i]);
+                const float2 v = upk(z[4 * j + i]);
                 w[i] = pack16(v.x, v.y, p.f16);
               }
               *reinterpret_cast<uint4*>(box_h + box_at(lane, j)) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -298,17 +282,17 @@ lin_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             uint32_t am = 0;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float2 v = up(z[i]);
+              const float2 v = upk(z[i]);
               am = max(am, max(abs_bits(v.x), abs_bits(v.y)));
             }
             const uint32_t b = ckpt_byte(am, p.ck);
             const float inv = ckpt_inv_scale(b);
-            const uint64_t i2 = f2(inv, inv);
+            const uint64_t i2 = pk(inv, inv);
             scale_word |= b << (8 * ch);
             uint32_t q[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const float2 u = up(mul2(z[2 * i], i2)), v = up(mul2(z[2 * i + 1], i2));
+              const float2 u = upk(mul_2(z[2 * i], i2)), v = upk(mul_2(z[2 * i + 1], i2));
               q[i] = fp8x2(u.x, u.y, p.ck) | (fp8x2(v.x, v.y, p.ck) << 16);
             }
             if (m < p.M) {
@@ -333,7 +317,7 @@ lin_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const float2 v = unpack16(w[i], p.f16);
-                z[4 * j + i] = add2(z[4 * j + i], f2(v.x, v.y));
+                z[4 * j + i] = add_2(z[4 * j + i], pk(v.x, v.y));
               }
             }
           }
@@ -343,7 +327,7 @@ lin_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
           uint32_t w[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float2 v = up(z[4 * j + i]);
+            const float2 v = upk(z[4 * j + i]);
             w[i] = pack16(v.x, v.y, p.f16);
           }
           *reinterpret_cast<uint4*>(box_o + box_at(lane, j)) = make_uint4(w[0], w[1], w[2], w[3]);
