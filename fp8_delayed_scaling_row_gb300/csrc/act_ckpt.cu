@@ -22,6 +22,8 @@ struct SaveParams {
   uint8_t* scales;
   int64_t rows, ldx, pitch, units;  // units: rows * ceil(blocks per row / kBlocksPerWarp)
   int cols, upr, dt;                // upr: units per row; dt: the lnfp8_dtype of the codes
+  int64_t row_step;                 // chunks of a pass over the grid, in rows and chunks
+  uint32_t chunk_step;
 };
 
 struct RestoreParams {
@@ -32,6 +34,8 @@ struct RestoreParams {
   void* out;
   int64_t rows, ldo, pitch, units;
   int cols, upr, act, param_elem, dt;
+  int64_t row_step;
+  uint32_t chunk_step;
 };
 
 // Any width and alignment: a warp takes kBlocksPerWarp blocks of a row, lane = column.
@@ -93,52 +97,63 @@ __global__ void __launch_bounds__(kThreads) restore_any_kernel(const RestorePara
 // HBM-bound: kChunks independent 16-byte loads a thread cover the latency.
 constexpr int kChunks = 4;
 
+// The place of a chunk, moved on by a fixed number of chunks at a time (one division in all).
 struct ChunkPlace {
   int64_t row;
-  int c;
+  uint32_t c;  // chunk within the row
+  __device__ __forceinline__ ChunkPlace(int64_t chunk, uint32_t cpr) {
+    row = chunk / cpr;
+    c = (uint32_t)(chunk - row * cpr);
+  }
+  __device__ __forceinline__ void move(int64_t rows, uint32_t chunks, uint32_t cpr) {
+    row += rows;
+    c += chunks;
+    if (c >= cpr) {
+      c -= cpr;
+      ++row;
+    }
+  }
 };
-__device__ __forceinline__ ChunkPlace place(int64_t chunk, uint32_t cpr) {
-  int64_t row;
-  if (chunk <= 0xFFFFFFFFll) row = (uint32_t)chunk / cpr;  // the 64-bit division costs several times this
-  else row = chunk / cpr;
-  return {row, (int)(chunk - row * cpr) * 8};
-}
 
 template <int ELEM>
 __global__ void __launch_bounds__(kThreads) save_vec_kernel(const SaveParams p) {
   constexpr int W = ELEM == LNFP8_FP32 ? 2 : 1;
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t total = p.rows * p.upr, step = (int64_t)gridDim.x * kThreads;  // upr: chunks per row here
-  const int64_t tail = (total + 31) / 32 * 32;                                  // whole warps reach the shuffles
-  for (int64_t i0 = (int64_t)blockIdx.x * kThreads + threadIdx.x; i0 < tail; i0 += step * kChunks) {
+  const int64_t step = (int64_t)gridDim.x * kThreads;
+  const uint32_t cpr = p.upr;  // chunks per row here
+  int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  ChunkPlace at(i, cpr);
+  const int64_t end = (p.rows * cpr + 31) / 32 * 32;  // whole warps reach the shuffles
+  while (i < end) {
     uint4 u[kChunks][W];
-    ChunkPlace at[kChunks];
-    bool ok[kChunks];
+    int64_t row[kChunks];
+    int col[kChunks];  // -1: past the row's or the tensor's end
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) {
-      const int64_t i = i0 + k * step;
-      at[k] = place(i, p.upr);
-      ok[k] = i < total && at[k].c < p.cols;
+      row[k] = at.row;
+      col[k] = at.row < p.rows && (int)at.c * 8 < p.cols ? (int)at.c * 8 : -1;
 #pragma unroll
       for (int w = 0; w < W; ++w) u[k][w] = make_uint4(0u, 0u, 0u, 0u);
-      if (ok[k]) {
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.x) + (at[k].row * p.ldx + at[k].c) * ElemSize<ELEM>::value);
+      if (col[k] >= 0) {
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.x) + (at.row * p.ldx + col[k]) * ElemSize<ELEM>::value);
 #pragma unroll
         for (int w = 0; w < W; ++w) u[k][w] = __ldcs(src + w);
       }
+      at.move(p.row_step, p.chunk_step, cpr);
     }
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) {
-      if (i0 + k * step >= tail) break;  // uniform over the warp
-      float v[8];
+      if (i + k * step >= end) break;  // uniform over the warp
+      uint64_t v[4];
       unpack8<ELEM>(u[k], v);
       const uint32_t b = ckpt_byte(block_amax8(v), p.dt);
-      if (ok[k]) {
-        *reinterpret_cast<uint2*>(p.codes + at[k].row * p.cols + at[k].c) = encode8(v, ckpt_inv_scale(b), p.dt);
-        if ((at[k].c & 31) == 0) p.scales[at[k].row * p.pitch + (at[k].c >> 5)] = (uint8_t)b;
+      if (col[k] >= 0) {
+        *reinterpret_cast<uint2*>(p.codes + row[k] * p.cols + col[k]) = encode8(v, ckpt_inv_scale(b), p.dt);
+        if ((col[k] & 31) == 0) p.scales[row[k] * p.pitch + (col[k] >> 5)] = (uint8_t)b;
       }
     }
+    i += kChunks * step;
   }
 }
 
@@ -146,33 +161,34 @@ template <int ELEM, int ACT, bool AFFINE>
 __global__ void __launch_bounds__(kThreads) restore_vec_kernel(const RestoreParams p) {
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t total = p.rows * p.upr, step = (int64_t)gridDim.x * kThreads;
-  for (int64_t i0 = (int64_t)blockIdx.x * kThreads + threadIdx.x; i0 < total; i0 += step * kChunks) {
+  const uint32_t cpr = p.upr;
+  ChunkPlace at((int64_t)blockIdx.x * kThreads + threadIdx.x, cpr);
+  while (at.row < p.rows) {
     uint2 q[kChunks];
     uint32_t b[kChunks];
-    ChunkPlace at[kChunks];
-    bool ok[kChunks];
+    int64_t row[kChunks];
+    int col[kChunks];
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) {
-      const int64_t i = i0 + k * step;
-      at[k] = place(i, p.upr);
-      ok[k] = i < total && at[k].c < p.cols;
+      row[k] = at.row;
+      col[k] = at.row < p.rows && (int)at.c * 8 < p.cols ? (int)at.c * 8 : -1;
       q[k] = make_uint2(0u, 0u);
       b[k] = 0u;
-      if (ok[k]) {
-        q[k] = __ldcs(reinterpret_cast<const uint2*>(p.codes + at[k].row * p.cols + at[k].c));
-        b[k] = __ldg(p.scales + at[k].row * p.pitch + (at[k].c >> 5));
+      if (col[k] >= 0) {
+        q[k] = __ldcs(reinterpret_cast<const uint2*>(p.codes + at.row * p.cols + col[k]));
+        b[k] = __ldg(p.scales + at.row * p.pitch + (at.c >> 2));
       }
+      at.move(p.row_step, p.chunk_step, cpr);
     }
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) {
-      if (!ok[k]) continue;
+      if (col[k] < 0) continue;
       uint64_t v[4];
       decode8(q[k], ckpt_scale(b[k]), p.dt, v);
       if constexpr (AFFINE) {
         uint64_t ga[4], be[4];
-        load8_rt(p.gamma, p.param_elem, at[k].c, ga);
-        load8_rt(p.beta, p.param_elem, at[k].c, be);
+        load8_rt(p.gamma, p.param_elem, col[k], ga);
+        load8_rt(p.beta, p.param_elem, col[k], be);
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = fma_2(v[e], ga[e], be[e]);
       }
@@ -185,7 +201,7 @@ __global__ void __launch_bounds__(kThreads) restore_vec_kernel(const RestorePara
           v[e] = pk(ckpt_clamp<ELEM>(t.x), ckpt_clamp<ELEM>(t.y));
         }
       }
-      store8<ELEM>(p.out, at[k].row * p.ldo + at[k].c, v);
+      store8<ELEM>(p.out, row[k] * p.ldo + col[k], v);
     }
   }
 }
@@ -226,8 +242,11 @@ lnfp8_status act_ckpt_save_launch(const void* x, int elem, int64_t rows, int64_t
   // 16-byte rows take the vector kernel
   if (cols % 8 == 0 && al(x, 16) && ldx * (elem == LNFP8_FP32 ? 4 : 2) % 16 == 0 && al(c.codes, 8)) {
     p.upr = (int)((cols + 31) / 32 * 4);
+    const unsigned grid = vec_grid(rows * p.upr);
+    p.row_step = (int64_t)grid * kThreads / p.upr;
+    p.chunk_step = (uint32_t)((int64_t)grid * kThreads % p.upr);
     auto vec = [&](auto kernel) {
-      if (launch_pdl(kernel, dim3(vec_grid(rows * p.upr)), dim3(kThreads), 0, st, p) != cudaSuccess) return check_launch("act_ckpt_save launch");
+      if (launch_pdl(kernel, dim3(grid), dim3(kThreads), 0, st, p) != cudaSuccess) return check_launch("act_ckpt_save launch");
       return check_launch("act_ckpt_save");
     };
     if (elem == LNFP8_BF16) return vec(save_vec_kernel<LNFP8_BF16>);
@@ -263,8 +282,11 @@ lnfp8_status act_ckpt_restore_launch(const lnfp8_ckpt& c, int64_t rows, int64_t 
   if (cols % 8 == 0 && al(out, 16) && ldo * (elem == LNFP8_FP32 ? 4 : 2) % 16 == 0 && al(c.codes, 8) &&
       (!gamma || (al(gamma, 16) && al(beta, 16)))) {
     p.upr = (int)((cols + 31) / 32 * 4);
+    const unsigned grid = vec_grid(rows * p.upr);
+    p.row_step = (int64_t)grid * kThreads / p.upr;
+    p.chunk_step = (uint32_t)((int64_t)grid * kThreads % p.upr);
     auto vec = [&](auto kernel) {
-      if (launch_pdl(kernel, dim3(vec_grid(rows * p.upr)), dim3(kThreads), 0, st, p) != cudaSuccess) return check_launch("act_ckpt_restore launch");
+      if (launch_pdl(kernel, dim3(grid), dim3(kThreads), 0, st, p) != cudaSuccess) return check_launch("act_ckpt_restore launch");
       return check_launch("act_ckpt_restore");
     };
     auto by_act = [&](auto e) {

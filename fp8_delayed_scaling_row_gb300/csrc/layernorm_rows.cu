@@ -10,6 +10,7 @@
 // All arithmetic is fp32; the statistics are two sums over the row in registers
 // (the mean first, then the centred squares, so a large mean loses nothing).
 #include "common.cuh"
+#include "cp_async.cuh"
 #include "internal.h"
 #include "kernel_setup.cuh"
 #include "rowmath.cuh"
@@ -268,36 +269,6 @@ ln_bwd_any_kernel(const LnBwdParams p) {
 // bound by HBM: each thread copies (cp.async) the chunks of its next RING - 1 rows into its own
 // slots of a shared-memory ring, so the bytes in flight cost no registers, and a slot is
 // refilled one row after it was read. Four neighbouring lanes hold a checkpoint block.
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp8(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ uint4 lds16(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t lds4(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint2 lds8(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 template <int ELEM, int TPR, int NV, bool RES>
 struct FwdShape {
   static constexpr int THREADS = TPR < 256 ? 256 : TPR;

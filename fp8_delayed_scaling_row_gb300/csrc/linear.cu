@@ -9,6 +9,7 @@
 #include <cudaTypedefs.h>
 
 #include "common.cuh"
+#include "cp_async.cuh"
 #include "internal.h"
 #include "kernel_setup.cuh"
 #include "rowmath.cuh"
@@ -291,70 +292,95 @@ struct DactParams {
 };
 
 enum DactSource { DACT_NONE, DACT_TENSOR, DACT_CKPT };  // no activation; h as a tensor; h as a checkpoint
-constexpr int kDactRows = 4;       // rows a thread has in flight
-constexpr int kDactBlocksPerSm = 3;
+constexpr int kDactBlocksPerSm = 4;
+constexpr int kDactRing = 6;  // rows of a thread in its shared-memory ring: 5 on their way while one is used
+
+template <int SRC>
+struct DactShape {
+  static constexpr int H_OFF = 16, S_OFF = SRC == DACT_TENSOR ? 32 : 24;  // bytes per thread: dy, h or codes, scale word
+  static constexpr int BYTES = SRC == DACT_NONE ? 16 : SRC == DACT_TENSOR ? 32 : 28;
+  static constexpr size_t SMEM = (size_t)kDactRing * BYTES * 256;
+};
 
 template <int ELEM, int SRC, int ACT>
 __global__ void __launch_bounds__(256, kDactBlocksPerSm) lin_dact_kernel(const DactParams p) {
+  using S = DactShape<SRC>;
+  constexpr int P = kDactRing - 1;
+  constexpr uint32_t SB = S::BYTES * 256;
   __shared__ float red[8][32][9];
+  extern __shared__ uint4 ring[];  // [kDactRing][BYTES * 256], each kind an array over the threads
   pdl_wait();
   pdl_launch_dependents();
   const int cl = threadIdx.x & 31, rl = threadIdx.x >> 5;
   const int c = (blockIdx.x * 32 + cl) * 8;
-  const bool ok = c < p.N;
   const int64_t r0 = (int64_t)blockIdx.y * p.rows_per_block;
-  const int64_t r1 = min64(p.M, r0 + p.rows_per_block);
+  const int64_t r1 = c < p.N ? min64(p.M, r0 + p.rows_per_block) : 0;
   uint64_t acc[4], accr[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) acc[k] = accr[k] = 0;
-  if (ok) {
-    for (int64_t rb = r0 + rl; rb < r1; rb += 8 * kDactRows) {
-      uint4 dy[kDactRows], h[kDactRows];
-      uint32_t sb[kDactRows];
-#pragma unroll
-      for (int i = 0; i < kDactRows; ++i) {
-        const int64_t r = rb + 8 * i;
-        dy[i] = h[i] = make_uint4(0u, 0u, 0u, 0u);
-        sb[i] = 127u;
-        if (r < r1) {
-          dy[i] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.dy) + r * p.lddy + c);
-          if constexpr (SRC == DACT_TENSOR) h[i] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.h) + r * p.N + c);
-          if constexpr (SRC == DACT_CKPT) {
-            const uint2 q = *reinterpret_cast<const uint2*>(p.codes + r * p.N + c);
-            h[i].x = q.x;
-            h[i].y = q.y;
-            sb[i] = p.scales[r * p.pitch + (c >> 5)];
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kDactRows; ++i) {
-        const int64_t r = rb + 8 * i;
-        if (r >= r1) break;
-        uint64_t v[4];
-        unpack8<ELEM>(&dy[i], v);
-        if constexpr (SRC != DACT_NONE) {
-          uint64_t z[4], sl[4];
-          if constexpr (SRC == DACT_TENSOR) unpack8<ELEM>(&h[i], z);
-          else decode8(make_uint2(h[i].x, h[i].y), ckpt_scale(sb[i]), p.dt, z);
-          slope8<ACT>(z, sl);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) v[k] = mul_2(v[k], sl[k]);
-          uint4 w;
-          pack8<ELEM>(v, &w);
-          *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.dz) + r * p.N + c) = w;
-          if (p.both) {
-            uint64_t u[4];
-            unpack8<ELEM>(&w, u);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) accr[k] = add_2(accr[k], u[k]);
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) acc[k] = add_2(acc[k], v[k]);
+  const uint32_t base = (uint32_t)__cvta_generic_to_shared(ring);
+  const uint32_t a_dy = threadIdx.x * 16, a_h = S::H_OFF * 256 + threadIdx.x * (SRC == DACT_TENSOR ? 16 : 8),
+                 a_s = S::S_OFF * 256 + threadIdx.x * 4;
+  int64_t r = r0 + rl;
+  const uint16_t* dyp = reinterpret_cast<const uint16_t*>(p.dy) + r * p.lddy + c;
+  const uint16_t* hp = reinterpret_cast<const uint16_t*>(p.h) + r * p.N + c;
+  const uint8_t* qp = p.codes + r * p.N + c;
+  const uint8_t* sp = p.scales + r * p.pitch + ((c >> 7) << 2);  // the word that holds this column's scale byte
+  const int64_t dystep = 8 * p.lddy, hstep = 8 * (int64_t)p.N, sstep = 8 * p.pitch;
+  auto issue = [&](int64_t row, uint32_t slot) {
+    if (row < r1) {
+      cp16(slot + a_dy, dyp);
+      dyp += dystep;
+      if constexpr (SRC == DACT_TENSOR) {
+        cp16(slot + a_h, hp);
+        hp += hstep;
+      } else if constexpr (SRC == DACT_CKPT) {
+        cp8(slot + a_h, qp);
+        cp4(slot + a_s, sp);
+        qp += hstep;
+        sp += sstep;
       }
     }
+    cp_commit();
+  };
+#pragma unroll
+  for (int k = 0; k < P; ++k) issue(r + 8 * k, base + k * SB);
+  uint32_t slot = base, last = base + P * SB;
+  const int byte = ((c >> 5) & 3) * 8;
+  uint16_t* zp = reinterpret_cast<uint16_t*>(p.dz) + r * p.N + c;
+  for (; r < r1; r += 8) {
+    issue(r + 8 * P, last);
+    cp_wait<P>();
+    uint64_t v[4];
+    uint4 w = lds16(slot + a_dy);
+    unpack8<ELEM>(&w, v);
+    if constexpr (SRC != DACT_NONE) {
+      uint64_t z[4], sl[4];
+      if constexpr (SRC == DACT_TENSOR) {
+        w = lds16(slot + a_h);
+        unpack8<ELEM>(&w, z);
+      } else {
+        decode8(lds8(slot + a_h), ckpt_scale((lds4(slot + a_s) >> byte) & 0xFFu), p.dt, z);
+      }
+      slope8<ACT>(z, sl);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = mul_2(v[k], sl[k]);
+      pack8<ELEM>(v, &w);
+      *reinterpret_cast<uint4*>(zp) = w;
+      zp += hstep;
+      if (p.both) {
+        uint64_t u[4];
+        unpack8<ELEM>(&w, u);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) accr[k] = add_2(accr[k], u[k]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] = add_2(acc[k], v[k]);
+    last = slot;
+    slot = slot == base + P * SB ? base : slot + SB;
   }
+  cp_wait<0>();
   if (p.part == nullptr) return;
   for (int k = 0; k <= p.both; ++k) {
     __syncthreads();
@@ -482,6 +508,16 @@ lnfp8_status tile_launch(const LinGemm& g, cudaStream_t st) {
 
 #include "linear_pair.cuh"
 
+template <int ELEM, int SRC, int ACT>
+lnfp8_status dact_launch(const DactParams& p, dim3 grid, cudaStream_t st) {
+  constexpr auto k = lin_dact_kernel<ELEM, SRC, ACT>;
+  const lnfp8_status set = kernel_setup<k>(256, DactShape<SRC>::SMEM, nullptr, "linear_act_bwd: kernel set-up");
+  if (set != LNFP8_OK) return set;
+  LaunchScope ls("linear_dact", st);
+  if (launch_pdl(k, grid, dim3(256), DactShape<SRC>::SMEM, st, p) != cudaSuccess) return check_launch("linear_act_bwd launch");
+  return check_launch("linear_act_bwd: dz");
+}
+
 // Rows of the dz pass per block: one wave of resident blocks.
 int64_t dact_rows_per_block(int64_t M, int64_t N) {
   const int64_t col_blocks = (N + 255) / 256;
@@ -590,20 +626,17 @@ lnfp8_status linear_act_bwd_launch(const lnfp8_linear_act_bwd_args* a, cudaStrea
     p.dt = a->h_ckpt.dtype;
     p.rows_per_block = (int)dact_rows_per_block(a->M, a->N);
     const int64_t row_blocks = (a->M + p.rows_per_block - 1) / p.rows_per_block;
-    auto go = [&](auto kernel) {
-      LaunchScope ls("linear_dact", st);
-      if (launch_pdl(kernel, dim3((unsigned)((a->N + 255) / 256), (unsigned)row_blocks), dim3(256), 0, st, p) != cudaSuccess)
-        return check_launch("linear_act_bwd launch");
-      return check_launch("linear_act_bwd: dz");
-    };
+    const dim3 grid((unsigned)((a->N + 255) / 256), (unsigned)row_blocks);
     auto pick = [&](auto elem) {
       constexpr int E = decltype(elem)::value;
-      if (!has_act) return go(lin_dact_kernel<E, DACT_NONE, LNFP8_ACT_NONE>);
+      if (!has_act) return dact_launch<E, DACT_NONE, LNFP8_ACT_NONE>(p, grid, st);
       if (p.codes)
-        return a->act == LNFP8_ACT_GELU ? go(lin_dact_kernel<E, DACT_CKPT, LNFP8_ACT_GELU>)
-               : a->act == LNFP8_ACT_SILU ? go(lin_dact_kernel<E, DACT_CKPT, LNFP8_ACT_SILU>) : go(lin_dact_kernel<E, DACT_CKPT, LNFP8_ACT_RELU>);
-      return a->act == LNFP8_ACT_GELU ? go(lin_dact_kernel<E, DACT_TENSOR, LNFP8_ACT_GELU>)
-             : a->act == LNFP8_ACT_SILU ? go(lin_dact_kernel<E, DACT_TENSOR, LNFP8_ACT_SILU>) : go(lin_dact_kernel<E, DACT_TENSOR, LNFP8_ACT_RELU>);
+        return a->act == LNFP8_ACT_GELU   ? dact_launch<E, DACT_CKPT, LNFP8_ACT_GELU>(p, grid, st)
+               : a->act == LNFP8_ACT_SILU ? dact_launch<E, DACT_CKPT, LNFP8_ACT_SILU>(p, grid, st)
+                                          : dact_launch<E, DACT_CKPT, LNFP8_ACT_RELU>(p, grid, st);
+      return a->act == LNFP8_ACT_GELU   ? dact_launch<E, DACT_TENSOR, LNFP8_ACT_GELU>(p, grid, st)
+             : a->act == LNFP8_ACT_SILU ? dact_launch<E, DACT_TENSOR, LNFP8_ACT_SILU>(p, grid, st)
+                                        : dact_launch<E, DACT_TENSOR, LNFP8_ACT_RELU>(p, grid, st);
     };
     lnfp8_status s = a->elem == LNFP8_BF16 ? pick(std::integral_constant<int, LNFP8_BF16>()) : pick(std::integral_constant<int, LNFP8_FP16>());
     if (s != LNFP8_OK) return s;
