@@ -210,7 +210,8 @@ struct LinGemm {
   const void* cvec;    // [N] elem
   const float* rvec;   // [M]
 };
-lnfp8_status lin_gemm_launch(const LinGemm& g, cudaStream_t st);
+// One product of K-major operands (with the epilogue), or one or two independent ones of an MN-major b.
+lnfp8_status lin_gemm_launch(const LinGemm* g, int count, cudaStream_t st);
 lnfp8_status lin_status_read_clear(unsigned int* word);
 lnfp8_status linear_act_fwd_launch(const lnfp8_linear_act_fwd_args* a, cudaStream_t st);
 int64_t linear_act_bwd_ws_bytes(int64_t M, int64_t K, int64_t N, bool has_act, bool x_from_ckpt);

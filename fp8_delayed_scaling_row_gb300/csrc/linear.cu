@@ -120,17 +120,26 @@ struct TileCfg {
   static_assert(128 * (BN + 4) * 4 <= STAGES * STAGE && BN * 132 * 4 <= STAGES * STAGE, "the fp32 tile reuses the ring");
 };
 
-struct TileParams {
+// One product, or (neither swapped) two independent ones in one launch: the first `clusters` clusters
+// take the first product's tiles.
+struct TileProb {
   EpiParams e;
-  int num_p, num_kb, splits, kb_per_split;
+  int num_p, num_kb, kb_per_split, clusters, p_mn;
   uint32_t idesc;
+};
+struct TileParams {
+  TileProb prob[2];
+  int splits;
+};
+struct TileMaps {
+  CUtensorMap p[2], q[2];
 };
 
 constexpr int kTileThreads = 256;
 
-template <int BN, bool P_MN, bool Q_MN, bool SWAP>
+template <int BN, bool Q_MN, bool SWAP>
 __global__ void __launch_bounds__(kTileThreads, 1)
-lin_tile_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ, const TileParams p) {
+lin_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ TileParams p) {
   using C = TileCfg<BN>;
   constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
@@ -152,8 +161,8 @@ lin_tile_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
     mbar_init(done_bar, 1);
     *abort_flag = 0;
     mbar_init_fence();
-    tma_prefetch_map(&tmP);
-    tma_prefetch_map(&tmQ);
+    tma_prefetch_map(&maps.p[0]);
+    tma_prefetch_map(&maps.q[0]);
   }
   if (warp == 1) tmem_alloc<false>(smem_u32((const void*)(misc + 1)), C::TMEM_COLS);
   tc_fence_before();
@@ -165,9 +174,13 @@ lin_tile_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
 
   const int S = p.splits;
   const int rank = S > 1 ? (int)cluster_rank() : 0;
-  const int tile = blockIdx.x / S;
-  const int p0 = (tile % p.num_p) * 128, q0 = (tile / p.num_p) * BN;
-  const int kb0 = rank * p.kb_per_split, kb1 = min(p.num_kb, kb0 + p.kb_per_split);
+  const int cl = blockIdx.x / S, which = cl >= p.prob[0].clusters ? 1 : 0;
+  const TileProb& pr = p.prob[which];
+  const CUtensorMap *tmP = &maps.p[which], *tmQ = &maps.q[which];
+  const int tile = which ? cl - p.prob[0].clusters : cl;
+  const int p0 = (tile % pr.num_p) * 128, q0 = (tile / pr.num_p) * BN;
+  const int kb0 = rank * pr.kb_per_split, kb1 = min(pr.num_kb, kb0 + pr.kb_per_split);
+  const bool p_mn = pr.p_mn != 0;
 
   if (warp == 0 && lane == 0) {
     int stage = 0;
@@ -178,15 +191,15 @@ lin_tile_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
       if (!mbar_wait(empty_bar(stage), phase ^ 1, abort_flag)) { ok = false; break; }
       const uint32_t fb = full_bar(stage), pd = ring + stage * C::STAGE, qd = pd + C::P_BYTES;
       mbar_expect_tx(fb, C::STAGE);
-      if constexpr (!P_MN) tma_load(pd, &tmP, kb * BK, p0, fb);
+      if (!p_mn) tma_load(pd, tmP, kb * BK, p0, fb);
       else {
-        tma_load(pd, &tmP, p0, kb * BK, fb);
-        tma_load(pd + 8192, &tmP, p0 + 64, kb * BK, fb);
+        tma_load(pd, tmP, p0, kb * BK, fb);
+        tma_load(pd + 8192, tmP, p0 + 64, kb * BK, fb);
       }
-      if constexpr (!Q_MN) tma_load(qd, &tmQ, kb * BK, q0, fb);
+      if constexpr (!Q_MN) tma_load(qd, tmQ, kb * BK, q0, fb);
       else
 #pragma unroll
-        for (int j = 0; j < BN / 64; ++j) tma_load(qd + j * 8192, &tmQ, q0 + 64 * j, kb * BK, fb);
+        for (int j = 0; j < BN / 64; ++j) tma_load(qd + j * 8192, tmQ, q0 + 64 * j, kb * BK, fb);
       ++issued;
       if (++stage == STAGES) { stage = 0; phase ^= 1; }
     }
@@ -198,15 +211,16 @@ lin_tile_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
   } else if (warp == 1 && lane == 0) {
     int stage = 0;
     uint32_t phase = 0;
+    const uint32_t p_step = p_mn ? 2048 : 32, p_lbo = p_mn ? 8192 : 16;  // P's descriptor by its layout
     for (int kb = kb0; kb < kb1; ++kb) {
       if (!mbar_wait(full_bar(stage), phase, abort_flag)) break;
       tc_fence_after();
       const uint32_t pb = ring + stage * C::STAGE, qb = pb + C::P_BYTES;
 #pragma unroll
       for (int kk = 0; kk < BK / 16; ++kk) {
-        const uint64_t pd = P_MN ? mat_desc(pb + kk * 2048, 8192, 1024) : mat_desc(pb + kk * 32, 16, 1024);
+        const uint64_t pd = mat_desc(pb + kk * p_step, p_lbo, 1024);
         const uint64_t qd = Q_MN ? mat_desc(qb + kk * 2048, 8192, 1024) : mat_desc(qb + kk * 32, 16, 1024);
-        mma_16bit<false>(tmem, pd, qd, p.idesc, kb != kb0 || kk != 0);
+        mma_16bit<false>(tmem, pd, qd, pr.idesc, kb != kb0 || kk != 0);
       }
       mma_commit<false>(empty_bar(stage));
       if (++stage == STAGES) { stage = 0; phase ^= 1; }
@@ -266,7 +280,7 @@ lin_tile_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
       v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
     }
     const int m = (SWAP ? q0 : p0) + r, n = (SWAP ? p0 : q0) + c;
-    epilogue8(p.e, v, m, n, m < p.e.M && n < p.e.N);
+    epilogue8(pr.e, v, m, n, m < pr.e.M && n < pr.e.N);
   }
   __syncthreads();
   if (S > 1) cluster_sync_all();  // nobody leaves while its tile may still be read
@@ -460,29 +474,46 @@ EpiParams epi_params(const LinGemm& g) {
   return e;
 }
 
-template <int BN, bool P_MN, bool Q_MN, bool SWAP>
-lnfp8_status tile_launch(const LinGemm& g, cudaStream_t st) {
+template <int BN, bool Q_MN, bool SWAP>
+lnfp8_status tile_launch(const LinGemm* g, int count, cudaStream_t st) {
   using C = TileCfg<BN>;
-  constexpr auto k = lin_tile_kernel<BN, P_MN, Q_MN, SWAP>;
+  constexpr auto k = lin_tile_kernel<BN, Q_MN, SWAP>;
   const lnfp8_status set = kernel_setup<k>(kTileThreads, C::SMEM, nullptr, "linear: kernel set-up");
   if (set != LNFP8_OK) return set;
-  const int64_t prow = SWAP ? g.N : g.M, qrow = SWAP ? g.M : g.N;
-  const int64_t num_p = (prow + 127) / 128, num_q = (qrow + BN - 1) / BN;
-  TileParams p;
-  p.e = epi_params(g);
-  p.num_p = (int)num_p;
-  p.num_kb = (int)((g.K + BK - 1) / BK);
+  TileParams p = {};
+  TileMaps maps;
+  int64_t tiles = 0;
+  int min_kb = 0x7FFFFFFF;
+  bool ok = true;
+  for (int i = 0; i < count; ++i) {
+    const LinGemm& q = g[i];
+    TileProb& r = p.prob[i];
+    const int64_t prow = SWAP ? q.N : q.M, qrow = SWAP ? q.M : q.N;
+    const bool p_mn = SWAP ? q.b_mn : q.a_mn;
+    const int64_t num_p = (prow + 127) / 128, num_q = (qrow + BN - 1) / BN;
+    if (num_p * num_q > 0x0FFFFFFF) return set_error(LNFP8_ERR_UNSUPPORTED_SHAPE, "linear: too many tiles");
+    r.e = epi_params(q);
+    r.num_p = (int)num_p;
+    r.num_kb = (int)((q.K + BK - 1) / BK);
+    r.clusters = (int)(num_p * num_q);
+    r.p_mn = p_mn;
+    r.idesc = make_idesc(q.elem, 128, BN, p_mn, Q_MN);
+    tiles += num_p * num_q;
+    min_kb = r.num_kb < min_kb ? r.num_kb : min_kb;
+    ok = ok && (SWAP ? operand_map(&maps.p[i], q.b, p_mn, q.N, q.K, q.ldb, 128) && operand_map(&maps.q[i], q.a, Q_MN, q.M, q.K, q.lda, BN)
+                     : operand_map(&maps.p[i], q.a, p_mn, q.M, q.K, q.lda, 128) && operand_map(&maps.q[i], q.b, Q_MN, q.N, q.K, q.ldb, BN));
+  }
+  if (!ok) return set_error(LNFP8_ERR_CUDA, "linear: cuTensorMapEncodeTiled failed (driver entry point or arguments)");
+  if (count == 1) {
+    p.prob[1] = p.prob[0];
+    maps.p[1] = maps.p[0];
+    maps.q[1] = maps.q[0];
+  }
   // K pieces: while they run on SMs that would idle and each keeps a few K blocks
   int S = 1;
-  while (S < 8 && num_p * num_q * S * 2 <= num_sms() && p.num_kb >= S * 2 * 2) S *= 2;
+  while (S < 8 && tiles * S * 2 <= num_sms() && min_kb >= S * 2 * 2) S *= 2;
   p.splits = S;
-  p.kb_per_split = (p.num_kb + S - 1) / S;
-  if (num_p * num_q * S > 0x7FFFFFFF) return set_error(LNFP8_ERR_UNSUPPORTED_SHAPE, "linear: too many tiles");
-  p.idesc = make_idesc(g.elem, 128, BN, P_MN, Q_MN);
-  CUtensorMap tp, tq;
-  const bool ok = SWAP ? operand_map(&tp, g.b, P_MN, g.N, g.K, g.ldb, 128) && operand_map(&tq, g.a, Q_MN, g.M, g.K, g.lda, BN)
-                       : operand_map(&tp, g.a, P_MN, g.M, g.K, g.lda, 128) && operand_map(&tq, g.b, Q_MN, g.N, g.K, g.ldb, BN);
-  if (!ok) return set_error(LNFP8_ERR_CUDA, "linear: cuTensorMapEncodeTiled failed (driver entry point or arguments)");
+  for (TileProb& r : p.prob) r.kb_per_split = (r.num_kb + S - 1) / S;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -491,14 +522,14 @@ lnfp8_status tile_launch(const LinGemm& g, cudaStream_t st) {
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)(num_p * num_q * S));
+  cfg.gridDim = dim3((unsigned)(tiles * S));
   cfg.blockDim = dim3(kTileThreads);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
   LaunchScope ls("linear_tile", st);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, tp, tq, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, maps, p);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return set_error(LNFP8_ERR_CUDA, "linear launch: %s", cudaGetErrorString(e));
@@ -529,26 +560,37 @@ int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
 }  // namespace
 
-lnfp8_status lin_gemm_launch(const LinGemm& g, cudaStream_t st) {
-  if (g.M == 0 || g.N == 0) return LNFP8_OK;
-  const bool swap = g.M <= 64 && !g.a_mn;
-  if (swap && !g.b_mn) {
-    if (g.M <= 16) return tile_launch<16, false, false, true>(g, st);
-    if (g.M <= 32) return tile_launch<32, false, false, true>(g, st);
-    return tile_launch<64, false, false, true>(g, st);
+namespace {
+// Enough 256 x 256 tiles for half of the CTA pairs.
+bool takes_pairs(const LinGemm& g) { return ((g.M + 255) / 256) * ((g.N + 255) / 256) * 4 >= num_sms(); }
+bool takes_swap(const LinGemm& g) { return g.M <= 64 && !g.a_mn; }
+
+lnfp8_status swap_launch(const LinGemm& g, cudaStream_t st) {
+  if (g.M <= 16) return tile_launch<16, false, true>(&g, 1, st);
+  if (g.M <= 32) return tile_launch<32, false, true>(&g, 1, st);
+  return tile_launch<64, false, true>(&g, 1, st);
+}
+}  // namespace
+
+lnfp8_status lin_gemm_launch(const LinGemm* g, int count, cudaStream_t st) {
+  if (!g[0].b_mn) {  // the forward: both operands K-major
+    if (g->M == 0 || g->N == 0) return LNFP8_OK;
+    if (takes_swap(*g)) return swap_launch(*g, st);
+    return takes_pairs(*g) ? pair_launch<256, LIN_FULL>(g, 1, st) : tile_launch<128, false, false>(g, 1, st);
   }
-  if (swap) {
-    if (g.M <= 16) return tile_launch<16, true, false, true>(g, st);
-    if (g.M <= 32) return tile_launch<32, true, false, true>(g, st);
-    return tile_launch<64, true, false, true>(g, st);
+  // the backward: two products run in one launch where both take the same kernel
+  if (count == 2 && !takes_swap(g[0]) && !takes_swap(g[1])) {
+    if (takes_pairs(g[0]) && takes_pairs(g[1])) return pair_launch<256, LIN_PLAIN>(g, 2, st);
+    if (!takes_pairs(g[0]) && !takes_pairs(g[1])) return tile_launch<128, true, false>(g, 2, st);
   }
-  if (((g.M + 255) / 256) * ((g.N + 255) / 256) * 4 >= num_sms()) {
-    if (!g.a_mn && !g.b_mn) return pair_launch<256, false, false, LIN_FULL>(g, st);
-    if (!g.a_mn) return pair_launch<256, false, true, LIN_PLAIN>(g, st);
-    return g.cscale ? pair_launch<256, true, true, LIN_AFFINE>(g, st) : pair_launch<256, true, true, LIN_PLAIN>(g, st);
+  for (int i = 0; i < count; ++i) {
+    lnfp8_status s;
+    if (takes_swap(g[i])) s = swap_launch(g[i], st);
+    else if (takes_pairs(g[i])) s = pair_launch<256, LIN_PLAIN>(g + i, 1, st);
+    else s = tile_launch<128, true, false>(g + i, 1, st);
+    if (s != LNFP8_OK) return s;
   }
-  if (!g.a_mn) return g.b_mn ? tile_launch<128, false, true, false>(g, st) : tile_launch<128, false, false, false>(g, st);
-  return tile_launch<128, true, true, false>(g, st);
+  return LNFP8_OK;
 }
 
 lnfp8_status linear_act_fwd_launch(const lnfp8_linear_act_fwd_args* a, cudaStream_t st) {
@@ -569,7 +611,7 @@ lnfp8_status linear_act_fwd_launch(const lnfp8_linear_act_fwd_args* a, cudaStrea
   g.ldr = a->ld_residual;
   g.h = a->h;
   g.ckpt = a->ckpt;
-  return lin_gemm_launch(g, st);
+  return lin_gemm_launch(&g, 1, st);
 }
 
 // dz [M, N], the restored x [M, K], two column sums for the affine input, and the columns' partial
@@ -645,50 +687,49 @@ lnfp8_status linear_act_bwd_launch(const lnfp8_linear_act_bwd_args* a, cudaStrea
       if (s != LNFP8_OK) return s;
     }
   }
-  LinGemm g = {};
-  g.elem = a->elem;
+  LinGemm g[2] = {};
+  int count = 0;
   if (a->dx) {  // [M, K] = dz [M, N] . w, contracted over N
-    g.M = a->M;
-    g.N = a->K;
-    g.K = a->N;
-    g.a = dz;
-    g.lda = lddz;
-    g.b = a->w;
-    g.ldb = a->K;
-    g.b_mn = true;
-    g.out = a->dx;
-    g.ldo = a->ld_dx;
-    const lnfp8_status s = lin_gemm_launch(g, st);
-    if (s != LNFP8_OK) return s;
+    LinGemm& q = g[count++];
+    q.elem = a->elem;
+    q.M = a->M;
+    q.N = a->K;
+    q.K = a->N;
+    q.a = dz;
+    q.lda = lddz;
+    q.b = a->w;
+    q.ldb = a->K;
+    q.b_mn = true;
+    q.out = a->dx;
+    q.ldo = a->ld_dx;
   }
   if (a->dw) {  // [N, K] = dz^T . x, contracted over the tokens
-    const void* x = a->x;
-    int64_t ldx = a->ldx;
+    LinGemm& q = g[count++];
+    q.elem = a->elem;
+    q.b = a->x;
+    q.ldb = a->ldx;
     if (xck) {
       const lnfp8_status s = act_ckpt_restore_launch(a->x_ckpt, a->M, a->K, a->x_act, nullptr, nullptr, a->elem, x_ws, a->elem, a->K, st);
       if (s != LNFP8_OK) return s;
-      x = x_ws;
-      ldx = a->K;
+      q.b = x_ws;
+      q.ldb = a->K;
     }
-    g.M = a->N;
-    g.N = a->K;
-    g.K = a->M;
-    g.a = dz;
-    g.lda = lddz;
-    g.a_mn = true;
-    g.b = x;
-    g.ldb = ldx;
-    g.b_mn = true;
-    g.out = a->dw;
-    g.ldo = a->K;
+    q.M = a->N;
+    q.N = a->K;
+    q.K = a->M;
+    q.a = dz;
+    q.lda = lddz;
+    q.a_mn = true;
+    q.b_mn = true;
+    q.out = a->dw;
+    q.ldo = a->K;
     if (affine) {
-      g.cscale = a->x_gamma;
-      g.cvec = a->x_beta;
-      g.rvec = dbr;
+      q.cscale = a->x_gamma;
+      q.cvec = a->x_beta;
+      q.rvec = dbr;
     }
-    return lin_gemm_launch(g, st);
   }
-  return LNFP8_OK;
+  return count ? lin_gemm_launch(g, count, st) : LNFP8_OK;
 }
 
 }  // namespace lnfp8

@@ -11,10 +11,13 @@
 // columns, 32 x 32 at a time: a thread holds 32 columns of one row, which is one
 // checkpoint block, so the scale needs no exchange between threads.
 
+// A launch computes one product with the full epilogue (the forward), or up to two plain ones (the
+// backward's dx and dw, independent of one another): their tiles are one list, so that the last
+// round of the persistent loop is incomplete once, not twice (8192 x 2048 x 8192: 256 + 256 tiles on 76
+// pairs are 7 rounds instead of 4 + 4).
 enum LinEpi {
-  LIN_PLAIN = 0,   // out = T(acc)
-  LIN_FULL = 1,    // bias, saved pre-activation, activation, residual
-  LIN_AFFINE = 2,  // out = T(acc * cscale[col] + rvec[row] * cvec[col])
+  LIN_FULL = 0,   // bias, saved pre-activation, activation, residual; both operands K-major
+  LIN_PLAIN = 1,  // out = T(acc), or T(acc * cscale[col] + rvec[row] * cvec[col]); A either way, B MN-major
 };
 
 constexpr int kPairEpiWarps = 16;
@@ -37,16 +40,27 @@ struct PairCfg {
   static_assert(STAGES >= 4 && SMEM <= 232448, "shared memory budget");
 };
 
-struct PairParams {
-  int M, N, num_m2, num_n, num_kb, group_m;
+struct PairProb {
+  int M, N, num_m2, num_n, num_kb, group_m, tiles, a_mn;
   uint32_t idesc;
+  const void* cscale;  // with cvec and rvec, or NULL
+  const void* cvec;
+  const float* rvec;
+};
+
+struct PairParams {
+  PairProb prob[2];
+  int tiles;  // of both
+  // the full epilogue
   int f16, act, ck, has_resid, has_h, codes16;
-  const void* bias;     // FULL; AFFINE: cscale
-  const void* cvec;     // AFFINE
-  const float* rvec;    // AFFINE
+  const void* bias;
   uint8_t* codes;
   uint8_t* scales;
   int64_t pitch;
+};
+
+struct PairMaps {
+  CUtensorMap a[2], b[2], o[2], r, h;
 };
 
 // Tile t of a [num_m2 x num_n] grid: M fastest inside groups of G, then N, then the next
@@ -55,6 +69,17 @@ __device__ __forceinline__ int2 pair_tile(int t, int num_m2, int num_n, int G) {
   const int span = G * num_n, grp = t / span, r = t - grp * span, m0 = grp * G;
   const int gs = min(G, num_m2 - m0);
   return make_int2(m0 + r % gs, r / gs);
+}
+
+// The product and tile of position t in the list.
+struct PairTile {
+  int prob, m2, n;
+};
+__device__ __forceinline__ PairTile pair_locate(const PairParams& p, int t) {
+  const int q = t >= p.prob[0].tiles ? 1 : 0;
+  const PairProb& r = p.prob[q];
+  const int2 mn = pair_tile(q ? t - p.prob[0].tiles : t, r.num_m2, r.num_n, r.group_m);
+  return {q, mn.x, mn.y};
 }
 
 // Row r, 16-byte chunk j of a 32 x 32 16-bit box with the 64-byte swizzle.
@@ -67,12 +92,11 @@ __device__ __forceinline__ void act_pairs(uint64_t* z) {
   for (int i = 0; i < 16; i += 4) act8<ACT>(z + i);
 }
 
-template <int BN, bool A_MN, bool B_MN, int EPI>
+template <int BN, int EPI>
 __global__ void __launch_bounds__(kPairThreads, 1)
-lin_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmR,
-                const __grid_constant__ CUtensorMap tmH, const PairParams p) {
+lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ PairParams p) {
   using C = PairCfg<BN, EPI>;
+  constexpr bool B_MN = EPI == LIN_PLAIN;
   constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -103,8 +127,8 @@ lin_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     for (int w = 0; w < kPairEpiWarps; ++w) mbar_init(rload_bar(w), 1);
     *abort_flag = 0;
     mbar_init_fence();
-    tma_prefetch_map(&tmA);
-    tma_prefetch_map(&tmB);
+    tma_prefetch_map(&maps.a[0]);
+    tma_prefetch_map(&maps.b[0]);
   }
   cluster_sync_all();  // the peer signals this CTA's barriers
   if (warp == 1) tmem_alloc<true>(smem_u32((const void*)(misc + 1)), C::TMEM_COLS);
@@ -117,7 +141,7 @@ lin_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 
   const int rank = (int)cluster_rank();
   const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
-  const int tiles = p.num_m2 * p.num_n;
+  const int tiles = p.tiles;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -126,22 +150,25 @@ lin_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
       int64_t issued = 0;
       bool ok = true;
       for (int t = cid; t < tiles && ok; t += ncl) {
-        const int2 mn = pair_tile(t, p.num_m2, p.num_n, p.group_m);
-        const int m0 = mn.x * 256 + rank * 128, n0 = mn.y * BN + rank * (BN / 2);
-        for (int kb = 0; kb < p.num_kb; ++kb) {
+        const PairTile at = pair_locate(p, t);
+        const CUtensorMap *tmA = &maps.a[at.prob], *tmB = &maps.b[at.prob];
+        const bool a_mn = EPI == LIN_PLAIN && p.prob[at.prob].a_mn;
+        const int num_kb = p.prob[at.prob].num_kb;
+        const int m0 = at.m2 * 256 + rank * 128, n0 = at.n * BN + rank * (BN / 2);
+        for (int kb = 0; kb < num_kb; ++kb) {
           if (!mbar_wait(empty_bar(stage), phase ^ 1, abort_flag)) { ok = false; break; }
           const uint32_t fb = map_to_rank(full_bar(stage), 0);
           const uint32_t ad = ring + stage * C::STAGE, bd = ad + C::A_BYTES;
           if (rank == 0) mbar_expect_tx(full_bar(stage), 2 * C::STAGE);
-          if constexpr (!A_MN) tma_load_pair(ad, &tmA, kb * BK, m0, fb);
+          if (!a_mn) tma_load_pair(ad, tmA, kb * BK, m0, fb);
           else {
-            tma_load_pair(ad, &tmA, m0, kb * BK, fb);
-            tma_load_pair(ad + 8192, &tmA, m0 + 64, kb * BK, fb);
+            tma_load_pair(ad, tmA, m0, kb * BK, fb);
+            tma_load_pair(ad + 8192, tmA, m0 + 64, kb * BK, fb);
           }
-          if constexpr (!B_MN) tma_load_pair(bd, &tmB, kb * BK, n0, fb);
+          if constexpr (!B_MN) tma_load_pair(bd, tmB, kb * BK, n0, fb);
           else
 #pragma unroll
-            for (int j = 0; j < BN / 128; ++j) tma_load_pair(bd + j * 8192, &tmB, n0 + 64 * j, kb * BK, fb);
+            for (int j = 0; j < BN / 128; ++j) tma_load_pair(bd + j * 8192, tmB, n0 + 64 * j, kb * BK, fb);
           ++issued;
           if (++stage == STAGES) { stage = 0; phase ^= 1; }
         }
@@ -160,16 +187,22 @@ lin_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
       for (int t = cid; t < tiles && ok; t += ncl) {
         if (!mbar_wait(tempty_bar(acc), acc_phase ^ 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
+        const PairProb& pr = p.prob[t >= p.prob[0].tiles ? 1 : 0];
+        const uint32_t idesc = pr.idesc;
+        const int num_kb = pr.num_kb;
+        // the A descriptor's step per 16 k and its leading offset, by A's layout
+        const bool a_mn = EPI == LIN_PLAIN && pr.a_mn;
+        const uint32_t a_step = a_mn ? 2048 : 32, a_lbo = a_mn ? 8192 : 16;
         const uint32_t d = tmem + (uint32_t)(acc * BN);
-        for (int kb = 0; kb < p.num_kb; ++kb) {
+        for (int kb = 0; kb < num_kb; ++kb) {
           if (!mbar_wait(full_bar(stage), phase, abort_flag)) { ok = false; break; }
           tc_fence_after();
           const uint32_t ab = ring + stage * C::STAGE, bb = ab + C::A_BYTES;
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk) {
-            const uint64_t ad = A_MN ? mat_desc(ab + kk * 2048, 8192, 1024) : mat_desc(ab + kk * 32, 16, 1024);
+            const uint64_t ad = mat_desc(ab + kk * a_step, a_lbo, 1024);
             const uint64_t bd = B_MN ? mat_desc(bb + kk * 2048, 8192, 1024) : mat_desc(bb + kk * 32, 16, 1024);
-            mma_16bit<true>(d, ad, bd, p.idesc, kb != 0 || kk != 0);
+            mma_16bit<true>(d, ad, bd, idesc, kb != 0 || kk != 0);
           }
           mma_commit<true>(empty_bar(stage));
           if (++stage == STAGES) { stage = 0; phase ^= 1; }
@@ -193,12 +226,11 @@ lin_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     uint32_t rphase = 0, acc_phase = 0;
     bool r_pending = false;
     const uint32_t tempty = map_to_rank(tempty_bar(acc), 0);
-    auto tile_at = [&](int t) { return pair_tile(t, p.num_m2, p.num_n, p.group_m); };
     auto load_resid = [&](int t, int ch) {  // the 32 x 32 residual block of (tile, chunk)
       if (lane == 0) {
-        const int2 mn = tile_at(t);
+        const PairTile at = pair_locate(p, t);
         mbar_expect_tx(rbar, 2048);
-        tma_load(smem_u32(box_r), &tmR, mn.y * BN + half * HALF + ch * 32, mn.x * 256 + rank * 128 + quarter * 32, rbar);
+        tma_load(smem_u32(box_r), &maps.r, at.n * BN + half * HALF + ch * 32, at.m2 * 256 + rank * 128 + quarter * 32, rbar);
       }
       r_pending = true;
     };
@@ -206,20 +238,21 @@ lin_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     if constexpr (EPI == LIN_FULL)
       if (p.has_resid && t0 < tiles) load_resid(t0, 0);
     for (int t = t0; t < tiles; t += 2 * ncl) {
-      const int2 mn = tile_at(t);
-      const int m = mn.x * 256 + rank * 128 + quarter * 32 + lane;
-      const int nh = mn.y * BN + half * HALF;  // this warp's first column
+      const PairTile at = pair_locate(p, t);
+      const PairProb& pr = p.prob[at.prob];
+      const int m = at.m2 * 256 + rank * 128 + quarter * 32 + lane;
+      const int nh = at.n * BN + half * HALF;  // this warp's first column
       // four columns of the per-column vectors per lane, asked for before the accumulator is waited for
       uint2 cb = make_uint2(0u, 0u), cv = make_uint2(0u, 0u);
       float rv = 0.f;
       const int lc = nh + lane * 4;
-      if constexpr (EPI != LIN_PLAIN) {
-        if (p.bias && lane * 4 < HALF && lc < p.N) cb = __ldg(reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(p.bias) + lc));
+      const bool affine = EPI == LIN_PLAIN && pr.cscale != nullptr;
+      const void* col_vec = EPI == LIN_FULL ? p.bias : pr.cscale;
+      if (lane * 4 < HALF && lc < pr.N) {
+        if (col_vec) cb = __ldg(reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(col_vec) + lc));
+        if (affine) cv = __ldg(reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(pr.cvec) + lc));
       }
-      if constexpr (EPI == LIN_AFFINE) {
-        if (lane * 4 < HALF && lc < p.N) cv = __ldg(reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(p.cvec) + lc));
-        if (m < p.M) rv = __ldg(p.rvec + m);
-      }
+      if (affine && m < pr.M) rv = __ldg(pr.rvec + m);
       if (!mbar_wait(tfull_bar(acc), acc_phase, abort_flag)) break;
       tc_fence_after();
       bool aborted = false;
@@ -237,7 +270,7 @@ lin_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         uint64_t z[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) z[i] = pk(__uint_as_float(rr[2 * i]), __uint_as_float(rr[2 * i + 1]));
-        if constexpr (EPI != LIN_PLAIN) {
+        if (EPI == LIN_FULL || affine) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) {  // columns 2i, 2i + 1 of the chunk sit in lane 8 ch + i / 2
             const float2 b = unpack16(__shfl_sync(0xFFFFFFFFu, i & 1 ? cb.y : cb.x, ch * 8 + (i >> 1)), p.f16);
@@ -295,15 +328,15 @@ lin_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
               const float2 u = upk(mul_2(z[2 * i], i2)), v = upk(mul_2(z[2 * i + 1], i2));
               q[i] = fp8x2(u.x, u.y, p.ck) | (fp8x2(v.x, v.y, p.ck) << 16);
             }
-            if (m < p.M) {
-              uint8_t* dst = p.codes + (int64_t)m * p.N + n0;
-              if (p.codes16 && n0 + 32 <= p.N) {
+            if (m < pr.M) {
+              uint8_t* dst = p.codes + (int64_t)m * pr.N + n0;
+              if (p.codes16 && n0 + 32 <= pr.N) {
                 reinterpret_cast<uint4*>(dst)[0] = make_uint4(q[0], q[1], q[2], q[3]);
                 reinterpret_cast<uint4*>(dst)[1] = make_uint4(q[4], q[5], q[6], q[7]);
               } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                  if (n0 + 8 * j < p.N) reinterpret_cast<uint2*>(dst)[j] = make_uint2(q[2 * j], q[2 * j + 1]);
+                  if (n0 + 8 * j < pr.N) reinterpret_cast<uint2*>(dst)[j] = make_uint2(q[2 * j], q[2 * j + 1]);
               }
             }
           }
@@ -335,18 +368,18 @@ lin_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
-          const int y = mn.x * 256 + rank * 128 + quarter * 32;
-          if (y < p.M && n0 < p.N) {  // TMA clips the rest of a box at the tensor's edge
-            tma_store(&tmO, smem_u32(box_o), n0, y);
+          const int y = at.m2 * 256 + rank * 128 + quarter * 32;
+          if (y < pr.M && n0 < pr.N) {  // TMA clips the rest of a box at the tensor's edge
+            tma_store(&maps.o[at.prob], smem_u32(box_o), n0, y);
             if constexpr (EPI == LIN_FULL)
-              if (p.has_h) tma_store(&tmH, smem_u32(box_h), n0, y);
+              if (p.has_h) tma_store(&maps.h, smem_u32(box_h), n0, y);
           }
           bulk_commit();
         }
       }
       if (aborted) break;
       if constexpr (EPI == LIN_FULL) {
-        if (p.ck >= 0 && m < p.M && nh < p.N) {  // the four (or, at the edge, fewer) blocks' bytes, one word of the row
+        if (p.ck >= 0 && m < pr.M && nh < pr.N) {  // the four (or, at the edge, fewer) blocks' bytes, one word of the row
           if constexpr (CHUNKS == 4) *reinterpret_cast<uint32_t*>(p.scales + (int64_t)m * p.pitch + (nh >> 5)) = scale_word;
           else *reinterpret_cast<uint16_t*>(p.scales + (int64_t)m * p.pitch + (nh >> 5)) = (uint16_t)scale_word;
         }
@@ -371,41 +404,63 @@ lin_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
   cluster_sync_all();  // nobody leaves while the peer may still signal its barriers
 }
 
-template <int BN, bool A_MN, bool B_MN, int EPI>
-lnfp8_status pair_launch(const LinGemm& g, cudaStream_t st) {
+// One product (EPI LIN_FULL), or one or two (LIN_PLAIN).
+template <int BN, int EPI>
+lnfp8_status pair_launch(const LinGemm* g, int count, cudaStream_t st) {
   using C = PairCfg<BN, EPI>;
-  constexpr auto k = lin_pair_kernel<BN, A_MN, B_MN, EPI>;
+  constexpr auto k = lin_pair_kernel<BN, EPI>;
   const lnfp8_status set = kernel_setup<k>(kPairThreads, C::SMEM, nullptr, "linear: kernel set-up");
   if (set != LNFP8_OK) return set;
   PairParams p = {};
-  p.M = (int)g.M;
-  p.N = (int)g.N;
-  p.num_m2 = (int)((g.M + 255) / 256);
-  p.num_n = (int)((g.N + BN - 1) / BN);
-  p.num_kb = (int)((g.K + BK - 1) / BK);
-  if ((int64_t)p.num_m2 * p.num_n > 0x7FFFFFFF) return set_error(LNFP8_ERR_UNSUPPORTED_SHAPE, "linear: too many tiles");
-  // A panels (256 rows x K) of a raster group: what fits in 48 MB of L2
-  const int64_t panel = 512 * max64(g.K, 1);
-  p.group_m = (int)max64(1, min64((48ll << 20) / panel, p.num_m2));
-  p.idesc = make_idesc(g.elem, 256, BN, A_MN, B_MN);
-  p.f16 = g.elem == LNFP8_FP16;
-  p.act = g.act;
-  p.ck = g.ckpt.codes ? g.ckpt.dtype : -1;
-  p.has_resid = g.resid != nullptr;
-  p.has_h = g.h != nullptr;
-  p.bias = EPI == LIN_AFFINE ? g.cscale : g.bias;
-  p.cvec = g.cvec;
-  p.rvec = g.rvec;
-  p.codes = g.ckpt.codes;
-  p.scales = g.ckpt.scales;
-  p.codes16 = g.N % 16 == 0 && reinterpret_cast<uintptr_t>(g.ckpt.codes) % 16 == 0;
-  p.pitch = lnfp8_act_ckpt_scale_pitch(g.N);
-  CUtensorMap ta, tb, to, tr, th;
-  bool ok = operand_map(&ta, g.a, A_MN, g.M, g.K, g.lda, 128) && operand_map(&tb, g.b, B_MN, g.N, g.K, g.ldb, BN / 2) &&
-            make_map(&to, g.out, g.N, g.M, g.ldo, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
-  tr = th = to;
-  if (ok && g.resid) ok = make_map(&tr, g.resid, g.N, g.M, g.ldr, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
-  if (ok && g.h) ok = make_map(&th, g.h, g.N, g.M, g.N, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  PairMaps maps;
+  bool ok = true;
+  int64_t tiles = 0;
+  // the product of more K blocks first: the short tiles fill the last round
+  const int first = count == 2 && g[1].K > g[0].K ? 1 : 0;
+  for (int i = 0; i < count; ++i) {
+    const LinGemm& q = g[i ^ first];
+    PairProb& r = p.prob[i];
+    r.M = (int)q.M;
+    r.N = (int)q.N;
+    r.num_m2 = (int)((q.M + 255) / 256);
+    r.num_n = (int)((q.N + BN - 1) / BN);
+    r.num_kb = (int)((q.K + BK - 1) / BK);
+    // A panels (256 rows x K) of a raster group: what fits in 48 MB of L2
+    r.group_m = (int)max64(1, min64((48ll << 20) / (512 * max64(q.K, 1)), r.num_m2));
+    r.tiles = r.num_m2 * r.num_n;
+    r.a_mn = q.a_mn;
+    r.idesc = make_idesc(q.elem, 256, BN, q.a_mn, q.b_mn);
+    r.cscale = q.cscale;
+    r.cvec = q.cvec;
+    r.rvec = q.rvec;
+    tiles += (int64_t)r.num_m2 * r.num_n;
+    ok = ok && operand_map(&maps.a[i], q.a, q.a_mn, q.M, q.K, q.lda, 128) && operand_map(&maps.b[i], q.b, q.b_mn, q.N, q.K, q.ldb, BN / 2) &&
+         make_map(&maps.o[i], q.out, q.N, q.M, q.ldo, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  }
+  if (tiles > 0x3FFFFFFF) return set_error(LNFP8_ERR_UNSUPPORTED_SHAPE, "linear: too many tiles");
+  p.tiles = (int)tiles;
+  if (count == 1) {
+    p.prob[1] = p.prob[0];
+    maps.a[1] = maps.a[0];
+    maps.b[1] = maps.b[0];
+    maps.o[1] = maps.o[0];
+  }
+  maps.r = maps.h = maps.o[0];
+  p.f16 = g->elem == LNFP8_FP16;
+  p.ck = -1;
+  if constexpr (EPI == LIN_FULL) {
+    p.act = g->act;
+    p.ck = g->ckpt.codes ? g->ckpt.dtype : -1;
+    p.has_resid = g->resid != nullptr;
+    p.has_h = g->h != nullptr;
+    p.bias = g->bias;
+    p.codes = g->ckpt.codes;
+    p.scales = g->ckpt.scales;
+    p.codes16 = g->N % 16 == 0 && reinterpret_cast<uintptr_t>(g->ckpt.codes) % 16 == 0;
+    p.pitch = lnfp8_act_ckpt_scale_pitch(g->N);
+    if (ok && g->resid) ok = make_map(&maps.r, g->resid, g->N, g->M, g->ldr, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+    if (ok && g->h) ok = make_map(&maps.h, g->h, g->N, g->M, g->N, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  }
   if (!ok) return set_error(LNFP8_ERR_CUDA, "linear: cuTensorMapEncodeTiled failed (driver entry point or arguments)");
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
@@ -415,15 +470,14 @@ lnfp8_status pair_launch(const LinGemm& g, cudaStream_t st) {
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
-  const int64_t tiles = (int64_t)p.num_m2 * p.num_n, pairs = num_sms() / 2;
-  cfg.gridDim = dim3((unsigned)(2 * max64(1, min64(tiles, pairs))));
+  cfg.gridDim = dim3((unsigned)(2 * max64(1, min64(tiles, num_sms() / 2))));
   cfg.blockDim = dim3(kPairThreads);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
   LaunchScope ls("linear_pair", st);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, ta, tb, to, tr, th, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, maps, p);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return set_error(LNFP8_ERR_CUDA, "linear launch: %s", cudaGetErrorString(e));

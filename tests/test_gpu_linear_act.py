@@ -225,14 +225,20 @@ def test_strides_and_neighbours(L, M, K, N):
 
 
 def test_some_gradients_only(L):
+    """What is not asked for is left out. How many pieces K is cut into depends on which products a launch holds, so
+    a gradient asked for alone is another sum of the same terms: each is within sum_error of the exact one and half
+    a step of the type from that, and the two within twice that of one another. dbias is the same sum."""
     M, K, N = 200, 128, 192
     x, w, dy = draw(M, K, torch.bfloat16, 1), draw(N, K, torch.bfloat16, 2, 0.1), draw(M, N, torch.bfloat16, 3)
     full = L.linear_act_bwd(dy, x, w, L.LinearActCtx())
+    d = dy.double()
+    bound = {"dx": sum_error(N) * (d.abs() @ w.double().abs()), "dw": sum_error(M) * (d.abs().t() @ x.double().abs()), "dbias": 0}
     for keep in ("dx", "dw", "bias"):
         g = L.linear_act_grads(M, K, N, **{k: k == keep for k in ("dx", "dw", "bias")})
         L.linear_act_bwd(dy, x if keep == "dw" else None, w, L.LinearActCtx(), grads=g)
         name = "dbias" if keep == "bias" else keep
-        assert torch.equal(getattr(g, name), getattr(full, name))
+        want = getattr(full, name).double()
+        P.assert_within(getattr(g, name), want, 2 * (bound[name] + P.half(torch.bfloat16) * (want.abs() + bound[name])) * (name != "dbias"), name)
         assert sum(v is not None for v in (g.dx, g.dw, g.dbias)) == 1
     assert L.linear_act_bwd(dy, None, w, L.LinearActCtx()).dw is None
 
