@@ -134,6 +134,16 @@ ln_fwd_any_kernel(const LnFwdParams p) {
   pdl_launch_dependents();
   const int g = threadIdx.x / TPR, t = threadIdx.x % TPR;
   const float inv_d = 1.0f / (float)p.D;
+  constexpr bool HOLD = TPR < 1024;  // gamma and beta in registers (1024 threads have too few)
+  float ga[HOLD ? NE : 1], be[HOLD ? NE : 1];
+  if constexpr (HOLD) {
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+      if (t + TPR * i < p.D) {
+        ga[i] = load_elem_rt(p.gamma, p.param_elem, t + TPR * i);
+        be[i] = load_elem_rt(p.beta, p.param_elem, t + TPR * i);
+      }
+  }
   int turn = 0;
   for (int64_t row0 = (int64_t)blockIdx.x * GPB; row0 < p.M; row0 += (int64_t)gridDim.x * GPB) {
     const int64_t row = row0 + g;
@@ -168,8 +178,9 @@ ln_fwd_any_kernel(const LnFwdParams p) {
       const bool in = c < p.D;
       const float xh = v[i] * rs;
       if (in) {
-        const float ga = load_elem_rt(p.gamma, p.param_elem, c), be = load_elem_rt(p.beta, p.param_elem, c);
-        store_elem<ELEM>(p.y, row * p.ldy + c, fmaf(xh, ga, be));
+        const float gi = HOLD ? ga[HOLD ? i : 0] : load_elem_rt(p.gamma, p.param_elem, c);
+        const float bi = HOLD ? be[HOLD ? i : 0] : load_elem_rt(p.beta, p.param_elem, c);
+        store_elem<ELEM>(p.y, row * p.ldy + c, fmaf(xh, gi, bi));
       }
       if constexpr (CK) {
         const uint32_t b = ckpt_byte(warp_max_u32(in ? abs_bits(xh) : 0u), p.dt);
@@ -196,9 +207,14 @@ ln_bwd_any_kernel(const LnBwdParams p) {
   pdl_launch_dependents();
   const int g = threadIdx.x / TPR, t = threadIdx.x % TPR;
   const float inv_d = 1.0f / (float)p.D;
-  float accg[NE], accb[NE];
+  constexpr bool HOLD = TPR < 512;  // gamma in registers
+  float accg[NE], accb[NE], ga[HOLD ? NE : 1];
 #pragma unroll
-  for (int i = 0; i < NE; ++i) accg[i] = accb[i] = 0.f;
+  for (int i = 0; i < NE; ++i) {
+    accg[i] = accb[i] = 0.f;
+    if constexpr (HOLD)
+      if (t + TPR * i < p.D) ga[i] = load_elem_rt(p.gamma, p.param_elem, t + TPR * i);
+  }
   int turn = 0;
   for (int64_t row0 = (int64_t)blockIdx.x * GPB; row0 < p.M; row0 += (int64_t)gridDim.x * GPB) {
     const int64_t row = row0 + g;
@@ -219,7 +235,7 @@ ln_bwd_any_kernel(const LnBwdParams p) {
           xh[i] = (load_elem<ELEM>(p.x, row * p.ldx + c) - mu) * rs;
         accg[i] = fmaf(d, xh[i], accg[i]);
         accb[i] += d;
-        gg[i] = d * load_elem_rt(p.gamma, p.param_elem, c);
+        gg[i] = d * (HOLD ? ga[HOLD ? i : 0] : load_elem_rt(p.gamma, p.param_elem, c));
       }
       s1 += gg[i];
       s2 = fmaf(gg[i], xh[i], s2);

@@ -290,6 +290,100 @@ lin_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ T
   }
 }
 
+// ------------------------------------------------------------ a few tokens
+// One to four tokens: bound by the weight's bytes, so each warp streams kRowsPerWarp rows of w with
+// 16-byte loads straight into FMAs; x sits in shared memory in its own type. WK warps share a
+// row group (K cut into WK pieces, added in order) when there are too few rows to fill the SMs.
+// A lane's partial sum covers every 256th group of 8 columns; a warp's lanes are added by shuffles.
+constexpr int kRowsPerWarp = 2;
+constexpr int kFewTokens = 4;
+constexpr int kFewMaxX = 96 * 1024;  // bytes of x in shared memory
+
+template <int MT, bool F16>
+__global__ void __launch_bounds__(256) lin_few_kernel(const EpiParams e, const void* __restrict__ x, int64_t ldx,
+                                                      const void* __restrict__ w, int K, int WK) {
+  constexpr int ELEM = F16 ? LNFP8_FP16 : LNFP8_BF16;
+  extern __shared__ uint4 xs[];  // [MT][K / 8]
+  __shared__ float red[8][kRowsPerWarp][MT];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = warp / WK, part = warp % WK;
+  const int n0 = (blockIdx.x * (8 / WK) + group) * kRowsPerWarp;
+  const int K8 = K >> 3;
+  const int per = ((K8 + WK - 1) / WK + 31) / 32 * 32;  // 16-byte groups of a piece, whole warps of them
+  const int k0 = part * per, k1 = min(K8, k0 + per);
+  constexpr int U = 4;  // loads in flight per row
+  uint4 wv[kRowsPerWarp][U];
+  const uint4* wr[kRowsPerWarp];
+#pragma unroll
+  for (int r = 0; r < kRowsPerWarp; ++r) wr[r] = reinterpret_cast<const uint4*>(w) + (int64_t)min(n0 + r, e.N - 1) * K8;
+  auto fetch = [&](int k) {
+#pragma unroll
+    for (int r = 0; r < kRowsPerWarp; ++r)
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (k + 32 * u < k1) wv[r][u] = __ldcs(wr[r] + k + 32 * u);
+  };
+  fetch(k0 + lane);  // the first weights are on their way while x is staged
+  for (int m = 0; m < MT; ++m)
+    for (int k = threadIdx.x; k < K8; k += 256)
+      xs[m * K8 + k] = m < e.M ? reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(x) + m * ldx)[k] : make_uint4(0u, 0u, 0u, 0u);
+  __syncthreads();
+  uint64_t acc[kRowsPerWarp][MT];
+#pragma unroll
+  for (int r = 0; r < kRowsPerWarp; ++r)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[r][m] = 0;
+  for (int k = k0 + lane; k < k1; k += 32 * U) {
+    uint4 cur[kRowsPerWarp][U];
+#pragma unroll
+    for (int r = 0; r < kRowsPerWarp; ++r)
+#pragma unroll
+      for (int u = 0; u < U; ++u) cur[r][u] = wv[r][u];
+    fetch(k + 32 * U);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (k + 32 * u >= k1) break;
+      uint64_t wf[kRowsPerWarp][4];
+#pragma unroll
+      for (int r = 0; r < kRowsPerWarp; ++r) unpack8<ELEM>(&cur[r][u], wf[r]);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        uint64_t xf[4];
+        const uint4 xv = xs[m * K8 + k + 32 * u];
+        unpack8<ELEM>(&xv, xf);
+#pragma unroll
+        for (int r = 0; r < kRowsPerWarp; ++r)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[r][m] = fma_2(wf[r][i], xf[i], acc[r][m]);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kRowsPerWarp; ++r)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const float2 t = upk(acc[r][m]);
+      const float v = warp_sum(t.x + t.y);
+      if (lane == 0) red[warp][r][m] = v;
+    }
+  __syncthreads();
+  // one thread per (row group, row, token)
+  const int i = threadIdx.x;
+  if (i >= (8 / WK) * kRowsPerWarp * MT) return;
+  const int m = i % MT, r = i / MT % kRowsPerWarp, g = i / (MT * kRowsPerWarp);
+  const int n = (blockIdx.x * (8 / WK) + g) * kRowsPerWarp + r;
+  if (m >= e.M || n >= e.N) return;
+  float z = 0.f;
+  for (int q = 0; q < WK; ++q) z += red[g * WK + q][r][m];
+  if (e.bias) z += load_elem<ELEM>(e.bias, n);
+  if (e.h) store_elem<ELEM>(e.h, (int64_t)m * e.N + n, z);
+  z = act_fwd(z, e.act);
+  if (e.resid) z += load_elem<ELEM>(e.resid, m * e.ldr + n);
+  store_elem<ELEM>(e.out, m * e.ldo + n, z);
+}
+
 // ------------------------------------------------------------ dz = dy act'(h), db
 // A block takes 256 columns (32 threads of 8) and `rows_per_block` rows, 8 at a time; each
 // thread keeps the sums of its columns, added over the 8 row lanes at the end.
@@ -370,13 +464,17 @@ __global__ void __launch_bounds__(256, kDactBlocksPerSm) lin_dact_kernel(const D
     unpack8<ELEM>(&w, v);
     if constexpr (SRC != DACT_NONE) {
       uint64_t z[4], sl[4];
+      uint32_t sb = 0;
       if constexpr (SRC == DACT_TENSOR) {
         w = lds16(slot + a_h);
         unpack8<ELEM>(&w, z);
       } else {
-        decode8(lds8(slot + a_h), ckpt_scale((lds4(slot + a_s) >> byte) & 0xFFu), p.dt, z);
+        sb = (lds4(slot + a_s) >> byte) & 0xFFu;
+        decode8(lds8(slot + a_h), ckpt_scale(sb), p.dt, z);
       }
-      slope8<ACT>(z, sl);
+      // z^2 leaves fp32 only from bf16 values, or in blocks of scales above 2^40
+      if (SRC == DACT_TENSOR ? ELEM == LNFP8_BF16 : sb >= 167u) slope8<ACT, true>(z, sl);
+      else slope8<ACT, false>(z, sl);
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[k] = mul_2(v[k], sl[k]);
       pack8<ELEM>(v, &w);
@@ -565,6 +663,31 @@ namespace {
 bool takes_pairs(const LinGemm& g) { return ((g.M + 255) / 256) * ((g.N + 255) / 256) * 4 >= num_sms(); }
 bool takes_swap(const LinGemm& g) { return g.M <= 64 && !g.a_mn; }
 
+// The forward of one to four tokens, without a checkpoint (whose blocks span more columns than a warp
+// has here; a decoding step keeps none).
+bool takes_few(const LinGemm& g) {
+  return g.M <= kFewTokens && !g.a_mn && !g.b_mn && !g.ckpt.codes && g.K * (g.M > 2 ? 4 : g.M) * 2 <= kFewMaxX;
+}
+template <int MT, bool F16>
+lnfp8_status few_launch(const LinGemm& g, cudaStream_t st) {
+  constexpr auto k = lin_few_kernel<MT, F16>;
+  const lnfp8_status set = kernel_setup<k>(256, kFewMaxX, nullptr, "linear: kernel set-up");
+  if (set != LNFP8_OK) return set;
+  // warps per row group: until there are 16 warps for each SM, while each keeps 512 columns
+  int WK = 1;
+  while (WK < 8 && (g.N + kRowsPerWarp - 1) / kRowsPerWarp * WK < (int64_t)num_sms() * 16 && g.K >= 1024 * WK) WK *= 2;
+  const int64_t per_block = 8 / WK * kRowsPerWarp;
+  LaunchScope ls("linear_few", st);
+  if (launch_pdl(k, dim3((unsigned)((g.N + per_block - 1) / per_block)), dim3(256), (size_t)(MT * g.K * 2), st, epi_params(g), g.a, g.lda, g.b,
+                 (int)g.K, WK) != cudaSuccess)
+    return check_launch("linear launch");
+  return check_launch("linear");
+}
+template <bool F16>
+lnfp8_status few_by_tokens(const LinGemm& g, cudaStream_t st) {
+  return g.M == 1 ? few_launch<1, F16>(g, st) : g.M == 2 ? few_launch<2, F16>(g, st) : few_launch<4, F16>(g, st);
+}
+
 lnfp8_status swap_launch(const LinGemm& g, cudaStream_t st) {
   if (g.M <= 16) return tile_launch<16, false, true>(&g, 1, st);
   if (g.M <= 32) return tile_launch<32, false, true>(&g, 1, st);
@@ -575,6 +698,7 @@ lnfp8_status swap_launch(const LinGemm& g, cudaStream_t st) {
 lnfp8_status lin_gemm_launch(const LinGemm* g, int count, cudaStream_t st) {
   if (!g[0].b_mn) {  // the forward: both operands K-major
     if (g->M == 0 || g->N == 0) return LNFP8_OK;
+    if (takes_few(*g)) return g->elem == LNFP8_FP16 ? few_by_tokens<true>(*g, st) : few_by_tokens<false>(*g, st);
     if (takes_swap(*g)) return swap_launch(*g, st);
     return takes_pairs(*g) ? pair_launch<256, LIN_FULL>(g, 1, st) : tile_launch<128, false, false>(g, 1, st);
   }

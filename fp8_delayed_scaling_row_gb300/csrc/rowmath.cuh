@@ -391,7 +391,8 @@ __device__ __forceinline__ void act8(uint64_t* z) {
   }
 }
 
-template <int ACT>
+// FAR: z may be so large that its square leaves fp32.
+template <int ACT, bool FAR>
 __device__ __forceinline__ void slope8(const uint64_t* z, uint64_t* out) {
   if constexpr (ACT == LNFP8_ACT_RELU || ACT == LNFP8_ACT_NONE) {
 #pragma unroll
@@ -404,8 +405,11 @@ __device__ __forceinline__ void slope8(const uint64_t* z, uint64_t* out) {
     const uint64_t one = pk(1.0f, 1.0f), minus = pk(-1.0f, -1.0f);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float2 t = upk(mul_2(z[k], z[k]));
-      zz[k] = pk(fminf(t.x, 1e30f), fminf(t.y, 1e30f));  // see act_slope
+      zz[k] = mul_2(z[k], z[k]);
+      if constexpr (FAR) {
+        const float2 t = upk(zz[k]);
+        zz[k] = pk(fminf(t.x, 1e30f), fminf(t.y, 1e30f));  // see act_slope
+      }
       nu[k] = ACT == LNFP8_ACT_GELU ? gelu_nu2(z[k], zz[k]) : mul_2(z[k], pk(-kLog2e, -kLog2e));
     }
     logistic8(nu, s);
