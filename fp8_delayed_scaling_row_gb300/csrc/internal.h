@@ -209,6 +209,9 @@ struct LinGemm {
   const void* cscale;  // [N] elem
   const void* cvec;    // [N] elem
   const float* rvec;   // [M]
+  // K cut into `pieces` whose fp32 products [pieces][M][N] go to `part` and are added afterwards (0: whole)
+  int pieces;
+  float* part;
 };
 // One product of K-major operands (with the epilogue), or one or two independent ones of an MN-major b.
 lnfp8_status lin_gemm_launch(const LinGemm* g, int count, cudaStream_t st);

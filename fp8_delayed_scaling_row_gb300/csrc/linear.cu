@@ -102,22 +102,24 @@ __device__ __forceinline__ void epilogue8(const EpiParams& p, float* v, int m, i
 }
 
 // ------------------------------------------------------------ one tile per cluster
-// A cluster of S CTAs computes one tile, each CTA a piece of K with the 1-SM MMA
-// (128 x BN x 16), then the pieces' fp32 sums are read from one another's shared
-// memory and added in rank order, each CTA finishing 1/S of the tile's rows: K is
-// split over S SMs without a workspace, and the result does not depend on timing.
-// SWAP: the 128 accumulator lanes are output features and the BN columns tokens, so
-// that few tokens fill the instruction; else lanes are tokens.
-template <int BN>
+// A cluster computes one tile, its K cut into S pieces on S SMs (PAIR: S CTA pairs). The pieces'
+// fp32 sums are then read from one another's shared memory and added in the pieces' order, each CTA
+// finishing 1/S of its rows of the tile: no workspace, and the result does not depend on timing.
+//   PAIR    the 2-SM MMA, 256 x BN x 16: a CTA holds 128 rows and loads half of the BN side. A
+//           128 x 128 tile on one SM reads and fills 256 bytes of shared memory a clock, twice what
+//           there is; 256 x 256 on a pair just fits (measured on 181 x 6392 x 7112: 52 -> 23 us).
+//   SWAP    the accumulator's lanes are output features and its BN columns tokens, so that few
+//           tokens fill the instruction; else lanes are tokens.
+template <int BN, bool PAIR>
 struct TileCfg {
   static constexpr int P_BYTES = 128 * BK * 2;
-  static constexpr int Q_BYTES = BN * BK * 2;
+  static constexpr int Q_BYTES = (PAIR ? BN / 2 : BN) * BK * 2;
   static constexpr int STAGE = P_BYTES + Q_BYTES;
   static constexpr int STAGES = 196608 / STAGE > 8 ? 8 : 196608 / STAGE;
   static constexpr int SMEM = 1024 + STAGES * STAGE + 256;
   static constexpr int TMEM_COLS = BN < 32 ? 32 : BN;
   static_assert(SMEM <= 232448, "shared memory budget");
-  static_assert(128 * (BN + 4) * 4 <= STAGES * STAGE && BN * 132 * 4 <= STAGES * STAGE, "the fp32 tile reuses the ring");
+  static_assert(128 * (BN + 4) * 4 <= STAGES * STAGE, "the fp32 tile reuses the ring");
 };
 
 // One product, or (neither swapped) two independent ones in one launch: the first `clusters` clusters
@@ -137,11 +139,11 @@ struct TileMaps {
 
 constexpr int kTileThreads = 256;
 
-template <int BN, bool Q_MN, bool SWAP>
+template <int BN, bool PAIR, bool Q_MN, bool SWAP>
 __global__ void __launch_bounds__(kTileThreads, 1)
 lin_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ TileParams p) {
-  using C = TileCfg<BN>;
-  constexpr int STAGES = C::STAGES;
+  using C = TileCfg<BN, PAIR>;
+  constexpr int STAGES = C::STAGES, SIDES = PAIR ? 2 : 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t ring = smem_u32(smem);
@@ -152,6 +154,8 @@ lin_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ T
   auto empty_bar = [&](int s) { return bars + 8u * (STAGES + s); };
   const uint32_t done_bar = bars + 8u * (2 * STAGES);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int S = p.splits;
+  const bool clustered = S * SIDES > 1;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -164,7 +168,8 @@ lin_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ T
     tma_prefetch_map(&maps.p[0]);
     tma_prefetch_map(&maps.q[0]);
   }
-  if (warp == 1) tmem_alloc<false>(smem_u32((const void*)(misc + 1)), C::TMEM_COLS);
+  if constexpr (PAIR) cluster_sync_all();  // the peer signals this CTA's barriers
+  if (warp == 1) tmem_alloc<PAIR>(smem_u32((const void*)(misc + 1)), C::TMEM_COLS);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -172,43 +177,50 @@ lin_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ T
   pdl_wait();
   pdl_launch_dependents();
 
-  const int S = p.splits;
-  const int rank = S > 1 ? (int)cluster_rank() : 0;
-  const int cl = blockIdx.x / S, which = cl >= p.prob[0].clusters ? 1 : 0;
+  const int crank = clustered ? (int)cluster_rank() : 0;
+  const int side = PAIR ? crank & 1 : 0, piece = crank / SIDES, leader = crank - side;
+  const int cl = blockIdx.x / (S * SIDES), which = cl >= p.prob[0].clusters ? 1 : 0;
   const TileProb& pr = p.prob[which];
   const CUtensorMap *tmP = &maps.p[which], *tmQ = &maps.q[which];
   const int tile = which ? cl - p.prob[0].clusters : cl;
-  const int p0 = (tile % pr.num_p) * 128, q0 = (tile / pr.num_p) * BN;
-  const int kb0 = rank * pr.kb_per_split, kb1 = min(pr.num_kb, kb0 + pr.kb_per_split);
+  const int p0 = (tile % pr.num_p) * (128 * SIDES) + side * 128, q0 = (tile / pr.num_p) * BN;
+  const int kb0 = piece * pr.kb_per_split, kb1 = min(pr.num_kb, kb0 + pr.kb_per_split);
   const bool p_mn = pr.p_mn != 0;
+  const uint16_t both = (uint16_t)(3u << leader);
 
   if (warp == 0 && lane == 0) {
     int stage = 0;
     uint32_t phase = 0;
     int issued = 0;
     bool ok = true;
+    auto load = [&](uint32_t dst, const CUtensorMap* tm, int x, int y, uint32_t bar) {
+      if constexpr (PAIR) tma_load_pair(dst, tm, x, y, bar);
+      else tma_load(dst, tm, x, y, bar);
+    };
+    const int qs = q0 + side * (BN / 2);  // the rows of Q this CTA loads
     for (int kb = kb0; kb < kb1; ++kb) {
       if (!mbar_wait(empty_bar(stage), phase ^ 1, abort_flag)) { ok = false; break; }
-      const uint32_t fb = full_bar(stage), pd = ring + stage * C::STAGE, qd = pd + C::P_BYTES;
-      mbar_expect_tx(fb, C::STAGE);
-      if (!p_mn) tma_load(pd, tmP, kb * BK, p0, fb);
+      const uint32_t pd = ring + stage * C::STAGE, qd = pd + C::P_BYTES;
+      const uint32_t fb = PAIR ? map_to_rank(full_bar(stage), leader) : full_bar(stage);
+      if (side == 0) mbar_expect_tx(full_bar(stage), SIDES * C::STAGE);
+      if (!p_mn) load(pd, tmP, kb * BK, p0, fb);
       else {
-        tma_load(pd, tmP, p0, kb * BK, fb);
-        tma_load(pd + 8192, tmP, p0 + 64, kb * BK, fb);
+        load(pd, tmP, p0, kb * BK, fb);
+        load(pd + 8192, tmP, p0 + 64, kb * BK, fb);
       }
-      if constexpr (!Q_MN) tma_load(qd, tmQ, kb * BK, q0, fb);
+      if constexpr (!Q_MN) load(qd, tmQ, kb * BK, qs, fb);
       else
 #pragma unroll
-        for (int j = 0; j < BN / 64; ++j) tma_load(qd + j * 8192, tmQ, q0 + 64 * j, kb * BK, fb);
+        for (int j = 0; j < BN / SIDES / 64; ++j) load(qd + j * 8192, tmQ, qs + 64 * j, kb * BK, fb);
       ++issued;
       if (++stage == STAGES) { stage = 0; phase ^= 1; }
     }
-    if (!ok)
+    if (!ok && side == 0)
       for (int i = min(issued, STAGES); i > 0; --i) {  // copies in flight land before the CTA leaves
         if (--stage < 0) { stage = STAGES - 1; phase ^= 1; }
         mbar_drain(full_bar(stage), phase);
       }
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1 && lane == 0 && side == 0) {
     int stage = 0;
     uint32_t phase = 0;
     const uint32_t p_step = p_mn ? 2048 : 32, p_lbo = p_mn ? 8192 : 16;  // P's descriptor by its layout
@@ -220,12 +232,12 @@ lin_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ T
       for (int kk = 0; kk < BK / 16; ++kk) {
         const uint64_t pd = mat_desc(pb + kk * p_step, p_lbo, 1024);
         const uint64_t qd = Q_MN ? mat_desc(qb + kk * 2048, 8192, 1024) : mat_desc(qb + kk * 32, 16, 1024);
-        mma_16bit<false>(tmem, pd, qd, pr.idesc, kb != kb0 || kk != 0);
+        mma_16bit<PAIR>(tmem, pd, qd, pr.idesc, kb != kb0 || kk != 0);
       }
-      mma_commit<false>(empty_bar(stage));
+      mma_commit<PAIR>(empty_bar(stage), both);
       if (++stage == STAGES) { stage = 0; phase ^= 1; }
     }
-    mma_commit<false>(done_bar);  // after an abort too: no MMA outlives the CTA
+    mma_commit<PAIR>(done_bar, both);  // after an abort too: no MMA outlives the CTA
   }
 
   // the fp32 tile, tokens by features, over the ring (every copy and MMA has completed)
@@ -261,7 +273,7 @@ lin_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ T
   const int rows = ROWS / S;  // of this CTA; a multiple of 32 items in all
   constexpr int CH = COLS / 8;
   for (int i = threadIdx.x; i < rows * CH; i += kTileThreads) {
-    const int r = rank * rows + i / CH, c = (i % CH) * 8;
+    const int r = piece * rows + i / CH, c = (i % CH) * 8;
     float v[8];
     const uint32_t at = ring + (uint32_t)(r * PITCH + c) * 4u;
 #pragma unroll
@@ -269,7 +281,7 @@ lin_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ T
     for (int s = 0; s < S; ++s) {
       float4 a, b;
       if (S > 1) {
-        const uint32_t ra = map_to_rank(at, s);
+        const uint32_t ra = map_to_rank(at, s * SIDES + side);
         a = ld_cluster_f4(ra);
         b = ld_cluster_f4(ra + 16);
       } else {
@@ -282,12 +294,14 @@ lin_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ T
     const int m = (SWAP ? q0 : p0) + r, n = (SWAP ? p0 : q0) + c;
     epilogue8(pr.e, v, m, n, m < pr.e.M && n < pr.e.N);
   }
+  tc_fence_before();
   __syncthreads();
-  if (S > 1) cluster_sync_all();  // nobody leaves while its tile may still be read
+  if (clustered) cluster_sync_all();  // nobody leaves while its tile may be read, nor frees the pair's tensor memory
   if (warp == 1) {
     tc_fence_after();
-    tmem_free<false>(tmem, C::TMEM_COLS);
+    tmem_free<PAIR>(tmem, C::TMEM_COLS);
   }
+  if constexpr (PAIR) cluster_sync_all();
 }
 
 // ------------------------------------------------------------ a few tokens
@@ -537,6 +551,17 @@ bool make_map(CUtensorMap* tm, const void* base, int64_t inner, int64_t outer, i
             CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
          CUDA_SUCCESS;
 }
+// [pieces][M][N] fp32, boxes of 32 x 32 x 1 (128-byte rows): a box is clipped at M and N.
+bool make_part_map(CUtensorMap* tm, void* base, int64_t N, int64_t M, int64_t pieces) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)N, (cuuint64_t)M, (cuuint64_t)pieces};
+  cuuint64_t strides[2] = {(cuuint64_t)(N * 4), (cuuint64_t)(N * M * 4)};
+  cuuint32_t box[3] = {32u, 32u, 1u};
+  cuuint32_t estr[3] = {1u, 1u, 1u};
+  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 // An operand of `rows` rows/columns over K: `box_rows` of them per box when K-major, 64 when MN-major.
 bool operand_map(CUtensorMap* tm, const void* base, bool mn, int64_t rows, int64_t K, int64_t ld, int box_rows) {
   return mn ? make_map(tm, base, rows, K, ld, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B)
@@ -572,34 +597,33 @@ EpiParams epi_params(const LinGemm& g) {
   return e;
 }
 
-template <int BN, bool Q_MN, bool SWAP>
-lnfp8_status tile_launch(const LinGemm* g, int count, cudaStream_t st) {
-  using C = TileCfg<BN>;
-  constexpr auto k = lin_tile_kernel<BN, Q_MN, SWAP>;
+// S pieces of K per tile (1, 2 or 4; PAIR: 1 or 2).
+template <int BN, bool PAIR, bool Q_MN, bool SWAP>
+lnfp8_status tile_launch(const LinGemm* g, int count, int S, cudaStream_t st) {
+  using C = TileCfg<BN, PAIR>;
+  constexpr auto k = lin_tile_kernel<BN, PAIR, Q_MN, SWAP>;
   const lnfp8_status set = kernel_setup<k>(kTileThreads, C::SMEM, nullptr, "linear: kernel set-up");
   if (set != LNFP8_OK) return set;
   TileParams p = {};
   TileMaps maps;
   int64_t tiles = 0;
-  int min_kb = 0x7FFFFFFF;
   bool ok = true;
   for (int i = 0; i < count; ++i) {
     const LinGemm& q = g[i];
     TileProb& r = p.prob[i];
     const int64_t prow = SWAP ? q.N : q.M, qrow = SWAP ? q.M : q.N;
     const bool p_mn = SWAP ? q.b_mn : q.a_mn;
-    const int64_t num_p = (prow + 127) / 128, num_q = (qrow + BN - 1) / BN;
+    const int64_t num_p = (prow + (PAIR ? 255 : 127)) / (PAIR ? 256 : 128), num_q = (qrow + BN - 1) / BN;
     if (num_p * num_q > 0x0FFFFFFF) return set_error(LNFP8_ERR_UNSUPPORTED_SHAPE, "linear: too many tiles");
     r.e = epi_params(q);
     r.num_p = (int)num_p;
     r.num_kb = (int)((q.K + BK - 1) / BK);
     r.clusters = (int)(num_p * num_q);
     r.p_mn = p_mn;
-    r.idesc = make_idesc(q.elem, 128, BN, p_mn, Q_MN);
+    r.idesc = make_idesc(q.elem, PAIR ? 256 : 128, BN, p_mn, Q_MN);
     tiles += num_p * num_q;
-    min_kb = r.num_kb < min_kb ? r.num_kb : min_kb;
-    ok = ok && (SWAP ? operand_map(&maps.p[i], q.b, p_mn, q.N, q.K, q.ldb, 128) && operand_map(&maps.q[i], q.a, Q_MN, q.M, q.K, q.lda, BN)
-                     : operand_map(&maps.p[i], q.a, p_mn, q.M, q.K, q.lda, 128) && operand_map(&maps.q[i], q.b, Q_MN, q.N, q.K, q.ldb, BN));
+    ok = ok && (SWAP ? operand_map(&maps.p[i], q.b, p_mn, q.N, q.K, q.ldb, 128) && operand_map(&maps.q[i], q.a, Q_MN, q.M, q.K, q.lda, PAIR ? BN / 2 : BN)
+                     : operand_map(&maps.p[i], q.a, p_mn, q.M, q.K, q.lda, 128) && operand_map(&maps.q[i], q.b, Q_MN, q.N, q.K, q.ldb, PAIR ? BN / 2 : BN));
   }
   if (!ok) return set_error(LNFP8_ERR_CUDA, "linear: cuTensorMapEncodeTiled failed (driver entry point or arguments)");
   if (count == 1) {
@@ -607,20 +631,17 @@ lnfp8_status tile_launch(const LinGemm* g, int count, cudaStream_t st) {
     maps.p[1] = maps.p[0];
     maps.q[1] = maps.q[0];
   }
-  // K pieces: while they run on SMs that would idle and each keeps a few K blocks
-  int S = 1;
-  while (S < 8 && tiles * S * 2 <= num_sms() && min_kb >= S * 2 * 2) S *= 2;
   p.splits = S;
   for (TileProb& r : p.prob) r.kb_per_split = (r.num_kb + S - 1) / S;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = S;
+  attr[0].val.clusterDim.x = S * (PAIR ? 2 : 1);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)(tiles * S));
+  cfg.gridDim = dim3((unsigned)(tiles * S * (PAIR ? 2 : 1)));
   cfg.blockDim = dim3(kTileThreads);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = st;
@@ -659,9 +680,88 @@ int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 }  // namespace
 
 namespace {
-// Enough 256 x 256 tiles for half of the CTA pairs.
-bool takes_pairs(const LinGemm& g) { return ((g.M + 255) / 256) * ((g.N + 255) / 256) * 4 >= num_sms(); }
-bool takes_swap(const LinGemm& g) { return g.M <= 64 && !g.a_mn; }
+bool takes_swap(const LinGemm& g) { return g.M <= 128 && !g.a_mn; }
+
+// How a product, or two in one launch, runs when lanes are tokens: the persistent kernel over
+// 256 x 256 tiles, or one 256 x bn tile per cluster with K in S pieces. Costs in ns, fitted to measurements of
+// both (21 shapes of 65 to 8192 tokens): a 64-wide K block takes a pair 340 (256 columns) or 260 (128),
+// the rest is launch, set-up and epilogue; 76 clusters of one pair or 36 of two fit on the chip at once,
+// and of four too few (two rounds at 16 clusters). At 512 x 768 x 2304: persistent 10.4 us, 128 columns and
+// two pieces 9.6; at 512 x 2048 x 2048 15.8 and 12.0; at 2048 x 2048 x 2048 18.1 and 46.8.
+struct LinPlan {
+  int bn, S;  // bn 0: the persistent kernel
+};
+// K blocks of the pair with the most: the list of units, longest first, dealt out forwards and backwards.
+int64_t longest_pair(const int64_t* units, const int64_t* kb, int count, int64_t pairs) {
+  const int first = count == 2 && kb[1] > kb[0] ? 1 : 0;
+  const int64_t n0 = units[first], n = n0 + (count == 2 ? units[1 - first] : 0);
+  const int64_t k0 = kb[first], k1 = count == 2 ? kb[1 - first] : 0;
+  // rounds wholly of the first product cost every pair the same; look at what is left of them and the second
+  int64_t worst = 0;
+  for (int64_t c = 0; c < pairs; ++c) {
+    int64_t sum = 0;
+    const int64_t skip = n0 / (2 * pairs) * 2;
+    sum += skip * k0;
+    int64_t r = skip;
+    for (; r * pairs < n && r < skip + 4; ++r) {
+      const int64_t t = r * pairs + (r & 1 ? pairs - 1 - c : c);
+      if (t < n) sum += t < n0 ? k0 : k1;
+    }
+    if (r * pairs < n) sum += ((n - r * pairs) + pairs - 1) / pairs * k1;
+    worst = max64(worst, sum);
+  }
+  return worst;
+}
+
+LinPlan lin_plan(LinGemm* g, int count) {
+  const int64_t pairs = max64(num_sms() / 2, 1);
+  int64_t max_kb = 1, min_kb = 1 << 30, t128 = 0, units[2], kb[2];
+  for (int i = 0; i < count; ++i) {
+    kb[i] = (g[i].K + BK - 1) / BK;
+    const int64_t m2 = (g[i].M + 255) / 256;
+    units[i] = m2 * ((g[i].N + 255) / 256);
+    max_kb = max64(max_kb, kb[i]);
+    min_kb = min64(min_kb, kb[i]);
+    t128 += m2 * ((g[i].N + 127) / 128);
+  }
+  int64_t cost = longest_pair(units, kb, count, pairs) * 340 + 6200;
+  LinPlan best = {0, 1};
+  auto offer = [&](int bn, int S, int64_t tiles, int64_t per_kb, int64_t fixed) {
+    if (min_kb < 2 * S) return;
+    const int64_t fit = max64(S == 1 ? pairs : pairs * 36 / 76, 1), c = (tiles + fit - 1) / fit * ((max_kb + S - 1) / S * per_kb + fixed);
+    if (c < cost) {
+      cost = c;
+      best = {bn, S};
+    }
+  };
+  offer(128, 1, t128, 260, 6700);
+  offer(128, 2, t128, 260, 7700);
+  offer(256, 2, units[0] + (count == 2 ? units[1] : 0), 340, 9500);
+  // a weight gradient in pieces, if that and joining them (its bytes once out and once in) is less
+  bool pieces = false;
+  for (int i = 0; i < count; ++i) {
+    if (g[i].pieces <= 1) continue;
+    const int64_t u[2] = {units[0] * (i == 0 ? g[i].pieces : 1), count == 2 ? units[1] * (i == 1 ? g[i].pieces : 1) : 0};
+    const int64_t k[2] = {i == 0 ? (kb[0] + g[i].pieces - 1) / g[i].pieces : kb[0],
+                          count == 2 ? (i == 1 ? (kb[1] + g[i].pieces - 1) / g[i].pieces : kb[1]) : 0};
+    const int64_t c = longest_pair(u, k, count, pairs) * 340 + 6200 + 4000 + g[i].pieces * g[i].M * g[i].N * 8 / 4000;
+    if (c < cost) {
+      cost = c;
+      best = {0, 1};
+      pieces = true;
+    }
+  }
+  if (!pieces)
+    for (int i = 0; i < count; ++i) g[i].pieces = 1;
+  return best;
+}
+
+// The most K pieces of a weight gradient [N, K] over many tokens whose tiles leave pairs idle: as many as
+// fill them, of 16 K blocks or more each (the workspace holds their fp32 products).
+int wgrad_pieces(int64_t M, int64_t K, int64_t N) {
+  const int64_t pairs = max64(num_sms() / 2, 1), tiles = ((N + 255) / 256) * ((K + 255) / 256), kb = (M + BK - 1) / BK;
+  return (int)max64(1, min64(min64(8, pairs / max64(tiles, 1)), kb / 16));
+}
 
 // The forward of one to four tokens, without a checkpoint (whose blocks span more columns than a warp
 // has here; a decoding step keeps none).
@@ -688,10 +788,18 @@ lnfp8_status few_by_tokens(const LinGemm& g, cudaStream_t st) {
   return g.M == 1 ? few_launch<1, F16>(g, st) : g.M == 2 ? few_launch<2, F16>(g, st) : few_launch<4, F16>(g, st);
 }
 
+// Few tokens: K pieces while they run on SMs that would idle and each keeps a few K blocks.
+int swap_splits(const LinGemm& g, int lanes, int most) {
+  const int64_t tiles = (g.N + lanes - 1) / lanes, kb = (g.K + BK - 1) / BK;
+  int S = 1;
+  while (S < most && tiles * (lanes / 128) * S * 2 <= num_sms() && kb >= S * 2 * 2) S *= 2;
+  return S;
+}
 lnfp8_status swap_launch(const LinGemm& g, cudaStream_t st) {
-  if (g.M <= 16) return tile_launch<16, false, true>(&g, 1, st);
-  if (g.M <= 32) return tile_launch<32, false, true>(&g, 1, st);
-  return tile_launch<64, false, true>(&g, 1, st);
+  if (g.M <= 16) return tile_launch<16, false, false, true>(&g, 1, swap_splits(g, 128, 4), st);
+  if (g.M <= 32) return tile_launch<32, false, false, true>(&g, 1, swap_splits(g, 128, 4), st);
+  if (g.M <= 64) return tile_launch<64, false, false, true>(&g, 1, swap_splits(g, 128, 4), st);
+  return tile_launch<128, true, false, true>(&g, 1, swap_splits(g, 256, 2), st);
 }
 }  // namespace
 
@@ -700,21 +808,31 @@ lnfp8_status lin_gemm_launch(const LinGemm* g, int count, cudaStream_t st) {
     if (g->M == 0 || g->N == 0) return LNFP8_OK;
     if (takes_few(*g)) return g->elem == LNFP8_FP16 ? few_by_tokens<true>(*g, st) : few_by_tokens<false>(*g, st);
     if (takes_swap(*g)) return swap_launch(*g, st);
-    return takes_pairs(*g) ? pair_launch<256, LIN_FULL>(g, 1, st) : tile_launch<128, false, false>(g, 1, st);
+    LinGemm one = *g;
+    const LinPlan pl = lin_plan(&one, 1);
+    if (pl.bn == 0) return pair_launch<256, LIN_FULL>(g, 1, st);
+    return pl.bn == 256 ? tile_launch<256, true, false, false>(g, 1, pl.S, st) : tile_launch<128, true, false, false>(g, 1, pl.S, st);
   }
-  // the backward: two products run in one launch where both take the same kernel
-  if (count == 2 && !takes_swap(g[0]) && !takes_swap(g[1])) {
-    if (takes_pairs(g[0]) && takes_pairs(g[1])) return pair_launch<256, LIN_PLAIN>(g, 2, st);
-    if (!takes_pairs(g[0]) && !takes_pairs(g[1])) return tile_launch<128, true, false>(g, 2, st);
-  }
+  // the backward: what few tokens leave swapped runs alone, the rest in one launch
+  LinGemm rest[2];
+  int n = 0;
   for (int i = 0; i < count; ++i) {
-    lnfp8_status s;
-    if (takes_swap(g[i])) s = swap_launch(g[i], st);
-    else if (takes_pairs(g[i])) s = pair_launch<256, LIN_PLAIN>(g + i, 1, st);
-    else s = tile_launch<128, true, false>(g + i, 1, st);
+    if (!takes_swap(g[i])) {
+      rest[n++] = g[i];
+      continue;
+    }
+    const lnfp8_status s = swap_launch(g[i], st);
     if (s != LNFP8_OK) return s;
   }
-  return LNFP8_OK;
+  if (n == 0) return LNFP8_OK;
+  const LinPlan pl = lin_plan(rest, n);
+  if (pl.bn == 0) {
+    lnfp8_status s = pair_launch<256, LIN_PLAIN>(rest, n, st);
+    for (int i = 0; i < n && s == LNFP8_OK; ++i)
+      if (rest[i].pieces > 1) s = join_launch(rest[i], st);
+    return s;
+  }
+  return pl.bn == 256 ? tile_launch<256, true, true, false>(rest, n, pl.S, st) : tile_launch<128, true, true, false>(rest, n, pl.S, st);
 }
 
 lnfp8_status linear_act_fwd_launch(const lnfp8_linear_act_fwd_args* a, cudaStream_t st) {
@@ -738,13 +856,17 @@ lnfp8_status linear_act_fwd_launch(const lnfp8_linear_act_fwd_args* a, cudaStrea
   return lin_gemm_launch(&g, 1, st);
 }
 
-// dz [M, N], the restored x [M, K], two column sums for the affine input, and the columns' partial
-// sums, each from a multiple of 256 on.
+// dz [M, N], the restored x [M, K], two column sums for the affine input, the columns' partial sums and
+// the K pieces of dw, each from a multiple of 256 on.
+static int64_t wgrad_bytes(int64_t M, int64_t K, int64_t N) {
+  const int pieces = wgrad_pieces(M, K, N);
+  return pieces > 1 ? up256(pieces * N * K * 4) : 0;
+}
 int64_t linear_act_bwd_ws_bytes(int64_t M, int64_t K, int64_t N, bool has_act, bool x_from_ckpt) {
   if (M == 0 || N == 0) return 0;
   const int64_t rpb = dact_rows_per_block(M, N);
   return (has_act ? up256(M * N * 2) : 0) + (x_from_ckpt ? up256(M * K * 2) + 2 * up256(N * 4) : 0) +
-         up256((M + rpb - 1) / rpb * N * 4 * (has_act && x_from_ckpt ? 2 : 1));
+         up256((M + rpb - 1) / rpb * N * 4 * (has_act && x_from_ckpt ? 2 : 1)) + wgrad_bytes(M, K, N);
 }
 
 lnfp8_status linear_act_bwd_launch(const lnfp8_linear_act_bwd_args* a, cudaStream_t st) {
@@ -847,6 +969,10 @@ lnfp8_status linear_act_bwd_launch(const lnfp8_linear_act_bwd_args* a, cudaStrea
     q.b_mn = true;
     q.out = a->dw;
     q.ldo = a->K;
+    q.pieces = wgrad_pieces(a->M, a->K, a->N);
+    if (q.pieces > 1)  // the last part of the workspace
+      q.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + linear_act_bwd_ws_bytes(a->M, a->K, a->N, has_act, xck) -
+                                        wgrad_bytes(a->M, a->K, a->N));
     if (affine) {
       q.cscale = a->x_gamma;
       q.cvec = a->x_beta;

@@ -29,8 +29,8 @@ struct PairCfg {
   static constexpr int B_BYTES = BN / 2 * BK * 2;
   static constexpr int STAGE = A_BYTES + B_BYTES;
   // per epilogue warp: 32 x 32 16-bit boxes (2 KB) for the output and, with the full epilogue,
-  // for the saved pre-activation and the residual
-  static constexpr int BOXES = EPI == LIN_FULL ? 3 : 1;
+  // for the saved pre-activation and the residual; or a 32 x 32 fp32 box (4 KB) for a piece's sums
+  static constexpr int BOXES = EPI == LIN_FULL ? 3 : 2;  // a plain one may be fp32
   static constexpr int BOX_BYTES = kPairEpiWarps * BOXES * 2048;
   static constexpr int STAGES = (232448 - 1024 - 512 - BOX_BYTES) / STAGE;
   static constexpr int BOX_OFF = STAGES * STAGE;
@@ -42,7 +42,9 @@ struct PairCfg {
 
 struct PairProb {
   int M, N, num_m2, num_n, num_kb, group_m, tiles, a_mn;
+  int pieces, kb_per_piece;  // K pieces of a tile, neighbours in the list; `tiles` counts them
   uint32_t idesc;
+
   const void* cscale;  // with cvec and rvec, or NULL
   const void* cvec;
   const float* rvec;
@@ -60,7 +62,7 @@ struct PairParams {
 };
 
 struct PairMaps {
-  CUtensorMap a[2], b[2], o[2], r, h;
+  CUtensorMap a[2], b[2], o[2], r, h;  // o of a product in pieces: the fp32 parts, three-dimensional
 };
 
 // Tile t of a [num_m2 x num_n] grid: M fastest inside groups of G, then N, then the next
@@ -71,19 +73,29 @@ __device__ __forceinline__ int2 pair_tile(int t, int num_m2, int num_n, int G) {
   return make_int2(m0 + r % gs, r / gs);
 }
 
-// The product and tile of position t in the list.
+// The product, tile and K blocks of position t in the list.
 struct PairTile {
-  int prob, m2, n;
+  int prob, m2, n, piece, kb0, kb1;
 };
 __device__ __forceinline__ PairTile pair_locate(const PairParams& p, int t) {
   const int q = t >= p.prob[0].tiles ? 1 : 0;
   const PairProb& r = p.prob[q];
-  const int2 mn = pair_tile(q ? t - p.prob[0].tiles : t, r.num_m2, r.num_n, r.group_m);
-  return {q, mn.x, mn.y};
+  int u = q ? t - p.prob[0].tiles : t, piece = 0;
+  if (r.pieces > 1) {
+    piece = u % r.pieces;
+    u /= r.pieces;
+  }
+  const int2 mn = pair_tile(u, r.num_m2, r.num_n, r.group_m);
+  const int kb0 = piece * r.kb_per_piece;
+  return {q, mn.x, mn.y, piece, kb0, min(r.num_kb, kb0 + r.kb_per_piece)};
 }
 
 // Row r, 16-byte chunk j of a 32 x 32 16-bit box with the 64-byte swizzle.
 __device__ __forceinline__ uint32_t box_at(int r, int j) { return (uint32_t)(r * 64 + ((j ^ ((r >> 1) & 3)) << 4)); }
+
+// A pair's unit of round r: the rounds run forwards and backwards in turn, so that the pairs that got
+// the longer units of a round (they come first) get the later ones of the next.
+__device__ __forceinline__ int pair_unit(int r, int cid, int ncl) { return r * ncl + (r & 1 ? ncl - 1 - cid : cid); }
 
 // The activation of 32 values held as 16 pairs.
 template <int ACT>
@@ -149,13 +161,14 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
       uint32_t phase = 0;
       int64_t issued = 0;
       bool ok = true;
-      for (int t = cid; t < tiles && ok; t += ncl) {
+      for (int rd = 0; ok; ++rd) {
+        const int t = pair_unit(rd, cid, ncl);
+        if (t >= tiles) break;
         const PairTile at = pair_locate(p, t);
         const CUtensorMap *tmA = &maps.a[at.prob], *tmB = &maps.b[at.prob];
         const bool a_mn = EPI == LIN_PLAIN && p.prob[at.prob].a_mn;
-        const int num_kb = p.prob[at.prob].num_kb;
         const int m0 = at.m2 * 256 + rank * 128, n0 = at.n * BN + rank * (BN / 2);
-        for (int kb = 0; kb < num_kb; ++kb) {
+        for (int kb = at.kb0; kb < at.kb1; ++kb) {
           if (!mbar_wait(empty_bar(stage), phase ^ 1, abort_flag)) { ok = false; break; }
           const uint32_t fb = map_to_rank(full_bar(stage), 0);
           const uint32_t ad = ring + stage * C::STAGE, bd = ad + C::A_BYTES;
@@ -184,17 +197,19 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
-      for (int t = cid; t < tiles && ok; t += ncl) {
+      for (int rd = 0; ok; ++rd) {
+        const int t = pair_unit(rd, cid, ncl);
+        if (t >= tiles) break;
         if (!mbar_wait(tempty_bar(acc), acc_phase ^ 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
-        const PairProb& pr = p.prob[t >= p.prob[0].tiles ? 1 : 0];
+        const PairTile at = pair_locate(p, t);
+        const PairProb& pr = p.prob[at.prob];
         const uint32_t idesc = pr.idesc;
-        const int num_kb = pr.num_kb;
         // the A descriptor's step per 16 k and its leading offset, by A's layout
         const bool a_mn = EPI == LIN_PLAIN && pr.a_mn;
         const uint32_t a_step = a_mn ? 2048 : 32, a_lbo = a_mn ? 8192 : 16;
         const uint32_t d = tmem + (uint32_t)(acc * BN);
-        for (int kb = 0; kb < num_kb; ++kb) {
+        for (int kb = at.kb0; kb < at.kb1; ++kb) {
           if (!mbar_wait(full_bar(stage), phase, abort_flag)) { ok = false; break; }
           tc_fence_after();
           const uint32_t ab = ring + stage * C::STAGE, bb = ab + C::A_BYTES;
@@ -202,7 +217,7 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
           for (int kk = 0; kk < BK / 16; ++kk) {
             const uint64_t ad = mat_desc(ab + kk * a_step, a_lbo, 1024);
             const uint64_t bd = B_MN ? mat_desc(bb + kk * 2048, 8192, 1024) : mat_desc(bb + kk * 32, 16, 1024);
-            mma_16bit<true>(d, ad, bd, idesc, kb != 0 || kk != 0);
+            mma_16bit<true>(d, ad, bd, idesc, kb != at.kb0 || kk != 0);
           }
           mma_commit<true>(empty_bar(stage));
           if (++stage == STAGES) { stage = 0; phase ^= 1; }
@@ -234,7 +249,8 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
       }
       r_pending = true;
     };
-    const int t0 = cid + acc * ncl;
+    // this group's rounds have its parity: a step of two rounds keeps the direction
+    const int t0 = pair_unit(acc, cid, ncl);
     if constexpr (EPI == LIN_FULL)
       if (p.has_resid && t0 < tiles) load_resid(t0, 0);
     for (int t = t0; t < tiles; t += 2 * ncl) {
@@ -246,8 +262,8 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
       uint2 cb = make_uint2(0u, 0u), cv = make_uint2(0u, 0u);
       float rv = 0.f;
       const int lc = nh + lane * 4;
-      const bool affine = EPI == LIN_PLAIN && pr.cscale != nullptr;
-      const void* col_vec = EPI == LIN_FULL ? p.bias : pr.cscale;
+      const bool affine = EPI == LIN_PLAIN && pr.cscale != nullptr && pr.pieces == 1;
+      const void* col_vec = EPI == LIN_FULL ? p.bias : affine ? pr.cscale : nullptr;
       if (lane * 4 < HALF && lc < pr.N) {
         if (col_vec) cb = __ldg(reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(col_vec) + lc));
         if (affine) cv = __ldg(reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(pr.cvec) + lc));
@@ -270,6 +286,21 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
         uint64_t z[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) z[i] = pk(__uint_as_float(rr[2 * i]), __uint_as_float(rr[2 * i + 1]));
+        if (EPI == LIN_PLAIN && pr.pieces > 1) {  // the piece's sums, 128-byte rows with the 128-byte swizzle
+          if (lane == 0) bulk_wait_read();
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4*>(box_o + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_uint4(rr[4 * j], rr[4 * j + 1], rr[4 * j + 2], rr[4 * j + 3]);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            const int y = at.m2 * 256 + rank * 128 + quarter * 32;
+            if (y < pr.M && n0 < pr.N) tma_store_3d(&maps.o[at.prob], smem_u32(box_o), n0, y, at.piece);
+            bulk_commit();
+          }
+          continue;
+        }
         if (EPI == LIN_FULL || affine) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) {  // columns 2i, 2i + 1 of the chunk sit in lane 8 ch + i / 2
@@ -416,7 +447,8 @@ lnfp8_status pair_launch(const LinGemm* g, int count, cudaStream_t st) {
   bool ok = true;
   int64_t tiles = 0;
   // the product of more K blocks first: the short tiles fill the last round
-  const int first = count == 2 && g[1].K > g[0].K ? 1 : 0;
+  auto blocks = [](const LinGemm& q) { return q.K / (q.pieces > 1 ? q.pieces : 1); };
+  const int first = count == 2 && blocks(g[1]) > blocks(g[0]) ? 1 : 0;
   for (int i = 0; i < count; ++i) {
     const LinGemm& q = g[i ^ first];
     PairProb& r = p.prob[i];
@@ -427,15 +459,18 @@ lnfp8_status pair_launch(const LinGemm* g, int count, cudaStream_t st) {
     r.num_kb = (int)((q.K + BK - 1) / BK);
     // A panels (256 rows x K) of a raster group: what fits in 48 MB of L2
     r.group_m = (int)max64(1, min64((48ll << 20) / (512 * max64(q.K, 1)), r.num_m2));
-    r.tiles = r.num_m2 * r.num_n;
+    r.pieces = EPI == LIN_PLAIN && q.pieces > 1 ? q.pieces : 1;
+    r.kb_per_piece = (r.num_kb + r.pieces - 1) / r.pieces;
+    r.tiles = r.num_m2 * r.num_n * r.pieces;
     r.a_mn = q.a_mn;
     r.idesc = make_idesc(q.elem, 256, BN, q.a_mn, q.b_mn);
     r.cscale = q.cscale;
     r.cvec = q.cvec;
     r.rvec = q.rvec;
-    tiles += (int64_t)r.num_m2 * r.num_n;
+    tiles += (int64_t)r.num_m2 * r.num_n * r.pieces;
     ok = ok && operand_map(&maps.a[i], q.a, q.a_mn, q.M, q.K, q.lda, 128) && operand_map(&maps.b[i], q.b, q.b_mn, q.N, q.K, q.ldb, BN / 2) &&
-         make_map(&maps.o[i], q.out, q.N, q.M, q.ldo, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+         (r.pieces > 1 ? make_part_map(&maps.o[i], q.part, q.N, q.M, r.pieces)
+                       : make_map(&maps.o[i], q.out, q.N, q.M, q.ldo, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B));
   }
   if (tiles > 0x3FFFFFFF) return set_error(LNFP8_ERR_UNSUPPORTED_SHAPE, "linear: too many tiles");
   p.tiles = (int)tiles;
@@ -445,7 +480,7 @@ lnfp8_status pair_launch(const LinGemm* g, int count, cudaStream_t st) {
     maps.b[1] = maps.b[0];
     maps.o[1] = maps.o[0];
   }
-  maps.r = maps.h = maps.o[0];
+  maps.r = maps.h = maps.a[0];  // unused unless set below
   p.f16 = g->elem == LNFP8_FP16;
   p.ck = -1;
   if constexpr (EPI == LIN_FULL) {
@@ -483,4 +518,61 @@ lnfp8_status pair_launch(const LinGemm* g, int count, cudaStream_t st) {
     return set_error(LNFP8_ERR_CUDA, "linear launch: %s", cudaGetErrorString(e));
   }
   return check_launch("linear");
+}
+
+// out = T(sum of the pieces, in order), with the affine epilogue: 8 columns a thread.
+struct JoinParams {
+  const float* part;
+  int pieces, f16;
+  int64_t M, N, ldo;
+  void* out;
+  const void* cscale;
+  const void* cvec;
+  const float* rvec;
+};
+__global__ void __launch_bounds__(256) lin_join_kernel(const JoinParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t n8 = p.N >> 3, total = p.M * n8;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t m = i / n8;
+    const int n = (int)(i - m * n8) * 8;
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = 0.f;
+#pragma unroll 4
+    for (int q = 0; q < p.pieces; ++q) {
+      const float4* src = reinterpret_cast<const float4*>(p.part + ((int64_t)q * p.M + m) * p.N + n);
+      const float4 a = __ldcs(src), b = __ldcs(src + 1);
+      v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+      v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+    }
+    if (p.cscale) {
+      float cs[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, cv[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      add16x8(cs, *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.cscale) + n), p.f16);
+      add16x8(cv, *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.cvec) + n), p.f16);
+      const float rv = p.rvec[m];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = fmaf(v[k], cs[k], rv * cv[k]);
+    }
+    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + m * p.ldo + n) = pack16x8(v, p.f16);
+  }
+}
+
+lnfp8_status join_launch(const LinGemm& g, cudaStream_t st) {
+  JoinParams p;
+  p.part = g.part;
+  p.pieces = g.pieces;
+  p.f16 = g.elem == LNFP8_FP16;
+  p.M = g.M;
+  p.N = g.N;
+  p.ldo = g.ldo;
+  p.out = g.out;
+  p.cscale = g.cscale;
+  p.cvec = g.cvec;
+  p.rvec = g.rvec;
+  const int64_t blocks = min64((g.M * g.N / 8 + 255) / 256, (int64_t)num_sms() * 8);
+  LaunchScope ls("linear_join", st);
+  if (launch_pdl(lin_join_kernel, dim3((unsigned)blocks), dim3(256), 0, st, p) != cudaSuccess) return check_launch("linear_act_bwd launch");
+  return check_launch("linear_act_bwd: joining K pieces");
 }
