@@ -551,17 +551,6 @@ bool make_map(CUtensorMap* tm, const void* base, int64_t inner, int64_t outer, i
             CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
          CUDA_SUCCESS;
 }
-// [pieces][M][N] fp32, boxes of 32 x 32 x 1 (128-byte rows): a box is clipped at M and N.
-bool make_part_map(CUtensorMap* tm, void* base, int64_t N, int64_t M, int64_t pieces) {
-  auto fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[3] = {(cuuint64_t)N, (cuuint64_t)M, (cuuint64_t)pieces};
-  cuuint64_t strides[2] = {(cuuint64_t)(N * 4), (cuuint64_t)(N * M * 4)};
-  cuuint32_t box[3] = {32u, 32u, 1u};
-  cuuint32_t estr[3] = {1u, 1u, 1u};
-  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 // An operand of `rows` rows/columns over K: `box_rows` of them per box when K-major, 64 when MN-major.
 bool operand_map(CUtensorMap* tm, const void* base, bool mn, int64_t rows, int64_t K, int64_t ld, int box_rows) {
   return mn ? make_map(tm, base, rows, K, ld, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B)
@@ -860,7 +849,7 @@ lnfp8_status linear_act_fwd_launch(const lnfp8_linear_act_fwd_args* a, cudaStrea
 // the K pieces of dw, each from a multiple of 256 on.
 static int64_t wgrad_bytes(int64_t M, int64_t K, int64_t N) {
   const int pieces = wgrad_pieces(M, K, N);
-  return pieces > 1 ? up256(pieces * N * K * 4) : 0;
+  return pieces > 1 ? up256(pieces * N * K * 4) + 256 : 0;  // moved up to a 32-byte boundary
 }
 int64_t linear_act_bwd_ws_bytes(int64_t M, int64_t K, int64_t N, bool has_act, bool x_from_ckpt) {
   if (M == 0 || N == 0) return 0;
@@ -970,9 +959,11 @@ lnfp8_status linear_act_bwd_launch(const lnfp8_linear_act_bwd_args* a, cudaStrea
     q.out = a->dw;
     q.ldo = a->K;
     q.pieces = wgrad_pieces(a->M, a->K, a->N);
-    if (q.pieces > 1)  // the last part of the workspace
-      q.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + linear_act_bwd_ws_bytes(a->M, a->K, a->N, has_act, xck) -
-                                        wgrad_bytes(a->M, a->K, a->N));
+    if (q.pieces > 1) {  // the last part of the workspace
+      const uintptr_t at = reinterpret_cast<uintptr_t>(a->workspace) + linear_act_bwd_ws_bytes(a->M, a->K, a->N, has_act, xck) -
+                           wgrad_bytes(a->M, a->K, a->N);
+      q.part = reinterpret_cast<float*>((at + 31) / 32 * 32);
+    }
     if (affine) {
       q.cscale = a->x_gamma;
       q.cvec = a->x_beta;

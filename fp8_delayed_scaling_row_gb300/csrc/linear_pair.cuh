@@ -23,19 +23,18 @@ enum LinEpi {
 constexpr int kPairEpiWarps = 16;
 constexpr int kPairThreads = 128 + 32 * kPairEpiWarps;
 
-template <int BN, int EPI>
+template <int BN>
 struct PairCfg {
   static constexpr int A_BYTES = 128 * BK * 2;
   static constexpr int B_BYTES = BN / 2 * BK * 2;
   static constexpr int STAGE = A_BYTES + B_BYTES;
-  // per epilogue warp: 32 x 32 16-bit boxes (2 KB) for the output and, with the full epilogue,
-  // for the saved pre-activation and the residual; or a 32 x 32 fp32 box (4 KB) for a piece's sums
-  static constexpr int BOXES = EPI == LIN_FULL ? 3 : 2;  // a plain one may be fp32
-  static constexpr int BOX_BYTES = kPairEpiWarps * BOXES * 2048;
-  static constexpr int STAGES = (232448 - 1024 - 512 - BOX_BYTES) / STAGE;
-  static constexpr int BOX_OFF = STAGES * STAGE;
-  static constexpr int BAR_OFF = BOX_OFF + BOX_BYTES;
-  static constexpr int SMEM = 1024 + BAR_OFF + 512;
+  // The ring takes all of shared memory: the way from a stage's release to its next data (barrier, TMA,
+  // L2, the leader's barrier) is about 1500 cycles and a stage's MMAs 512, so four stages leave the tensor
+  // cores waiting: 16384 x 8192 x 2048 took 340 us with four and staged boxes, 312 with seven. The epilogue
+  // has no staging: a thread's 32 columns are whole 32-byte sectors of its row, and are stored and loaded so.
+  static constexpr int STAGES = (232448 - 1024 - 256) / STAGE;
+  static constexpr int BAR_OFF = STAGES * STAGE;
+  static constexpr int SMEM = 1024 + BAR_OFF + 256;
   static constexpr int TMEM_COLS = 512;
   static_assert(STAGES >= 4 && SMEM <= 232448, "shared memory budget");
 };
@@ -44,7 +43,10 @@ struct PairProb {
   int M, N, num_m2, num_n, num_kb, group_m, tiles, a_mn;
   int pieces, kb_per_piece;  // K pieces of a tile, neighbours in the list; `tiles` counts them
   uint32_t idesc;
-
+  int wide_out;        // rows of out on 32-byte boundaries
+  void* out;
+  int64_t ldo;
+  float* part;         // with pieces > 1: [pieces][M][N] fp32 instead, on a 32-byte boundary
   const void* cscale;  // with cvec and rvec, or NULL
   const void* cvec;
   const float* rvec;
@@ -54,15 +56,18 @@ struct PairParams {
   PairProb prob[2];
   int tiles;  // of both
   // the full epilogue
-  int f16, act, ck, has_resid, has_h, codes16;
+  int f16, act, ck, wide_resid, wide_h, wide_codes;
   const void* bias;
+  const void* resid;
+  int64_t ldr;
+  void* h;
   uint8_t* codes;
   uint8_t* scales;
   int64_t pitch;
 };
 
 struct PairMaps {
-  CUtensorMap a[2], b[2], o[2], r, h;  // o of a product in pieces: the fp32 parts, three-dimensional
+  CUtensorMap a[2], b[2];
 };
 
 // Tile t of a [num_m2 x num_n] grid: M fastest inside groups of G, then N, then the next
@@ -90,8 +95,50 @@ __device__ __forceinline__ PairTile pair_locate(const PairParams& p, int t) {
   return {q, mn.x, mn.y, piece, kb0, min(r.num_kb, kb0 + r.kb_per_piece)};
 }
 
-// Row r, 16-byte chunk j of a 32 x 32 16-bit box with the 64-byte swizzle.
-__device__ __forceinline__ uint32_t box_at(int r, int j) { return (uint32_t)(r * 64 + ((j ^ ((r >> 1) & 3)) << 4)); }
+// 32-byte accesses (sm_100 and later)
+__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
+               "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+__device__ __forceinline__ void load32(const void* p, uint32_t* w) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p)
+               : "memory");
+}
+// 32 columns n0.. of a row of 16-bit elements: those below N (a multiple of 8).
+__device__ __forceinline__ void store_row32(uint16_t* row, int n0, int N, int wide, const uint64_t* z, int f16) {
+  uint32_t w[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float2 v = upk(z[i]);
+    w[i] = pack16(v.x, v.y, f16);
+  }
+  if (wide && n0 + 32 <= N) {
+    store32(row + n0, w);
+    store32(row + n0 + 16, w + 8);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (n0 + 8 * j < N) *reinterpret_cast<uint4*>(row + n0 + 8 * j) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+  }
+}
+__device__ __forceinline__ void load_row32(const uint16_t* row, int n0, int N, int wide, uint32_t* w) {
+  if (wide && n0 + 32 <= N) {
+    load32(row + n0, w);
+    load32(row + n0 + 16, w + 8);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint4 u = n0 + 8 * j < N ? *reinterpret_cast<const uint4*>(row + n0 + 8 * j) : make_uint4(0u, 0u, 0u, 0u);
+      w[4 * j] = u.x;
+      w[4 * j + 1] = u.y;
+      w[4 * j + 2] = u.z;
+      w[4 * j + 3] = u.w;
+    }
+  }
+}
 
 // A pair's unit of round r: the rounds run forwards and backwards in turn, so that the pairs that got
 // the longer units of a round (they come first) get the later ones of the next.
@@ -107,22 +154,21 @@ __device__ __forceinline__ void act_pairs(uint64_t* z) {
 template <int BN, int EPI>
 __global__ void __launch_bounds__(kPairThreads, 1)
 lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ PairParams p) {
-  using C = PairCfg<BN, EPI>;
+  using C = PairCfg<BN>;
   constexpr bool B_MN = EPI == LIN_PLAIN;
   constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t ring = smem_u32(smem);
   const uint32_t bar0 = ring + C::BAR_OFF;
-  // full[STAGES], empty[STAGES], tfull[2], tempty[2], drain, rload[kPairEpiWarps]
+  // full[STAGES], empty[STAGES], tfull[2], tempty[2], drain
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
   auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + a); };
   auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + 2 + a); };
   const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 4);
-  auto rload_bar = [&](int w) { return bar0 + 8u * (2 * STAGES + 5 + w); };
-  static_assert(8 * (2 * STAGES + 5 + kPairEpiWarps) + 8 <= 512, "barrier space");
-  volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + C::BAR_OFF + 8 * (2 * STAGES + 5 + kPairEpiWarps));
+  static_assert(8 * (2 * STAGES + 5) + 8 <= 256, "barrier space");
+  volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + C::BAR_OFF + 8 * (2 * STAGES + 5));
   volatile uint32_t* abort_flag = misc;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -136,7 +182,6 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
       mbar_init(tempty_bar(a), kPairEpiWarps);  // the 8 warps of this buffer in both CTAs
     }
     mbar_init(drain_bar, 1);
-    for (int w = 0; w < kPairEpiWarps; ++w) mbar_init(rload_bar(w), 1);
     *abort_flag = 0;
     mbar_init_fence();
     tma_prefetch_map(&maps.a[0]);
@@ -234,25 +279,10 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
   } else if (warp >= 4) {
     const int ew = warp - 4, acc = ew >> 3, quarter = warp & 3, half = (ew >> 2) & 1;
     constexpr int HALF = BN / 2, CHUNKS = HALF / 32;
-    uint8_t* box_o = smem + C::BOX_OFF + ew * C::BOXES * 2048;
-    uint8_t* box_h = box_o + 2048;
-    uint8_t* box_r = box_o + 4096;
-    const uint32_t rbar = rload_bar(ew);
-    uint32_t rphase = 0, acc_phase = 0;
-    bool r_pending = false;
+    uint32_t acc_phase = 0;
     const uint32_t tempty = map_to_rank(tempty_bar(acc), 0);
-    auto load_resid = [&](int t, int ch) {  // the 32 x 32 residual block of (tile, chunk)
-      if (lane == 0) {
-        const PairTile at = pair_locate(p, t);
-        mbar_expect_tx(rbar, 2048);
-        tma_load(smem_u32(box_r), &maps.r, at.n * BN + half * HALF + ch * 32, at.m2 * 256 + rank * 128 + quarter * 32, rbar);
-      }
-      r_pending = true;
-    };
     // this group's rounds have its parity: a step of two rounds keeps the direction
     const int t0 = pair_unit(acc, cid, ncl);
-    if constexpr (EPI == LIN_FULL)
-      if (p.has_resid && t0 < tiles) load_resid(t0, 0);
     for (int t = t0; t < tiles; t += 2 * ncl) {
       const PairTile at = pair_locate(p, t);
       const PairProb& pr = p.prob[at.prob];
@@ -271,11 +301,12 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
       if (affine && m < pr.M) rv = __ldg(pr.rvec + m);
       if (!mbar_wait(tfull_bar(acc), acc_phase, abort_flag)) break;
       tc_fence_after();
-      bool aborted = false;
+      const bool row_ok = m < pr.M;
       uint32_t scale_word = 0;
 #pragma unroll 1
       for (int ch = 0; ch < CHUNKS; ++ch) {
         const int n0 = nh + ch * 32;
+        __syncwarp();  // rows past M took other branches
         uint32_t rr[32];
         tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * BN + half * HALF + ch * 32), rr);
         if (ch == CHUNKS - 1) {
@@ -286,22 +317,19 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
         uint64_t z[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) z[i] = pk(__uint_as_float(rr[2 * i]), __uint_as_float(rr[2 * i + 1]));
-        if (EPI == LIN_PLAIN && pr.pieces > 1) {  // the piece's sums, 128-byte rows with the 128-byte swizzle
-          if (lane == 0) bulk_wait_read();
-          __syncwarp();
+        if (EPI == LIN_PLAIN && pr.pieces > 1) {  // the piece's sums
+          if (row_ok) {
+            float* dst = pr.part + ((int64_t)at.piece * pr.M + m) * pr.N + n0;
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<uint4*>(box_o + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_uint4(rr[4 * j], rr[4 * j + 1], rr[4 * j + 2], rr[4 * j + 3]);
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            const int y = at.m2 * 256 + rank * 128 + quarter * 32;
-            if (y < pr.M && n0 < pr.N) tma_store_3d(&maps.o[at.prob], smem_u32(box_o), n0, y, at.piece);
-            bulk_commit();
+            for (int j = 0; j < 4; ++j)
+              if (n0 + 8 * j < pr.N) store32(dst + 8 * j, rr + 8 * j);
           }
           continue;
         }
-        if (EPI == LIN_FULL || affine) {
+        uint32_t res[16];
+        if constexpr (EPI == LIN_FULL)
+          if (p.resid && row_ok) load_row32(reinterpret_cast<const uint16_t*>(p.resid) + m * p.ldr, n0, pr.N, p.wide_resid, res);
+        if (col_vec) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) {  // columns 2i, 2i + 1 of the chunk sit in lane 8 ch + i / 2
             const float2 b = unpack16(__shfl_sync(0xFFFFFFFFu, i & 1 ? cb.y : cb.x, ch * 8 + (i >> 1)), p.f16);
@@ -312,44 +340,17 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
             }
           }
         }
-        uint4 res[4];
         if constexpr (EPI == LIN_FULL) {
-          if (p.has_resid) {
-            if (!mbar_wait(rbar, rphase, abort_flag)) { aborted = true; break; }
-            rphase ^= 1;
-            r_pending = false;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) res[j] = *reinterpret_cast<const uint4*>(box_r + box_at(lane, j));
-            fence_async_smem();
-            __syncwarp();
-            if (ch + 1 < CHUNKS) load_resid(t, ch + 1);
-            else if (t + 2 * ncl < tiles) load_resid(t + 2 * ncl, 0);
-          }
-        }
-        if (lane == 0) bulk_wait_read();  // the previous chunk's stores have read their boxes
-        __syncwarp();
-        if constexpr (EPI == LIN_FULL) {
-          if (p.has_h) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t w[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float2 v = upk(z[4 * j + i]);
-                w[i] = pack16(v.x, v.y, p.f16);
-              }
-              *reinterpret_cast<uint4*>(box_h + box_at(lane, j)) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          }
+          if (p.h && row_ok) store_row32(reinterpret_cast<uint16_t*>(p.h) + (int64_t)m * pr.N, n0, pr.N, p.wide_h, z, p.f16);
           if (p.ck >= 0) {
             // columns past N are zero (no operand, no bias) and do not move the block's maximum
-            uint32_t am = 0;
+            float am = 0.f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const float2 v = upk(z[i]);
-              am = max(am, max(abs_bits(v.x), abs_bits(v.y)));
+              am = amax3(am, v.x, v.y);
             }
-            const uint32_t b = ckpt_byte(am, p.ck);
+            const uint32_t b = ckpt_byte(abs_bits(am), p.ck);
             const float inv = ckpt_inv_scale(b);
             const uint64_t i2 = pk(inv, inv);
             scale_word |= b << (8 * ch);
@@ -359,11 +360,10 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
               const float2 u = upk(mul_2(z[2 * i], i2)), v = upk(mul_2(z[2 * i + 1], i2));
               q[i] = fp8x2(u.x, u.y, p.ck) | (fp8x2(v.x, v.y, p.ck) << 16);
             }
-            if (m < pr.M) {
+            if (row_ok) {
               uint8_t* dst = p.codes + (int64_t)m * pr.N + n0;
-              if (p.codes16 && n0 + 32 <= pr.N) {
-                reinterpret_cast<uint4*>(dst)[0] = make_uint4(q[0], q[1], q[2], q[3]);
-                reinterpret_cast<uint4*>(dst)[1] = make_uint4(q[4], q[5], q[6], q[7]);
+              if (p.wide_codes && n0 + 32 <= pr.N) {
+                store32(dst, q);
               } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -374,55 +374,24 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
           if (p.act == LNFP8_ACT_GELU) act_pairs<LNFP8_ACT_GELU>(z);
           else if (p.act == LNFP8_ACT_SILU) act_pairs<LNFP8_ACT_SILU>(z);
           else if (p.act == LNFP8_ACT_RELU) act_pairs<LNFP8_ACT_RELU>(z);
-          if (p.has_resid) {
+          if (p.resid && row_ok) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t w[4] = {res[j].x, res[j].y, res[j].z, res[j].w};
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float2 v = unpack16(w[i], p.f16);
-                z[4 * j + i] = add_2(z[4 * j + i], pk(v.x, v.y));
-              }
+            for (int i = 0; i < 16; ++i) {
+              const float2 v = unpack16(res[i], p.f16);
+              z[i] = add_2(z[i], pk(v.x, v.y));
             }
           }
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t w[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 v = upk(z[4 * j + i]);
-            w[i] = pack16(v.x, v.y, p.f16);
-          }
-          *reinterpret_cast<uint4*>(box_o + box_at(lane, j)) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          const int y = at.m2 * 256 + rank * 128 + quarter * 32;
-          if (y < pr.M && n0 < pr.N) {  // TMA clips the rest of a box at the tensor's edge
-            tma_store(&maps.o[at.prob], smem_u32(box_o), n0, y);
-            if constexpr (EPI == LIN_FULL)
-              if (p.has_h) tma_store(&maps.h, smem_u32(box_h), n0, y);
-          }
-          bulk_commit();
-        }
+        if (row_ok) store_row32(reinterpret_cast<uint16_t*>(pr.out) + m * pr.ldo, n0, pr.N, pr.wide_out, z, p.f16);
       }
-      if (aborted) break;
       if constexpr (EPI == LIN_FULL) {
-        if (p.ck >= 0 && m < pr.M && nh < pr.N) {  // the four (or, at the edge, fewer) blocks' bytes, one word of the row
+        if (p.ck >= 0 && row_ok && nh < pr.N) {  // the four (or, at the edge, fewer) blocks' bytes, one word of the row
           if constexpr (CHUNKS == 4) *reinterpret_cast<uint32_t*>(p.scales + (int64_t)m * p.pitch + (nh >> 5)) = scale_word;
           else *reinterpret_cast<uint16_t*>(p.scales + (int64_t)m * p.pitch + (nh >> 5)) = (uint16_t)scale_word;
         }
       }
       acc_phase ^= 1;
     }
-    if (r_pending) {  // a residual block still on its way
-      if (lane == 0) mbar_drain(rbar, rphase);
-      __syncwarp();
-    }
-    if (lane == 0) bulk_wait();
-    __syncwarp();
   }
 
   tc_fence_before();
@@ -438,12 +407,13 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
 // One product (EPI LIN_FULL), or one or two (LIN_PLAIN).
 template <int BN, int EPI>
 lnfp8_status pair_launch(const LinGemm* g, int count, cudaStream_t st) {
-  using C = PairCfg<BN, EPI>;
+  using C = PairCfg<BN>;
   constexpr auto k = lin_pair_kernel<BN, EPI>;
   const lnfp8_status set = kernel_setup<k>(kPairThreads, C::SMEM, nullptr, "linear: kernel set-up");
   if (set != LNFP8_OK) return set;
   PairParams p = {};
   PairMaps maps;
+  auto wide = [](const void* q, int64_t ld, int size) { return (int)(reinterpret_cast<uintptr_t>(q) % 32 == 0 && ld * size % 32 == 0); };
   bool ok = true;
   int64_t tiles = 0;
   // the product of more K blocks first: the short tiles fill the last round
@@ -468,9 +438,11 @@ lnfp8_status pair_launch(const LinGemm* g, int count, cudaStream_t st) {
     r.cvec = q.cvec;
     r.rvec = q.rvec;
     tiles += (int64_t)r.num_m2 * r.num_n * r.pieces;
-    ok = ok && operand_map(&maps.a[i], q.a, q.a_mn, q.M, q.K, q.lda, 128) && operand_map(&maps.b[i], q.b, q.b_mn, q.N, q.K, q.ldb, BN / 2) &&
-         (r.pieces > 1 ? make_part_map(&maps.o[i], q.part, q.N, q.M, r.pieces)
-                       : make_map(&maps.o[i], q.out, q.N, q.M, q.ldo, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B));
+    r.out = q.out;
+    r.ldo = q.ldo;
+    r.part = q.part;
+    r.wide_out = wide(q.out, q.ldo, 2);
+    ok = ok && operand_map(&maps.a[i], q.a, q.a_mn, q.M, q.K, q.lda, 128) && operand_map(&maps.b[i], q.b, q.b_mn, q.N, q.K, q.ldb, BN / 2);
   }
   if (tiles > 0x3FFFFFFF) return set_error(LNFP8_ERR_UNSUPPORTED_SHAPE, "linear: too many tiles");
   p.tiles = (int)tiles;
@@ -478,23 +450,22 @@ lnfp8_status pair_launch(const LinGemm* g, int count, cudaStream_t st) {
     p.prob[1] = p.prob[0];
     maps.a[1] = maps.a[0];
     maps.b[1] = maps.b[0];
-    maps.o[1] = maps.o[0];
   }
-  maps.r = maps.h = maps.a[0];  // unused unless set below
   p.f16 = g->elem == LNFP8_FP16;
   p.ck = -1;
   if constexpr (EPI == LIN_FULL) {
     p.act = g->act;
     p.ck = g->ckpt.codes ? g->ckpt.dtype : -1;
-    p.has_resid = g->resid != nullptr;
-    p.has_h = g->h != nullptr;
+    p.resid = g->resid;
+    p.ldr = g->ldr;
+    p.wide_resid = wide(g->resid, g->ldr, 2);
+    p.h = g->h;
+    p.wide_h = wide(g->h, g->N, 2);
     p.bias = g->bias;
     p.codes = g->ckpt.codes;
     p.scales = g->ckpt.scales;
-    p.codes16 = g->N % 16 == 0 && reinterpret_cast<uintptr_t>(g->ckpt.codes) % 16 == 0;
+    p.wide_codes = wide(g->ckpt.codes, g->N, 1);
     p.pitch = lnfp8_act_ckpt_scale_pitch(g->N);
-    if (ok && g->resid) ok = make_map(&maps.r, g->resid, g->N, g->M, g->ldr, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
-    if (ok && g->h) ok = make_map(&maps.h, g->h, g->N, g->M, g->N, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
   }
   if (!ok) return set_error(LNFP8_ERR_CUDA, "linear: cuTensorMapEncodeTiled failed (driver entry point or arguments)");
   cudaLaunchConfig_t cfg = {};
