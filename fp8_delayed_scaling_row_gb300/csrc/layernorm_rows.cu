@@ -122,24 +122,26 @@ struct LnBwdParams {
 };
 
 // ------------------------------------------------------------ any width, any alignment
-// A group of TPR threads owns a row; thread t holds columns t, t + TPR, ... (so that
-// a warp reads 32 neighbours and a checkpoint block is one warp's value i).
+// A group of TPR threads owns a row; thread t holds columns t, t + TPR, ... (so that a warp reads 32
+// neighbours and a checkpoint block is one warp's value i). Addresses are one pointer per tensor
+// and row, the columns compile-time offsets. HOLD: gamma and beta stay in registers.
 template <int ELEM, int TPR, int NE, bool CK>  // CK: with a checkpoint
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
 ln_fwd_any_kernel(const LnFwdParams p) {
-  constexpr int kThreads = TPR < 256 ? 256 : TPR;
+  constexpr int kThreads = TPR < 256 ? 256 : TPR, ES = ElemSize<ELEM>::value;
   constexpr int GPB = kThreads / TPR;
+  constexpr bool HOLD = NE <= 8;
   __shared__ float2 xch[2 * kThreads / 32];
   pdl_wait();
   pdl_launch_dependents();
   const int g = threadIdx.x / TPR, t = threadIdx.x % TPR;
   const float inv_d = 1.0f / (float)p.D;
-  constexpr bool HOLD = TPR < 1024;  // gamma and beta in registers (1024 threads have too few)
+  const int n = (p.D - t + TPR - 1) / TPR;  // this thread's columns (0 or fewer: none)
   float ga[HOLD ? NE : 1], be[HOLD ? NE : 1];
   if constexpr (HOLD) {
 #pragma unroll
     for (int i = 0; i < NE; ++i)
-      if (t + TPR * i < p.D) {
+      if (i < n) {
         ga[i] = load_elem_rt(p.gamma, p.param_elem, t + TPR * i);
         be[i] = load_elem_rt(p.beta, p.param_elem, t + TPR * i);
       }
@@ -150,43 +152,51 @@ ln_fwd_any_kernel(const LnFwdParams p) {
     const bool active = row < p.M;
     float v[NE];
     float s = 0.f;
+    const uint8_t* xr = static_cast<const uint8_t*>(p.x) + (row * p.ldx + t) * ES;
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      const int c = t + TPR * i;
-      v[i] = 0.f;
-      if (active && c < p.D) {
-        v[i] = load_elem<ELEM>(p.x, row * p.ldx + c);
-        if (p.resid) {
-          v[i] = round_elem<ELEM>(v[i] + load_elem<ELEM>(p.resid, row * p.ldr + c));
-          store_elem<ELEM>(p.xsum, row * p.D + c, v[i]);
-        }
-      }
-      s += v[i];
+    for (int i = 0; i < NE; ++i) v[i] = active && i < n ? load_elem<ELEM>(xr, TPR * i) : 0.f;
+    if (p.resid) {
+      const uint8_t* rr = static_cast<const uint8_t*>(p.resid) + (row * p.ldr + t) * ES;
+      uint8_t* hr = static_cast<uint8_t*>(p.xsum) + (row * p.D + t) * ES;
+#pragma unroll
+      for (int i = 0; i < NE; ++i)  // every load before the first store, which they could not pass
+        if (active && i < n) v[i] = round_elem<ELEM>(v[i] + load_elem<ELEM>(rr, TPR * i));
+#pragma unroll
+      for (int i = 0; i < NE; ++i)
+        if (active && i < n) store_elem<ELEM>(hr, TPR * i, v[i]);
     }
+#pragma unroll
+    for (int i = 0; i < NE; ++i) s += v[i];
     const float mu = row_sum<TPR>(s, xch, turn) * inv_d;
     float q = 0.f;
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      v[i] -= mu;
-      if (t + TPR * i < p.D) q = fmaf(v[i], v[i], q);
-    }
+    for (int i = 0; i < NE; ++i)
+      if (i < n) {
+        v[i] -= mu;
+        q = fmaf(v[i], v[i], q);
+      }
     const float rs = rsqrt_nr(row_sum<TPR>(q, xch, turn) * inv_d + p.eps);
     if (!active) continue;  // uniform over the row group; the barriers above are behind it
+    uint8_t* yr = static_cast<uint8_t*>(p.y) + (row * p.ldy + t) * ES;
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
-      const int c = t + TPR * i;
-      const bool in = c < p.D;
-      const float xh = v[i] * rs;
-      if (in) {
-        const float gi = HOLD ? ga[HOLD ? i : 0] : load_elem_rt(p.gamma, p.param_elem, c);
-        const float bi = HOLD ? be[HOLD ? i : 0] : load_elem_rt(p.beta, p.param_elem, c);
-        store_elem<ELEM>(p.y, row * p.ldy + c, fmaf(xh, gi, bi));
+      v[i] *= rs;  // columns past D hold zeros
+      if (i < n) {
+        const float gi = HOLD ? ga[HOLD ? i : 0] : load_elem_rt(p.gamma, p.param_elem, t + TPR * i);
+        const float bi = HOLD ? be[HOLD ? i : 0] : load_elem_rt(p.beta, p.param_elem, t + TPR * i);
+        store_elem<ELEM>(yr, TPR * i, fmaf(v[i], gi, bi));
       }
-      if constexpr (CK) {
-        const uint32_t b = ckpt_byte(warp_max_u32(in ? abs_bits(xh) : 0u), p.dt);
-        const uint32_t code = fp8x2(xh * ckpt_inv_scale(b), 0.f, p.dt);
-        if (in) p.codes[row * p.D + c] = (uint8_t)code;
-        if ((threadIdx.x & 31) == 0 && in) p.scales[row * p.pitch + (c >> 5)] = (uint8_t)b;
+    }
+    if constexpr (CK) {
+      uint8_t *cr = p.codes + row * p.D + t, *sr = p.scales + row * p.pitch + (t >> 5);
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        const uint32_t b = ckpt_byte(__reduce_max_sync(0xFFFFFFFFu, abs_bits(v[i])), p.dt);
+        const uint32_t code = fp8x2(v[i] * ckpt_inv_scale(b), 0.f, p.dt);
+        if (i < n) {
+          cr[TPR * i] = (uint8_t)code;
+          if ((t & 31) == 0) sr[TPR / 32 * i] = (uint8_t)b;
+        }
       }
     }
     if (t == 0) {
@@ -199,7 +209,7 @@ ln_fwd_any_kernel(const LnFwdParams p) {
 template <int ELEM, int TPR, int NE, bool CK>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
 ln_bwd_any_kernel(const LnBwdParams p) {
-  constexpr int kThreads = TPR < 256 ? 256 : TPR;
+  constexpr int kThreads = TPR < 256 ? 256 : TPR, ES = ElemSize<ELEM>::value;
   constexpr int GPB = kThreads / TPR;
   __shared__ float2 xch[2 * kThreads / 32];
   extern __shared__ float colred[];  // [2][D], only with several row groups
@@ -207,13 +217,14 @@ ln_bwd_any_kernel(const LnBwdParams p) {
   pdl_launch_dependents();
   const int g = threadIdx.x / TPR, t = threadIdx.x % TPR;
   const float inv_d = 1.0f / (float)p.D;
-  constexpr bool HOLD = TPR < 512;  // gamma in registers
+  const int n = (p.D - t + TPR - 1) / TPR;
+  constexpr bool HOLD = NE <= 8;  // gamma in registers
   float accg[NE], accb[NE], ga[HOLD ? NE : 1];
 #pragma unroll
   for (int i = 0; i < NE; ++i) {
     accg[i] = accb[i] = 0.f;
     if constexpr (HOLD)
-      if (t + TPR * i < p.D) ga[i] = load_elem_rt(p.gamma, p.param_elem, t + TPR * i);
+      if (i < n) ga[i] = load_elem_rt(p.gamma, p.param_elem, t + TPR * i);
   }
   int turn = 0;
   for (int64_t row0 = (int64_t)blockIdx.x * GPB; row0 < p.M; row0 += (int64_t)gridDim.x * GPB) {
@@ -223,19 +234,34 @@ ln_bwd_any_kernel(const LnBwdParams p) {
     const float mu = active && !CK ? p.mu[row] : 0.f;
     float xh[NE], gg[NE];
     float s1 = 0.f, s2 = 0.f;
+    const uint8_t* dr = static_cast<const uint8_t*>(p.dy) + (row * p.lddy + t) * ES;
+    const uint8_t* xr = CK ? p.codes + row * p.D + t : static_cast<const uint8_t*>(p.x) + (row * p.ldx + t) * ES;
+    const uint8_t* sr = p.scales + row * p.pitch + (t >> 5);
+    const uint8_t* rr = static_cast<const uint8_t*>(p.dres) + (row * p.lddres + t) * ES;
+    float res[NE];
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {  // every load of the row first
+      xh[i] = gg[i] = res[i] = 0.f;
+      if (active && i < n) {
+        if (p.dres) res[i] = load_elem<ELEM>(rr, TPR * i);
+        gg[i] = load_elem<ELEM>(dr, TPR * i);
+        if constexpr (CK) xh[i] = __uint_as_float((uint32_t)xr[TPR * i] | ((uint32_t)sr[TPR / 32 * i] << 8));
+        else xh[i] = load_elem<ELEM>(xr, TPR * i);
+      }
+    }
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
-      const int c = t + TPR * i;
-      xh[i] = gg[i] = 0.f;
-      if (active && c < p.D) {
-        const float d = load_elem<ELEM>(p.dy, row * p.lddy + c);
-        if constexpr (CK)
-          xh[i] = fp8x2_to_f32(p.codes[row * p.D + c], p.dt).x * ckpt_scale(p.scales[row * p.pitch + (c >> 5)]);
-        else
-          xh[i] = (load_elem<ELEM>(p.x, row * p.ldx + c) - mu) * rs;
+      if (active && i < n) {
+        if constexpr (CK) {
+          const uint32_t w = __float_as_uint(xh[i]);
+          xh[i] = fp8x2_to_f32(w & 0xFFu, p.dt).x * ckpt_scale(w >> 8);
+        } else {
+          xh[i] = (xh[i] - mu) * rs;
+        }
+        const float d = gg[i];
         accg[i] = fmaf(d, xh[i], accg[i]);
         accb[i] += d;
-        gg[i] = d * (HOLD ? ga[HOLD ? i : 0] : load_elem_rt(p.gamma, p.param_elem, c));
+        gg[i] = d * (HOLD ? ga[HOLD ? i : 0] : load_elem_rt(p.gamma, p.param_elem, t + TPR * i));
       }
       s1 += gg[i];
       s2 = fmaf(gg[i], xh[i], s2);
@@ -243,13 +269,11 @@ ln_bwd_any_kernel(const LnBwdParams p) {
     const float2 sums = row_sum2<TPR>(s1, s2, xch, turn);
     if (!active) continue;  // uniform over the row group
     const float mg = sums.x * inv_d, mgx = sums.y * inv_d;
+    uint8_t* orow = static_cast<uint8_t*>(p.dx) + (row * p.lddx + t) * ES;
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
-      const int c = t + TPR * i;
-      if (c >= p.D) continue;
-      float o = (fmaf(-mgx, xh[i], gg[i] - mg)) * rs;
-      if (p.dres) o += load_elem<ELEM>(p.dres, row * p.lddres + c);
-      store_elem<ELEM>(p.dx, row * p.lddx + c, o);
+      if (i >= n) continue;
+      store_elem<ELEM>(orow, TPR * i, fmaf(-mgx, xh[i], gg[i] - mg) * rs + res[i]);
     }
   }
   // this block's column partials: the row groups add theirs in turn
@@ -285,17 +309,18 @@ ln_bwd_any_kernel(const LnBwdParams p) {
 // bound by HBM: each thread copies (cp.async) the chunks of its next RING - 1 rows into its own
 // slots of a shared-memory ring, so the bytes in flight cost no registers, and a slot is
 // refilled one row after it was read. Four neighbouring lanes hold a checkpoint block.
+// Beyond 8192 columns (NV 4) the forward reads gamma and beta again for each row.
 template <int ELEM, int TPR, int NV, bool RES>
 struct FwdShape {
   static constexpr int THREADS = TPR < 256 ? 256 : TPR;
   static constexpr int W = ELEM == LNFP8_FP32 ? 2 : 1;           // 16-byte words per chunk
   static constexpr int WORDS = NV * W * (RES ? 2 : 1);           // per thread and row
-  static constexpr int RING = WORDS <= 4 ? 4 : 3;
+  static constexpr int RING = WORDS <= 4 ? 4 : 3 * WORDS * THREADS * 16 <= 224 * 1024 ? 3 : 2;
   static constexpr size_t SMEM = (size_t)RING * WORDS * THREADS * 16;
 };
 
 template <int ELEM, int TPR, int NV, bool CK, bool RES>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR < 512 ? 3 : 1)
 ln_fwd_vec_kernel(const LnFwdParams p) {
   using S = FwdShape<ELEM, TPR, NV, RES>;
   constexpr int T = S::THREADS, GPB = T / TPR, W = S::W, RING = S::RING, P = RING - 1;
@@ -330,13 +355,16 @@ ln_fwd_vec_kernel(const LnFwdParams p) {
   };
 #pragma unroll
   for (int k = 0; k < P; ++k) issue(row + k * p.step, mine + k * SB);
-  uint64_t ga[NV][4], be[NV][4];  // pairs of columns
+  constexpr bool HOLD = NV <= 2;
+  uint64_t ga[HOLD ? NV : 1][4], be[HOLD ? NV : 1][4];  // pairs of columns
+  if constexpr (HOLD) {
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int c = (t + TPR * j) * 8;
-    if (c < p.D) {
-      load8_rt(p.gamma, p.param_elem, c, ga[j]);
-      load8_rt(p.beta, p.param_elem, c, be[j]);
+    for (int j = 0; j < NV; ++j) {
+      const int c = (t + TPR * j) * 8;
+      if (c < p.D) {
+        load8_rt(p.gamma, p.param_elem, c, ga[j]);
+        load8_rt(p.beta, p.param_elem, c, be[j]);
+      }
     }
   }
   const float inv_d = 1.0f / (float)p.D;
@@ -407,8 +435,12 @@ ln_fwd_vec_kernel(const LnFwdParams p) {
       for (int k = 0; k < 4; ++k) v[j][k] = mul_2(v[j][k], rs2);
       if (in) {
         uint64_t y[4];
+        if constexpr (!HOLD) {
+          load8_rt(p.gamma, p.param_elem, c, ga[0]);
+          load8_rt(p.beta, p.param_elem, c, be[0]);
+        }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) y[k] = fma_2(v[j][k], ga[j][k], be[j][k]);
+        for (int k = 0; k < 4; ++k) y[k] = fma_2(v[j][k], ga[HOLD ? j : 0][k], be[HOLD ? j : 0][k]);
         store8<ELEM>(yp, TPR * j * 8, y);
       }
       if constexpr (CK) {
@@ -645,9 +677,12 @@ lnfp8_status fwd_any(const LnFwdParams& p, cudaStream_t st) {
     if (launch_pdl(kernel, dim3((unsigned)blocks), dim3(threads), 0, st, p) != cudaSuccess) return check_launch("layernorm_fwd launch");
     return check_launch("layernorm_fwd");
   };
-  if (p.D <= 512) return go(ln_fwd_any_kernel<ELEM, 32, 16, CK>, 32);
-  if (p.D <= 2048) return go(ln_fwd_any_kernel<ELEM, 128, 16, CK>, 128);
-  if (p.D <= 8192) return go(ln_fwd_any_kernel<ELEM, 512, 16, CK>, 512);
+  if (p.D <= 256) return go(ln_fwd_any_kernel<ELEM, 32, 8, CK>, 32);
+  if (p.D <= 512) return go(ln_fwd_any_kernel<ELEM, 64, 8, CK>, 64);
+  if (p.D <= 1024) return go(ln_fwd_any_kernel<ELEM, 128, 8, CK>, 128);
+  if (p.D <= 2048) return go(ln_fwd_any_kernel<ELEM, 256, 8, CK>, 256);
+  if (p.D <= 4096) return go(ln_fwd_any_kernel<ELEM, 512, 8, CK>, 512);
+  if (p.D <= 8192) return go(ln_fwd_any_kernel<ELEM, 1024, 8, CK>, 1024);
   return go(ln_fwd_any_kernel<ELEM, 1024, 16, CK>, 1024);
 }
 
@@ -661,9 +696,12 @@ lnfp8_status bwd_any(const LnBwdParams& p, int* blocks_out, cudaStream_t st) {
     if (launch_pdl(kernel, dim3((unsigned)blocks), dim3(threads), smem, st, p) != cudaSuccess) return check_launch("layernorm_bwd launch");
     return check_launch("layernorm_bwd");
   };
-  if (p.D <= 512) return go(ln_bwd_any_kernel<ELEM, 32, 16, CK>, 32);
-  if (p.D <= 2048) return go(ln_bwd_any_kernel<ELEM, 128, 16, CK>, 128);
-  if (p.D <= 8192) return go(ln_bwd_any_kernel<ELEM, 512, 16, CK>, 512);
+  if (p.D <= 256) return go(ln_bwd_any_kernel<ELEM, 32, 8, CK>, 32);
+  if (p.D <= 512) return go(ln_bwd_any_kernel<ELEM, 64, 8, CK>, 64);
+  if (p.D <= 1024) return go(ln_bwd_any_kernel<ELEM, 128, 8, CK>, 128);
+  if (p.D <= 2048) return go(ln_bwd_any_kernel<ELEM, 256, 8, CK>, 256);
+  if (p.D <= 4096) return go(ln_bwd_any_kernel<ELEM, 512, 8, CK>, 512);
+  if (p.D <= 8192) return go(ln_bwd_any_kernel<ELEM, 1024, 8, CK>, 1024);
   return go(ln_bwd_any_kernel<ELEM, 1024, 16, CK>, 1024);
 }
 
@@ -697,7 +735,8 @@ lnfp8_status fwd_vec(const LnFwdParams& p, cudaStream_t st) {
   if (p.D <= 1024) return fwd_vec_launch<ELEM, 64, 2, CK, RES>(p, st);
   if (p.D <= 2048) return fwd_vec_launch<ELEM, 128, 2, CK, RES>(p, st);
   if (p.D <= 4096) return fwd_vec_launch<ELEM, 256, 2, CK, RES>(p, st);
-  return fwd_vec_launch<ELEM, 512, 2, CK, RES>(p, st);
+  if constexpr (ELEM == LNFP8_FP32 && RES) return fwd_vec_launch<ELEM, 512, 2, CK, RES>(p, st);
+  else return p.D <= 8192 ? fwd_vec_launch<ELEM, 512, 2, CK, RES>(p, st) : fwd_vec_launch<ELEM, 512, 4, CK, RES>(p, st);
 }
 
 template <int ELEM, int TPR, int NV, bool CK, bool RES>
@@ -733,13 +772,13 @@ lnfp8_status bwd_vec(const LnBwdParams& p, int* blocks_out, cudaStream_t st) {
   return bwd_vec_launch<ELEM, 512, 2, CK, RES>(p, blocks_out, st);
 }
 
-// Rows of 16-byte words up to 8192 columns take the vector kernels (beyond, and for any other
-// width or alignment, the kernels above).
+// Rows of 16-byte words take the vector kernels up to 16384 columns forward (8192 in fp32 with a residual, whose
+// ring would not fit) and 8192 backward; all others the kernels above.
 bool row_aligned(const void* p, int64_t ld, int es) { return al(p, 16) && ld * es % 16 == 0; }
 template <int ELEM, bool CK>
 lnfp8_status fwd(const LnFwdParams& p, cudaStream_t st) {
   constexpr int es = ElemSize<ELEM>::value;
-  const bool vec = p.D % 8 == 0 && p.D <= 8192 && row_aligned(p.x, p.ldx, es) && row_aligned(p.y, p.ldy, es) && al(p.gamma, 16) && al(p.beta, 16) &&
+  const bool vec = p.D % 8 == 0 && (p.D <= 8192 || !(ELEM == LNFP8_FP32 && p.resid)) && row_aligned(p.x, p.ldx, es) && row_aligned(p.y, p.ldy, es) && al(p.gamma, 16) && al(p.beta, 16) &&
                    (!p.resid || (row_aligned(p.resid, p.ldr, es) && al(p.xsum, 16))) && (!CK || al(p.codes, 8));
   if (!vec) return fwd_any<ELEM, CK>(p, st);
   return p.resid ? fwd_vec<ELEM, CK, true>(p, st) : fwd_vec<ELEM, CK, false>(p, st);

@@ -356,7 +356,7 @@ __device__ __forceinline__ void logistic8(const uint64_t* nu, uint64_t* s) {
     for (int k = 0; k < 4; ++k) {
       const float2 t = upk(d[k]);
       const float r = rcp_fast(q[k]);
-      s[k] = mul_2(pk(t.y, t.x), pk(r, r));
+      s[k] = pk(r * t.y, r * t.x);  // scalar products: a swapped pair would cost moves
     }
   } else {
 #pragma unroll
