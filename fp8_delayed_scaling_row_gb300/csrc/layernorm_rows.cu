@@ -304,17 +304,26 @@ ln_bwd_any_kernel(const LnBwdParams p) {
 }
 
 // ------------------------------------------------------------ 16-byte rows
-// D a multiple of 8 and rows on 16-byte boundaries. A group of TPR threads owns a row, thread t
-// the chunks of 8 columns t, t + TPR, ...; gamma and beta stay in registers. Both kernels are
-// bound by HBM: each thread copies (cp.async) the chunks of its next RING - 1 rows into its own
+// D a multiple of 8 and rows on 16-byte boundaries. A group of TPR threads owns a row. Both kernels are
+// bound by HBM: each thread copies (cp.async) the words of its next RING - 1 rows into its own
 // slots of a shared-memory ring, so the bytes in flight cost no registers, and a slot is
-// refilled one row after it was read. Four neighbouring lanes hold a checkpoint block.
-// Beyond 8192 columns (NV 4) the forward reads gamma and beta again for each row.
+// refilled one row after it was read. Neighbouring lanes hold a checkpoint block. 16 columns a thread
+// measured best (8 or 32, or 96 threads for 768 columns, up to 2x slower backward: fewer columns share a
+// row's reductions, more cost occupancy). bf16, 16384 x 2048, with residual and checkpoint: forward 51 us,
+// 5.9 TB/s, 88% of a copy; backward 44 us with its column sums, 79%.
+// A thread's NV 16-byte words of a row are words t, t + TPR, ... (EPC columns each: 8 of a 16-bit type, 4 of
+// fp32), so that every access of a warp is of whole sectors. HOLD: gamma and beta stay in registers; beyond
+// 16 columns a thread they are read again for each row.
+template <int ELEM>
+struct Word {
+  static constexpr int EPC = ELEM == LNFP8_FP32 ? 4 : 8;
+  static constexpr int LANES = 32 / EPC;  // that hold a checkpoint block
+};
+
 template <int ELEM, int TPR, int NV, bool RES>
 struct FwdShape {
   static constexpr int THREADS = TPR < 256 ? 256 : TPR;
-  static constexpr int W = ELEM == LNFP8_FP32 ? 2 : 1;           // 16-byte words per chunk
-  static constexpr int WORDS = NV * W * (RES ? 2 : 1);           // per thread and row
+  static constexpr int WORDS = NV * (RES ? 2 : 1);  // per thread and row
   static constexpr int RING = WORDS <= 4 ? 4 : 3 * WORDS * THREADS * 16 <= 224 * 1024 ? 3 : 2;
   static constexpr size_t SMEM = (size_t)RING * WORDS * THREADS * 16;
 };
@@ -323,29 +332,27 @@ template <int ELEM, int TPR, int NV, bool CK, bool RES>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR < 512 ? 3 : 1)
 ln_fwd_vec_kernel(const LnFwdParams p) {
   using S = FwdShape<ELEM, TPR, NV, RES>;
-  constexpr int T = S::THREADS, GPB = T / TPR, W = S::W, RING = S::RING, P = RING - 1;
+  constexpr int T = S::THREADS, GPB = T / TPR, RING = S::RING, P = RING - 1;
+  constexpr int EPC = Word<ELEM>::EPC, PP = EPC / 2, ES = ElemSize<ELEM>::value;
+  constexpr bool HOLD = NV * EPC <= 16;
   __shared__ float2 xch[2 * T / 32];
   extern __shared__ uint4 ring[];  // [RING][WORDS][T]
   const int g = threadIdx.x / TPR, t = threadIdx.x % TPR;
   pdl_wait();
   pdl_launch_dependents();
-  constexpr int ES = ElemSize<ELEM>::value;
   constexpr uint32_t WB = T * 16, SB = S::WORDS * WB;  // bytes of a word of all threads, of a slot
   const uint32_t mine = (uint32_t)__cvta_generic_to_shared(ring) + threadIdx.x * 16;
   int64_t row = (int64_t)blockIdx.x * GPB + g;
-  // this thread's first chunk in the row to be loaded next: the pointers run ahead of `row`
-  const uint8_t* xp = static_cast<const uint8_t*>(p.x) + (row * p.ldx + t * 8) * ES;
-  const uint8_t* rp = RES ? static_cast<const uint8_t*>(p.resid) + (row * p.ldr + t * 8) * ES : nullptr;
+  // this thread's first word in the row to be loaded next: the pointers run ahead of `row`
+  const uint8_t* xp = static_cast<const uint8_t*>(p.x) + row * p.ldx * ES + t * 16;
+  const uint8_t* rp = RES ? static_cast<const uint8_t*>(p.resid) + row * p.ldr * ES + t * 16 : nullptr;
   auto issue = [&](int64_t r, uint32_t slot) {
     if (r < p.M) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        if ((t + TPR * j) * 8 < p.D) {
-#pragma unroll
-          for (int k = 0; k < W; ++k) {
-            cp16(slot + (j * W + k) * WB, xp + TPR * j * 8 * ES + 16 * k);
-            if constexpr (RES) cp16(slot + ((NV + j) * W + k) * WB, rp + TPR * j * 8 * ES + 16 * k);
-          }
+        if ((t + TPR * j) * EPC < p.D) {
+          cp16(slot + j * WB, xp + TPR * j * 16);
+          if constexpr (RES) cp16(slot + (NV + j) * WB, rp + TPR * j * 16);
         }
       }
       xp += p.xstep;
@@ -355,58 +362,49 @@ ln_fwd_vec_kernel(const LnFwdParams p) {
   };
 #pragma unroll
   for (int k = 0; k < P; ++k) issue(row + k * p.step, mine + k * SB);
-  constexpr bool HOLD = NV <= 2;
-  uint64_t ga[HOLD ? NV : 1][4], be[HOLD ? NV : 1][4];  // pairs of columns
+  uint64_t ga[HOLD ? NV : 1][PP], be[HOLD ? NV : 1][PP];  // pairs of columns
   if constexpr (HOLD) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (t + TPR * j) * 8;
+      const int c = (t + TPR * j) * EPC;
       if (c < p.D) {
-        load8_rt(p.gamma, p.param_elem, c, ga[j]);
-        load8_rt(p.beta, p.param_elem, c, be[j]);
+        load_params<EPC>(p.gamma, p.param_elem, c, ga[j]);
+        load_params<EPC>(p.beta, p.param_elem, c, be[j]);
       }
     }
   }
   const float inv_d = 1.0f / (float)p.D;
   int turn = 0;
   uint32_t slot = mine, last = mine + P * SB;  // the row's slot; the one read before it, filled next
-  // the chunk's place in the outputs, advanced row by row
-  uint8_t* yp = static_cast<uint8_t*>(p.y) + (row * p.ldy + t * 8) * ES;
-  uint8_t* hp = RES ? static_cast<uint8_t*>(p.xsum) + (row * p.D + t * 8) * ES : nullptr;
-  uint8_t* cp = CK ? p.codes + row * p.D + t * 8 : nullptr;
-  uint8_t* sp8 = CK ? p.scales + row * p.pitch + (t >> 2) : nullptr;
+  // the word's place in the outputs, advanced row by row
+  uint8_t* yp = static_cast<uint8_t*>(p.y) + row * p.ldy * ES + t * 16;
+  uint8_t* hp = RES ? static_cast<uint8_t*>(p.xsum) + row * p.D * ES + t * 16 : nullptr;
+  uint8_t* cp = CK ? p.codes + row * p.D + t * EPC : nullptr;
+  uint8_t* sp8 = CK ? p.scales + row * p.pitch + t / Word<ELEM>::LANES : nullptr;
   for (; row - g < p.M; row += p.step) {  // the same trip count for every group of the block
     issue(row + P * p.step, last);
     cp_wait<P>();
     const bool active = row < p.M;
-    uint64_t v[NV][4];
+    uint64_t v[NV][PP];
     uint64_t s2 = 0;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (t + TPR * j) * 8;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[j][k] = 0;
-      if (active && c < p.D) {
-        uint4 u[W];
-#pragma unroll
-        for (int k = 0; k < W; ++k) u[k] = lds16(slot + (j * W + k) * WB);
-        unpack8<ELEM>(u, v[j]);
+      for (int k = 0; k < PP; ++k) v[j][k] = 0;
+      if (active && (t + TPR * j) * EPC < p.D) {
+        unpack_word<ELEM>(lds16(slot + j * WB), v[j]);
         if constexpr (RES) {
-          uint64_t r[4];
+          uint64_t r[PP];
+          unpack_word<ELEM>(lds16(slot + (NV + j) * WB), r);
 #pragma unroll
-          for (int k = 0; k < W; ++k) u[k] = lds16(slot + ((NV + j) * W + k) * WB);
-          unpack8<ELEM>(u, r);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) v[j][k] = add_2(v[j][k], r[k]);
-          pack8<ELEM>(v[j], u);
-          unpack8<ELEM>(u, v[j]);  // normalised as it is kept
-          uint4* dst = reinterpret_cast<uint4*>(hp + TPR * j * 8 * ES);
-#pragma unroll
-          for (int k = 0; k < W; ++k) dst[k] = u[k];
+          for (int k = 0; k < PP; ++k) v[j][k] = add_2(v[j][k], r[k]);
+          const uint4 u = pack_word<ELEM>(v[j]);
+          unpack_word<ELEM>(u, v[j]);  // normalised as it is kept
+          *reinterpret_cast<uint4*>(hp + TPR * j * 16) = u;
         }
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) s2 = add_2(s2, v[j][k]);
+      for (int k = 0; k < PP; ++k) s2 = add_2(s2, v[j][k]);
     }
     last = slot;
     slot = slot == mine + P * SB ? mine : slot + SB;
@@ -416,9 +414,9 @@ ln_fwd_vec_kernel(const LnFwdParams p) {
     uint64_t q2 = 0;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if ((t + TPR * j) * 8 < p.D) {
+      if ((t + TPR * j) * EPC < p.D) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < PP; ++k) {
           v[j][k] = sub_2(v[j][k], mu2);
           q2 = fma_2(v[j][k], v[j][k], q2);
         }
@@ -429,25 +427,25 @@ ln_fwd_vec_kernel(const LnFwdParams p) {
     const uint64_t rs2 = pk(rs, rs);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (t + TPR * j) * 8;
+      const int c = (t + TPR * j) * EPC;
       const bool in = c < p.D;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[j][k] = mul_2(v[j][k], rs2);
+      for (int k = 0; k < PP; ++k) v[j][k] = mul_2(v[j][k], rs2);
       if (in) {
-        uint64_t y[4];
+        uint64_t y[PP];
         if constexpr (!HOLD) {
-          load8_rt(p.gamma, p.param_elem, c, ga[0]);
-          load8_rt(p.beta, p.param_elem, c, be[0]);
+          load_params<EPC>(p.gamma, p.param_elem, c, ga[0]);
+          load_params<EPC>(p.beta, p.param_elem, c, be[0]);
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) y[k] = fma_2(v[j][k], ga[HOLD ? j : 0][k], be[HOLD ? j : 0][k]);
-        store8<ELEM>(yp, TPR * j * 8, y);
+        for (int k = 0; k < PP; ++k) y[k] = fma_2(v[j][k], ga[HOLD ? j : 0][k], be[HOLD ? j : 0][k]);
+        *reinterpret_cast<uint4*>(yp + TPR * j * 16) = pack_word<ELEM>(y);
       }
-      if constexpr (CK) {
-        const uint32_t b = ckpt_byte(block_amax8(v[j]), p.dt);  // columns past D hold zeros
+      if constexpr (CK) {  // columns past D hold zeros
+        const uint32_t b = ckpt_byte(EPC == 8 ? block_amax8(v[j]) : block_amax4(v[j]), p.dt);
         if (in) {
-          *reinterpret_cast<uint2*>(cp + TPR * j * 8) = encode8(v[j], ckpt_inv_scale(b), p.dt);
-          if ((t & 3) == 0) sp8[TPR / 4 * j] = (uint8_t)b;
+          encode_pairs<EPC>(v[j], ckpt_inv_scale(b), p.dt, cp + TPR * j * EPC);
+          if (t % Word<ELEM>::LANES == 0) sp8[TPR / Word<ELEM>::LANES * j] = (uint8_t)b;
         }
       }
     }
@@ -468,11 +466,10 @@ ln_fwd_vec_kernel(const LnFwdParams p) {
 template <int ELEM, int TPR, int NV, bool CK, bool RES>
 struct BwdShape {
   static constexpr int THREADS = TPR < 256 ? 256 : TPR;
-  static constexpr int W = ELEM == LNFP8_FP32 ? 2 : 1;
   // bytes per thread and row, each kind an array over the threads (so that a warp's accesses fill whole
   // lines of banks): dy, x or the codes, dres, then rsigma and mu or the scale words
-  static constexpr int X_OFF = NV * W * 16, R_OFF = X_OFF + (CK ? NV * 8 : NV * W * 16);
-  static constexpr int S_OFF = R_OFF + (RES ? NV * W * 16 : 0), BYTES = S_OFF + 4 + (CK ? NV * 4 : 4);
+  static constexpr int X_OFF = NV * 16, R_OFF = X_OFF + (CK ? NV * Word<ELEM>::EPC : NV * 16);
+  static constexpr int S_OFF = R_OFF + (RES ? NV * 16 : 0), BYTES = S_OFF + 4 + (CK ? NV * 4 : 4);
   static constexpr int RING = 4 * BYTES * THREADS <= 104 * 1024 ? 4 : 3 * BYTES * THREADS <= 224 * 1024 ? 3 : 2;
   static constexpr size_t SMEM = (size_t)RING * BYTES * THREADS;
   static_assert(SMEM <= 224 * 1024, "shared memory budget");
@@ -482,40 +479,39 @@ template <int ELEM, int TPR, int NV, bool CK, bool RES>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR < 512 ? 2 : 1)
 ln_bwd_vec_kernel(const LnBwdParams p) {
   using S = BwdShape<ELEM, TPR, NV, CK, RES>;
-  constexpr int T = S::THREADS, GPB = T / TPR, W = S::W, RING = S::RING, P = RING - 1;
+  constexpr int T = S::THREADS, GPB = T / TPR, RING = S::RING, P = RING - 1;
+  constexpr int EPC = Word<ELEM>::EPC, PP = EPC / 2, ES = ElemSize<ELEM>::value, LANES = Word<ELEM>::LANES;
   __shared__ float2 xch[2 * T / 32];
   extern __shared__ uint4 ring[];  // [RING][BYTES * T]
   const int g = threadIdx.x / TPR, t = threadIdx.x % TPR;
   pdl_wait();
   pdl_launch_dependents();
-  constexpr int ES = ElemSize<ELEM>::value;
   constexpr uint32_t SB = S::BYTES * T;
   const uint32_t base = (uint32_t)__cvta_generic_to_shared(ring);
-  const uint32_t t16 = threadIdx.x * 16, t8 = S::X_OFF * T + threadIdx.x * 8, t4 = S::S_OFF * T + threadIdx.x * 4;
+  const uint32_t t16 = threadIdx.x * 16, tq = S::X_OFF * T + threadIdx.x * EPC, t4 = S::S_OFF * T + threadIdx.x * 4;
   int64_t row = (int64_t)blockIdx.x * GPB + g;
-  // this thread's first chunk in the row to be loaded next: the pointers run ahead of `row`
-  const uint8_t* dp = static_cast<const uint8_t*>(p.dy) + (row * p.lddy + t * 8) * ES;
-  const uint8_t* xp = CK ? p.codes + row * p.D + t * 8 : static_cast<const uint8_t*>(p.x) + (row * p.ldx + t * 8) * ES;
-  const uint8_t* bp = CK ? p.scales + row * p.pitch + ((t >> 4) << 2) : nullptr;  // the word of this chunk's scale byte
-  const uint8_t* rp = RES ? static_cast<const uint8_t*>(p.dres) + (row * p.lddres + t * 8) * ES : nullptr;
+  // this thread's first word in the row to be loaded next: the pointers run ahead of `row`
+  const uint8_t* dp = static_cast<const uint8_t*>(p.dy) + row * p.lddy * ES + t * 16;
+  const uint8_t* xp = CK ? p.codes + row * p.D + t * EPC : static_cast<const uint8_t*>(p.x) + row * p.ldx * ES + t * 16;
+  const uint8_t* bp = CK ? p.scales + row * p.pitch + t / (4 * LANES) * 4 : nullptr;  // the word of this one's scale byte
+  const uint8_t* rp = RES ? static_cast<const uint8_t*>(p.dres) + row * p.lddres * ES + t * 16 : nullptr;
   const float* mp = p.mu + row;
   const float* sp = p.rs + row;
+  static_assert(TPR % (4 * LANES) == 0, "a thread's scale byte has one place in its words");
   auto issue = [&](int64_t r, uint32_t slot) {
     if (r < p.M) {
       cp4(slot + t4, sp);
       if constexpr (!CK) cp4(slot + t4 + 4 * T, mp);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        if ((t + TPR * j) * 8 < p.D) {
-#pragma unroll
-          for (int k = 0; k < W; ++k) {
-            cp16(slot + t16 + (j * W + k) * 16 * T, dp + TPR * j * 8 * ES + 16 * k);
-            if constexpr (!CK) cp16(slot + t16 + (S::X_OFF + (j * W + k) * 16) * T, xp + TPR * j * 8 * ES + 16 * k);
-            if constexpr (RES) cp16(slot + t16 + (S::R_OFF + (j * W + k) * 16) * T, rp + TPR * j * 8 * ES + 16 * k);
-          }
+        if ((t + TPR * j) * EPC < p.D) {
+          cp16(slot + t16 + j * 16 * T, dp + TPR * j * 16);
+          if constexpr (!CK) cp16(slot + t16 + (S::X_OFF + j * 16) * T, xp + TPR * j * 16);
+          if constexpr (RES) cp16(slot + t16 + (S::R_OFF + j * 16) * T, rp + TPR * j * 16);
           if constexpr (CK) {
-            cp8(slot + t8 + j * 8 * T, xp + TPR * j * 8);
-            cp4(slot + t4 + (4 + 4 * j) * T, bp + TPR / 16 * j * 4);
+            if constexpr (EPC == 8) cp8(slot + tq + j * 8 * T, xp + TPR * j * 8);
+            else cp4(slot + tq + j * 4 * T, xp + TPR * j * 4);
+            cp4(slot + t4 + (4 + 4 * j) * T, bp + TPR / LANES * j);
           }
         }
       }
@@ -530,51 +526,53 @@ ln_bwd_vec_kernel(const LnBwdParams p) {
   };
 #pragma unroll
   for (int k = 0; k < P; ++k) issue(row + k * p.step, base + k * SB);
-  uint64_t ga[NV][4], accg[NV][4], accb[NV][4];  // pairs of columns
+  uint64_t ga[NV][PP], accg[NV][PP], accb[NV][PP];  // pairs of columns
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) ga[j][k] = accg[j][k] = accb[j][k] = 0;
-    const int c = (t + TPR * j) * 8;
-    if (c < p.D) load8_rt(p.gamma, p.param_elem, c, ga[j]);
+    for (int k = 0; k < PP; ++k) ga[j][k] = accg[j][k] = accb[j][k] = 0;
+    const int c = (t + TPR * j) * EPC;
+    if (c < p.D) load_params<EPC>(p.gamma, p.param_elem, c, ga[j]);
   }
   const float inv_d = 1.0f / (float)p.D;
   int turn = 0;
   uint32_t slot = base, last = base + P * SB;
-  const int byte = ((t >> 2) & 3) * 8;  // of this thread's scale in its word, the same in every chunk (TPR is a multiple of 16)
-  uint8_t* op = static_cast<uint8_t*>(p.dx) + (row * p.lddx + t * 8) * ES;
+  const int byte = t / LANES % 4 * 8;  // of this thread's scale in each of its words
+  uint8_t* op = static_cast<uint8_t*>(p.dx) + row * p.lddx * ES + t * 16;
   for (; row - g < p.M; row += p.step) {
     issue(row + P * p.step, last);
     cp_wait<P>();
     const bool active = row < p.M;
-    uint64_t xh[NV][4], gg[NV][4];
+    uint64_t xh[NV][PP], gg[NV][PP];
     uint64_t a1 = 0, a2 = 0;
     const float rs = active ? __uint_as_float(lds4(slot + t4)) : 0.f;
     const uint64_t rs2 = pk(rs, rs);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (t + TPR * j) * 8;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) xh[j][k] = gg[j][k] = 0;
-      if (active && c < p.D) {
-        uint4 u[W];
-        uint64_t d[4];
-#pragma unroll
-        for (int k = 0; k < W; ++k) u[k] = lds16(slot + t16 + (j * W + k) * 16 * T);
-        unpack8<ELEM>(u, d);
+      for (int k = 0; k < PP; ++k) xh[j][k] = gg[j][k] = 0;
+      if (active && (t + TPR * j) * EPC < p.D) {
+        uint64_t d[PP];
+        unpack_word<ELEM>(lds16(slot + t16 + j * 16 * T), d);
         if constexpr (CK) {
-          decode8(lds8(slot + t8 + j * 8 * T), ckpt_scale((lds4(slot + t4 + (4 + 4 * j) * T) >> byte) & 0xFFu), p.dt, xh[j]);
+          const float s = ckpt_scale((lds4(slot + t4 + (4 + 4 * j) * T) >> byte) & 0xFFu);
+          if constexpr (EPC == 8) {
+            decode8(lds8(slot + tq + j * 8 * T), s, p.dt, xh[j]);
+          } else {
+            const uint32_t q = lds4(slot + tq + j * 4 * T);
+            const float2 a = fp8x2_to_f32(q & 0xFFFFu, p.dt), b = fp8x2_to_f32(q >> 16, p.dt);
+            xh[j][0] = mul_2(pk(a.x, a.y), pk(s, s));
+            xh[j][1] = mul_2(pk(b.x, b.y), pk(s, s));
+          }
         } else {
           const float mu = __uint_as_float(lds4(slot + t4 + 4 * T));
           const uint64_t mu2 = pk(mu, mu);
+          unpack_word<ELEM>(lds16(slot + t16 + (S::X_OFF + j * 16) * T), xh[j]);
 #pragma unroll
-          for (int k = 0; k < W; ++k) u[k] = lds16(slot + t16 + (S::X_OFF + (j * W + k) * 16) * T);
-          unpack8<ELEM>(u, xh[j]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) xh[j][k] = mul_2(sub_2(xh[j][k], mu2), rs2);
+          for (int k = 0; k < PP; ++k) xh[j][k] = mul_2(sub_2(xh[j][k], mu2), rs2);
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < PP; ++k) {
           gg[j][k] = mul_2(d[k], ga[j][k]);
           accg[j][k] = fma_2(d[k], xh[j][k], accg[j][k]);
           accb[j][k] = add_2(accb[j][k], d[k]);
@@ -590,21 +588,17 @@ ln_bwd_vec_kernel(const LnBwdParams p) {
       const uint64_t mg2 = pk(mg, mg), nmx2 = pk(nmx, nmx);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int c = (t + TPR * j) * 8;
-        if (c >= p.D) continue;
-        uint64_t o[4];
+        if ((t + TPR * j) * EPC >= p.D) continue;
+        uint64_t o[PP];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o[k] = mul_2(fma_2(nmx2, xh[j][k], sub_2(gg[j][k], mg2)), rs2);
+        for (int k = 0; k < PP; ++k) o[k] = mul_2(fma_2(nmx2, xh[j][k], sub_2(gg[j][k], mg2)), rs2);
         if constexpr (RES) {
-          uint4 u[W];
-          uint64_t r[4];
+          uint64_t r[PP];
+          unpack_word<ELEM>(lds16(slot + t16 + (S::R_OFF + j * 16) * T), r);
 #pragma unroll
-          for (int k = 0; k < W; ++k) u[k] = lds16(slot + t16 + (S::R_OFF + (j * W + k) * 16) * T);
-          unpack8<ELEM>(u, r);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) o[k] = add_2(o[k], r[k]);
+          for (int k = 0; k < PP; ++k) o[k] = add_2(o[k], r[k]);
         }
-        store8<ELEM>(op, TPR * j * 8, o);
+        *reinterpret_cast<uint4*>(op + TPR * j * 16) = pack_word<ELEM>(o);
       }
     }
     op += p.ostep;
@@ -621,12 +615,13 @@ ln_bwd_vec_kernel(const LnBwdParams p) {
     if (g != turn_g) continue;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (t + TPR * j) * 8;
+      const int c = (t + TPR * j) * EPC;
       if (c >= p.D) continue;
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {  // dgamma then dbeta, 4 columns at a time
-        const uint64_t* acc = h < 2 ? accg[j] + 2 * h : accb[j] + 2 * (h - 2);
-        const int at_c = (h < 2 ? 0 : p.D) + c + 4 * (h & 1);
+      for (int h = 0; h < EPC / 2; ++h) {  // dgamma then dbeta, 4 columns at a time
+        const int q = h % (EPC / 4);
+        const uint64_t* acc = h < EPC / 4 ? accg[j] + 2 * q : accb[j] + 2 * q;
+        const int at_c = (h < EPC / 4 ? 0 : p.D) + c + 4 * q;
         const float2 lo = upk(acc[0]), hi = upk(acc[1]);
         float4 v = make_float4(lo.x, lo.y, hi.x, hi.y);
         if (turn_g > 0) {
@@ -728,21 +723,22 @@ lnfp8_status fwd_vec_launch(const LnFwdParams& p, cudaStream_t st) {
   return check_launch("layernorm_fwd");
 }
 
+// 16 columns a thread; the forward's last step takes 32.
 template <int ELEM, bool CK, bool RES>
 lnfp8_status fwd_vec(const LnFwdParams& p, cudaStream_t st) {
-  if (p.D <= 256) return fwd_vec_launch<ELEM, 32, 1, CK, RES>(p, st);
-  if (p.D <= 512) return fwd_vec_launch<ELEM, 32, 2, CK, RES>(p, st);
-  if (p.D <= 1024) return fwd_vec_launch<ELEM, 64, 2, CK, RES>(p, st);
-  if (p.D <= 2048) return fwd_vec_launch<ELEM, 128, 2, CK, RES>(p, st);
-  if (p.D <= 4096) return fwd_vec_launch<ELEM, 256, 2, CK, RES>(p, st);
-  if constexpr (ELEM == LNFP8_FP32 && RES) return fwd_vec_launch<ELEM, 512, 2, CK, RES>(p, st);
-  else return p.D <= 8192 ? fwd_vec_launch<ELEM, 512, 2, CK, RES>(p, st) : fwd_vec_launch<ELEM, 512, 4, CK, RES>(p, st);
+  constexpr int NV = 16 / Word<ELEM>::EPC;
+  if (p.D <= 512) return fwd_vec_launch<ELEM, 32, NV, CK, RES>(p, st);
+  if (p.D <= 1024) return fwd_vec_launch<ELEM, 64, NV, CK, RES>(p, st);
+  if (p.D <= 2048) return fwd_vec_launch<ELEM, 128, NV, CK, RES>(p, st);
+  if (p.D <= 4096) return fwd_vec_launch<ELEM, 256, NV, CK, RES>(p, st);
+  if constexpr (ELEM == LNFP8_FP32 && RES) return fwd_vec_launch<ELEM, 512, NV, CK, RES>(p, st);
+  else return p.D <= 8192 ? fwd_vec_launch<ELEM, 512, NV, CK, RES>(p, st) : fwd_vec_launch<ELEM, 512, 2 * NV, CK, RES>(p, st);
 }
 
 template <int ELEM, int TPR, int NV, bool CK, bool RES>
 lnfp8_status bwd_vec_launch(const LnBwdParams& p, int* blocks_out, cudaStream_t st) {
   using S = BwdShape<ELEM, TPR, NV, CK, RES>;
-  static_assert(S::SMEM >= TPR * NV * 8 * 2 * sizeof(float), "the column partials reuse the ring");
+  static_assert(S::SMEM >= TPR * NV * Word<ELEM>::EPC * 2 * sizeof(float), "the column partials reuse the ring");
   constexpr auto kernel = ln_bwd_vec_kernel<ELEM, TPR, NV, CK, RES>;
   int bps = 1;
   const lnfp8_status s = kernel_setup<kernel>(S::THREADS, S::SMEM, &bps, "layernorm_bwd: kernel set-up");
@@ -764,12 +760,12 @@ lnfp8_status bwd_vec_launch(const LnBwdParams& p, int* blocks_out, cudaStream_t 
 
 template <int ELEM, bool CK, bool RES>
 lnfp8_status bwd_vec(const LnBwdParams& p, int* blocks_out, cudaStream_t st) {
-  if (p.D <= 256) return bwd_vec_launch<ELEM, 32, 1, CK, RES>(p, blocks_out, st);
-  if (p.D <= 512) return bwd_vec_launch<ELEM, 32, 2, CK, RES>(p, blocks_out, st);
-  if (p.D <= 1024) return bwd_vec_launch<ELEM, 64, 2, CK, RES>(p, blocks_out, st);
-  if (p.D <= 2048) return bwd_vec_launch<ELEM, 128, 2, CK, RES>(p, blocks_out, st);
-  if (p.D <= 4096) return bwd_vec_launch<ELEM, 256, 2, CK, RES>(p, blocks_out, st);
-  return bwd_vec_launch<ELEM, 512, 2, CK, RES>(p, blocks_out, st);
+  constexpr int NV = 16 / Word<ELEM>::EPC;
+  if (p.D <= 512) return bwd_vec_launch<ELEM, 32, NV, CK, RES>(p, blocks_out, st);
+  if (p.D <= 1024) return bwd_vec_launch<ELEM, 64, NV, CK, RES>(p, blocks_out, st);
+  if (p.D <= 2048) return bwd_vec_launch<ELEM, 128, NV, CK, RES>(p, blocks_out, st);
+  if (p.D <= 4096) return bwd_vec_launch<ELEM, 256, NV, CK, RES>(p, blocks_out, st);
+  return bwd_vec_launch<ELEM, 512, NV, CK, RES>(p, blocks_out, st);
 }
 
 // Rows of 16-byte words take the vector kernels up to 16384 columns forward (8192 in fp32 with a residual, whose

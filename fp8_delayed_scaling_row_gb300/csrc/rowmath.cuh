@@ -177,6 +177,45 @@ __device__ __forceinline__ void store8(void* p, int64_t i, const V* v) {
   for (int k = 0; k < W; ++k) q[k] = u[k];
 }
 
+// One 16-byte word as pairs: 4 of a 16-bit type, 2 of fp32.
+template <int ELEM>
+__device__ __forceinline__ void unpack_word(const uint4& u, uint64_t* v) {
+  if constexpr (ELEM == LNFP8_FP32) {
+    v[0] = pk(__uint_as_float(u.x), __uint_as_float(u.y));
+    v[1] = pk(__uint_as_float(u.z), __uint_as_float(u.w));
+  } else {
+    unpack8<ELEM>(&u, v);
+  }
+}
+template <int ELEM>
+__device__ __forceinline__ uint4 pack_word(const uint64_t* v) {
+  uint4 u;
+  if constexpr (ELEM == LNFP8_FP32) {
+    const float2 a = upk(v[0]), b = upk(v[1]);
+    u = make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+  } else {
+    pack8<ELEM>(v, &u);
+  }
+  return u;
+}
+// The N (4 or 8) parameters from column i on, as pairs.
+template <int N>
+__device__ __forceinline__ void load_params(const void* p, int elem, int i, uint64_t* v) {
+  if constexpr (N == 8) {
+    load8_rt(p, elem, i, v);
+  } else if (elem == LNFP8_FP32) {
+    unpack_word<LNFP8_FP32>(*reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(p) + i), v);
+  } else {
+    const uint2 u = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(p) + i);
+    const uint4 w = make_uint4(u.x, u.y, 0u, 0u);
+    uint64_t t[4];
+    if (elem == LNFP8_FP16) unpack8<LNFP8_FP16>(&w, t);
+    else unpack8<LNFP8_BF16>(&w, t);
+    v[0] = t[0];
+    v[1] = t[1];
+  }
+}
+
 // The largest finite value of the type.
 template <int ELEM>
 __device__ __forceinline__ float elem_max() {
@@ -249,6 +288,17 @@ __device__ __forceinline__ uint2 encode8(const uint64_t* v, float inv, int dt) {
   }
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
+// N / 2 pairs times inv -> N codes, low byte first.
+template <int N>
+__device__ __forceinline__ void encode_pairs(const uint64_t* v, float inv, int dt, uint8_t* dst) {
+  if constexpr (N == 8) {
+    *reinterpret_cast<uint2*>(dst) = encode8(v, inv, dt);
+  } else {
+    const uint64_t i2 = pk(inv, inv);
+    const float2 a = upk(mul_2(v[0], i2)), b = upk(mul_2(v[1], i2));
+    *reinterpret_cast<uint32_t*>(dst) = fp8x2(a.x, a.y, dt) | (fp8x2(b.x, b.y, dt) << 16);
+  }
+}
 __device__ __forceinline__ void decode8(uint2 q, float scale, int dt, uint64_t* v) {
   const uint32_t w[4] = {q.x & 0xFFFFu, q.x >> 16, q.y & 0xFFFFu, q.y >> 16};
   const uint64_t s2 = pk(scale, scale);
@@ -281,6 +331,15 @@ __device__ __forceinline__ uint32_t block_amax8(const uint64_t* v) {
     f[2 * k + 1] = t.y;
   }
   return block_amax8(f);
+}
+
+// The same of 4 values a lane: 8 lanes hold a block.
+__device__ __forceinline__ uint32_t block_amax4(const uint64_t* v) {
+  const float2 a = upk(v[0]), b = upk(v[1]);
+  uint32_t am = abs_bits(amax3(amax3(a.x, a.y, b.x), b.y, 0.f));
+  am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
+  am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
+  return max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 4));
 }
 
 // A restored value: code * 2^e, kept inside the type (a block whose largest value
