@@ -524,6 +524,23 @@ ln_bwd_vec_kernel(const LnBwdParams p) {
     }
     cp_commit();
   };
+  // words past D, and the slots of a group that gets no row at all, are read but never filled
+#pragma unroll
+  for (int k = 0; k < RING; ++k) {
+    sts4(base + k * SB + t4, 0u);
+    sts4(base + k * SB + t4 + 4 * T, 0u);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if ((t + TPR * j) * EPC < p.D && row < p.M) continue;
+      sts16_zero(base + k * SB + t16 + j * 16 * T);
+      if constexpr (!CK) sts16_zero(base + k * SB + t16 + (S::X_OFF + j * 16) * T);
+      if constexpr (CK) {
+#pragma unroll
+        for (int q = 0; q < EPC; q += 4) sts4(base + k * SB + tq + j * EPC * T + q, 0u);
+        sts4(base + k * SB + t4 + (4 + 4 * j) * T, 0u);
+      }
+    }
+  }
 #pragma unroll
   for (int k = 0; k < P; ++k) issue(row + k * p.step, base + k * SB);
   uint64_t ga[NV][PP], accg[NV][PP], accb[NV][PP];  // pairs of columns
@@ -545,39 +562,57 @@ ln_bwd_vec_kernel(const LnBwdParams p) {
     const bool active = row < p.M;
     uint64_t xh[NV][PP], gg[NV][PP];
     uint64_t a1 = 0, a2 = 0;
-    const float rs = active ? __uint_as_float(lds4(slot + t4)) : 0.f;
-    const uint64_t rs2 = pk(rs, rs);
+    // every word of the row first; those past D hold zeros from the start, and a group without a row
+    // goes through the motions on an old one
+    uint4 du[NV], xu[NV];
+    uint32_t sw[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-#pragma unroll
-      for (int k = 0; k < PP; ++k) xh[j][k] = gg[j][k] = 0;
-      if (active && (t + TPR * j) * EPC < p.D) {
-        uint64_t d[PP];
-        unpack_word<ELEM>(lds16(slot + t16 + j * 16 * T), d);
-        if constexpr (CK) {
-          const float s = ckpt_scale((lds4(slot + t4 + (4 + 4 * j) * T) >> byte) & 0xFFu);
-          if constexpr (EPC == 8) {
-            decode8(lds8(slot + tq + j * 8 * T), s, p.dt, xh[j]);
-          } else {
-            const uint32_t q = lds4(slot + tq + j * 4 * T);
-            const float2 a = fp8x2_to_f32(q & 0xFFFFu, p.dt), b = fp8x2_to_f32(q >> 16, p.dt);
-            xh[j][0] = mul_2(pk(a.x, a.y), pk(s, s));
-            xh[j][1] = mul_2(pk(b.x, b.y), pk(s, s));
-          }
+      du[j] = lds16(slot + t16 + j * 16 * T);
+      if constexpr (!CK) xu[j] = lds16(slot + t16 + (S::X_OFF + j * 16) * T);
+      if constexpr (CK) {
+        if constexpr (EPC == 8) {
+          const uint2 q = lds8(slot + tq + j * 8 * T);
+          xu[j].x = q.x;
+          xu[j].y = q.y;
         } else {
-          const float mu = __uint_as_float(lds4(slot + t4 + 4 * T));
-          const uint64_t mu2 = pk(mu, mu);
-          unpack_word<ELEM>(lds16(slot + t16 + (S::X_OFF + j * 16) * T), xh[j]);
-#pragma unroll
-          for (int k = 0; k < PP; ++k) xh[j][k] = mul_2(sub_2(xh[j][k], mu2), rs2);
+          xu[j].x = lds4(slot + tq + j * 4 * T);
         }
+        sw[j] = lds4(slot + t4 + (4 + 4 * j) * T);
+      }
+    }
+    const float rs = __uint_as_float(lds4(slot + t4));
+    const float mu = CK ? 0.f : __uint_as_float(lds4(slot + t4 + 4 * T));
+    const uint64_t rs2 = pk(rs, rs), mu2 = pk(mu, mu);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      uint64_t d[PP];
+      unpack_word<ELEM>(du[j], d);
+      if constexpr (CK) {
+        const float s = ckpt_scale((sw[j] >> byte) & 0xFFu);
+        if constexpr (EPC == 8) {
+          decode8(make_uint2(xu[j].x, xu[j].y), s, p.dt, xh[j]);
+        } else {
+          const float2 a = fp8x2_to_f32(xu[j].x & 0xFFFFu, p.dt), b = fp8x2_to_f32(xu[j].x >> 16, p.dt);
+          xh[j][0] = mul_2(pk(a.x, a.y), pk(s, s));
+          xh[j][1] = mul_2(pk(b.x, b.y), pk(s, s));
+        }
+      } else {
+        unpack_word<ELEM>(xu[j], xh[j]);
+#pragma unroll
+        for (int k = 0; k < PP; ++k) xh[j][k] = mul_2(sub_2(xh[j][k], mu2), rs2);
+      }
+#pragma unroll
+      for (int k = 0; k < PP; ++k) {
+        gg[j][k] = mul_2(d[k], ga[j][k]);
+        a1 = add_2(a1, gg[j][k]);
+        a2 = fma_2(gg[j][k], xh[j][k], a2);
+      }
+      if (active) {
 #pragma unroll
         for (int k = 0; k < PP; ++k) {
-          gg[j][k] = mul_2(d[k], ga[j][k]);
           accg[j][k] = fma_2(d[k], xh[j][k], accg[j][k]);
           accb[j][k] = add_2(accb[j][k], d[k]);
-          a1 = add_2(a1, gg[j][k]);
-          a2 = fma_2(gg[j][k], xh[j][k], a2);
         }
       }
     }
