@@ -223,17 +223,15 @@ lin_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ T
   } else if (warp == 1 && lane == 0 && side == 0) {
     int stage = 0;
     uint32_t phase = 0;
-    const uint32_t p_step = p_mn ? 2048 : 32, p_lbo = p_mn ? 8192 : 16;  // P's descriptor by its layout
+    const MatDesc pdesc = mat_desc(ring, p_mn), qdesc = mat_desc(ring + C::P_BYTES, Q_MN);
     for (int kb = kb0; kb < kb1; ++kb) {
       if (!mbar_wait(full_bar(stage), phase, abort_flag)) break;
       tc_fence_after();
-      const uint32_t pb = ring + stage * C::STAGE, qb = pb + C::P_BYTES;
+      const uint32_t off = stage * (C::STAGE >> 4);
 #pragma unroll
-      for (int kk = 0; kk < BK / 16; ++kk) {
-        const uint64_t pd = mat_desc(pb + kk * p_step, p_lbo, 1024);
-        const uint64_t qd = Q_MN ? mat_desc(qb + kk * 2048, 8192, 1024) : mat_desc(qb + kk * 32, 16, 1024);
-        mma_16bit<PAIR>(tmem, pd, qd, pr.idesc, kb != kb0 || kk != 0);
-      }
+      for (int kk = 0; kk < BK / 16; ++kk)
+        mma_16bit<PAIR>(tmem, mat_desc64(pdesc.lo + off + kk * pdesc.k_step), mat_desc64(qdesc.lo + off + kk * qdesc.k_step), pr.idesc,
+                        kk != 0 || kb != kb0);
       mma_commit<PAIR>(empty_bar(stage), both);
       if (++stage == STAGES) { stage = 0; phase ^= 1; }
     }

@@ -202,10 +202,13 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
 
   if (warp == 0) {
     if (lane == 0) {
+      // (this loop and the MMA issuer's share their schedulers with busy epilogue warps: a K block's instructions are
+      // the pipeline's slowest part unless they are few, so addresses and descriptors only move by additions)
       int stage = 0;
       uint32_t phase = 0;
       int64_t issued = 0;
       bool ok = true;
+      const uint32_t fb0 = map_to_rank(full_bar(0), 0);
       for (int rd = 0; ok; ++rd) {
         const int t = pair_unit(rd, cid, ncl);
         if (t >= tiles) break;
@@ -215,7 +218,7 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
         const int m0 = at.m2 * 256 + rank * 128, n0 = at.n * BN + rank * (BN / 2);
         for (int kb = at.kb0; kb < at.kb1; ++kb) {
           if (!mbar_wait(empty_bar(stage), phase ^ 1, abort_flag)) { ok = false; break; }
-          const uint32_t fb = map_to_rank(full_bar(stage), 0);
+          const uint32_t fb = fb0 + 8u * stage;
           const uint32_t ad = ring + stage * C::STAGE, bd = ad + C::A_BYTES;
           if (rank == 0) mbar_expect_tx(full_bar(stage), 2 * C::STAGE);
           if (!a_mn) tma_load_pair(ad, tmA, kb * BK, m0, fb);
@@ -242,6 +245,7 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
+      const MatDesc bdesc = mat_desc(ring + C::A_BYTES, B_MN);
       for (int rd = 0; ok; ++rd) {
         const int t = pair_unit(rd, cid, ncl);
         if (t >= tiles) break;
@@ -250,20 +254,16 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
         const PairTile at = pair_locate(p, t);
         const PairProb& pr = p.prob[at.prob];
         const uint32_t idesc = pr.idesc;
-        // the A descriptor's step per 16 k and its leading offset, by A's layout
-        const bool a_mn = EPI == LIN_PLAIN && pr.a_mn;
-        const uint32_t a_step = a_mn ? 2048 : 32, a_lbo = a_mn ? 8192 : 16;
+        const MatDesc adesc = mat_desc(ring, EPI == LIN_PLAIN && pr.a_mn);
         const uint32_t d = tmem + (uint32_t)(acc * BN);
         for (int kb = at.kb0; kb < at.kb1; ++kb) {
           if (!mbar_wait(full_bar(stage), phase, abort_flag)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t ab = ring + stage * C::STAGE, bb = ab + C::A_BYTES;
+          const uint32_t off = stage * (C::STAGE >> 4);
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) {
-            const uint64_t ad = mat_desc(ab + kk * a_step, a_lbo, 1024);
-            const uint64_t bd = B_MN ? mat_desc(bb + kk * 2048, 8192, 1024) : mat_desc(bb + kk * 32, 16, 1024);
-            mma_16bit<true>(d, ad, bd, idesc, kb != at.kb0 || kk != 0);
-          }
+          for (int kk = 0; kk < BK / 16; ++kk)
+            mma_16bit<true>(d, mat_desc64(adesc.lo + off + kk * adesc.k_step), mat_desc64(bdesc.lo + off + kk * bdesc.k_step), idesc,
+                            kk != 0 || kb != at.kb0);
           mma_commit<true>(empty_bar(stage));
           if (++stage == STAGES) { stage = 0; phase ^= 1; }
         }

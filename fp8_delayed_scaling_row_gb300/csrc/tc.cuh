@@ -103,14 +103,19 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// Shared-memory matrix descriptor with the 128-byte swizzle. A 16-bit operand tile is kept in
-// 128-byte rows: K-major tiles hold 64 k per row, groups of 8 rows are 1024 B apart (sbo), lbo is
-// unused; MN-major tiles hold 64 rows/columns per k, groups of 8 k are 1024 B apart (sbo) and
-// the next 64 rows/columns are lbo bytes on.
-__device__ __forceinline__ uint64_t mat_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
+// Shared-memory matrix descriptor with the 128-byte swizzle, as its two 32-bit halves (the address is in the
+// low one, in units of 16 bytes, so that a tile's k steps and the ring's stages are plain additions to it). A
+// 16-bit operand tile is kept in 128-byte rows: K-major tiles hold 64 k per row, groups of 8 rows are
+// 1024 B apart, 16 k are 32 B; MN-major tiles hold 64 rows/columns per k, groups of 8 k are 1024 B apart, 16 k
+// 2048 B, and the next 64 rows/columns are 8192 B on.
+struct MatDesc {
+  uint32_t lo, k_step;
+};
+__device__ __forceinline__ MatDesc mat_desc(uint32_t saddr, bool mn) {
+  return {((saddr & 0x3FFFFu) >> 4) | ((mn ? 8192u >> 4 : 1u) << 16), mn ? 2048u >> 4 : 32u >> 4};
 }
+constexpr uint32_t kMatDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // 1024 B groups, version, 128-byte swizzle
+__device__ __forceinline__ uint64_t mat_desc64(uint32_t lo) { return ((uint64_t)kMatDescHi << 32) | lo; }
 
 // One matrix instruction: 128 (PAIR: 256 over the CTA pair) x N x 16, 16-bit operands, fp32 accumulation.
 template <bool PAIR>
