@@ -407,12 +407,17 @@ struct DactParams {
   void* dz;      // NULL: no activation, only the column sums
   float* part;   // [row blocks][N] or NULL; with `both` [row blocks][2][N]: the sums of dz, then of dz as rounded
   int both;
+  // or, with clusters of kDactCluster row blocks: the sums themselves
+  float* db;
+  float* dbr;
   int64_t M, lddy, pitch;
   int N, dt, rows_per_block;  // dt: the lnfp8_dtype of the codes
 };
 
 enum DactSource { DACT_NONE, DACT_TENSOR, DACT_CKPT };  // no activation; h as a tensor; h as a checkpoint
 constexpr int kDactBlocksPerSm = 4;
+constexpr int kDactCluster = 8;
+constexpr int64_t kDactClusterRows = 1024;  // up to here 8 row blocks are enough and the sums need no second launch
 constexpr int kDactRing = 6;  // rows of a thread in its shared-memory ring: 5 on their way while one is used
 
 template <int SRC>
@@ -505,8 +510,12 @@ __global__ void __launch_bounds__(256, kDactBlocksPerSm) lin_dact_kernel(const D
     slot = slot == base + P * SB ? base : slot + SB;
   }
   cp_wait<0>();
-  if (p.part == nullptr) return;
-  for (int k = 0; k <= p.both; ++k) {
+  if (p.part == nullptr && p.db == nullptr) return;
+  const int col = threadIdx.x;  // 256 columns
+  float sum[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (k > p.both) break;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -515,12 +524,32 @@ __global__ void __launch_bounds__(256, kDactBlocksPerSm) lin_dact_kernel(const D
       red[rl][cl][2 * i + 1] = t.y;
     }
     __syncthreads();
-    const int col = threadIdx.x;  // 256 columns
-    float s = 0.f;
+    sum[k] = 0.f;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) s += red[q][col >> 3][col & 7];
-    if (blockIdx.x * 256 + col < p.N) p.part[((int64_t)blockIdx.y * (1 + p.both) + k) * p.N + blockIdx.x * 256 + col] = s;
+    for (int q = 0; q < 8; ++q) sum[k] += red[q][col >> 3][col & 7];
   }
+  const int n = blockIdx.x * 256 + col;
+  if (p.part != nullptr) {
+    for (int k = 0; k <= p.both; ++k)
+      if (n < p.N) p.part[((int64_t)blockIdx.y * (1 + p.both) + k) * p.N + n] = sum[k ? 1 : 0];
+    return;
+  }
+  // the row blocks of a column block are one cluster: each adds an eighth of the columns over all of them
+  __syncthreads();
+  float* fin = &red[0][0][0];  // [2][256]
+  fin[col] = sum[0];
+  if (p.both) fin[256 + col] = sum[1];
+  cluster_sync_all();
+  const int rank = (int)cluster_rank(), lane = threadIdx.x & 31, k = threadIdx.x >> 5;
+  if (k <= p.both) {
+    const uint32_t at = smem_u32(fin + 256 * k + rank * 32 + lane);
+    float t = 0.f;
+#pragma unroll
+    for (int q = 0; q < kDactCluster; ++q) t += ld_cluster_f(map_to_rank(at, q));
+    const int m = blockIdx.x * 256 + rank * 32 + lane;
+    if (m < p.N) (k ? p.dbr : p.db)[m] = t;
+  }
+  cluster_sync_all();  // nobody leaves while its sums may be read
 }
 
 // ------------------------------------------------------------ host side
@@ -651,12 +680,27 @@ lnfp8_status dact_launch(const DactParams& p, dim3 grid, cudaStream_t st) {
   const lnfp8_status set = kernel_setup<k>(256, DactShape<SRC>::SMEM, nullptr, "linear_act_bwd: kernel set-up");
   if (set != LNFP8_OK) return set;
   LaunchScope ls("linear_dact", st);
-  if (launch_pdl(k, grid, dim3(256), DactShape<SRC>::SMEM, st, p) != cudaSuccess) return check_launch("linear_act_bwd launch");
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.y = kDactCluster;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = DactShape<SRC>::SMEM;
+  cfg.stream = st;
+  cfg.attrs = pdl_enabled() ? attr : attr + 1;
+  cfg.numAttrs = (pdl_enabled() ? 1 : 0) + (p.db ? 1 : 0);
+  if (cudaLaunchKernelEx(&cfg, k, p) != cudaSuccess) return check_launch("linear_act_bwd launch");
   return check_launch("linear_act_bwd: dz");
 }
 
 // Rows of the dz pass per block: one wave of resident blocks.
 int64_t dact_rows_per_block(int64_t M, int64_t N) {
+  if (M <= kDactClusterRows) return (M + 8 * kDactCluster - 1) / (8 * kDactCluster) * 8;
   const int64_t col_blocks = (N + 255) / 256;
   const int64_t row_blocks = max64(1, (int64_t)num_sms() * kDactBlocksPerSm / col_blocks);
   const int64_t rows = (M + row_blocks - 1) / row_blocks;
@@ -892,7 +936,10 @@ lnfp8_status linear_act_bwd_launch(const lnfp8_linear_act_bwd_args* a, cudaStrea
     p.codes = a->h_ckpt.codes;
     p.scales = a->h_ckpt.scales;
     p.dz = dz_ws;
-    p.part = db ? reinterpret_cast<float*>(ws) : nullptr;
+    const bool clustered = db && a->M <= kDactClusterRows;
+    p.part = db && !clustered ? reinterpret_cast<float*>(ws) : nullptr;
+    p.db = clustered ? db : nullptr;
+    p.dbr = dbr;
     p.both = affine && has_act;
     p.M = a->M;
     p.lddy = a->ld_dy;
@@ -900,7 +947,7 @@ lnfp8_status linear_act_bwd_launch(const lnfp8_linear_act_bwd_args* a, cudaStrea
     p.N = (int)a->N;
     p.dt = a->h_ckpt.dtype;
     p.rows_per_block = (int)dact_rows_per_block(a->M, a->N);
-    const int64_t row_blocks = (a->M + p.rows_per_block - 1) / p.rows_per_block;
+    const int64_t row_blocks = a->M <= kDactClusterRows ? kDactCluster : (a->M + p.rows_per_block - 1) / p.rows_per_block;
     const dim3 grid((unsigned)((a->N + 255) / 256), (unsigned)row_blocks);
     auto pick = [&](auto elem) {
       constexpr int E = decltype(elem)::value;
@@ -915,7 +962,7 @@ lnfp8_status linear_act_bwd_launch(const lnfp8_linear_act_bwd_args* a, cudaStrea
     };
     lnfp8_status s = a->elem == LNFP8_BF16 ? pick(std::integral_constant<int, LNFP8_BF16>()) : pick(std::integral_constant<int, LNFP8_FP16>());
     if (s != LNFP8_OK) return s;
-    if (db) {
+    if (p.part) {
       s = colsum_launch(p.part, (int)row_blocks, p.N * (1 + p.both), p.N, db, dbr, st);
       if (s != LNFP8_OK) return s;
     }

@@ -712,21 +712,11 @@ def _flat(t, name, shape, dtype, dev) -> None:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-class _On:
-    """Allocations of a call belong to the stream that it runs on."""
-
-    def __init__(self, stream, dev):
-        if stream is not None and stream.device.index != dev:
-            raise ValueError(f"the stream is on {stream.device}, the tensors are on cuda:{dev}")
-        self.ctx = torch.cuda.stream(stream) if stream is not None else None
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+def _on(stream, dev):
+    """Context in which a call runs on a given stream: what it allocates belongs to that stream."""
+    if stream.device.index != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on cuda:{dev}")
+    return torch.cuda.stream(stream)
 
 
 @dataclass
@@ -751,6 +741,12 @@ def act_ckpt_scale_pitch(cols) -> int:
     return int(_c_ckpt_pitch(cols))
 
 
+def _new_ckpt(rows, cols, dtype, device):
+    """A checkpoint and its C form (nothing in it to check)."""
+    codes, scales = _e((rows, cols), torch.uint8, device), _e((rows, (cols + 127) // 128 * 4), torch.uint8, device)
+    return ActCkpt(codes, scales, dtype), CCkpt(codes.data_ptr(), scales.data_ptr(), dtype)
+
+
 def act_ckpt(rows, cols, *, dtype=E4M3, device="cuda") -> ActCkpt:
     """An uninitialised checkpoint of a [rows, cols] tensor."""
     return ActCkpt(_e((rows, cols), torch.uint8, device), _e((rows, (cols + 127) // 128 * 4), torch.uint8, device), dtype)
@@ -763,10 +759,15 @@ def act_ckpt_save(x, *, dtype=E4M3, ckpt: ActCkpt | None = None, stream=None) ->
         raise ValueError(f"x has shape {tuple(x.shape)}: expected two dimensions")
     rows, cols = x.shape
     dev = _dev(x, "x")
+    if stream is not None:
+        with _on(stream, dev):
+            return act_ckpt_save(x, dtype=dtype, ckpt=ckpt)
     ldx = _rows(x, "x", rows, cols, x.dtype, dev)
-    with _On(stream, dev):
-        ckpt = ckpt if ckpt is not None else act_ckpt(rows, cols, dtype=dtype, device=dev)
-        _check(_c_ckpt_save(x.data_ptr(), elem, rows, cols, ldx, C.byref(ckpt.c(rows, cols, dev)), _raw_stream(dev)))
+    if ckpt is None:
+        ckpt, cc = _new_ckpt(rows, cols, dtype, x.device)
+    else:
+        cc = ckpt.c(rows, cols, dev)
+    _check(_c_ckpt_save(x.data_ptr(), elem, rows, cols, ldx, C.byref(cc), _raw_stream(dev)))
     return ckpt
 
 
@@ -776,18 +777,22 @@ def act_ckpt_restore(ckpt: ActCkpt, *, out_dtype=torch.bfloat16, act="none", gam
     output from its checkpointed rows). Values beyond the type's range saturate."""
     rows, cols = ckpt.codes.shape
     dev = _dev(ckpt.codes, "ckpt.codes")
+    if stream is not None:
+        with _on(stream, dev):
+            return act_ckpt_restore(ckpt, out_dtype=out_dtype, act=act, gamma=gamma, beta=beta, out=out)
     cc = ckpt.c(rows, cols, dev)
     pe = 0
     if gamma is not None and beta is not None:
         pe = _elem(gamma, "gamma")
         _flat(gamma, "gamma", (cols,), gamma.dtype, dev)
         _flat(beta, "beta", (cols,), gamma.dtype, dev)
-    with _On(stream, dev):
-        out = out if out is not None else _e((rows, cols), out_dtype, dev)
-        elem = _elem(out, "out")
+    ldo = cols
+    if out is None:
+        out = _e((rows, cols), out_dtype, ckpt.codes.device)
+    else:
         ldo = _rows(out, "out", rows, cols, out.dtype, dev)
-        _check(_c_ckpt_restore(C.byref(cc), rows, cols, _act(act), _ptr(gamma), _ptr(beta), pe, out.data_ptr(), elem,
-                               ldo, _raw_stream(dev)))
+    _check(_c_ckpt_restore(C.byref(cc), rows, cols, _act(act), _ptr(gamma), _ptr(beta), pe, out.data_ptr(),
+                           _elem(out, "out"), ldo, _raw_stream(dev)))
     return out
 
 
@@ -810,24 +815,33 @@ def layernorm_fwd(x, gamma, beta, *, eps=1e-5, residual=None, ckpt=False, y=None
     if x.dim() != 2:
         raise ValueError(f"x has shape {tuple(x.shape)}: expected two dimensions")
     M, D = x.shape
-    dt, dev = x.dtype, _dev(x, "x")
+    dt, dev, device = x.dtype, _dev(x, "x"), x.device
+    if stream is not None:
+        with _on(stream, dev):
+            return layernorm_fwd(x, gamma, beta, eps=eps, residual=residual, ckpt=ckpt, y=y)
     ldx = _rows(x, "x", M, D, dt, dev)
     _flat(gamma, "gamma", (D,), gamma.dtype, dev)
     _flat(beta, "beta", (D,), gamma.dtype, dev)
     ldr = _rows(residual, "residual", M, D, dt, dev) if residual is not None else 0
-    with _On(stream, dev):
-        y = y if y is not None else _e((M, D), dt, dev)
+    ldy = D
+    if y is None:
+        y = _e((M, D), dt, device)
+    else:
         ldy = _rows(y, "y", M, D, dt, dev)
-        mu, rs = _e((M,), torch.float32, dev), _e((M,), torch.float32, dev)
-        h = _e((M, D), dt, dev) if residual is not None else x
-        if ckpt is True:
-            ckpt = act_ckpt(M, D, device=dev)
-        elif ckpt is False:
-            ckpt = None
-        a = CLayerNormFwd(M, D, elem, pe, x.data_ptr(), _ptr(residual), gamma.data_ptr(), beta.data_ptr(), y.data_ptr(),
-                          h.data_ptr() if residual is not None else None, mu.data_ptr(), rs.data_ptr(),
-                          ckpt.c(M, D, dev) if ckpt is not None else _NO_CKPT, ldx, ldr, ldy, eps)
-        _check(_c_layernorm_fwd(C.byref(a), _raw_stream(dev)))
+    mu, rs = _e((M,), torch.float32, device), _e((M,), torch.float32, device)
+    h, hp = x, None
+    if residual is not None:
+        h = _e((M, D), dt, device)
+        hp = h.data_ptr()
+    if ckpt is False or ckpt is None:
+        ckpt, cc = None, _NO_CKPT
+    elif ckpt is True:
+        ckpt, cc = _new_ckpt(M, D, E4M3, device)
+    else:
+        cc = ckpt.c(M, D, dev)
+    a = CLayerNormFwd(M, D, elem, pe, x.data_ptr(), _ptr(residual), gamma.data_ptr(), beta.data_ptr(), y.data_ptr(), hp,
+                      mu.data_ptr(), rs.data_ptr(), cc, ldx, ldr, ldy, eps)
+    _check(_c_layernorm_fwd(C.byref(a), _raw_stream(dev)))
     return y, LayerNormCtx(h, mu, rs, ckpt)
 
 
@@ -845,7 +859,7 @@ def layernorm_bwd_workspace_size(M, D) -> int:
 
 def layernorm_grads(M, D, *, dtype=torch.bfloat16, device="cuda") -> LayerNormGrads:
     return LayerNormGrads(_e((M, D), dtype, device), _e((D,), torch.float32, device), _e((D,), torch.float32, device),
-                          _e((layernorm_bwd_workspace_size(M, D),), torch.uint8, device))
+                          _e((_c_layernorm_bwd_ws(M, D),), torch.uint8, device))
 
 
 def layernorm_bwd(dy, ctx: LayerNormCtx, gamma, *, dresidual=None, grads: LayerNormGrads | None = None,
@@ -857,26 +871,34 @@ def layernorm_bwd(dy, ctx: LayerNormCtx, gamma, *, dresidual=None, grads: LayerN
         raise ValueError(f"dy has shape {tuple(dy.shape)}: expected two dimensions")
     M, D = dy.shape
     dt, dev = dy.dtype, _dev(dy, "dy")
+    if stream is not None:
+        with _on(stream, dev):
+            return layernorm_bwd(dy, ctx, gamma, dresidual=dresidual, grads=grads)
     lddy = _rows(dy, "dy", M, D, dt, dev)
     _flat(gamma, "gamma", (D,), gamma.dtype, dev)
     _flat(ctx.rsigma, "ctx.rsigma", (M,), torch.float32, dev)
     if ctx.ckpt is not None:
         ck, x, mu, ldx = ctx.ckpt.c(M, D, dev), None, None, 0
+    elif ctx.x is None or ctx.mu is None:
+        raise ValueError("ctx holds neither a checkpoint nor x and mu")
     else:
         ck, x, mu = _NO_CKPT, ctx.x.data_ptr(), ctx.mu.data_ptr()
         ldx = _rows(ctx.x, "ctx.x", M, D, dt, dev)
         _flat(ctx.mu, "ctx.mu", (M,), torch.float32, dev)
     lddr = _rows(dresidual, "dresidual", M, D, dt, dev) if dresidual is not None else 0
-    with _On(stream, dev):
-        g = grads if grads is not None else layernorm_grads(M, D, dtype=dt, device=dev)
-        lddx = _rows(g.dx, "grads.dx", M, D, dt, dev)
-        _flat(g.dgamma, "grads.dgamma", (D,), torch.float32, dev)
-        _flat(g.dbeta, "grads.dbeta", (D,), torch.float32, dev)
-        a = CLayerNormBwd(M, D, elem, pe, dy.data_ptr(), x, mu, ctx.rsigma.data_ptr(), ck, gamma.data_ptr(),
-                          _ptr(dresidual), g.dx.data_ptr(), g.dgamma.data_ptr(), g.dbeta.data_ptr(), _ptr(g.workspace),
-                          g.workspace.numel() if g.workspace is not None else 0, lddy, ldx, lddr, lddx)
-        _check(_c_layernorm_bwd(C.byref(a), _raw_stream(dev)))
-    return g
+    lddx = D
+    if grads is None:
+        grads = layernorm_grads(M, D, dtype=dt, device=dy.device)
+    else:
+        lddx = _rows(grads.dx, "grads.dx", M, D, dt, dev)
+        _flat(grads.dgamma, "grads.dgamma", (D,), torch.float32, dev)
+        _flat(grads.dbeta, "grads.dbeta", (D,), torch.float32, dev)
+    ws = grads.workspace
+    a = CLayerNormBwd(M, D, elem, pe, dy.data_ptr(), x, mu, ctx.rsigma.data_ptr(), ck, gamma.data_ptr(), _ptr(dresidual),
+                      grads.dx.data_ptr(), grads.dgamma.data_ptr(), grads.dbeta.data_ptr(), _ptr(ws),
+                      ws.numel() if ws is not None else 0, lddy, ldx, lddr, lddx)
+    _check(_c_layernorm_bwd(C.byref(a), _raw_stream(dev)))
+    return grads
 
 
 _ELEM16 = {torch.bfloat16: 0, torch.float16: 1}
@@ -904,29 +926,41 @@ def linear_act_fwd(x, w, bias=None, *, act="none", residual=None, save="none", y
     M, K = x.shape
     N = w.shape[0]
     dt, dev = x.dtype, _dev(x, "x")
+    if stream is not None:
+        with _on(stream, dev):
+            return linear_act_fwd(x, w, bias, act=act, residual=residual, save=save, y=y, ctx=ctx)
     ldx = _rows(x, "x", M, K, dt, dev)
     _flat(w, "w", (N, K), dt, dev)
     if bias is not None:
         _flat(bias, "bias", (N,), dt, dev)
     ldr = _rows(residual, "residual", M, N, dt, dev) if residual is not None else 0
-    with _On(stream, dev):
-        y = y if y is not None else _e((M, N), dt, dev)
+    ldy = N
+    if y is None:
+        y = _e((M, N), dt, x.device)
+    else:
         ldy = _rows(y, "y", M, N, dt, dev)
-        ctx = ctx if ctx is not None else LinearActCtx()
-        ctx.act = act
-        h, ck = None, _NO_CKPT
-        if save == "h":
-            ctx.ckpt = None
-            ctx.h = ctx.h if ctx.h is not None else _e((M, N), dt, dev)
+    if ctx is None:
+        ctx = LinearActCtx()
+    ctx.act = act
+    h, ck = None, _NO_CKPT
+    if save == "h":
+        ctx.ckpt = None
+        if ctx.h is None:
+            ctx.h = _e((M, N), dt, x.device)
+        else:
             _flat(ctx.h, "ctx.h", (M, N), dt, dev)
-            h = ctx.h.data_ptr()
-        elif save == "ckpt":
-            ctx.h = None
-            ctx.ckpt = ctx.ckpt if ctx.ckpt is not None else act_ckpt(M, N, device=dev)
+        h = ctx.h.data_ptr()
+    elif save == "ckpt":
+        ctx.h = None
+        if ctx.ckpt is None:
+            ctx.ckpt, ck = _new_ckpt(M, N, E4M3, x.device)
+        else:
             ck = ctx.ckpt.c(M, N, dev, "ctx.ckpt")
-        a = CLinearActFwd(M, K, N, elem, ia, x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual), y.data_ptr(), h, ck,
-                          ldx, ldr, ldy)
-        _check(_c_linear_act_fwd(C.byref(a), _raw_stream(dev)))
+    else:
+        ctx.h = ctx.ckpt = None
+    a = CLinearActFwd(M, K, N, elem, ia, x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual), y.data_ptr(), h, ck, ldx,
+                      ldr, ldy)
+    _check(_c_linear_act_fwd(C.byref(a), _raw_stream(dev)))
     return y, ctx
 
 
@@ -945,7 +979,7 @@ def linear_act_bwd_workspace_size(M, K, N, *, has_act, x_from_ckpt) -> int:
 def linear_act_grads(M, K, N, *, act="none", x_from_ckpt=False, dx=True, dw=True, bias=True, dtype=torch.bfloat16,
                      device="cuda") -> LinearActGrads:
     """Gradients and workspace of one linear_act_bwd; dx, dw, bias=False leave theirs out."""
-    ws = linear_act_bwd_workspace_size(M, K, N, has_act=act != "none", x_from_ckpt=x_from_ckpt)
+    ws = _c_linear_act_bwd_ws(M, K, N, int(act != "none"), int(x_from_ckpt))
     return LinearActGrads(_e((M, K), dtype, device) if dx else None, _e((N, K), dtype, device) if dw else None,
                           _e((N,), torch.float32, device) if bias else None, _e((ws,), torch.uint8, device))
 
@@ -961,6 +995,9 @@ def linear_act_bwd(dy, x, w, ctx: LinearActCtx, *, x_act="none", x_gamma=None, x
     M, N = dy.shape
     K = w.shape[1]
     dt, dev = dy.dtype, _dev(dy, "dy")
+    if stream is not None:
+        with _on(stream, dev):
+            return linear_act_bwd(dy, x, w, ctx, x_act=x_act, x_gamma=x_gamma, x_beta=x_beta, grads=grads)
     lddy = _rows(dy, "dy", M, N, dt, dev)
     _flat(w, "w", (N, K), dt, dev)
     h, hck, xp, xck, ldx = None, _NO_CKPT, None, _NO_CKPT, 0
@@ -977,19 +1014,24 @@ def linear_act_bwd(dy, x, w, ctx: LinearActCtx, *, x_act="none", x_gamma=None, x
     elif x is not None:
         ldx = _rows(x, "x", M, K, dt, dev)
         xp = x.data_ptr()
-    for t, name in ((x_gamma, "x_gamma"), (x_beta, "x_beta")):
-        if t is not None:
-            _flat(t, name, (K,), dt, dev)
-    with _On(stream, dev):
-        g = grads if grads is not None else linear_act_grads(M, K, N, act=ctx.act, x_from_ckpt=xck is not _NO_CKPT,
-                                                             dw=x is not None, dtype=dt, device=dev)
-        lddx = _rows(g.dx, "grads.dx", M, K, dt, dev) if g.dx is not None else 0
-        if g.dw is not None:
-            _flat(g.dw, "grads.dw", (N, K), dt, dev)
-        if g.dbias is not None:
-            _flat(g.dbias, "grads.dbias", (N,), torch.float32, dev)
-        a = CLinearActBwd(M, K, N, elem, ia, dy.data_ptr(), xp, xck, _act(x_act), _ptr(x_gamma), _ptr(x_beta), w.data_ptr(),
-                          h, hck, _ptr(g.dx), _ptr(g.dw), _ptr(g.dbias), _ptr(g.workspace),
-                          g.workspace.numel() if g.workspace is not None else 0, lddy, ldx, lddx)
-        _check(_c_linear_act_bwd(C.byref(a), _raw_stream(dev)))
-    return g
+    if x_gamma is not None:
+        _flat(x_gamma, "x_gamma", (K,), dt, dev)
+    if x_beta is not None:
+        _flat(x_beta, "x_beta", (K,), dt, dev)
+    lddx = K
+    if grads is None:
+        grads = linear_act_grads(M, K, N, act=ctx.act, x_from_ckpt=xck is not _NO_CKPT, dw=x is not None, dtype=dt,
+                                 device=dy.device)
+    else:
+        if grads.dx is not None:
+            lddx = _rows(grads.dx, "grads.dx", M, K, dt, dev)
+        if grads.dw is not None:
+            _flat(grads.dw, "grads.dw", (N, K), dt, dev)
+        if grads.dbias is not None:
+            _flat(grads.dbias, "grads.dbias", (N,), torch.float32, dev)
+    ws = grads.workspace
+    a = CLinearActBwd(M, K, N, elem, ia, dy.data_ptr(), xp, xck, _act(x_act), _ptr(x_gamma), _ptr(x_beta), w.data_ptr(), h,
+                      hck, _ptr(grads.dx), _ptr(grads.dw), _ptr(grads.dbias), _ptr(ws), ws.numel() if ws is not None else 0,
+                      lddy, ldx, lddx)
+    _check(_c_linear_act_bwd(C.byref(a), _raw_stream(dev)))
+    return grads
