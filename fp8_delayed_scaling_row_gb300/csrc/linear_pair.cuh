@@ -288,17 +288,9 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
       const PairProb& pr = p.prob[at.prob];
       const int m = at.m2 * 256 + rank * 128 + quarter * 32 + lane;
       const int nh = at.n * BN + half * HALF;  // this warp's first column
-      // four columns of the per-column vectors per lane, asked for before the accumulator is waited for
-      uint2 cb = make_uint2(0u, 0u), cv = make_uint2(0u, 0u);
-      float rv = 0.f;
-      const int lc = nh + lane * 4;
       const bool affine = EPI == LIN_PLAIN && pr.cscale != nullptr && pr.pieces == 1;
-      const void* col_vec = EPI == LIN_FULL ? p.bias : affine ? pr.cscale : nullptr;
-      if (lane * 4 < HALF && lc < pr.N) {
-        if (col_vec) cb = __ldg(reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(col_vec) + lc));
-        if (affine) cv = __ldg(reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(pr.cvec) + lc));
-      }
-      if (affine && m < pr.M) rv = __ldg(pr.rvec + m);
+      const uint16_t* col_vec = static_cast<const uint16_t*>(EPI == LIN_FULL ? p.bias : affine ? pr.cscale : nullptr);
+      const float rv = affine && m < pr.M ? __ldg(pr.rvec + m) : 0.f;
       if (!mbar_wait(tfull_bar(acc), acc_phase, abort_flag)) break;
       tc_fence_after();
       const bool row_ok = m < pr.M;
@@ -329,14 +321,25 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
         uint32_t res[16];
         if constexpr (EPI == LIN_FULL)
           if (p.resid && row_ok) load_row32(reinterpret_cast<const uint16_t*>(p.resid) + m * p.ldr, n0, pr.N, p.wide_resid, res);
+        // every lane reads the same 32 columns: broadcasts from L1, fewer instructions than a lane's columns
+        // spread by shuffles (8192 x 2048 x 8192 161 -> 158 us, 16384 x 8192 x 2048 297 -> 292 us)
         if (col_vec) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {  // columns 2i, 2i + 1 of the chunk sit in lane 8 ch + i / 2
-            const float2 b = unpack16(__shfl_sync(0xFFFFFFFFu, i & 1 ? cb.y : cb.x, ch * 8 + (i >> 1)), p.f16);
-            if constexpr (EPI == LIN_FULL) z[i] = add_2(z[i], pk(b.x, b.y));
-            else {
-              const float2 v = unpack16(__shfl_sync(0xFFFFFFFFu, i & 1 ? cv.y : cv.x, ch * 8 + (i >> 1)), p.f16);
-              z[i] = fma_2(z[i], pk(b.x, b.y), mul_2(pk(rv, rv), pk(v.x, v.y)));
+          for (int j = 0; j < 4; ++j) {
+            if (n0 + 8 * j >= pr.N) break;
+            const uint4 bu = __ldg(reinterpret_cast<const uint4*>(col_vec + n0 + 8 * j));
+            const uint32_t bw[4] = {bu.x, bu.y, bu.z, bu.w};
+            uint4 vu = make_uint4(0u, 0u, 0u, 0u);
+            if (affine) vu = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(pr.cvec) + n0 + 8 * j));
+            const uint32_t vw[4] = {vu.x, vu.y, vu.z, vu.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 b = unpack16(bw[i], p.f16);
+              if constexpr (EPI == LIN_FULL) z[4 * j + i] = add_2(z[4 * j + i], pk(b.x, b.y));
+              else {
+                const float2 v = unpack16(vw[i], p.f16);
+                z[4 * j + i] = fma_2(z[4 * j + i], pk(b.x, b.y), mul_2(pk(rv, rv), pk(v.x, v.y)));
+              }
             }
           }
         }
