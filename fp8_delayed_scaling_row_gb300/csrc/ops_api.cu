@@ -16,6 +16,7 @@ namespace {
   } while (0)
 
 constexpr int64_t kMaxRows = (1ll << 31) - 1;
+constexpr int64_t kMaxTokens = (1ll << 31) - 1024;  // linear_act: tile rows past the last token stay 32-bit numbers
 constexpr int64_t kMaxCols = 1ll << 30;
 
 int elem_size(int elem) { return elem == LNFP8_FP32 ? 4 : 2; }
@@ -42,9 +43,9 @@ lnfp8_status check_act(int act, const char* name, const char* who) {
   if (act < LNFP8_ACT_NONE || act > LNFP8_ACT_SILU) return set_error(LNFP8_ERR_INVALID_ARG, "%s: bad %s %d", who, name, act);
   return LNFP8_OK;
 }
-lnfp8_status check_rows(int64_t v, const char* name, const char* who) {
+lnfp8_status check_rows(int64_t v, const char* name, const char* who, int64_t most = kMaxRows) {
   if (v < 0) return set_error(LNFP8_ERR_INVALID_ARG, "%s: %s = %lld < 0", who, name, (long long)v);
-  if (v > kMaxRows) return set_error(LNFP8_ERR_UNSUPPORTED_SHAPE, "%s: %s = %lld too large", who, name, (long long)v);
+  if (v > most) return set_error(LNFP8_ERR_UNSUPPORTED_SHAPE, "%s: %s = %lld too large", who, name, (long long)v);
   return LNFP8_OK;
 }
 lnfp8_status check_cols(int64_t v, int64_t most, const char* name, const char* who) {
@@ -202,7 +203,7 @@ lnfp8_status linear_act_fwd(const lnfp8_linear_act_fwd_args* args, lnfp8_stream 
   lnfp8_linear_act_fwd_args a = *args;
   TRY(check_elem16(a.elem, who));
   TRY(check_act(a.act, "act", who));
-  TRY(check_rows(a.M, "M", who));
+  TRY(check_rows(a.M, "M", who, kMaxTokens));
   TRY(check_feature(a.K, "K", who));
   TRY(check_feature(a.N, "N", who));
   TRY(fill_ld8(&a.ldx, a.K, "ldx", who));
@@ -235,7 +236,7 @@ lnfp8_status linear_act_bwd(const lnfp8_linear_act_bwd_args* args, lnfp8_stream 
   TRY(check_elem16(a.elem, who));
   TRY(check_act(a.act, "act", who));
   TRY(check_act(a.x_act, "x_act", who));
-  TRY(check_rows(a.M, "M", who));
+  TRY(check_rows(a.M, "M", who, kMaxTokens));
   TRY(check_feature(a.K, "K", who));
   TRY(check_feature(a.N, "N", who));
   TRY(fill_ld8(&a.ld_dy, a.N, "ld_dy", who));

@@ -622,7 +622,7 @@ lnfp8_status layernorm_bwd(const lnfp8_layernorm_bwd_args* args, lnfp8_stream st
 int64_t lnfp8_layernorm_bwd_workspace_size(int64_t M, int64_t D);
 
 typedef struct {
-  int64_t M, K, N;        /* rows (tokens) >= 0, in_features, out_features (multiples of 8) */
+  int64_t M, K, N;        /* rows (tokens) 0..2^31 - 1024, in_features, out_features (multiples of 8) */
   int elem;               /* LNFP8_BF16 or LNFP8_FP16, of every tensor */
   int act;                /* lnfp8_act */
   const void* x;          /* [M, K] */

@@ -158,6 +158,15 @@ def test_linear_act_bwd_refuses_checkpoint_mixes(L):
     assert small >= 96 * 4 and big >= small + 100 * (64 + 96) * 2
 
 
+@pytest.mark.parametrize("M", [(1 << 31) - 1, (1 << 31) - 1023])
+def test_linear_act_refuses_more_tokens_than_its_tiles_count(L, M):
+    """Rows of a tile are 32-bit numbers up to a tile past the last token."""
+    f = L.CLinearActFwd(M=M, K=64, N=64, x=FAKE, w=FAKE, y=FAKE)
+    assert L._c_linear_act_fwd(ctypes.byref(f), None) == 2 and "M" in L.last_error()
+    b = L.CLinearActBwd(M=M, K=64, N=64, dy=FAKE, x=FAKE, w=FAKE, dx=FAKE, dw=FAKE, workspace=FAKE, workspace_bytes=1 << 60)
+    assert L._c_linear_act_bwd(ctypes.byref(b), None) == 2 and "M" in L.last_error()
+
+
 STRUCTS = {"lnfp8_ckpt": "CCkpt", "lnfp8_layernorm_fwd_args": "CLayerNormFwd", "lnfp8_layernorm_bwd_args": "CLayerNormBwd",
            "lnfp8_linear_act_fwd_args": "CLinearActFwd", "lnfp8_linear_act_bwd_args": "CLinearActBwd"}
 
