@@ -250,8 +250,12 @@ lnfp8_status linear_act_bwd(const lnfp8_linear_act_bwd_args* args, lnfp8_stream 
     TRY(maybe(a.dx, 16, "dx", who));
     if (a.dx) TRY(need(a.w, 16, "w", who));
     if (a.act != LNFP8_ACT_NONE) {
-      if (hck) TRY(check_ckpt(a.h_ckpt, 8, "h_ckpt", who));
-      else TRY(need(a.h, 16, "h", who));
+      if (hck) {
+        TRY(check_ckpt(a.h_ckpt, 8, "h_ckpt", who));
+        if (a.h) return set_error(LNFP8_ERR_INVALID_ARG, "%s: h and a checkpoint of it", who);
+      } else {
+        TRY(need(a.h, 16, "h", who));
+      }
     }
     if (a.dw) {
       if (xck) {

@@ -167,6 +167,12 @@ def test_linear_act_refuses_more_tokens_than_its_tiles_count(L, M):
     assert L._c_linear_act_bwd(ctypes.byref(b), None) == 2 and "M" in L.last_error()
 
 
+def test_linear_act_bwd_refuses_both_forms_of_h(L):
+    a = L.CLinearActBwd(M=4, K=64, N=64, act=1, dy=FAKE, x=FAKE, w=FAKE, h=FAKE, h_ckpt=ck(L), dx=FAKE, dw=FAKE, workspace=FAKE,
+                        workspace_bytes=1 << 40)
+    assert L._c_linear_act_bwd(ctypes.byref(a), None) == 1 and "h and a checkpoint" in L.last_error()
+
+
 STRUCTS = {"lnfp8_ckpt": "CCkpt", "lnfp8_layernorm_fwd_args": "CLayerNormFwd", "lnfp8_layernorm_bwd_args": "CLayerNormBwd",
            "lnfp8_linear_act_fwd_args": "CLinearActFwd", "lnfp8_linear_act_bwd_args": "CLinearActBwd"}
 
