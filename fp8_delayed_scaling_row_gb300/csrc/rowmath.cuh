@@ -381,21 +381,10 @@ __device__ __forceinline__ float act_fwd(float z, int act) {
   return z;
 }
 
-__device__ __forceinline__ float act_slope(float z, int act) {
-  if (act == LNFP8_ACT_GELU) {
-    const float z2 = fminf(z * z, 1e30f);  // finite, so that the vanished s (1 - s) wins far out
-    const float s = logistic_neg2(z * (-kLog2e * kGelu2K - kLog2e * kGelu2KC * z2));
-    return s + z * (s * (1.0f - s)) * (kGelu2K + 3.0f * kGelu2KC * z2);
-  }
-  if (act == LNFP8_ACT_SILU) {
-    const float s = logistic_neg2(-kLog2e * z);
-    return s + z * (s * (1.0f - s));
-  }
-  if (act == LNFP8_ACT_RELU) return z > 0.f ? 1.0f : 0.f;
-  return 1.0f;
-}
+// relu'(z); a NaN stays one (a lost pre-activation must not pass for an inactive one)
+__device__ __forceinline__ float relu_slope(float z) { return z > 0.f ? 1.0f : (z != z ? z : 0.f); }
 
-// The same for 8 values as 4 pairs. s(u) of a pair takes one reciprocal, of the product
+// act_fwd and the slopes of 8 values as 4 pairs. s(u) of a pair takes one reciprocal, of the product
 // (1 + e^-u0)(1 + e^-u1), while the products stay in range: kernels that pass over a tensor once are
 // bound by the special-function unit otherwise (16 a clock per SM: 2 per value are 58 us for the
 // 134 M values of 16384 x 8192, as long as their bytes take).
@@ -453,11 +442,11 @@ __device__ __forceinline__ void act8(uint64_t* z) {
 // FAR: z may be so large that its square leaves fp32.
 template <int ACT, bool FAR>
 __device__ __forceinline__ void slope8(const uint64_t* z, uint64_t* out) {
-  if constexpr (ACT == LNFP8_ACT_RELU || ACT == LNFP8_ACT_NONE) {
+  if constexpr (ACT == LNFP8_ACT_RELU) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float2 t = upk(z[k]);
-      out[k] = pk(act_slope(t.x, ACT), act_slope(t.y, ACT));
+      out[k] = pk(relu_slope(t.x), relu_slope(t.y));
     }
   } else {
     uint64_t nu[4], s[4], zz[4];
@@ -467,7 +456,7 @@ __device__ __forceinline__ void slope8(const uint64_t* z, uint64_t* out) {
       zz[k] = mul_2(z[k], z[k]);
       if constexpr (FAR) {
         const float2 t = upk(zz[k]);
-        zz[k] = pk(fminf(t.x, 1e30f), fminf(t.y, 1e30f));  // see act_slope
+        zz[k] = pk(fminf(t.x, 1e30f), fminf(t.y, 1e30f));  // finite, so that the vanished s (1 - s) wins far out
       }
       nu[k] = ACT == LNFP8_ACT_GELU ? gelu_nu2(z[k], zz[k]) : mul_2(z[k], pk(-kLog2e, -kLog2e));
     }

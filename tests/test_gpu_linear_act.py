@@ -261,6 +261,20 @@ def test_nan_and_inf_stay_in_their_rows(L):
         assert torch.isnan(back[1:3]).all() and torch.isfinite(back[keep]).all()
 
 
+@pytest.mark.parametrize("act", ["gelu", "relu", "silu"])
+def test_nan_pre_activations_reach_the_gradients(L, act):
+    """A pre-activation that was NaN, or whose checkpoint block holds an Inf, must not pass for a zero slope."""
+    for M in (8, 300):
+        h = draw(M, 64, torch.bfloat16, 1)
+        h[1, 3], h[2, 40] = float("nan"), float("inf")
+        ck = L.act_ckpt_save(h)
+        dy, w = torch.ones_like(h), torch.eye(64, dtype=torch.bfloat16, device="cuda")
+        g = L.linear_act_bwd(dy, h, w, L.LinearActCtx(act=act, h=h))
+        assert torch.isnan(g.dbias[3]) and torch.isnan(g.dx[1]).all() and torch.isfinite(g.dx[3:]).all()
+        g = L.linear_act_bwd(dy, h, w, L.LinearActCtx(act=act, ckpt=ck))
+        assert torch.isnan(g.dbias).all() and torch.isnan(g.dx[1:3]).all() and torch.isfinite(g.dx[3:]).all()
+
+
 def test_far_out_pre_activations(L):
     """Slopes and values where e^-u and z^2 leave fp32."""
     h = torch.tensor([[0.0, -0.0, 20.0, -20.0, 1e4, -1e4, 1e20, -1e20] * 2], dtype=torch.bfloat16, device="cuda")
