@@ -242,6 +242,18 @@ def test_stream_and_graph(L):
     assert all(torch.equal(a, b) for a, b in zip(got, step()))
 
 
+def test_binding_refuses_workspaces_it_cannot_use(L):
+    x = draw(4, 64, torch.bfloat16, 1)
+    gamma, beta = params(64, torch.bfloat16)
+    _, ctx = L.layernorm_fwd(x, gamma, beta)
+    for ws, err in ((torch.empty(1 << 20, dtype=torch.uint8), TypeError),
+                    (torch.empty(1, dtype=torch.uint8, device="cuda").expand(1 << 20), ValueError)):
+        g = L.layernorm_grads(4, 64)
+        g.workspace = ws
+        with pytest.raises(err, match="workspace"):
+            L.layernorm_bwd(x, ctx, gamma, grads=g)
+
+
 def test_binding_refuses(L):
     x = draw(4, 64, torch.bfloat16, 1)
     gamma, beta = params(64, torch.bfloat16)

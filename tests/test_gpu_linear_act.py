@@ -312,6 +312,17 @@ def test_stream_and_graph(L):
     L.sync_status()
 
 
+def test_binding_refuses_workspaces_it_cannot_use(L):
+    x, w = draw(8, 64, torch.bfloat16, 1), draw(32, 64, torch.bfloat16, 2)
+    dy = draw(8, 32, torch.bfloat16, 3)
+    for ws, err in ((torch.empty(1 << 20, dtype=torch.uint8), TypeError),
+                    (torch.empty(1, dtype=torch.uint8, device="cuda").expand(1 << 20), ValueError)):
+        g = L.linear_act_grads(8, 64, 32)
+        g.workspace = ws
+        with pytest.raises(err, match="workspace"):
+            L.linear_act_bwd(dy, x, w, L.LinearActCtx(), grads=g)
+
+
 def test_binding_refuses(L):
     x, w = draw(8, 64, torch.bfloat16, 1), draw(32, 64, torch.bfloat16, 2)
     for call in (lambda: L.linear_act_fwd(x.float(), w.float()), lambda: L.linear_act_fwd(x, w.half()), lambda: L.linear_act_fwd(x.cpu(), w)):
