@@ -707,7 +707,7 @@ def _flat(t, name, shape, dtype, dev) -> None:
         raise ValueError(f"{name} is not contiguous")
 
 
-def _ws(t, dev):
+def _given_ws(t, dev):
     """A workspace's address and bytes (all of them there: contiguous)."""
     if t is None:
         return None, 0
@@ -904,7 +904,7 @@ def layernorm_bwd(dy, ctx: LayerNormCtx, gamma, *, dresidual=None, grads: LayerN
         lddx = _rows(grads.dx, "grads.dx", M, D, dt, dev)
         _flat(grads.dgamma, "grads.dgamma", (D,), torch.float32, dev)
         _flat(grads.dbeta, "grads.dbeta", (D,), torch.float32, dev)
-    ws, ws_bytes = _ws(grads.workspace, dev)
+    ws, ws_bytes = _given_ws(grads.workspace, dev)
     a = CLayerNormBwd(M, D, elem, pe, dy.data_ptr(), x, mu, ctx.rsigma.data_ptr(), ck, gamma.data_ptr(), _ptr(dresidual),
                       grads.dx.data_ptr(), grads.dgamma.data_ptr(), grads.dbeta.data_ptr(), ws, ws_bytes, lddy, ldx,
                       lddr, lddx)
@@ -1040,7 +1040,7 @@ def linear_act_bwd(dy, x, w, ctx: LinearActCtx, *, x_act="none", x_gamma=None, x
             _flat(grads.dw, "grads.dw", (N, K), dt, dev)
         if grads.dbias is not None:
             _flat(grads.dbias, "grads.dbias", (N,), torch.float32, dev)
-    ws, ws_bytes = _ws(grads.workspace, dev)
+    ws, ws_bytes = _given_ws(grads.workspace, dev)
     a = CLinearActBwd(M, K, N, elem, ia, dy.data_ptr(), xp, xck, _act(x_act), _ptr(x_gamma), _ptr(x_beta), w.data_ptr(), h,
                       hck, _ptr(grads.dx), _ptr(grads.dw), _ptr(grads.dbias), ws, ws_bytes, lddy, ldx, lddx)
     _check(_c_linear_act_bwd(C.byref(a), _raw_stream(dev)))

@@ -224,6 +224,24 @@ def test_strides_and_neighbours(L, M, K, N):
     assert torch.equal(g.dx, want.dx) and torch.equal(g.dw, want.dw) and torch.equal(g.dbias, want.dbias)
 
 
+def test_offsets_past_32_bits(L):
+    """2.2e9 elements of y, h and dz: the last rows as those of a call of their own (whole numbers: no order matters)."""
+    M, K, N, tail = 270001, 64, 8192, 300
+    x, w = whole(M, K, torch.bfloat16, 1), whole(N, K, torch.bfloat16, 2)
+    y, ctx = L.linear_act_fwd(x, w, act="relu", save="ckpt")
+    y2, ctx2 = L.linear_act_fwd(x[-tail:], w, act="relu", save="ckpt")
+    assert torch.equal(y[-tail:], y2) and torch.equal(ctx.ckpt.codes[-tail:], ctx2.ckpt.codes)
+    assert torch.equal(ctx.ckpt.scales[-tail:], ctx2.ckpt.scales)
+    del y, y2
+    dy = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
+    dy[-tail:] = whole(tail, N, torch.bfloat16, 3)
+    g = L.linear_act_bwd(dy, x, w, ctx)
+    g2 = L.linear_act_bwd(dy[-tail:], x[-tail:], w, ctx2)
+    assert torch.equal(g.dx[-tail:], g2.dx) and not g.dx[:-tail].any()
+    assert torch.equal(g.dw, g2.dw) and torch.equal(g.dbias, g2.dbias)
+    L.sync_status()
+
+
 def test_some_gradients_only(L):
     """What is not asked for is left out. How many pieces K is cut into depends on which products a launch holds, so
     a gradient asked for alone is another sum of the same terms: each is within sum_error of the exact one and half
