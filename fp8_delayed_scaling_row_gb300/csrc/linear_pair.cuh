@@ -389,8 +389,8 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
       }
       if constexpr (EPI == LIN_FULL) {
         if (p.ck >= 0 && row_ok && nh < pr.N) {  // the four (or, at the edge, fewer) blocks' bytes, one word of the row
-          if constexpr (CHUNKS == 4) *reinterpret_cast<uint32_t*>(p.scales + (int64_t)m * p.pitch + (nh >> 5)) = scale_word;
-          else *reinterpret_cast<uint16_t*>(p.scales + (int64_t)m * p.pitch + (nh >> 5)) = (uint16_t)scale_word;
+          static_assert(CHUNKS == 4);
+          *reinterpret_cast<uint32_t*>(p.scales + (int64_t)m * p.pitch + (nh >> 5)) = scale_word;
         }
       }
       acc_phase ^= 1;
