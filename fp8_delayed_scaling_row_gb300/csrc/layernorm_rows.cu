@@ -22,14 +22,15 @@ namespace {
 
 constexpr int kMaxD = 16384;
 
-// Sums of two values over a warp in 6 shuffles: the halves of the warp first swap, so that each
+// Sums of two values over W neighbouring lanes (a warp: in 6 shuffles): the halves first swap, so that each
 // goes on with one of the two.
+template <int W = 32>
 __device__ __forceinline__ float2 warp_sum2(float a, float b) {
-  const bool hi = (threadIdx.x & 16) != 0;
-  float v = (hi ? b : a) + __shfl_xor_sync(0xFFFFFFFFu, hi ? a : b, 16);
+  const bool hi = (threadIdx.x & (W / 2)) != 0;
+  float v = (hi ? b : a) + __shfl_xor_sync(0xFFFFFFFFu, hi ? a : b, W / 2);
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  const float w = __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+  for (int o = W / 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  const float w = __shfl_xor_sync(0xFFFFFFFFu, v, W / 2);
   return hi ? make_float2(w, v) : make_float2(v, w);
 }
 
@@ -43,8 +44,8 @@ __device__ __forceinline__ void group_sync() {
 }
 template <int TPR>
 __device__ __forceinline__ float2 row_sum2(float a, float b, float2* xch, int& turn) {
-  const float2 s = warp_sum2(a, b);
-  if constexpr (TPR == 32) {
+  const float2 s = warp_sum2<TPR < 32 ? TPR : 32>(a, b);
+  if constexpr (TPR <= 32) {
     return s;
   } else {
     constexpr int W = TPR / 32;
@@ -68,8 +69,13 @@ __device__ __forceinline__ float2 row_sum2(float a, float b, float2* xch, int& t
 }
 template <int TPR>
 __device__ __forceinline__ float row_sum(float a, float2* xch, int& turn) {
+  if constexpr (TPR < 32) {
+#pragma unroll
+    for (int o = TPR / 2; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+    return a;
+  }
   a = warp_sum(a);
-  if constexpr (TPR == 32) {
+  if constexpr (TPR <= 32) {
     return a;
   } else {
     constexpr int W = TPR / 32;
@@ -124,7 +130,9 @@ struct LnBwdParams {
 // ------------------------------------------------------------ any width, any alignment
 // A group of TPR threads owns a row; thread t holds columns t, t + TPR, ... (so that a warp reads 32
 // neighbours and a checkpoint block is one warp's value i). Addresses are one pointer per tensor
-// and row, the columns compile-time offsets. HOLD: gamma and beta stay in registers.
+// and row, the columns compile-time offsets. A column or row that a thread does not have is replaced by one that
+// exists, and its value by zero, so that no load waits for a condition. Bound by a row's latency: nothing is copied
+// ahead. 8191 x 1001 fp16: forward 12 us, backward 46 -> 20. HOLD: gamma and beta stay in registers.
 template <int ELEM, int TPR, int NE, bool CK>  // CK: with a checkpoint
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
 ln_fwd_any_kernel(const LnFwdParams p) {
@@ -137,6 +145,7 @@ ln_fwd_any_kernel(const LnFwdParams p) {
   const int g = threadIdx.x / TPR, t = threadIdx.x % TPR;
   const float inv_d = 1.0f / (float)p.D;
   const int n = (p.D - t + TPR - 1) / TPR;  // this thread's columns (0 or fewer: none)
+  const int tc = min(t, p.D - 1);           // a column to load in place of those it has not
   float ga[HOLD ? NE : 1], be[HOLD ? NE : 1];
   if constexpr (HOLD) {
 #pragma unroll
@@ -152,15 +161,22 @@ ln_fwd_any_kernel(const LnFwdParams p) {
     const bool active = row < p.M;
     float v[NE];
     float s = 0.f;
-    const uint8_t* xr = static_cast<const uint8_t*>(p.x) + (row * p.ldx + t) * ES;
+    const int64_t rowc = active ? row : p.M - 1;
+    const uint8_t* xr = static_cast<const uint8_t*>(p.x) + (rowc * p.ldx + tc) * ES;
+    uint32_t xb[NE];
 #pragma unroll
-    for (int i = 0; i < NE; ++i) v[i] = active && i < n ? load_elem<ELEM>(xr, TPR * i) : 0.f;
-    if (p.resid) {
-      const uint8_t* rr = static_cast<const uint8_t*>(p.resid) + (row * p.ldr + t) * ES;
+    for (int i = 0; i < NE; ++i) xb[i] = load_bits<ELEM>(xr, i < n ? TPR * i : 0);
+    if (!p.resid) {
+#pragma unroll
+      for (int i = 0; i < NE; ++i) v[i] = active && i < n ? bits_value<ELEM>(xb[i]) : 0.f;
+    } else {
+      const uint8_t* rr = static_cast<const uint8_t*>(p.resid) + (rowc * p.ldr + tc) * ES;
+      uint32_t rb[NE];
+#pragma unroll
+      for (int i = 0; i < NE; ++i) rb[i] = load_bits<ELEM>(rr, i < n ? TPR * i : 0);
       uint8_t* hr = static_cast<uint8_t*>(p.xsum) + (row * p.D + t) * ES;
 #pragma unroll
-      for (int i = 0; i < NE; ++i)  // every load before the first store, which they could not pass
-        if (active && i < n) v[i] = round_elem<ELEM>(v[i] + load_elem<ELEM>(rr, TPR * i));
+      for (int i = 0; i < NE; ++i) v[i] = active && i < n ? round_elem<ELEM>(bits_value<ELEM>(xb[i]) + bits_value<ELEM>(rb[i])) : 0.f;
 #pragma unroll
       for (int i = 0; i < NE; ++i)
         if (active && i < n) store_elem<ELEM>(hr, TPR * i, v[i]);
@@ -212,17 +228,24 @@ ln_bwd_any_kernel(const LnBwdParams p) {
   constexpr int kThreads = TPR < 256 ? 256 : TPR, ES = ElemSize<ELEM>::value;
   constexpr int GPB = kThreads / TPR;
   __shared__ float2 xch[2 * kThreads / 32];
-  extern __shared__ float colred[];  // [2][D], only with several row groups
+  // [2][D]: where several row groups add their column sums, or, with more than 8 columns a thread, where the
+  // sums are kept from the start (in registers 2048 x 16384 spilled and took 318 us)
+  extern __shared__ float colred[];
+  constexpr bool SACC = NE > 8;
   pdl_wait();
   pdl_launch_dependents();
   const int g = threadIdx.x / TPR, t = threadIdx.x % TPR;
   const float inv_d = 1.0f / (float)p.D;
-  const int n = (p.D - t + TPR - 1) / TPR;
+  const int n = (p.D - t + TPR - 1) / TPR, tc = min(t, p.D - 1);
   constexpr bool HOLD = NE <= 8;  // gamma in registers
-  float accg[NE], accb[NE], ga[HOLD ? NE : 1];
+  float accg[SACC ? 1 : NE], accb[SACC ? 1 : NE], ga[HOLD ? NE : 1];
 #pragma unroll
   for (int i = 0; i < NE; ++i) {
-    accg[i] = accb[i] = 0.f;
+    if constexpr (SACC) {
+      if (i < n) colred[t + TPR * i] = colred[p.D + t + TPR * i] = 0.f;
+    } else {
+      accg[i] = accb[i] = 0.f;
+    }
     if constexpr (HOLD)
       if (i < n) ga[i] = load_elem_rt(p.gamma, p.param_elem, t + TPR * i);
   }
@@ -230,39 +253,49 @@ ln_bwd_any_kernel(const LnBwdParams p) {
   for (int64_t row0 = (int64_t)blockIdx.x * GPB; row0 < p.M; row0 += (int64_t)gridDim.x * GPB) {
     const int64_t row = row0 + g;
     const bool active = row < p.M;
-    const float rs = active ? p.rs[row] : 0.f;
-    const float mu = active && !CK ? p.mu[row] : 0.f;
+    const int64_t rowc = active ? row : p.M - 1;
+    const float rs = p.rs[rowc];
+    const float mu = CK ? 0.f : p.mu[rowc];
     float xh[NE], gg[NE];
     float s1 = 0.f, s2 = 0.f;
-    const uint8_t* dr = static_cast<const uint8_t*>(p.dy) + (row * p.lddy + t) * ES;
-    const uint8_t* xr = CK ? p.codes + row * p.D + t : static_cast<const uint8_t*>(p.x) + (row * p.ldx + t) * ES;
-    const uint8_t* sr = p.scales + row * p.pitch + (t >> 5);
-    const uint8_t* rr = static_cast<const uint8_t*>(p.dres) + (row * p.lddres + t) * ES;
-    float res[NE];
+    const uint8_t* dr = static_cast<const uint8_t*>(p.dy) + (rowc * p.lddy + tc) * ES;
+    const uint8_t* xr = CK ? p.codes + rowc * p.D + tc : static_cast<const uint8_t*>(p.x) + (rowc * p.ldx + tc) * ES;
+    const uint8_t* sr = p.scales + rowc * p.pitch + (tc >> 5);
+    uint32_t db[NE], xb[NE], sb[CK ? NE : 1], rb[SACC ? 1 : NE];
 #pragma unroll
     for (int i = 0; i < NE; ++i) {  // every load of the row first
-      xh[i] = gg[i] = res[i] = 0.f;
-      if (active && i < n) {
-        if (p.dres) res[i] = load_elem<ELEM>(rr, TPR * i);
-        gg[i] = load_elem<ELEM>(dr, TPR * i);
-        if constexpr (CK) xh[i] = __uint_as_float((uint32_t)xr[TPR * i] | ((uint32_t)sr[TPR / 32 * i] << 8));
-        else xh[i] = load_elem<ELEM>(xr, TPR * i);
+      const int at = i < n ? TPR * i : 0;
+      db[i] = load_bits<ELEM>(dr, at);
+      if constexpr (CK) {
+        xb[i] = xr[at];
+        sb[i] = sr[at / 32];
+      } else {
+        xb[i] = load_bits<ELEM>(xr, at);
+      }
+    }
+    const uint8_t* rr = static_cast<const uint8_t*>(p.dres) + (rowc * p.lddres + tc) * ES;
+    if constexpr (!SACC) {
+      if (p.dres) {
+#pragma unroll
+        for (int i = 0; i < NE; ++i) rb[i] = load_bits<ELEM>(rr, i < n ? TPR * i : 0);
       }
     }
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
-      if (active && i < n) {
-        if constexpr (CK) {
-          const uint32_t w = __float_as_uint(xh[i]);
-          xh[i] = fp8x2_to_f32(w & 0xFFu, p.dt).x * ckpt_scale(w >> 8);
-        } else {
-          xh[i] = (xh[i] - mu) * rs;
+      const bool in = active && i < n;
+      const float x = CK ? fp8x2_to_f32(xb[i], p.dt).x * ckpt_scale(sb[CK ? i : 0]) : (bits_value<ELEM>(xb[i]) - mu) * rs;
+      const float d = in ? bits_value<ELEM>(db[i]) : 0.f;
+      xh[i] = in ? x : 0.f;
+      if constexpr (SACC) {
+        if (in) {
+          colred[t + TPR * i] = fmaf(d, xh[i], colred[t + TPR * i]);
+          colred[p.D + t + TPR * i] += d;
         }
-        const float d = gg[i];
+      } else {
         accg[i] = fmaf(d, xh[i], accg[i]);
         accb[i] += d;
-        gg[i] = d * (HOLD ? ga[HOLD ? i : 0] : load_elem_rt(p.gamma, p.param_elem, t + TPR * i));
       }
+      gg[i] = in ? d * (HOLD ? ga[HOLD ? i : 0] : load_elem_rt(p.gamma, p.param_elem, tc + (i < n ? TPR * i : 0))) : 0.f;
       s1 += gg[i];
       s2 = fmaf(gg[i], xh[i], s2);
     }
@@ -273,7 +306,9 @@ ln_bwd_any_kernel(const LnBwdParams p) {
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
       if (i >= n) continue;
-      store_elem<ELEM>(orow, TPR * i, fmaf(-mgx, xh[i], gg[i] - mg) * rs + res[i]);
+      const float o = fmaf(-mgx, xh[i], gg[i] - mg) * rs;
+      if constexpr (SACC) store_elem<ELEM>(orow, TPR * i, p.dres ? o + load_elem<ELEM>(rr, TPR * i) : o);
+      else store_elem<ELEM>(orow, TPR * i, p.dres ? o + bits_value<ELEM>(rb[i]) : o);
     }
   }
   // this block's column partials: the row groups add theirs in turn
@@ -297,8 +332,8 @@ ln_bwd_any_kernel(const LnBwdParams p) {
     for (int i = 0; i < NE; ++i) {
       const int c = t + TPR * i;
       if (c >= p.D) continue;
-      part[c] = accg[i];
-      part[p.D + c] = accb[i];
+      part[c] = SACC ? colred[c] : accg[SACC ? 0 : i];
+      part[p.D + c] = SACC ? colred[p.D + c] : accb[SACC ? 0 : i];
     }
   }
 }
@@ -309,8 +344,9 @@ ln_bwd_any_kernel(const LnBwdParams p) {
 // slots of a shared-memory ring, so the bytes in flight cost no registers, and a slot is
 // refilled one row after it was read. Neighbouring lanes hold a checkpoint block. 16 columns a thread
 // measured best (8 or 32, or 96 threads for 768 columns, up to 2x slower backward: fewer columns share a
-// row's reductions, more cost occupancy). bf16, 16384 x 2048, with residual and checkpoint: forward 51 us,
-// 5.9 TB/s, 88% of a copy; backward 44 us with its column sums, 79%.
+// row's reductions, more cost occupancy); up to 256 columns 8 or 16 lanes hold a row, and a warp several
+// (262144 x 128: forward 55 -> 24 us, backward 111 -> 38). bf16, 16384 x 2048, with residual and checkpoint: forward
+// 52 us, 5.8 TB/s, 85% of a copy; backward 44 us with its column sums, 80%.
 // A thread's NV 16-byte words of a row are words t, t + TPR, ... (EPC columns each: 8 of a 16-bit type, 4 of
 // fp32), so that every access of a warp is of whole sectors. HOLD: gamma and beta stay in registers; beyond
 // 16 columns a thread they are read again for each row.
@@ -423,12 +459,12 @@ ln_fwd_vec_kernel(const LnFwdParams p) {
       }
     const float2 qp = upk(q2);
     const float rs = rsqrt_nr(row_sum<TPR>(qp.x + qp.y, xch, turn) * inv_d + p.eps);
-    if (!active) continue;  // uniform over the row group
+    if (TPR >= 32 && !active) continue;  // uniform over the row group; narrower groups meet in the shuffles below
     const uint64_t rs2 = pk(rs, rs);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (t + TPR * j) * EPC;
-      const bool in = c < p.D;
+      const bool in = c < p.D && (TPR >= 32 || active);
 #pragma unroll
       for (int k = 0; k < PP; ++k) v[j][k] = mul_2(v[j][k], rs2);
       if (in) {
@@ -449,7 +485,7 @@ ln_fwd_vec_kernel(const LnFwdParams p) {
         }
       }
     }
-    if (t == 0) {
+    if (t == 0 && (TPR >= 32 || active)) {
       p.mu[row] = mu;
       p.rs[row] = rs;
     }
@@ -493,11 +529,16 @@ ln_bwd_vec_kernel(const LnBwdParams p) {
   // this thread's first word in the row to be loaded next: the pointers run ahead of `row`
   const uint8_t* dp = static_cast<const uint8_t*>(p.dy) + row * p.lddy * ES + t * 16;
   const uint8_t* xp = CK ? p.codes + row * p.D + t * EPC : static_cast<const uint8_t*>(p.x) + row * p.ldx * ES + t * 16;
-  const uint8_t* bp = CK ? p.scales + row * p.pitch + t / (4 * LANES) * 4 : nullptr;  // the word of this one's scale byte
+  // the scale byte of word j is byte t / LANES + TPR / LANES j of the row: in the word at bp + scale_word(j), from bit
+  // byte + scale_byte(j) on
+  constexpr bool kWide = TPR % (4 * LANES) == 0;  // else TPR is 1 or 2 blocks
+  auto scale_word = [](int j) { return kWide ? TPR / LANES * j : TPR / LANES * j / 4 * 4; };
+  auto scale_byte = [](int j) { return kWide ? 0 : TPR / LANES * j % 4 * 8; };
+  const uint8_t* bp = CK ? p.scales + row * p.pitch + t / (4 * LANES) * 4 : nullptr;
   const uint8_t* rp = RES ? static_cast<const uint8_t*>(p.dres) + row * p.lddres * ES + t * 16 : nullptr;
   const float* mp = p.mu + row;
   const float* sp = p.rs + row;
-  static_assert(TPR % (4 * LANES) == 0, "a thread's scale byte has one place in its words");
+  static_assert(kWide || 4 * LANES % TPR == 0, "a group's blocks do not cross a scale word");
   auto issue = [&](int64_t r, uint32_t slot) {
     if (r < p.M) {
       cp4(slot + t4, sp);
@@ -511,7 +552,7 @@ ln_bwd_vec_kernel(const LnBwdParams p) {
           if constexpr (CK) {
             if constexpr (EPC == 8) cp8(slot + tq + j * 8 * T, xp + TPR * j * 8);
             else cp4(slot + tq + j * 4 * T, xp + TPR * j * 4);
-            cp4(slot + t4 + (4 + 4 * j) * T, bp + TPR / LANES * j);
+            cp4(slot + t4 + (4 + 4 * j) * T, bp + scale_word(j));
           }
         }
       }
@@ -589,7 +630,7 @@ ln_bwd_vec_kernel(const LnBwdParams p) {
       uint64_t d[PP];
       unpack_word<ELEM>(du[j], d);
       if constexpr (CK) {
-        const float s = ckpt_scale((sw[j] >> byte) & 0xFFu);
+        const float s = ckpt_scale((sw[j] >> (byte + scale_byte(j))) & 0xFFu);
         if constexpr (EPC == 8) {
           decode8(make_uint2(xu[j].x, xu[j].y), s, p.dt, xh[j]);
         } else {
@@ -641,13 +682,25 @@ ln_bwd_vec_kernel(const LnBwdParams p) {
     slot = slot == base + P * SB ? base : slot + SB;
   }
   cp_wait<0>();
-  // column partials: the row groups add theirs in turn in the ring's memory
+  // column partials: the row groups of a warp by shuffles, then the others in turn in the ring's memory
   float* part = p.part + (int64_t)blockIdx.x * 2 * p.D;
   float* red = reinterpret_cast<float*>(ring);
+  constexpr int TURNS = TPR < 32 ? T / 32 : GPB;
+  if constexpr (TPR < 32) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int k = 0; k < PP; ++k)
+#pragma unroll
+        for (int o = TPR; o < 32; o <<= 1) {
+          accg[j][k] = add_2(accg[j][k], __shfl_xor_sync(0xFFFFFFFFu, accg[j][k], o));
+          accb[j][k] = add_2(accb[j][k], __shfl_xor_sync(0xFFFFFFFFu, accb[j][k], o));
+        }
+  }
 #pragma unroll 1
-  for (int turn_g = 0; turn_g < GPB; ++turn_g) {
-    if constexpr (GPB > 1) __syncthreads();
-    if (g != turn_g) continue;
+  for (int turn_g = 0; turn_g < TURNS; ++turn_g) {
+    if constexpr (TURNS > 1) __syncthreads();
+    if (TPR < 32 ? (int)threadIdx.x >> 5 != turn_g || (threadIdx.x & 31) >= TPR : g != turn_g) continue;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (t + TPR * j) * EPC;
@@ -663,7 +716,7 @@ ln_bwd_vec_kernel(const LnBwdParams p) {
           const float4 o = *reinterpret_cast<const float4*>(red + at_c);
           v = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
         }
-        if (turn_g == GPB - 1) *reinterpret_cast<float4*>(part + at_c) = v;
+        if (turn_g == TURNS - 1) *reinterpret_cast<float4*>(part + at_c) = v;
         else *reinterpret_cast<float4*>(red + at_c) = v;
       }
     }
@@ -672,8 +725,8 @@ ln_bwd_vec_kernel(const LnBwdParams p) {
 
 // Sums over n partial rows of `cols` floats in a fixed order: 32 columns per block, warp w adds rows
 // w, w + 32, ..., then the warps' sums are added over the lanes of a warp. A few hundred rows leave
-// each thread about ten loads, all in flight at once: with 8 warps a block it took 9.9 us for
-// 304 x 1536, cold, against 5.
+// each thread about ten loads, all in flight at once: 304 x 1536, cold, took 9.9 us with 8 warps a
+// block, 8.6 with 32.
 __global__ void __launch_bounds__(1024) colsum_kernel(const float* __restrict__ part, int n, int cols, int split,
                                                       float* __restrict__ a, float* __restrict__ b) {
   __shared__ float red[32][33];
@@ -696,8 +749,11 @@ __global__ void __launch_bounds__(1024) colsum_kernel(const float* __restrict__ 
   }
 }
 
-// Blocks of the backward's row pass: the partial rows it leaves are summed afterwards.
-constexpr int kBwdBlocksPerSm = 2;
+// The most blocks an SM gets of the backward's row pass, each of which leaves a partial row of column sums: two
+// (measured best for the vector kernels), or three of up to 2048 columns, where the kernels of any width are bound by
+// the latency of a row (41654 x 457 bf16 52 us with two, 39 with three).
+int bwd_blocks_per_sm(int64_t D) { return D <= 2048 ? 3 : 2; }
+constexpr int kBwdVecBlocksPerSm = 2;
 
 template <int ELEM, bool CK>
 lnfp8_status fwd_any(const LnFwdParams& p, cudaStream_t st) {
@@ -716,23 +772,30 @@ lnfp8_status fwd_any(const LnFwdParams& p, cudaStream_t st) {
   return go(ln_fwd_any_kernel<ELEM, 1024, 16, CK>, 1024);
 }
 
+template <int ELEM, int TPR, int NE, bool CK>
+lnfp8_status bwd_any_launch(const LnBwdParams& p, int* blocks_out, cudaStream_t st) {
+  constexpr auto kernel = ln_bwd_any_kernel<ELEM, TPR, NE, CK>;
+  constexpr int threads = TPR < 256 ? 256 : TPR, gpb = threads / TPR;
+  constexpr bool sums = gpb > 1 || NE > 8;  // in shared memory
+  int bps = 1;
+  const lnfp8_status s = kernel_setup<kernel>(threads, sums ? 2 * TPR * NE * sizeof(float) : 0, &bps, "layernorm_bwd: kernel set-up");
+  if (s != LNFP8_OK) return s;
+  const int64_t blocks = min64((p.M + gpb - 1) / gpb, (int64_t)num_sms() * std::min(bwd_blocks_per_sm(p.D), bps));
+  *blocks_out = (int)blocks;
+  if (launch_pdl(kernel, dim3((unsigned)blocks), dim3(threads), sums ? 2 * (size_t)p.D * sizeof(float) : 0, st, p) != cudaSuccess)
+    return check_launch("layernorm_bwd launch");
+  return check_launch("layernorm_bwd");
+}
+
 template <int ELEM, bool CK>
 lnfp8_status bwd_any(const LnBwdParams& p, int* blocks_out, cudaStream_t st) {
-  auto go = [&](auto kernel, int tpr) {
-    const int threads = tpr < 256 ? 256 : tpr, gpb = threads / tpr;
-    const size_t smem = gpb > 1 ? 2 * (size_t)p.D * sizeof(float) : 0;
-    const int64_t blocks = min64((p.M + gpb - 1) / gpb, (int64_t)num_sms() * kBwdBlocksPerSm);
-    *blocks_out = (int)blocks;
-    if (launch_pdl(kernel, dim3((unsigned)blocks), dim3(threads), smem, st, p) != cudaSuccess) return check_launch("layernorm_bwd launch");
-    return check_launch("layernorm_bwd");
-  };
-  if (p.D <= 256) return go(ln_bwd_any_kernel<ELEM, 32, 8, CK>, 32);
-  if (p.D <= 512) return go(ln_bwd_any_kernel<ELEM, 64, 8, CK>, 64);
-  if (p.D <= 1024) return go(ln_bwd_any_kernel<ELEM, 128, 8, CK>, 128);
-  if (p.D <= 2048) return go(ln_bwd_any_kernel<ELEM, 256, 8, CK>, 256);
-  if (p.D <= 4096) return go(ln_bwd_any_kernel<ELEM, 512, 8, CK>, 512);
-  if (p.D <= 8192) return go(ln_bwd_any_kernel<ELEM, 1024, 8, CK>, 1024);
-  return go(ln_bwd_any_kernel<ELEM, 1024, 16, CK>, 1024);
+  if (p.D <= 256) return bwd_any_launch<ELEM, 32, 8, CK>(p, blocks_out, st);
+  if (p.D <= 512) return bwd_any_launch<ELEM, 64, 8, CK>(p, blocks_out, st);
+  if (p.D <= 1024) return bwd_any_launch<ELEM, 128, 8, CK>(p, blocks_out, st);
+  if (p.D <= 2048) return bwd_any_launch<ELEM, 256, 8, CK>(p, blocks_out, st);
+  if (p.D <= 4096) return bwd_any_launch<ELEM, 512, 8, CK>(p, blocks_out, st);
+  if (p.D <= 8192) return bwd_any_launch<ELEM, 1024, 8, CK>(p, blocks_out, st);
+  return bwd_any_launch<ELEM, 1024, 16, CK>(p, blocks_out, st);
 }
 
 bool al(const void* p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
@@ -762,6 +825,8 @@ lnfp8_status fwd_vec_launch(const LnFwdParams& p, cudaStream_t st) {
 template <int ELEM, bool CK, bool RES>
 lnfp8_status fwd_vec(const LnFwdParams& p, cudaStream_t st) {
   constexpr int NV = 16 / Word<ELEM>::EPC;
+  if (p.D <= 128) return fwd_vec_launch<ELEM, 8, NV, CK, RES>(p, st);
+  if (p.D <= 256) return fwd_vec_launch<ELEM, 16, NV, CK, RES>(p, st);
   if (p.D <= 512) return fwd_vec_launch<ELEM, 32, NV, CK, RES>(p, st);
   if (p.D <= 1024) return fwd_vec_launch<ELEM, 64, NV, CK, RES>(p, st);
   if (p.D <= 2048) return fwd_vec_launch<ELEM, 128, NV, CK, RES>(p, st);
@@ -779,7 +844,7 @@ lnfp8_status bwd_vec_launch(const LnBwdParams& p, int* blocks_out, cudaStream_t 
   const lnfp8_status s = kernel_setup<kernel>(S::THREADS, S::SMEM, &bps, "layernorm_bwd: kernel set-up");
   if (s != LNFP8_OK) return s;
   constexpr int gpb = S::THREADS / TPR, es = ElemSize<ELEM>::value;
-  const int64_t blocks = min64((p.M + gpb - 1) / gpb, (int64_t)num_sms() * std::min(kBwdBlocksPerSm, bps));
+  const int64_t blocks = min64((p.M + gpb - 1) / gpb, (int64_t)num_sms() * std::min(kBwdVecBlocksPerSm, bps));
   *blocks_out = (int)blocks;
   LnBwdParams q = p;
   q.step = blocks * gpb;
@@ -796,6 +861,8 @@ lnfp8_status bwd_vec_launch(const LnBwdParams& p, int* blocks_out, cudaStream_t 
 template <int ELEM, bool CK, bool RES>
 lnfp8_status bwd_vec(const LnBwdParams& p, int* blocks_out, cudaStream_t st) {
   constexpr int NV = 16 / Word<ELEM>::EPC;
+  if (p.D <= 128) return bwd_vec_launch<ELEM, 8, NV, CK, RES>(p, blocks_out, st);
+  if (p.D <= 256) return bwd_vec_launch<ELEM, 16, NV, CK, RES>(p, blocks_out, st);
   if (p.D <= 512) return bwd_vec_launch<ELEM, 32, NV, CK, RES>(p, blocks_out, st);
   if (p.D <= 1024) return bwd_vec_launch<ELEM, 64, NV, CK, RES>(p, blocks_out, st);
   if (p.D <= 2048) return bwd_vec_launch<ELEM, 128, NV, CK, RES>(p, blocks_out, st);
@@ -829,7 +896,7 @@ int64_t layernorm_max_d() { return kMaxD; }
 
 int64_t layernorm_bwd_ws_bytes(int64_t M, int64_t D) {
   if (M == 0) return 0;
-  return min64(M, (int64_t)num_sms() * kBwdBlocksPerSm) * 2 * D * (int64_t)sizeof(float);
+  return min64(M, (int64_t)num_sms() * bwd_blocks_per_sm(D)) * 2 * D * (int64_t)sizeof(float);
 }
 
 lnfp8_status colsum_launch(const float* part, int n, int cols, int split, float* a, float* b, cudaStream_t st) {

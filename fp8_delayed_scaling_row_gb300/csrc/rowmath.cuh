@@ -28,6 +28,20 @@ __device__ __forceinline__ float load_elem(const void* p, int64_t i) {
   else return bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(p)[i]);
 }
 
+// An element's bits, and their value. Kernels that guard their columns load bits from addresses that are always
+// inside and choose afterwards: loads behind a condition would wait for one another.
+template <int ELEM>
+__device__ __forceinline__ uint32_t load_bits(const void* p, int64_t i) {
+  if constexpr (ELEM == LNFP8_FP32) return reinterpret_cast<const uint32_t*>(p)[i];
+  else return reinterpret_cast<const uint16_t*>(p)[i];
+}
+template <int ELEM>
+__device__ __forceinline__ float bits_value(uint32_t w) {
+  if constexpr (ELEM == LNFP8_FP32) return __uint_as_float(w);
+  else if constexpr (ELEM == LNFP8_FP16) return __half2float(__ushort_as_half((unsigned short)w));
+  else return __uint_as_float(w << 16);
+}
+
 // Parameter vectors (gamma, beta) come in a type of their own, read a few times per block.
 __device__ __forceinline__ float load_elem_rt(const void* p, int elem, int64_t i) {
   if (elem == LNFP8_FP32) return load_elem<LNFP8_FP32>(p, i);

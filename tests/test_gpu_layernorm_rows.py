@@ -143,6 +143,20 @@ def test_backward(L, rows, cols, dtype, ckpt, res):
         assert torch.equal(a, b)
 
 
+# rows of a few lanes (a head's columns), the last of a block's row groups without one, rings that turn more than once;
+# and rows wide enough to keep their column sums elsewhere, several to a block
+MORE = [(1, 8), (33, 16), (70, 24), (100, 64), (259, 72), (131, 128), (70, 136), (133, 200), (1000, 256), (40000, 64), (12001, 128),
+        (700, 9001), (640, 16384)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,cols", MORE)
+@pytest.mark.parametrize("res,ckpt", [(False, False), (True, True), (False, True)])
+def test_narrow_and_wide_rows(L, rows, cols, dtype, res, ckpt):
+    test_forward(L, rows, cols, dtype, res, ckpt)
+    test_backward(L, rows, cols, dtype, ckpt, res)
+
+
 @pytest.mark.parametrize("rows,cols", [(9, 64), (6, 77)])
 def test_backward_against_differences(L, rows, cols):
     """fp32 gradients against central differences of the 64-bit forward: step 1e-5 leaves 1e-9 of truncation,
