@@ -25,6 +25,8 @@
  *     Weights are [out_features, in_features] (the nn.Linear layout).
  *   - Every tensor pointer must be 16-byte aligned. Feature sizes (K, N, D, F)
  *     must be multiples of 16; the token count M may be any value >= 0.
+ *     (The 16- and 32-bit operators at the end of this file state their own
+ *     rules, types and sizes.)
  *   - Work is enqueued on `stream` (NULL = the legacy default stream) and runs
  *     asynchronously. Argument errors are detected before anything is
  *     enqueued and returned synchronously. Asynchronous CUDA errors are
@@ -535,7 +537,9 @@ int lnfp8_ctx_offsets(int op, int64_t M, int64_t D, int64_t F, int64_t* offsets,
  * rows that are multiples of 16 bytes on 16-byte boundaries run faster.
  * linear_act_* moves its tiles with TMA: 16-byte aligned pointers, K and N
  * multiples of 8, row strides multiples of 8 elements.
- * NaN and Inf pass through the arithmetic as IEEE gives them. */
+ * NaN and Inf pass through the arithmetic as IEEE gives them. A workspace
+ * belongs to one call at a time: calls on two streams, or two captured graphs
+ * that may run at the same time, need one each. */
 typedef enum { LNFP8_BF16 = 0, LNFP8_FP16 = 1, LNFP8_FP32 = 2 } lnfp8_elem;
 
 /* Activations: GELU is the tanh form, SILU is z / (1 + e^-z). */
