@@ -241,14 +241,16 @@ lin_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ T
   // the fp32 tile, tokens by features, over the ring (every copy and MMA has completed)
   constexpr int ROWS = SWAP ? BN : 128, COLS = SWAP ? 128 : BN, PITCH = COLS + 4;
   float* tile_f = reinterpret_cast<float*>(smem);
-  if (warp >= 4) {
+  {
+    __syncwarp();  // lane 0 of warps 0 and 1 comes from its loop
     uint32_t never = 0;
     mbar_wait(done_bar, 0, &never);
+    __syncwarp();
     tc_fence_after();
-    const int quarter = warp & 3;
+    const int quarter = warp & 3;  // a warp's lanes of tensor memory; the two warps of a quarter take every other chunk
     const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16);
 #pragma unroll 1
-    for (int c = 0; c < BN; c += 16) {
+    for (int c = (warp >> 2) * 16; c < BN; c += 32) {
       uint32_t r[16];
       if (kb1 > kb0) tmem_ld16(t0 + c, r);
       else
@@ -270,36 +272,51 @@ lin_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ T
 
   const int rows = ROWS / S;  // of this CTA; a multiple of 32 items in all
   constexpr int CH = COLS / 8;
-  for (int i = threadIdx.x; i < rows * CH; i += kTileThreads) {
-    const int r = piece * rows + i / CH, c = (i % CH) * 8;
-    float v[8];
-    const uint32_t at = ring + (uint32_t)(r * PITCH + c) * 4u;
+  constexpr int kMostPieces = PAIR ? 2 : 4, U = PAIR ? 2 : 1;  // U items of a thread together
+  for (int i0 = threadIdx.x; i0 < rows * CH; i0 += U * kTileThreads) {
+    // every piece's words first: loads from another SM's shared memory take most of a microsecond
+    float4 a[U][kMostPieces], b[U][kMostPieces];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = 0.f;
-    for (int s = 0; s < S; ++s) {
-      float4 a, b;
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kTileThreads, r = piece * rows + i / CH, c = (i % CH) * 8;
+      if (i >= rows * CH) break;
       if (S > 1) {
-        const uint32_t ra = map_to_rank(at, s * SIDES + side);
-        a = ld_cluster_f4(ra);
-        b = ld_cluster_f4(ra + 16);
+        const uint32_t at = ring + (uint32_t)(r * PITCH + c) * 4u;
+#pragma unroll
+        for (int s = 0; s < kMostPieces; ++s) {
+          if (s >= S) break;
+          const uint32_t ra = map_to_rank(at, s * SIDES + side);
+          a[u][s] = ld_cluster_f4(ra);
+          b[u][s] = ld_cluster_f4(ra + 16);
+        }
       } else {
-        a = *reinterpret_cast<const float4*>(tile_f + r * PITCH + c);
-        b = *reinterpret_cast<const float4*>(tile_f + r * PITCH + c + 4);
+        a[u][0] = *reinterpret_cast<const float4*>(tile_f + r * PITCH + c);
+        b[u][0] = *reinterpret_cast<const float4*>(tile_f + r * PITCH + c + 4);
       }
-      v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-      v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
     }
-    const int m = (SWAP ? q0 : p0) + r, n = (SWAP ? p0 : q0) + c;
-    epilogue8(pr.e, v, m, n, m < pr.e.M && n < pr.e.N);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kTileThreads, r = piece * rows + i / CH, c = (i % CH) * 8;
+      if (i >= rows * CH) break;  // uniform over the warp
+      float v[8] = {a[u][0].x, a[u][0].y, a[u][0].z, a[u][0].w, b[u][0].x, b[u][0].y, b[u][0].z, b[u][0].w};
+#pragma unroll
+      for (int s = 1; s < kMostPieces; ++s) {
+        if (s >= S) break;
+        v[0] += a[u][s].x; v[1] += a[u][s].y; v[2] += a[u][s].z; v[3] += a[u][s].w;
+        v[4] += b[u][s].x; v[5] += b[u][s].y; v[6] += b[u][s].z; v[7] += b[u][s].w;
+      }
+      const int m = (SWAP ? q0 : p0) + r, n = (SWAP ? p0 : q0) + c;
+      epilogue8(pr.e, v, m, n, m < pr.e.M && n < pr.e.N);
+    }
   }
   tc_fence_before();
   __syncthreads();
-  if (clustered) cluster_sync_all();  // nobody leaves while its tile may be read, nor frees the pair's tensor memory
+  if (clustered) cluster_sync_relaxed();  // nobody leaves while its tile may be read, nor frees the pair's tensor memory
   if (warp == 1) {
     tc_fence_after();
     tmem_free<PAIR>(tmem, C::TMEM_COLS);
   }
-  if constexpr (PAIR) cluster_sync_all();
+  if constexpr (PAIR) cluster_sync_relaxed();
 }
 
 // ------------------------------------------------------------ a few tokens

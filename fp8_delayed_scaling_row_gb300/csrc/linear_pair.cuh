@@ -301,7 +301,7 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
         __syncwarp();  // rows past M took other branches
         uint32_t rr[32];
         tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * BN + half * HALF + ch * 32), rr);
-        if (ch == CHUNKS - 1) {
+        if (ch == CHUNKS - 1 && t + 2 * ncl < tiles) {  // someone waits for it: nothing is in flight when the CTA leaves
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_remote(tempty);
@@ -399,12 +399,12 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
 
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();  // both CTAs are done with the pair's tensor memory
+  cluster_sync_relaxed();  // both CTAs are done with the pair's tensor memory
   if (warp == 1) {
     tc_fence_after();
     tmem_free<true>(tmem, C::TMEM_COLS);
   }
-  cluster_sync_all();  // nobody leaves while the peer may still signal its barriers
+  cluster_sync_relaxed();  // nobody leaves while the peer may still signal its barriers
 }
 
 // One product (EPI LIN_FULL), or one or two (LIN_PLAIN).
