@@ -153,7 +153,7 @@ lin_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ T
   auto full_bar = [&](int s) { return bars + 8u * s; };
   auto empty_bar = [&](int s) { return bars + 8u * (STAGES + s); };
   const uint32_t done_bar = bars + 8u * (2 * STAGES);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int S = p.splits;
   const bool clustered = S * SIDES > 1;
 
@@ -173,11 +173,11 @@ lin_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ T
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = misc[1];
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, misc[1], 0);
   pdl_wait();
   pdl_launch_dependents();
 
-  const int crank = clustered ? (int)cluster_rank() : 0;
+  const int crank = blockIdx.x % (S * SIDES);  // in the cluster
   const int side = PAIR ? crank & 1 : 0, piece = crank / SIDES, leader = crank - side;
   const int cl = blockIdx.x / (S * SIDES), which = cl >= p.prob[0].clusters ? 1 : 0;
   const TileProb& pr = p.prob[which];
@@ -188,7 +188,8 @@ lin_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ T
   const bool p_mn = pr.p_mn != 0;
   const uint16_t both = (uint16_t)(3u << leader);
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
+    const bool one = elect_one();
     int stage = 0;
     uint32_t phase = 0;
     int issued = 0;
@@ -198,51 +199,61 @@ lin_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ T
       else tma_load(dst, tm, x, y, bar);
     };
     const int qs = q0 + side * (BN / 2);  // the rows of Q this CTA loads
+    const uint32_t fb0 = PAIR ? map_to_rank(full_bar(0), leader) : full_bar(0);
     for (int kb = kb0; kb < kb1; ++kb) {
-      if (!mbar_wait(empty_bar(stage), phase ^ 1, abort_flag)) { ok = false; break; }
-      const uint32_t pd = ring + stage * C::STAGE, qd = pd + C::P_BYTES;
-      const uint32_t fb = PAIR ? map_to_rank(full_bar(stage), leader) : full_bar(stage);
-      if (side == 0) mbar_expect_tx(full_bar(stage), SIDES * C::STAGE);
-      if (!p_mn) load(pd, tmP, kb * BK, p0, fb);
-      else {
-        load(pd, tmP, p0, kb * BK, fb);
-        load(pd + 8192, tmP, p0 + 64, kb * BK, fb);
-      }
-      if constexpr (!Q_MN) load(qd, tmQ, kb * BK, qs, fb);
-      else
+      if (!mbar_wait_warp(empty_bar(stage), phase ^ 1, abort_flag)) { ok = false; break; }
+      if (one) {
+        const uint32_t pd = ring + stage * C::STAGE, qd = pd + C::P_BYTES;
+        const uint32_t fb = fb0 + 8u * stage;
+        if (side == 0) mbar_expect_tx(full_bar(stage), SIDES * C::STAGE);
+        if (!p_mn) load(pd, tmP, kb * BK, p0, fb);
+        else {
+          load(pd, tmP, p0, kb * BK, fb);
+          load(pd + 8192, tmP, p0 + 64, kb * BK, fb);
+        }
+        if constexpr (!Q_MN) load(qd, tmQ, kb * BK, qs, fb);
+        else
 #pragma unroll
-        for (int j = 0; j < BN / SIDES / 64; ++j) load(qd + j * 8192, tmQ, qs + 64 * j, kb * BK, fb);
+          for (int j = 0; j < BN / SIDES / 64; ++j) load(qd + j * 8192, tmQ, qs + 64 * j, kb * BK, fb);
+      }
+      __syncwarp();
       ++issued;
       if (++stage == STAGES) { stage = 0; phase ^= 1; }
     }
-    if (!ok && side == 0)
+    if (!ok && side == 0 && one)
       for (int i = min(issued, STAGES); i > 0; --i) {  // copies in flight land before the CTA leaves
         if (--stage < 0) { stage = STAGES - 1; phase ^= 1; }
         mbar_drain(full_bar(stage), phase);
       }
-  } else if (warp == 1 && lane == 0 && side == 0) {
+    __syncwarp();
+  } else if (warp == 1 && side == 0) {
+    const bool one = elect_one();
     int stage = 0;
     uint32_t phase = 0;
     const MatDesc pdesc = mat_desc(ring, p_mn), qdesc = mat_desc(ring + C::P_BYTES, Q_MN);
+    const uint32_t idesc = pr.idesc;
     for (int kb = kb0; kb < kb1; ++kb) {
-      if (!mbar_wait(full_bar(stage), phase, abort_flag)) break;
+      if (!mbar_wait_warp(full_bar(stage), phase, abort_flag)) break;
       tc_fence_after();
-      const uint32_t off = stage * (C::STAGE >> 4);
+      if (one) {
+        const uint32_t off = stage * (C::STAGE >> 4);
 #pragma unroll
-      for (int kk = 0; kk < BK / 16; ++kk)
-        mma_16bit<PAIR>(tmem, mat_desc64(pdesc.lo + off + kk * pdesc.k_step), mat_desc64(qdesc.lo + off + kk * qdesc.k_step), pr.idesc,
-                        kk != 0 || kb != kb0);
-      mma_commit<PAIR>(empty_bar(stage), both);
+        for (int kk = 0; kk < BK / 16; ++kk)
+          mma_16bit<PAIR>(tmem, mat_desc64(pdesc.lo + off + kk * pdesc.k_step), mat_desc64(qdesc.lo + off + kk * qdesc.k_step), idesc,
+                          kk != 0 || kb != kb0);
+        mma_commit<PAIR>(empty_bar(stage), both);
+      }
+      __syncwarp();
       if (++stage == STAGES) { stage = 0; phase ^= 1; }
     }
-    mma_commit<PAIR>(done_bar, both);  // after an abort too: no MMA outlives the CTA
+    if (one) mma_commit<PAIR>(done_bar, both);  // after an abort too: no MMA outlives the CTA
+    __syncwarp();
   }
 
   // the fp32 tile, tokens by features, over the ring (every copy and MMA has completed)
   constexpr int ROWS = SWAP ? BN : 128, COLS = SWAP ? 128 : BN, PITCH = COLS + 4;
   float* tile_f = reinterpret_cast<float*>(smem);
   {
-    __syncwarp();  // lane 0 of warps 0 and 1 comes from its loop
     uint32_t never = 0;
     mbar_wait(done_bar, 0, &never);
     __syncwarp();
@@ -738,6 +749,7 @@ bool takes_swap(const LinGemm& g) { return g.M <= 128 && !g.a_mn; }
 // two pieces 9.6; at 512 x 2048 x 2048 15.8 and 12.0; at 2048 x 2048 x 2048 18.1 and 46.8.
 struct LinPlan {
   int bn, S;  // bn 0: the persistent kernel
+  int tile;   // its columns
 };
 // K blocks of the pair with the most: the list of units, longest first, dealt out forwards and backwards.
 int64_t longest_pair(const int64_t* units, const int64_t* kb, int count, int64_t pairs) {
@@ -773,13 +785,13 @@ LinPlan lin_plan(LinGemm* g, int count) {
     t128 += m2 * ((g[i].N + 127) / 128);
   }
   int64_t cost = longest_pair(units, kb, count, pairs) * 340 + 6200;
-  LinPlan best = {0, 1};
+  LinPlan best = {0, 1, 256};
   auto offer = [&](int bn, int S, int64_t tiles, int64_t per_kb, int64_t fixed) {
     if (min_kb < 2 * S) return;
     const int64_t fit = max64(S == 1 ? pairs : pairs * 36 / 76, 1), c = (tiles + fit - 1) / fit * ((max_kb + S - 1) / S * per_kb + fixed);
     if (c < cost) {
       cost = c;
-      best = {bn, S};
+      best = {bn, S, 0};
     }
   };
   offer(128, 1, t128, 260, 6700);
@@ -795,7 +807,7 @@ LinPlan lin_plan(LinGemm* g, int count) {
     const int64_t c = longest_pair(u, k, count, pairs) * 340 + 6200 + 4000 + g[i].pieces * g[i].M * g[i].N * 8 / 4000;
     if (c < cost) {
       cost = c;
-      best = {0, 1};
+      best = {0, 1, 256};
       pieces = true;
     }
   }
@@ -858,7 +870,7 @@ lnfp8_status lin_gemm_launch(const LinGemm* g, int count, cudaStream_t st) {
     if (takes_swap(*g)) return swap_launch(*g, st);
     LinGemm one = *g;
     const LinPlan pl = lin_plan(&one, 1);
-    if (pl.bn == 0) return pair_launch<256, LIN_FULL>(g, 1, st);
+    if (pl.bn == 0) return pl.tile == 64 ? pair_launch<64, LIN_FULL>(g, 1, st) : pl.tile == 128 ? pair_launch<128, LIN_FULL>(g, 1, st) : pair_launch<256, LIN_FULL>(g, 1, st);
     return pl.bn == 256 ? tile_launch<256, true, false, false>(g, 1, pl.S, st) : tile_launch<128, true, false, false>(g, 1, pl.S, st);
   }
   // the backward: what few tokens leave swapped runs alone, the rest in one launch
@@ -875,7 +887,7 @@ lnfp8_status lin_gemm_launch(const LinGemm* g, int count, cudaStream_t st) {
   if (n == 0) return LNFP8_OK;
   const LinPlan pl = lin_plan(rest, n);
   if (pl.bn == 0) {
-    lnfp8_status s = pair_launch<256, LIN_PLAIN>(rest, n, st);
+    lnfp8_status s = pl.tile == 128 ? pair_launch<128, LIN_PLAIN>(rest, n, st) : pair_launch<256, LIN_PLAIN>(rest, n, st);
     for (int i = 0; i < n && s == LNFP8_OK; ++i)
       if (rest[i].pieces > 1) s = join_launch(rest[i], st);
     return s;

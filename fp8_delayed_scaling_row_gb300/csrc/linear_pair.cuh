@@ -35,7 +35,7 @@ struct PairCfg {
   static constexpr int STAGES = (232448 - 1024 - 256) / STAGE;
   static constexpr int BAR_OFF = STAGES * STAGE;
   static constexpr int SMEM = 1024 + BAR_OFF + 256;
-  static constexpr int TMEM_COLS = 512;
+  static constexpr int TMEM_COLS = 2 * BN;
   static_assert(STAGES >= 4 && SMEM <= 232448, "shared memory budget");
 };
 
@@ -156,6 +156,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ PairParams p) {
   using C = PairCfg<BN>;
   constexpr bool B_MN = EPI == LIN_PLAIN;
+  static_assert(!B_MN || BN >= 128, "a CTA's half of an MN-major tile is whole boxes of 64 columns");
   constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -170,7 +171,7 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
   static_assert(8 * (2 * STAGES + 5) + 8 <= 256, "barrier space");
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + C::BAR_OFF + 8 * (2 * STAGES + 5));
   volatile uint32_t* abort_flag = misc;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -192,32 +193,33 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = misc[1];
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, misc[1], 0);
   pdl_wait();
   pdl_launch_dependents();
 
-  const int rank = (int)cluster_rank();
+  const int rank = blockIdx.x & 1;  // in the cluster
   const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
   const int tiles = p.tiles;
 
   if (warp == 0) {
-    if (lane == 0) {
-      // (this loop and the MMA issuer's share their schedulers with busy epilogue warps: a K block's instructions are
-      // the pipeline's slowest part unless they are few, so addresses and descriptors only move by additions)
-      int stage = 0;
-      uint32_t phase = 0;
-      int64_t issued = 0;
-      bool ok = true;
-      const uint32_t fb0 = map_to_rank(full_bar(0), 0);
-      for (int rd = 0; ok; ++rd) {
-        const int t = pair_unit(rd, cid, ncl);
-        if (t >= tiles) break;
-        const PairTile at = pair_locate(p, t);
-        const CUtensorMap *tmA = &maps.a[at.prob], *tmB = &maps.b[at.prob];
-        const bool a_mn = EPI == LIN_PLAIN && p.prob[at.prob].a_mn;
-        const int m0 = at.m2 * 256 + rank * 128, n0 = at.n * BN + rank * (BN / 2);
-        for (int kb = at.kb0; kb < at.kb1; ++kb) {
-          if (!mbar_wait(empty_bar(stage), phase ^ 1, abort_flag)) { ok = false; break; }
+    // (this loop and the MMA issuer's share their schedulers with busy epilogue warps: a K block's instructions are
+    // the pipeline's slowest part unless they are few, so addresses and descriptors only move by additions)
+    const bool one = elect_one();
+    int stage = 0;
+    uint32_t phase = 0;
+    int64_t issued = 0;
+    bool ok = true;
+    const uint32_t fb0 = map_to_rank(full_bar(0), 0);
+    for (int rd = 0; ok; ++rd) {
+      const int t = pair_unit(rd, cid, ncl);
+      if (t >= tiles) break;
+      const PairTile at = pair_locate(p, t);
+      const CUtensorMap *tmA = &maps.a[at.prob], *tmB = &maps.b[at.prob];
+      const bool a_mn = EPI == LIN_PLAIN && p.prob[at.prob].a_mn;
+      const int m0 = at.m2 * 256 + rank * 128, n0 = at.n * BN + rank * (BN / 2);
+      for (int kb = at.kb0; kb < at.kb1; ++kb) {
+        if (!mbar_wait_warp(empty_bar(stage), phase ^ 1, abort_flag)) { ok = false; break; }
+        if (one) {
           const uint32_t fb = fb0 + 8u * stage;
           const uint32_t ad = ring + stage * C::STAGE, bd = ad + C::A_BYTES;
           if (rank == 0) mbar_expect_tx(full_bar(stage), 2 * C::STAGE);
@@ -230,18 +232,21 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
           else
 #pragma unroll
             for (int j = 0; j < BN / 128; ++j) tma_load_pair(bd + j * 8192, tmB, n0 + 64 * j, kb * BK, fb);
-          ++issued;
-          if (++stage == STAGES) { stage = 0; phase ^= 1; }
         }
+        __syncwarp();
+        ++issued;
+        if (++stage == STAGES) { stage = 0; phase ^= 1; }
       }
-      if (!ok && rank == 0)
-        for (int64_t i = min64(issued, STAGES); i > 0; --i) {
-          if (--stage < 0) { stage = STAGES - 1; phase ^= 1; }
-          mbar_drain(full_bar(stage), phase);
-        }
     }
+    if (!ok && rank == 0 && one)
+      for (int64_t i = min64(issued, STAGES); i > 0; --i) {
+        if (--stage < 0) { stage = STAGES - 1; phase ^= 1; }
+        mbar_drain(full_bar(stage), phase);
+      }
+    __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
+      const bool one = elect_one();
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
@@ -249,7 +254,7 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
       for (int rd = 0; ok; ++rd) {
         const int t = pair_unit(rd, cid, ncl);
         if (t >= tiles) break;
-        if (!mbar_wait(tempty_bar(acc), acc_phase ^ 1, abort_flag)) { ok = false; break; }
+        if (!mbar_wait_warp(tempty_bar(acc), acc_phase ^ 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
         const PairTile at = pair_locate(p, t);
         const PairProb& pr = p.prob[at.prob];
@@ -257,24 +262,29 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
         const MatDesc adesc = mat_desc(ring, EPI == LIN_PLAIN && pr.a_mn);
         const uint32_t d = tmem + (uint32_t)(acc * BN);
         for (int kb = at.kb0; kb < at.kb1; ++kb) {
-          if (!mbar_wait(full_bar(stage), phase, abort_flag)) { ok = false; break; }
+          if (!mbar_wait_warp(full_bar(stage), phase, abort_flag)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t off = stage * (C::STAGE >> 4);
+          if (one) {
+            const uint32_t off = stage * (C::STAGE >> 4);
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk)
-            mma_16bit<true>(d, mat_desc64(adesc.lo + off + kk * adesc.k_step), mat_desc64(bdesc.lo + off + kk * bdesc.k_step), idesc,
-                            kk != 0 || kb != at.kb0);
-          mma_commit<true>(empty_bar(stage));
+            for (int kk = 0; kk < BK / 16; ++kk)
+              mma_16bit<true>(d, mat_desc64(adesc.lo + off + kk * adesc.k_step), mat_desc64(bdesc.lo + off + kk * bdesc.k_step), idesc,
+                              kk != 0 || kb != at.kb0);
+            mma_commit<true>(empty_bar(stage));
+          }
+          __syncwarp();
           if (++stage == STAGES) { stage = 0; phase ^= 1; }
         }
         if (!ok) break;
-        mma_commit<true>(tfull_bar(acc));
+        if (one) mma_commit<true>(tfull_bar(acc));
+        __syncwarp();
         if (++acc == 2) { acc = 0; acc_phase ^= 1; }
       }
-      if (!ok) {  // no MMA may still write tensor memory when it is freed
+      if (!ok && one) {  // no MMA may still write tensor memory when it is freed
         mma_commit<true>(drain_bar, 1);
         mbar_drain(drain_bar, 0);
       }
+      __syncwarp();
     }
   } else if (warp >= 4) {
     const int ew = warp - 4, acc = ew >> 3, quarter = warp & 3, half = (ew >> 2) & 1;
@@ -389,8 +399,10 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
       }
       if constexpr (EPI == LIN_FULL) {
         if (p.ck >= 0 && row_ok && nh < pr.N) {  // the four (or, at the edge, fewer) blocks' bytes, one word of the row
-          static_assert(CHUNKS == 4);
-          *reinterpret_cast<uint32_t*>(p.scales + (int64_t)m * p.pitch + (nh >> 5)) = scale_word;
+          uint8_t* sc = p.scales + (int64_t)m * p.pitch + (nh >> 5);
+          if constexpr (CHUNKS == 4) *reinterpret_cast<uint32_t*>(sc) = scale_word;
+          else if constexpr (CHUNKS == 2) *reinterpret_cast<uint16_t*>(sc) = (uint16_t)scale_word;
+          else *sc = (uint8_t)scale_word;
         }
       }
       acc_phase ^= 1;

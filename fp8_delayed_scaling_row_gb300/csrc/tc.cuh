@@ -55,6 +55,17 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     }
   }
 }
+// For the loops that issue copies and MMAs: the whole warp runs them, so that barriers, addresses and descriptors are
+// the same in every lane and stay in uniform registers, and one elected lane issues. With a single lane in the loop
+// each MMA took 60 cycles to issue and a K block 490, whatever its width.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.u32 %0, 1, 0, p; }" : "=r"(one));
+  return one != 0;
+}
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag));
+}
 // Waits (bounded, silently) for copies or MMAs still in flight before the CTA leaves early.
 __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = globaltimer();
