@@ -40,9 +40,6 @@ struct EpiParams {
   uint8_t* codes;
   uint8_t* scales;
   int64_t pitch;
-  const void* cscale;
-  const void* cvec;
-  const float* rvec;
 };
 
 __device__ __forceinline__ uint32_t pack16(float a, float b, int f16) {
@@ -73,14 +70,6 @@ __device__ __forceinline__ void add16x8(float* v, uint4 u, int f16) {
 // are neighbours; every lane of the warp calls it (`ok`: inside the tensor).
 __device__ __forceinline__ void epilogue8(const EpiParams& p, float* v, int m, int n, bool ok) {
   const int64_t row = m;
-  if (p.cscale && ok) {
-    float cs[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, cv[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    add16x8(cs, *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.cscale) + n), p.f16);
-    add16x8(cv, *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.cvec) + n), p.f16);
-    const float rv = p.rvec[m];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = fmaf(v[i], cs[i], rv * cv[i]);
-  }
   if (p.bias && ok) add16x8(v, *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.bias) + n), p.f16);
   if (p.h && ok)
     *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.h) + row * p.N + n) = pack16x8(v, p.f16);
@@ -122,24 +111,18 @@ struct TileCfg {
   static_assert(128 * (BN + 4) * 4 <= STAGES * STAGE, "the fp32 tile reuses the ring");
 };
 
-// One product, or (neither swapped) two independent ones in one launch: the first `clusters` clusters
-// take the first product's tiles.
-struct TileProb {
+struct TileParams {
   EpiParams e;
-  int num_p, num_kb, kb_per_split, clusters, p_mn;
+  int num_p, num_kb, kb_per_split, p_mn, splits;
   uint32_t idesc;
 };
-struct TileParams {
-  TileProb prob[2];
-  int splits;
-};
 struct TileMaps {
-  CUtensorMap p[2], q[2];
+  CUtensorMap p, q;
 };
 
 constexpr int kTileThreads = 256;
 
-template <int BN, bool PAIR, bool Q_MN, bool SWAP>
+template <int BN, bool PAIR, bool SWAP>
 __global__ void __launch_bounds__(kTileThreads, 1)
 lin_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ TileParams p) {
   using C = TileCfg<BN, PAIR>;
@@ -165,8 +148,8 @@ lin_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ T
     mbar_init(done_bar, 1);
     *abort_flag = 0;
     mbar_init_fence();
-    tma_prefetch_map(&maps.p[0]);
-    tma_prefetch_map(&maps.q[0]);
+    tma_prefetch_map(&maps.p);
+    tma_prefetch_map(&maps.q);
   }
   if constexpr (PAIR) cluster_sync_all();  // the peer signals this CTA's barriers
   if (warp == 1) tmem_alloc<PAIR>(smem_u32((const void*)(misc + 1)), C::TMEM_COLS);
@@ -179,13 +162,11 @@ lin_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ T
 
   const int crank = blockIdx.x % (S * SIDES);  // in the cluster
   const int side = PAIR ? crank & 1 : 0, piece = crank / SIDES, leader = crank - side;
-  const int cl = blockIdx.x / (S * SIDES), which = cl >= p.prob[0].clusters ? 1 : 0;
-  const TileProb& pr = p.prob[which];
-  const CUtensorMap *tmP = &maps.p[which], *tmQ = &maps.q[which];
-  const int tile = which ? cl - p.prob[0].clusters : cl;
-  const int p0 = (tile % pr.num_p) * (128 * SIDES) + side * 128, q0 = (tile / pr.num_p) * BN;
-  const int kb0 = piece * pr.kb_per_split, kb1 = min(pr.num_kb, kb0 + pr.kb_per_split);
-  const bool p_mn = pr.p_mn != 0;
+  const CUtensorMap *tmP = &maps.p, *tmQ = &maps.q;
+  const int tile = blockIdx.x / (S * SIDES);
+  const int p0 = (tile % p.num_p) * (128 * SIDES) + side * 128, q0 = (tile / p.num_p) * BN;
+  const int kb0 = piece * p.kb_per_split, kb1 = min(p.num_kb, kb0 + p.kb_per_split);
+  const bool p_mn = p.p_mn != 0;
   const uint16_t both = (uint16_t)(3u << leader);
 
   if (warp == 0) {
@@ -211,10 +192,7 @@ lin_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ T
           load(pd, tmP, p0, kb * BK, fb);
           load(pd + 8192, tmP, p0 + 64, kb * BK, fb);
         }
-        if constexpr (!Q_MN) load(qd, tmQ, kb * BK, qs, fb);
-        else
-#pragma unroll
-          for (int j = 0; j < BN / SIDES / 64; ++j) load(qd + j * 8192, tmQ, qs + 64 * j, kb * BK, fb);
+        load(qd, tmQ, kb * BK, qs, fb);
       }
       __syncwarp();
       ++issued;
@@ -230,8 +208,8 @@ lin_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ T
     const bool one = elect_one();
     int stage = 0;
     uint32_t phase = 0;
-    const MatDesc pdesc = mat_desc(ring, p_mn), qdesc = mat_desc(ring + C::P_BYTES, Q_MN);
-    const uint32_t idesc = pr.idesc;
+    const MatDesc pdesc = mat_desc(ring, p_mn), qdesc = mat_desc(ring + C::P_BYTES, false);
+    const uint32_t idesc = p.idesc;
     for (int kb = kb0; kb < kb1; ++kb) {
       if (!mbar_wait_warp(full_bar(stage), phase, abort_flag)) break;
       tc_fence_after();
@@ -317,7 +295,7 @@ lin_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ T
         v[4] += b[u][s].x; v[5] += b[u][s].y; v[6] += b[u][s].z; v[7] += b[u][s].w;
       }
       const int m = (SWAP ? q0 : p0) + r, n = (SWAP ? p0 : q0) + c;
-      epilogue8(pr.e, v, m, n, m < pr.e.M && n < pr.e.N);
+      epilogue8(p.e, v, m, n, m < p.e.M && n < p.e.N);
     }
   }
   tc_fence_before();
@@ -635,48 +613,32 @@ EpiParams epi_params(const LinGemm& g) {
   e.codes = g.ckpt.codes;
   e.scales = g.ckpt.scales;
   e.pitch = lnfp8_act_ckpt_scale_pitch(g.N);
-  e.cscale = g.cscale;
-  e.cvec = g.cvec;
-  e.rvec = g.rvec;
   return e;
 }
 
-// S pieces of K per tile (1, 2 or 4; PAIR: 1 or 2).
-template <int BN, bool PAIR, bool Q_MN, bool SWAP>
-lnfp8_status tile_launch(const LinGemm* g, int count, int S, cudaStream_t st) {
+// S pieces of K per tile (1, 2 or 4; PAIR: 2). The lanes' operand (SWAP: b) may be MN-major, the other is K-major.
+template <int BN, bool PAIR, bool SWAP>
+lnfp8_status tile_launch(const LinGemm& q, int S, cudaStream_t st) {
   using C = TileCfg<BN, PAIR>;
-  constexpr auto k = lin_tile_kernel<BN, PAIR, Q_MN, SWAP>;
+  constexpr auto k = lin_tile_kernel<BN, PAIR, SWAP>;
   const lnfp8_status set = kernel_setup<k>(kTileThreads, C::SMEM, nullptr, "linear: kernel set-up");
   if (set != LNFP8_OK) return set;
   TileParams p = {};
   TileMaps maps;
-  int64_t tiles = 0;
-  bool ok = true;
-  for (int i = 0; i < count; ++i) {
-    const LinGemm& q = g[i];
-    TileProb& r = p.prob[i];
-    const int64_t prow = SWAP ? q.N : q.M, qrow = SWAP ? q.M : q.N;
-    const bool p_mn = SWAP ? q.b_mn : q.a_mn;
-    const int64_t num_p = (prow + (PAIR ? 255 : 127)) / (PAIR ? 256 : 128), num_q = (qrow + BN - 1) / BN;
-    if (num_p * num_q > 0x0FFFFFFF) return set_error(LNFP8_ERR_UNSUPPORTED_SHAPE, "linear: too many tiles");
-    r.e = epi_params(q);
-    r.num_p = (int)num_p;
-    r.num_kb = (int)((q.K + BK - 1) / BK);
-    r.clusters = (int)(num_p * num_q);
-    r.p_mn = p_mn;
-    r.idesc = make_idesc(q.elem, PAIR ? 256 : 128, BN, p_mn, Q_MN);
-    tiles += num_p * num_q;
-    ok = ok && (SWAP ? operand_map(&maps.p[i], q.b, p_mn, q.N, q.K, q.ldb, 128) && operand_map(&maps.q[i], q.a, Q_MN, q.M, q.K, q.lda, PAIR ? BN / 2 : BN)
-                     : operand_map(&maps.p[i], q.a, p_mn, q.M, q.K, q.lda, 128) && operand_map(&maps.q[i], q.b, Q_MN, q.N, q.K, q.ldb, PAIR ? BN / 2 : BN));
-  }
-  if (!ok) return set_error(LNFP8_ERR_CUDA, "linear: cuTensorMapEncodeTiled failed (driver entry point or arguments)");
-  if (count == 1) {
-    p.prob[1] = p.prob[0];
-    maps.p[1] = maps.p[0];
-    maps.q[1] = maps.q[0];
-  }
+  const int64_t prow = SWAP ? q.N : q.M, qrow = SWAP ? q.M : q.N;
+  const bool p_mn = SWAP ? q.b_mn : q.a_mn;
+  const int64_t num_p = (prow + (PAIR ? 255 : 127)) / (PAIR ? 256 : 128), num_q = (qrow + BN - 1) / BN, tiles = num_p * num_q;
+  if (tiles > 0x0FFFFFFF) return set_error(LNFP8_ERR_UNSUPPORTED_SHAPE, "linear: too many tiles");
+  p.e = epi_params(q);
+  p.num_p = (int)num_p;
+  p.num_kb = (int)((q.K + BK - 1) / BK);
+  p.kb_per_split = (p.num_kb + S - 1) / S;
   p.splits = S;
-  for (TileProb& r : p.prob) r.kb_per_split = (r.num_kb + S - 1) / S;
+  p.p_mn = p_mn;
+  p.idesc = make_idesc(q.elem, PAIR ? 256 : 128, BN, p_mn, false);
+  const bool ok = SWAP ? operand_map(&maps.p, q.b, p_mn, q.N, q.K, q.ldb, 128) && operand_map(&maps.q, q.a, false, q.M, q.K, q.lda, PAIR ? BN / 2 : BN)
+                       : operand_map(&maps.p, q.a, p_mn, q.M, q.K, q.lda, 128) && operand_map(&maps.q, q.b, false, q.N, q.K, q.ldb, PAIR ? BN / 2 : BN);
+  if (!ok) return set_error(LNFP8_ERR_CUDA, "linear: cuTensorMapEncodeTiled failed (driver entry point or arguments)");
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -739,17 +701,17 @@ int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 }  // namespace
 
 namespace {
-bool takes_swap(const LinGemm& g) { return g.M <= 128 && !g.a_mn; }
+bool takes_swap(const LinGemm& g) { return g.M <= 64 && !g.a_mn; }
 
-// How a product, or two in one launch, runs when lanes are tokens: the persistent kernel over
-// 256 x 256 tiles, or one 256 x bn tile per cluster with K in S pieces. Costs in ns, fitted to measurements of
-// both (21 shapes of 65 to 8192 tokens): a 64-wide K block takes a pair 340 (256 columns) or 260 (128),
-// the rest is launch, set-up and epilogue; 76 clusters of one pair or 36 of two fit on the chip at once,
-// and of four too few (two rounds at 16 clusters). At 512 x 768 x 2304: persistent 10.4 us, 128 columns and
-// two pieces 9.6; at 512 x 2048 x 2048 15.8 and 12.0; at 2048 x 2048 x 2048 18.1 and 46.8.
+// How a product, or two in one launch, runs when lanes are tokens: the persistent kernel over tiles of 256, 128 or (K-major
+// operands) 64 columns, or, forward, one 256 x tile per cluster with K in two pieces. Costs in ns, fitted to
+// measurements of all of them (36 shapes of 33 to 16384 tokens): a 64-wide K block takes a pair 270 (256 columns: the
+// matrix rate) or 171 (128 and 64: the issue of copies and MMAs); the rest is launch, set-up, the last epilogue, and
+// 500 a round. A tile takes no less than four K blocks' time, for its epilogue. Of the clusters of two pairs 36 fit on the
+// chip at once. 333 x 768 x 2304 takes 5.8 us with 64 columns, 5.9 with 128, 8.2 with 256 and 8.3 with 128 in two
+// pieces; 129 x 4096 x 4096 takes 14.6, 15.1, 22.7 and 13.8; 2048 x 2048 x 2048 takes 25.8, 16.4, 15.3 and 40.1.
 struct LinPlan {
-  int bn, S;  // bn 0: the persistent kernel
-  int tile;   // its columns
+  int tile, S;  // S 1: the persistent kernel
 };
 // K blocks of the pair with the most: the list of units, longest first, dealt out forwards and backwards.
 int64_t longest_pair(const int64_t* units, const int64_t* kb, int count, int64_t pairs) {
@@ -775,42 +737,41 @@ int64_t longest_pair(const int64_t* units, const int64_t* kb, int count, int64_t
 
 LinPlan lin_plan(LinGemm* g, int count) {
   const int64_t pairs = max64(num_sms() / 2, 1);
-  int64_t max_kb = 1, min_kb = 1 << 30, t128 = 0, units[2], kb[2];
-  for (int i = 0; i < count; ++i) {
-    kb[i] = (g[i].K + BK - 1) / BK;
-    const int64_t m2 = (g[i].M + 255) / 256;
-    units[i] = m2 * ((g[i].N + 255) / 256);
-    max_kb = max64(max_kb, kb[i]);
-    min_kb = min64(min_kb, kb[i]);
-    t128 += m2 * ((g[i].N + 127) / 128);
-  }
-  int64_t cost = longest_pair(units, kb, count, pairs) * 340 + 6200;
-  LinPlan best = {0, 1, 256};
-  auto offer = [&](int bn, int S, int64_t tiles, int64_t per_kb, int64_t fixed) {
-    if (min_kb < 2 * S) return;
-    const int64_t fit = max64(S == 1 ? pairs : pairs * 36 / 76, 1), c = (tiles + fit - 1) / fit * ((max_kb + S - 1) / S * per_kb + fixed);
-    if (c < cost) {
-      cost = c;
-      best = {bn, S, 0};
+  // the persistent kernel; pieces: a weight gradient's K in pieces
+  auto persistent = [&](int bn, int64_t per_kb, int64_t fixed, bool pieces) {
+    int64_t units[2] = {0, 0}, kb[2] = {0, 0}, join = 0;
+    for (int i = 0; i < count; ++i) {
+      const int64_t n = pieces && g[i].pieces > 1 ? g[i].pieces : 1;
+      units[i] = (g[i].M + 255) / 256 * ((g[i].N + bn - 1) / bn) * n;
+      kb[i] = max64(4, ((g[i].K + BK - 1) / BK + n - 1) / n);
+      if (n > 1) join += 2000 + n * g[i].M * g[i].N * 8 / 6000;  // a launch, and the pieces' bytes out and in
     }
+    return longest_pair(units, kb, count, pairs) * per_kb + fixed + (units[0] + units[1] - 1) / pairs * 500 + join;
   };
-  offer(128, 1, t128, 260, 6700);
-  offer(128, 2, t128, 260, 7700);
-  offer(256, 2, units[0] + (count == 2 ? units[1] : 0), 340, 9500);
-  // a weight gradient in pieces, if that and joining them (its bytes once out and once in) is less
-  bool pieces = false;
-  for (int i = 0; i < count; ++i) {
-    if (g[i].pieces <= 1) continue;
-    const int64_t u[2] = {units[0] * (i == 0 ? g[i].pieces : 1), count == 2 ? units[1] * (i == 1 ? g[i].pieces : 1) : 0};
-    const int64_t k[2] = {i == 0 ? (kb[0] + g[i].pieces - 1) / g[i].pieces : kb[0],
-                          count == 2 ? (i == 1 ? (kb[1] + g[i].pieces - 1) / g[i].pieces : kb[1]) : 0};
-    const int64_t c = longest_pair(u, k, count, pairs) * 340 + 6200 + 4000 + g[i].pieces * g[i].M * g[i].N * 8 / 4000;
-    if (c < cost) {
-      cost = c;
-      best = {0, 1, 256};
-      pieces = true;
+  int64_t cost = persistent(256, 270, 4700, false);
+  LinPlan best = {256, 1};
+  auto offer = [&](int64_t c, int tile, int S) {
+    if (c >= cost) return false;
+    cost = c;
+    best = {tile, S};
+    return true;
+  };
+  offer(persistent(128, 171, 3640, false), 128, 1);
+  if (!g->b_mn) {
+    offer(persistent(64, 171, 3300, false), 64, 1);
+    const int64_t kb = (g->K + BK - 1) / BK, fit = max64(pairs * 36 / 76, 1), m2 = (g->M + 255) / 256;
+    auto halves = [&](int bn, int64_t per_kb, int64_t fixed) {
+      const int64_t tiles = m2 * ((g->N + bn - 1) / bn);
+      return (tiles + fit - 1) / fit * ((kb + 1) / 2 * per_kb + fixed);
+    };
+    if (kb >= 4) {
+      offer(halves(128, 180, 7700), 128, 2);
+      offer(halves(256, 270, 9800), 256, 2);
     }
   }
+  bool pieces = false;
+  for (int i = 0; i < count; ++i) pieces = pieces || g[i].pieces > 1;
+  if (pieces) pieces = offer(persistent(256, 270, 4700, true), 256, 1);
   if (!pieces)
     for (int i = 0; i < count; ++i) g[i].pieces = 1;
   return best;
@@ -849,17 +810,15 @@ lnfp8_status few_by_tokens(const LinGemm& g, cudaStream_t st) {
 }
 
 // Few tokens: K pieces while they run on SMs that would idle and each keeps a few K blocks.
-int swap_splits(const LinGemm& g, int lanes, int most) {
-  const int64_t tiles = (g.N + lanes - 1) / lanes, kb = (g.K + BK - 1) / BK;
+int swap_splits(const LinGemm& g) {
+  const int64_t tiles = (g.N + 127) / 128, kb = (g.K + BK - 1) / BK;
   int S = 1;
-  while (S < most && tiles * (lanes / 128) * S * 2 <= num_sms() && kb >= S * 2 * 2) S *= 2;
+  while (S < 4 && tiles * S * 2 <= num_sms() && kb >= S * 2 * 2) S *= 2;
   return S;
 }
 lnfp8_status swap_launch(const LinGemm& g, cudaStream_t st) {
-  if (g.M <= 16) return tile_launch<16, false, false, true>(&g, 1, swap_splits(g, 128, 4), st);
-  if (g.M <= 32) return tile_launch<32, false, false, true>(&g, 1, swap_splits(g, 128, 4), st);
-  if (g.M <= 64) return tile_launch<64, false, false, true>(&g, 1, swap_splits(g, 128, 4), st);
-  return tile_launch<128, true, false, true>(&g, 1, swap_splits(g, 256, 2), st);
+  const int S = swap_splits(g);
+  return g.M <= 16 ? tile_launch<16, false, true>(g, S, st) : g.M <= 32 ? tile_launch<32, false, true>(g, S, st) : tile_launch<64, false, true>(g, S, st);
 }
 }  // namespace
 
@@ -870,8 +829,8 @@ lnfp8_status lin_gemm_launch(const LinGemm* g, int count, cudaStream_t st) {
     if (takes_swap(*g)) return swap_launch(*g, st);
     LinGemm one = *g;
     const LinPlan pl = lin_plan(&one, 1);
-    if (pl.bn == 0) return pl.tile == 64 ? pair_launch<64, LIN_FULL>(g, 1, st) : pl.tile == 128 ? pair_launch<128, LIN_FULL>(g, 1, st) : pair_launch<256, LIN_FULL>(g, 1, st);
-    return pl.bn == 256 ? tile_launch<256, true, false, false>(g, 1, pl.S, st) : tile_launch<128, true, false, false>(g, 1, pl.S, st);
+    if (pl.S == 2) return pl.tile == 256 ? tile_launch<256, true, false>(*g, 2, st) : tile_launch<128, true, false>(*g, 2, st);
+    return pl.tile == 64 ? pair_launch<64, LIN_FULL>(g, 1, st) : pl.tile == 128 ? pair_launch<128, LIN_FULL>(g, 1, st) : pair_launch<256, LIN_FULL>(g, 1, st);
   }
   // the backward: what few tokens leave swapped runs alone, the rest in one launch
   LinGemm rest[2];
@@ -886,13 +845,10 @@ lnfp8_status lin_gemm_launch(const LinGemm* g, int count, cudaStream_t st) {
   }
   if (n == 0) return LNFP8_OK;
   const LinPlan pl = lin_plan(rest, n);
-  if (pl.bn == 0) {
-    lnfp8_status s = pl.tile == 128 ? pair_launch<128, LIN_PLAIN>(rest, n, st) : pair_launch<256, LIN_PLAIN>(rest, n, st);
-    for (int i = 0; i < n && s == LNFP8_OK; ++i)
-      if (rest[i].pieces > 1) s = join_launch(rest[i], st);
-    return s;
-  }
-  return pl.bn == 256 ? tile_launch<256, true, true, false>(rest, n, pl.S, st) : tile_launch<128, true, true, false>(rest, n, pl.S, st);
+  lnfp8_status s = pl.tile == 128 ? pair_launch<128, LIN_PLAIN>(rest, n, st) : pair_launch<256, LIN_PLAIN>(rest, n, st);
+  for (int i = 0; i < n && s == LNFP8_OK; ++i)
+    if (rest[i].pieces > 1) s = join_launch(rest[i], st);
+  return s;
 }
 
 lnfp8_status linear_act_fwd_launch(const lnfp8_linear_act_fwd_args* a, cudaStream_t st) {
