@@ -32,9 +32,10 @@ struct PairCfg {
   // L2, the leader's barrier) is about 1500 cycles and a stage's MMAs 512, so four stages leave the tensor
   // cores waiting: 16384 x 8192 x 2048 took 340 us with four and staged boxes, 312 with seven. The epilogue
   // has no staging: a thread's 32 columns are whole 32-byte sectors of its row, and are stored and loaded so.
-  static constexpr int STAGES = (232448 - 1024 - 256) / STAGE;
+  static constexpr int STAGES = (232448 - 1024 - 256 - 64 * kPairEpiWarps) / STAGE;
   static constexpr int BAR_OFF = STAGES * STAGE;
-  static constexpr int SMEM = 1024 + BAR_OFF + 256;
+  static constexpr int BIAS_OFF = BAR_OFF + 256;  // a chunk's 32 columns of the bias for each epilogue warp
+  static constexpr int SMEM = 1024 + BIAS_OFF + 64 * kPairEpiWarps;
   static constexpr int TMEM_COLS = 2 * BN;
   static_assert(STAGES >= 4 && SMEM <= 232448, "shared memory budget");
 };
@@ -290,7 +291,7 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
     const int ew = warp - 4, acc = ew >> 3, quarter = warp & 3, half = (ew >> 2) & 1;
     constexpr int HALF = BN / 2, CHUNKS = HALF / 32;
     uint32_t acc_phase = 0;
-    const uint32_t tempty = map_to_rank(tempty_bar(acc), 0);
+    const uint32_t tempty = map_to_rank(tempty_bar(acc), 0), bias_slot = ring + C::BIAS_OFF + 64 * ew;
     // this group's rounds have its parity: a step of two rounds keeps the direction
     const int t0 = pair_unit(acc, cid, ncl);
     for (int t = t0; t < tiles; t += 2 * ncl) {
@@ -299,8 +300,13 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
       const int m = at.m2 * 256 + rank * 128 + quarter * 32 + lane;
       const int nh = at.n * BN + half * HALF;  // this warp's first column
       const bool affine = EPI == LIN_PLAIN && pr.cscale != nullptr && pr.pieces == 1;
-      const uint16_t* col_vec = static_cast<const uint16_t*>(EPI == LIN_FULL ? p.bias : affine ? pr.cscale : nullptr);
       const float rv = affine && m < pr.M ? __ldg(pr.rvec + m) : 0.f;
+      const bool biased = EPI == LIN_FULL && p.bias != nullptr;
+      // two columns a lane (16 lanes), a chunk ahead
+      auto bias_word = [&](int n) {
+        return lane < 16 && n + 2 * lane < pr.N ? __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.bias) + n) + lane) : 0u;
+      };
+      uint32_t next_bias = biased ? bias_word(nh) : 0u;
       if (!mbar_wait(tfull_bar(acc), acc_phase, abort_flag)) break;
       tc_fence_after();
       const bool row_ok = m < pr.M;
@@ -308,7 +314,12 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
 #pragma unroll 1
       for (int ch = 0; ch < CHUNKS; ++ch) {
         const int n0 = nh + ch * 32;
-        __syncwarp();  // rows past M took other branches
+        __syncwarp();  // rows past M took other branches; the bias slot has been read
+        if (biased) {
+          if (lane < 16) sts4(bias_slot + 4 * lane, next_bias);
+          if (ch + 1 < CHUNKS) next_bias = bias_word(n0 + 32);
+          __syncwarp();
+        }
         uint32_t rr[32];
         tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * BN + half * HALF + ch * 32), rr);
         if (ch == CHUNKS - 1 && t + 2 * ncl < tiles) {  // someone waits for it: nothing is in flight when the CTA leaves
@@ -331,25 +342,31 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
         uint32_t res[16];
         if constexpr (EPI == LIN_FULL)
           if (p.resid && row_ok) load_row32(reinterpret_cast<const uint16_t*>(p.resid) + m * p.ldr, n0, pr.N, p.wide_resid, res);
-        // every lane reads the same 32 columns: broadcasts from L1, fewer instructions than a lane's columns
-        // spread by shuffles (8192 x 2048 x 8192 161 -> 158 us, 16384 x 8192 x 2048 297 -> 292 us)
-        if (col_vec) {
+        // every lane needs the same 32 columns: broadcast from the warp's slot (16 shuffles instead: 8192 x 2048 x 8192
+        // 158 -> 161 us; from global memory in place: 16384 x 768 x 768 17 -> 21 us, each chunk waiting for L2)
+        if (biased) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            if (n0 + 8 * j >= pr.N) break;
-            const uint4 bu = __ldg(reinterpret_cast<const uint4*>(col_vec + n0 + 8 * j));
+            const uint4 bu = lds16(bias_slot + 16 * j);
             const uint32_t bw[4] = {bu.x, bu.y, bu.z, bu.w};
-            uint4 vu = make_uint4(0u, 0u, 0u, 0u);
-            if (affine) vu = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(pr.cvec) + n0 + 8 * j));
-            const uint32_t vw[4] = {vu.x, vu.y, vu.z, vu.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const float2 b = unpack16(bw[i], p.f16);
-              if constexpr (EPI == LIN_FULL) z[4 * j + i] = add_2(z[4 * j + i], pk(b.x, b.y));
-              else {
-                const float2 v = unpack16(vw[i], p.f16);
-                z[4 * j + i] = fma_2(z[4 * j + i], pk(b.x, b.y), mul_2(pk(rv, rv), pk(v.x, v.y)));
-              }
+              z[4 * j + i] = add_2(z[4 * j + i], pk(b.x, b.y));
+            }
+          }
+        }
+        if (affine) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (n0 + 8 * j >= pr.N) break;
+            const uint4 su = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(pr.cscale) + n0 + 8 * j));
+            const uint4 vu = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(pr.cvec) + n0 + 8 * j));
+            const uint32_t sw[4] = {su.x, su.y, su.z, su.w}, vw[4] = {vu.x, vu.y, vu.z, vu.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 c = unpack16(sw[i], p.f16), v = unpack16(vw[i], p.f16);
+              z[4 * j + i] = fma_2(z[4 * j + i], pk(c.x, c.y), mul_2(pk(rv, rv), pk(v.x, v.y)));
             }
           }
         }
