@@ -1,9 +1,9 @@
-// Included by linear.cu: the persistent kernel for large products.
+// Included by linear.cu: the persistent kernel.
 //
 // A pair of CTAs (a cluster of 2) computes 256 x BN tiles with the 2-SM MMA
 // (256 x BN x 16 per instruction): each CTA loads its 128 rows of A and half of the
-// B tile by TMA into its own ring and signals the leader's barrier; the leader's one
-// thread issues the MMAs for both. Two accumulators (2 x BN tensor-memory columns)
+// B tile by TMA into its own ring and signals the leader's barrier; one lane of the leader
+// issues the MMAs for both. Two accumulators (2 x BN tensor-memory columns)
 // alternate, so that the epilogue of one tile runs under the MMAs of the next.
 //   warp 0      TMA producer          warp 1   tensor memory, MMA issuer (leader)
 //   warps 2-3   idle                  warps 4-19  epilogue, 8 per accumulator
@@ -28,9 +28,9 @@ struct PairCfg {
   static constexpr int A_BYTES = 128 * BK * 2;
   static constexpr int B_BYTES = BN / 2 * BK * 2;
   static constexpr int STAGE = A_BYTES + B_BYTES;
-  // The ring takes all of shared memory: the way from a stage's release to its next data (barrier, TMA,
-  // L2, the leader's barrier) is about 1500 cycles and a stage's MMAs 512, so four stages leave the tensor
-  // cores waiting: 16384 x 8192 x 2048 took 340 us with four and staged boxes, 312 with seven. The epilogue
+  // The ring takes all of shared memory but the bias slots: the way from a stage's release to its next data (barrier,
+  // TMA, L2, the leader's barrier) is about 1500 cycles and a stage's MMAs 512 or fewer, so four stages leave the
+  // tensor cores waiting: 16384 x 8192 x 2048 took 340 us with four and staged boxes, 312 with seven. The epilogue
   // has no staging: a thread's 32 columns are whole 32-byte sectors of its row, and are stored and loaded so.
   static constexpr int STAGES = (232448 - 1024 - 256 - 64 * kPairEpiWarps) / STAGE;
   static constexpr int BAR_OFF = STAGES * STAGE;
