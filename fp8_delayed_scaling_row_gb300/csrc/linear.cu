@@ -96,7 +96,7 @@ __device__ __forceinline__ void epilogue8(const EpiParams& p, float* v, int m, i
 // finishing 1/S of its rows of the tile: no workspace, and the result does not depend on timing.
 //   PAIR    the 2-SM MMA, 256 x BN x 16: a CTA holds 128 rows and loads half of the BN side. A
 //           128 x 128 tile on one SM reads and fills 256 bytes of shared memory a clock, twice what
-//           there is; 256 x 256 on a pair just fits (measured on 181 x 6392 x 7112: 52 -> 30 us). Taken
+//           there is; a pair holds half of the BN side each (measured on 181 x 6392 x 7112: 52 -> 30 us). Taken
 //           where K is long and the tiles are few: 256 x 4096 x 4096 13.9 us, 14.8 on persistent pairs.
 //   SWAP    (up to 64 tokens) the accumulator's lanes are output features and its BN columns tokens, so that few
 //           tokens fill the instruction; else lanes are tokens. 8 x 4096 x 4096 9.4 us, 3.6 TB/s.
@@ -705,7 +705,7 @@ namespace {
 bool takes_swap(const LinGemm& g) { return g.M <= 64 && !g.a_mn; }
 
 // How a product, or two in one launch, runs when lanes are tokens: the persistent kernel over tiles of 256, 128 or (K-major
-// operands) 64 columns, or, forward, one 256 x tile per cluster with K in two pieces. Costs in ns, fitted to
+// operands) 64 columns, or, forward, one 256 x 128 tile per cluster with K in two pieces. Costs in ns, fitted to
 // measurements of all of them (36 shapes of 33 to 16384 tokens): a 64-wide K block takes a pair 270 (256 columns: the
 // matrix rate) or 171 (128 and 64: the issue of copies and MMAs); the rest is launch, set-up, the last epilogue, and
 // 500 a round. A tile takes no less than four K blocks' time, for its epilogue. Of the clusters of two pairs 36 fit on the
@@ -760,15 +760,9 @@ LinPlan lin_plan(LinGemm* g, int count) {
   offer(persistent(128, 171, 3640, false), 128, 1);
   if (!g->b_mn) {
     offer(persistent(64, 171, 3300, false), 64, 1);
-    const int64_t kb = (g->K + BK - 1) / BK, fit = max64(pairs * 36 / 76, 1), m2 = (g->M + 255) / 256;
-    auto halves = [&](int bn, int64_t per_kb, int64_t fixed) {
-      const int64_t tiles = m2 * ((g->N + bn - 1) / bn);
-      return (tiles + fit - 1) / fit * ((kb + 1) / 2 * per_kb + fixed);
-    };
-    if (kb >= 4) {
-      offer(halves(128, 180, 7700), 128, 2);
-      offer(halves(256, 270, 9800), 256, 2);
-    }
+    const int64_t kb = (g->K + BK - 1) / BK, fit = max64(pairs * 36 / 76, 1);
+    const int64_t tiles = (g->M + 255) / 256 * ((g->N + 127) / 128);
+    if (kb >= 4) offer((tiles + fit - 1) / fit * ((kb + 1) / 2 * 180 + 7700), 128, 2);
   }
   bool pieces = false;
   for (int i = 0; i < count; ++i) pieces = pieces || g[i].pieces > 1;
@@ -830,7 +824,7 @@ lnfp8_status lin_gemm_launch(const LinGemm* g, int count, cudaStream_t st) {
     if (takes_swap(*g)) return swap_launch(*g, st);
     LinGemm one = *g;
     const LinPlan pl = lin_plan(&one, 1);
-    if (pl.S == 2) return pl.tile == 256 ? tile_launch<256, true, false>(*g, 2, st) : tile_launch<128, true, false>(*g, 2, st);
+    if (pl.S == 2) return tile_launch<128, true, false>(*g, 2, st);
     return pl.tile == 64 ? pair_launch<64, LIN_FULL>(g, 1, st) : pl.tile == 128 ? pair_launch<128, LIN_FULL>(g, 1, st) : pair_launch<256, LIN_FULL>(g, 1, st);
   }
   // the backward: what few tokens leave swapped runs alone, the rest in one launch

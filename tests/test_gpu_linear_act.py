@@ -279,6 +279,20 @@ def test_nan_and_inf_stay_in_their_rows(L):
         assert torch.isnan(back[1:3]).all() and torch.isfinite(back[keep]).all()
 
 
+# few tiles over a long K forward; few tiles of a weight gradient over many tokens, ragged
+LONG = [(200, 4096, 1000), (300, 4104, 520), (9001, 520, 264), (5000, 776, 520)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,K,N", LONG)
+def test_products_cut_along_their_sums(L, M, K, N, dtype):
+    test_whole_number_products_are_exact(L, M, K, N, dtype)
+    test_forward(L, M, K, N, dtype, "gelu", True, "ckpt")
+    test_forward(L, M, K, N, dtype, "none", False, "none")
+    for xsrc in ("x", "ln"):
+        test_backward(L, M, K, N, dtype, "gelu", "ckpt", xsrc)
+
+
 @pytest.mark.parametrize("act", ["gelu", "relu", "silu"])
 def test_nan_pre_activations_reach_the_gradients(L, act):
     """A pre-activation that was NaN, or whose checkpoint block holds an Inf, must not pass for a zero slope."""
