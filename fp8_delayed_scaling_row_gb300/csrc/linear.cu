@@ -74,7 +74,7 @@ __device__ __forceinline__ void epilogue8(const EpiParams& p, float* v, int m, i
   if (p.h && ok)
     *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.h) + row * p.N + n) = pack16x8(v, p.f16);
   if (p.ck >= 0) {
-    // columns past N hold zeros (no operand, no bias)
+    // items outside the tensor hold zeros
     const uint32_t b = ckpt_byte(block_amax8(v), p.ck);
     if (ok) {
       *reinterpret_cast<uint2*>(p.codes + row * p.N + n) = encode8(v, ckpt_inv_scale(b), p.ck);
@@ -264,13 +264,20 @@ lin_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ T
   constexpr int CH = COLS / 8;
   constexpr int kMostPieces = PAIR ? 2 : 4, U = PAIR ? 2 : 1;  // U items of a thread together
   for (int i0 = threadIdx.x; i0 < rows * CH; i0 += U * kTileThreads) {
-    // every piece's words first: loads from another SM's shared memory take most of a microsecond
+    // every piece's words first: loads from another SM's shared memory take most of a microsecond. Items outside the
+    // tensor load nothing: each value read from another CTA goes into a store to y, so that the thread has waited
+    // for it before it reaches the barrier behind which that CTA may leave
     float4 a[U][kMostPieces], b[U][kMostPieces];
+    bool ok[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u * kTileThreads, r = piece * rows + i / CH, c = (i % CH) * 8;
+      ok[u] = (SWAP ? q0 : p0) + r < p.e.M && (SWAP ? p0 : q0) + c < p.e.N;
       if (i >= rows * CH) break;
-      if (S > 1) {
+      if (!ok[u]) {
+#pragma unroll
+        for (int s = 0; s < kMostPieces; ++s) a[u][s] = b[u][s] = make_float4(0.f, 0.f, 0.f, 0.f);
+      } else if (S > 1) {
         const uint32_t at = ring + (uint32_t)(r * PITCH + c) * 4u;
 #pragma unroll
         for (int s = 0; s < kMostPieces; ++s) {
@@ -295,8 +302,7 @@ lin_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ T
         v[0] += a[u][s].x; v[1] += a[u][s].y; v[2] += a[u][s].z; v[3] += a[u][s].w;
         v[4] += b[u][s].x; v[5] += b[u][s].y; v[6] += b[u][s].z; v[7] += b[u][s].w;
       }
-      const int m = (SWAP ? q0 : p0) + r, n = (SWAP ? p0 : q0) + c;
-      epilogue8(p.e, v, m, n, m < p.e.M && n < p.e.N);
+      epilogue8(p.e, v, (SWAP ? q0 : p0) + r, (SWAP ? p0 : q0) + c, ok[u]);
     }
   }
   tc_fence_before();

@@ -103,7 +103,8 @@ __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // The same without ordering memory: a release would wait for every store of the epilogue (1.2 us at the end of a
-// kernel). For leaving together, once nothing of this CTA's is in flight to another's shared memory.
+// kernel). For leaving together, once nothing of this CTA's is in flight to another's shared memory: what it read there
+// has arrived, because a store or a sum took the values, and what it signals there somebody waits for first.
 __device__ __forceinline__ void cluster_sync_relaxed() {
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
