@@ -307,7 +307,7 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
         return lane < 16 && n + 2 * lane < pr.N ? __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.bias) + n) + lane) : 0u;
       };
       uint32_t next_bias = biased ? bias_word(nh) : 0u;
-      if (!mbar_wait(tfull_bar(acc), acc_phase, abort_flag)) break;
+      if (!mbar_wait_warp(tfull_bar(acc), acc_phase, abort_flag)) break;  // the whole warp: what follows is warp-wide
       tc_fence_after();
       const bool row_ok = m < pr.M;
       uint32_t scale_word = 0;

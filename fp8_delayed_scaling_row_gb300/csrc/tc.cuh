@@ -63,6 +63,8 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{ .reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.u32 %0, 1, 0, p; }" : "=r"(one));
   return one != 0;
 }
+// A wait of a whole warp: near the time limit lanes can see different results, and those that went on would meet
+// warp-wide instructions without the others, so the warp leaves if any of them gave up.
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
   return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag));
 }
