@@ -199,6 +199,11 @@ lin_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ T
       ++issued;
       if (++stage == STAGES) { stage = 0; phase ^= 1; }
     }
+    // the commits behind the last stages signal these barriers (PAIR: both CTAs'), which stay until every signal has come
+    for (int i = 0, s = stage, ph = phase; ok && i < STAGES; ++i) {
+      ok = mbar_wait_warp(empty_bar(s), ph ^ 1, abort_flag);
+      if (++s == STAGES) { s = 0; ph ^= 1; }
+    }
     if (!ok && side == 0 && one)
       for (int i = min(issued, STAGES); i > 0; --i) {  // copies in flight land before the CTA leaves
         if (--stage < 0) { stage = STAGES - 1; phase ^= 1; }

@@ -239,6 +239,12 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
         if (++stage == STAGES) { stage = 0; phase ^= 1; }
       }
     }
+    // the commits behind the last stages signal both CTAs' barriers, which stay until every signal has come (a stage
+    // that was never filled counts as released)
+    for (int i = 0, s = stage, ph = phase; ok && i < STAGES; ++i) {
+      ok = mbar_wait_warp(empty_bar(s), ph ^ 1, abort_flag);
+      if (++s == STAGES) { s = 0; ph ^= 1; }
+    }
     if (!ok && rank == 0 && one)
       for (int64_t i = min64(issued, STAGES); i > 0; --i) {
         if (--stage < 0) { stage = STAGES - 1; phase ^= 1; }
