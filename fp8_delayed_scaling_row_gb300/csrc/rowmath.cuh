@@ -399,7 +399,7 @@ __device__ __forceinline__ float act_fwd(float z, int act) {
 __device__ __forceinline__ float relu_slope(float z) { return z > 0.f ? 1.0f : (z != z ? z : 0.f); }
 
 // act_fwd and the slopes of 8 values as 4 pairs. s(u) of a pair takes one reciprocal, of the product
-// (1 + e^-u0)(1 + e^-u1), while the products stay in range: kernels that pass over a tensor once are
+// (1 + e^-u0)(1 + e^-u1), while the products are in range and none is NaN: kernels that pass over a tensor once are
 // bound by the special-function unit otherwise (16 a clock per SM: 2 per value are 58 us for the
 // 134 M values of 16384 x 8192, as long as their bytes take).
 __device__ __forceinline__ void logistic8(const uint64_t* nu, uint64_t* s) {
@@ -412,8 +412,8 @@ __device__ __forceinline__ void logistic8(const uint64_t* nu, uint64_t* s) {
     const float2 t = upk(d[k]);
     q[k] = t.x * t.y;
   }
-  const float top = fmaxf(fmaxf(q[0], q[1]), fmaxf(q[2], q[3]));
-  if (top < 0x1p120f) {  // a NaN beside finite values passes, and its own pair becomes NaN either way
+  const float top = amax3(amax3(q[0], q[1], q[2]), q[3], 0.f);  // keeps a NaN
+  if (top < 0x1p120f) {  // not with a NaN among them: one reciprocal would carry it to the pair's other value
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float2 t = upk(d[k]);

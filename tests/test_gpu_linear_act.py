@@ -370,3 +370,71 @@ def test_binding_refuses(L):
                  lambda: L.linear_act_bwd(y, x, w, L.LinearActCtx(), x_act="gelu")):
         with pytest.raises(L.LnFp8Error):
             call()
+
+
+NAN_ROWS = [8, 64, 300, 2048]  # few tokens, tokens on the columns, tiles of one and of several rounds
+
+
+def near_eight(N, cols):
+    """The other columns of the groups of eight that hold `cols`, and all columns outside those groups."""
+    eight = sorted({8 * (c // 8) + i for c in cols for i in range(8)} - set(cols))
+    return eight, [i for i in range(N) if i not in eight and i not in cols]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("act", ["gelu", "silu", "relu"])
+@pytest.mark.parametrize("where", ["w", "bias", "bias beside a far one"])
+@pytest.mark.parametrize("M", NAN_ROWS)
+def test_a_nan_feature_stays_in_its_column(L, M, where, act, dtype):
+    """A NaN in one row of w, or in one entry of the bias, makes that column NaN and no other. The activation of the other
+    columns of its group of eight may be computed in another way: both are within logistic_error of the exact value, and
+    half a step of the type. All other columns are the same bits."""
+    K, N, bad = 256, 776, [37, 100, 775]
+    x, w, b = draw(M, K, dtype, 1), draw(N, K, dtype, 2, 1.5 / math.sqrt(K)), draw(1, N, dtype, 3, 0.1)[0]
+    if where == "bias beside a far one":
+        b[[c ^ 1 for c in bad]] = -1000.0
+    y0, ctx0 = L.linear_act_fwd(x, w, b, act=act, save="h")
+    if where == "w":
+        w[bad, 5] = math.nan
+    else:
+        b[bad] = math.nan
+    y, ctx = L.linear_act_fwd(x, w, b, act=act, save="h")
+    near, rest = near_eight(N, bad)
+    assert torch.isnan(y[:, bad]).all() and torch.isnan(ctx.h[:, bad]).all()
+    assert torch.equal(ctx.h[:, near + rest], ctx0.h[:, near + rest]) and torch.equal(y[:, rest], y0[:, rest])
+    v = y0[:, near].double()
+    err = logistic_error(ctx0.h[:, near].double() * (1 + P.half(dtype)), act) if act != "relu" else 0
+    P.assert_within(y[:, near], v, (2 * err + 2 * P.half(dtype)) * 1.01 * v.abs() + 2 * P.tiny(dtype), "columns beside the NaN")
+    L.sync_status()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("act", ["gelu", "silu", "relu"])
+@pytest.mark.parametrize("far", [False, True])
+@pytest.mark.parametrize("M", NAN_ROWS)
+def test_a_nan_pre_activation_stays_in_its_column(L, M, far, act, dtype):
+    """One NaN of h makes its column's dbias and dw NaN, its row's dx, and nothing else. The slopes of its group of eight
+    may be computed in another way, each within slope_error; beside it a value whose e^-u leaves fp32."""
+    K, N, r, c = 136, 264, M - 2, 101
+    x, w, h, dy = draw(M, K, dtype, 1), draw(N, K, dtype, 2, 0.1), draw(M, N, dtype, 3), draw(M, N, dtype, 4, 0.1)
+    if far:
+        h[r, c ^ 1] = -100.0
+    g0 = L.linear_act_bwd(dy, x, w, L.LinearActCtx(act=act, h=h))
+    clean = h.double()
+    h = h.clone()
+    h[r, c] = math.nan
+    g = L.linear_act_bwd(dy, x, w, L.LinearActCtx(act=act, h=h))
+    near, rest = near_eight(N, [c])
+    assert torch.isnan(g.dbias[c]) and torch.isnan(g.dw[c]).all() and torch.isnan(g.dx[r]).all()
+    rows = [i for i in range(M) if i != r]
+    assert torch.equal(g.dx[rows], g0.dx[rows]) and torch.equal(g.dbias[rest], g0.dbias[rest]) and torch.equal(g.dw[rest], g0.dw[rest])
+    # the row's terms of these columns move by twice the slope's error, and as operands by a step of the type more
+    dz = dy.double().abs() * P.slope(clean, act).abs()
+    e = 2 * dy[r, near].double().abs() * (slope_error(clean[r, near], act) + P.U)
+    n = M / 600 + 8 + 8 + 608 / 8 + 8 + 40
+    P.assert_within(g.dbias[near], g0.dbias[near].double(), e + 2 * n * P.U * dz[:, near].sum(0), "dbias")
+    e16 = e + 2 * P.half(dtype) * dz[r, near] + 2 * P.tiny(dtype)
+    v = g0.dw[near].double()
+    tol = e16[:, None] * x[r].double().abs() + 2 * sum_error(M) * (dz[:, near].t() @ x.double().abs())
+    P.assert_within(g.dw[near], v, 1.01 * tol + 2 * P.half(dtype) * (v.abs() + 1.01 * tol) + 2 * P.tiny(dtype), "dw")
+    L.sync_status()
