@@ -18,6 +18,7 @@ namespace {
 constexpr int64_t kMaxRows = (1ll << 31) - 1;
 constexpr int64_t kMaxTokens = (1ll << 31) - 1024;  // linear_act: tile rows past the last token stay 32-bit numbers
 constexpr int64_t kMaxCols = 1ll << 30;
+constexpr int64_t kMaxFeature = (1ll << 30) - 32;  // linear_act: two column sums of each, rounded up to 32, are counted in 32 bits
 
 int elem_size(int elem) { return elem == LNFP8_FP32 ? 4 : 2; }
 
@@ -62,8 +63,9 @@ lnfp8_status fill_ld(int64_t* ld, int64_t cols, const char* name, const char* wh
 }
 // Feature sizes and row strides of the tensor-core products: 16-byte rows.
 lnfp8_status check_feature(int64_t v, const char* name, const char* who) {
-  if (v < 8 || v % 8 != 0 || v > kMaxCols)
-    return set_error(LNFP8_ERR_UNSUPPORTED_SHAPE, "%s: %s = %lld must be a positive multiple of 8", who, name, (long long)v);
+  if (v < 8 || v % 8 != 0 || v > kMaxFeature)
+    return set_error(LNFP8_ERR_UNSUPPORTED_SHAPE, "%s: %s = %lld must be a positive multiple of 8 up to %lld", who, name, (long long)v,
+                     (long long)kMaxFeature);
   return LNFP8_OK;
 }
 lnfp8_status fill_ld8(int64_t* ld, int64_t cols, const char* name, const char* who) {

@@ -536,7 +536,7 @@ int lnfp8_ctx_offsets(int op, int64_t M, int64_t D, int64_t F, int64_t* offsets,
  * and act_ckpt_* need the alignment of their element only, and any width;
  * rows that are multiples of 16 bytes on 16-byte boundaries run faster.
  * linear_act_* moves its tiles with TMA: 16-byte aligned pointers, K and N
- * multiples of 8, row strides multiples of 8 elements.
+ * multiples of 8 up to 2^30 - 32, row strides multiples of 8 elements.
  * NaN and Inf pass through the arithmetic as IEEE gives them. A workspace
  * belongs to one call at a time: calls on two streams, or two captured graphs
  * that may run at the same time, need one each. */

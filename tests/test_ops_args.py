@@ -173,6 +173,20 @@ def test_linear_act_bwd_refuses_both_forms_of_h(L):
     assert L._c_linear_act_bwd(ctypes.byref(a), None) == 1 and "h and a checkpoint" in L.last_error()
 
 
+@pytest.mark.parametrize("name", ["K", "N"])
+def test_linear_act_refuses_more_features_than_its_sums_count(L, name):
+    """The backward's two column sums of N, rounded up to whole blocks of 32, are a 32-bit number."""
+    for v in (1 << 30, (1 << 30) - 24):
+        f = L.CLinearActFwd(M=4, K=64, N=64, x=FAKE, w=FAKE, y=FAKE)
+        b = L.CLinearActBwd(M=4, K=64, N=64, dy=FAKE, x=FAKE, w=FAKE, dx=FAKE, dw=FAKE, workspace=FAKE, workspace_bytes=1 << 60)
+        for a, call in ((f, L._c_linear_act_fwd), (b, L._c_linear_act_bwd)):
+            setattr(a, name, v)
+            assert call(ctypes.byref(a), None) == 2 and f"{name} = {v}" in L.last_error()
+    f = L.CLinearActFwd(M=0, K=64, N=64, w=FAKE)
+    setattr(f, name, (1 << 30) - 32)
+    assert L._c_linear_act_fwd(ctypes.byref(f), None) == 0
+
+
 STRUCTS = {"lnfp8_ckpt": "CCkpt", "lnfp8_layernorm_fwd_args": "CLayerNormFwd", "lnfp8_layernorm_bwd_args": "CLayerNormBwd",
            "lnfp8_linear_act_fwd_args": "CLinearActFwd", "lnfp8_linear_act_bwd_args": "CLinearActBwd"}
 
