@@ -708,14 +708,12 @@ def _flat(t, name, shape, dtype, dev) -> None:
 
 
 def _given_ws(t, dev):
-    """A workspace's address and bytes (all of them there: contiguous)."""
-    if t is None:
-        return None, 0
+    """Checks a workspace that the caller keeps (all of its bytes there: contiguous)."""
     if t.get_device() != dev:
         _where(t, "grads.workspace")
     if not t.is_contiguous():
         raise ValueError("grads.workspace is not contiguous")
-    return t.data_ptr(), t.nbytes
+    return t
 
 
 # The current stream's handle without the Stream object around it (4 us less per call where
@@ -858,6 +856,8 @@ def layernorm_fwd(x, gamma, beta, *, eps=1e-5, residual=None, ckpt=False, y=None
 
 @dataclass
 class LayerNormGrads:
+    """Gradients of layernorm_bwd. workspace: scratch that the caller keeps from call to call; None: each call takes
+    its own from the current stream's memory and gives it back."""
     dx: torch.Tensor
     dgamma: torch.Tensor
     dbeta: torch.Tensor
@@ -868,9 +868,14 @@ def layernorm_bwd_workspace_size(M, D) -> int:
     return int(_c_layernorm_bwd_ws(M, D))
 
 
-def layernorm_grads(M, D, *, dtype=torch.bfloat16, device="cuda") -> LayerNormGrads:
+def _layernorm_ws(M, D, device):
+    return _e((_c_layernorm_bwd_ws(M, D),), torch.uint8, device)
+
+
+def layernorm_grads(M, D, *, dtype=torch.bfloat16, device="cuda", workspace=True) -> LayerNormGrads:
+    """Gradients of one layernorm_bwd, with a workspace to keep."""
     return LayerNormGrads(_e((M, D), dtype, device), _e((D,), torch.float32, device), _e((D,), torch.float32, device),
-                          _e((_c_layernorm_bwd_ws(M, D),), torch.uint8, device))
+                          _layernorm_ws(M, D, device) if workspace else None)
 
 
 def layernorm_bwd(dy, ctx: LayerNormCtx, gamma, *, dresidual=None, grads: LayerNormGrads | None = None,
@@ -899,15 +904,15 @@ def layernorm_bwd(dy, ctx: LayerNormCtx, gamma, *, dresidual=None, grads: LayerN
     lddr = _rows(dresidual, "dresidual", M, D, dt, dev) if dresidual is not None else 0
     lddx = D
     if grads is None:
-        grads = layernorm_grads(M, D, dtype=dt, device=dy.device)
+        grads = layernorm_grads(M, D, dtype=dt, device=dy.device, workspace=False)
     else:
         lddx = _rows(grads.dx, "grads.dx", M, D, dt, dev)
         _flat(grads.dgamma, "grads.dgamma", (D,), torch.float32, dev)
         _flat(grads.dbeta, "grads.dbeta", (D,), torch.float32, dev)
-    ws, ws_bytes = _given_ws(grads.workspace, dev)
+    ws = _layernorm_ws(M, D, dy.device) if grads.workspace is None else _given_ws(grads.workspace, dev)
     a = CLayerNormBwd(M, D, elem, pe, dy.data_ptr(), x, mu, ctx.rsigma.data_ptr(), ck, gamma.data_ptr(), _ptr(dresidual),
-                      grads.dx.data_ptr(), grads.dgamma.data_ptr(), grads.dbeta.data_ptr(), ws, ws_bytes, lddy, ldx,
-                      lddr, lddx)
+                      grads.dx.data_ptr(), grads.dgamma.data_ptr(), grads.dbeta.data_ptr(), ws.data_ptr(), ws.nbytes, lddy,
+                      ldx, lddr, lddx)
     _check(_c_layernorm_bwd(C.byref(a), _raw_stream(dev)))
     return grads
 
@@ -977,6 +982,8 @@ def linear_act_fwd(x, w, bias=None, *, act="none", residual=None, save="none", y
 
 @dataclass
 class LinearActGrads:
+    """Gradients of linear_act_bwd. workspace: scratch (dz and a restored x, most of it) that the caller keeps from call
+    to call; None: each call takes its own from the current stream's memory and gives it back."""
     dx: torch.Tensor | None
     dw: torch.Tensor | None
     dbias: torch.Tensor | None
@@ -987,12 +994,16 @@ def linear_act_bwd_workspace_size(M, K, N, *, has_act, x_from_ckpt) -> int:
     return int(_c_linear_act_bwd_ws(M, K, N, int(has_act), int(x_from_ckpt)))
 
 
+def _linear_act_ws(M, K, N, act, x_from_ckpt, device):
+    return _e((_c_linear_act_bwd_ws(M, K, N, int(act != "none"), int(x_from_ckpt)),), torch.uint8, device)
+
+
 def linear_act_grads(M, K, N, *, act="none", x_from_ckpt=False, dx=True, dw=True, bias=True, dtype=torch.bfloat16,
-                     device="cuda") -> LinearActGrads:
-    """Gradients and workspace of one linear_act_bwd; dx, dw, bias=False leave theirs out."""
-    ws = _c_linear_act_bwd_ws(M, K, N, int(act != "none"), int(x_from_ckpt))
+                     device="cuda", workspace=True) -> LinearActGrads:
+    """Gradients of one linear_act_bwd, with a workspace to keep; dx, dw, bias=False leave theirs out."""
     return LinearActGrads(_e((M, K), dtype, device) if dx else None, _e((N, K), dtype, device) if dw else None,
-                          _e((N,), torch.float32, device) if bias else None, _e((ws,), torch.uint8, device))
+                          _e((N,), torch.float32, device) if bias else None,
+                          _linear_act_ws(M, K, N, act, x_from_ckpt, device) if workspace else None)
 
 
 def linear_act_bwd(dy, x, w, ctx: LinearActCtx, *, x_act="none", x_gamma=None, x_beta=None,
@@ -1031,8 +1042,7 @@ def linear_act_bwd(dy, x, w, ctx: LinearActCtx, *, x_act="none", x_gamma=None, x
         _flat(x_beta, "x_beta", (K,), dt, dev)
     lddx = K
     if grads is None:
-        grads = linear_act_grads(M, K, N, act=ctx.act, x_from_ckpt=xck is not _NO_CKPT, dw=x is not None, dtype=dt,
-                                 device=dy.device)
+        grads = linear_act_grads(M, K, N, dw=x is not None, dtype=dt, device=dy.device, workspace=False)
     else:
         if grads.dx is not None:
             lddx = _rows(grads.dx, "grads.dx", M, K, dt, dev)
@@ -1040,8 +1050,9 @@ def linear_act_bwd(dy, x, w, ctx: LinearActCtx, *, x_act="none", x_gamma=None, x
             _flat(grads.dw, "grads.dw", (N, K), dt, dev)
         if grads.dbias is not None:
             _flat(grads.dbias, "grads.dbias", (N,), torch.float32, dev)
-    ws, ws_bytes = _given_ws(grads.workspace, dev)
+    ws = grads.workspace
+    ws = _linear_act_ws(M, K, N, ctx.act, xck is not _NO_CKPT, dy.device) if ws is None else _given_ws(ws, dev)
     a = CLinearActBwd(M, K, N, elem, ia, dy.data_ptr(), xp, xck, _act(x_act), _ptr(x_gamma), _ptr(x_beta), w.data_ptr(), h,
-                      hck, _ptr(grads.dx), _ptr(grads.dw), _ptr(grads.dbias), ws, ws_bytes, lddy, ldx, lddx)
+                      hck, _ptr(grads.dx), _ptr(grads.dw), _ptr(grads.dbias), ws.data_ptr(), ws.nbytes, lddy, ldx, lddx)
     _check(_c_linear_act_bwd(C.byref(a), _raw_stream(dev)))
     return grads

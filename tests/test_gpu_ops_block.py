@@ -128,3 +128,37 @@ def test_two_streams_at_once(L):
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
+def test_gradients_keep_no_scratch(L):
+    """What the backward calls return holds the gradients and nothing else; handed back, they are filled again (a
+    training loop's static buffers), with a workspace of the caller's or one of the call's own: the same bits."""
+    M, D, F = 1030, 256, 1024
+    p = weights(D, F)
+    x, dy = draw(M, D, 7), draw(M, D, 8, 0.1)
+    _, c0, c1 = forward(L, x, p)
+    da = draw(M, F, 9, 0.1)
+    calls = {
+        "linear_act": lambda grads=None: L.linear_act_bwd(da, c0.ckpt, p["w1"], c1, x_gamma=p["gamma"], x_beta=p["beta"], grads=grads),
+        "layernorm": lambda grads=None: L.layernorm_bwd(dy, c0, p["gamma"], dresidual=dy, grads=grads),
+    }
+    own = {"linear_act": L.linear_act_grads(M, D, F, act="gelu", x_from_ckpt=True), "layernorm": L.layernorm_grads(M, D)}
+
+    def check(name, call):
+        call()
+        torch.cuda.synchronize()
+        held = "requested_bytes.all.current"
+        before = torch.cuda.memory_stats()[held]
+        g = call()
+        fields = {k: v for k, v in vars(g).items() if v is not None}
+        assert "workspace" not in fields
+        assert torch.cuda.memory_stats()[held] - before == sum(v.nbytes for v in fields.values()), name
+        want = {k: v.clone() for k, v in fields.items()}
+        for again in (call(g), call(own[name])):
+            for k, v in want.items():
+                assert torch.equal(getattr(again, k), v), (name, k)
+                getattr(again, k).zero_()
+        assert g.workspace is None and own[name].workspace is not None
+
+    for name, call in calls.items():
+        check(name, call)
