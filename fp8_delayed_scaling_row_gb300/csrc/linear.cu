@@ -905,8 +905,10 @@ lnfp8_status linear_act_bwd_launch(const lnfp8_linear_act_bwd_args* a, cudaStrea
   void* x_ws = ws;
   if (xck) ws += up256(a->M * a->K * 2);
   // x = v gamma + beta from a checkpoint's values v: dw = (dz^T v) gamma + (sum dz) beta, applied in the
-  // product's epilogue. v has four significant bits, so the 16-bit operand is exact and x is never rounded. The
-  // sum is of dz as rounded for the product, so that where v gamma and beta cancel, dw does too.
+  // product's epilogue, and x is never formed or rounded. v has at most four significant bits: a bf16 operand holds it
+  // exactly, an fp16 one where it lies in fp16's range (past 65504 it saturates, and below 2^-14 it keeps steps of 2^-24,
+  // which the smallest codes do not reach in E4M3 blocks whose largest value is under 0.007 and in E5M2 blocks under
+  // 112). The sum is of dz as rounded for the product, so that where v gamma and beta cancel, dw does too.
   const bool affine = a->dw && xck && a->x_gamma;
   float* db = a->dbias;
   float* dbr = nullptr;

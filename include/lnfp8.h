@@ -649,7 +649,8 @@ typedef struct {
   int act;                /* of the forward */
   const void* dy;         /* [M, N] */
   const void* x;          /* [M, K] the forward's input; NULL with x_ckpt or without dw */
-  lnfp8_ckpt x_ckpt;      /* a checkpoint to restore x from: x = x_act(v), or v * x_gamma + x_beta */
+  lnfp8_ckpt x_ckpt;      /* a checkpoint to restore x from: x = x_act(v) rounded to elem, or v * x_gamma + x_beta with
+                           * v in elem (exact in bf16; fp16 saturates beyond 65504 and has steps of 2^-24) and x unrounded */
   int x_act;              /* lnfp8_act: e.g. the previous layer's activation of its checkpointed pre-activation */
   const void* x_gamma;    /* [K] or NULL: a LayerNorm's gamma and beta with its checkpointed rows */
   const void* x_beta;

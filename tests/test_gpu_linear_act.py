@@ -438,3 +438,35 @@ def test_a_nan_pre_activation_stays_in_its_column(L, M, far, act, dtype):
     tol = e16[:, None] * x[r].double().abs() + 2 * sum_error(M) * (dz[:, near].t() @ x.double().abs())
     P.assert_within(g.dw[near], v, 1.01 * tol + 2 * P.half(dtype) * (v.abs() + 1.01 * tol) + 2 * P.tiny(dtype), "dw")
     L.sync_status()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("std", [1.0, 1e-3])
+@pytest.mark.parametrize("M,K,N", [(64, 72, 200), (300, 264, 136), (2049, 520, 264), (9001, 520, 264)])
+def test_weight_gradient_of_normalised_rows_does_not_round_x(L, M, K, N, std, dtype):
+    """dw of x = v gamma + beta: the product reads v, exactly in bf16 and within half a step of fp16's subnormals, and x is
+    never formed. Left are the products' and the column sums' fp32 roundings, of v gamma and beta apart, and dw's own."""
+    xck = L.act_ckpt_save(draw(M, K, dtype, 1, std))
+    w, dy = draw(N, K, dtype, 2, 0.1), draw(M, N, dtype, 3, 0.1)
+    gamma, beta = draw(1, K, dtype, 4, 0.1, 1.0)[0], draw(1, K, dtype, 5, 0.1 * std)[0]
+    g = L.linear_act_bwd(dy, xck, w, L.LinearActCtx(), x_gamma=gamma, x_beta=beta)
+    v, d, ga, be = P.decode(xck.codes, xck.scales, 0), dy.double(), gamma.double(), beta.double()
+    want = d.t() @ (v * ga + be)
+    tol = (sum_error(M) + 4 * P.U) * (d.abs().t() @ (v.abs() * ga.abs() + be.abs()))
+    if dtype == torch.float16:
+        tol = tol + d.abs().sum(0)[:, None] * ga.abs() * P.tiny(dtype)
+    tol = 1.01 * tol
+    P.assert_within(g.dw, want, tol + P.half(dtype) * (want.abs() + tol) + P.tiny(dtype), "dw")
+
+
+def test_restored_inputs_saturate_at_the_types_largest_value(L):
+    """A checkpoint's values enter the products in the products' type: beyond 65504 fp16 holds 65504, gamma or not."""
+    x = torch.full((40, 32), 1e6, device="cuda")
+    x[:, :16] = -1e6
+    xck, w = L.act_ckpt_save(x), torch.zeros(8, 32, dtype=torch.float16, device="cuda")
+    dy = torch.full((40, 8), 2.0 ** -10, dtype=torch.float16, device="cuda")
+    sign = x[0].sign()
+    one, zero = torch.full_like(w[0], 0.125), torch.zeros_like(w[0])
+    assert torch.equal(L.linear_act_bwd(dy, xck, w, L.LinearActCtx()).dw[3], (40 * 2.0 ** -10 * 65504 * sign).half())
+    g = L.linear_act_bwd(dy, xck, w, L.LinearActCtx(), x_gamma=one, x_beta=zero)
+    assert torch.equal(g.dw[3], (40 * 2.0 ** -13 * 65504 * sign).half())
