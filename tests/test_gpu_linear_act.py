@@ -470,3 +470,13 @@ def test_restored_inputs_saturate_at_the_types_largest_value(L):
     assert torch.equal(L.linear_act_bwd(dy, xck, w, L.LinearActCtx()).dw[3], (40 * 2.0 ** -10 * 65504 * sign).half())
     g = L.linear_act_bwd(dy, xck, w, L.LinearActCtx(), x_gamma=one, x_beta=zero)
     assert torch.equal(g.dw[3], (40 * 2.0 ** -13 * 65504 * sign).half())
+
+
+# a few tokens, K long enough for one, two, four and eight warps to a row, whole and ragged pieces
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,K,N", [(1, 1000, 5000), (3, 2056, 2000), (2, 4104, 1032), (4, 8192, 264), (1, 16392, 136), (3, 12280, 16)])
+def test_a_few_tokens_over_long_rows(L, M, K, N, dtype):
+    x, w, b = whole(M, K, dtype, 1), whole(N, K, dtype, 2), whole(1, N, dtype, 3)[0]
+    assert torch.equal(L.linear_act_fwd(x, w, b)[0], (x.double() @ w.double().t() + b.double()).to(dtype))
+    x, w, b = draw(M, K, dtype, 1), draw(N, K, dtype, 2, 1.5 / math.sqrt(K)), draw(1, N, dtype, 3, 0.1)[0]
+    check_fwd(L, x, w, b, "gelu", draw(M, N, dtype, 4), "h")
