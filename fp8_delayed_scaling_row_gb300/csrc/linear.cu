@@ -425,7 +425,7 @@ struct DactParams {
   void* dz;      // NULL: no activation, only the column sums
   float* part;   // [row blocks][N] or NULL; with `both` [row blocks][2][N]: the sums of dz, then of dz as rounded
   int both;
-  // or, with clusters of kDactCluster row blocks: the sums themselves
+  // or, from clusters of kDactCluster row blocks (dact_cluster_rows): the sums themselves
   float* db;
   float* dbr;
   int64_t M, lddy, pitch;
@@ -435,7 +435,14 @@ struct DactParams {
 enum DactSource { DACT_NONE, DACT_TENSOR, DACT_CKPT };  // no activation; h as a tensor; h as a checkpoint
 constexpr int kDactBlocksPerSm = 4;
 constexpr int kDactCluster = 8;
-constexpr int64_t kDactClusterRows = 1024;  // up to here 8 row blocks are enough and the sums need no second launch
+// Up to how many rows the column sums come from clusters of 8 row blocks, without a second launch. Of the whole
+// backward, us with one launch and with two, GELU from a checkpoint (tokens x K x N): 65 x 768 x 768 8.0 and 9.7, 256 x
+// 4096 x 4096 32.3 and 33.0, 320 x 768 x 2304 19.3 and 18.8, 512 x 768 x 768 11.6 and 10.5, 1000 x 768 x 2304 32.1 and 19.8.
+// Without an activation, where dy alone is read: 512 x 768 x 1536 10.0 and 10.9, 512 x 4096 x 4096 34.2 and 34.2, 1024 x 768
+// x 1536 11.7 and 12.6, 1024 x 1024 x 1024 10.8 and 11.4, 1000 x 768 x 2304 17.5 and 15.4, 1024 x 1536 x 1536 18.6 and 16.8.
+inline int64_t dact_cluster_rows(int64_t K, int64_t N, bool has_act) {
+  return has_act ? 320 : K * N <= 3 << 19 ? 1024 : 512;
+}
 constexpr int kDactRing = 6;  // rows of a thread in its shared-memory ring: 5 on their way while one is used
 
 template <int SRC>
@@ -701,8 +708,8 @@ lnfp8_status dact_launch(const DactParams& p, dim3 grid, cudaStream_t st) {
 }
 
 // Rows of the dz pass per block: one wave of resident blocks.
-int64_t dact_rows_per_block(int64_t M, int64_t N) {
-  if (M <= kDactClusterRows) return (M + 8 * kDactCluster - 1) / (8 * kDactCluster) * 8;
+int64_t dact_rows_per_block(int64_t M, int64_t K, int64_t N, bool has_act) {
+  if (M <= dact_cluster_rows(K, N, has_act)) return (M + 8 * kDactCluster - 1) / (8 * kDactCluster) * 8;
   const int64_t col_blocks = (N + 255) / 256;
   const int64_t row_blocks = max64(1, (int64_t)num_sms() * kDactBlocksPerSm / col_blocks);
   const int64_t rows = (M + row_blocks - 1) / row_blocks;
@@ -888,7 +895,7 @@ static int64_t wgrad_bytes(int64_t M, int64_t K, int64_t N) {
 }
 int64_t linear_act_bwd_ws_bytes(int64_t M, int64_t K, int64_t N, bool has_act, bool x_from_ckpt) {
   if (M == 0 || N == 0) return 0;
-  const int64_t rpb = dact_rows_per_block(M, N);
+  const int64_t rpb = dact_rows_per_block(M, K, N, has_act);
   return (has_act ? up256(M * N * 2) : 0) + (x_from_ckpt ? up256(M * K * 2) + 2 * up256(N * 4) : 0) +
          up256((M + rpb - 1) / rpb * N * 4 * (has_act && x_from_ckpt ? 2 : 1)) + wgrad_bytes(M, K, N);
 }
@@ -931,7 +938,7 @@ lnfp8_status linear_act_bwd_launch(const lnfp8_linear_act_bwd_args* a, cudaStrea
     p.codes = a->h_ckpt.codes;
     p.scales = a->h_ckpt.scales;
     p.dz = dz_ws;
-    const bool clustered = db && a->M <= kDactClusterRows;
+    const bool few_rows = a->M <= dact_cluster_rows(a->K, a->N, has_act), clustered = db && few_rows;
     p.part = db && !clustered ? reinterpret_cast<float*>(ws) : nullptr;
     p.db = clustered ? db : nullptr;
     p.dbr = dbr;
@@ -941,8 +948,8 @@ lnfp8_status linear_act_bwd_launch(const lnfp8_linear_act_bwd_args* a, cudaStrea
     p.pitch = lnfp8_act_ckpt_scale_pitch(a->N);
     p.N = (int)a->N;
     p.dt = a->h_ckpt.dtype;
-    p.rows_per_block = (int)dact_rows_per_block(a->M, a->N);
-    const int64_t row_blocks = a->M <= kDactClusterRows ? kDactCluster : (a->M + p.rows_per_block - 1) / p.rows_per_block;
+    p.rows_per_block = (int)dact_rows_per_block(a->M, a->K, a->N, has_act);
+    const int64_t row_blocks = few_rows ? kDactCluster : (a->M + p.rows_per_block - 1) / p.rows_per_block;
     const dim3 grid((unsigned)((a->N + 255) / 256), (unsigned)row_blocks);
     auto pick = [&](auto elem) {
       constexpr int E = decltype(elem)::value;
