@@ -443,22 +443,28 @@ constexpr int kDactCluster = 8;
 inline int64_t dact_cluster_rows(int64_t K, int64_t N, bool has_act) {
   return has_act ? 320 : K * N <= 3 << 19 ? 1024 : 512;
 }
-constexpr int kDactRing = 6;  // rows of a thread in its shared-memory ring: 5 on their way while one is used
-
 template <int SRC>
 struct DactShape {
   static constexpr int H_OFF = 16, S_OFF = SRC == DACT_TENSOR ? 32 : 24;  // bytes per thread: dy, h or codes, scale word
   static constexpr int BYTES = SRC == DACT_NONE ? 16 : SRC == DACT_TENSOR ? 32 : 28;
-  static constexpr size_t SMEM = (size_t)kDactRing * BYTES * 256;
+  // Rows of a thread in its ring: all but one are on their way while that one is used. With h as a tensor six would leave
+  // room for three blocks an SM, where the grid has four to one (8192 x 8192, GELU 94 us; six rows and a grid of three
+  // 83; five rows 74, four 72; ReLU 65, 68, 67, 68; 8192 x 2048, GELU 28.4, 25.4, 23.8, 22.7, ReLU 20.3, 18.7, 19.0, 19.0).
+  static constexpr int RING = SRC == DACT_TENSOR ? 4 : 6;
+  static constexpr size_t SMEM = (size_t)RING * BYTES * 256;
+  static constexpr size_t RED = 8 * 32 * 9 * sizeof(float);
+  // of an SM's 228 KB each block takes 1 KB for itself
+  static_assert(kDactBlocksPerSm * (SMEM + RED + 1024) <= 228 * 1024, "one wave of kDactBlocksPerSm blocks an SM");
 };
 
 template <int ELEM, int SRC, int ACT>
 __global__ void __launch_bounds__(256, kDactBlocksPerSm) lin_dact_kernel(const DactParams p) {
   using S = DactShape<SRC>;
-  constexpr int P = kDactRing - 1;
+  constexpr int P = S::RING - 1;
   constexpr uint32_t SB = S::BYTES * 256;
   __shared__ float red[8][32][9];
-  extern __shared__ uint4 ring[];  // [kDactRing][BYTES * 256], each kind an array over the threads
+  static_assert(sizeof(red) == S::RED);
+  extern __shared__ uint4 ring[];  // [RING][BYTES * 256], each kind an array over the threads
   pdl_wait();
   pdl_launch_dependents();
   const int cl = threadIdx.x & 31, rl = threadIdx.x >> 5;
