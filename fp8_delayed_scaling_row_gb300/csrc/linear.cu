@@ -321,12 +321,12 @@ lin_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ T
 }
 
 // ------------------------------------------------------------ a few tokens
-// One to four tokens: bound by the weight's bytes, so each warp streams kRowsPerWarp rows of w with
+// One to four tokens (takes_few): bound by the weight's bytes, so each warp streams kRowsPerWarp rows of w with
 // 16-byte loads straight into FMAs; x sits in shared memory in its own type. WK warps share a
 // row group (K cut into WK pieces, added in order) when there are too few rows to fill the SMs.
 // A lane's partial sum covers every 256th group of 8 columns; a warp's lanes are added by shuffles.
 constexpr int kRowsPerWarp = 2;
-constexpr int kFewTokens = 4;
+constexpr int kFewTokens = 4, kFewOutputs = 10240;
 constexpr int kFewMaxX = 96 * 1024;  // bytes of x in shared memory
 
 template <int MT, bool F16>
@@ -803,10 +803,14 @@ int wgrad_pieces(int64_t M, int64_t K, int64_t N) {
   return (int)max64(1, min64(min64(8, pairs / max64(tiles, 1)), kb / 16));
 }
 
-// The forward of one to four tokens, without a checkpoint (whose blocks span more columns than a warp
-// has here; a decoding step keeps none).
+// The forward of one token, and of two to four with few outputs, without a checkpoint (whose blocks span more columns
+// than a warp has here; a decoding step keeps none). FMAs cost by the token and x is staged once a block; the form with
+// tokens on the accumulator's columns costs the same up to 16 of them. us, this form and that (K x N): one token 4096 x 1024 3.3
+// and 6.6, 4096 x 4096 7.8 and 9.0, 4096 x 14336 21.4 and 21.4; two 4096 x 4096 8.4 and 9.1, 4096 x 6144 13.8 and 12.2;
+// four 4096 x 1024 5.3 and 6.7, 4096 x 2048 7.4 and 7.2, 4096 x 4096 10.2 and 9.2, 4096 x 14336 26.6 and 21.5.
 bool takes_few(const LinGemm& g) {
-  return g.M <= kFewTokens && !g.a_mn && !g.b_mn && !g.ckpt.codes && g.K * (g.M > 2 ? 4 : g.M) * 2 <= kFewMaxX;
+  return g.M <= kFewTokens && (g.M == 1 || g.M * g.N <= kFewOutputs) && !g.a_mn && !g.b_mn && !g.ckpt.codes &&
+         g.K * (g.M > 2 ? 4 : g.M) * 2 <= kFewMaxX;
 }
 template <int MT, bool F16>
 lnfp8_status few_launch(const LinGemm& g, cudaStream_t st) {

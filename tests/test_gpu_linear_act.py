@@ -472,9 +472,11 @@ def test_restored_inputs_saturate_at_the_types_largest_value(L):
     assert torch.equal(g.dw[3], (40 * 2.0 ** -13 * 65504 * sign).half())
 
 
-# a few tokens, K long enough for one, two, four and eight warps to a row, whole and ragged pieces
+# a few tokens: K long enough for one, two, four and eight warps to a row, whole and ragged pieces; and outputs that are
+# too many for that form
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("M,K,N", [(1, 1000, 5000), (3, 2056, 2000), (2, 4104, 1032), (4, 8192, 264), (1, 16392, 136), (3, 12280, 16)])
+@pytest.mark.parametrize("M,K,N", [(1, 1000, 5000), (3, 2056, 2000), (2, 4104, 1032), (4, 8192, 264), (1, 16392, 136), (3, 12280, 16),
+                                   (2, 264, 8200), (4, 1032, 2568), (3, 4104, 4104)])
 def test_a_few_tokens_over_long_rows(L, M, K, N, dtype):
     x, w, b = whole(M, K, dtype, 1), whole(N, K, dtype, 2), whole(1, N, dtype, 3)[0]
     assert torch.equal(L.linear_act_fwd(x, w, b)[0], (x.double() @ w.double().t() + b.double()).to(dtype))
