@@ -324,7 +324,7 @@ lin_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ T
 // One to four tokens (takes_few): bound by the weight's bytes, so each warp streams kRowsPerWarp rows of w with
 // 16-byte loads straight into FMAs; x sits in shared memory in its own type. WK warps share a
 // row group (K cut into WK pieces, added in order) when there are too few rows to fill the SMs.
-// A lane's partial sum covers every 256th group of 8 columns; a warp's lanes are added by shuffles.
+// A lane's partial sum covers every 32nd group of 8 columns; a warp's lanes are added by shuffles.
 constexpr int kRowsPerWarp = 2;
 constexpr int kFewTokens = 4, kFewOutputs = 10240;
 constexpr int kFewMaxX = 96 * 1024;  // bytes of x in shared memory
@@ -834,7 +834,10 @@ lnfp8_status few_by_tokens(const LinGemm& g, cudaStream_t st) {
   return g.M == 1 ? few_launch<1, F16>(g, st) : g.M == 2 ? few_launch<2, F16>(g, st) : few_launch<4, F16>(g, st);
 }
 
-// Few tokens: K pieces while they run on SMs that would idle and each keeps a few K blocks.
+// Few tokens: K pieces while they run on SMs that would idle and each keeps a few K blocks. 8 tokens, us with 1, 2 and 4
+// pieces (K x N; 64 tokens within 5% the same way): 768 x 2304 5.0, 4.9, 4.6; 4096 x 1024 14.4, 9.4, 6.7; 4096 x 4096 14.9,
+// 10.4, 9.3; 2048 x 8192 (two fill the SMs) 9.5, 9.1, 13.2; 4096 x 14336 (one fills them) 21.7, -, 34.3. The rule takes 4, 4,
+// 4, 2 and 1; the one shape where it was not best is 64 x 1024 x 4096, 7.2, 6.6, 7.0.
 int swap_splits(const LinGemm& g) {
   const int64_t tiles = (g.N + 127) / 128, kb = (g.K + BK - 1) / BK;
   int S = 1;

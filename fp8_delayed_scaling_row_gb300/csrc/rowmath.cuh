@@ -367,10 +367,11 @@ __device__ __forceinline__ float ckpt_clamp(float v) {
 // ------------------------------------------------------------ activations
 // GELU is the tanh form, written with the logistic function s(u) = 1/(1 + e^-u):
 //   gelu(z) = z s(u), u = 2 sqrt(2/pi) (z + c z^3);  gelu'(z) = s + z s (1 - s) u'
-// silu(z) = z s(z); silu'(z) = s + z s (1 - s). ex2.approx and rcp.approx keep
-// s to about 2^-22 relative, also in the tails, where 1 + tanh would cancel. The .ftz forms: 2^x below
-// 2^-126 is added to 1, and 1/(1 + 2^x) below 2^-126 is a value of no more than 128 * 2^-126 lost; the plain
-// forms cost four more instructions each for it.
+// silu(z) = z s(z); silu'(z) = s + z s (1 - s). ex2.approx and rcp.approx (2 ulp each) and four
+// roundings of u log2(e) keep s within (16 + 4 |u|) 2^-24 relative: 2^-20 near 0, 2^-19 at u = -4, 2^-15 at u = -90 (1 + tanh
+// would have cancelled long before). That is far below a 16-bit output's half step (2^-8, 2^-11); an fp32 output shows it.
+// The .ftz forms: 2^x below 2^-126 is added to 1, and 1/(1 + 2^x) below 2^-126 is a value of no more than
+// 128 * 2^-126 lost; the plain forms cost four more instructions each for it.
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGelu2K = 1.5957691216057308f;  // 2 sqrt(2/pi)
 constexpr float kGelu2KC = kGelu2K * 0.044715f;

@@ -542,7 +542,9 @@ int lnfp8_ctx_offsets(int op, int64_t M, int64_t D, int64_t F, int64_t* offsets,
  * that may run at the same time, need one each. */
 typedef enum { LNFP8_BF16 = 0, LNFP8_FP16 = 1, LNFP8_FP32 = 2 } lnfp8_elem;
 
-/* Activations: GELU is the tanh form, SILU is z / (1 + e^-z). */
+/* Activations: GELU is the tanh form, SILU is z / (1 + e^-z). Computed in fp32,
+ * the logistic factor within (16 + 4 |u|) 2^-24 of its value (u the exponent's
+ * argument, z for SILU), whatever the output's type. */
 typedef enum { LNFP8_ACT_NONE = 0, LNFP8_ACT_GELU = 1, LNFP8_ACT_RELU = 2, LNFP8_ACT_SILU = 3 } lnfp8_act;
 
 /* An 8-bit checkpoint of a [rows, cols] tensor: codes [rows, cols], and for each
@@ -551,7 +553,8 @@ typedef enum { LNFP8_ACT_NONE = 0, LNFP8_ACT_GELU = 1, LNFP8_ACT_RELU = 2, LNFP8
  * value = code * 2^(b - 127). b is the least byte with max|v| <= fp8_max * 2^(b - 127)
  * over the block; codes round to nearest even. A block that holds an Inf or NaN
  * has b = 255 and restores as NaN throughout. The bytes of a scale row past the
- * last block are neither read nor defined. codes == NULL: no checkpoint.
+ * last block hold nothing: calls may write them, and do not use them. codes == NULL:
+ * no checkpoint.
  * scales must be 4-byte aligned. */
 typedef struct {
   uint8_t* codes;
@@ -640,7 +643,10 @@ typedef struct {
 } lnfp8_linear_act_fwd_args;
 
 /* Linear layer with its epilogue: z = x . w^T + bias (fp32), y = T(act(z) + residual);
- * h = T(z), or z as a checkpoint, saved on request. */
+ * h = T(z), or z as a checkpoint, saved on request. Products are summed in fp32 by the
+ * tensor cores, within (K / 16 + 8) 2^-22 of the sum of the terms' magnitudes, a little
+ * coarser than fp32 multiply-adds: codes of a checkpoint next to a rounding border can
+ * differ from theirs. */
 lnfp8_status linear_act_fwd(const lnfp8_linear_act_fwd_args* args, lnfp8_stream stream);
 
 typedef struct {
@@ -666,7 +672,7 @@ typedef struct {
 } lnfp8_linear_act_bwd_args;
 
 /* Backward of linear_act_fwd: dz = dy * act'(h) (fp32; rounded to the type for the
- * products), dbias = sum_rows dz (before that rounding, added in a fixed order),
+ * products, half a step of each term), dbias = sum_rows dz (before that rounding, added in a fixed order),
  * dx = T(dz . w), dw = T(dz^T . x). The residual's gradient is dy itself. With M = 0,
  * dw and dbias are zero. The same call gives the same bits. The workspace need
  * not be initialised. */
