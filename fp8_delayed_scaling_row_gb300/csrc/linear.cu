@@ -443,6 +443,7 @@ constexpr int kDactCluster = 8;
 inline int64_t dact_cluster_rows(int64_t K, int64_t N, bool has_act) {
   return has_act ? 320 : K * N <= 3 << 19 ? 1024 : 512;
 }
+
 template <int SRC>
 struct DactShape {
   static constexpr int H_OFF = 16, S_OFF = SRC == DACT_TENSOR ? 32 : 24;  // bytes per thread: dy, h or codes, scale word

@@ -672,10 +672,10 @@ typedef struct {
 } lnfp8_linear_act_bwd_args;
 
 /* Backward of linear_act_fwd: dz = dy * act'(h) (fp32; rounded to the type for the
- * products, half a step of each term), dbias = sum_rows dz (before that rounding, added in a fixed order),
- * dx = T(dz . w), dw = T(dz^T . x). The residual's gradient is dy itself. With M = 0,
- * dw and dbias are zero. The same call gives the same bits. The workspace need
- * not be initialised. */
+ * products, half a step of each term), dbias = sum_rows dz (before that rounding,
+ * added in a fixed order), dx = T(dz . w), dw = T(dz^T . x). The residual's gradient
+ * is dy itself. With M = 0, dw and dbias are zero. The same call gives the same bits.
+ * The workspace need not be initialised. */
 lnfp8_status linear_act_bwd(const lnfp8_linear_act_bwd_args* args, lnfp8_stream stream);
 
 /* Bytes of linear_act_bwd's workspace on the current device, for a forward with
