@@ -482,3 +482,14 @@ def test_a_few_tokens_over_long_rows(L, M, K, N, dtype):
     assert torch.equal(L.linear_act_fwd(x, w, b)[0], (x.double() @ w.double().t() + b.double()).to(dtype))
     x, w, b = draw(M, K, dtype, 1), draw(N, K, dtype, 2, 1.5 / math.sqrt(K)), draw(1, N, dtype, 3, 0.1)[0]
     check_fwd(L, x, w, b, "gelu", draw(M, N, dtype, 4), "h")
+
+
+# the last number of tokens whose bias sums come from one launch, and the next: without an activation small and large
+# weights, with one
+@pytest.mark.parametrize("M,K,N,act,save,xsrc", [(m, K, N, act, save, xsrc) for lo, K, N, act, save, xsrc in
+                                                 [(1024, 768, 776, "none", "none", "x"), (512, 1544, 1032, "none", "none", "ln"),
+                                                  (320, 264, 520, "gelu", "ckpt", "ln"), (320, 136, 264, "silu", "h", "x")] for m in (lo, lo + 1)])
+def test_backward_on_both_sides_of_the_one_launch_sums(L, M, K, N, act, save, xsrc):
+    test_backward(L, M, K, N, torch.bfloat16, act, save, xsrc)
+    if act == "none":
+        test_whole_number_products_are_exact(L, M, K, N, torch.bfloat16)
