@@ -185,6 +185,14 @@ lnfp8_status act_ckpt_restore_launch(const lnfp8_ckpt& c, int64_t rows, int64_t 
 // from `split` on to b[c - split].
 lnfp8_status colsum_launch(const float* part, int n, int cols, int split, float* a, float* b, cudaStream_t st);
 
+// Of 65536 draws, how many drop an element.
+inline uint32_t drop_threshold(double p) { return (uint32_t)(p * 65536.0 + 0.5); }
+lnfp8_status dropout_launch(const void* x, int elem, int64_t rows, int64_t cols, int64_t ldx, const lnfp8_dropout& d, void* y,
+                            int64_t ldy, cudaStream_t st);
+lnfp8_status block_join_fwd_launch(const lnfp8_block_join_fwd_args* a, cudaStream_t st);
+int64_t block_join_bwd_ws_bytes(int64_t M, int64_t D);
+lnfp8_status block_join_bwd_launch(const lnfp8_block_join_bwd_args* a, cudaStream_t st);
+
 // One product of 16-bit matrices on the tensor cores (linear.cu):
 //   out[M, N] = T(act(z) + resid), z = sum_k a[m, k] b[n, k] + bias[n]
 // a_mn / b_mn false: stored [rows, K] (K contiguous); true: stored [K, rows].
@@ -209,6 +217,8 @@ struct LinGemm {
   const void* cscale;  // [N] elem
   const void* cvec;    // [N] elem
   const float* rvec;   // [M]
+  // gated: b has 2N rows, gate rows first; out = T(act(z_gate) z_up), h is [M, 2N], bias [2N]; both operands K-major
+  bool glu;
   // K cut into `pieces` whose fp32 products [pieces][M][N] go to `part` and are added afterwards (0: whole)
   int pieces;
   float* part;
@@ -219,5 +229,8 @@ lnfp8_status lin_status_read_clear(unsigned int* word);
 lnfp8_status linear_act_fwd_launch(const lnfp8_linear_act_fwd_args* a, cudaStream_t st);
 int64_t linear_act_bwd_ws_bytes(int64_t M, int64_t K, int64_t N, bool has_act, bool x_from_ckpt);
 lnfp8_status linear_act_bwd_launch(const lnfp8_linear_act_bwd_args* a, cudaStream_t st);
+lnfp8_status linear_glu_fwd_launch(const lnfp8_linear_glu_fwd_args* a, cudaStream_t st);
+int64_t linear_glu_bwd_ws_bytes(int64_t M, int64_t K, int64_t N);
+lnfp8_status linear_glu_bwd_launch(const lnfp8_linear_glu_bwd_args* a, cudaStream_t st);
 
 }  // namespace lnfp8

@@ -424,7 +424,7 @@ struct DactParams {
   const uint8_t* scales;
   void* dz;      // NULL: no activation, only the column sums
   float* part;   // [row blocks][N] or NULL; with `both` [row blocks][2][N]: the sums of dz, then of dz as rounded
-  int both;
+  int both;      // (gated: of the gate's dz, then of the up projection's)
   // or, from clusters of kDactCluster row blocks (dact_cluster_rows): the sums themselves
   float* db;
   float* dbr;
@@ -432,7 +432,8 @@ struct DactParams {
   int N, dt, rows_per_block;  // dt: the lnfp8_dtype of the codes
 };
 
-enum DactSource { DACT_NONE, DACT_TENSOR, DACT_CKPT };  // no activation; h as a tensor; h as a checkpoint
+// No activation; h as a tensor; h as a checkpoint; gated, h and dz [M, 2N]: dz_gate = dy h_up act'(h_gate), dz_up = dy act(h_gate)
+enum DactSource { DACT_NONE, DACT_TENSOR, DACT_CKPT, DACT_GLU };
 constexpr int kDactBlocksPerSm = 4;
 constexpr int kDactCluster = 8;
 // Up to how many rows the column sums come from clusters of 8 row blocks, without a second launch. Of the whole
@@ -446,12 +447,13 @@ inline int64_t dact_cluster_rows(int64_t K, int64_t N, bool has_act) {
 
 template <int SRC>
 struct DactShape {
-  static constexpr int H_OFF = 16, S_OFF = SRC == DACT_TENSOR ? 32 : 24;  // bytes per thread: dy, h or codes, scale word
-  static constexpr int BYTES = SRC == DACT_NONE ? 16 : SRC == DACT_TENSOR ? 32 : 28;
+  // bytes per thread: dy, h or codes, scale word, or the gate's h and the up projection's
+  static constexpr int H_OFF = 16, S_OFF = SRC == DACT_TENSOR ? 32 : 24, U_OFF = 32;
+  static constexpr int BYTES = SRC == DACT_NONE ? 16 : SRC == DACT_TENSOR ? 32 : SRC == DACT_GLU ? 48 : 28;
   // Rows of a thread in its ring: all but one are on their way while that one is used. With h as a tensor six would leave
   // room for three blocks an SM, where the grid has four to one (8192 x 8192, GELU 94 us; six rows and a grid of three
   // 83; five rows 74, four 72; ReLU 65, 68, 67, 68; 8192 x 2048, GELU 28.4, 25.4, 23.8, 22.7, ReLU 20.3, 18.7, 19.0, 19.0).
-  static constexpr int RING = SRC == DACT_TENSOR ? 4 : 6;
+  static constexpr int RING = SRC == DACT_TENSOR ? 4 : SRC == DACT_GLU ? 3 : 6;
   static constexpr size_t SMEM = (size_t)RING * BYTES * 256;
   static constexpr size_t RED = 8 * 32 * 9 * sizeof(float);
   // of an SM's 228 KB each block takes 1 KB for itself
@@ -476,20 +478,22 @@ __global__ void __launch_bounds__(256, kDactBlocksPerSm) lin_dact_kernel(const D
 #pragma unroll
   for (int k = 0; k < 4; ++k) acc[k] = accr[k] = 0;
   const uint32_t base = (uint32_t)__cvta_generic_to_shared(ring);
-  const uint32_t a_dy = threadIdx.x * 16, a_h = S::H_OFF * 256 + threadIdx.x * (SRC == DACT_TENSOR ? 16 : 8),
-                 a_s = S::S_OFF * 256 + threadIdx.x * 4;
+  const uint32_t a_dy = threadIdx.x * 16, a_h = S::H_OFF * 256 + threadIdx.x * (SRC == DACT_CKPT ? 8 : 16),
+                 a_s = S::S_OFF * 256 + threadIdx.x * 4, a_u = S::U_OFF * 256 + threadIdx.x * 16;
+  const int64_t ldz = SRC == DACT_GLU ? 2 * (int64_t)p.N : p.N;  // of h and dz
   int64_t r = r0 + rl;
   const uint16_t* dyp = reinterpret_cast<const uint16_t*>(p.dy) + r * p.lddy + c;
-  const uint16_t* hp = reinterpret_cast<const uint16_t*>(p.h) + r * p.N + c;
+  const uint16_t* hp = reinterpret_cast<const uint16_t*>(p.h) + r * ldz + c;
   const uint8_t* qp = p.codes + r * p.N + c;
   const uint8_t* sp = p.scales + r * p.pitch + ((c >> 7) << 2);  // the word that holds this column's scale byte
-  const int64_t dystep = 8 * p.lddy, hstep = 8 * (int64_t)p.N, sstep = 8 * p.pitch;
+  const int64_t dystep = 8 * p.lddy, hstep = 8 * ldz, sstep = 8 * p.pitch;
   auto issue = [&](int64_t row, uint32_t slot) {
     if (row < r1) {
       cp16(slot + a_dy, dyp);
       dyp += dystep;
-      if constexpr (SRC == DACT_TENSOR) {
+      if constexpr (SRC == DACT_TENSOR || SRC == DACT_GLU) {
         cp16(slot + a_h, hp);
+        if constexpr (SRC == DACT_GLU) cp16(slot + a_u, hp + p.N);
         hp += hstep;
       } else if constexpr (SRC == DACT_CKPT) {
         cp8(slot + a_h, qp);
@@ -504,14 +508,32 @@ __global__ void __launch_bounds__(256, kDactBlocksPerSm) lin_dact_kernel(const D
   for (int k = 0; k < P; ++k) issue(r + 8 * k, base + k * SB);
   uint32_t slot = base, last = base + P * SB;
   const int byte = ((c >> 5) & 3) * 8;
-  uint16_t* zp = reinterpret_cast<uint16_t*>(p.dz) + r * p.N + c;
+  uint16_t* zp = reinterpret_cast<uint16_t*>(p.dz) + r * ldz + c;
   for (; r < r1; r += 8) {
     issue(r + 8 * P, last);
     cp_wait<P>();
     uint64_t v[4];
     uint4 w = lds16(slot + a_dy);
     unpack8<ELEM>(&w, v);
-    if constexpr (SRC != DACT_NONE) {
+    if constexpr (SRC == DACT_GLU) {
+      uint64_t z[4], a[4], sl[4], u[4];
+      w = lds16(slot + a_h);
+      unpack8<ELEM>(&w, z);
+      w = lds16(slot + a_u);
+      unpack8<ELEM>(&w, u);
+      act_slope8<ACT, ELEM == LNFP8_BF16>(z, a, sl);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        a[k] = mul_2(v[k], a[k]);
+        accr[k] = add_2(accr[k], a[k]);
+        v[k] = mul_2(mul_2(v[k], u[k]), sl[k]);
+      }
+      pack8<ELEM>(a, &w);
+      *reinterpret_cast<uint4*>(zp + p.N) = w;
+      pack8<ELEM>(v, &w);
+      *reinterpret_cast<uint4*>(zp) = w;
+      zp += hstep;
+    } else if constexpr (SRC != DACT_NONE) {
       uint64_t z[4], sl[4];
       uint32_t sb = 0;
       if constexpr (SRC == DACT_TENSOR) {
@@ -852,6 +874,13 @@ lnfp8_status swap_launch(const LinGemm& g, cudaStream_t st) {
 }  // namespace
 
 lnfp8_status lin_gemm_launch(const LinGemm* g, int count, cudaStream_t st) {
+  if (g->glu) {
+    if (g->M == 0) return LNFP8_OK;
+    LinGemm one = *g;
+    one.N *= 2;
+    const LinPlan pl = lin_plan(&one, 1);
+    return pl.tile == 64 ? pair_launch<64, LIN_GLU>(g, 1, st) : pl.tile == 128 ? pair_launch<128, LIN_GLU>(g, 1, st) : pair_launch<256, LIN_GLU>(g, 1, st);
+  }
   if (!g[0].b_mn) {  // the forward: both operands K-major
     if (g->M == 0 || g->N == 0) return LNFP8_OK;
     if (takes_few(*g)) return g->elem == LNFP8_FP16 ? few_by_tokens<true>(*g, st) : few_by_tokens<false>(*g, st);
@@ -1029,6 +1058,114 @@ lnfp8_status linear_act_bwd_launch(const lnfp8_linear_act_bwd_args* a, cudaStrea
       q.cscale = a->x_gamma;
       q.cvec = a->x_beta;
       q.rvec = dbr;
+    }
+  }
+  return count ? lin_gemm_launch(g, count, st) : LNFP8_OK;
+}
+
+// ------------------------------------------------------------ the gated linear layer
+//   forward   z = x w^T + b (w [2N, K], gate rows first), y = T(act(z_gate) z_up), T(z) kept if asked for
+//   backward  dz_gate = dy z_up act'(z_gate), dz_up = dy act(z_gate), db = sum_rows dz, dx = T(dz w), dw = T(dz^T x)
+// Behind dz the backward is the plain layer's with 2N features.
+lnfp8_status linear_glu_fwd_launch(const lnfp8_linear_glu_fwd_args* a, cudaStream_t st) {
+  LinGemm g = {};
+  g.M = a->M;
+  g.N = a->N;
+  g.K = a->K;
+  g.elem = a->elem;
+  g.a = a->x;
+  g.lda = a->ldx;
+  g.b = a->w;
+  g.ldb = a->K;
+  g.out = a->y;
+  g.ldo = a->ldy;
+  g.bias = a->bias;
+  g.act = a->act;
+  g.h = a->h;
+  g.glu = true;
+  return lin_gemm_launch(&g, 1, st);
+}
+
+// dz [M, 2N], the columns' partial sums and the K pieces of dw, each from a multiple of 256 on.
+int64_t linear_glu_bwd_ws_bytes(int64_t M, int64_t K, int64_t N) {
+  if (M == 0 || N == 0) return 0;
+  const int64_t rpb = dact_rows_per_block(M, K, N, true);
+  return up256(M * 2 * N * 2) + up256((M + rpb - 1) / rpb * 2 * N * 4) + wgrad_bytes(M, K, 2 * N);
+}
+
+lnfp8_status linear_glu_bwd_launch(const lnfp8_linear_glu_bwd_args* a, cudaStream_t st) {
+  const int64_t M = a->M, K = a->K, N = a->N, N2 = 2 * N;
+  if (M == 0) {
+    if ((a->dw && cudaMemsetAsync(a->dw, 0, N2 * K * 2, st) != cudaSuccess) ||
+        (a->dbias && cudaMemsetAsync(a->dbias, 0, N2 * sizeof(float), st) != cudaSuccess))
+      return check_launch("linear_glu_bwd: clearing dw/dbias");
+    return LNFP8_OK;
+  }
+  uint8_t* ws = static_cast<uint8_t*>(a->workspace);
+  void* dz = ws;
+  ws += up256(M * N2 * 2);
+  const bool few_rows = M <= dact_cluster_rows(K, N, true);
+  DactParams p = {};
+  p.dy = a->dy;
+  p.h = a->h;
+  p.dz = dz;
+  p.part = a->dbias && !few_rows ? reinterpret_cast<float*>(ws) : nullptr;
+  p.db = a->dbias && few_rows ? a->dbias : nullptr;
+  p.dbr = a->dbias ? a->dbias + N : nullptr;
+  p.both = 1;
+  p.M = M;
+  p.lddy = a->ld_dy;
+  p.N = (int)N;
+  p.rows_per_block = (int)dact_rows_per_block(M, K, N, true);
+  const int64_t row_blocks = few_rows ? kDactCluster : (M + p.rows_per_block - 1) / p.rows_per_block;
+  const dim3 grid((unsigned)((N + 255) / 256), (unsigned)row_blocks);
+  auto pick = [&](auto elem) {
+    constexpr int E = decltype(elem)::value;
+    return a->act == LNFP8_ACT_GELU   ? dact_launch<E, DACT_GLU, LNFP8_ACT_GELU>(p, grid, st)
+           : a->act == LNFP8_ACT_SILU ? dact_launch<E, DACT_GLU, LNFP8_ACT_SILU>(p, grid, st)
+           : a->act == LNFP8_ACT_RELU ? dact_launch<E, DACT_GLU, LNFP8_ACT_RELU>(p, grid, st)
+                                      : dact_launch<E, DACT_GLU, LNFP8_ACT_NONE>(p, grid, st);
+  };
+  lnfp8_status s = a->elem == LNFP8_BF16 ? pick(std::integral_constant<int, LNFP8_BF16>()) : pick(std::integral_constant<int, LNFP8_FP16>());
+  if (s != LNFP8_OK) return s;
+  if (p.part) {
+    s = colsum_launch(p.part, (int)row_blocks, (int)N2, (int)N2, a->dbias, nullptr, st);
+    if (s != LNFP8_OK) return s;
+  }
+  LinGemm g[2] = {};
+  int count = 0;
+  if (a->dx) {  // [M, K] = dz [M, 2N] . w, contracted over both projections
+    LinGemm& q = g[count++];
+    q.elem = a->elem;
+    q.M = M;
+    q.N = K;
+    q.K = N2;
+    q.a = dz;
+    q.lda = N2;
+    q.b = a->w;
+    q.ldb = K;
+    q.b_mn = true;
+    q.out = a->dx;
+    q.ldo = a->ld_dx;
+  }
+  if (a->dw) {  // [2N, K] = dz^T . x, contracted over the tokens
+    LinGemm& q = g[count++];
+    q.elem = a->elem;
+    q.M = N2;
+    q.N = K;
+    q.K = M;
+    q.a = dz;
+    q.lda = N2;
+    q.a_mn = true;
+    q.b = a->x;
+    q.ldb = a->ldx;
+    q.b_mn = true;
+    q.out = a->dw;
+    q.ldo = K;
+    q.pieces = wgrad_pieces(M, K, N2);
+    if (q.pieces > 1) {  // the last part of the workspace
+      const uintptr_t at = reinterpret_cast<uintptr_t>(a->workspace) + linear_glu_bwd_ws_bytes(M, K, N) - wgrad_bytes(M, K, N2);
+      q.part = reinterpret_cast<float*>((at + 31) / 32 * 32);
     }
   }
   return count ? lin_gemm_launch(g, count, st) : LNFP8_OK;

@@ -18,6 +18,10 @@
 enum LinEpi {
   LIN_FULL = 0,   // bias, saved pre-activation, activation, residual; both operands K-major
   LIN_PLAIN = 1,  // out = T(acc), or T(acc * cscale[col] + rvec[row] * cvec[col]); A either way, B MN-major
+  // Gated: the left half of a tile's columns are gate features and the right half the up features of the same outputs, so
+  // that a thread finds both factors of an output in its own row of tensor memory and neither goes through HBM. A CTA loads
+  // half of the B tile in any case: the pair's first CTA takes the gate rows of w, the second the up rows.
+  LIN_GLU = 2,
 };
 
 constexpr int kPairEpiWarps = 16;
@@ -141,6 +145,23 @@ __device__ __forceinline__ void load_row32(const uint16_t* row, int n0, int N, i
   }
 }
 
+// 16 columns, one 32-byte sector.
+__device__ __forceinline__ void store_row16(uint16_t* row, int n0, int N, int wide, const uint64_t* z, int f16) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 v = upk(z[i]);
+    w[i] = pack16(v.x, v.y, f16);
+  }
+  if (wide && n0 + 16 <= N) {
+    store32(row + n0, w);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (n0 + 8 * j < N) *reinterpret_cast<uint4*>(row + n0 + 8 * j) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+  }
+}
+
 // A pair's unit of round r: the rounds run forwards and backwards in turn, so that the pairs that got
 // the longer units of a round (they come first) get the later ones of the next.
 __device__ __forceinline__ int pair_unit(int r, int cid, int ncl) { return r * ncl + (r & 1 ? ncl - 1 - cid : cid); }
@@ -150,6 +171,83 @@ template <int ACT>
 __device__ __forceinline__ void act_pairs(uint64_t* z) {
 #pragma unroll
   for (int i = 0; i < 16; i += 4) act8<ACT>(z + i);
+}
+
+// The gated epilogue of one warp: its 32 rows (m_in: this lane's row of a tile) and half of the outputs of every tile of its
+// accumulator, 16 at a time: 16 gate and 16 up columns are as many registers as the other epilogues' 32 columns.
+template <int BN>
+__device__ __forceinline__ void glu_epilogue(const PairParams& p, uint32_t tacc, uint32_t tfull, uint32_t tempty, uint32_t bias_slot,
+                                             volatile uint32_t* abort_flag, int m_in, int half, int t0, int t_step) {
+  constexpr int HALF = BN / 4, CHUNKS = HALF / 16;
+  const PairProb& pr = p.prob[0];
+  const int lane = threadIdx.x & 31;
+  const bool biased = p.bias != nullptr;
+  // two columns a lane, eight lanes of the gate's and eight of the up projection's
+  auto bias_word = [&](int n) {
+    const int c = n + 2 * (lane & 7);
+    return lane < 16 && c < pr.N ? __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.bias) + (lane < 8 ? 0 : pr.N) + c)) : 0u;
+  };
+  uint32_t acc_phase = 0;
+  for (int t = t0; t < p.tiles; t += t_step) {
+    const PairTile at = pair_locate(p, t);
+    const int m = at.m2 * 256 + m_in;
+    const int nh = at.n * (BN / 2) + half * HALF;
+    uint32_t next_bias = biased ? bias_word(nh) : 0u;
+    if (!mbar_wait_warp(tfull, acc_phase, abort_flag)) break;  // the whole warp: what follows is warp-wide
+    tc_fence_after();
+    const bool row_ok = m < pr.M;
+#pragma unroll 1
+    for (int ch = 0; ch < CHUNKS; ++ch) {
+      const int n0 = nh + ch * 16;
+      __syncwarp();  // rows past M took other branches; the bias slot has been read
+      if (biased) {
+        if (lane < 16) sts4(bias_slot + 4 * lane, next_bias);
+        if (ch + 1 < CHUNKS) next_bias = bias_word(n0 + 16);
+        __syncwarp();
+      }
+      uint32_t rg[16], ru[16];
+      tmem_ld16x2(tacc + half * HALF + ch * 16, rg, tacc + BN / 2 + half * HALF + ch * 16, ru);
+      if (ch == CHUNKS - 1 && t + t_step < p.tiles) {  // someone waits for it: nothing is in flight when the CTA leaves
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(tempty);
+      }
+      uint64_t zg[8], zu[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        zg[i] = pk(__uint_as_float(rg[2 * i]), __uint_as_float(rg[2 * i + 1]));
+        zu[i] = pk(__uint_as_float(ru[2 * i]), __uint_as_float(ru[2 * i + 1]));
+      }
+      if (biased) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint4 bu = lds16(bias_slot + 16 * j);
+          const uint32_t bw[4] = {bu.x, bu.y, bu.z, bu.w};
+          uint64_t* z = j < 2 ? zg + 4 * j : zu + 4 * (j - 2);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 b = unpack16(bw[i], p.f16);
+            z[i] = add_2(z[i], pk(b.x, b.y));
+          }
+        }
+      }
+      if (p.h && row_ok) {
+        uint16_t* hr = reinterpret_cast<uint16_t*>(p.h) + (int64_t)m * 2 * pr.N;
+        store_row16(hr, n0, pr.N, p.wide_h, zg, p.f16);
+        store_row16(hr + pr.N, n0, pr.N, p.wide_h, zu, p.f16);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; i += 4) {
+        if (p.act == LNFP8_ACT_SILU) act8<LNFP8_ACT_SILU>(zg + i);
+        else if (p.act == LNFP8_ACT_GELU) act8<LNFP8_ACT_GELU>(zg + i);
+        else if (p.act == LNFP8_ACT_RELU) act8<LNFP8_ACT_RELU>(zg + i);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) zg[i] = mul_2(zg[i], zu[i]);
+      if (row_ok) store_row16(reinterpret_cast<uint16_t*>(pr.out) + m * pr.ldo, n0, pr.N, pr.wide_out, zg, p.f16);
+    }
+    acc_phase ^= 1;
+  }
 }
 
 template <int BN, int EPI>
@@ -187,7 +285,7 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
     *abort_flag = 0;
     mbar_init_fence();
     tma_prefetch_map(&maps.a[0]);
-    tma_prefetch_map(&maps.b[0]);
+    tma_prefetch_map(&maps.b[EPI == LIN_GLU ? blockIdx.x & 1 : 0]);
   }
   cluster_sync_all();  // the peer signals this CTA's barriers
   if (warp == 1) tmem_alloc<true>(smem_u32((const void*)(misc + 1)), C::TMEM_COLS);
@@ -215,9 +313,9 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
       const int t = pair_unit(rd, cid, ncl);
       if (t >= tiles) break;
       const PairTile at = pair_locate(p, t);
-      const CUtensorMap *tmA = &maps.a[at.prob], *tmB = &maps.b[at.prob];
+      const CUtensorMap *tmA = &maps.a[at.prob], *tmB = &maps.b[EPI == LIN_GLU ? rank : at.prob];
       const bool a_mn = EPI == LIN_PLAIN && p.prob[at.prob].a_mn;
-      const int m0 = at.m2 * 256 + rank * 128, n0 = at.n * BN + rank * (BN / 2);
+      const int m0 = at.m2 * 256 + rank * 128, n0 = EPI == LIN_GLU ? at.n * (BN / 2) : at.n * BN + rank * (BN / 2);
       for (int kb = at.kb0; kb < at.kb1; ++kb) {
         if (!mbar_wait_warp(empty_bar(stage), phase ^ 1, abort_flag)) { ok = false; break; }
         if (one) {
@@ -300,6 +398,10 @@ lin_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ P
     const uint32_t tempty = map_to_rank(tempty_bar(acc), 0), bias_slot = ring + C::BIAS_OFF + 64 * ew;
     // this group's rounds have its parity: a step of two rounds keeps the direction
     const int t0 = pair_unit(acc, cid, ncl);
+    if constexpr (EPI == LIN_GLU)
+      glu_epilogue<BN>(p, tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * BN), tfull_bar(acc), tempty, bias_slot, abort_flag,
+                       rank * 128 + quarter * 32 + lane, half, t0, 2 * ncl);
+    else
     for (int t = t0; t < tiles; t += 2 * ncl) {
       const PairTile at = pair_locate(p, t);
       const PairProb& pr = p.prob[at.prob];
@@ -463,7 +565,7 @@ lnfp8_status pair_launch(const LinGemm* g, int count, cudaStream_t st) {
     r.M = (int)q.M;
     r.N = (int)q.N;
     r.num_m2 = (int)((q.M + 255) / 256);
-    r.num_n = (int)((q.N + BN - 1) / BN);
+    r.num_n = (int)((q.N * (EPI == LIN_GLU ? 2 : 1) + BN - 1) / BN);
     r.num_kb = (int)((q.K + BK - 1) / BK);
     // A panels (256 rows x K) of a raster group: what fits in 48 MB of L2
     r.group_m = (int)max64(1, min64((48ll << 20) / (512 * max64(q.K, 1)), r.num_m2));
@@ -482,15 +584,23 @@ lnfp8_status pair_launch(const LinGemm* g, int count, cudaStream_t st) {
     r.wide_out = wide(q.out, q.ldo, 2);
     ok = ok && operand_map(&maps.a[i], q.a, q.a_mn, q.M, q.K, q.lda, 128) && operand_map(&maps.b[i], q.b, q.b_mn, q.N, q.K, q.ldb, BN / 2);
   }
+  if constexpr (EPI == LIN_GLU)
+    ok = ok && operand_map(&maps.b[1], static_cast<const uint16_t*>(g->b) + g->N * g->ldb, false, g->N, g->K, g->ldb, BN / 2);
   if (tiles > 0x3FFFFFFF) return set_error(LNFP8_ERR_UNSUPPORTED_SHAPE, "linear: too many tiles");
   p.tiles = (int)tiles;
   if (count == 1) {
     p.prob[1] = p.prob[0];
     maps.a[1] = maps.a[0];
-    maps.b[1] = maps.b[0];
+    if constexpr (EPI != LIN_GLU) maps.b[1] = maps.b[0];
   }
   p.f16 = g->elem == LNFP8_FP16;
   p.ck = -1;
+  if constexpr (EPI == LIN_GLU) {
+    p.act = g->act;
+    p.h = g->h;
+    p.wide_h = wide(g->h, g->N, 2);
+    p.bias = g->bias;
+  }
   if constexpr (EPI == LIN_FULL) {
     p.act = g->act;
     p.ck = g->ckpt.codes ? g->ckpt.dtype : -1;

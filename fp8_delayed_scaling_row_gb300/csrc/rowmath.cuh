@@ -455,6 +455,49 @@ __device__ __forceinline__ void act8(uint64_t* z) {
   }
 }
 
+// act(z) and act'(z) of the same 8 values, one logistic function for both.
+template <int ACT, bool FAR>
+__device__ __forceinline__ void act_slope8(const uint64_t* z, uint64_t* a, uint64_t* out) {
+  const uint64_t one = pk(1.0f, 1.0f), minus = pk(-1.0f, -1.0f);
+  if constexpr (ACT == LNFP8_ACT_NONE) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      a[k] = z[k];
+      out[k] = one;
+    }
+  } else if constexpr (ACT == LNFP8_ACT_RELU) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 t = upk(z[k]);
+      a[k] = pk(act_fwd(t.x, ACT), act_fwd(t.y, ACT));
+      out[k] = pk(relu_slope(t.x), relu_slope(t.y));
+    }
+  } else {
+    uint64_t nu[4], s[4], zz[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      zz[k] = mul_2(z[k], z[k]);
+      if constexpr (FAR) {
+        const float2 t = upk(zz[k]);
+        zz[k] = pk(fminf(t.x, 1e30f), fminf(t.y, 1e30f));  // finite, so that the vanished s (1 - s) wins far out
+      }
+      nu[k] = ACT == LNFP8_ACT_GELU ? gelu_nu2(z[k], zz[k]) : mul_2(z[k], pk(-kLog2e, -kLog2e));
+    }
+    logistic8(nu, s);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      a[k] = mul_2(z[k], s[k]);
+      const uint64_t t = mul_2(a[k], fma_2(s[k], minus, one));
+      if constexpr (ACT == LNFP8_ACT_GELU) {
+        const uint64_t du = fma_2(zz[k], pk(3.0f * kGelu2KC, 3.0f * kGelu2KC), pk(kGelu2K, kGelu2K));
+        out[k] = fma_2(t, du, s[k]);
+      } else {
+        out[k] = add_2(t, s[k]);
+      }
+    }
+  }
+}
+
 // FAR: z may be so large that its square leaves fp32.
 template <int ACT, bool FAR>
 __device__ __forceinline__ void slope8(const uint64_t* z, uint64_t* out) {

@@ -7,8 +7,9 @@ the shared library has not been built, importing this module raises.
 Names follow the C ABI: lnfp8_meta_init, amax_history_update, fp8_quantize,
 ln_fwd_cast, ln_bwd, fp8_gemm, ln_linear_fwd / ln_linear_bwd,
 ln_mlp_fwd / ln_mlp_bwd; and, for what a model keeps in 16 or 32 bits,
-layernorm_fwd / layernorm_bwd, act_ckpt_save / act_ckpt_restore and
-linear_act_fwd / linear_act_bwd.
+layernorm_fwd / layernorm_bwd, act_ckpt_save / act_ckpt_restore,
+linear_act_fwd / linear_act_bwd, linear_glu_fwd / linear_glu_bwd,
+block_join_fwd / block_join_bwd and dropout_fwd / dropout_bwd (dropout_apply).
 """
 from __future__ import annotations
 
@@ -37,7 +38,8 @@ EXPORTED = [
     "lnfp8_ln_linear_bwd_workspace_size", "lnfp8_ln_mlp_bwd_workspace_size", "lnfp8_ln_mlp_fwd_workspace_size",
     "lnfp8_ctx_bytes", "lnfp8_ctx_offsets", "lnfp8_act_ckpt_scale_pitch", "act_ckpt_save", "act_ckpt_restore",
     "layernorm_fwd", "layernorm_bwd", "lnfp8_layernorm_bwd_workspace_size", "linear_act_fwd", "linear_act_bwd",
-    "lnfp8_linear_act_bwd_workspace_size",
+    "lnfp8_linear_act_bwd_workspace_size", "linear_glu_fwd", "linear_glu_bwd", "lnfp8_linear_glu_bwd_workspace_size",
+    "dropout_apply", "block_join_fwd", "block_join_bwd", "lnfp8_block_join_bwd_workspace_size",
 ]
 OP_LN_LINEAR, OP_LINEAR, OP_LN_MLP = 0, 1, 2
 
@@ -126,6 +128,38 @@ class CLinearActBwd(C.Structure):
                 ("ld_dy", _I64), ("ldx", _I64), ("ld_dx", _I64)]
 
 
+class CLinearGluFwd(C.Structure):
+    _fields_ = [("M", _I64), ("K", _I64), ("N", _I64), ("elem", C.c_int), ("act", C.c_int), ("x", _P), ("w", _P),
+                ("bias", _P), ("y", _P), ("h", _P), ("ldx", _I64), ("ldy", _I64)]
+
+
+class CLinearGluBwd(C.Structure):
+    _fields_ = [("M", _I64), ("K", _I64), ("N", _I64), ("elem", C.c_int), ("act", C.c_int), ("dy", _P), ("x", _P),
+                ("w", _P), ("h", _P), ("dx", _P), ("dw", _P), ("dbias", _P), ("workspace", _P), ("workspace_bytes", _I64),
+                ("ld_dy", _I64), ("ldx", _I64), ("ld_dx", _I64)]
+
+
+class CDropout(C.Structure):
+    _fields_ = [("p", C.c_double), ("rng", _P), ("rng_saved", _P), ("site", C.c_uint32)]
+
+
+class CBlockJoinFwd(C.Structure):
+    _fields_ = [("M", _I64), ("D", _I64), ("elem", C.c_int), ("param_elem", C.c_int), ("norm", C.c_int), ("eps", C.c_float),
+                ("scale", C.c_float), ("x", _P), ("residual", _P), ("post_gamma", _P), ("post_beta", _P), ("gate", _P),
+                ("pre_gamma", _P), ("pre_beta", _P), ("drop", CDropout), ("h", _P), ("y", _P), ("post_mu", _P),
+                ("post_rsigma", _P), ("pre_mu", _P), ("pre_rsigma", _P), ("ldx", _I64), ("ld_residual", _I64),
+                ("ldh", _I64), ("ldy", _I64)]
+
+
+class CBlockJoinBwd(C.Structure):
+    _fields_ = [("M", _I64), ("D", _I64), ("elem", C.c_int), ("param_elem", C.c_int), ("norm", C.c_int), ("scale", C.c_float),
+                ("dh", _P), ("dy", _P), ("x", _P), ("h", _P), ("post_gamma", _P), ("post_beta", _P), ("gate", _P),
+                ("pre_gamma", _P), ("post_mu", _P), ("post_rsigma", _P), ("pre_mu", _P), ("pre_rsigma", _P),
+                ("drop", CDropout), ("dx", _P), ("dresidual", _P), ("dpost_gamma", _P), ("dpost_beta", _P), ("dgate", _P),
+                ("dpre_gamma", _P), ("dpre_beta", _P), ("workspace", _P), ("workspace_bytes", _I64), ("ld_dh", _I64),
+                ("ld_dy", _I64), ("ldx", _I64), ("ldh", _I64), ("ld_dx", _I64), ("ld_dresidual", _I64)]
+
+
 def _sig(name, args, res=C.c_int):
     f = getattr(_lib, name)
     f.argtypes = args
@@ -173,6 +207,13 @@ _c_layernorm_bwd = _sig("layernorm_bwd", [C.POINTER(CLayerNormBwd), _P])
 _c_linear_act_fwd = _sig("linear_act_fwd", [C.POINTER(CLinearActFwd), _P])
 _c_linear_act_bwd = _sig("linear_act_bwd", [C.POINTER(CLinearActBwd), _P])
 _c_linear_act_bwd_ws = _sig("lnfp8_linear_act_bwd_workspace_size", [_I64, _I64, _I64, C.c_int, C.c_int], C.c_int64)
+_c_linear_glu_fwd = _sig("linear_glu_fwd", [C.POINTER(CLinearGluFwd), _P])
+_c_linear_glu_bwd = _sig("linear_glu_bwd", [C.POINTER(CLinearGluBwd), _P])
+_c_linear_glu_bwd_ws = _sig("lnfp8_linear_glu_bwd_workspace_size", [_I64, _I64, _I64], C.c_int64)
+_c_dropout = _sig("dropout_apply", [_P, C.c_int, _I64, _I64, _I64, C.POINTER(CDropout), _P, _I64, _P])
+_c_block_join_fwd = _sig("block_join_fwd", [C.POINTER(CBlockJoinFwd), _P])
+_c_block_join_bwd = _sig("block_join_bwd", [C.POINTER(CBlockJoinBwd), _P])
+_c_block_join_bwd_ws = _sig("lnfp8_block_join_bwd_workspace_size", [_I64, _I64], C.c_int64)
 _c_layernorm_bwd_ws = _sig("lnfp8_layernorm_bwd_workspace_size", [_I64, _I64], C.c_int64)
 
 
@@ -1055,4 +1096,364 @@ def linear_act_bwd(dy, x, w, ctx: LinearActCtx, *, x_act="none", x_gamma=None, x
     a = CLinearActBwd(M, K, N, elem, ia, dy.data_ptr(), xp, xck, _act(x_act), _ptr(x_gamma), _ptr(x_beta), w.data_ptr(), h,
                       hck, _ptr(grads.dx), _ptr(grads.dw), _ptr(grads.dbias), ws.data_ptr(), ws.nbytes, lddy, ldx, lddx)
     _check(_c_linear_act_bwd(C.byref(a), _raw_stream(dev)))
+    return grads
+
+
+@dataclass
+class LinearGluCtx:
+    """What linear_glu_bwd needs of its forward besides x and w: the gate's activation and z = x w^T + bias [M, 2N]."""
+    act: str = "silu"
+    h: torch.Tensor | None = None
+
+
+def linear_glu_fwd(x, w, bias=None, *, act="silu", save="none", y=None, ctx: LinearGluCtx | None = None, stream=None):
+    """act(x wg^T + bg) * (x wu^T + bu) of bf16 or fp16 tensors, x [M, K], w [2N, K] with the gate's rows wg first,
+    bias [2N]; returns (y [M, N], ctx). act: "silu", "gelu" (tanh form), "relu" or "none". save: "h" keeps both projections
+    [M, 2N] for the backward (in ctx.h if it is there), "none" keeps nothing."""
+    elem, ia = _elem(x, "x", _ELEM16), _act(act)
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError(f"x and w have shapes {tuple(x.shape)} and {tuple(w.shape)}: expected two dimensions")
+    if save not in ("none", "h"):
+        raise ValueError(f"unknown save {save!r}: one of none, h")
+    M, K = x.shape
+    N2 = w.shape[0]
+    N = N2 // 2
+    if N2 % 2:
+        raise ValueError(f"w has {N2} rows: expected the gate's and as many of the up projection")
+    dt, dev = x.dtype, _dev(x, "x")
+    if stream is not None:
+        with _on(stream, dev):
+            return linear_glu_fwd(x, w, bias, act=act, save=save, y=y, ctx=ctx)
+    ldx = _rows(x, "x", M, K, dt, dev)
+    _flat(w, "w", (N2, K), dt, dev)
+    if bias is not None:
+        _flat(bias, "bias", (N2,), dt, dev)
+    ldy = N
+    if y is None:
+        y = _e((M, N), dt, x.device)
+    else:
+        ldy = _rows(y, "y", M, N, dt, dev)
+    if ctx is None:
+        ctx = LinearGluCtx()
+    ctx.act = act
+    h = None
+    if save == "none":
+        ctx.h = None
+    else:
+        if ctx.h is None:
+            ctx.h = _e((M, N2), dt, x.device)
+        else:
+            _flat(ctx.h, "ctx.h", (M, N2), dt, dev)
+        h = ctx.h.data_ptr()
+    a = CLinearGluFwd(M, K, N, elem, ia, x.data_ptr(), w.data_ptr(), _ptr(bias), y.data_ptr(), h, ldx, ldy)
+    _check(_c_linear_glu_fwd(C.byref(a), _raw_stream(dev)))
+    return y, ctx
+
+
+@dataclass
+class LinearGluGrads:
+    """Gradients of linear_glu_bwd. workspace: scratch (dz, most of it) that the caller keeps from call to call; None: each
+    call takes its own from the current stream's memory and gives it back."""
+    dx: torch.Tensor | None
+    dw: torch.Tensor | None
+    dbias: torch.Tensor | None
+    workspace: torch.Tensor | None = None
+
+
+def linear_glu_bwd_workspace_size(M, K, N) -> int:
+    return int(_c_linear_glu_bwd_ws(M, K, N))
+
+
+def linear_glu_grads(M, K, N, *, dx=True, dw=True, bias=True, dtype=torch.bfloat16, device="cuda", workspace=True) -> LinearGluGrads:
+    """Gradients of one linear_glu_bwd, with a workspace to keep; dx, dw, bias=False leave theirs out."""
+    return LinearGluGrads(_e((M, K), dtype, device) if dx else None, _e((2 * N, K), dtype, device) if dw else None,
+                          _e((2 * N,), torch.float32, device) if bias else None,
+                          _e((_c_linear_glu_bwd_ws(M, K, N),), torch.uint8, device) if workspace else None)
+
+
+def linear_glu_bwd(dy, x, w, ctx: LinearGluCtx, *, dbias=True, grads: LinearGluGrads | None = None, stream=None) -> LinearGluGrads:
+    """Gradients of linear_glu_fwd with save="h". Gradients that `grads` leaves None are not computed; without `grads`
+    dbias=False leaves the bias's out; x may be None without dw."""
+    elem, ia = _elem(dy, "dy", _ELEM16), _act(ctx.act)
+    if dy.dim() != 2 or w.dim() != 2:
+        raise ValueError(f"dy and w have shapes {tuple(dy.shape)} and {tuple(w.shape)}: expected two dimensions")
+    M, N = dy.shape
+    K = w.shape[1]
+    dt, dev = dy.dtype, _dev(dy, "dy")
+    if stream is not None:
+        with _on(stream, dev):
+            return linear_glu_bwd(dy, x, w, ctx, dbias=dbias, grads=grads)
+    lddy = _rows(dy, "dy", M, N, dt, dev)
+    _flat(w, "w", (2 * N, K), dt, dev)
+    if ctx.h is None:
+        raise ValueError("the forward saved no h")
+    _flat(ctx.h, "ctx.h", (M, 2 * N), dt, dev)
+    xp, ldx, lddx = None, 0, K
+    if x is not None:
+        ldx = _rows(x, "x", M, K, dt, dev)
+        xp = x.data_ptr()
+    if grads is None:
+        grads = linear_glu_grads(M, K, N, dw=x is not None, bias=dbias, dtype=dt, device=dy.device, workspace=False)
+    else:
+        if grads.dx is not None:
+            lddx = _rows(grads.dx, "grads.dx", M, K, dt, dev)
+        if grads.dw is not None:
+            _flat(grads.dw, "grads.dw", (2 * N, K), dt, dev)
+        if grads.dbias is not None:
+            _flat(grads.dbias, "grads.dbias", (2 * N,), torch.float32, dev)
+    ws = grads.workspace
+    ws = _e((_c_linear_glu_bwd_ws(M, K, N),), torch.uint8, dy.device) if ws is None else _given_ws(ws, dev)
+    a = CLinearGluBwd(M, K, N, elem, ia, dy.data_ptr(), xp, w.data_ptr(), ctx.h.data_ptr(), _ptr(grads.dx), _ptr(grads.dw),
+                      _ptr(grads.dbias), ws.data_ptr(), ws.nbytes, lddy, ldx, lddx)
+    _check(_c_linear_glu_bwd(C.byref(a), _raw_stream(dev)))
+    return grads
+
+
+# ------------------------------------------------------------------ dropout and the join of a block's output
+_NO_DROP = CDropout(0.0, None, None, 0)
+
+
+def dropout_rng(seed: int, *, step: int = 0, device="cuda") -> torch.Tensor:
+    """(seed, step), int64 [2] on the device: what every dropout of a step draws from, each with a site of its own.
+    Advance it in place (rng[1] += 1) from step to step, inside a captured graph too. Only step's low 32 bits are used."""
+    return torch.tensor([seed - (1 << 64) if seed >= 1 << 63 else seed, step], dtype=torch.int64, device=device)
+
+
+def _drop(p, rng, site, saved, dev) -> CDropout:
+    """saved: the forward keeps a copy of rng for the backward there."""
+    if not 0.0 <= p <= 1.0:
+        raise ValueError(f"p is {p}: expected 0..1")
+    if not 0 <= site < 1 << 32:
+        raise ValueError(f"site is {site}: expected 0..2^32 - 1")
+    if rng is None:
+        if p * 65536 + 0.5 >= 1.0:
+            raise ValueError("dropout needs rng (see dropout_rng)")
+        return _NO_DROP
+    _flat(rng, "rng", (2,), torch.int64, dev)
+    return CDropout(p, rng.data_ptr(), _ptr(saved), site)
+
+
+@dataclass
+class DropoutCtx:
+    """What dropout_bwd needs of its forward: the probability, the (seed, step) it drew from, and its site."""
+    p: float
+    rng: torch.Tensor | None
+    site: int = 0
+
+
+def _dropout(x, name, p, rng, site, saved, out, out_name):
+    elem = _elem(x, name)
+    if x.dim() != 2:
+        raise ValueError(f"{name} has shape {tuple(x.shape)}: expected two dimensions")
+    rows, cols = x.shape
+    dev = _dev(x, name)
+    ldx = _rows(x, name, rows, cols, x.dtype, dev)
+    d = _drop(p, rng, site, saved, dev)
+    ldo = cols
+    if out is None:
+        out = _e((rows, cols), x.dtype, x.device)
+    else:
+        ldo = _rows(out, out_name, rows, cols, x.dtype, dev)
+    _check(_c_dropout(x.data_ptr(), elem, rows, cols, ldx, C.byref(d), out.data_ptr(), ldo, _raw_stream(dev)))
+    return out
+
+
+def dropout_fwd(x, p, rng, *, site=0, y=None, stream=None):
+    """Dropout of a 2-D bf16, fp16 or fp32 tensor; returns (y, ctx). No mask is kept: the backward draws it again from
+    ctx.rng, a copy of rng as the call read it, so rng may be advanced in between."""
+    if stream is not None:
+        with _on(stream, _dev(x, "x")):
+            return dropout_fwd(x, p, rng, site=site, y=y)
+    ctx = DropoutCtx(p, None if rng is None else torch.empty_like(rng), site)
+    return _dropout(x, "x", p, rng, site, ctx.rng, y, "y"), ctx
+
+
+def dropout_bwd(dy, ctx: DropoutCtx, *, dx=None, stream=None) -> torch.Tensor:
+    """The gradient of dropout_fwd: dy where the forward kept, scaled as it was, else 0."""
+    if stream is not None:
+        with _on(stream, _dev(dy, "dy")):
+            return dropout_bwd(dy, ctx, dx=dx)
+    return _dropout(dy, "dy", ctx.p, ctx.rng, ctx.site, None, dx, "dx")
+
+
+NORMS = {"rms": 0, "layer": 1}
+
+
+@dataclass
+class BlockJoinCtx:
+    """What block_join_bwd needs of its forward: x (with a norm of it, or a gate), h (with the norm behind it), their
+    statistics, and the dropout's probability, (seed, step) and site."""
+    x: torch.Tensor | None = None
+    h: torch.Tensor | None = None
+    norm: str = "rms"
+    scale: float = 1.0
+    p: float = 0.0
+    rng: torch.Tensor | None = None
+    site: int = 0
+    post_mu: torch.Tensor | None = None
+    post_rsigma: torch.Tensor | None = None
+    pre_mu: torch.Tensor | None = None
+    pre_rsigma: torch.Tensor | None = None
+
+
+def _norm(norm) -> int:
+    if norm not in NORMS:
+        raise ValueError(f"unknown norm {norm!r}: one of {', '.join(NORMS)}")
+    return NORMS[norm]
+
+
+def _vectors(D, dev, **vectors):
+    """Checks the [D] vectors that are there, all of one type; returns its number."""
+    kind = None
+    for name, v in vectors.items():
+        if v is None:
+            continue
+        if kind is None:
+            kind = v.dtype
+            elem = _elem(v, name)
+        _flat(v, name, (D,), kind, dev)
+    return 0 if kind is None else elem
+
+
+def block_join_fwd(x, residual=None, *, norm="rms", post_gamma=None, post_beta=None, gate=None, scale=1.0, p=0.0, rng=None,
+                   site=0, pre_gamma=None, pre_beta=None, eps=1e-5, h=None, y=None, stream=None):
+    """Joins a block's output x to the residual stream, 2-D tensors of one type (bf16, fp16 or fp32):
+        h = residual + scale * dropout(gate * norm(x)),  y = norm(h)
+    where post_gamma (and post_beta) ask for the norm of x, pre_gamma (and pre_beta) for y, the next block's input, and every
+    part may be left out; norm: "rms" or "layer". Returns (h, y, ctx); y is None without pre_gamma. h is rounded to the type
+    before it is normalised. p, rng, site: as dropout_fwd's. The vectors are of one type, any of the three."""
+    elem, kind = _elem(x, "x"), _norm(norm)
+    if x.dim() != 2:
+        raise ValueError(f"x has shape {tuple(x.shape)}: expected two dimensions")
+    M, D = x.shape
+    dt, dev, device = x.dtype, _dev(x, "x"), x.device
+    if stream is not None:
+        with _on(stream, dev):
+            return block_join_fwd(x, residual, norm=norm, post_gamma=post_gamma, post_beta=post_beta, gate=gate, scale=scale, p=p,
+                                  rng=rng, site=site, pre_gamma=pre_gamma, pre_beta=pre_beta, eps=eps, h=h, y=y)
+    ldx = _rows(x, "x", M, D, dt, dev)
+    ldr = _rows(residual, "residual", M, D, dt, dev) if residual is not None else 0
+    pe = _vectors(D, dev, post_gamma=post_gamma, post_beta=post_beta, gate=gate, pre_gamma=pre_gamma, pre_beta=pre_beta)
+    ctx = BlockJoinCtx(None, None, norm, scale, p, None, site)
+    if rng is not None:
+        ctx.rng = torch.empty_like(rng)
+    drop = _drop(p, rng, site, ctx.rng, dev)
+    ldh = ldy = D
+    if h is None:
+        h = _e((M, D), dt, device)
+    else:
+        ldh = _rows(h, "h", M, D, dt, dev)
+    if pre_gamma is None:
+        if y is not None:
+            raise ValueError("y without pre_gamma")
+    else:
+        if y is None:
+            y = _e((M, D), dt, device)
+        else:
+            ldy = _rows(y, "y", M, D, dt, dev)
+        ctx.h, ctx.pre_rsigma = h, _e((M,), torch.float32, device)
+        if kind:
+            ctx.pre_mu = _e((M,), torch.float32, device)
+    if post_gamma is not None:
+        ctx.post_rsigma = _e((M,), torch.float32, device)
+        if kind:
+            ctx.post_mu = _e((M,), torch.float32, device)
+    if post_gamma is not None or gate is not None:
+        ctx.x = x
+    a = CBlockJoinFwd(M, D, elem, pe, kind, eps, scale, x.data_ptr(), _ptr(residual), _ptr(post_gamma), _ptr(post_beta), _ptr(gate),
+                      _ptr(pre_gamma), _ptr(pre_beta), drop, h.data_ptr(), _ptr(y), _ptr(ctx.post_mu), _ptr(ctx.post_rsigma),
+                      _ptr(ctx.pre_mu), _ptr(ctx.pre_rsigma), ldx, ldr, ldh, ldy)
+    _check(_c_block_join_fwd(C.byref(a), _raw_stream(dev)))
+    return h, y, ctx
+
+
+@dataclass
+class BlockJoinGrads:
+    """Gradients of block_join_bwd; those of parts that the forward left out are None. workspace: scratch that the caller
+    keeps from call to call; None: each call takes its own from the current stream's memory and gives it back."""
+    dx: torch.Tensor
+    dresidual: torch.Tensor | None = None
+    dpost_gamma: torch.Tensor | None = None
+    dpost_beta: torch.Tensor | None = None
+    dgate: torch.Tensor | None = None
+    dpre_gamma: torch.Tensor | None = None
+    dpre_beta: torch.Tensor | None = None
+    workspace: torch.Tensor | None = None
+
+
+def block_join_bwd_workspace_size(M, D) -> int:
+    return int(_c_block_join_bwd_ws(M, D))
+
+
+def block_join_grads(M, D, *, dresidual=True, post_gamma=False, post_beta=False, gate=False, pre_gamma=False, pre_beta=False,
+                     dtype=torch.bfloat16, device="cuda", workspace=True) -> BlockJoinGrads:
+    """Gradients of one block_join_bwd, with a workspace to keep: those of the vectors that are named True."""
+    f = lambda on: _e((D,), torch.float32, device) if on else None  # noqa: E731
+    return BlockJoinGrads(_e((M, D), dtype, device), _e((M, D), dtype, device) if dresidual else None, f(post_gamma),
+                          f(post_beta), f(gate), f(pre_gamma), f(pre_beta),
+                          _e((_c_block_join_bwd_ws(M, D),), torch.uint8, device) if workspace else None)
+
+
+def block_join_bwd(dh, dy, ctx: BlockJoinCtx, *, post_gamma=None, post_beta=None, gate=None, pre_gamma=None, pre_beta=None,
+                   grads: BlockJoinGrads | None = None, stream=None) -> BlockJoinGrads:
+    """Gradients of block_join_fwd from those of h (dh, None: zero) and of y (dy, with pre_gamma): dx, dresidual, and in fp32,
+    summed in a fixed order, those of the vectors given, which are the forward's (pre_beta: for its gradient alone)."""
+    first, name = (dh, "dh") if dh is not None else (dy, "dy")
+    if first is None:
+        raise ValueError("neither dh nor dy")
+    elem, kind = _elem(first, name), _norm(ctx.norm)
+    if first.dim() != 2:
+        raise ValueError(f"{name} has shape {tuple(first.shape)}: expected two dimensions")
+    M, D = first.shape
+    dt, dev, device = first.dtype, _dev(first, name), first.device
+    if stream is not None:
+        with _on(stream, dev):
+            return block_join_bwd(dh, dy, ctx, post_gamma=post_gamma, post_beta=post_beta, gate=gate, pre_gamma=pre_gamma,
+                                  pre_beta=pre_beta, grads=grads)
+    lddh = _rows(dh, "dh", M, D, dt, dev) if dh is not None else 0
+    lddy = _rows(dy, "dy", M, D, dt, dev) if dy is not None else 0
+    pe = _vectors(D, dev, post_gamma=post_gamma, post_beta=post_beta, gate=gate, pre_gamma=pre_gamma, pre_beta=pre_beta)
+    if pre_beta is not None and pre_gamma is None:
+        raise ValueError("pre_beta without pre_gamma")
+    drop = _drop(ctx.p, ctx.rng, ctx.site, None, dev)
+
+    def kept(part, gamma, row, name):
+        """Pointers of a norm's input and statistics, and its row stride."""
+        mu = rs = None
+        if gamma is not None:
+            rs, mu = getattr(ctx, part + "_rsigma"), getattr(ctx, part + "_mu")
+            if rs is None or (kind and mu is None):
+                raise ValueError(f"the forward kept no statistics for {part}_gamma")
+            _flat(rs, f"ctx.{part}_rsigma", (M,), torch.float32, dev)
+            if kind:
+                _flat(mu, f"ctx.{part}_mu", (M,), torch.float32, dev)
+        if row is None:
+            raise ValueError(f"ctx.{name} is missing")
+        return row.data_ptr(), _rows(row, "ctx." + name, M, D, dt, dev), _ptr(mu if kind else None), _ptr(rs)
+
+    xp = hp = m1 = r1 = m2 = r2 = None
+    ldx = ldh = 0
+    if post_gamma is not None or gate is not None:
+        xp, ldx, m1, r1 = kept("post", post_gamma, ctx.x, "x")
+    if pre_gamma is not None:
+        hp, ldh, m2, r2 = kept("pre", pre_gamma, ctx.h, "h")
+    lddx = lddr = D
+    if grads is None:
+        grads = block_join_grads(M, D, post_gamma=post_gamma is not None, post_beta=post_beta is not None, gate=gate is not None,
+                                 pre_gamma=pre_gamma is not None, pre_beta=pre_beta is not None, dtype=dt, device=device,
+                                 workspace=False)
+    else:
+        lddx = _rows(grads.dx, "grads.dx", M, D, dt, dev)
+        if grads.dresidual is not None:
+            lddr = _rows(grads.dresidual, "grads.dresidual", M, D, dt, dev)
+        for v in ("dpost_gamma", "dpost_beta", "dgate", "dpre_gamma", "dpre_beta"):
+            if getattr(grads, v) is not None:
+                _flat(getattr(grads, v), "grads." + v, (D,), torch.float32, dev)
+    ws = grads.workspace
+    ws = _e((_c_block_join_bwd_ws(M, D),), torch.uint8, device) if ws is None else _given_ws(ws, dev)
+    a = CBlockJoinBwd(M, D, elem, pe, kind, ctx.scale, _ptr(dh), _ptr(dy), xp, hp, _ptr(post_gamma), _ptr(post_beta), _ptr(gate),
+                      _ptr(pre_gamma), m1, r1, m2, r2, drop, grads.dx.data_ptr(), _ptr(grads.dresidual), _ptr(grads.dpost_gamma),
+                      _ptr(grads.dpost_beta), _ptr(grads.dgate), _ptr(grads.dpre_gamma), _ptr(grads.dpre_beta), ws.data_ptr(),
+                      ws.nbytes, lddh, lddy, ldx, ldh, lddx, lddr)
+    _check(_c_block_join_bwd(C.byref(a), _raw_stream(dev)))
     return grads

@@ -527,15 +527,17 @@ int lnfp8_ctx_offsets(int op, int64_t M, int64_t D, int64_t F, int64_t* offsets,
  * tour: te.LayerNorm, te.Linear; code block 2: the MiniGPT's final norm and
  * head): a LayerNorm with 16- or 32-bit output, 8-bit checkpoints of
  * activations, and a linear layer with bias, activation and residual in its
- * epilogue, each with its backward.
+ * epilogue, each with its backward; and what a block runs beside them: the gated
+ * linear layer of a feed-forward block, the join of a block's output with the
+ * residual stream (norms, gate, dropout, scale), and dropout.
  *
  * Tensors are typed (lnfp8_elem) and row-major; every [rows, cols] tensor that
  * has an ld argument may have a row stride of its own, in elements (0: cols).
  * Checkpoints, mu, rsigma, x_sum, h, w, dw and vectors are contiguous. Outputs
- * must not overlap inputs or each other. Row tensors and vectors of layernorm_*
- * and act_ckpt_* need the alignment of their element only, and any width;
+ * must not overlap inputs or each other. Row tensors and vectors of layernorm_*,
+ * act_ckpt_*, block_join_* and dropout_apply need the alignment of their element only, and any width;
  * rows that are multiples of 16 bytes on 16-byte boundaries run faster.
- * linear_act_* moves its tiles with TMA: 16-byte aligned pointers, K and N
+ * linear_act_* and linear_glu_* move their tiles with TMA: 16-byte aligned pointers, K and N
  * multiples of 8 up to 2^30 - 32, row strides multiples of 8 elements.
  * NaN and Inf pass through the arithmetic as IEEE gives them. A workspace
  * belongs to one call at a time: calls on two streams, or two captured graphs
@@ -682,6 +684,147 @@ lnfp8_status linear_act_bwd(const lnfp8_linear_act_bwd_args* args, lnfp8_stream 
  * (has_act) or without activation, x given as a tensor or restored from a
  * checkpoint (x_from_ckpt); -1 for a negative size. */
 int64_t lnfp8_linear_act_bwd_workspace_size(int64_t M, int64_t K, int64_t N, int has_act, int x_from_ckpt);
+
+typedef struct {
+  int64_t M, K, N;        /* tokens, input features, outputs */
+  int elem;               /* LNFP8_BF16 or LNFP8_FP16, of every tensor */
+  int act;                /* lnfp8_act of the gate */
+  const void* x;          /* [M, K] */
+  const void* w;          /* [2N, K]: the gate's N rows, then the up projection's */
+  const void* bias;       /* [2N] or NULL */
+  void* y;                /* out [M, N] */
+  void* h;                /* out [M, 2N] or NULL: z in the type, what the backward reads */
+  int64_t ldx, ldy;
+} lnfp8_linear_glu_fwd_args;
+
+/* Gated linear layer (the two first projections of a gated feed-forward block):
+ * z = x . w^T + bias, y = T(act(z[:, :N]) * z[:, N:]), both projections, the
+ * activation and the product in one launch and without a workspace. K and N are
+ * multiples of 8, N at most 2^29 - 16. */
+lnfp8_status linear_glu_fwd(const lnfp8_linear_glu_fwd_args* args, lnfp8_stream stream);
+
+typedef struct {
+  int64_t M, K, N;
+  int elem;
+  int act;                /* of the forward */
+  const void* dy;         /* [M, N] */
+  const void* x;          /* [M, K] the forward's input; may be NULL without dw */
+  const void* w;          /* [2N, K]; may be NULL without dx */
+  const void* h;          /* [M, 2N] the forward's h */
+  void* dx;               /* out [M, K] or NULL */
+  void* dw;               /* out [2N, K] or NULL */
+  float* dbias;           /* out [2N] or NULL */
+  void* workspace;        /* lnfp8_linear_glu_bwd_workspace_size bytes, 16-byte aligned */
+  int64_t workspace_bytes;
+  int64_t ld_dy, ldx, ld_dx;
+} lnfp8_linear_glu_bwd_args;
+
+/* Backward of linear_glu_fwd, from h: dz_gate = dy * h_up * act'(h_gate), dz_up = dy * act(h_gate)
+ * (fp32; rounded to the type for the products, as linear_act_bwd's dz), dbias = sum_rows dz (before that
+ * rounding, in a fixed order), dx = T(dz . w), dw = T(dz^T . x). With M = 0, dw and dbias are zero.
+ * The same call gives the same bits. The workspace need not be initialised. */
+lnfp8_status linear_glu_bwd(const lnfp8_linear_glu_bwd_args* args, lnfp8_stream stream);
+
+/* Bytes of linear_glu_bwd's workspace on the current device; -1 for a negative size. */
+int64_t lnfp8_linear_glu_bwd_workspace_size(int64_t M, int64_t K, int64_t N);
+
+/* Dropout. Element (row, col) of a [rows, cols] tensor draws 16 bits u and is dropped (exactly 0, whatever it
+ * holds) where u < t = floor(65536 p + 1/2), else multiplied by 65536 / (65536 - t): p is taken to the nearest
+ * 2^-16, and what is kept is scaled by the probability it was kept with. No mask is stored: the bits are a function
+ * of (seed, step, site, row, col) alone, Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel random numbers: as easy
+ * as 1, 2, 3", 2011) with the key seed (low word first) and the counter (col / 8, row, step mod 2^32, site), whose four
+ * words' 16-bit parts, low part first, belong to columns 8 (col / 8) to 8 (col / 8) + 7. Strides, types and
+ * alignment do not change them.
+ *   rng        device [2] int64: seed and step, read when the call runs; a captured graph draws anew when the caller
+ *              changes them between its launches
+ *   site       a number for each dropout of a step (two calls with the same seed, step and site draw the same bits)
+ *   rng_saved  device [2] int64 or NULL: a copy of rng as the call read it, for the backward */
+typedef struct {
+  double p;                 /* 0..1; NaN is refused */
+  const int64_t* rng;       /* may be NULL with p < 2^-17 (t = 0: nothing is drawn) */
+  int64_t* rng_saved;       /* out, optional */
+  uint32_t site;
+} lnfp8_dropout;
+
+/* y [rows, cols] = dropout of x (elem, row strides ldx, ldy). The backward is the same call on the gradient with the
+ * forward's rng_saved as rng. cols 1..2^30, rows >= 0. */
+lnfp8_status dropout_apply(const void* x, int elem, int64_t rows, int64_t cols, int64_t ldx, const lnfp8_dropout* drop,
+                           void* y, int64_t ldy, lnfp8_stream stream);
+
+/* Norms of block_join: RMS v / sqrt(mean(v^2) + eps), LAYER (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps). */
+typedef enum { LNFP8_NORM_RMS = 0, LNFP8_NORM_LAYER = 1 } lnfp8_norm;
+
+typedef struct {
+  int64_t M, D;             /* rows >= 0, columns 1..16384 */
+  int elem;                 /* lnfp8_elem of x, residual, h, y */
+  int param_elem;           /* lnfp8_elem of the [D] vectors */
+  int norm;                 /* lnfp8_norm of both norms */
+  float eps;                /* >= 0, of both norms */
+  float scale;              /* of the block's output in the sum */
+  const void* x;            /* [M, D] the block's output */
+  const void* residual;     /* [M, D] or NULL (zero) */
+  const void* post_gamma;   /* [D] or NULL: no norm of x */
+  const void* post_beta;    /* [D] or NULL */
+  const void* gate;         /* [D] or NULL */
+  const void* pre_gamma;    /* [D] or NULL: no y */
+  const void* pre_beta;     /* [D] or NULL */
+  lnfp8_dropout drop;
+  void* h;                  /* out [M, D] */
+  void* y;                  /* out [M, D], with pre_gamma */
+  float* post_mu;           /* out [M], with post_gamma and LAYER */
+  float* post_rsigma;       /* out [M], with post_gamma */
+  float* pre_mu;            /* out [M], with pre_gamma and LAYER */
+  float* pre_rsigma;        /* out [M], with pre_gamma */
+  int64_t ldx, ld_residual, ldh, ldy;
+} lnfp8_block_join_fwd_args;
+
+/* Joins a block's output to the residual stream, between one block and the next:
+ *   n = norm(x) * post_gamma + post_beta     (or x)
+ *   h = T(residual + scale * dropout(gate * n))
+ *   y = T(norm(h) * pre_gamma + pre_beta)    of h as it is kept
+ * every part of it optional, in one launch. Statistics and sums in fp32, h and y rounded once. */
+lnfp8_status block_join_fwd(const lnfp8_block_join_fwd_args* args, lnfp8_stream stream);
+
+typedef struct {
+  int64_t M, D;
+  int elem;                 /* of dh, dy, x, h, dx, dresidual */
+  int param_elem;
+  int norm;
+  float scale;
+  const void* dh;           /* [M, D] the gradient of h that comes down the residual stream, or NULL (zero) */
+  const void* dy;           /* [M, D], with pre_gamma */
+  const void* x;            /* [M, D], with post_gamma or gate */
+  const void* h;            /* [M, D] the forward's h, with pre_gamma */
+  const void* post_gamma;   /* the forward's vectors */
+  const void* post_beta;
+  const void* gate;
+  const void* pre_gamma;
+  const float* post_mu;     /* the forward's statistics */
+  const float* post_rsigma;
+  const float* pre_mu;
+  const float* pre_rsigma;
+  lnfp8_dropout drop;       /* rng: the forward's rng_saved; rng_saved is not written */
+  void* dx;                 /* out [M, D] */
+  void* dresidual;          /* out [M, D] or NULL */
+  float* dpost_gamma;       /* out [D], with post_gamma */
+  float* dpost_beta;        /* out [D] or NULL */
+  float* dgate;             /* out [D], with gate */
+  float* dpre_gamma;        /* out [D], with pre_gamma */
+  float* dpre_beta;         /* out [D] or NULL */
+  void* workspace;          /* lnfp8_block_join_bwd_workspace_size bytes, 16-byte aligned */
+  int64_t workspace_bytes;
+  int64_t ld_dh, ld_dy, ldx, ldh, ld_dx, ld_dresidual;
+} lnfp8_block_join_bwd_args;
+
+/* Backward of block_join_fwd: with g = dy * pre_gamma, dH = dh + norm'(g) (the norm's backward at h),
+ * dt = scale * dropout'(dH) and dn = gate * dt:
+ *   dresidual = T(dH), dx = T(norm'(dn * post_gamma)) (or T(dn)), dpre_gamma = sum_rows dy * norm(h),
+ *   dpre_beta = sum_rows dy, dpost_gamma = sum_rows dn * norm(x), dpost_beta = sum_rows dn, dgate = sum_rows dt * n.
+ * Column sums in fp32 in a fixed order: the same call gives the same bits. With M = 0 they are zero. */
+lnfp8_status block_join_bwd(const lnfp8_block_join_bwd_args* args, lnfp8_stream stream);
+
+/* Bytes of block_join_bwd's workspace on the current device; -1 for a negative size. */
+int64_t lnfp8_block_join_bwd_workspace_size(int64_t M, int64_t D);
 
 #ifdef __cplusplus
 }
