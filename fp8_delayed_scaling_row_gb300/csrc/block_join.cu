@@ -8,8 +8,10 @@
 // summand a column: t = xhat a + c where kept. Of column sums the backward needs four at most, since
 // dgate = sum dt n = g1 A + b1 B, dg1 = gate A, db1 = gate B with A = sum dt xhat, B = sum dt.
 #include <algorithm>
+#include <initializer_list>
 
 #include "common.cuh"
+#include "cp_async.cuh"
 #include "internal.h"
 #include "kernel_setup.cuh"
 #include "philox.cuh"
@@ -37,6 +39,7 @@ struct JoinFwdParams {
   int D, param_elem, layer;
   float eps, scale;  // scale: s / (1 - p)
   DropParams drop;
+  int64_t step, xstep, rstep, hstep, ystep;  // rows a group moves on by; the same in bytes of each tensor
 };
 
 struct JoinBwdParams {
@@ -58,6 +61,7 @@ struct JoinBwdParams {
   int D, param_elem, layer, sums;
   float scale;
   DropParams drop;
+  int64_t step, dhstep, dystep, xstep, hstep, dxstep, drstep;
 };
 
 // A column's parameter, or `none` where there is no such vector.
@@ -296,6 +300,462 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) join_bwd_any_kernel(con
   }
 }
 
+// ------------------------------------------------------------ 16-byte rows
+// D a multiple of 8 and rows on 16-byte boundaries: thread t of a row's TPR holds its 16-byte words t, t + TPR, ... (EPC
+// columns each), 16 columns in all, and copies (cp.async) the words of its next RING - 1 rows into its own slots of a ring in
+// shared memory, so that the bytes in flight cost no registers. Both kernels are bound by HBM.
+template <int ELEM>
+struct Word {
+  static constexpr int EPC = ELEM == LNFP8_FP32 ? 4 : 8;
+};
+
+// The draws of a word's columns, one bit a column: kept. An fp32 word is half a group of draws.
+template <int EPC>
+__device__ __forceinline__ uint32_t word_keep(const DropKey& key, uint32_t cut, int c, uint32_t row) {
+  const uint4 u = drop_bits(key, (uint32_t)c >> 3, row);
+  uint32_t w[EPC / 2];
+  if constexpr (EPC == 8) {
+    w[0] = u.x;
+    w[1] = u.y;
+    w[2] = u.z;
+    w[3] = u.w;
+  } else {
+    w[0] = c & 4 ? u.z : u.x;
+    w[1] = c & 4 ? u.w : u.y;
+  }
+  uint32_t keep = 0;
+#pragma unroll
+  for (int k = 0; k < EPC / 2; ++k) {
+    keep |= (w[k] & 0xFFFFu) >= cut ? 1u << (2 * k) : 0u;
+    keep |= (w[k] >> 16) >= cut ? 2u << (2 * k) : 0u;
+  }
+  return keep;
+}
+__device__ __forceinline__ uint64_t keep_pair(uint64_t v, uint32_t keep, int k) {
+  const float2 t = upk(v);
+  return pk(keep >> (2 * k) & 1 ? t.x : 0.f, keep >> (2 * k) & 2 ? t.y : 0.f);
+}
+// A word's parameters as pairs, ones or zeros where there is no such vector.
+template <int EPC>
+__device__ __forceinline__ void params_or(const void* p, int elem, int c, float none, uint64_t* v) {
+  if (p) {
+    load_params<EPC>(p, elem, c, v);
+  } else {
+#pragma unroll
+    for (int k = 0; k < EPC / 2; ++k) v[k] = pk(none, none);
+  }
+}
+
+template <int ELEM, int TPR, int NV>
+struct JoinFwdShape {
+  static constexpr int THREADS = TPR < 256 ? 256 : TPR;
+  static constexpr int WORDS = 2 * NV;  // per thread and row: x, residual
+  static constexpr int RING = 4 * WORDS * THREADS * 16 <= 72 * 1024 ? 4 : 3 * WORDS * THREADS * 16 <= 100 * 1024 ? 3 : 2;
+  static constexpr size_t SMEM = (size_t)RING * WORDS * THREADS * 16;
+};
+
+template <int ELEM, int TPR, int NV>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR < 512 ? 2 : 1) join_fwd_vec_kernel(const JoinFwdParams p) {
+  using S = JoinFwdShape<ELEM, TPR, NV>;
+  constexpr int T = S::THREADS, GPB = T / TPR, RING = S::RING, P = RING - 1;
+  constexpr int EPC = Word<ELEM>::EPC, PP = EPC / 2, ES = ElemSize<ELEM>::value;
+  __shared__ float2 xch[2 * T / 32];
+  extern __shared__ uint4 ring[];  // [RING][WORDS][T]
+  const int g = threadIdx.x / TPR, t = threadIdx.x % TPR;
+  pdl_wait();
+  pdl_launch_dependents();
+  constexpr uint32_t WB = T * 16, SB = S::WORDS * WB;  // bytes of a word of all threads, of a slot
+  const uint32_t mine = (uint32_t)__cvta_generic_to_shared(ring) + threadIdx.x * 16;
+  int64_t row = (int64_t)blockIdx.x * GPB + g;
+  const uint8_t* xp = static_cast<const uint8_t*>(p.x) + row * p.ldx * ES + t * 16;
+  const uint8_t* rp = static_cast<const uint8_t*>(p.resid) + row * p.ldr * ES + t * 16;
+  auto issue = [&](int64_t r, uint32_t slot) {
+    if (r < p.M) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        if ((t + TPR * j) * EPC < p.D) {
+          cp16(slot + j * WB, xp + TPR * j * 16);
+          if (p.resid) cp16(slot + (NV + j) * WB, rp + TPR * j * 16);
+        }
+      }
+      xp += p.xstep;
+      rp += p.rstep;
+    }
+    cp_commit();
+  };
+  // words past D, and a residual that is not there, hold zeros
+#pragma unroll
+  for (int k = 0; k < RING; ++k)
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const bool in = (t + TPR * j) * EPC < p.D;
+      if (!in) sts16_zero(mine + k * SB + j * WB);
+      if (!in || !p.resid) sts16_zero(mine + k * SB + (NV + j) * WB);
+    }
+#pragma unroll
+  for (int k = 0; k < P; ++k) issue(row + k * p.step, mine + k * SB);
+  drop_save(p.drop);
+  const DropKey key = drop_key(p.drop);
+  // the factors of a word's columns: scale * gate * post_gamma, and pre_gamma
+  uint64_t fa[NV][PP], fg[NV][PP];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (t + TPR * j) * EPC, cc = c < p.D ? c : 0;
+    uint64_t f[PP];
+    params_or<EPC>(p.gate, p.param_elem, cc, 1.f, f);
+    params_or<EPC>(p.g1, p.param_elem, cc, 1.f, fa[j]);
+    params_or<EPC>(p.g2, p.param_elem, cc, 0.f, fg[j]);
+#pragma unroll
+    for (int k = 0; k < PP; ++k) fa[j][k] = mul_2(mul_2(f[k], pk(p.scale, p.scale)), fa[j][k]);
+  }
+  const float inv_d = 1.0f / (float)p.D;
+  int turn = 0;
+  uint32_t slot = mine, last = mine + P * SB;  // the row's slot; the one read before it, filled next
+  uint8_t* hp = static_cast<uint8_t*>(p.h) + row * p.ldh * ES + t * 16;
+  uint8_t* yp = static_cast<uint8_t*>(p.y) + row * p.ldy * ES + t * 16;
+  // v becomes the centred row; returns the reciprocal deviation
+  auto stats = [&](uint64_t(&v)[NV][PP], float& mu) {
+    mu = 0.f;
+    if (p.layer) {
+      uint64_t s2 = 0;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int k = 0; k < PP; ++k) s2 = add_2(s2, v[j][k]);
+      const float2 s = upk(s2);
+      mu = row_sum<TPR>(s.x + s.y, xch, turn) * inv_d;
+      const uint64_t mu2 = pk(mu, mu);
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if ((t + TPR * j) * EPC < p.D) {
+#pragma unroll
+          for (int k = 0; k < PP; ++k) v[j][k] = sub_2(v[j][k], mu2);
+        }
+    }
+    uint64_t q2 = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int k = 0; k < PP; ++k) q2 = fma_2(v[j][k], v[j][k], q2);
+    const float2 q = upk(q2);
+    return rsqrt_nr(row_sum<TPR>(q.x + q.y, xch, turn) * inv_d + p.eps);
+  };
+  for (; row - g < p.M; row += p.step) {  // the same trip count for every group of the block
+    issue(row + P * p.step, last);
+    cp_wait<P>();
+    const bool active = row < p.M;
+    uint64_t v[NV][PP];
+    uint32_t keep[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) unpack_word<ELEM>(lds16(slot + j * WB), v[j]);
+    if (p.drop.cut) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) keep[j] = word_keep<EPC>(key, p.drop.cut, (t + TPR * j) * EPC, (uint32_t)row);
+    }
+    if (p.g1) {
+      float mu;
+      const float rs = stats(v, mu);
+      const uint64_t rs2 = pk(rs, rs);
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int k = 0; k < PP; ++k) v[j][k] = mul_2(v[j][k], rs2);
+      if (t == 0 && active) {
+        p.rs1[row] = rs;
+        if (p.layer) p.mu1[row] = mu;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (t + TPR * j) * EPC;
+      if (p.b1) {  // read again for each row (from L1)
+        uint64_t b[PP], f[PP];
+        params_or<EPC>(p.b1, p.param_elem, c < p.D ? c : 0, 0.f, b);
+        params_or<EPC>(p.gate, p.param_elem, c < p.D ? c : 0, 1.f, f);
+#pragma unroll
+        for (int k = 0; k < PP; ++k) v[j][k] = fma_2(v[j][k], fa[j][k], mul_2(mul_2(f[k], pk(p.scale, p.scale)), b[k]));
+      } else {
+#pragma unroll
+        for (int k = 0; k < PP; ++k) v[j][k] = mul_2(v[j][k], fa[j][k]);
+      }
+      if (p.drop.cut) {
+#pragma unroll
+        for (int k = 0; k < PP; ++k) v[j][k] = keep_pair(v[j][k], keep[j], k);
+      }
+      uint64_t r[PP];
+      unpack_word<ELEM>(lds16(slot + (NV + j) * WB), r);
+#pragma unroll
+      for (int k = 0; k < PP; ++k) v[j][k] = add_2(v[j][k], r[k]);
+      const uint4 u = pack_word<ELEM>(v[j]);
+      unpack_word<ELEM>(u, v[j]);  // normalised as it is kept
+      if (c < p.D) {
+        if (active) *reinterpret_cast<uint4*>(hp + TPR * j * 16) = u;
+      } else {
+#pragma unroll
+        for (int k = 0; k < PP; ++k) v[j][k] = 0;  // a beta there
+      }
+    }
+    last = slot;
+    slot = slot == mine + P * SB ? mine : slot + SB;
+    hp += p.hstep;
+    if (!p.g2) continue;
+    float mu;
+    const float rs = stats(v, mu);
+    if (active) {
+      const uint64_t rs2 = pk(rs, rs);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (t + TPR * j) * EPC;
+        if (c >= p.D) continue;
+        uint64_t b[PP];
+        params_or<EPC>(p.b2, p.param_elem, c, 0.f, b);
+#pragma unroll
+        for (int k = 0; k < PP; ++k) v[j][k] = fma_2(mul_2(v[j][k], rs2), fg[j][k], b[k]);
+        *reinterpret_cast<uint4*>(yp + TPR * j * 16) = pack_word<ELEM>(v[j]);
+      }
+      if (t == 0) {
+        p.rs2[row] = rs;
+        if (p.layer) p.mu2[row] = mu;
+      }
+    }
+    yp += p.ystep;
+  }
+  cp_wait<0>();
+}
+
+template <int ELEM, int TPR, int NV>
+struct JoinBwdShape {
+  static constexpr int THREADS = TPR < 256 ? 256 : TPR;
+  // bytes per thread and row, each kind an array over the threads: dy, h, dh, x, then rs2, mu2, rs1, mu1
+  static constexpr int W = NV * 16, S_OFF = 4 * W, BYTES = S_OFF + 16;
+  static constexpr int RING = 3 * BYTES * THREADS <= 224 * 1024 ? 3 : 2;
+  static constexpr size_t SMEM = (size_t)RING * BYTES * THREADS;
+  static_assert(SMEM <= 224 * 1024, "shared memory budget");
+};
+
+// SUMS: with the sums of dy and dt (for the betas), or without them.
+template <int ELEM, int TPR, int NV, bool SUMS>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR < 512 ? 2 : 1) join_bwd_vec_kernel(const JoinBwdParams p) {
+  using S = JoinBwdShape<ELEM, TPR, NV>;
+  constexpr int T = S::THREADS, GPB = T / TPR, RING = S::RING, P = RING - 1;
+  constexpr int EPC = Word<ELEM>::EPC, PP = EPC / 2, ES = ElemSize<ELEM>::value;
+  __shared__ float2 xch[2 * T / 32];
+  extern __shared__ uint4 ring[];  // [RING][BYTES * T]
+  const int g = threadIdx.x / TPR, t = threadIdx.x % TPR;
+  pdl_wait();
+  pdl_launch_dependents();
+  constexpr uint32_t WB = T * 16, TB = NV * WB, SB = S::BYTES * T;  // bytes of a word of all threads, of a tensor, of a slot
+  const uint32_t base = (uint32_t)__cvta_generic_to_shared(ring);
+  const uint32_t t16 = threadIdx.x * 16, t4 = S::S_OFF * T + threadIdx.x * 4;
+  int64_t row = (int64_t)blockIdx.x * GPB + g;
+  const bool has_x = p.g1 != nullptr || p.gate != nullptr;
+  const uint8_t* dyp = static_cast<const uint8_t*>(p.dy) + row * p.lddy * ES + t * 16;
+  const uint8_t* hp = static_cast<const uint8_t*>(p.h) + row * p.ldh * ES + t * 16;
+  const uint8_t* dhp = static_cast<const uint8_t*>(p.dh) + row * p.lddh * ES + t * 16;
+  const uint8_t* xp = static_cast<const uint8_t*>(p.x) + row * p.ldx * ES + t * 16;
+  auto issue = [&](int64_t r, uint32_t slot) {
+    if (r < p.M) {
+      if (p.g2) {
+        cp4(slot + t4, p.rs2 + r);
+        if (p.layer) cp4(slot + t4 + 4 * T, p.mu2 + r);
+      }
+      if (p.g1) {
+        cp4(slot + t4 + 8 * T, p.rs1 + r);
+        if (p.layer) cp4(slot + t4 + 12 * T, p.mu1 + r);
+      }
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        if ((t + TPR * j) * EPC < p.D) {
+          if (p.g2) {
+            cp16(slot + t16 + j * WB, dyp + TPR * j * 16);
+            cp16(slot + t16 + TB + j * WB, hp + TPR * j * 16);
+          }
+          if (p.dh) cp16(slot + t16 + 2 * TB + j * WB, dhp + TPR * j * 16);
+          if (has_x) cp16(slot + t16 + 3 * TB + j * WB, xp + TPR * j * 16);
+        }
+      }
+      dyp += p.dystep;
+      hp += p.hstep;
+      dhp += p.dhstep;
+      xp += p.xstep;
+    }
+    cp_commit();
+  };
+  // words past D, tensors and means that are not there hold zeros
+#pragma unroll
+  for (int k = 0; k < RING; ++k) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sts4(base + k * SB + t4 + 4 * i * T, 0u);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const bool in = (t + TPR * j) * EPC < p.D;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (!in || !(i < 2 ? p.g2 != nullptr : i == 2 ? p.dh != nullptr : has_x)) sts16_zero(base + k * SB + t16 + i * TB + j * WB);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < P; ++k) issue(row + k * p.step, base + k * SB);
+  const DropKey key = drop_key(p.drop);
+  constexpr int NS = SUMS ? 4 : 2;
+  uint64_t acc[NS][NV][PP];  // sums of dy hhat, dt xhat, dy, dt
+#pragma unroll
+  for (int i = 0; i < NS; ++i)
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int k = 0; k < PP; ++k) acc[i][j][k] = 0;
+  const float inv_d = 1.0f / (float)p.D;
+  int turn = 0;
+  uint32_t slot = base, last = base + P * SB;
+  uint8_t* op = static_cast<uint8_t*>(p.dx) + row * p.lddx * ES + t * 16;
+  uint8_t* drp = static_cast<uint8_t*>(p.dres) + row * p.lddres * ES + t * 16;
+  for (; row - g < p.M; row += p.step) {
+    issue(row + P * p.step, last);
+    cp_wait<P>();
+    const bool active = row < p.M;
+    uint64_t d[NV][PP], xh[NV][PP];
+    uint32_t keep[NV];
+    if (p.drop.cut) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) keep[j] = word_keep<EPC>(key, p.drop.cut, (t + TPR * j) * EPC, (uint32_t)row);
+    }
+    if (p.g2) {
+      const float rs = __uint_as_float(lds4(slot + t4)), mu = __uint_as_float(lds4(slot + t4 + 4 * T));
+      const uint64_t rs2 = pk(rs, rs), mu2 = pk(mu, mu);
+      uint64_t a1 = 0, a2 = 0;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (t + TPR * j) * EPC;
+        const bool in = c < p.D;
+        uint64_t ga[PP];
+        load_params<EPC>(p.g2, p.param_elem, in ? c : 0, ga);
+        unpack_word<ELEM>(lds16(slot + t16 + j * WB), d[j]);
+        unpack_word<ELEM>(lds16(slot + t16 + TB + j * WB), xh[j]);
+#pragma unroll
+        for (int k = 0; k < PP; ++k) {
+          xh[j][k] = mul_2(sub_2(xh[j][k], mu2), rs2);
+          if (active) {
+            acc[0][j][k] = fma_2(d[j][k], xh[j][k], acc[0][j][k]);
+            if constexpr (SUMS) acc[2][j][k] = add_2(acc[2][j][k], d[j][k]);
+          }
+          d[j][k] = mul_2(d[j][k], ga[k]);  // zero past D
+          a1 = add_2(a1, d[j][k]);
+          a2 = fma_2(d[j][k], xh[j][k], a2);
+        }
+      }
+      const float2 p1 = upk(a1), p2 = upk(a2);
+      const float2 sums = row_sum2<TPR>(p1.x + p1.y, p2.x + p2.y, xch, turn);
+      const float mg = p.layer ? sums.x * inv_d : 0.f, nmx = -sums.y * inv_d;
+      const uint64_t mg2 = pk(mg, mg), nmx2 = pk(nmx, nmx);
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int k = 0; k < PP; ++k) d[j][k] = mul_2(fma_2(nmx2, xh[j][k], sub_2(d[j][k], mg2)), rs2);
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int k = 0; k < PP; ++k) d[j][k] = 0;
+    }
+    const float rs = __uint_as_float(lds4(slot + t4 + 8 * T)), mu = __uint_as_float(lds4(slot + t4 + 12 * T));
+    const uint64_t rs2 = pk(rs, rs), mu2 = pk(mu, mu);
+    uint64_t a1 = 0, a2 = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (t + TPR * j) * EPC;
+      const bool in = c < p.D;
+      uint64_t r[PP];
+      unpack_word<ELEM>(lds16(slot + t16 + 2 * TB + j * WB), r);
+#pragma unroll
+      for (int k = 0; k < PP; ++k) d[j][k] = add_2(d[j][k], r[k]);
+      if (p.dres && active && in) *reinterpret_cast<uint4*>(drp + TPR * j * 16) = pack_word<ELEM>(d[j]);
+#pragma unroll
+      for (int k = 0; k < PP; ++k) {
+        d[j][k] = mul_2(d[j][k], pk(p.scale, p.scale));
+        if (p.drop.cut) d[j][k] = keep_pair(d[j][k], keep[j], k);
+        if (!in) d[j][k] = 0;  // the norm's mean there
+      }
+      if (has_x) {
+        uint64_t f[PP], q[PP];
+        params_or<EPC>(p.gate, p.param_elem, in ? c : 0, 1.f, f);
+        params_or<EPC>(p.g1, p.param_elem, in ? c : 0, 1.f, q);
+        unpack_word<ELEM>(lds16(slot + t16 + 3 * TB + j * WB), xh[j]);
+#pragma unroll
+        for (int k = 0; k < PP; ++k) {
+          if (p.g1) xh[j][k] = mul_2(sub_2(xh[j][k], mu2), rs2);
+          if (active) {
+            acc[1][j][k] = fma_2(d[j][k], xh[j][k], acc[1][j][k]);
+            if constexpr (SUMS) acc[3][j][k] = add_2(acc[3][j][k], d[j][k]);
+          }
+          d[j][k] = mul_2(d[j][k], mul_2(f[k], q[k]));
+          a1 = add_2(a1, d[j][k]);
+          a2 = fma_2(d[j][k], xh[j][k], a2);
+        }
+      }
+    }
+    if (p.g1) {
+      const float2 p1 = upk(a1), p2 = upk(a2);
+      const float2 sums = row_sum2<TPR>(p1.x + p1.y, p2.x + p2.y, xch, turn);
+      const float mg = p.layer ? sums.x * inv_d : 0.f, nmx = -sums.y * inv_d;
+      const uint64_t mg2 = pk(mg, mg), nmx2 = pk(nmx, nmx);
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int k = 0; k < PP; ++k) d[j][k] = mul_2(fma_2(nmx2, xh[j][k], sub_2(d[j][k], mg2)), rs2);
+    }
+    if (active) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if ((t + TPR * j) * EPC < p.D) *reinterpret_cast<uint4*>(op + TPR * j * 16) = pack_word<ELEM>(d[j]);
+    }
+    op += p.dxstep;
+    drp += p.drstep;
+    last = slot;
+    slot = slot == base + P * SB ? base : slot + SB;
+  }
+  cp_wait<0>();
+  // column partials: the row groups of a warp by shuffles, then the others in turn in the ring's memory
+  float* red = reinterpret_cast<float*>(ring);
+  constexpr int TURNS = TPR < 32 ? T / 32 : GPB;
+  if constexpr (TPR < 32) {
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int k = 0; k < PP; ++k)
+#pragma unroll
+          for (int o = TPR; o < 32; o <<= 1) acc[i][j][k] = add_2(acc[i][j][k], __shfl_xor_sync(0xFFFFFFFFu, acc[i][j][k], o));
+  }
+#pragma unroll
+  for (int i = 0; i < NS; ++i) {
+    constexpr int kPlace[4] = {0, 2, 1, 3};
+    if (!(p.sums >> kPlace[i] & 1)) continue;
+    float* part = p.part + ((int64_t)blockIdx.x * 4 + kPlace[i]) * p.D;
+#pragma unroll 1
+    for (int turn_g = 0; turn_g < TURNS; ++turn_g) {
+      if constexpr (TURNS > 1) __syncthreads();
+      if (TPR < 32 ? (int)threadIdx.x >> 5 != turn_g || (threadIdx.x & 31) >= TPR : g != turn_g) continue;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (t + TPR * j) * EPC;
+        if (c >= p.D) continue;
+#pragma unroll
+        for (int q = 0; q < PP / 2; ++q) {
+          const float2 lo = upk(acc[i][j][2 * q]), hi = upk(acc[i][j][2 * q + 1]);
+          float4 v = make_float4(lo.x, lo.y, hi.x, hi.y);
+          if (turn_g > 0) {
+            const float4 o = *reinterpret_cast<const float4*>(red + c + 4 * q);
+            v = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
+          }
+          *reinterpret_cast<float4*>((turn_g == TURNS - 1 ? part : red) + c + 4 * q) = v;
+        }
+      }
+    }
+  }
+}
+
 // The column sums of n partial rows in a fixed order (32 columns a block, warp w adds rows w, w + 32, ..., then the warps'
 // sums are added over the lanes), and what the gradients make of them.
 struct JoinSumParams {
@@ -386,6 +846,91 @@ lnfp8_status bwd_any(const JoinBwdParams& p, int* blocks_out, cudaStream_t st) {
   return bwd_any_launch<ELEM, 1024, 16>(p, blocks_out, st);
 }
 
+bool row_aligned(const void* p, int64_t ld, int es) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * es % 16 == 0; }
+bool vectors_aligned(std::initializer_list<const void*> v) {
+  for (const void* p : v)
+    if (reinterpret_cast<uintptr_t>(p) % 16) return false;
+  return true;
+}
+
+template <int ELEM, int TPR, int NV>
+lnfp8_status fwd_vec_launch(const JoinFwdParams& p, cudaStream_t st) {
+  using S = JoinFwdShape<ELEM, TPR, NV>;
+  constexpr auto kernel = join_fwd_vec_kernel<ELEM, TPR, NV>;
+  int bps = 1;
+  const lnfp8_status s = kernel_setup<kernel>(S::THREADS, S::SMEM, &bps, "block_join_fwd: kernel set-up");
+  if (s != LNFP8_OK) return s;
+  constexpr int gpb = S::THREADS / TPR, es = ElemSize<ELEM>::value;
+  const int64_t blocks = min64((p.M + gpb - 1) / gpb, (int64_t)num_sms() * bps);
+  JoinFwdParams q = p;
+  q.step = blocks * gpb;
+  q.xstep = q.step * p.ldx * es;
+  q.rstep = q.step * p.ldr * es;
+  q.hstep = q.step * p.ldh * es;
+  q.ystep = q.step * p.ldy * es;
+  if (launch_pdl(kernel, dim3((unsigned)blocks), dim3(S::THREADS), S::SMEM, st, q) != cudaSuccess) return check_launch("block_join_fwd launch");
+  return check_launch("block_join_fwd");
+}
+template <int ELEM>
+lnfp8_status fwd(const JoinFwdParams& p, cudaStream_t st) {
+  constexpr int es = ElemSize<ELEM>::value, NV = 16 / Word<ELEM>::EPC;
+  const bool vec = p.D % 8 == 0 && p.D <= 8192 && row_aligned(p.x, p.ldx, es) && row_aligned(p.h, p.ldh, es) &&
+                   (!p.resid || row_aligned(p.resid, p.ldr, es)) && (!p.g2 || row_aligned(p.y, p.ldy, es)) &&
+                   vectors_aligned({p.g1, p.b1, p.gate, p.g2, p.b2});
+  if (!vec) return fwd_any<ELEM>(p, st);
+  if (p.D <= 128) return fwd_vec_launch<ELEM, 8, NV>(p, st);
+  if (p.D <= 256) return fwd_vec_launch<ELEM, 16, NV>(p, st);
+  if (p.D <= 512) return fwd_vec_launch<ELEM, 32, NV>(p, st);
+  if (p.D <= 1024) return fwd_vec_launch<ELEM, 64, NV>(p, st);
+  if (p.D <= 2048) return fwd_vec_launch<ELEM, 128, NV>(p, st);
+  if (p.D <= 4096) return fwd_vec_launch<ELEM, 256, NV>(p, st);
+  return fwd_vec_launch<ELEM, 512, NV>(p, st);
+}
+
+template <int ELEM, int TPR, int NV, bool SUMS>
+lnfp8_status bwd_vec_launch(const JoinBwdParams& p, int* blocks_out, cudaStream_t st) {
+  using S = JoinBwdShape<ELEM, TPR, NV>;
+  static_assert(S::SMEM >= TPR * NV * Word<ELEM>::EPC * sizeof(float), "the column partials reuse the ring");
+  constexpr auto kernel = join_bwd_vec_kernel<ELEM, TPR, NV, SUMS>;
+  int bps = 1;
+  const lnfp8_status s = kernel_setup<kernel>(S::THREADS, S::SMEM, &bps, "block_join_bwd: kernel set-up");
+  if (s != LNFP8_OK) return s;
+  constexpr int gpb = S::THREADS / TPR, es = ElemSize<ELEM>::value;
+  const int64_t blocks = min64((p.M + gpb - 1) / gpb, (int64_t)num_sms() * std::min(kBwdBlocksPerSm, bps));
+  *blocks_out = (int)blocks;
+  JoinBwdParams q = p;
+  q.step = blocks * gpb;
+  q.dhstep = q.step * p.lddh * es;
+  q.dystep = q.step * p.lddy * es;
+  q.xstep = q.step * p.ldx * es;
+  q.hstep = q.step * p.ldh * es;
+  q.dxstep = q.step * p.lddx * es;
+  q.drstep = q.step * p.lddres * es;
+  if (launch_pdl(kernel, dim3((unsigned)blocks), dim3(S::THREADS), S::SMEM, st, q) != cudaSuccess) return check_launch("block_join_bwd launch");
+  return check_launch("block_join_bwd");
+}
+template <int ELEM, int NV, bool SUMS>
+lnfp8_status bwd_vec(const JoinBwdParams& p, int* blocks_out, cudaStream_t st) {
+  constexpr int W = NV * Word<ELEM>::EPC;  // columns a thread
+  if (p.D <= 8 * W) return bwd_vec_launch<ELEM, 8, NV, SUMS>(p, blocks_out, st);
+  if (p.D <= 16 * W) return bwd_vec_launch<ELEM, 16, NV, SUMS>(p, blocks_out, st);
+  if (p.D <= 32 * W) return bwd_vec_launch<ELEM, 32, NV, SUMS>(p, blocks_out, st);
+  if (p.D <= 64 * W) return bwd_vec_launch<ELEM, 64, NV, SUMS>(p, blocks_out, st);
+  if (p.D <= 128 * W) return bwd_vec_launch<ELEM, 128, NV, SUMS>(p, blocks_out, st);
+  if (p.D <= 256 * W) return bwd_vec_launch<ELEM, 256, NV, SUMS>(p, blocks_out, st);
+  return bwd_vec_launch<ELEM, 512, NV, SUMS>(p, blocks_out, st);
+}
+template <int ELEM>
+lnfp8_status bwd(const JoinBwdParams& p, int* blocks_out, cudaStream_t st) {
+  constexpr int es = ElemSize<ELEM>::value, NV = 2;
+  const bool vec = p.D % 8 == 0 && p.D <= 512 * NV * Word<ELEM>::EPC && row_aligned(p.dx, p.lddx, es) &&
+                   (!p.dres || row_aligned(p.dres, p.lddres, es)) && (!p.dh || row_aligned(p.dh, p.lddh, es)) &&
+                   (!p.g2 || (row_aligned(p.dy, p.lddy, es) && row_aligned(p.h, p.ldh, es))) &&
+                   (!(p.g1 || p.gate) || row_aligned(p.x, p.ldx, es)) && vectors_aligned({p.g1, p.gate, p.g2});
+  if (!vec) return bwd_any<ELEM>(p, blocks_out, st);
+  return p.sums & 10 ? bwd_vec<ELEM, NV, true>(p, blocks_out, st) : bwd_vec<ELEM, NV, false>(p, blocks_out, st);
+}
+
 }  // namespace
 
 lnfp8_status block_join_fwd_launch(const lnfp8_block_join_fwd_args* a, cudaStream_t st) {
@@ -416,8 +961,8 @@ lnfp8_status block_join_fwd_launch(const lnfp8_block_join_fwd_args* a, cudaStrea
   p.scale = (float)(a->scale * drop_scale(a->drop));
   p.drop = drop_params(a->drop);
   LaunchScope ls("block_join_fwd", st);
-  if (a->elem == LNFP8_BF16) return fwd_any<LNFP8_BF16>(p, st);
-  return a->elem == LNFP8_FP16 ? fwd_any<LNFP8_FP16>(p, st) : fwd_any<LNFP8_FP32>(p, st);
+  if (a->elem == LNFP8_BF16) return fwd<LNFP8_BF16>(p, st);
+  return a->elem == LNFP8_FP16 ? fwd<LNFP8_FP16>(p, st) : fwd<LNFP8_FP32>(p, st);
 }
 
 int64_t block_join_bwd_ws_bytes(int64_t M, int64_t D) {
@@ -464,9 +1009,9 @@ lnfp8_status block_join_bwd_launch(const lnfp8_block_join_bwd_args* a, cudaStrea
   lnfp8_status s;
   {
     LaunchScope ls("block_join_bwd", st);
-    s = a->elem == LNFP8_BF16   ? bwd_any<LNFP8_BF16>(p, &blocks, st)
-        : a->elem == LNFP8_FP16 ? bwd_any<LNFP8_FP16>(p, &blocks, st)
-                                : bwd_any<LNFP8_FP32>(p, &blocks, st);
+    s = a->elem == LNFP8_BF16   ? bwd<LNFP8_BF16>(p, &blocks, st)
+        : a->elem == LNFP8_FP16 ? bwd<LNFP8_FP16>(p, &blocks, st)
+                                : bwd<LNFP8_FP32>(p, &blocks, st);
   }
   if (s != LNFP8_OK || p.sums == 0) return s;
   JoinSumParams q;
