@@ -309,11 +309,10 @@ struct Word {
   static constexpr int EPC = ELEM == LNFP8_FP32 ? 4 : 8;
 };
 
-// The draws of a word's columns, one bit a column: kept. An fp32 word is half a group of draws.
+// The draws of a word's columns, two to a register. An fp32 word is half a group of draws.
 template <int EPC>
-__device__ __forceinline__ uint32_t word_keep(const DropKey& key, uint32_t cut, int c, uint32_t row) {
+__device__ __forceinline__ void word_draws(const DropKey& key, int c, uint32_t row, uint32_t* w) {
   const uint4 u = drop_bits(key, (uint32_t)c >> 3, row);
-  uint32_t w[EPC / 2];
   if constexpr (EPC == 8) {
     w[0] = u.x;
     w[1] = u.y;
@@ -323,17 +322,6 @@ __device__ __forceinline__ uint32_t word_keep(const DropKey& key, uint32_t cut, 
     w[0] = c & 4 ? u.z : u.x;
     w[1] = c & 4 ? u.w : u.y;
   }
-  uint32_t keep = 0;
-#pragma unroll
-  for (int k = 0; k < EPC / 2; ++k) {
-    keep |= (w[k] & 0xFFFFu) >= cut ? 1u << (2 * k) : 0u;
-    keep |= (w[k] >> 16) >= cut ? 2u << (2 * k) : 0u;
-  }
-  return keep;
-}
-__device__ __forceinline__ uint64_t keep_pair(uint64_t v, uint32_t keep, int k) {
-  const float2 t = upk(v);
-  return pk(keep >> (2 * k) & 1 ? t.x : 0.f, keep >> (2 * k) & 2 ? t.y : 0.f);
 }
 // A word's parameters as pairs, ones or zeros where there is no such vector.
 template <int EPC>
@@ -445,12 +433,12 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR < 512 ? 2 : 1) join
     cp_wait<P>();
     const bool active = row < p.M;
     uint64_t v[NV][PP];
-    uint32_t keep[NV];
+    uint32_t draws[NV][PP];
 #pragma unroll
     for (int j = 0; j < NV; ++j) unpack_word<ELEM>(lds16(slot + j * WB), v[j]);
     if (p.drop.cut) {
 #pragma unroll
-      for (int j = 0; j < NV; ++j) keep[j] = word_keep<EPC>(key, p.drop.cut, (t + TPR * j) * EPC, (uint32_t)row);
+      for (int j = 0; j < NV; ++j) word_draws<EPC>(key, (t + TPR * j) * EPC, (uint32_t)row, draws[j]);
     }
     if (p.g1) {
       float mu;
@@ -480,7 +468,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR < 512 ? 2 : 1) join
       }
       if (p.drop.cut) {
 #pragma unroll
-        for (int k = 0; k < PP; ++k) v[j][k] = keep_pair(v[j][k], keep[j], k);
+        for (int k = 0; k < PP; ++k) v[j][k] = drop_pair(v[j][k], draws[j][k], key.cutw);
       }
       uint64_t r[PP];
       unpack_word<ELEM>(lds16(slot + (NV + j) * WB), r);
@@ -615,10 +603,10 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR < 512 ? 2 : 1) join
     cp_wait<P>();
     const bool active = row < p.M;
     uint64_t d[NV][PP], xh[NV][PP];
-    uint32_t keep[NV];
+    uint32_t draws[NV][PP];
     if (p.drop.cut) {
 #pragma unroll
-      for (int j = 0; j < NV; ++j) keep[j] = word_keep<EPC>(key, p.drop.cut, (t + TPR * j) * EPC, (uint32_t)row);
+      for (int j = 0; j < NV; ++j) word_draws<EPC>(key, (t + TPR * j) * EPC, (uint32_t)row, draws[j]);
     }
     if (p.g2) {
       const float rs = __uint_as_float(lds4(slot + t4)), mu = __uint_as_float(lds4(slot + t4 + 4 * T));
@@ -673,7 +661,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR < 512 ? 2 : 1) join
 #pragma unroll
       for (int k = 0; k < PP; ++k) {
         d[j][k] = mul_2(d[j][k], pk(p.scale, p.scale));
-        if (p.drop.cut) d[j][k] = keep_pair(d[j][k], keep[j], k);
+        if (p.drop.cut) d[j][k] = drop_pair(d[j][k], draws[j][k], key.cutw);
         if (!in) d[j][k] = 0;  // the norm's mean there
       }
       if (has_x) {

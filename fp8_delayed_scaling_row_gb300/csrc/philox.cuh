@@ -34,11 +34,14 @@ inline double drop_scale(const lnfp8_dropout& d) {
   return cut >= 65536 ? 0.0 : 65536.0 / (65536.0 - cut);
 }
 
+// `cut` as the high half of a word to compare draws with. Where everything is dropped (cut 65536) draws are zeros
+// instead, below any other cut.
 struct DropKey {
-  uint32_t k0, k1, step, site;
+  uint32_t k0, k1, step, site, cutw;
+  bool all;
 };
 __device__ __forceinline__ DropKey drop_key(const DropParams& d) {
-  DropKey k = {0u, 0u, 0u, d.site};
+  DropKey k = {0u, 0u, 0u, d.site, d.cut > 65535u ? 0xFFFF0000u : d.cut << 16, d.cut > 65535u};
   if (d.cut) {
     const uint64_t seed = (uint64_t)d.rng[0];
     k.k0 = (uint32_t)seed;
@@ -68,7 +71,17 @@ __device__ __forceinline__ uint4 drop_bits(const DropKey& key, uint32_t group, u
     k0 += 0x9E3779B9u;
     k1 += 0xBB67AE85u;
   }
-  return make_uint4(c0, c1, c2, c3);
+  return key.all ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(c0, c1, c2, c3);
+}
+
+// Two neighbouring elements, zero where their draws (the halves of w) are below the cut.
+__device__ __forceinline__ uint64_t drop_pair(uint64_t v, uint32_t w, uint32_t cutw) {
+  float lo, hi;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+  lo = (w << 16) >= cutw ? lo : 0.f;
+  hi = w >= cutw ? hi : 0.f;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
 }
 
 }  // namespace lnfp8
