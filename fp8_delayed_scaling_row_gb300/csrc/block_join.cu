@@ -56,7 +56,7 @@ struct JoinBwdParams {
   const float* rs2;
   void* dx;
   void* dres;
-  float* part;  // [blocks][4][D]: sums of dy hhat, dy, dt xhat, dt, as far as `sums` has their bits
+  float* part;  // [blocks][4][D]: sums of dy hhat, dy, dt xhat / scale, dt / scale, as far as `sums` has their bits
   int64_t M, lddh, lddy, ldx, ldh, lddx, lddres;
   int D, param_elem, layer, sums;
   float scale;
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) join_bwd_any_kernel(con
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
       const bool keep = p.drop.cut == 0 || bits[32 * i + lane] >= p.drop.cut;
-      d[i] = keep && active && i < n ? d[i] * p.scale : 0.f;  // dt
+      d[i] = keep && active && i < n ? d[i] : 0.f;
     }
     float rs = 1.f;
     if (p.g1 || p.gate) {
@@ -255,12 +255,10 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) join_bwd_any_kernel(con
       }
     }
     float mu_ = 0.f, mux = 0.f;
-    if (p.g1 || p.gate) {
 #pragma unroll
-      for (int i = 0; i < NE; ++i) {
-        const int c = tc + (i < n ? TPR * i : 0);
-        d[i] *= param_or(p.gate, p.param_elem, c, 1.f) * param_or(p.g1, p.param_elem, c, 1.f);
-      }
+    for (int i = 0; i < NE; ++i) {
+      const int c = tc + (i < n ? TPR * i : 0);
+      d[i] *= p.scale * param_or(p.gate, p.param_elem, c, 1.f) * param_or(p.g1, p.param_elem, c, 1.f);
     }
     if (p.g1) {
       float s1 = 0.f, s2 = 0.f;
@@ -323,37 +321,58 @@ __device__ __forceinline__ void word_draws(const DropKey& key, int c, uint32_t r
     w[1] = c & 4 ? u.w : u.y;
   }
 }
-// A word's parameters as pairs, ones or zeros where there is no such vector.
-template <int EPC>
-__device__ __forceinline__ void params_or(const void* p, int elem, int c, float none, uint64_t* v) {
-  if (p) {
-    load_params<EPC>(p, elem, c, v);
-  } else {
+// A block has 512 threads, one to an SM, whose row groups share the columns' factors: in fp32 in shared memory, 16 bytes of
+// neighbouring lanes side by side, ready to be used (in registers they cost a block's worth of occupancy, read again as
+// parameters 60 instructions a row). FULL: with means (layer norms) and betas; without them (RMS) rows cost half the instructions.
+constexpr int kVecThreads = 512;
+constexpr int kVecSmem = 226 * 1024;
+
+// Four columns of a factor array: quarter q of the row's words' quarters.
+template <int TPR, int NV, int EPC>
+__device__ __forceinline__ void put_factors(uint4* at, int k, const void* a, const void* b, int elem, float scale, float none, int D) {
+  constexpr int Q = NV * EPC / 4;  // of a thread
+  float4* dst = reinterpret_cast<float4*>(at) + k * Q * TPR;
+  for (int i = threadIdx.x; i < Q * TPR; i += kVecThreads) {
+    const int t = i % TPR, q = i / TPR, c = (t + TPR * (q * 4 / EPC)) * EPC + q * 4 % EPC;
+    float v[4];
 #pragma unroll
-    for (int k = 0; k < EPC / 2; ++k) v[k] = pk(none, none);
+    for (int e = 0; e < 4; ++e) v[e] = c < D ? scale * param_or(a, elem, c + e, none) * param_or(b, elem, c + e, 1.f) : 0.f;
+    dst[i] = make_float4(v[0], v[1], v[2], v[3]);
+  }
+}
+template <int TPR, int NV, int EPC>
+__device__ __forceinline__ void get_factors(uint32_t at, int k, int j, uint64_t* v) {
+  constexpr int Q = NV * EPC / 4;
+#pragma unroll
+  for (int h = 0; h < EPC / 4; ++h) {
+    const uint4 u = lds16(at + ((k * Q + j * (EPC / 4) + h) * TPR) * 16);
+    v[2 * h] = pk(__uint_as_float(u.x), __uint_as_float(u.y));
+    v[2 * h + 1] = pk(__uint_as_float(u.z), __uint_as_float(u.w));
   }
 }
 
-template <int ELEM, int TPR, int NV>
+template <int ELEM, int TPR, int NV, bool FULL>
 struct JoinFwdShape {
-  static constexpr int THREADS = TPR < 256 ? 256 : TPR;
   static constexpr int WORDS = 2 * NV;  // per thread and row: x, residual
-  static constexpr int RING = 4 * WORDS * THREADS * 16 <= 72 * 1024 ? 4 : 3 * WORDS * THREADS * 16 <= 100 * 1024 ? 3 : 2;
-  static constexpr size_t SMEM = (size_t)RING * WORDS * THREADS * 16;
+  static constexpr int SLOT = WORDS * 16 * kVecThreads, FACTORS = (FULL ? 4 : 2) * TPR * NV * Word<ELEM>::EPC * 4;
+  static constexpr int FIT = (kVecSmem - FACTORS) / SLOT, RING = FIT < 4 ? FIT : 4;
+  static constexpr size_t SMEM = (size_t)RING * SLOT + FACTORS;
+  static_assert(RING >= 2, "shared memory budget");
 };
 
-template <int ELEM, int TPR, int NV>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR < 512 ? 2 : 1) join_fwd_vec_kernel(const JoinFwdParams p) {
-  using S = JoinFwdShape<ELEM, TPR, NV>;
-  constexpr int T = S::THREADS, GPB = T / TPR, RING = S::RING, P = RING - 1;
+template <int ELEM, int TPR, int NV, bool FULL>
+__global__ void __launch_bounds__(kVecThreads, 1) join_fwd_vec_kernel(const JoinFwdParams p) {
+  using S = JoinFwdShape<ELEM, TPR, NV, FULL>;
+  constexpr int T = kVecThreads, GPB = T / TPR, RING = S::RING, P = RING - 1;
   constexpr int EPC = Word<ELEM>::EPC, PP = EPC / 2, ES = ElemSize<ELEM>::value;
   __shared__ float2 xch[2 * T / 32];
-  extern __shared__ uint4 ring[];  // [RING][WORDS][T]
+  extern __shared__ uint4 ring[];  // [RING][WORDS][T], then the factors: scale gate post_gamma, pre_gamma, scale gate post_beta, pre_beta
   const int g = threadIdx.x / TPR, t = threadIdx.x % TPR;
   pdl_wait();
   pdl_launch_dependents();
-  constexpr uint32_t WB = T * 16, SB = S::WORDS * WB;  // bytes of a word of all threads, of a slot
+  constexpr uint32_t WB = T * 16, SB = S::SLOT;  // bytes of a word of all threads, of a slot
   const uint32_t mine = (uint32_t)__cvta_generic_to_shared(ring) + threadIdx.x * 16;
+  const uint32_t fac = (uint32_t)__cvta_generic_to_shared(ring) + RING * SB + t * 16;
   int64_t row = (int64_t)blockIdx.x * GPB + g;
   const uint8_t* xp = static_cast<const uint8_t*>(p.x) + row * p.ldx * ES + t * 16;
   const uint8_t* rp = static_cast<const uint8_t*>(p.resid) + row * p.ldr * ES + t * 16;
@@ -384,27 +403,23 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR < 512 ? 2 : 1) join
   for (int k = 0; k < P; ++k) issue(row + k * p.step, mine + k * SB);
   drop_save(p.drop);
   const DropKey key = drop_key(p.drop);
-  // the factors of a word's columns: scale * gate * post_gamma, and pre_gamma
-  uint64_t fa[NV][PP], fg[NV][PP];
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int c = (t + TPR * j) * EPC, cc = c < p.D ? c : 0;
-    uint64_t f[PP];
-    params_or<EPC>(p.gate, p.param_elem, cc, 1.f, f);
-    params_or<EPC>(p.g1, p.param_elem, cc, 1.f, fa[j]);
-    params_or<EPC>(p.g2, p.param_elem, cc, 0.f, fg[j]);
-#pragma unroll
-    for (int k = 0; k < PP; ++k) fa[j][k] = mul_2(mul_2(f[k], pk(p.scale, p.scale)), fa[j][k]);
+  uint4* fput = ring + RING * SB / 16;
+  put_factors<TPR, NV, EPC>(fput, 0, p.gate, p.g1, p.param_elem, p.scale, 1.f, p.D);
+  if (p.g2) put_factors<TPR, NV, EPC>(fput, 1, p.g2, nullptr, p.param_elem, 1.f, 0.f, p.D);
+  if constexpr (FULL) {
+    put_factors<TPR, NV, EPC>(fput, 2, p.b1, p.gate, p.param_elem, p.scale, 0.f, p.D);
+    put_factors<TPR, NV, EPC>(fput, 3, p.b2, nullptr, p.param_elem, 1.f, 0.f, p.D);
   }
+  __syncthreads();
   const float inv_d = 1.0f / (float)p.D;
   int turn = 0;
   uint32_t slot = mine, last = mine + P * SB;  // the row's slot; the one read before it, filled next
   uint8_t* hp = static_cast<uint8_t*>(p.h) + row * p.ldh * ES + t * 16;
   uint8_t* yp = static_cast<uint8_t*>(p.y) + row * p.ldy * ES + t * 16;
-  // v becomes the centred row; returns the reciprocal deviation
+  // v becomes the centred row (FULL); returns the reciprocal deviation
   auto stats = [&](uint64_t(&v)[NV][PP], float& mu) {
     mu = 0.f;
-    if (p.layer) {
+    if (FULL && p.layer) {
       uint64_t s2 = 0;
 #pragma unroll
       for (int j = 0; j < NV; ++j)
@@ -440,48 +455,39 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR < 512 ? 2 : 1) join
 #pragma unroll
       for (int j = 0; j < NV; ++j) word_draws<EPC>(key, (t + TPR * j) * EPC, (uint32_t)row, draws[j]);
     }
+    uint64_t rs2 = pk(1.f, 1.f);
     if (p.g1) {
       float mu;
       const float rs = stats(v, mu);
-      const uint64_t rs2 = pk(rs, rs);
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int k = 0; k < PP; ++k) v[j][k] = mul_2(v[j][k], rs2);
+      rs2 = pk(rs, rs);
       if (t == 0 && active) {
         p.rs1[row] = rs;
-        if (p.layer) p.mu1[row] = mu;
+        if (FULL && p.layer) p.mu1[row] = mu;
       }
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (t + TPR * j) * EPC;
-      if (p.b1) {  // read again for each row (from L1)
-        uint64_t b[PP], f[PP];
-        params_or<EPC>(p.b1, p.param_elem, c < p.D ? c : 0, 0.f, b);
-        params_or<EPC>(p.gate, p.param_elem, c < p.D ? c : 0, 1.f, f);
+      uint64_t f[PP], r[PP];
+      get_factors<TPR, NV, EPC>(fac, 0, j, f);
+      unpack_word<ELEM>(lds16(slot + (NV + j) * WB), r);
+      if constexpr (FULL) {
+        uint64_t b[PP];
+        get_factors<TPR, NV, EPC>(fac, 2, j, b);
 #pragma unroll
-        for (int k = 0; k < PP; ++k) v[j][k] = fma_2(v[j][k], fa[j][k], mul_2(mul_2(f[k], pk(p.scale, p.scale)), b[k]));
+        for (int k = 0; k < PP; ++k) v[j][k] = fma_2(mul_2(v[j][k], rs2), f[k], b[k]);
       } else {
 #pragma unroll
-        for (int k = 0; k < PP; ++k) v[j][k] = mul_2(v[j][k], fa[j][k]);
+        for (int k = 0; k < PP; ++k) v[j][k] = mul_2(mul_2(v[j][k], rs2), f[k]);
       }
       if (p.drop.cut) {
 #pragma unroll
         for (int k = 0; k < PP; ++k) v[j][k] = drop_pair(v[j][k], draws[j][k], key.cutw);
       }
-      uint64_t r[PP];
-      unpack_word<ELEM>(lds16(slot + (NV + j) * WB), r);
 #pragma unroll
-      for (int k = 0; k < PP; ++k) v[j][k] = add_2(v[j][k], r[k]);
+      for (int k = 0; k < PP; ++k) v[j][k] = add_2(v[j][k], r[k]);  // zeros past D
       const uint4 u = pack_word<ELEM>(v[j]);
       unpack_word<ELEM>(u, v[j]);  // normalised as it is kept
-      if (c < p.D) {
-        if (active) *reinterpret_cast<uint4*>(hp + TPR * j * 16) = u;
-      } else {
-#pragma unroll
-        for (int k = 0; k < PP; ++k) v[j][k] = 0;  // a beta there
-      }
+      if (active && (t + TPR * j) * EPC < p.D) *reinterpret_cast<uint4*>(hp + TPR * j * 16) = u;
     }
     last = slot;
     slot = slot == mine + P * SB ? mine : slot + SB;
@@ -490,20 +496,26 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR < 512 ? 2 : 1) join
     float mu;
     const float rs = stats(v, mu);
     if (active) {
-      const uint64_t rs2 = pk(rs, rs);
+      rs2 = pk(rs, rs);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int c = (t + TPR * j) * EPC;
-        if (c >= p.D) continue;
-        uint64_t b[PP];
-        params_or<EPC>(p.b2, p.param_elem, c, 0.f, b);
+        if ((t + TPR * j) * EPC >= p.D) continue;
+        uint64_t f[PP];
+        get_factors<TPR, NV, EPC>(fac, 1, j, f);
+        if constexpr (FULL) {
+          uint64_t b[PP];
+          get_factors<TPR, NV, EPC>(fac, 3, j, b);
 #pragma unroll
-        for (int k = 0; k < PP; ++k) v[j][k] = fma_2(mul_2(v[j][k], rs2), fg[j][k], b[k]);
+          for (int k = 0; k < PP; ++k) v[j][k] = fma_2(mul_2(v[j][k], rs2), f[k], b[k]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < PP; ++k) v[j][k] = mul_2(mul_2(v[j][k], rs2), f[k]);
+        }
         *reinterpret_cast<uint4*>(yp + TPR * j * 16) = pack_word<ELEM>(v[j]);
       }
       if (t == 0) {
         p.rs2[row] = rs;
-        if (p.layer) p.mu2[row] = mu;
+        if (FULL && p.layer) p.mu2[row] = mu;
       }
     }
     yp += p.ystep;
@@ -511,30 +523,31 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR < 512 ? 2 : 1) join
   cp_wait<0>();
 }
 
-template <int ELEM, int TPR, int NV>
+template <int ELEM, int TPR, int NV, bool FULL>
 struct JoinBwdShape {
-  static constexpr int THREADS = TPR < 256 ? 256 : TPR;
-  // bytes per thread and row, each kind an array over the threads: dy, h, dh, x, then rs2, mu2, rs1, mu1
-  static constexpr int W = NV * 16, S_OFF = 4 * W, BYTES = S_OFF + 16;
-  static constexpr int RING = 3 * BYTES * THREADS <= 224 * 1024 ? 3 : 2;
-  static constexpr size_t SMEM = (size_t)RING * BYTES * THREADS;
-  static_assert(SMEM <= 224 * 1024, "shared memory budget");
+  // bytes per thread and row, each kind an array over the threads: dy, h, dh, x, then rs2, rs1 and, FULL, mu2, mu1
+  static constexpr int W = NV * 16, S_OFF = 4 * W, BYTES = S_OFF + (FULL ? 16 : 8);
+  static constexpr int SLOT = BYTES * kVecThreads, FACTORS = 2 * TPR * NV * Word<ELEM>::EPC * 4;
+  static constexpr int FIT = (kVecSmem - FACTORS) / SLOT, RING = FIT < 4 ? FIT : 4;
+  static constexpr size_t SMEM = (size_t)RING * SLOT + FACTORS;
+  static_assert(RING >= 2, "shared memory budget");
 };
 
-// SUMS: with the sums of dy and dt (for the betas), or without them.
-template <int ELEM, int TPR, int NV, bool SUMS>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR < 512 ? 2 : 1) join_bwd_vec_kernel(const JoinBwdParams p) {
-  using S = JoinBwdShape<ELEM, TPR, NV>;
-  constexpr int T = S::THREADS, GPB = T / TPR, RING = S::RING, P = RING - 1;
+// FULL: with means, and with the sums of dy and dt (for the betas).
+template <int ELEM, int TPR, int NV, bool FULL>
+__global__ void __launch_bounds__(kVecThreads, 1) join_bwd_vec_kernel(const JoinBwdParams p) {
+  using S = JoinBwdShape<ELEM, TPR, NV, FULL>;
+  constexpr int T = kVecThreads, GPB = T / TPR, RING = S::RING, P = RING - 1;
   constexpr int EPC = Word<ELEM>::EPC, PP = EPC / 2, ES = ElemSize<ELEM>::value;
   __shared__ float2 xch[2 * T / 32];
-  extern __shared__ uint4 ring[];  // [RING][BYTES * T]
+  extern __shared__ uint4 ring[];  // [RING][BYTES * T], then the factors pre_gamma, scale gate post_gamma
   const int g = threadIdx.x / TPR, t = threadIdx.x % TPR;
   pdl_wait();
   pdl_launch_dependents();
-  constexpr uint32_t WB = T * 16, TB = NV * WB, SB = S::BYTES * T;  // bytes of a word of all threads, of a tensor, of a slot
+  constexpr uint32_t WB = T * 16, TB = NV * WB, SB = S::SLOT;  // bytes of a word of all threads, of a tensor, of a slot
   const uint32_t base = (uint32_t)__cvta_generic_to_shared(ring);
   const uint32_t t16 = threadIdx.x * 16, t4 = S::S_OFF * T + threadIdx.x * 4;
+  const uint32_t fac = base + RING * SB + t * 16;
   int64_t row = (int64_t)blockIdx.x * GPB + g;
   const bool has_x = p.g1 != nullptr || p.gate != nullptr;
   const uint8_t* dyp = static_cast<const uint8_t*>(p.dy) + row * p.lddy * ES + t * 16;
@@ -545,11 +558,11 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR < 512 ? 2 : 1) join
     if (r < p.M) {
       if (p.g2) {
         cp4(slot + t4, p.rs2 + r);
-        if (p.layer) cp4(slot + t4 + 4 * T, p.mu2 + r);
+        if (FULL && p.layer) cp4(slot + t4 + 8 * T, p.mu2 + r);
       }
       if (p.g1) {
-        cp4(slot + t4 + 8 * T, p.rs1 + r);
-        if (p.layer) cp4(slot + t4 + 12 * T, p.mu1 + r);
+        cp4(slot + t4 + 4 * T, p.rs1 + r);
+        if (FULL && p.layer) cp4(slot + t4 + 12 * T, p.mu1 + r);
       }
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
@@ -573,7 +586,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR < 512 ? 2 : 1) join
 #pragma unroll
   for (int k = 0; k < RING; ++k) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sts4(base + k * SB + t4 + 4 * i * T, 0u);
+    for (int i = 0; i < (FULL ? 4 : 2); ++i) sts4(base + k * SB + t4 + 4 * i * T, 0u);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const bool in = (t + TPR * j) * EPC < p.D;
@@ -585,8 +598,12 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR < 512 ? 2 : 1) join
 #pragma unroll
   for (int k = 0; k < P; ++k) issue(row + k * p.step, base + k * SB);
   const DropKey key = drop_key(p.drop);
-  constexpr int NS = SUMS ? 4 : 2;
-  uint64_t acc[NS][NV][PP];  // sums of dy hhat, dt xhat, dy, dt
+  uint4* fput = ring + RING * SB / 16;
+  if (p.g2) put_factors<TPR, NV, EPC>(fput, 0, p.g2, nullptr, p.param_elem, 1.f, 0.f, p.D);
+  put_factors<TPR, NV, EPC>(fput, 1, p.gate, p.g1, p.param_elem, p.scale, 1.f, p.D);
+  __syncthreads();
+  constexpr int NS = FULL ? 4 : 2;
+  uint64_t acc[NS][NV][PP];  // sums of dy hhat, drop(dH) xhat, dy, drop(dH)
 #pragma unroll
   for (int i = 0; i < NS; ++i)
 #pragma unroll
@@ -598,6 +615,22 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR < 512 ? 2 : 1) join
   uint32_t slot = base, last = base + P * SB;
   uint8_t* op = static_cast<uint8_t*>(p.dx) + row * p.lddx * ES + t * 16;
   uint8_t* drp = static_cast<uint8_t*>(p.dres) + row * p.lddres * ES + t * 16;
+  // -mean(q xhat) and -mean(q), times the reciprocal deviation
+  auto means = [&](uint64_t a1, uint64_t a2, float rs, uint64_t& m1, uint64_t& m2) {
+    const float2 p2 = upk(a2);
+    const float f = -inv_d * rs;
+    if constexpr (FULL) {
+      const float2 p1 = upk(a1);
+      const float2 sums = row_sum2<TPR>(p1.x + p1.y, p2.x + p2.y, xch, turn);
+      const float v = p.layer ? sums.x * f : 0.f;
+      m1 = pk(v, v);
+      m2 = pk(sums.y * f, sums.y * f);
+    } else {
+      const float v = row_sum<TPR>(p2.x + p2.y, xch, turn) * f;
+      m1 = 0;
+      m2 = pk(v, v);
+    }
+  };
   for (; row - g < p.M; row += p.step) {
     issue(row + P * p.step, last);
     cp_wait<P>();
@@ -608,89 +641,87 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR < 512 ? 2 : 1) join
 #pragma unroll
       for (int j = 0; j < NV; ++j) word_draws<EPC>(key, (t + TPR * j) * EPC, (uint32_t)row, draws[j]);
     }
+    uint64_t rs2 = 0, m1 = 0, m2 = 0;
     if (p.g2) {
-      const float rs = __uint_as_float(lds4(slot + t4)), mu = __uint_as_float(lds4(slot + t4 + 4 * T));
-      const uint64_t rs2 = pk(rs, rs), mu2 = pk(mu, mu);
+      const float rs = __uint_as_float(lds4(slot + t4)), mu = FULL ? __uint_as_float(lds4(slot + t4 + 8 * T)) : 0.f;
+      rs2 = pk(rs, rs);
+      const uint64_t mu2 = pk(mu, mu);
       uint64_t a1 = 0, a2 = 0;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int c = (t + TPR * j) * EPC;
-        const bool in = c < p.D;
-        uint64_t ga[PP];
-        load_params<EPC>(p.g2, p.param_elem, in ? c : 0, ga);
+        uint64_t f[PP];
+        get_factors<TPR, NV, EPC>(fac, 0, j, f);
         unpack_word<ELEM>(lds16(slot + t16 + j * WB), d[j]);
         unpack_word<ELEM>(lds16(slot + t16 + TB + j * WB), xh[j]);
 #pragma unroll
         for (int k = 0; k < PP; ++k) {
-          xh[j][k] = mul_2(sub_2(xh[j][k], mu2), rs2);
+          if constexpr (FULL) xh[j][k] = sub_2(xh[j][k], mu2);
+          xh[j][k] = mul_2(xh[j][k], rs2);
           if (active) {
             acc[0][j][k] = fma_2(d[j][k], xh[j][k], acc[0][j][k]);
-            if constexpr (SUMS) acc[2][j][k] = add_2(acc[2][j][k], d[j][k]);
+            if constexpr (FULL) acc[2][j][k] = add_2(acc[2][j][k], d[j][k]);
           }
-          d[j][k] = mul_2(d[j][k], ga[k]);  // zero past D
-          a1 = add_2(a1, d[j][k]);
+          d[j][k] = mul_2(d[j][k], f[k]);  // zero past D
+          if constexpr (FULL) a1 = add_2(a1, d[j][k]);
           a2 = fma_2(d[j][k], xh[j][k], a2);
         }
       }
-      const float2 p1 = upk(a1), p2 = upk(a2);
-      const float2 sums = row_sum2<TPR>(p1.x + p1.y, p2.x + p2.y, xch, turn);
-      const float mg = p.layer ? sums.x * inv_d : 0.f, nmx = -sums.y * inv_d;
-      const uint64_t mg2 = pk(mg, mg), nmx2 = pk(nmx, nmx);
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int k = 0; k < PP; ++k) d[j][k] = mul_2(fma_2(nmx2, xh[j][k], sub_2(d[j][k], mg2)), rs2);
+      means(a1, a2, rs, m1, m2);
     } else {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int k = 0; k < PP; ++k) d[j][k] = 0;
+        for (int k = 0; k < PP; ++k) d[j][k] = xh[j][k] = 0;
     }
-    const float rs = __uint_as_float(lds4(slot + t4 + 8 * T)), mu = __uint_as_float(lds4(slot + t4 + 12 * T));
-    const uint64_t rs2 = pk(rs, rs), mu2 = pk(mu, mu);
+    const float rs = __uint_as_float(lds4(slot + t4 + 4 * T)), mu = FULL ? __uint_as_float(lds4(slot + t4 + 12 * T)) : 0.f;
+    const uint64_t rs1 = p.g1 ? pk(rs, rs) : pk(1.f, 1.f), mu1 = pk(mu, mu);
     uint64_t a1 = 0, a2 = 0;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (t + TPR * j) * EPC;
-      const bool in = c < p.D;
+      const bool in = (t + TPR * j) * EPC < p.D;
       uint64_t r[PP];
       unpack_word<ELEM>(lds16(slot + t16 + 2 * TB + j * WB), r);
 #pragma unroll
-      for (int k = 0; k < PP; ++k) d[j][k] = add_2(d[j][k], r[k]);
-      if (p.dres && active && in) *reinterpret_cast<uint4*>(drp + TPR * j * 16) = pack_word<ELEM>(d[j]);
-#pragma unroll
-      for (int k = 0; k < PP; ++k) {
-        d[j][k] = mul_2(d[j][k], pk(p.scale, p.scale));
-        if (p.drop.cut) d[j][k] = drop_pair(d[j][k], draws[j][k], key.cutw);
-        if (!in) d[j][k] = 0;  // the norm's mean there
+      for (int k = 0; k < PP; ++k) {  // dH
+        if constexpr (FULL) r[k] = add_2(r[k], m1);
+        d[j][k] = fma_2(xh[j][k], m2, fma_2(d[j][k], rs2, r[k]));
       }
+      if (p.dres && active && in) *reinterpret_cast<uint4*>(drp + TPR * j * 16) = pack_word<ELEM>(d[j]);
+      if (p.drop.cut) {
+#pragma unroll
+        for (int k = 0; k < PP; ++k) d[j][k] = drop_pair(d[j][k], draws[j][k], key.cutw);
+      }
+      uint64_t f[PP];
+      get_factors<TPR, NV, EPC>(fac, 1, j, f);  // zeros past D
       if (has_x) {
-        uint64_t f[PP], q[PP];
-        params_or<EPC>(p.gate, p.param_elem, in ? c : 0, 1.f, f);
-        params_or<EPC>(p.g1, p.param_elem, in ? c : 0, 1.f, q);
         unpack_word<ELEM>(lds16(slot + t16 + 3 * TB + j * WB), xh[j]);
 #pragma unroll
         for (int k = 0; k < PP; ++k) {
-          if (p.g1) xh[j][k] = mul_2(sub_2(xh[j][k], mu2), rs2);
+          if constexpr (FULL) xh[j][k] = sub_2(xh[j][k], mu1);
+          xh[j][k] = mul_2(xh[j][k], rs1);
           if (active) {
             acc[1][j][k] = fma_2(d[j][k], xh[j][k], acc[1][j][k]);
-            if constexpr (SUMS) acc[3][j][k] = add_2(acc[3][j][k], d[j][k]);
+            if constexpr (FULL) acc[3][j][k] = add_2(acc[3][j][k], d[j][k]);
           }
-          d[j][k] = mul_2(d[j][k], mul_2(f[k], q[k]));
-          a1 = add_2(a1, d[j][k]);
-          a2 = fma_2(d[j][k], xh[j][k], a2);
         }
+      }
+#pragma unroll
+      for (int k = 0; k < PP; ++k) {
+        d[j][k] = mul_2(d[j][k], f[k]);
+        if constexpr (FULL) a1 = add_2(a1, d[j][k]);
+        a2 = fma_2(d[j][k], xh[j][k], a2);
       }
     }
     if (p.g1) {
-      const float2 p1 = upk(a1), p2 = upk(a2);
-      const float2 sums = row_sum2<TPR>(p1.x + p1.y, p2.x + p2.y, xch, turn);
-      const float mg = p.layer ? sums.x * inv_d : 0.f, nmx = -sums.y * inv_d;
-      const uint64_t mg2 = pk(mg, mg), nmx2 = pk(nmx, nmx);
+      means(a1, a2, rs, m1, m2);
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int k = 0; k < PP; ++k) d[j][k] = mul_2(fma_2(nmx2, xh[j][k], sub_2(d[j][k], mg2)), rs2);
+        for (int k = 0; k < PP; ++k) {
+          uint64_t o = mul_2(xh[j][k], m2);
+          if constexpr (FULL) o = add_2(o, m1);
+          d[j][k] = fma_2(d[j][k], rs1, o);
+        }
     }
     if (active) {
 #pragma unroll
@@ -757,6 +788,7 @@ struct JoinSumParams {
   float* dg2;
   float* db2;
   int n, D, param_elem, sums;
+  float scale;  // of the last two sums
 };
 __global__ void __launch_bounds__(1024) join_sum_kernel(const JoinSumParams p) {
   __shared__ float red[32][33];
@@ -785,6 +817,8 @@ __global__ void __launch_bounds__(1024) join_sum_kernel(const JoinSumParams p) {
   if (p.dg2) p.dg2[cw] = s[0];
   if (p.db2) p.db2[cw] = s[1];
   const float f = param_or(p.gate, p.param_elem, cw, 1.f);
+  s[2] *= p.scale;
+  s[3] *= p.scale;
   if (p.dg1) p.dg1[cw] = f * s[2];
   if (p.db1) p.db1[cw] = f * s[3];
   if (p.dgate) p.dgate[cw] = p.g1 ? fmaf(load_elem_rt(p.g1, p.param_elem, cw), s[2], p.b1 ? load_elem_rt(p.b1, p.param_elem, cw) * s[3] : 0.f) : s[2];
@@ -835,56 +869,53 @@ lnfp8_status bwd_any(const JoinBwdParams& p, int* blocks_out, cudaStream_t st) {
 }
 
 bool row_aligned(const void* p, int64_t ld, int es) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * es % 16 == 0; }
-bool vectors_aligned(std::initializer_list<const void*> v) {
-  for (const void* p : v)
-    if (reinterpret_cast<uintptr_t>(p) % 16) return false;
-  return true;
-}
-
-template <int ELEM, int TPR, int NV>
+template <int ELEM, int TPR, int NV, bool FULL>
 lnfp8_status fwd_vec_launch(const JoinFwdParams& p, cudaStream_t st) {
-  using S = JoinFwdShape<ELEM, TPR, NV>;
-  constexpr auto kernel = join_fwd_vec_kernel<ELEM, TPR, NV>;
-  int bps = 1;
-  const lnfp8_status s = kernel_setup<kernel>(S::THREADS, S::SMEM, &bps, "block_join_fwd: kernel set-up");
+  using S = JoinFwdShape<ELEM, TPR, NV, FULL>;
+  constexpr auto kernel = join_fwd_vec_kernel<ELEM, TPR, NV, FULL>;
+  const lnfp8_status s = kernel_setup<kernel>(kVecThreads, S::SMEM, nullptr, "block_join_fwd: kernel set-up");
   if (s != LNFP8_OK) return s;
-  constexpr int gpb = S::THREADS / TPR, es = ElemSize<ELEM>::value;
-  const int64_t blocks = min64((p.M + gpb - 1) / gpb, (int64_t)num_sms() * bps);
+  constexpr int gpb = kVecThreads / TPR, es = ElemSize<ELEM>::value;
+  const int64_t blocks = min64((p.M + gpb - 1) / gpb, num_sms());
   JoinFwdParams q = p;
   q.step = blocks * gpb;
   q.xstep = q.step * p.ldx * es;
   q.rstep = q.step * p.ldr * es;
   q.hstep = q.step * p.ldh * es;
   q.ystep = q.step * p.ldy * es;
-  if (launch_pdl(kernel, dim3((unsigned)blocks), dim3(S::THREADS), S::SMEM, st, q) != cudaSuccess) return check_launch("block_join_fwd launch");
+  if (launch_pdl(kernel, dim3((unsigned)blocks), dim3(kVecThreads), S::SMEM, st, q) != cudaSuccess) return check_launch("block_join_fwd launch");
   return check_launch("block_join_fwd");
+}
+template <int ELEM, bool FULL>
+lnfp8_status fwd_vec(const JoinFwdParams& p, cudaStream_t st) {
+  constexpr int NV = 16 / Word<ELEM>::EPC;
+  if (p.D <= 128) return fwd_vec_launch<ELEM, 8, NV, FULL>(p, st);
+  if (p.D <= 256) return fwd_vec_launch<ELEM, 16, NV, FULL>(p, st);
+  if (p.D <= 512) return fwd_vec_launch<ELEM, 32, NV, FULL>(p, st);
+  if (p.D <= 1024) return fwd_vec_launch<ELEM, 64, NV, FULL>(p, st);
+  if (p.D <= 2048) return fwd_vec_launch<ELEM, 128, NV, FULL>(p, st);
+  if constexpr (ELEM == LNFP8_FP32) return p.D <= 4096 ? fwd_vec_launch<ELEM, 256, NV, FULL>(p, st) : fwd_any<ELEM>(p, st);
+  else return p.D <= 4096 ? fwd_vec_launch<ELEM, 256, NV, FULL>(p, st) : fwd_vec_launch<ELEM, 512, NV, FULL>(p, st);
 }
 template <int ELEM>
 lnfp8_status fwd(const JoinFwdParams& p, cudaStream_t st) {
-  constexpr int es = ElemSize<ELEM>::value, NV = 16 / Word<ELEM>::EPC;
+  constexpr int es = ElemSize<ELEM>::value;
   const bool vec = p.D % 8 == 0 && p.D <= 8192 && row_aligned(p.x, p.ldx, es) && row_aligned(p.h, p.ldh, es) &&
-                   (!p.resid || row_aligned(p.resid, p.ldr, es)) && (!p.g2 || row_aligned(p.y, p.ldy, es)) &&
-                   vectors_aligned({p.g1, p.b1, p.gate, p.g2, p.b2});
+                   (!p.resid || row_aligned(p.resid, p.ldr, es)) && (!p.g2 || row_aligned(p.y, p.ldy, es));
   if (!vec) return fwd_any<ELEM>(p, st);
-  if (p.D <= 128) return fwd_vec_launch<ELEM, 8, NV>(p, st);
-  if (p.D <= 256) return fwd_vec_launch<ELEM, 16, NV>(p, st);
-  if (p.D <= 512) return fwd_vec_launch<ELEM, 32, NV>(p, st);
-  if (p.D <= 1024) return fwd_vec_launch<ELEM, 64, NV>(p, st);
-  if (p.D <= 2048) return fwd_vec_launch<ELEM, 128, NV>(p, st);
-  if (p.D <= 4096) return fwd_vec_launch<ELEM, 256, NV>(p, st);
-  return fwd_vec_launch<ELEM, 512, NV>(p, st);
+  const bool full = (p.layer && (p.g1 || p.g2)) || p.b1 || p.b2;
+  return full ? fwd_vec<ELEM, true>(p, st) : fwd_vec<ELEM, false>(p, st);
 }
 
-template <int ELEM, int TPR, int NV, bool SUMS>
+template <int ELEM, int TPR, int NV, bool FULL>
 lnfp8_status bwd_vec_launch(const JoinBwdParams& p, int* blocks_out, cudaStream_t st) {
-  using S = JoinBwdShape<ELEM, TPR, NV>;
+  using S = JoinBwdShape<ELEM, TPR, NV, FULL>;
   static_assert(S::SMEM >= TPR * NV * Word<ELEM>::EPC * sizeof(float), "the column partials reuse the ring");
-  constexpr auto kernel = join_bwd_vec_kernel<ELEM, TPR, NV, SUMS>;
-  int bps = 1;
-  const lnfp8_status s = kernel_setup<kernel>(S::THREADS, S::SMEM, &bps, "block_join_bwd: kernel set-up");
+  constexpr auto kernel = join_bwd_vec_kernel<ELEM, TPR, NV, FULL>;
+  const lnfp8_status s = kernel_setup<kernel>(kVecThreads, S::SMEM, nullptr, "block_join_bwd: kernel set-up");
   if (s != LNFP8_OK) return s;
-  constexpr int gpb = S::THREADS / TPR, es = ElemSize<ELEM>::value;
-  const int64_t blocks = min64((p.M + gpb - 1) / gpb, (int64_t)num_sms() * std::min(kBwdBlocksPerSm, bps));
+  constexpr int gpb = kVecThreads / TPR, es = ElemSize<ELEM>::value;
+  const int64_t blocks = min64((p.M + gpb - 1) / gpb, num_sms());
   *blocks_out = (int)blocks;
   JoinBwdParams q = p;
   q.step = blocks * gpb;
@@ -894,29 +925,33 @@ lnfp8_status bwd_vec_launch(const JoinBwdParams& p, int* blocks_out, cudaStream_
   q.hstep = q.step * p.ldh * es;
   q.dxstep = q.step * p.lddx * es;
   q.drstep = q.step * p.lddres * es;
-  if (launch_pdl(kernel, dim3((unsigned)blocks), dim3(S::THREADS), S::SMEM, st, q) != cudaSuccess) return check_launch("block_join_bwd launch");
+  if (launch_pdl(kernel, dim3((unsigned)blocks), dim3(kVecThreads), S::SMEM, st, q) != cudaSuccess) return check_launch("block_join_bwd launch");
   return check_launch("block_join_bwd");
 }
-template <int ELEM, int NV, bool SUMS>
+template <int ELEM, int NV, bool FULL>
 lnfp8_status bwd_vec(const JoinBwdParams& p, int* blocks_out, cudaStream_t st) {
   constexpr int W = NV * Word<ELEM>::EPC;  // columns a thread
-  if (p.D <= 8 * W) return bwd_vec_launch<ELEM, 8, NV, SUMS>(p, blocks_out, st);
-  if (p.D <= 16 * W) return bwd_vec_launch<ELEM, 16, NV, SUMS>(p, blocks_out, st);
-  if (p.D <= 32 * W) return bwd_vec_launch<ELEM, 32, NV, SUMS>(p, blocks_out, st);
-  if (p.D <= 64 * W) return bwd_vec_launch<ELEM, 64, NV, SUMS>(p, blocks_out, st);
-  if (p.D <= 128 * W) return bwd_vec_launch<ELEM, 128, NV, SUMS>(p, blocks_out, st);
-  if (p.D <= 256 * W) return bwd_vec_launch<ELEM, 256, NV, SUMS>(p, blocks_out, st);
-  return bwd_vec_launch<ELEM, 512, NV, SUMS>(p, blocks_out, st);
+  if (p.D <= 8 * W) return bwd_vec_launch<ELEM, 8, NV, FULL>(p, blocks_out, st);
+  if (p.D <= 16 * W) return bwd_vec_launch<ELEM, 16, NV, FULL>(p, blocks_out, st);
+  if (p.D <= 32 * W) return bwd_vec_launch<ELEM, 32, NV, FULL>(p, blocks_out, st);
+  if (p.D <= 64 * W) return bwd_vec_launch<ELEM, 64, NV, FULL>(p, blocks_out, st);
+  if (p.D <= 128 * W) return bwd_vec_launch<ELEM, 128, NV, FULL>(p, blocks_out, st);
+  if (p.D <= 256 * W) return bwd_vec_launch<ELEM, 256, NV, FULL>(p, blocks_out, st);
+  return bwd_vec_launch<ELEM, 512, NV, FULL>(p, blocks_out, st);
 }
+// With means and betas' sums 8 columns a thread, or 16 where a row would not fit 512 threads.
 template <int ELEM>
 lnfp8_status bwd(const JoinBwdParams& p, int* blocks_out, cudaStream_t st) {
-  constexpr int es = ElemSize<ELEM>::value, NV = 2;
-  const bool vec = p.D % 8 == 0 && p.D <= 512 * NV * Word<ELEM>::EPC && row_aligned(p.dx, p.lddx, es) &&
+  constexpr int es = ElemSize<ELEM>::value;
+  const bool vec = p.D % 8 == 0 && p.D <= 1024 * Word<ELEM>::EPC && row_aligned(p.dx, p.lddx, es) &&
                    (!p.dres || row_aligned(p.dres, p.lddres, es)) && (!p.dh || row_aligned(p.dh, p.lddh, es)) &&
                    (!p.g2 || (row_aligned(p.dy, p.lddy, es) && row_aligned(p.h, p.ldh, es))) &&
-                   (!(p.g1 || p.gate) || row_aligned(p.x, p.ldx, es)) && vectors_aligned({p.g1, p.gate, p.g2});
+                   (!(p.g1 || p.gate) || row_aligned(p.x, p.ldx, es));
   if (!vec) return bwd_any<ELEM>(p, blocks_out, st);
-  return p.sums & 10 ? bwd_vec<ELEM, NV, true>(p, blocks_out, st) : bwd_vec<ELEM, NV, false>(p, blocks_out, st);
+  const bool full = (p.layer && (p.g1 || p.g2)) || (p.sums & 10);
+  if (!full) return bwd_vec<ELEM, 2, false>(p, blocks_out, st);
+  if constexpr (ELEM == LNFP8_FP32) return bwd_vec<ELEM, 2, true>(p, blocks_out, st);
+  else return p.D <= 512 * 8 ? bwd_vec<ELEM, 1, true>(p, blocks_out, st) : bwd_vec_launch<ELEM, 512, 2, true>(p, blocks_out, st);
 }
 
 }  // namespace
@@ -1016,6 +1051,7 @@ lnfp8_status block_join_bwd_launch(const lnfp8_block_join_bwd_args* a, cudaStrea
   q.D = p.D;
   q.param_elem = p.param_elem;
   q.sums = p.sums;
+  q.scale = p.scale;
   LaunchScope ls("block_join_sum", st);
   if (launch_pdl(join_sum_kernel, dim3((unsigned)((p.D + 31) / 32)), dim3(1024), 0, st, q) != cudaSuccess)
     return check_launch("block_join_bwd launch");
