@@ -90,6 +90,24 @@ __device__ __forceinline__ void epilogue8(const EpiParams& p, float* v, int m, i
   }
 }
 
+// The gated epilogue of 8 outputs n.. of row m, all inside the tensor: vg the gate's sums, vu the up projection's.
+__device__ __forceinline__ void epilogue8_glu(const EpiParams& p, float* vg, float* vu, int m, int n) {
+  const int64_t row = m;
+  if (p.bias) {
+    const uint16_t* b = reinterpret_cast<const uint16_t*>(p.bias) + n;
+    add16x8(vg, *reinterpret_cast<const uint4*>(b), p.f16);
+    add16x8(vu, *reinterpret_cast<const uint4*>(b + p.N), p.f16);
+  }
+  if (p.h) {
+    uint16_t* h = reinterpret_cast<uint16_t*>(p.h) + row * 2 * p.N + n;
+    *reinterpret_cast<uint4*>(h) = pack16x8(vg, p.f16);
+    *reinterpret_cast<uint4*>(h + p.N) = pack16x8(vu, p.f16);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) vg[i] = act_fwd(vg[i], p.act) * vu[i];
+  *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + row * p.ldo + n) = pack16x8(vg, p.f16);
+}
+
 // ------------------------------------------------------------ one tile per cluster
 // A cluster computes one tile, its K cut into S pieces on S SMs (PAIR: S CTA pairs). The pieces'
 // fp32 sums are then read from one another's shared memory and added in the pieces' order, each CTA
@@ -100,6 +118,8 @@ __device__ __forceinline__ void epilogue8(const EpiParams& p, float* v, int m, i
 //           where K is long and the tiles are few: 256 x 4096 x 4096 13.9 us, 14.8 on persistent pairs.
 //   SWAP    (up to 64 tokens) the accumulator's lanes are output features and its BN columns tokens, so that few
 //           tokens fill the instruction; else lanes are tokens. 8 x 4096 x 4096 9.4 us, 3.6 TB/s.
+//   GLU     64 of the tile's 128 features are gate rows of w and 64 the up rows of the same outputs (SWAP: in the halves of
+//           the lanes; PAIR, BN = 128: the two CTAs' halves), so that the fp32 tile holds both factors of 64 outputs.
 template <int BN, bool PAIR>
 struct TileCfg {
   static constexpr int P_BYTES = 128 * BK * 2;
@@ -118,12 +138,12 @@ struct TileParams {
   uint32_t idesc;
 };
 struct TileMaps {
-  CUtensorMap p, q;
+  CUtensorMap p, q, u;  // u: the up rows (GLU)
 };
 
 constexpr int kTileThreads = 256;
 
-template <int BN, bool PAIR, bool SWAP>
+template <int BN, bool PAIR, bool SWAP, bool GLU>
 __global__ void __launch_bounds__(kTileThreads, 1)
 lin_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ TileParams p) {
   using C = TileCfg<BN, PAIR>;
@@ -151,6 +171,7 @@ lin_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ T
     mbar_init_fence();
     tma_prefetch_map(&maps.p);
     tma_prefetch_map(&maps.q);
+    if constexpr (GLU) tma_prefetch_map(&maps.u);
   }
   if constexpr (PAIR) cluster_sync_all();  // the peer signals this CTA's barriers
   if (warp == 1) tmem_alloc<PAIR>(smem_u32((const void*)(misc + 1)), C::TMEM_COLS);
@@ -163,9 +184,10 @@ lin_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ T
 
   const int crank = blockIdx.x % (S * SIDES);  // in the cluster
   const int side = PAIR ? crank & 1 : 0, piece = crank / SIDES, leader = crank - side;
-  const CUtensorMap *tmP = &maps.p, *tmQ = &maps.q;
+  const CUtensorMap *tmP = &maps.p, *tmQ = GLU && PAIR && side ? &maps.u : &maps.q;
   const int tile = blockIdx.x / (S * SIDES);
-  const int p0 = (tile % p.num_p) * (128 * SIDES) + side * 128, q0 = (tile / p.num_p) * BN;
+  const int p0 = GLU && SWAP ? (tile % p.num_p) * 64 : (tile % p.num_p) * (128 * SIDES) + side * 128;
+  const int q0 = (tile / p.num_p) * (GLU && PAIR ? BN / 2 : BN);
   const int kb0 = piece * p.kb_per_split, kb1 = min(p.num_kb, kb0 + p.kb_per_split);
   const bool p_mn = p.p_mn != 0;
   const uint16_t both = (uint16_t)(3u << leader);
@@ -180,7 +202,7 @@ lin_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ T
       if constexpr (PAIR) tma_load_pair(dst, tm, x, y, bar);
       else tma_load(dst, tm, x, y, bar);
     };
-    const int qs = q0 + side * (BN / 2);  // the rows of Q this CTA loads
+    const int qs = GLU ? q0 : q0 + side * (BN / 2);  // the rows of Q this CTA loads
     const uint32_t fb0 = PAIR ? map_to_rank(full_bar(0), leader) : full_bar(0);
     for (int kb = kb0; kb < kb1; ++kb) {
       if (!mbar_wait_warp(empty_bar(stage), phase ^ 1, abort_flag)) { ok = false; break; }
@@ -188,7 +210,10 @@ lin_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ T
         const uint32_t pd = ring + stage * C::STAGE, qd = pd + C::P_BYTES;
         const uint32_t fb = fb0 + 8u * stage;
         if (side == 0) mbar_expect_tx(full_bar(stage), SIDES * C::STAGE);
-        if (!p_mn) load(pd, tmP, kb * BK, p0, fb);
+        if constexpr (GLU && SWAP) {
+          load(pd, tmP, kb * BK, p0, fb);
+          load(pd + 8192, &maps.u, kb * BK, p0, fb);
+        } else if (!p_mn) load(pd, tmP, kb * BK, p0, fb);
         else {
           load(pd, tmP, p0, kb * BK, fb);
           load(pd + 8192, tmP, p0 + 64, kb * BK, fb);
@@ -268,6 +293,42 @@ lin_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ T
   const int rows = ROWS / S;  // of this CTA; a multiple of 32 items in all
   constexpr int CH = COLS / 8;
   constexpr int kMostPieces = PAIR ? 2 : 4, U = PAIR ? 2 : 1;  // U items of a thread together
+  if constexpr (GLU) {
+    constexpr int H = COLS / 2, GCH = H / 8;
+    for (int i = threadIdx.x; i < rows * GCH; i += kTileThreads) {
+      const int r = piece * rows + i / GCH, c = (i % GCH) * 8;
+      const int m = (SWAP ? q0 : p0) + r, n = (SWAP ? p0 : q0) + c;
+      if (m >= p.e.M || n >= p.e.N) continue;
+      float4 w[kMostPieces][4];  // every piece's words first, as below: each goes into a store to y
+      if (S > 1) {
+        const uint32_t at = ring + (uint32_t)(r * PITCH + c) * 4u;
+#pragma unroll
+        for (int s = 0; s < kMostPieces; ++s) {
+          if (s >= S) break;
+          const uint32_t ra = map_to_rank(at, s * SIDES + side);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[s][k] = ld_cluster_f4(ra + (k >> 1) * (H * 4) + (k & 1) * 16);
+        }
+      } else {
+        const float4* at = reinterpret_cast<const float4*>(tile_f + r * PITCH + c);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[0][k] = at[(k >> 1) * (H / 4) + (k & 1)];
+      }
+      float v[2][8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float4 t = w[0][k];
+#pragma unroll
+        for (int s = 1; s < kMostPieces; ++s) {
+          if (s >= S) break;
+          t.x += w[s][k].x; t.y += w[s][k].y; t.z += w[s][k].z; t.w += w[s][k].w;
+        }
+        float* d = v[k >> 1] + (k & 1) * 4;
+        d[0] = t.x; d[1] = t.y; d[2] = t.z; d[3] = t.w;
+      }
+      epilogue8_glu(p.e, v[0], v[1], m, n);
+    }
+  } else
   for (int i0 = threadIdx.x; i0 < rows * CH; i0 += U * kTileThreads) {
     // every piece's words first: loads from another SM's shared memory take most of a microsecond. Items outside the
     // tensor load nothing: each value read from another CTA goes into a store to y, so that the thread has waited
@@ -329,7 +390,8 @@ constexpr int kRowsPerWarp = 2;
 constexpr int kFewTokens = 4, kFewOutputs = 10240;
 constexpr int kFewMaxX = 96 * 1024;  // bytes of x in shared memory
 
-template <int MT, bool F16>
+// GLU: the two rows of a warp are the gate's and the up projection's of one output.
+template <int MT, bool F16, bool GLU>
 __global__ void __launch_bounds__(256) lin_few_kernel(const EpiParams e, const void* __restrict__ x, int64_t ldx,
                                                       const void* __restrict__ w, int K, int WK) {
   constexpr int ELEM = F16 ? LNFP8_FP16 : LNFP8_BF16;
@@ -339,7 +401,7 @@ __global__ void __launch_bounds__(256) lin_few_kernel(const EpiParams e, const v
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = warp / WK, part = warp % WK;
-  const int n0 = (blockIdx.x * (8 / WK) + group) * kRowsPerWarp;
+  const int n0 = (blockIdx.x * (8 / WK) + group) * (GLU ? 1 : kRowsPerWarp);
   const int K8 = K >> 3;
   const int per = ((K8 + WK - 1) / WK + 31) / 32 * 32;  // 16-byte groups of a piece, whole warps of them
   const int k0 = part * per, k1 = min(K8, k0 + per);
@@ -347,7 +409,8 @@ __global__ void __launch_bounds__(256) lin_few_kernel(const EpiParams e, const v
   uint4 wv[kRowsPerWarp][U];
   const uint4* wr[kRowsPerWarp];
 #pragma unroll
-  for (int r = 0; r < kRowsPerWarp; ++r) wr[r] = reinterpret_cast<const uint4*>(w) + (int64_t)min(n0 + r, e.N - 1) * K8;
+  for (int r = 0; r < kRowsPerWarp; ++r)
+    wr[r] = reinterpret_cast<const uint4*>(w) + (GLU ? min(n0, e.N - 1) + (int64_t)r * e.N : (int64_t)min(n0 + r, e.N - 1)) * K8;
   auto fetch = [&](int k) {
 #pragma unroll
     for (int r = 0; r < kRowsPerWarp; ++r)
@@ -401,6 +464,25 @@ __global__ void __launch_bounds__(256) lin_few_kernel(const EpiParams e, const v
   __syncthreads();
   // one thread per (row group, row, token)
   const int i = threadIdx.x;
+  if constexpr (GLU) {
+    const int m = i % MT, g = i / MT, n = blockIdx.x * (8 / WK) + g;
+    if (g >= 8 / WK || m >= e.M || n >= e.N) return;
+    float zg = 0.f, zu = 0.f;
+    for (int q = 0; q < WK; ++q) {
+      zg += red[g * WK + q][0][m];
+      zu += red[g * WK + q][1][m];
+    }
+    if (e.bias) {
+      zg += load_elem<ELEM>(e.bias, n);
+      zu += load_elem<ELEM>(e.bias, (int64_t)e.N + n);
+    }
+    if (e.h) {
+      store_elem<ELEM>(e.h, (int64_t)m * 2 * e.N + n, zg);
+      store_elem<ELEM>(e.h, ((int64_t)m * 2 + 1) * e.N + n, zu);
+    }
+    store_elem<ELEM>(e.out, m * e.ldo + n, act_fwd(zg, e.act) * zu);
+    return;
+  }
   if (i >= (8 / WK) * kRowsPerWarp * MT) return;
   const int m = i % MT, r = i / MT % kRowsPerWarp, g = i / (MT * kRowsPerWarp);
   const int n = (blockIdx.x * (8 / WK) + g) * kRowsPerWarp + r;
@@ -665,17 +747,19 @@ EpiParams epi_params(const LinGemm& g) {
 }
 
 // S pieces of K per tile (1, 2 or 4; PAIR: 2). The lanes' operand (SWAP: b) may be MN-major, the other is K-major.
-template <int BN, bool PAIR, bool SWAP>
+template <int BN, bool PAIR, bool SWAP, bool GLU = false>
 lnfp8_status tile_launch(const LinGemm& q, int S, cudaStream_t st) {
   using C = TileCfg<BN, PAIR>;
-  constexpr auto k = lin_tile_kernel<BN, PAIR, SWAP>;
+  static_assert(!GLU || SWAP || (PAIR && BN == 128), "the gated tile is 64 gate and 64 up features");
+  constexpr auto k = lin_tile_kernel<BN, PAIR, SWAP, GLU>;
   const lnfp8_status set = kernel_setup<k>(kTileThreads, C::SMEM, nullptr, "linear: kernel set-up");
   if (set != LNFP8_OK) return set;
   TileParams p = {};
   TileMaps maps;
   const int64_t prow = SWAP ? q.N : q.M, qrow = SWAP ? q.M : q.N;
   const bool p_mn = SWAP ? q.b_mn : q.a_mn;
-  const int64_t num_p = (prow + (PAIR ? 255 : 127)) / (PAIR ? 256 : 128), num_q = (qrow + BN - 1) / BN, tiles = num_p * num_q;
+  constexpr int PT = GLU && SWAP ? 64 : PAIR ? 256 : 128, QT = GLU && !SWAP ? BN / 2 : BN;  // a tile's rows and columns
+  const int64_t num_p = (prow + PT - 1) / PT, num_q = (qrow + QT - 1) / QT, tiles = num_p * num_q;
   if (tiles > 0x0FFFFFFF) return set_error(LNFP8_ERR_UNSUPPORTED_SHAPE, "linear: too many tiles");
   p.e = epi_params(q);
   p.num_p = (int)num_p;
@@ -684,8 +768,10 @@ lnfp8_status tile_launch(const LinGemm& q, int S, cudaStream_t st) {
   p.splits = S;
   p.p_mn = p_mn;
   p.idesc = make_idesc(q.elem, PAIR ? 256 : 128, BN, p_mn, false);
-  const bool ok = SWAP ? operand_map(&maps.p, q.b, p_mn, q.N, q.K, q.ldb, 128) && operand_map(&maps.q, q.a, false, q.M, q.K, q.lda, PAIR ? BN / 2 : BN)
-                       : operand_map(&maps.p, q.a, p_mn, q.M, q.K, q.lda, 128) && operand_map(&maps.q, q.b, false, q.N, q.K, q.ldb, PAIR ? BN / 2 : BN);
+  bool ok = SWAP ? operand_map(&maps.p, q.b, p_mn, q.N, q.K, q.ldb, GLU ? 64 : 128) && operand_map(&maps.q, q.a, false, q.M, q.K, q.lda, PAIR ? BN / 2 : BN)
+                 : operand_map(&maps.p, q.a, p_mn, q.M, q.K, q.lda, 128) && operand_map(&maps.q, q.b, false, q.N, q.K, q.ldb, PAIR ? BN / 2 : BN);
+  if constexpr (GLU) ok = ok && operand_map(&maps.u, static_cast<const uint16_t*>(q.b) + q.N * q.ldb, false, q.N, q.K, q.ldb, 64);
+  else maps.u = maps.q;
   if (!ok) return set_error(LNFP8_ERR_CUDA, "linear: cuTensorMapEncodeTiled failed (driver entry point or arguments)");
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
@@ -832,29 +918,30 @@ int wgrad_pieces(int64_t M, int64_t K, int64_t N) {
 // and 6.6, 4096 x 4096 7.8 and 9.0, 4096 x 14336 21.4 and 21.4; two 4096 x 4096 8.4 and 9.1, 4096 x 6144 13.8 and 12.2;
 // four 4096 x 1024 5.3 and 6.7, 4096 x 2048 7.4 and 7.2, 4096 x 4096 10.2 and 9.2, 4096 x 14336 26.6 and 21.5.
 bool takes_few(const LinGemm& g) {
-  return g.M <= kFewTokens && (g.M == 1 || g.M * g.N <= kFewOutputs) && !g.a_mn && !g.b_mn && !g.ckpt.codes &&
+  return g.M <= kFewTokens && (g.M == 1 || g.M * g.N * (g.glu ? 2 : 1) <= kFewOutputs) && !g.a_mn && !g.b_mn && !g.ckpt.codes &&
          g.K * (g.M > 2 ? 4 : g.M) * 2 <= kFewMaxX;
 }
-template <int MT, bool F16>
+template <int MT, bool F16, bool GLU>
 lnfp8_status few_launch(const LinGemm& g, cudaStream_t st) {
-  constexpr auto k = lin_few_kernel<MT, F16>;
+  constexpr auto k = lin_few_kernel<MT, F16, GLU>;
   const lnfp8_status set = kernel_setup<k>(256, kFewMaxX, nullptr, "linear: kernel set-up");
   if (set != LNFP8_OK) return set;
   // warps per row group: until there are 8 warps for each SM, while each keeps 512 columns. One token, us with 1, 2, 4 and 8:
   // 1024 x 4096 3.2, 4.4, 6.7, 10.6; 4096 x 4096 7.8, 9.3, 10.9, 14.8; 8192 x 2048 9.2, 7.7, 9.1, 10.8;
   // 4096 x 1024 4.8, 3.7, 3.4, 4.7 (K x N; the rule takes 1, 1, 2, 4; until 16 warps it took one step more)
+  constexpr int per_warp = GLU ? 1 : kRowsPerWarp;
   int WK = 1;
-  while (WK < 8 && (g.N + kRowsPerWarp - 1) / kRowsPerWarp * WK < (int64_t)num_sms() * 8 && g.K >= 1024 * WK) WK *= 2;
-  const int64_t per_block = 8 / WK * kRowsPerWarp;
+  while (WK < 8 && (g.N + per_warp - 1) / per_warp * WK < (int64_t)num_sms() * 8 && g.K >= 1024 * WK) WK *= 2;
+  const int64_t per_block = 8 / WK * per_warp;
   LaunchScope ls("linear_few", st);
   if (launch_pdl(k, dim3((unsigned)((g.N + per_block - 1) / per_block)), dim3(256), (size_t)(MT * g.K * 2), st, epi_params(g), g.a, g.lda, g.b,
                  (int)g.K, WK) != cudaSuccess)
     return check_launch("linear launch");
   return check_launch("linear");
 }
-template <bool F16>
+template <bool F16, bool GLU>
 lnfp8_status few_by_tokens(const LinGemm& g, cudaStream_t st) {
-  return g.M == 1 ? few_launch<1, F16>(g, st) : g.M == 2 ? few_launch<2, F16>(g, st) : few_launch<4, F16>(g, st);
+  return g.M == 1 ? few_launch<1, F16, GLU>(g, st) : g.M == 2 ? few_launch<2, F16, GLU>(g, st) : few_launch<4, F16, GLU>(g, st);
 }
 
 // Few tokens: K pieces while they run on SMs that would idle and each keeps a few K blocks. 8 tokens, us with 1, 2 and 4
@@ -862,28 +949,34 @@ lnfp8_status few_by_tokens(const LinGemm& g, cudaStream_t st) {
 // 10.4, 9.3; 2048 x 8192 (two fill the SMs) 9.5, 9.1, 13.2; 4096 x 14336 (one fills them) 21.7, -, 34.3. The rule takes 4, 4,
 // 4, 2 and 1; the one shape where it was not best is 64 x 1024 x 4096, 7.2, 6.6, 7.0.
 int swap_splits(const LinGemm& g) {
-  const int64_t tiles = (g.N + 127) / 128, kb = (g.K + BK - 1) / BK;
+  const int64_t tiles = (g.N * (g.glu ? 2 : 1) + 127) / 128, kb = (g.K + BK - 1) / BK;
   int S = 1;
   while (S < 4 && tiles * S * 2 <= num_sms() && kb >= S * 2 * 2) S *= 2;
   return S;
 }
+template <bool GLU = false>
 lnfp8_status swap_launch(const LinGemm& g, cudaStream_t st) {
   const int S = swap_splits(g);
-  return g.M <= 16 ? tile_launch<16, false, true>(g, S, st) : g.M <= 32 ? tile_launch<32, false, true>(g, S, st) : tile_launch<64, false, true>(g, S, st);
+  return g.M <= 16   ? tile_launch<16, false, true, GLU>(g, S, st)
+         : g.M <= 32 ? tile_launch<32, false, true, GLU>(g, S, st)
+                     : tile_launch<64, false, true, GLU>(g, S, st);
 }
 }  // namespace
 
 lnfp8_status lin_gemm_launch(const LinGemm* g, int count, cudaStream_t st) {
   if (g->glu) {
     if (g->M == 0) return LNFP8_OK;
+    if (takes_few(*g)) return g->elem == LNFP8_FP16 ? few_by_tokens<true, true>(*g, st) : few_by_tokens<false, true>(*g, st);
+    if (takes_swap(*g)) return swap_launch<true>(*g, st);
     LinGemm one = *g;
     one.N *= 2;
     const LinPlan pl = lin_plan(&one, 1);
+    if (pl.S == 2) return tile_launch<128, true, false, true>(*g, 2, st);
     return pl.tile == 64 ? pair_launch<64, LIN_GLU>(g, 1, st) : pl.tile == 128 ? pair_launch<128, LIN_GLU>(g, 1, st) : pair_launch<256, LIN_GLU>(g, 1, st);
   }
   if (!g[0].b_mn) {  // the forward: both operands K-major
     if (g->M == 0 || g->N == 0) return LNFP8_OK;
-    if (takes_few(*g)) return g->elem == LNFP8_FP16 ? few_by_tokens<true>(*g, st) : few_by_tokens<false>(*g, st);
+    if (takes_few(*g)) return g->elem == LNFP8_FP16 ? few_by_tokens<true, false>(*g, st) : few_by_tokens<false, false>(*g, st);
     if (takes_swap(*g)) return swap_launch(*g, st);
     LinGemm one = *g;
     const LinPlan pl = lin_plan(&one, 1);
