@@ -97,6 +97,22 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) join_fwd_any_kernel(con
   const float inv_d = 1.0f / (float)p.D;
   const int n = (p.D - t + TPR - 1) / TPR;  // this thread's columns (0 or fewer: none)
   const int tc = min(t, p.D - 1);           // a column to load in place of those it has not
+  constexpr bool HOLD = NE <= 8;            // the columns' factors stay in registers
+  float fa[HOLD ? NE : 1], fc[HOLD ? NE : 1], fg[HOLD ? NE : 1], fb[HOLD ? NE : 1];
+  auto factors = [&](int c, float& a, float& cc) {
+    const float f = p.scale * param_or(p.gate, p.param_elem, c, 1.f);
+    a = f * param_or(p.g1, p.param_elem, c, 1.f);
+    cc = p.b1 ? f * load_elem_rt(p.b1, p.param_elem, c) : 0.f;
+  };
+  if constexpr (HOLD) {
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      const int c = tc + (i < n ? TPR * i : 0);
+      factors(c, fa[i], fc[i]);
+      fg[i] = param_or(p.g2, p.param_elem, c, 0.f);
+      fb[i] = param_or(p.b2, p.param_elem, c, 0.f);
+    }
+  }
   int turn = 0;
   // mean and reciprocal deviation of a row; v becomes the normalised values
   auto normalise = [&](float* v, float& mu, float& rs) {
@@ -147,9 +163,10 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) join_fwd_any_kernel(con
     uint8_t* hr = static_cast<uint8_t*>(p.h) + (row * p.ldh + t) * ES;
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
-      const int c = tc + (i < n ? TPR * i : 0);
-      const float f = p.scale * param_or(p.gate, p.param_elem, c, 1.f);
-      const float tv = fmaf(v[i], f * param_or(p.g1, p.param_elem, c, 1.f), f * param_or(p.b1, p.param_elem, c, 0.f));
+      float fai, fci;
+      if constexpr (HOLD) fai = fa[i], fci = fc[i];
+      else factors(tc + (i < n ? TPR * i : 0), fai, fci);
+      const float tv = fmaf(v[i], fai, fci);
       const bool keep = p.drop.cut == 0 || bits[32 * i + lane] >= p.drop.cut;
       const float sum = bits_value<ELEM>(rb[i]) + (keep ? tv : 0.f);
       v[i] = active && i < n ? round_elem<ELEM>(sum) : 0.f;
@@ -166,8 +183,9 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) join_fwd_any_kernel(con
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
       if (i >= n) continue;
-      const int c = t + TPR * i;
-      store_elem<ELEM>(yr, TPR * i, fmaf(v[i], load_elem_rt(p.g2, p.param_elem, c), param_or(p.b2, p.param_elem, c, 0.f)));
+      const float gi = HOLD ? fg[HOLD ? i : 0] : load_elem_rt(p.g2, p.param_elem, t + TPR * i);
+      const float bi = HOLD ? fb[HOLD ? i : 0] : param_or(p.b2, p.param_elem, t + TPR * i, 0.f);
+      store_elem<ELEM>(yr, TPR * i, fmaf(v[i], gi, bi));
     }
   }
 }
@@ -190,6 +208,17 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) join_bwd_any_kernel(con
   for (int k = 0; k < 4; ++k)
 #pragma unroll
     for (int i = 0; i < NE; ++i) acc[k][i] = 0.f;
+  constexpr bool HOLD = NE <= 8;  // the columns' factors stay in registers
+  float fg[HOLD ? NE : 1], fa[HOLD ? NE : 1];
+  auto factor = [&](int c) { return p.scale * param_or(p.gate, p.param_elem, c, 1.f) * param_or(p.g1, p.param_elem, c, 1.f); };
+  if constexpr (HOLD) {
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      const int c = tc + (i < n ? TPR * i : 0);
+      fg[i] = param_or(p.g2, p.param_elem, c, 0.f);
+      fa[i] = factor(c);
+    }
+  }
   int turn = 0;
   for (int64_t row0 = (int64_t)blockIdx.x * GPB; row0 < p.M; row0 += (int64_t)gridDim.x * GPB) {
     const int64_t row = row0 + g;
@@ -218,7 +247,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) join_bwd_any_kernel(con
         xh[i] = active && i < n ? (xh[i] - mu) * rs : 0.f;
         acc[0][i] = fmaf(q[i], xh[i], acc[0][i]);
         acc[1][i] += q[i];
-        q[i] *= load_elem_rt(p.g2, p.param_elem, tc + (i < n ? TPR * i : 0));
+        q[i] *= HOLD ? fg[HOLD ? i : 0] : load_elem_rt(p.g2, p.param_elem, tc + (i < n ? TPR * i : 0));
         s1 += q[i];
         s2 = fmaf(q[i], xh[i], s2);
       }
@@ -256,10 +285,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) join_bwd_any_kernel(con
     }
     float mu_ = 0.f, mux = 0.f;
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      const int c = tc + (i < n ? TPR * i : 0);
-      d[i] *= p.scale * param_or(p.gate, p.param_elem, c, 1.f) * param_or(p.g1, p.param_elem, c, 1.f);
-    }
+    for (int i = 0; i < NE; ++i) d[i] *= HOLD ? fa[HOLD ? i : 0] : factor(tc + (i < n ? TPR * i : 0));
     if (p.g1) {
       float s1 = 0.f, s2 = 0.f;
 #pragma unroll

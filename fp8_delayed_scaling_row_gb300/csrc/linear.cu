@@ -897,11 +897,26 @@ LinPlan lin_plan(LinGemm* g, int count) {
     const int64_t tiles = (g->M + 255) / 256 * ((g->N + 127) / 128);
     if (kb >= 4) offer((tiles + fit - 1) / fit * ((kb + 1) / 2 * 180 + 7700), 128, 2);
   }
+  // a data gradient's pieces: any number up to those there is room for, the other product whole
+  int most[2] = {1, 1}, data = -1, taken = 0;
+  for (int i = 0; i < count; ++i) {
+    most[i] = g[i].pieces;
+    if (g[i].pieces > 1 && !g[i].a_mn) data = i;
+  }
+  if (data >= 0) {
+    for (int i = 0; i < count; ++i) g[i].pieces = 1;
+    for (int n = 2; n <= most[data]; ++n) {
+      g[data].pieces = n;
+      if (offer(persistent(128, 171, 3640, true), 128, 1)) taken = n;
+      if (offer(persistent(256, 270, 4700, true), 256, 1)) taken = n;
+    }
+    for (int i = 0; i < count; ++i) g[i].pieces = i == data ? 1 : most[i];
+  }
   bool pieces = false;
   for (int i = 0; i < count; ++i) pieces = pieces || g[i].pieces > 1;
   if (pieces) pieces = offer(persistent(256, 270, 4700, true), 256, 1);
   if (!pieces)
-    for (int i = 0; i < count; ++i) g[i].pieces = 1;
+    for (int i = 0; i < count; ++i) g[i].pieces = i == data && taken ? taken : 1;
   return best;
 }
 
@@ -912,13 +927,24 @@ int wgrad_pieces(int64_t M, int64_t K, int64_t N) {
   return (int)max64(1, min64(min64(8, pairs / max64(tiles, 1)), kb / 16));
 }
 
+// The most K pieces of a data gradient [M, K] contracted over n features (both projections of a gated layer) whose tiles leave
+// pairs idle: up to four, of 16 K blocks or more each. One piece and the best number of them, dx and dw together behind
+// their dz pass, us (tokens x in x out): 300 x 2048 x 5504 54.0 and 42.2 (four), 512 x 1024 x 2736 30.7 and 21.9 (four), 1000 x
+// 768 x 2048 22.2 and 21.8 (two), 200 x 4096 x 1024 20.0 and 18.6 (two), 2000 x 2048 x 5504 120 and 124 (two): lin_plan chooses.
+int dgrad_pieces(int64_t M, int64_t K, int64_t n) {
+  const int64_t pairs = max64(num_sms() / 2, 1), tiles = ((M + 255) / 256) * ((K + 255) / 256), kb = (n + BK - 1) / BK;
+  return M <= 64 ? 1 : (int)max64(1, min64(min64(4, pairs / max64(tiles, 1)), kb / 16));
+}
+
 // The forward of one token, and of two to four with few outputs, without a checkpoint (whose blocks span more columns
 // than a warp has here; a decoding step keeps none). FMAs cost by the token and x is staged once a block; the form with
 // tokens on the accumulator's columns costs the same up to 16 of them. us, this form and that (K x N): one token 4096 x 1024 3.3
 // and 6.6, 4096 x 4096 7.8 and 9.0, 4096 x 14336 21.4 and 21.4; two 4096 x 4096 8.4 and 9.1, 4096 x 6144 13.8 and 12.2;
 // four 4096 x 1024 5.3 and 6.7, 4096 x 2048 7.4 and 7.2, 4096 x 4096 10.2 and 9.2, 4096 x 14336 26.6 and 21.5.
+// The gated layer (K x N, both projections): one token 1024 x 4096 6.4 and 6.6, 2048 x 2048 5.4 and 6.8, 4096 x 4096 14.0 and
+// 13.6, 2048 x 5504 11.6 and 10.4, 2048 x 8192 15.2 and 13.2, 4096 x 14336 38.8 and 39.0: the limit of outputs holds there too.
 bool takes_few(const LinGemm& g) {
-  return g.M <= kFewTokens && (g.M == 1 || g.M * g.N * (g.glu ? 2 : 1) <= kFewOutputs) && !g.a_mn && !g.b_mn && !g.ckpt.codes &&
+  return g.M <= kFewTokens && ((g.M == 1 && !g.glu) || g.M * g.N * (g.glu ? 2 : 1) <= kFewOutputs) && !g.a_mn && !g.b_mn && !g.ckpt.codes &&
          g.K * (g.M > 2 ? 4 : g.M) * 2 <= kFewMaxX;
 }
 template <int MT, bool F16, bool GLU>
@@ -1179,11 +1205,15 @@ lnfp8_status linear_glu_fwd_launch(const lnfp8_linear_glu_fwd_args* a, cudaStrea
   return lin_gemm_launch(&g, 1, st);
 }
 
-// dz [M, 2N], the columns' partial sums and the K pieces of dw, each from a multiple of 256 on.
+// dz [M, 2N], the columns' partial sums and the K pieces of dx or of dw, each from a multiple of 256 on.
+static int64_t glu_pieces_bytes(int64_t M, int64_t K, int64_t N) {
+  const int dx = dgrad_pieces(M, K, 2 * N);
+  return max64(wgrad_bytes(M, K, 2 * N), dx > 1 ? up256(dx * M * K * 4) + 256 : 0);  // one of the two is cut at most
+}
 int64_t linear_glu_bwd_ws_bytes(int64_t M, int64_t K, int64_t N) {
   if (M == 0 || N == 0) return 0;
   const int64_t rpb = dact_rows_per_block(M, K, N, true);
-  return up256(M * 2 * N * 2) + up256((M + rpb - 1) / rpb * 2 * N * 4) + wgrad_bytes(M, K, 2 * N);
+  return up256(M * 2 * N * 2) + up256((M + rpb - 1) / rpb * 2 * N * 4) + glu_pieces_bytes(M, K, N);
 }
 
 lnfp8_status linear_glu_bwd_launch(const lnfp8_linear_glu_bwd_args* a, cudaStream_t st) {
@@ -1227,6 +1257,9 @@ lnfp8_status linear_glu_bwd_launch(const lnfp8_linear_glu_bwd_args* a, cudaStrea
   }
   LinGemm g[2] = {};
   int count = 0;
+  // the last part of the workspace, for the product that is cut
+  const uintptr_t at = reinterpret_cast<uintptr_t>(a->workspace) + linear_glu_bwd_ws_bytes(M, K, N) - glu_pieces_bytes(M, K, N);
+  float* part = reinterpret_cast<float*>((at + 31) / 32 * 32);
   if (a->dx) {  // [M, K] = dz [M, 2N] . w, contracted over both projections
     LinGemm& q = g[count++];
     q.elem = a->elem;
@@ -1240,6 +1273,8 @@ lnfp8_status linear_glu_bwd_launch(const lnfp8_linear_glu_bwd_args* a, cudaStrea
     q.b_mn = true;
     q.out = a->dx;
     q.ldo = a->ld_dx;
+    q.pieces = dgrad_pieces(M, K, N2);
+    q.part = part;
   }
   if (a->dw) {  // [2N, K] = dz^T . x, contracted over the tokens
     LinGemm& q = g[count++];
@@ -1256,10 +1291,7 @@ lnfp8_status linear_glu_bwd_launch(const lnfp8_linear_glu_bwd_args* a, cudaStrea
     q.out = a->dw;
     q.ldo = K;
     q.pieces = wgrad_pieces(M, K, N2);
-    if (q.pieces > 1) {  // the last part of the workspace
-      const uintptr_t at = reinterpret_cast<uintptr_t>(a->workspace) + linear_glu_bwd_ws_bytes(M, K, N) - wgrad_bytes(M, K, N2);
-      q.part = reinterpret_cast<float*>((at + 31) / 32 * 32);
-    }
+    q.part = part;
   }
   return count ? lin_gemm_launch(g, count, st) : LNFP8_OK;
 }
