@@ -84,7 +84,7 @@ __device__ __forceinline__ void any_draws(uint16_t* bits, const DropKey& key, in
 }
 
 template <int ELEM, int TPR, int NE>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) join_fwd_any_kernel(const JoinFwdParams p) {
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 ? 2 : 1) join_fwd_any_kernel(const JoinFwdParams p) {
   constexpr int kThreads = TPR < 256 ? 256 : TPR, ES = ElemSize<ELEM>::value, GPB = kThreads / TPR;
   __shared__ float2 xch[2 * kThreads / 32];
   __shared__ __align__(16) uint16_t draws[kThreads / 32][32 * NE];
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) join_fwd_any_kernel(con
   const float inv_d = 1.0f / (float)p.D;
   const int n = (p.D - t + TPR - 1) / TPR;  // this thread's columns (0 or fewer: none)
   const int tc = min(t, p.D - 1);           // a column to load in place of those it has not
-  constexpr bool HOLD = NE <= 8;            // the columns' factors stay in registers
+  constexpr bool HOLD = TPR <= 512;         // the columns' factors stay in registers
   float fa[HOLD ? NE : 1], fc[HOLD ? NE : 1], fg[HOLD ? NE : 1], fb[HOLD ? NE : 1];
   auto factors = [&](int c, float& a, float& cc) {
     const float f = p.scale * param_or(p.gate, p.param_elem, c, 1.f);
@@ -134,24 +134,34 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) join_fwd_any_kernel(con
 #pragma unroll
     for (int i = 0; i < NE; ++i) v[i] *= rs;
   };
-  for (int64_t row0 = (int64_t)blockIdx.x * GPB; row0 < p.M; row0 += (int64_t)gridDim.x * GPB) {
-    const int64_t row = row0 + g;
-    const bool active = row < p.M;
-    const int64_t rowc = active ? row : p.M - 1;
+  // the bits of the next row, where there are registers for them, are on their way while one is worked on
+  constexpr bool AHEAD = TPR <= 512;
+  uint32_t xb[NE], rb[NE];
+#pragma unroll
+  for (int i = 0; i < NE; ++i) rb[i] = 0u;
+  auto fetch = [&](int64_t row) {
+    const int64_t rowc = min64(row, p.M - 1);
     const uint8_t* xr = static_cast<const uint8_t*>(p.x) + (rowc * p.ldx + tc) * ES;
     const uint8_t* rr = static_cast<const uint8_t*>(p.resid) + (rowc * p.ldr + tc) * ES;
-    uint32_t xb[NE], rb[NE];
 #pragma unroll
     for (int i = 0; i < NE; ++i) xb[i] = load_bits<ELEM>(xr, i < n ? TPR * i : 0);
-#pragma unroll
-    for (int i = 0; i < NE; ++i) rb[i] = 0u;
     if (p.resid) {
 #pragma unroll
       for (int i = 0; i < NE; ++i) rb[i] = load_bits<ELEM>(rr, i < n ? TPR * i : 0);
     }
+  };
+  if constexpr (AHEAD) fetch((int64_t)blockIdx.x * GPB + g);
+  for (int64_t row0 = (int64_t)blockIdx.x * GPB; row0 < p.M; row0 += (int64_t)gridDim.x * GPB) {
+    const int64_t row = row0 + g;
+    const bool active = row < p.M;
+    if constexpr (!AHEAD) fetch(row);
     float v[NE], mu, rs;
 #pragma unroll
     for (int i = 0; i < NE; ++i) v[i] = active && i < n ? bits_value<ELEM>(xb[i]) : 0.f;
+    float r[NE];
+#pragma unroll
+    for (int i = 0; i < NE; ++i) r[i] = bits_value<ELEM>(rb[i]);
+    if constexpr (AHEAD) fetch(row + (int64_t)gridDim.x * GPB);
     if (p.g1) {
       normalise(v, mu, rs);
       if (t == 0 && active) {
@@ -168,7 +178,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) join_fwd_any_kernel(con
       else factors(tc + (i < n ? TPR * i : 0), fai, fci);
       const float tv = fmaf(v[i], fai, fci);
       const bool keep = p.drop.cut == 0 || bits[32 * i + lane] >= p.drop.cut;
-      const float sum = bits_value<ELEM>(rb[i]) + (keep ? tv : 0.f);
+      const float sum = r[i] + (keep ? tv : 0.f);
       v[i] = active && i < n ? round_elem<ELEM>(sum) : 0.f;
       if (active && i < n) store_elem<ELEM>(hr, TPR * i, v[i]);
     }
@@ -191,7 +201,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) join_fwd_any_kernel(con
 }
 
 template <int ELEM, int TPR, int NE>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) join_bwd_any_kernel(const JoinBwdParams p) {
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 ? 2 : 1) join_bwd_any_kernel(const JoinBwdParams p) {
   constexpr int kThreads = TPR < 256 ? 256 : TPR, ES = ElemSize<ELEM>::value, GPB = kThreads / TPR;
   __shared__ float2 xch[2 * kThreads / 32];
   __shared__ __align__(16) uint16_t draws[kThreads / 32][32 * NE];
@@ -208,7 +218,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) join_bwd_any_kernel(con
   for (int k = 0; k < 4; ++k)
 #pragma unroll
     for (int i = 0; i < NE; ++i) acc[k][i] = 0.f;
-  constexpr bool HOLD = NE <= 8;  // the columns' factors stay in registers
+  constexpr bool HOLD = TPR <= 512;  // the columns' factors stay in registers
   float fg[HOLD ? NE : 1], fa[HOLD ? NE : 1];
   auto factor = [&](int c) { return p.scale * param_or(p.gate, p.param_elem, c, 1.f) * param_or(p.g1, p.param_elem, c, 1.f); };
   if constexpr (HOLD) {
@@ -224,22 +234,33 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) join_bwd_any_kernel(con
     const int64_t row = row0 + g;
     const bool active = row < p.M;
     const int64_t rowc = active ? row : p.M - 1;
-    auto load = [&](const void* src, int64_t ld, float* v) {
+    auto fetch = [&](const void* src, int64_t ld, uint32_t* b) {
       const uint8_t* r = static_cast<const uint8_t*>(src) + (rowc * ld + tc) * ES;
-      uint32_t b[NE];
 #pragma unroll
       for (int i = 0; i < NE; ++i) b[i] = load_bits<ELEM>(r, i < n ? TPR * i : 0);
+    };
+    auto value = [&](const uint32_t* b, float* v) {
 #pragma unroll
       for (int i = 0; i < NE; ++i) v[i] = active && i < n ? bits_value<ELEM>(b[i]) : 0.f;
     };
+    // every load of the row first, where there are registers for them
+    constexpr bool FIRST = TPR <= 512;
+    uint32_t b0[NE], b1[NE], b2[FIRST ? NE : 1], b3[FIRST ? NE : 1];
+    if (p.g2) {
+      fetch(p.dy, p.lddy, b0);
+      fetch(p.h, p.ldh, b1);
+    }
+    if constexpr (FIRST) {
+      if (p.dh) fetch(p.dh, p.lddh, b2);
+      if (p.g1 || p.gate) fetch(p.x, p.ldx, b3);
+    }
     float d[NE], xh[NE];  // the gradient on its way down; normalised values
 #pragma unroll
     for (int i = 0; i < NE; ++i) d[i] = 0.f;
-    if (p.dh) load(p.dh, p.lddh, d);
     if (p.g2) {
       float q[NE];
-      load(p.dy, p.lddy, q);
-      load(p.h, p.ldh, xh);
+      value(b0, q);
+      value(b1, xh);
       const float rs = p.rs2[rowc], mu = p.layer ? p.mu2[rowc] : 0.f;
       float s1 = 0.f, s2 = 0.f;
 #pragma unroll
@@ -254,7 +275,18 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) join_bwd_any_kernel(con
       const float2 s = row_sum2<TPR>(s1, s2, xch, turn);
       const float mq = p.layer ? s.x * inv_d : 0.f, mqx = s.y * inv_d;
 #pragma unroll
-      for (int i = 0; i < NE; ++i) d[i] += fmaf(-mqx, xh[i], q[i] - mq) * rs;
+      for (int i = 0; i < NE; ++i) d[i] = fmaf(-mqx, xh[i], q[i] - mq) * rs;
+    }
+    if (p.dh) {
+      float r[NE];
+      if constexpr (FIRST) {
+        value(b2, r);
+      } else {
+        fetch(p.dh, p.lddh, b0);
+        value(b0, r);
+      }
+#pragma unroll
+      for (int i = 0; i < NE; ++i) d[i] += r[i];
     }
     if (p.dres && active) {
       uint8_t* o = static_cast<uint8_t*>(p.dres) + (row * p.lddres + t) * ES;
@@ -270,7 +302,12 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) join_bwd_any_kernel(con
     }
     float rs = 1.f;
     if (p.g1 || p.gate) {
-      load(p.x, p.ldx, xh);
+      if constexpr (FIRST) {
+        value(b3, xh);
+      } else {
+        fetch(p.x, p.ldx, b0);
+        value(b0, xh);
+      }
       if (p.g1) {
         rs = p.rs1[rowc];
         const float mu = p.layer ? p.mu1[rowc] : 0.f;
@@ -354,11 +391,11 @@ constexpr int kVecThreads = 512;
 constexpr int kVecSmem = 226 * 1024;
 
 // Four columns of a factor array: quarter q of the row's words' quarters.
-template <int TPR, int NV, int EPC>
+template <int T, int TPR, int NV, int EPC>
 __device__ __forceinline__ void put_factors(uint4* at, int k, const void* a, const void* b, int elem, float scale, float none, int D) {
   constexpr int Q = NV * EPC / 4;  // of a thread
   float4* dst = reinterpret_cast<float4*>(at) + k * Q * TPR;
-  for (int i = threadIdx.x; i < Q * TPR; i += kVecThreads) {
+  for (int i = threadIdx.x; i < Q * TPR; i += T) {
     const int t = i % TPR, q = i / TPR, c = (t + TPR * (q * 4 / EPC)) * EPC + q * 4 % EPC;
     float v[4];
 #pragma unroll
@@ -430,11 +467,11 @@ __global__ void __launch_bounds__(kVecThreads, 1) join_fwd_vec_kernel(const Join
   drop_save(p.drop);
   const DropKey key = drop_key(p.drop);
   uint4* fput = ring + RING * SB / 16;
-  put_factors<TPR, NV, EPC>(fput, 0, p.gate, p.g1, p.param_elem, p.scale, 1.f, p.D);
-  if (p.g2) put_factors<TPR, NV, EPC>(fput, 1, p.g2, nullptr, p.param_elem, 1.f, 0.f, p.D);
+  put_factors<T, TPR, NV, EPC>(fput, 0, p.gate, p.g1, p.param_elem, p.scale, 1.f, p.D);
+  if (p.g2) put_factors<T, TPR, NV, EPC>(fput, 1, p.g2, nullptr, p.param_elem, 1.f, 0.f, p.D);
   if constexpr (FULL) {
-    put_factors<TPR, NV, EPC>(fput, 2, p.b1, p.gate, p.param_elem, p.scale, 0.f, p.D);
-    put_factors<TPR, NV, EPC>(fput, 3, p.b2, nullptr, p.param_elem, 1.f, 0.f, p.D);
+    put_factors<T, TPR, NV, EPC>(fput, 2, p.b1, p.gate, p.param_elem, p.scale, 0.f, p.D);
+    put_factors<T, TPR, NV, EPC>(fput, 3, p.b2, nullptr, p.param_elem, 1.f, 0.f, p.D);
   }
   __syncthreads();
   const float inv_d = 1.0f / (float)p.D;
@@ -549,21 +586,21 @@ __global__ void __launch_bounds__(kVecThreads, 1) join_fwd_vec_kernel(const Join
   cp_wait<0>();
 }
 
-template <int ELEM, int TPR, int NV, bool FULL>
+template <int ELEM, int TPR, int NV, bool FULL, int T>
 struct JoinBwdShape {
   // bytes per thread and row, each kind an array over the threads: dy, h, dh, x, then rs2, rs1 and, FULL, mu2, mu1
   static constexpr int W = NV * 16, S_OFF = 4 * W, BYTES = S_OFF + (FULL ? 16 : 8);
-  static constexpr int SLOT = BYTES * kVecThreads, FACTORS = 2 * TPR * NV * Word<ELEM>::EPC * 4;
+  static constexpr int SLOT = BYTES * T, FACTORS = 2 * TPR * NV * Word<ELEM>::EPC * 4;
   static constexpr int FIT = (kVecSmem - FACTORS) / SLOT, RING = FIT < 4 ? FIT : 4;
   static constexpr size_t SMEM = (size_t)RING * SLOT + FACTORS;
   static_assert(RING >= 2, "shared memory budget");
 };
 
 // FULL: with means, and with the sums of dy and dt (for the betas).
-template <int ELEM, int TPR, int NV, bool FULL>
-__global__ void __launch_bounds__(kVecThreads, 1) join_bwd_vec_kernel(const JoinBwdParams p) {
-  using S = JoinBwdShape<ELEM, TPR, NV, FULL>;
-  constexpr int T = kVecThreads, GPB = T / TPR, RING = S::RING, P = RING - 1;
+template <int ELEM, int TPR, int NV, bool FULL, int T>
+__global__ void __launch_bounds__(T, 1) join_bwd_vec_kernel(const JoinBwdParams p) {
+  using S = JoinBwdShape<ELEM, TPR, NV, FULL, T>;
+  constexpr int GPB = T / TPR, RING = S::RING, P = RING - 1;
   constexpr int EPC = Word<ELEM>::EPC, PP = EPC / 2, ES = ElemSize<ELEM>::value;
   __shared__ float2 xch[2 * T / 32];
   extern __shared__ uint4 ring[];  // [RING][BYTES * T], then the factors pre_gamma, scale gate post_gamma
@@ -625,8 +662,8 @@ __global__ void __launch_bounds__(kVecThreads, 1) join_bwd_vec_kernel(const Join
   for (int k = 0; k < P; ++k) issue(row + k * p.step, base + k * SB);
   const DropKey key = drop_key(p.drop);
   uint4* fput = ring + RING * SB / 16;
-  if (p.g2) put_factors<TPR, NV, EPC>(fput, 0, p.g2, nullptr, p.param_elem, 1.f, 0.f, p.D);
-  put_factors<TPR, NV, EPC>(fput, 1, p.gate, p.g1, p.param_elem, p.scale, 1.f, p.D);
+  if (p.g2) put_factors<T, TPR, NV, EPC>(fput, 0, p.g2, nullptr, p.param_elem, 1.f, 0.f, p.D);
+  put_factors<T, TPR, NV, EPC>(fput, 1, p.gate, p.g1, p.param_elem, p.scale, 1.f, p.D);
   __syncthreads();
   constexpr int NS = FULL ? 4 : 2;
   uint64_t acc[NS][NV][PP];  // sums of dy hhat, drop(dH) xhat, dy, drop(dH)
@@ -851,21 +888,27 @@ __global__ void __launch_bounds__(1024) join_sum_kernel(const JoinSumParams p) {
 }
 
 // ------------------------------------------------------------ host side
+template <int ELEM, int TPR, int NE>
+lnfp8_status fwd_any_launch(const JoinFwdParams& p, cudaStream_t st) {
+  constexpr auto kernel = join_fwd_any_kernel<ELEM, TPR, NE>;
+  constexpr int threads = TPR < 256 ? 256 : TPR, gpb = threads / TPR;
+  int bps = 1;
+  const lnfp8_status s = kernel_setup<kernel>(threads, 0, &bps, "block_join_fwd: kernel set-up");
+  if (s != LNFP8_OK) return s;
+  // blocks that are all resident: each reads the columns' factors once
+  const int64_t blocks = min64((p.M + gpb - 1) / gpb, (int64_t)num_sms() * bps);
+  if (launch_pdl(kernel, dim3((unsigned)blocks), dim3(threads), 0, st, p) != cudaSuccess) return check_launch("block_join_fwd launch");
+  return check_launch("block_join_fwd");
+}
 template <int ELEM>
 lnfp8_status fwd_any(const JoinFwdParams& p, cudaStream_t st) {
-  auto go = [&](auto kernel, int tpr) {
-    const int threads = tpr < 256 ? 256 : tpr, gpb = threads / tpr;
-    const int64_t blocks = min64((p.M + gpb - 1) / gpb, (int64_t)num_sms() * (2048 / threads));
-    if (launch_pdl(kernel, dim3((unsigned)blocks), dim3(threads), 0, st, p) != cudaSuccess) return check_launch("block_join_fwd launch");
-    return check_launch("block_join_fwd");
-  };
-  if (p.D <= 256) return go(join_fwd_any_kernel<ELEM, 32, 8>, 32);
-  if (p.D <= 512) return go(join_fwd_any_kernel<ELEM, 64, 8>, 64);
-  if (p.D <= 1024) return go(join_fwd_any_kernel<ELEM, 128, 8>, 128);
-  if (p.D <= 2048) return go(join_fwd_any_kernel<ELEM, 256, 8>, 256);
-  if (p.D <= 4096) return go(join_fwd_any_kernel<ELEM, 512, 8>, 512);
-  if (p.D <= 8192) return go(join_fwd_any_kernel<ELEM, 1024, 8>, 1024);
-  return go(join_fwd_any_kernel<ELEM, 1024, 16>, 1024);
+  if (p.D <= 256) return fwd_any_launch<ELEM, 32, 8>(p, st);
+  if (p.D <= 512) return fwd_any_launch<ELEM, 64, 8>(p, st);
+  if (p.D <= 1024) return fwd_any_launch<ELEM, 128, 8>(p, st);
+  if (p.D <= 2048) return fwd_any_launch<ELEM, 256, 8>(p, st);
+  if (p.D <= 4096) return fwd_any_launch<ELEM, 512, 8>(p, st);
+  if (p.D <= 8192) return fwd_any_launch<ELEM, 1024, 8>(p, st);
+  return fwd_any_launch<ELEM, 1024, 16>(p, st);
 }
 
 constexpr int kBwdBlocksPerSm = 2;  // at most: each leaves partial rows of the column sums
@@ -918,7 +961,11 @@ lnfp8_status fwd_vec(const JoinFwdParams& p, cudaStream_t st) {
   if (p.D <= 128) return fwd_vec_launch<ELEM, 8, NV, FULL>(p, st);
   if (p.D <= 256) return fwd_vec_launch<ELEM, 16, NV, FULL>(p, st);
   if (p.D <= 512) return fwd_vec_launch<ELEM, 32, NV, FULL>(p, st);
+  if constexpr (ELEM != LNFP8_FP32)
+    if (p.D <= 768) return fwd_vec_launch<ELEM, 32, 3, FULL>(p, st);
   if (p.D <= 1024) return fwd_vec_launch<ELEM, 64, NV, FULL>(p, st);
+  if constexpr (ELEM != LNFP8_FP32)
+    if (p.D <= 1536) return fwd_vec_launch<ELEM, 64, 3, FULL>(p, st);
   if (p.D <= 2048) return fwd_vec_launch<ELEM, 128, NV, FULL>(p, st);
   if constexpr (ELEM == LNFP8_FP32) return p.D <= 4096 ? fwd_vec_launch<ELEM, 256, NV, FULL>(p, st) : fwd_any<ELEM>(p, st);
   else return p.D <= 4096 ? fwd_vec_launch<ELEM, 256, NV, FULL>(p, st) : fwd_vec_launch<ELEM, 512, NV, FULL>(p, st);
@@ -933,14 +980,20 @@ lnfp8_status fwd(const JoinFwdParams& p, cudaStream_t st) {
   return full ? fwd_vec<ELEM, true>(p, st) : fwd_vec<ELEM, false>(p, st);
 }
 
+// Threads of a block (one an SM): as many as leave each the registers of its sums and its row.
+constexpr int bwd_threads(int elem, int tpr, int nv, bool full) {
+  if (nv == 3) return full ? 256 : 384;
+  return full && elem != LNFP8_FP32 && tpr <= 128 ? 384 : 512;
+}
 template <int ELEM, int TPR, int NV, bool FULL>
 lnfp8_status bwd_vec_launch(const JoinBwdParams& p, int* blocks_out, cudaStream_t st) {
-  using S = JoinBwdShape<ELEM, TPR, NV, FULL>;
+  constexpr int T = bwd_threads(ELEM, TPR, NV, FULL);
+  using S = JoinBwdShape<ELEM, TPR, NV, FULL, T>;
   static_assert(S::SMEM >= TPR * NV * Word<ELEM>::EPC * sizeof(float), "the column partials reuse the ring");
-  constexpr auto kernel = join_bwd_vec_kernel<ELEM, TPR, NV, FULL>;
-  const lnfp8_status s = kernel_setup<kernel>(kVecThreads, S::SMEM, nullptr, "block_join_bwd: kernel set-up");
+  constexpr auto kernel = join_bwd_vec_kernel<ELEM, TPR, NV, FULL, T>;
+  const lnfp8_status s = kernel_setup<kernel>(T, S::SMEM, nullptr, "block_join_bwd: kernel set-up");
   if (s != LNFP8_OK) return s;
-  constexpr int gpb = kVecThreads / TPR, es = ElemSize<ELEM>::value;
+  constexpr int gpb = T / TPR, es = ElemSize<ELEM>::value;
   const int64_t blocks = min64((p.M + gpb - 1) / gpb, num_sms());
   *blocks_out = (int)blocks;
   JoinBwdParams q = p;
@@ -951,21 +1004,26 @@ lnfp8_status bwd_vec_launch(const JoinBwdParams& p, int* blocks_out, cudaStream_
   q.hstep = q.step * p.ldh * es;
   q.dxstep = q.step * p.lddx * es;
   q.drstep = q.step * p.lddres * es;
-  if (launch_pdl(kernel, dim3((unsigned)blocks), dim3(kVecThreads), S::SMEM, st, q) != cudaSuccess) return check_launch("block_join_bwd launch");
+  if (launch_pdl(kernel, dim3((unsigned)blocks), dim3(T), S::SMEM, st, q) != cudaSuccess) return check_launch("block_join_bwd launch");
   return check_launch("block_join_bwd");
 }
-template <int ELEM, int NV, bool FULL>
+// Columns a thread: 16 of a 16-bit type (24 where a row of 16 would leave a quarter of the threads or more without any), 8
+// of fp32, whose words of four tensors fill the ring sooner.
+template <int ELEM, bool FULL>
 lnfp8_status bwd_vec(const JoinBwdParams& p, int* blocks_out, cudaStream_t st) {
-  constexpr int W = NV * Word<ELEM>::EPC;  // columns a thread
-  if (p.D <= 8 * W) return bwd_vec_launch<ELEM, 8, NV, FULL>(p, blocks_out, st);
-  if (p.D <= 16 * W) return bwd_vec_launch<ELEM, 16, NV, FULL>(p, blocks_out, st);
-  if (p.D <= 32 * W) return bwd_vec_launch<ELEM, 32, NV, FULL>(p, blocks_out, st);
-  if (p.D <= 64 * W) return bwd_vec_launch<ELEM, 64, NV, FULL>(p, blocks_out, st);
-  if (p.D <= 128 * W) return bwd_vec_launch<ELEM, 128, NV, FULL>(p, blocks_out, st);
-  if (p.D <= 256 * W) return bwd_vec_launch<ELEM, 256, NV, FULL>(p, blocks_out, st);
-  return bwd_vec_launch<ELEM, 512, NV, FULL>(p, blocks_out, st);
+  constexpr int W = 2 * Word<ELEM>::EPC;
+  if (p.D <= 8 * W) return bwd_vec_launch<ELEM, 8, 2, FULL>(p, blocks_out, st);
+  if (p.D <= 16 * W) return bwd_vec_launch<ELEM, 16, 2, FULL>(p, blocks_out, st);
+  if (p.D <= 32 * W) return bwd_vec_launch<ELEM, 32, 2, FULL>(p, blocks_out, st);
+  if constexpr (ELEM != LNFP8_FP32)
+    if (p.D <= 48 * W) return bwd_vec_launch<ELEM, 32, 3, FULL>(p, blocks_out, st);
+  if (p.D <= 64 * W) return bwd_vec_launch<ELEM, 64, 2, FULL>(p, blocks_out, st);
+  if constexpr (ELEM != LNFP8_FP32)
+    if (p.D <= 96 * W) return bwd_vec_launch<ELEM, 64, 3, FULL>(p, blocks_out, st);
+  if (p.D <= 128 * W) return bwd_vec_launch<ELEM, 128, 2, FULL>(p, blocks_out, st);
+  if (p.D <= 256 * W) return bwd_vec_launch<ELEM, 256, 2, FULL>(p, blocks_out, st);
+  return bwd_vec_launch<ELEM, 512, 2, FULL>(p, blocks_out, st);
 }
-// With means and betas' sums 8 columns a thread, or 16 where a row would not fit 512 threads.
 template <int ELEM>
 lnfp8_status bwd(const JoinBwdParams& p, int* blocks_out, cudaStream_t st) {
   constexpr int es = ElemSize<ELEM>::value;
@@ -975,9 +1033,7 @@ lnfp8_status bwd(const JoinBwdParams& p, int* blocks_out, cudaStream_t st) {
                    (!(p.g1 || p.gate) || row_aligned(p.x, p.ldx, es));
   if (!vec) return bwd_any<ELEM>(p, blocks_out, st);
   const bool full = (p.layer && (p.g1 || p.g2)) || (p.sums & 10);
-  if (!full) return bwd_vec<ELEM, 2, false>(p, blocks_out, st);
-  if constexpr (ELEM == LNFP8_FP32) return bwd_vec<ELEM, 2, true>(p, blocks_out, st);
-  else return p.D <= 512 * 8 ? bwd_vec<ELEM, 1, true>(p, blocks_out, st) : bwd_vec_launch<ELEM, 512, 2, true>(p, blocks_out, st);
+  return full ? bwd_vec<ELEM, true>(p, blocks_out, st) : bwd_vec<ELEM, false>(p, blocks_out, st);
 }
 
 }  // namespace
