@@ -1219,18 +1219,21 @@ def dropout_rng(seed: int, *, step: int = 0, device="cuda") -> torch.Tensor:
     return torch.tensor([seed - (1 << 64) if seed >= 1 << 63 else seed, step], dtype=torch.int64, device=device)
 
 
-def _drop(p, rng, site, saved, dev) -> CDropout:
-    """saved: the forward keeps a copy of rng for the backward there."""
+def _drop(p, rng, site, dev, save=False):
+    """The C form, and with `save` where the forward keeps a copy of rng for the backward. Nothing is drawn below p = 2^-17."""
     if not 0.0 <= p <= 1.0:
         raise ValueError(f"p is {p}: expected 0..1")
     if not 0 <= site < 1 << 32:
         raise ValueError(f"site is {site}: expected 0..2^32 - 1")
+    if p * 65536 + 0.5 < 1.0:
+        return _NO_DROP, None
     if rng is None:
-        if p * 65536 + 0.5 >= 1.0:
-            raise ValueError("dropout needs rng (see dropout_rng)")
-        return _NO_DROP
+        raise ValueError("dropout needs rng (see dropout_rng)")
     _flat(rng, "rng", (2,), torch.int64, dev)
-    return CDropout(p, rng.data_ptr(), _ptr(saved), site)
+    if not save:
+        return CDropout(p, rng.data_ptr(), None, site), None
+    kept = torch.empty_like(rng)
+    return CDropout(p, rng.data_ptr(), kept.data_ptr(), site), kept
 
 
 @dataclass
@@ -1241,21 +1244,21 @@ class DropoutCtx:
     site: int = 0
 
 
-def _dropout(x, name, p, rng, site, saved, out, out_name):
+def _dropout(x, name, p, rng, site, save, out, out_name):
     elem = _elem(x, name)
     if x.dim() != 2:
         raise ValueError(f"{name} has shape {tuple(x.shape)}: expected two dimensions")
     rows, cols = x.shape
     dev = _dev(x, name)
     ldx = _rows(x, name, rows, cols, x.dtype, dev)
-    d = _drop(p, rng, site, saved, dev)
+    d, kept = _drop(p, rng, site, dev, save)
     ldo = cols
     if out is None:
         out = _e((rows, cols), x.dtype, x.device)
     else:
         ldo = _rows(out, out_name, rows, cols, x.dtype, dev)
     _check(_c_dropout(x.data_ptr(), elem, rows, cols, ldx, C.byref(d), out.data_ptr(), ldo, _raw_stream(dev)))
-    return out
+    return out, kept
 
 
 def dropout_fwd(x, p, rng, *, site=0, y=None, stream=None):
@@ -1264,8 +1267,8 @@ def dropout_fwd(x, p, rng, *, site=0, y=None, stream=None):
     if stream is not None:
         with _on(stream, _dev(x, "x")):
             return dropout_fwd(x, p, rng, site=site, y=y)
-    ctx = DropoutCtx(p, None if rng is None else torch.empty_like(rng), site)
-    return _dropout(x, "x", p, rng, site, ctx.rng, y, "y"), ctx
+    y, kept = _dropout(x, "x", p, rng, site, True, y, "y")
+    return y, DropoutCtx(p, kept, site)
 
 
 def dropout_bwd(dy, ctx: DropoutCtx, *, dx=None, stream=None) -> torch.Tensor:
@@ -1273,7 +1276,7 @@ def dropout_bwd(dy, ctx: DropoutCtx, *, dx=None, stream=None) -> torch.Tensor:
     if stream is not None:
         with _on(stream, _dev(dy, "dy")):
             return dropout_bwd(dy, ctx, dx=dx)
-    return _dropout(dy, "dy", ctx.p, ctx.rng, ctx.site, None, dx, "dx")
+    return _dropout(dy, "dy", ctx.p, ctx.rng, ctx.site, False, dx, "dx")[0]
 
 
 NORMS = {"rms": 0, "layer": 1}
@@ -1302,17 +1305,19 @@ def _norm(norm) -> int:
     return NORMS[norm]
 
 
-def _vectors(D, dev, **vectors):
-    """Checks the [D] vectors that are there, all of one type; returns its number."""
-    kind = None
-    for name, v in vectors.items():
+_VECTORS = ("post_gamma", "post_beta", "gate", "pre_gamma", "pre_beta")
+
+
+def _vectors(D, dev, vectors):
+    """Checks the [D] vectors (as in _VECTORS) that are there, all of one type; returns its number."""
+    kind, elem, shape = None, 0, (D,)
+    for name, v in zip(_VECTORS, vectors):
         if v is None:
             continue
         if kind is None:
-            kind = v.dtype
-            elem = _elem(v, name)
-        _flat(v, name, (D,), kind, dev)
-    return 0 if kind is None else elem
+            kind, elem = v.dtype, _elem(v, name)
+        _flat(v, name, shape, kind, dev)
+    return elem
 
 
 def block_join_fwd(x, residual=None, *, norm="rms", post_gamma=None, post_beta=None, gate=None, scale=1.0, p=0.0, rng=None,
@@ -1333,17 +1338,16 @@ def block_join_fwd(x, residual=None, *, norm="rms", post_gamma=None, post_beta=N
                                   rng=rng, site=site, pre_gamma=pre_gamma, pre_beta=pre_beta, eps=eps, h=h, y=y)
     ldx = _rows(x, "x", M, D, dt, dev)
     ldr = _rows(residual, "residual", M, D, dt, dev) if residual is not None else 0
-    pe = _vectors(D, dev, post_gamma=post_gamma, post_beta=post_beta, gate=gate, pre_gamma=pre_gamma, pre_beta=pre_beta)
-    ctx = BlockJoinCtx(None, None, norm, scale, p, None, site)
-    if rng is not None:
-        ctx.rng = torch.empty_like(rng)
-    drop = _drop(p, rng, site, ctx.rng, dev)
+    pe = _vectors(D, dev, (post_gamma, post_beta, gate, pre_gamma, pre_beta))
+    drop, kept = _drop(p, rng, site, dev, True)
     ldh = ldy = D
     if h is None:
         h = _e((M, D), dt, device)
     else:
         ldh = _rows(h, "h", M, D, dt, dev)
-    if pre_gamma is None:
+    post, pre = post_gamma is not None, pre_gamma is not None
+    m1 = r1 = m2 = r2 = None
+    if not pre:
         if y is not None:
             raise ValueError("y without pre_gamma")
     else:
@@ -1351,20 +1355,18 @@ def block_join_fwd(x, residual=None, *, norm="rms", post_gamma=None, post_beta=N
             y = _e((M, D), dt, device)
         else:
             ldy = _rows(y, "y", M, D, dt, dev)
-        ctx.h, ctx.pre_rsigma = h, _e((M,), torch.float32, device)
+        r2 = _e((M,), torch.float32, device)
         if kind:
-            ctx.pre_mu = _e((M,), torch.float32, device)
-    if post_gamma is not None:
-        ctx.post_rsigma = _e((M,), torch.float32, device)
+            m2 = _e((M,), torch.float32, device)
+    if post:
+        r1 = _e((M,), torch.float32, device)
         if kind:
-            ctx.post_mu = _e((M,), torch.float32, device)
-    if post_gamma is not None or gate is not None:
-        ctx.x = x
+            m1 = _e((M,), torch.float32, device)
     a = CBlockJoinFwd(M, D, elem, pe, kind, eps, scale, x.data_ptr(), _ptr(residual), _ptr(post_gamma), _ptr(post_beta), _ptr(gate),
-                      _ptr(pre_gamma), _ptr(pre_beta), drop, h.data_ptr(), _ptr(y), _ptr(ctx.post_mu), _ptr(ctx.post_rsigma),
-                      _ptr(ctx.pre_mu), _ptr(ctx.pre_rsigma), ldx, ldr, ldh, ldy)
+                      _ptr(pre_gamma), _ptr(pre_beta), drop, h.data_ptr(), _ptr(y), _ptr(m1), _ptr(r1), _ptr(m2), _ptr(r2), ldx, ldr,
+                      ldh, ldy)
     _check(_c_block_join_fwd(C.byref(a), _raw_stream(dev)))
-    return h, y, ctx
+    return h, y, BlockJoinCtx(x if post or gate is not None else None, h if pre else None, norm, scale, p, kept, site, m1, r1, m2, r2)
 
 
 @dataclass
@@ -1412,10 +1414,10 @@ def block_join_bwd(dh, dy, ctx: BlockJoinCtx, *, post_gamma=None, post_beta=None
                                   pre_beta=pre_beta, grads=grads)
     lddh = _rows(dh, "dh", M, D, dt, dev) if dh is not None else 0
     lddy = _rows(dy, "dy", M, D, dt, dev) if dy is not None else 0
-    pe = _vectors(D, dev, post_gamma=post_gamma, post_beta=post_beta, gate=gate, pre_gamma=pre_gamma, pre_beta=pre_beta)
+    pe = _vectors(D, dev, (post_gamma, post_beta, gate, pre_gamma, pre_beta))
     if pre_beta is not None and pre_gamma is None:
         raise ValueError("pre_beta without pre_gamma")
-    drop = _drop(ctx.p, ctx.rng, ctx.site, None, dev)
+    drop = _drop(ctx.p, ctx.rng, ctx.site, dev)[0]
 
     def kept(part, gamma, row, name):
         """Pointers of a norm's input and statistics, and its row stride."""
