@@ -2,7 +2,7 @@
 // act_ckpt_restore, linear_act_fwd / linear_act_bwd, linear_glu_fwd / linear_glu_bwd,
 // block_join_fwd / block_join_bwd and dropout_apply. Checks every argument
 // before anything is enqueued, fills in the default row strides, and runs the
-// launchers of layernorm_rows.cu, act_ckpt.cu, linear.cu, block_join.cu and dropout.cu.
+// launchers of layernorm_rows.cu, act_ckpt.cu, linear.cu, block_join_fwd.cu, block_join_bwd.cu and dropout.cu.
 #include "common.cuh"
 #include "internal.h"
 

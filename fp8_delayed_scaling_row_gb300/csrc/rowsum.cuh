@@ -1,5 +1,5 @@
 // Sums over the threads that share a row, for the kernels that give a row to a group of TPR threads
-// (layernorm_rows.cu, block_join.cu).
+// (layernorm_rows.cu, block_join_fwd.cu, block_join_bwd.cu).
 #pragma once
 
 #include "common.cuh"
