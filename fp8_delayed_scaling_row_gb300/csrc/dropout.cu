@@ -22,7 +22,7 @@ struct DropoutParams {
 
 constexpr int kDropWarps = 8;
 
-// Any width and alignment: a warp takes 256 columns of a row. Lane q draws for the q-th group of eight, and the draws go
+// Any width and alignment, bound by its accesses of one element (16384 x 8191 bf16 153 us, fp32 8192 x 8191 93): a warp takes 256 columns of a row. Lane q draws for the q-th group of eight, and the draws go
 // through shared memory to the lanes that hold the columns (32 neighbours at a time).
 template <int ELEM>
 __global__ void __launch_bounds__(32 * kDropWarps) dropout_any_kernel(const DropoutParams p) {
@@ -53,8 +53,47 @@ __global__ void __launch_bounds__(32 * kDropWarps) dropout_any_kernel(const Drop
   }
 }
 
-// Rows of 16-byte words: a thread takes groups of eight columns, kItems of them at a time so that their loads are on their
-// way together, a whole grid apart; row and group move on by additions.
+// The same of rows of up to 128 columns, where a warp a row would leave most of its draws unused: a warp takes 32 groups of eight
+// columns one after another, from one row into the next, and the lane of a column gets its row and group from the lane that
+// drew for it.
+template <int ELEM>
+__global__ void __launch_bounds__(32 * kDropWarps) dropout_narrow_kernel(const DropoutParams p) {
+  __shared__ __align__(16) uint16_t bits[kDropWarps][256];
+  pdl_wait();
+  pdl_launch_dependents();
+  drop_save(p.drop);
+  const DropKey key = drop_key(p.drop);
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t groups = ((uint32_t)p.cols + 7) >> 3;
+  const int64_t items = p.rows * groups;
+  for (int64_t i0 = ((int64_t)blockIdx.x * kDropWarps + w) * 32; i0 < items; i0 += (int64_t)gridDim.x * kDropWarps * 32) {
+    const int64_t item = i0 + lane;
+    const bool in = item < items;
+    const uint32_t row = in ? (uint32_t)(item / groups) : 0u, g = in ? (uint32_t)(item - (int64_t)row * groups) : groups;  // past every column
+    uint32_t v[8], r[8], c[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      r[k] = __shfl_sync(0xFFFFFFFFu, row, 4 * k + (lane >> 3));
+      c[k] = 8 * __shfl_sync(0xFFFFFFFFu, g, 4 * k + (lane >> 3)) + (lane & 7);
+      v[k] = c[k] < (uint32_t)p.cols ? load_bits<ELEM>(p.x, (int64_t)r[k] * p.ldx + c[k]) : 0u;
+    }
+    if (p.drop.cut) {
+      __syncwarp();  // the last draws have been read
+      *reinterpret_cast<uint4*>(&bits[w][8 * lane]) = drop_bits(key, g, row);
+      __syncwarp();
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const bool keep = p.drop.cut == 0 || bits[w][32 * k + lane] >= key.cutw >> 16;
+      if (c[k] < (uint32_t)p.cols) store_elem<ELEM>(p.y, (int64_t)r[k] * p.ldy + c[k], keep ? bits_value<ELEM>(v[k]) * p.scale : 0.f);
+    }
+  }
+}
+
+// Rows of whole groups of eight columns, one access of 16 or (fp32) 32 bytes each: a thread takes kItems of them at a time, so
+// that their loads are on their way together, a whole grid apart; row and group move on by additions. 16384 x 8192 bf16 95 us (two
+// items 100, eight 113, with streaming accesses 99), 84% of a copy: 2.2 of an SM's 4 instructions a clock, the wide
+// multiplications' pipe at 64%. 8192 x 8192 fp32 88 us, 91% (as two 16-byte accesses 110).
 template <int ELEM>
 __global__ void __launch_bounds__(256) dropout_vec_kernel(const DropoutParams p) {
   constexpr int kItems = ELEM == LNFP8_FP32 ? 2 : 4, W = ELEM == LNFP8_FP32 ? 2 : 1, ES = ElemSize<ELEM>::value;
@@ -76,9 +115,9 @@ __global__ void __launch_bounds__(256) dropout_vec_kernel(const DropoutParams p)
       at[i] = row;
       gr[i] = g;
       if (row < p.rows) {
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.x) + (row * p.ldx + 8 * (int64_t)g) * ES);
-#pragma unroll
-        for (int k = 0; k < W; ++k) u[i][k] = __ldcs(src + k);
+        const uint8_t* src = static_cast<const uint8_t*>(p.x) + (row * p.ldx + 8 * (int64_t)g) * ES;
+        if constexpr (W == 1) u[i][0] = *reinterpret_cast<const uint4*>(src);
+        else load32(src, reinterpret_cast<uint32_t*>(u[i]));
       }
       row += p.step_rows;
       g += p.step_groups;
@@ -102,9 +141,9 @@ __global__ void __launch_bounds__(256) dropout_vec_kernel(const DropoutParams p)
       }
       uint4 o[W];
       pack8<ELEM>(v, o);
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.y) + (at[i] * p.ldy + 8 * (int64_t)gr[i]) * ES);
-#pragma unroll
-      for (int k = 0; k < W; ++k) __stcs(dst + k, o[k]);
+      uint8_t* dst = static_cast<uint8_t*>(p.y) + (at[i] * p.ldy + 8 * (int64_t)gr[i]) * ES;
+      if constexpr (W == 1) *reinterpret_cast<uint4*>(dst) = o[0];
+      else store32(dst, reinterpret_cast<const uint32_t*>(o));
     }
   }
 }
@@ -127,10 +166,11 @@ lnfp8_status dropout_vec(const DropoutParams& q, cudaStream_t st) {
 
 template <int ELEM>
 lnfp8_status dropout_any(const DropoutParams& p, cudaStream_t st) {
-  const int64_t items = p.rows * ((p.cols + 255) / 256);
+  const bool narrow = p.cols <= 128;
+  const int64_t items = narrow ? (p.rows * ((p.cols + 7) / 8) + 31) / 32 : p.rows * ((p.cols + 255) / 256);
   const int64_t blocks = min64((items + kDropWarps - 1) / kDropWarps, (int64_t)num_sms() * 8);
   LaunchScope ls("dropout", st);
-  if (launch_pdl(dropout_any_kernel<ELEM>, dim3((unsigned)blocks), dim3(32 * kDropWarps), 0, st, p) != cudaSuccess)
+  if (launch_pdl(narrow ? dropout_narrow_kernel<ELEM> : dropout_any_kernel<ELEM>, dim3((unsigned)blocks), dim3(32 * kDropWarps), 0, st, p) != cudaSuccess)
     return check_launch("dropout_apply launch");
   return check_launch("dropout_apply");
 }
@@ -138,8 +178,9 @@ lnfp8_status dropout_any(const DropoutParams& p, cudaStream_t st) {
 template <int ELEM>
 lnfp8_status dropout(const DropoutParams& p, cudaStream_t st) {
   constexpr int es = ElemSize<ELEM>::value;
-  auto rows16 = [](const void* q, int64_t ld) { return reinterpret_cast<uintptr_t>(q) % 16 == 0 && ld * es % 16 == 0; };
-  return p.cols % 8 == 0 && rows16(p.x, p.ldx) && rows16(p.y, p.ldy) ? dropout_vec<ELEM>(p, st) : dropout_any<ELEM>(p, st);
+  // a group of eight columns is one access, of 16 or 32 bytes
+  auto whole = [](const void* q, int64_t ld) { return reinterpret_cast<uintptr_t>(q) % (8 * es) == 0 && ld % 8 == 0; };
+  return p.cols % 8 == 0 && whole(p.x, p.ldx) && whole(p.y, p.ldy) ? dropout_vec<ELEM>(p, st) : dropout_any<ELEM>(p, st);
 }
 
 }  // namespace

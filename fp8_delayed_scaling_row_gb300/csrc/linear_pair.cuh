@@ -100,18 +100,6 @@ __device__ __forceinline__ PairTile pair_locate(const PairParams& p, int t) {
   return {q, mn.x, mn.y, piece, kb0, min(r.num_kb, kb0 + r.kb_per_piece)};
 }
 
-// 32-byte accesses (sm_100 and later)
-__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
-               "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
-__device__ __forceinline__ void load32(const void* p, uint32_t* w) {
-  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-               : "l"(p)
-               : "memory");
-}
 // 32 columns n0.. of a row of 16-bit elements: those below N (a multiple of 8).
 __device__ __forceinline__ void store_row32(uint16_t* row, int n0, int N, int wide, const uint64_t* z, int f16) {
   uint32_t w[16];

@@ -64,6 +64,19 @@ __device__ __forceinline__ float round_elem(float v) {
   else return __bfloat162float(__float2bfloat16_rn(v));
 }
 
+// 32-byte accesses (sm_100 and later)
+__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
+               "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+__device__ __forceinline__ void load32(const void* p, uint32_t* w) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p)
+               : "memory");
+}
+
 // Packed fp32 pairs: the f32x2 instructions give two IEEE round-to-nearest results each.
 __device__ __forceinline__ uint64_t pk(float a, float b) {
   uint64_t r;
