@@ -24,6 +24,23 @@ namespace {
 // A column's parameter, or `none` where there is no such vector.
 __device__ __forceinline__ float param_or(const void* p, int elem, int c, float none) { return p ? load_elem_rt(p, elem, c) : none; }
 
+// The parameters of a thread's columns t, t + TPR, ... (tc in place of one it has not, n of them), all on their way together: the
+// choice of the type around each load would make it wait for the one before.
+template <int ELEM, int TPR, int NE>
+__device__ __forceinline__ void load_params_as(const void* p, int tc, int n, float* v) {
+  uint32_t b[NE];
+#pragma unroll
+  for (int i = 0; i < NE; ++i) b[i] = load_bits<ELEM>(p, tc + (i < n ? TPR * i : 0));
+#pragma unroll
+  for (int i = 0; i < NE; ++i) v[i] = bits_value<ELEM>(b[i]);
+}
+template <int TPR, int NE>
+__device__ __forceinline__ void load_params_any(const void* p, int elem, int tc, int n, float* v) {
+  if (elem == LNFP8_FP32) load_params_as<LNFP8_FP32, TPR, NE>(p, tc, n, v);
+  else if (elem == LNFP8_FP16) load_params_as<LNFP8_FP16, TPR, NE>(p, tc, n, v);
+  else load_params_as<LNFP8_BF16, TPR, NE>(p, tc, n, v);
+}
+
 // ------------------------------------------------------------ any width, any alignment
 // A group of TPR threads owns a row; thread t holds columns t, t + TPR, ..., so that a warp's value i is 32 neighbours:
 // four groups of draws. Lane q draws for group q of the warp's NE * 4, and the draws pass through shared memory. A column

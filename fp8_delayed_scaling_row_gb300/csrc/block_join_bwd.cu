@@ -33,7 +33,10 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 ? 2 : 1) joi
   constexpr int kThreads = TPR < 256 ? 256 : TPR, ES = ElemSize<ELEM>::value, GPB = kThreads / TPR;
   __shared__ float2 xch[2 * kThreads / 32];
   __shared__ __align__(16) uint16_t draws[kThreads / 32][32 * NE];
-  extern __shared__ float colred[];  // [D]: where several row groups add their column sums
+  // [D]: where several row groups add their column sums; or, from 1024 threads a row on, which have 64 registers each, [3][D] where
+  // the first three of them are kept from the start (2048 x 16384 bf16 with two RMS norms 428 -> XXX us)
+  extern __shared__ float colred[];
+  constexpr bool SACC = TPR >= 1024;
   pdl_wait();
   pdl_launch_dependents();
   const DropKey key = drop_key(p.drop);
@@ -45,16 +48,22 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 ? 2 : 1) joi
 #pragma unroll
   for (int k = 0; k < 4; ++k)
 #pragma unroll
-    for (int i = 0; i < NE; ++i) acc[k][i] = 0.f;
+    for (int i = 0; i < NE; ++i) {
+      acc[k][i] = 0.f;
+      if (SACC && k < 3 && i < n) colred[k * p.D + t + TPR * i] = 0.f;
+    }
+  auto add = [&](int k, int i, float v) {  // (zero where the thread has no column or no row)
+    if (!SACC || k == 3) acc[k][i] += v;
+    else if (i < n && (p.sums >> k & 1)) colred[k * p.D + t + TPR * i] += v;
+  };
   constexpr bool HOLD = TPR <= 512;  // the columns' factors stay in registers
   float fg[HOLD ? NE : 1], fa[HOLD ? NE : 1];
-  auto factor = [&](int c) { return p.scale * param_or(p.gate, p.param_elem, c, 1.f) * param_or(p.g1, p.param_elem, c, 1.f); };
   if constexpr (HOLD) {
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
       const int c = tc + (i < n ? TPR * i : 0);
       fg[i] = param_or(p.g2, p.param_elem, c, 0.f);
-      fa[i] = factor(c);
+      fa[i] = p.scale * param_or(p.gate, p.param_elem, c, 1.f) * param_or(p.g1, p.param_elem, c, 1.f);
     }
   }
   int turn = 0;
@@ -90,13 +99,15 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 ? 2 : 1) joi
       value(b0, q);
       value(b1, xh);
       const float rs = p.rs2[rowc], mu = p.layer ? p.mu2[rowc] : 0.f;
-      float s1 = 0.f, s2 = 0.f;
+      float s1 = 0.f, s2 = 0.f, f[HOLD ? 1 : NE];
+      if constexpr (!HOLD) load_params_any<TPR, NE>(p.g2, p.param_elem, tc, n, f);
 #pragma unroll
       for (int i = 0; i < NE; ++i) {
         xh[i] = active && i < n ? (xh[i] - mu) * rs : 0.f;
-        acc[0][i] = fmaf(q[i], xh[i], acc[0][i]);
-        acc[1][i] += q[i];
-        q[i] *= HOLD ? fg[HOLD ? i : 0] : load_elem_rt(p.g2, p.param_elem, tc + (i < n ? TPR * i : 0));
+        add(0, i, q[i] * xh[i]);
+        add(1, i, q[i]);
+        if constexpr (HOLD) q[i] *= fg[i];
+        else q[i] *= f[i];
         s1 += q[i];
         s2 = fmaf(q[i], xh[i], s2);
       }
@@ -144,13 +155,29 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 ? 2 : 1) joi
       }
 #pragma unroll
       for (int i = 0; i < NE; ++i) {
-        acc[2][i] = fmaf(d[i], xh[i], acc[2][i]);
-        acc[3][i] += d[i];
+        add(2, i, d[i] * xh[i]);
+        add(3, i, d[i]);
       }
     }
     float mu_ = 0.f, mux = 0.f;
+    if constexpr (HOLD) {
 #pragma unroll
-    for (int i = 0; i < NE; ++i) d[i] *= HOLD ? fa[HOLD ? i : 0] : factor(tc + (i < n ? TPR * i : 0));
+      for (int i = 0; i < NE; ++i) d[i] *= fa[i];
+    } else {
+      float f[NE];
+      if (p.gate) {
+        load_params_any<TPR, NE>(p.gate, p.param_elem, tc, n, f);
+#pragma unroll
+        for (int i = 0; i < NE; ++i) d[i] *= f[i];
+      }
+      if (p.g1) {
+        load_params_any<TPR, NE>(p.g1, p.param_elem, tc, n, f);
+#pragma unroll
+        for (int i = 0; i < NE; ++i) d[i] *= f[i];
+      }
+#pragma unroll
+      for (int i = 0; i < NE; ++i) d[i] *= p.scale;
+    }
     if (p.g1) {
       float s1 = 0.f, s2 = 0.f;
 #pragma unroll
@@ -181,7 +208,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 ? 2 : 1) joi
       for (int i = 0; i < NE; ++i) {
         const int c = t + TPR * i;
         if (c >= p.D) continue;
-        const float v = turn_g ? colred[c] + acc[k][i] : acc[k][i];
+        const float v = SACC && k < 3 ? colred[k * p.D + c] : turn_g ? colred[c] + acc[k][i] : acc[k][i];
         if (turn_g == GPB - 1) part[c] = v;
         else colred[c] = v;
       }
@@ -319,7 +346,9 @@ __global__ void __launch_bounds__(T, 1) join_bwd_vec_kernel(const JoinBwdParams 
       for (int k = 0; k < PP; ++k) v[k] = 0;
     }
   };
-  for (int64_t row0 = blockIdx.x; row0 < p.M; row0 += p.step, row += p.step) {
+  // groups of whole warps leave when they have no more rows; narrower ones go on while another of their warp has
+  constexpr bool LEAVE = TPR >= 32;
+  for (int64_t row0 = blockIdx.x; LEAVE ? row < p.M : row0 < p.M; row0 += p.step, row += p.step) {
     if constexpr (SHIFT) {
       cp_wait<P - 1>();
       group_meet<TPR>();  // the row is there for all, and all have left the slot that is filled next
@@ -328,9 +357,9 @@ __global__ void __launch_bounds__(T, 1) join_bwd_vec_kernel(const JoinBwdParams 
       issue(row + P * p.step, last);
       cp_wait<P>();
     }
-    const bool active = row < p.M;
+    const bool active = LEAVE || row < p.M;
     uint64_t d[NV][PP], xh[NV][PP];
-    uint32_t draws[NV][PP];
+    uint32_t draws[NV][PP];  // drawn ahead of the sums, beside whose exchanges they cost least
     if (p.drop.cut) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) word_draws<EPC>(key, (t + TPR * j) * EPC, (uint32_t)row, draws[j]);
@@ -372,7 +401,6 @@ __global__ void __launch_bounds__(T, 1) join_bwd_vec_kernel(const JoinBwdParams 
     uint64_t a1 = 0, a2 = 0;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const bool in = (t + TPR * j) * EPC < p.D;
       uint64_t r[PP];
       take(slot, 2, j, p.dh, p.lddh, r);
 #pragma unroll
@@ -382,7 +410,7 @@ __global__ void __launch_bounds__(T, 1) join_bwd_vec_kernel(const JoinBwdParams 
       }
       if constexpr (SHIFT) {
         if (p.dres) write_shifted<ELEM, TPR>(drp - t * 16, (t + TPR * j) * EPC, p.D, t, active, pack_word<ELEM>(d[j]));
-      } else if (p.dres && active && in) {
+      } else if (p.dres && active && (t + TPR * j) * EPC < p.D) {
         *reinterpret_cast<uint4*>(drp + TPR * j * 16) = pack_word<ELEM>(d[j]);
       }
       if (p.drop.cut) {
@@ -536,7 +564,7 @@ template <int ELEM, int TPR, int NE>
 lnfp8_status bwd_any_launch(const JoinBwdParams& p, int* blocks_out, cudaStream_t st) {
   constexpr auto kernel = join_bwd_any_kernel<ELEM, TPR, NE>;
   constexpr int threads = TPR < 256 ? 256 : TPR, gpb = threads / TPR;
-  constexpr size_t smem = gpb > 1 ? TPR * NE * sizeof(float) : 0;
+  constexpr size_t smem = TPR >= 1024 ? 3 * TPR * NE * sizeof(float) : gpb > 1 ? TPR * NE * sizeof(float) : 0;
   int bps = 1;
   const lnfp8_status s = kernel_setup<kernel>(threads, smem, &bps, "block_join_bwd: kernel set-up");
   if (s != LNFP8_OK) return s;
@@ -585,8 +613,8 @@ lnfp8_status bwd_vec_launch(const JoinBwdParams& p, int* blocks_out, cudaStream_
   if (launch_pdl(kernel, dim3((unsigned)blocks), dim3(T), S::SMEM, st, q) != cudaSuccess) return check_launch("block_join_bwd launch");
   return check_launch("block_join_bwd");
 }
-// Columns a thread: 16 of a 16-bit type (24 where a row of 16 would leave a quarter of the threads or more without any), 8
-// of fp32, whose words of four tensors fill the ring sooner.
+// Columns a thread: 16 of a 16-bit type (24 where those would leave a quarter of the threads or more without any: 16384 x 768
+// 45.6 -> 38 us), 8 of fp32, whose words of four tensors fill the ring sooner.
 template <int ELEM, bool FULL>
 lnfp8_status bwd_vec(const JoinBwdParams& p, int* blocks_out, cudaStream_t st) {
   constexpr int W = 2 * Word<ELEM>::EPC;

@@ -41,16 +41,13 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 ? 2 : 1) joi
   const int tc = min(t, p.D - 1);           // a column to load in place of those it has not
   constexpr bool HOLD = TPR <= 512;         // the columns' factors stay in registers
   float fa[HOLD ? NE : 1], fc[HOLD ? NE : 1], fg[HOLD ? NE : 1], fb[HOLD ? NE : 1];
-  auto factors = [&](int c, float& a, float& cc) {
-    const float f = p.scale * param_or(p.gate, p.param_elem, c, 1.f);
-    a = f * param_or(p.g1, p.param_elem, c, 1.f);
-    cc = p.b1 ? f * load_elem_rt(p.b1, p.param_elem, c) : 0.f;
-  };
   if constexpr (HOLD) {
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
       const int c = tc + (i < n ? TPR * i : 0);
-      factors(c, fa[i], fc[i]);
+      const float f = p.scale * param_or(p.gate, p.param_elem, c, 1.f);
+      fa[i] = f * param_or(p.g1, p.param_elem, c, 1.f);
+      fc[i] = f * param_or(p.b1, p.param_elem, c, 0.f);
       fg[i] = param_or(p.g2, p.param_elem, c, 0.f);
       fb[i] = param_or(p.b2, p.param_elem, c, 0.f);
     }
@@ -112,15 +109,34 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 ? 2 : 1) joi
       }
     }
     if (p.drop.cut) any_draws<NE>(bits, key, t, TPR, (uint32_t)row);
+    if constexpr (HOLD) {
+#pragma unroll
+      for (int i = 0; i < NE; ++i) v[i] = fmaf(v[i], fa[i], fc[i]);
+    } else {  // one vector after the other
+      float f[NE];
+      if (p.g1) {
+        load_params_any<TPR, NE>(p.g1, p.param_elem, tc, n, f);
+#pragma unroll
+        for (int i = 0; i < NE; ++i) v[i] *= f[i];
+      }
+      if (p.b1) {
+        load_params_any<TPR, NE>(p.b1, p.param_elem, tc, n, f);
+#pragma unroll
+        for (int i = 0; i < NE; ++i) v[i] += f[i];
+      }
+      if (p.gate) {
+        load_params_any<TPR, NE>(p.gate, p.param_elem, tc, n, f);
+#pragma unroll
+        for (int i = 0; i < NE; ++i) v[i] *= f[i];
+      }
+#pragma unroll
+      for (int i = 0; i < NE; ++i) v[i] *= p.scale;
+    }
     uint8_t* hr = static_cast<uint8_t*>(p.h) + (row * p.ldh + t) * ES;
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
-      float fai, fci;
-      if constexpr (HOLD) fai = fa[i], fci = fc[i];
-      else factors(tc + (i < n ? TPR * i : 0), fai, fci);
-      const float tv = fmaf(v[i], fai, fci);
       const bool keep = p.drop.cut == 0 || bits[32 * i + lane] >= p.drop.cut;
-      const float sum = r[i] + (keep ? tv : 0.f);
+      const float sum = r[i] + (keep ? v[i] : 0.f);
       v[i] = active && i < n ? round_elem<ELEM>(sum) : 0.f;
       if (active && i < n) store_elem<ELEM>(hr, TPR * i, v[i]);
     }
@@ -132,13 +148,23 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 ? 2 : 1) joi
       if (p.layer) p.mu2[row] = mu;
     }
     uint8_t* yr = static_cast<uint8_t*>(p.y) + (row * p.ldy + t) * ES;
+    if constexpr (HOLD) {
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      if (i >= n) continue;
-      const float gi = HOLD ? fg[HOLD ? i : 0] : load_elem_rt(p.g2, p.param_elem, t + TPR * i);
-      const float bi = HOLD ? fb[HOLD ? i : 0] : param_or(p.b2, p.param_elem, t + TPR * i, 0.f);
-      store_elem<ELEM>(yr, TPR * i, fmaf(v[i], gi, bi));
+      for (int i = 0; i < NE; ++i) v[i] = fmaf(v[i], fg[i], fb[i]);
+    } else {
+      float f[NE];
+      load_params_any<TPR, NE>(p.g2, p.param_elem, tc, n, f);
+#pragma unroll
+      for (int i = 0; i < NE; ++i) v[i] *= f[i];
+      if (p.b2) {
+        load_params_any<TPR, NE>(p.b2, p.param_elem, tc, n, f);
+#pragma unroll
+        for (int i = 0; i < NE; ++i) v[i] += f[i];
+      }
     }
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+      if (i < n) store_elem<ELEM>(yr, TPR * i, v[i]);
   }
 }
 
@@ -155,7 +181,7 @@ struct JoinFwdShape {
 template <int ELEM, int TPR, int NV, bool FULL, bool SHIFT>
 __global__ void __launch_bounds__(kVecThreads, 1) join_fwd_vec_kernel(const JoinFwdParams p) {
   using S = JoinFwdShape<ELEM, TPR, NV, FULL, SHIFT>;
-  constexpr int T = kVecThreads, GPB = T / TPR, RING = S::RING, P = RING - 1;
+  constexpr int T = kVecThreads, RING = S::RING, P = RING - 1;
   constexpr int EPC = Word<ELEM>::EPC, PP = EPC / 2, ES = ElemSize<ELEM>::value;
   __shared__ float2 xch[2 * T / 32];
   // [RING][2 tensors][NV][T] (SHIFT: [2 tensors][groups][words of a row]), then the factors: scale gate post_gamma, pre_gamma,
@@ -252,7 +278,9 @@ __global__ void __launch_bounds__(kVecThreads, 1) join_fwd_vec_kernel(const Join
     const float2 q = upk(q2);
     return rsqrt_nr(row_sum<TPR>(q.x + q.y, xch, turn) * inv_d + p.eps);
   };
-  for (int64_t row0 = blockIdx.x; row0 < p.M; row0 += p.step, row += p.step) {  // the same trip count for every group of the block
+  // groups of whole warps leave when they have no more rows; narrower ones go on while another of their warp has
+  constexpr bool LEAVE = TPR >= 32;
+  for (int64_t row0 = blockIdx.x; LEAVE ? row < p.M : row0 < p.M; row0 += p.step, row += p.step) {
     if constexpr (SHIFT) {
       cp_wait<P - 1>();
       group_meet<TPR>();  // the row is there for all, and all have left the slot that is filled next
@@ -261,16 +289,16 @@ __global__ void __launch_bounds__(kVecThreads, 1) join_fwd_vec_kernel(const Join
       issue(row + P * p.step, last);
       cp_wait<P>();
     }
-    const bool active = row < p.M;
+    const bool active = LEAVE || row < p.M;
     const uint32_t xm = SHIFT ? row_shift(static_cast<const uint8_t*>(p.x) + row * p.ldx * ES) : 0;
     const uint32_t rm = SHIFT ? row_shift(static_cast<const uint8_t*>(p.resid) + row * p.ldr * ES) : 0;
-    uint64_t v[NV][PP];
-    uint32_t draws[NV][PP];
+    uint64_t v[NV][PP], r[NV][PP];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       if constexpr (SHIFT) read_shifted<ELEM>(slot + j * WB, xm, (t + TPR * j) * EPC, p.D, v[j]);
       else unpack_word<ELEM>(lds16(slot + j * WB), v[j]);
     }
+    uint32_t draws[NV][PP];  // drawn ahead of the sums, beside whose exchanges they cost least
     if (p.drop.cut) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) word_draws<EPC>(key, (t + TPR * j) * EPC, (uint32_t)row, draws[j]);
@@ -287,14 +315,14 @@ __global__ void __launch_bounds__(kVecThreads, 1) join_fwd_vec_kernel(const Join
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      uint64_t f[PP], r[PP];
+      uint64_t f[PP];
       get_factors<TPR, NV, EPC>(fac, 0, j, f);
       if constexpr (SHIFT) {
 #pragma unroll
-        for (int k = 0; k < PP; ++k) r[k] = 0;
-        if (p.resid) read_shifted<ELEM>(slot + TB + j * WB, rm, (t + TPR * j) * EPC, p.D, r);
+        for (int k = 0; k < PP; ++k) r[j][k] = 0;
+        if (p.resid) read_shifted<ELEM>(slot + TB + j * WB, rm, (t + TPR * j) * EPC, p.D, r[j]);
       } else {
-        unpack_word<ELEM>(lds16(slot + TB + j * WB), r);
+        unpack_word<ELEM>(lds16(slot + TB + j * WB), r[j]);
       }
       if constexpr (FULL) {
         uint64_t b[PP];
@@ -305,12 +333,18 @@ __global__ void __launch_bounds__(kVecThreads, 1) join_fwd_vec_kernel(const Join
 #pragma unroll
         for (int k = 0; k < PP; ++k) v[j][k] = mul_2(mul_2(v[j][k], rs2), f[k]);
       }
-      if (p.drop.cut) {
+    }
+    if (p.drop.cut) {  // (branches around whole rows: inside the words' loops they would keep their loads and sums apart)
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
 #pragma unroll
         for (int k = 0; k < PP; ++k) v[j][k] = drop_pair(v[j][k], draws[j][k], key.cutw);
       }
+    }
 #pragma unroll
-      for (int k = 0; k < PP; ++k) v[j][k] = add_2(v[j][k], r[k]);  // zeros past D
+    for (int j = 0; j < NV; ++j) {
+#pragma unroll
+      for (int k = 0; k < PP; ++k) v[j][k] = add_2(v[j][k], r[j][k]);  // zeros past D
       const uint4 u = pack_word<ELEM>(v[j]);
       unpack_word<ELEM>(u, v[j]);  // normalised as it is kept
       if constexpr (SHIFT) write_shifted<ELEM, TPR>(hp - t * 16, (t + TPR * j) * EPC, p.D, t, active, u);
