@@ -460,9 +460,10 @@ __global__ void __launch_bounds__(T, 1) join_bwd_vec_kernel(const JoinBwdParams 
     slot = slot == base + P * SB ? base : slot + SB;
   }
   cp_wait<0>();
-  // column partials: the row groups of a warp by shuffles, then the others in turn in the ring's memory
+  // column partials: the row groups of a warp by shuffles, then the others' over the ring's memory, a column's in the groups' order
   float* red = reinterpret_cast<float*>(ring);
-  constexpr int TURNS = TPR < 32 ? T / 32 : GPB;
+  constexpr int TURNS = TPR < 32 ? T / 32 : GPB, COLS = TPR * NV * EPC;
+  static_assert(S::SMEM >= (size_t)TURNS * COLS * sizeof(float), "the column partials reuse the ring");
   if constexpr (TPR < 32) {
 #pragma unroll
     for (int i = 0; i < NS; ++i)
@@ -473,43 +474,36 @@ __global__ void __launch_bounds__(T, 1) join_bwd_vec_kernel(const JoinBwdParams 
 #pragma unroll
           for (int o = TPR; o < 32; o <<= 1) acc[i][j][k] = add_2(acc[i][j][k], __shfl_xor_sync(0xFFFFFFFFu, acc[i][j][k], o));
   }
+  const int mine = TPR < 32 ? (int)threadIdx.x >> 5 : g;
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
     constexpr int kPlace[4] = {0, 2, 1, 3};
     if (!(p.sums >> kPlace[i] & 1)) continue;
     float* part = p.part + ((int64_t)blockIdx.x * 4 + kPlace[i]) * p.D;
-#pragma unroll 1
-    for (int turn_g = 0; turn_g < TURNS; ++turn_g) {
-      if constexpr (TURNS > 1) __syncthreads();
-      if (TPR < 32 ? (int)threadIdx.x >> 5 != turn_g || (threadIdx.x & 31) >= TPR : g != turn_g) continue;
+    __syncthreads();  // the ring, or the sum before this one, has been read
+    if (TPR >= 32 || (threadIdx.x & 31) < TPR) {
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int c = (t + TPR * j) * EPC;
-        if (c >= p.D) continue;
+      for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int q = 0; q < PP / 2; ++q) {
           const float2 lo = upk(acc[i][j][2 * q]), hi = upk(acc[i][j][2 * q + 1]);
-          float4 v = make_float4(lo.x, lo.y, hi.x, hi.y);
-          if (turn_g > 0) {
-            const float4 o = *reinterpret_cast<const float4*>(red + c + 4 * q);
-            v = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
-          }
-          if (!SHIFT || turn_g < TURNS - 1) {
-            *reinterpret_cast<float4*>((turn_g == TURNS - 1 ? part : red) + c + 4 * q) = v;
-          } else {
-            const float e[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (c + 4 * q + k < p.D) part[c + 4 * q + k] = e[k];
-          }
+          *reinterpret_cast<float4*>(red + mine * COLS + (t + TPR * j) * EPC + 4 * q) = make_float4(lo.x, lo.y, hi.x, hi.y);
         }
-      }
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < p.D; c += T) {
+      float v = red[c];
+#pragma unroll
+      for (int q = 1; q < TURNS; ++q) v += red[q * COLS + c];
+      part[c] = v;
     }
   }
 }
 
 // The column sums of n partial rows in a fixed order (32 columns a block, warp w adds rows w, w + 32, ..., then the warps'
-// sums are added over the lanes), and what the gradients make of them.
+// sums are added over the lanes), and what the gradients make of them: blocks y = 0 those of the second norm, y = 1 of the first
+// and the gate. A few hundred rows are all latency: both sums' loads of five rows a warp, all that an SM's one block leaves, are on
+// their way together.
 struct JoinSumParams {
   const float* part;
   const void* g1;
@@ -524,37 +518,45 @@ struct JoinSumParams {
   float scale;  // of the last two sums
 };
 __global__ void __launch_bounds__(1024) join_sum_kernel(const JoinSumParams p) {
-  __shared__ float red[32][33];
+  __shared__ float red[2][32][33];
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane, cw = blockIdx.x * 32 + w;
-  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  const int first = 2 * blockIdx.y;  // of this block's two sums
+  const bool has[2] = {(p.sums >> first & 1) != 0, (p.sums >> first & 2) != 0};
+  float s[2] = {0.f, 0.f};
+  for (int i0 = w; i0 < p.n; i0 += 32 * 5) {
+    float v[2][5];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    if (!(p.sums >> k & 1)) continue;
-    if (c < p.D) {
-#pragma unroll 10
-      for (int i = w; i < p.n; i += 32) s[k] += __ldcs(p.part + ((int64_t)i * 4 + k) * p.D + c);
-    }
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int u = 0; u < 5; ++u) {
+        const int i = i0 + 32 * u;
+        v[k][u] = has[k] && c < p.D && i < p.n ? __ldcs(p.part + ((int64_t)i * 4 + first + k) * p.D + c) : 0.f;
+      }
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int u = 0; u < 5; ++u) s[k] += v[k][u];
   }
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    if (!(p.sums >> k & 1)) continue;
-    __syncthreads();
-    red[w][lane] = s[k];
-    __syncthreads();
-    s[k] = warp_sum(red[lane][w]);  // warp w: column w of the block
-  }
+  for (int k = 0; k < 2; ++k) red[k][w][lane] = s[k];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 2; ++k) s[k] = warp_sum(red[k][lane][w]);  // warp w: column w of the block
   if (lane != 0 || cw >= p.D) return;
-  if (p.dg2) p.dg2[cw] = s[0];
-  if (p.db2) p.db2[cw] = s[1];
+  if (blockIdx.y == 0) {
+    if (p.dg2) p.dg2[cw] = s[0];
+    if (p.db2) p.db2[cw] = s[1];
+    return;
+  }
   const float f = param_or(p.gate, p.param_elem, cw, 1.f);
-  s[2] *= p.scale;
-  s[3] *= p.scale;
-  if (p.dg1) p.dg1[cw] = f * s[2];
-  if (p.db1) p.db1[cw] = f * s[3];
-  if (p.dgate) p.dgate[cw] = p.g1 ? fmaf(load_elem_rt(p.g1, p.param_elem, cw), s[2], p.b1 ? load_elem_rt(p.b1, p.param_elem, cw) * s[3] : 0.f) : s[2];
+  s[0] *= p.scale;
+  s[1] *= p.scale;
+  if (p.dg1) p.dg1[cw] = f * s[0];
+  if (p.db1) p.db1[cw] = f * s[1];
+  if (p.dgate) p.dgate[cw] = p.g1 ? fmaf(load_elem_rt(p.g1, p.param_elem, cw), s[0], p.b1 ? load_elem_rt(p.b1, p.param_elem, cw) * s[1] : 0.f) : s[0];
 }
 
 // ------------------------------------------------------------ host side
@@ -595,7 +597,6 @@ template <int ELEM, int TPR, int NV, bool FULL, bool SHIFT = false>
 lnfp8_status bwd_vec_launch(const JoinBwdParams& p, int* blocks_out, cudaStream_t st) {
   constexpr int T = bwd_threads(ELEM, TPR, NV, FULL);
   using S = JoinBwdShape<ELEM, TPR, NV, FULL, T, SHIFT>;
-  static_assert(S::SMEM >= TPR * NV * Word<ELEM>::EPC * sizeof(float), "the column partials reuse the ring");
   constexpr auto kernel = join_bwd_vec_kernel<ELEM, TPR, NV, FULL, T, SHIFT>;
   const lnfp8_status s = kernel_setup<kernel>(T, S::SMEM, nullptr, "block_join_bwd: kernel set-up");
   if (s != LNFP8_OK) return s;
@@ -723,7 +724,7 @@ lnfp8_status block_join_bwd_launch(const lnfp8_block_join_bwd_args* a, cudaStrea
   q.sums = p.sums;
   q.scale = p.scale;
   LaunchScope ls("block_join_sum", st);
-  if (launch_pdl(join_sum_kernel, dim3((unsigned)((p.D + 31) / 32)), dim3(1024), 0, st, q) != cudaSuccess)
+  if (launch_pdl(join_sum_kernel, dim3((unsigned)((p.D + 31) / 32), 2), dim3(1024), 0, st, q) != cudaSuccess)
     return check_launch("block_join_bwd launch");
   return check_launch("block_join_bwd: column sums");
 }
