@@ -10,6 +10,8 @@
 // This header: what the two kernels of each direction (block_join_fwd.cu, block_join_bwd.cu) share.
 #pragma once
 
+#include <initializer_list>
+
 #include "common.cuh"
 #include "cp_async.cuh"
 #include "internal.h"
@@ -172,6 +174,16 @@ __device__ __forceinline__ void put_factors(uint4* at, int k, const void* a, con
     dst[i] = make_float4(v[0], v[1], v[2], v[3]);
   }
 }
+// A word's parameters as pairs, `none` where there is no such vector.
+template <int EPC>
+__device__ __forceinline__ void params_or(const void* p, int elem, int c, float none, uint64_t* v) {
+  if (p) {
+    load_params<EPC>(p, elem, c, v);
+  } else {
+#pragma unroll
+    for (int k = 0; k < EPC / 2; ++k) v[k] = pk(none, none);
+  }
+}
 template <int TPR, int NV, int EPC>
 __device__ __forceinline__ void get_factors(uint32_t at, int k, int j, uint64_t* v) {
   constexpr int Q = NV * EPC / 4;
@@ -183,6 +195,11 @@ __device__ __forceinline__ void get_factors(uint32_t at, int k, int j, uint64_t*
   }
 }
 
+inline bool vectors_aligned(std::initializer_list<const void*> v) {
+  for (const void* p : v)
+    if (reinterpret_cast<uintptr_t>(p) % 16) return false;
+  return true;
+}
 inline bool row_aligned(const void* p, int64_t ld, int es) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * es % 16 == 0; }
 
 }  // namespace

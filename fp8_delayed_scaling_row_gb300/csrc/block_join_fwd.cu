@@ -172,7 +172,9 @@ template <int ELEM, int TPR, int NV, bool FULL, bool SHIFT>
 struct JoinFwdShape {
   // bytes of a tensor's rows (x, residual): words of all threads, with SHIFT one more a row
   static constexpr int TENSOR = (kVecThreads * NV + (SHIFT ? kVecThreads / TPR : 0)) * 16;
-  static constexpr int SLOT = 2 * TENSOR, FACTORS = (FULL ? 4 : 2) * TPR * NV * Word<ELEM>::EPC * 4;
+  // Rows of more than 8192 columns: the factors would not fit beside two rows and are made of the vectors for each row.
+  static constexpr bool MAKE = TPR * NV * Word<ELEM>::EPC > 8192;
+  static constexpr int SLOT = 2 * TENSOR, FACTORS = MAKE ? 0 : (FULL ? 4 : 2) * TPR * NV * Word<ELEM>::EPC * 4;
   static constexpr int FIT = (kVecSmem - FACTORS) / SLOT, RING = FIT < 4 ? FIT : 4;
   static constexpr size_t SMEM = (size_t)RING * SLOT + FACTORS;
   static_assert(RING >= 2, "shared memory budget");
@@ -230,14 +232,35 @@ __global__ void __launch_bounds__(kVecThreads, 1) join_fwd_vec_kernel(const Join
   for (int k = 0; k < P; ++k) issue(row + k * p.step, mine + k * SB);
   drop_save(p.drop);
   const DropKey key = drop_key(p.drop);
-  uint4* fput = ring + RING * SB / 16;
-  put_factors<T, TPR, NV, EPC>(fput, 0, p.gate, p.g1, p.param_elem, p.scale, 1.f, p.D);
-  if (p.g2) put_factors<T, TPR, NV, EPC>(fput, 1, p.g2, nullptr, p.param_elem, 1.f, 0.f, p.D);
-  if constexpr (FULL) {
-    put_factors<T, TPR, NV, EPC>(fput, 2, p.b1, p.gate, p.param_elem, p.scale, 0.f, p.D);
-    put_factors<T, TPR, NV, EPC>(fput, 3, p.b2, nullptr, p.param_elem, 1.f, 0.f, p.D);
+  if constexpr (!S::MAKE) {
+    uint4* fput = ring + RING * SB / 16;
+    put_factors<T, TPR, NV, EPC>(fput, 0, p.gate, p.g1, p.param_elem, p.scale, 1.f, p.D);
+    if (p.g2) put_factors<T, TPR, NV, EPC>(fput, 1, p.g2, nullptr, p.param_elem, 1.f, 0.f, p.D);
+    if constexpr (FULL) {
+      put_factors<T, TPR, NV, EPC>(fput, 2, p.b1, p.gate, p.param_elem, p.scale, 0.f, p.D);
+      put_factors<T, TPR, NV, EPC>(fput, 3, p.b2, nullptr, p.param_elem, 1.f, 0.f, p.D);
+    }
+    __syncthreads();
   }
-  __syncthreads();
+  // factor array k's part of word j, zeros past D
+  auto factors = [&](int k, int j, uint64_t* f) {
+    if constexpr (!S::MAKE) {
+      get_factors<TPR, NV, EPC>(fac, k, j, f);
+    } else {
+      const int c = (t + TPR * j) * EPC, cc = c < p.D ? c : 0;
+      params_or<EPC>(k == 0 ? p.g1 : k == 1 ? p.g2 : k == 2 ? p.b1 : p.b2, p.param_elem, cc, k == 0 ? 1.f : 0.f, f);
+      if (k == 0 || k == 2) {
+        uint64_t a[PP];
+        params_or<EPC>(p.gate, p.param_elem, cc, 1.f, a);
+#pragma unroll
+        for (int i = 0; i < PP; ++i) f[i] = mul_2(mul_2(a[i], pk(p.scale, p.scale)), f[i]);
+      }
+      if (c >= p.D) {
+#pragma unroll
+        for (int i = 0; i < PP; ++i) f[i] = 0;
+      }
+    }
+  };
   const float inv_d = 1.0f / (float)p.D;
   int turn = 0;
   uint32_t slot = mine, last = mine + P * SB;  // the row's slot; the one read before it, filled next
@@ -292,7 +315,7 @@ __global__ void __launch_bounds__(kVecThreads, 1) join_fwd_vec_kernel(const Join
     const bool active = LEAVE || row < p.M;
     const uint32_t xm = SHIFT ? row_shift(static_cast<const uint8_t*>(p.x) + row * p.ldx * ES) : 0;
     const uint32_t rm = SHIFT ? row_shift(static_cast<const uint8_t*>(p.resid) + row * p.ldr * ES) : 0;
-    uint64_t v[NV][PP], r[NV][PP];
+    uint64_t v[NV][PP];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       if constexpr (SHIFT) read_shifted<ELEM>(slot + j * WB, xm, (t + TPR * j) * EPC, p.D, v[j]);
@@ -316,17 +339,10 @@ __global__ void __launch_bounds__(kVecThreads, 1) join_fwd_vec_kernel(const Join
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       uint64_t f[PP];
-      get_factors<TPR, NV, EPC>(fac, 0, j, f);
-      if constexpr (SHIFT) {
-#pragma unroll
-        for (int k = 0; k < PP; ++k) r[j][k] = 0;
-        if (p.resid) read_shifted<ELEM>(slot + TB + j * WB, rm, (t + TPR * j) * EPC, p.D, r[j]);
-      } else {
-        unpack_word<ELEM>(lds16(slot + TB + j * WB), r[j]);
-      }
+      factors(0, j, f);
       if constexpr (FULL) {
         uint64_t b[PP];
-        get_factors<TPR, NV, EPC>(fac, 2, j, b);
+        factors(2, j, b);
 #pragma unroll
         for (int k = 0; k < PP; ++k) v[j][k] = fma_2(mul_2(v[j][k], rs2), f[k], b[k]);
       } else {
@@ -343,8 +359,16 @@ __global__ void __launch_bounds__(kVecThreads, 1) join_fwd_vec_kernel(const Join
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+      uint64_t r[PP];
+      if constexpr (SHIFT) {
 #pragma unroll
-      for (int k = 0; k < PP; ++k) v[j][k] = add_2(v[j][k], r[j][k]);  // zeros past D
+        for (int k = 0; k < PP; ++k) r[k] = 0;
+        if (p.resid) read_shifted<ELEM>(slot + TB + j * WB, rm, (t + TPR * j) * EPC, p.D, r);
+      } else {
+        unpack_word<ELEM>(lds16(slot + TB + j * WB), r);
+      }
+#pragma unroll
+      for (int k = 0; k < PP; ++k) v[j][k] = add_2(v[j][k], r[k]);  // zeros past D
       const uint4 u = pack_word<ELEM>(v[j]);
       unpack_word<ELEM>(u, v[j]);  // normalised as it is kept
       if constexpr (SHIFT) write_shifted<ELEM, TPR>(hp - t * 16, (t + TPR * j) * EPC, p.D, t, active, u);
@@ -362,10 +386,10 @@ __global__ void __launch_bounds__(kVecThreads, 1) join_fwd_vec_kernel(const Join
       for (int j = 0; j < NV; ++j) {
         if (!SHIFT && (t + TPR * j) * EPC >= p.D) continue;
         uint64_t f[PP];
-        get_factors<TPR, NV, EPC>(fac, 1, j, f);
+        factors(1, j, f);
         if constexpr (FULL) {
           uint64_t b[PP];
-          get_factors<TPR, NV, EPC>(fac, 3, j, b);
+          factors(3, j, b);
 #pragma unroll
           for (int k = 0; k < PP; ++k) v[j][k] = fma_2(mul_2(v[j][k], rs2), f[k], b[k]);
         } else {
@@ -441,7 +465,10 @@ lnfp8_status fwd_vec(const JoinFwdParams& p, cudaStream_t st) {
     if (p.D <= 1536) return fwd_vec_launch<ELEM, 64, 3, FULL>(p, st);
   if (p.D <= 2048) return fwd_vec_launch<ELEM, 128, NV, FULL>(p, st);
   if constexpr (ELEM == LNFP8_FP32) return p.D <= 4096 ? fwd_vec_launch<ELEM, 256, NV, FULL>(p, st) : fwd_any<ELEM>(p, st);
-  else return p.D <= 4096 ? fwd_vec_launch<ELEM, 256, NV, FULL>(p, st) : fwd_vec_launch<ELEM, 512, NV, FULL>(p, st);
+  else
+    return p.D <= 4096   ? fwd_vec_launch<ELEM, 256, NV, FULL>(p, st)
+           : p.D <= 8192 ? fwd_vec_launch<ELEM, 512, NV, FULL>(p, st)
+                         : fwd_vec_launch<ELEM, 512, 2 * NV, FULL>(p, st);
 }
 template <int ELEM>
 lnfp8_status fwd_shift(const JoinFwdParams& p, cudaStream_t st) {
@@ -453,18 +480,19 @@ lnfp8_status fwd_shift(const JoinFwdParams& p, cudaStream_t st) {
   if (p.D <= 4096) return fwd_vec_launch<ELEM, 256, 2, true, true>(p, st);
   return fwd_vec_launch<ELEM, 512, 2, true, true>(p, st);
 }
-// Up to 8192 columns (4096 in fp32) rows on 16-byte boundaries take the kernel of 16-byte words, others of a 16-bit type its
-// form that shifts them (8191 x 1001 fp16 with a gate and two layer norms 44 us by single elements, 30 shifted; fp32, whose elements
-// are half the accesses a byte, 100000 x 203 67 and 96). All else goes by single elements.
+// Rows on 16-byte boundaries (in fp32 up to 4096 columns) take the kernel of 16-byte words, others of a 16-bit type its form that
+// shifts them, up to 8192 columns (8191 x 1001 fp16 with a gate and two layer norms 44 us by single elements, 30 shifted; fp32,
+// whose elements are half the accesses a byte, 100000 x 203 67 and 96). All else goes by single elements.
 template <int ELEM>
 lnfp8_status fwd(const JoinFwdParams& p, cudaStream_t st) {
   constexpr int es = ElemSize<ELEM>::value;
-  if (p.D > 8192) return fwd_any<ELEM>(p, st);
   const bool vec = p.D % 8 == 0 && row_aligned(p.x, p.ldx, es) && row_aligned(p.h, p.ldh, es) &&
-                   (!p.resid || row_aligned(p.resid, p.ldr, es)) && (!p.g2 || row_aligned(p.y, p.ldy, es));
+                   (!p.resid || row_aligned(p.resid, p.ldr, es)) && (!p.g2 || row_aligned(p.y, p.ldy, es)) &&
+                   (p.D <= 8192 || vectors_aligned({p.g1, p.b1, p.gate, p.g2, p.b2}));
   if (!vec) {
-    if constexpr (ELEM == LNFP8_FP32) return fwd_any<ELEM>(p, st);
-    else return fwd_shift<ELEM>(p, st);
+    if constexpr (ELEM != LNFP8_FP32)
+      if (p.D <= 8192) return fwd_shift<ELEM>(p, st);
+    return fwd_any<ELEM>(p, st);
   }
   const bool full = (p.layer && (p.g1 || p.g2)) || p.b1 || p.b2;
   return full ? fwd_vec<ELEM, true>(p, st) : fwd_vec<ELEM, false>(p, st);
