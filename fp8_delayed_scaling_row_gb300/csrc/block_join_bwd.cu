@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 ? 2 : 1) joi
   __shared__ float2 xch[2 * kThreads / 32];
   __shared__ __align__(16) uint16_t draws[kThreads / 32][32 * NE];
   // [D]: where several row groups add their column sums; or, from 1024 threads a row on, which have 64 registers each, [3][D] where
-  // the first three of them are kept from the start (2048 x 16384 bf16 with two RMS norms 428 -> XXX us)
+  // the first three of them are kept from the start (2048 x 16384 bf16 with two RMS norms 428 -> 401 us)
   extern __shared__ float colred[];
   constexpr bool SACC = TPR >= 1024;
   pdl_wait();

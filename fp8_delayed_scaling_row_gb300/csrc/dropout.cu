@@ -22,8 +22,9 @@ struct DropoutParams {
 
 constexpr int kDropWarps = 8;
 
-// Any width and alignment, bound by its accesses of one element (16384 x 8191 bf16 153 us, fp32 8192 x 8191 93): a warp takes 256 columns of a row. Lane q draws for the q-th group of eight, and the draws go
-// through shared memory to the lanes that hold the columns (32 neighbours at a time).
+// Any width and alignment, bound by its accesses of one element (16384 x 8191 bf16 153 us, fp32 8192 x 8191 93): a warp takes
+// 256 columns of a row. Lane q draws for the q-th group of eight, and the draws go through shared memory to the lanes that hold
+// the columns (32 neighbours at a time).
 template <int ELEM>
 __global__ void __launch_bounds__(32 * kDropWarps) dropout_any_kernel(const DropoutParams p) {
   __shared__ __align__(16) uint16_t bits[kDropWarps][256];
