@@ -84,9 +84,9 @@ __device__ __forceinline__ void word_draws(const DropKey& key, int c, uint32_t r
     w[1] = c & 4 ? u.w : u.y;
   }
 }
-// SHIFT: rows of any width on any boundary, the same words of eight columns. A row's aligned words go through the ring (words
-// that hold a byte of it: nothing outside is touched), the group meets before it reads them, and a thread cuts its columns out of
-// two neighbours. On the way out a thread joins the last columns of the lane below to its first ones, so that all but a warp's
+// SHIFT: rows of any width on any boundary, the same words of eight columns. A row's aligned words go through the ring (from the
+// word that holds its first byte to its last byte, and no further), the group meets before it reads them, and a thread cuts its
+// columns out of two neighbours. On the way out a thread joins the last columns of the lane below to its first ones, so that all but a warp's
 // and a row's ends leave as aligned words.
 __device__ __forceinline__ void shift_words(uint32_t* w, uint32_t bytes) {  // the 16 bytes of 32 from `bytes` < 16 on
 #pragma unroll
@@ -101,12 +101,14 @@ __device__ __forceinline__ uint32_t row_shift(const void* p) { return (uint32_t)
 template <int TPR, int NV>
 __device__ __forceinline__ void copy_row(uint32_t dst, const uint8_t* row, int bytes, int t) {
   const uint32_t m = row_shift(row);
-  const int words = (int)(m + bytes + 15) >> 4;
+  const int end = (int)m + bytes;
   const uint8_t* src = row - m;
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
-    if (t + TPR * j < words) cp16(dst + (t + TPR * j) * 16, src + (t + TPR * j) * 16);
-  if (t == 0 && TPR * NV < words) cp16(dst + TPR * NV * 16, src + TPR * NV * 16);
+  for (int j = 0; j < NV; ++j) {
+    const int at = (t + TPR * j) * 16;
+    if (at < end) cp16_part(dst + at, src + at, min(16, end - at));
+  }
+  if (t == 0 && TPR * NV * 16 < end) cp16_part(dst + TPR * NV * 16, src + TPR * NV * 16, end - TPR * NV * 16);
 }
 // Word w (columns c on) of a copied row, zeros from D on.
 template <int ELEM>

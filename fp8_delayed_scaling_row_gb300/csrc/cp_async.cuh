@@ -1,5 +1,5 @@
 // Asynchronous copies into shared memory and plain shared-memory loads by 32-bit address, for the
-// kernels that keep a ring of rows per thread (layernorm_rows.cu, linear.cu).
+// kernels that keep a ring of rows per thread (layernorm_rows.cu, linear.cu, block_join.cuh).
 #pragma once
 
 #include <stdint.h>
@@ -8,6 +8,10 @@ namespace lnfp8 {
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// The first n (1..16) bytes, zeros for the rest.
+__device__ __forceinline__ void cp16_part(uint32_t dst, const void* src, int n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 __device__ __forceinline__ void cp8(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");

@@ -1309,15 +1309,15 @@ _VECTORS = ("post_gamma", "post_beta", "gate", "pre_gamma", "pre_beta")
 
 
 def _vectors(D, dev, vectors):
-    """Checks the [D] vectors (as in _VECTORS) that are there, all of one type; returns its number."""
-    kind, elem, shape = None, 0, (D,)
-    for name, v in zip(_VECTORS, vectors):
-        if v is None:
-            continue
-        if kind is None:
-            kind, elem = v.dtype, _elem(v, name)
-        _flat(v, name, shape, kind, dev)
-    return elem
+    """Checks the [D] vectors (as in _VECTORS) that are there, all of one type; returns its number and their addresses."""
+    kind, elem, shape, at = None, 0, (D,), [None] * 5
+    for i, v in enumerate(vectors):
+        if v is not None:
+            if kind is None:
+                kind, elem = v.dtype, _elem(v, _VECTORS[i])
+            _flat(v, _VECTORS[i], shape, kind, dev)
+            at[i] = v.data_ptr()
+    return elem, at
 
 
 def block_join_fwd(x, residual=None, *, norm="rms", post_gamma=None, post_beta=None, gate=None, scale=1.0, p=0.0, rng=None,
@@ -1338,16 +1338,15 @@ def block_join_fwd(x, residual=None, *, norm="rms", post_gamma=None, post_beta=N
                                   rng=rng, site=site, pre_gamma=pre_gamma, pre_beta=pre_beta, eps=eps, h=h, y=y)
     ldx = _rows(x, "x", M, D, dt, dev)
     ldr = _rows(residual, "residual", M, D, dt, dev) if residual is not None else 0
-    pe = _vectors(D, dev, (post_gamma, post_beta, gate, pre_gamma, pre_beta))
-    drop, kept = _drop(p, rng, site, dev, True)
+    pe, (g1, b1, gt, g2, b2) = _vectors(D, dev, (post_gamma, post_beta, gate, pre_gamma, pre_beta))
+    drop, kept = _drop(p, rng, site, dev, True) if p != 0.0 else (_NO_DROP, None)
     ldh = ldy = D
     if h is None:
         h = _e((M, D), dt, device)
     else:
         ldh = _rows(h, "h", M, D, dt, dev)
-    post, pre = post_gamma is not None, pre_gamma is not None
-    m1 = r1 = m2 = r2 = None
-    if not pre:
+    m1 = r1 = m2 = r2 = yp = m1p = r1p = m2p = r2p = None
+    if g2 is None:
         if y is not None:
             raise ValueError("y without pre_gamma")
     else:
@@ -1356,17 +1355,21 @@ def block_join_fwd(x, residual=None, *, norm="rms", post_gamma=None, post_beta=N
         else:
             ldy = _rows(y, "y", M, D, dt, dev)
         r2 = _e((M,), torch.float32, device)
+        yp, r2p = y.data_ptr(), r2.data_ptr()
         if kind:
             m2 = _e((M,), torch.float32, device)
-    if post:
+            m2p = m2.data_ptr()
+    if g1 is not None:
         r1 = _e((M,), torch.float32, device)
+        r1p = r1.data_ptr()
         if kind:
             m1 = _e((M,), torch.float32, device)
-    a = CBlockJoinFwd(M, D, elem, pe, kind, eps, scale, x.data_ptr(), _ptr(residual), _ptr(post_gamma), _ptr(post_beta), _ptr(gate),
-                      _ptr(pre_gamma), _ptr(pre_beta), drop, h.data_ptr(), _ptr(y), _ptr(m1), _ptr(r1), _ptr(m2), _ptr(r2), ldx, ldr,
-                      ldh, ldy)
+            m1p = m1.data_ptr()
+    a = CBlockJoinFwd(M, D, elem, pe, kind, eps, scale, x.data_ptr(), None if residual is None else residual.data_ptr(), g1, b1, gt, g2,
+                      b2, drop, h.data_ptr(), yp, m1p, r1p, m2p, r2p, ldx, ldr, ldh, ldy)
     _check(_c_block_join_fwd(C.byref(a), _raw_stream(dev)))
-    return h, y, BlockJoinCtx(x if post or gate is not None else None, h if pre else None, norm, scale, p, kept, site, m1, r1, m2, r2)
+    return h, y, BlockJoinCtx(x if g1 is not None or gt is not None else None, h if g2 is not None else None, norm, scale, p, kept, site,
+                              m1, r1, m2, r2)
 
 
 @dataclass
@@ -1396,6 +1399,24 @@ def block_join_grads(M, D, *, dresidual=True, post_gamma=False, post_beta=False,
                           _e((_c_block_join_bwd_ws(M, D),), torch.uint8, device) if workspace else None)
 
 
+def _kept_stats(part, mu, rs, kind, M, dev):
+    """Addresses of a norm's statistics (the mean's None where the norm has none)."""
+    if rs is None or (kind and mu is None):
+        raise ValueError(f"the forward kept no statistics for {part}_gamma")
+    _flat(rs, f"ctx.{part}_rsigma", (M,), torch.float32, dev)
+    if not kind:
+        return None, rs.data_ptr()
+    _flat(mu, f"ctx.{part}_mu", (M,), torch.float32, dev)
+    return mu.data_ptr(), rs.data_ptr()
+
+
+def _kept_rows(name, row, M, D, dt, dev):
+    """Address and row stride of a norm's input."""
+    if row is None:
+        raise ValueError(f"ctx.{name} is missing")
+    return row.data_ptr(), _rows(row, "ctx." + name, M, D, dt, dev)
+
+
 def block_join_bwd(dh, dy, ctx: BlockJoinCtx, *, post_gamma=None, post_beta=None, gate=None, pre_gamma=None, pre_beta=None,
                    grads: BlockJoinGrads | None = None, stream=None) -> BlockJoinGrads:
     """Gradients of block_join_fwd from those of h (dh, None: zero) and of y (dy, with pre_gamma): dx, dresidual, and in fp32,
@@ -1414,36 +1435,23 @@ def block_join_bwd(dh, dy, ctx: BlockJoinCtx, *, post_gamma=None, post_beta=None
                                   pre_beta=pre_beta, grads=grads)
     lddh = _rows(dh, "dh", M, D, dt, dev) if dh is not None else 0
     lddy = _rows(dy, "dy", M, D, dt, dev) if dy is not None else 0
-    pe = _vectors(D, dev, (post_gamma, post_beta, gate, pre_gamma, pre_beta))
-    if pre_beta is not None and pre_gamma is None:
+    pe, (g1, b1, gt, g2, b2) = _vectors(D, dev, (post_gamma, post_beta, gate, pre_gamma, pre_beta))
+    if b2 is not None and g2 is None:
         raise ValueError("pre_beta without pre_gamma")
-    drop = _drop(ctx.p, ctx.rng, ctx.site, dev)[0]
-
-    def kept(part, gamma, row, name):
-        """Pointers of a norm's input and statistics, and its row stride."""
-        mu = rs = None
-        if gamma is not None:
-            rs, mu = getattr(ctx, part + "_rsigma"), getattr(ctx, part + "_mu")
-            if rs is None or (kind and mu is None):
-                raise ValueError(f"the forward kept no statistics for {part}_gamma")
-            _flat(rs, f"ctx.{part}_rsigma", (M,), torch.float32, dev)
-            if kind:
-                _flat(mu, f"ctx.{part}_mu", (M,), torch.float32, dev)
-        if row is None:
-            raise ValueError(f"ctx.{name} is missing")
-        return row.data_ptr(), _rows(row, "ctx." + name, M, D, dt, dev), _ptr(mu if kind else None), _ptr(rs)
-
+    drop = _drop(ctx.p, ctx.rng, ctx.site, dev)[0] if ctx.p != 0.0 else _NO_DROP
     xp = hp = m1 = r1 = m2 = r2 = None
     ldx = ldh = 0
-    if post_gamma is not None or gate is not None:
-        xp, ldx, m1, r1 = kept("post", post_gamma, ctx.x, "x")
-    if pre_gamma is not None:
-        hp, ldh, m2, r2 = kept("pre", pre_gamma, ctx.h, "h")
+    if g1 is not None:
+        m1, r1 = _kept_stats("post", ctx.post_mu, ctx.post_rsigma, kind, M, dev)
+    if g1 is not None or gt is not None:
+        xp, ldx = _kept_rows("x", ctx.x, M, D, dt, dev)
+    if g2 is not None:
+        m2, r2 = _kept_stats("pre", ctx.pre_mu, ctx.pre_rsigma, kind, M, dev)
+        hp, ldh = _kept_rows("h", ctx.h, M, D, dt, dev)
     lddx = lddr = D
     if grads is None:
-        grads = block_join_grads(M, D, post_gamma=post_gamma is not None, post_beta=post_beta is not None, gate=gate is not None,
-                                 pre_gamma=pre_gamma is not None, pre_beta=pre_beta is not None, dtype=dt, device=device,
-                                 workspace=False)
+        grads = block_join_grads(M, D, post_gamma=g1 is not None, post_beta=b1 is not None, gate=gt is not None, pre_gamma=g2 is not None,
+                                 pre_beta=b2 is not None, dtype=dt, device=device, workspace=False)
     else:
         lddx = _rows(grads.dx, "grads.dx", M, D, dt, dev)
         if grads.dresidual is not None:
@@ -1453,8 +1461,7 @@ def block_join_bwd(dh, dy, ctx: BlockJoinCtx, *, post_gamma=None, post_beta=None
                 _flat(getattr(grads, v), "grads." + v, (D,), torch.float32, dev)
     ws = grads.workspace
     ws = _e((_c_block_join_bwd_ws(M, D),), torch.uint8, device) if ws is None else _given_ws(ws, dev)
-    a = CBlockJoinBwd(M, D, elem, pe, kind, ctx.scale, _ptr(dh), _ptr(dy), xp, hp, _ptr(post_gamma), _ptr(post_beta), _ptr(gate),
-                      _ptr(pre_gamma), m1, r1, m2, r2, drop, grads.dx.data_ptr(), _ptr(grads.dresidual), _ptr(grads.dpost_gamma),
+    a = CBlockJoinBwd(M, D, elem, pe, kind, ctx.scale, _ptr(dh), _ptr(dy), xp, hp, g1, b1, gt, g2, m1, r1, m2, r2, drop, grads.dx.data_ptr(), _ptr(grads.dresidual), _ptr(grads.dpost_gamma),
                       _ptr(grads.dpost_beta), _ptr(grads.dgate), _ptr(grads.dpre_gamma), _ptr(grads.dpre_beta), ws.data_ptr(),
                       ws.nbytes, lddh, lddy, ldx, ldh, lddx, lddr)
     _check(_c_block_join_bwd(C.byref(a), _raw_stream(dev)))

@@ -209,6 +209,19 @@ def test_strided_unaligned_rows(L, C, dtype):
     run_both(L, 21, C, dtype, "rms", ("post_gamma", "gate", "pre_gamma"), 0.25, 1.0, strided=True)
 
 
+@pytest.mark.parametrize("C", [64, 2048, 8200, 12000])
+def test_vectors_on_odd_boundaries(L, C):
+    """Rows on 16-byte boundaries, vectors that start at any element."""
+    M, dt = 9, torch.bfloat16
+    x, r, dh, dy = (draw(M, C, dt, s) for s in (1, 2, 3, 4))
+    vec = {k: torch.cat((v[:3], v))[3:] for k, v in vectors(C, ALL, dt).items()}
+    assert all(v.data_ptr() % 16 for v in vec.values())
+    h, y, ctx = L.block_join_fwd(x, r, norm="layer", **vec)
+    keep = keep_of((M, C), 0.0, 0, 0, 0)
+    check_fwd(h, y, ctx, x, r, vec, "layer", 1.0, keep)
+    check_bwd(L.block_join_bwd(dh, dy, ctx, **vec), dh, dy, ctx, vec, keep)
+
+
 @pytest.mark.parametrize("C", [2048, 1001])
 def test_given_buffers_and_what_lies_around_them(L, C):
     M, dt = 45, torch.bfloat16
