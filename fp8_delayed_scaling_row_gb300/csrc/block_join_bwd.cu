@@ -500,6 +500,222 @@ __global__ void __launch_bounds__(T, 1) join_bwd_vec_kernel(const JoinBwdParams 
   }
 }
 
+// ------------------------------------------------------------ 16-bit rows of 8200 to 16384 columns
+// A block's 512 threads share a row, 32 columns each. The registers hold the sums of dy hhat and dt xhat and the gradient on its
+// way down; the normalised values are made again from the row's words in shared memory for each pass over them, and the sums for the betas
+// (FULL) live in shared memory too, where dh then has no place and is loaded behind the first pass. A tensor's words of the next row
+// are copied once the last pass over them is done. 2048 x 16384 bf16: XXX.
+template <int ELEM, bool FULL>
+struct JoinBwdWide {
+  static constexpr int T = 512, NV = 4, EPC = Word<ELEM>::EPC, TENSOR = NV * T * 16, TENSORS = FULL ? 3 : 4;  // dy, h, x, dh
+  static constexpr int SUMS = FULL ? 2 * T * NV * EPC * 4 : 0;
+  static constexpr size_t SMEM = TENSORS * TENSOR + SUMS;
+  static_assert(SMEM <= kVecSmem && EPC == 8, "shared memory budget");
+};
+template <int ELEM, bool FULL>
+__global__ void __launch_bounds__(512, 1) join_bwd_wide_kernel(const JoinBwdParams p) {
+  using S = JoinBwdWide<ELEM, FULL>;
+  constexpr int T = S::T, NV = S::NV, EPC = S::EPC, PP = EPC / 2;
+  constexpr uint32_t WB = T * 16, TB = S::TENSOR;
+  __shared__ float2 xch[2 * T / 32];
+  extern __shared__ uint4 ring[];  // [TENSORS][NV][T], then the sums of dy and dt, [2][2 NV quarters of 8][T] float4
+  const int t = threadIdx.x;
+  pdl_wait();
+  pdl_launch_dependents();
+  const uint32_t at = (uint32_t)__cvta_generic_to_shared(ring) + t * 16;
+  float4* sums = reinterpret_cast<float4*>(ring + S::TENSORS * TB / 16) + t;
+  const bool has_x = p.g1 != nullptr || p.gate != nullptr;
+  auto col = [&](int j) { return (t + T * j) * EPC; };
+  auto copy = [&](int i, const void* src, int64_t ld, int64_t row) {
+    const uint8_t* r = static_cast<const uint8_t*>(src) + row * ld * 2 + t * 16;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (col(j) < p.D) cp16(at + i * TB + j * WB, r + j * T * 16);
+  };
+  auto copy_first = [&](int64_t row) {  // what the first pass reads
+    if (row < p.M && p.g2) {
+      copy(0, p.dy, p.lddy, row);
+      copy(1, p.h, p.ldh, row);
+    }
+    cp_commit();
+  };
+  auto copy_second = [&](int64_t row) {
+    if (row < p.M) {
+      if (has_x) copy(2, p.x, p.ldx, row);
+      if constexpr (!FULL)
+        if (p.dh) copy(3, p.dh, p.lddh, row);
+    }
+    cp_commit();
+  };
+  // words past D and tensors that are not there hold zeros
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+#pragma unroll
+    for (int i = 0; i < S::TENSORS; ++i)
+      if (col(j) >= p.D || !(i < 2 ? p.g2 != nullptr : i == 2 ? has_x : p.dh != nullptr)) sts16_zero(at + i * TB + j * WB);
+    if constexpr (FULL)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) sums[(4 * j + q) * T] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  copy_first(blockIdx.x);
+  copy_second(blockIdx.x);
+  const DropKey key = drop_key(p.drop);
+  uint64_t acc[2][NV][PP];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int k = 0; k < PP; ++k) acc[i][j][k] = 0;
+  auto add_sums = [&](int which, int j, const uint64_t* v) {  // to the sums of dy (0) or dt (1)
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      float4* s = sums + (which * 2 * NV + 2 * j + q) * T;
+      const float2 a = upk(v[2 * q]), b = upk(v[2 * q + 1]);
+      const float4 o = *s;
+      *s = make_float4(o.x + a.x, o.y + a.y, o.z + b.x, o.w + b.y);
+    }
+  };
+  const float inv_d = 1.0f / (float)p.D;
+  int turn = 0;
+  auto means = [&](uint64_t a1, uint64_t a2, float rs, uint64_t& m1, uint64_t& m2) {
+    const float2 p2 = upk(a2);
+    const float f = -inv_d * rs;
+    if constexpr (FULL) {
+      const float2 p1 = upk(a1);
+      const float2 s = row_sum2<T>(p1.x + p1.y, p2.x + p2.y, xch, turn);
+      const float v = p.layer ? s.x * f : 0.f;
+      m1 = pk(v, v);
+      m2 = pk(s.y * f, s.y * f);
+    } else {
+      const float v = row_sum<T>(p2.x + p2.y, xch, turn) * f;
+      m1 = 0;
+      m2 = pk(v, v);
+    }
+  };
+  // a normalised word, tensor 1 (h) or 2 (x)
+  auto normal = [&](int i, int j, uint64_t rs2, uint64_t mu2, uint64_t* v) {
+    unpack_word<ELEM>(lds16(at + i * TB + j * WB), v);
+#pragma unroll
+    for (int k = 0; k < PP; ++k) {
+      if constexpr (FULL) v[k] = sub_2(v[k], mu2);
+      v[k] = mul_2(v[k], rs2);
+    }
+  };
+  for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x) {
+    const float rsb = p.g2 ? p.rs2[row] : 0.f, rsa = p.g1 ? p.rs1[row] : 1.f;
+    const float mub = FULL && p.layer && p.g2 ? p.mu2[row] : 0.f, mua = FULL && p.layer && p.g1 ? p.mu1[row] : 0.f;
+    const uint64_t rs2 = pk(rsb, rsb), mu2 = pk(mub, mub), rs1 = pk(rsa, rsa), mu1 = pk(mua, mua);
+    cp_wait<1>();
+    uint64_t a1 = 0, a2 = 0, m1 = 0, m2 = 0;
+    uint4 dhw[FULL ? NV : 1];
+    if (p.g2) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        uint64_t f[PP], q[PP], xh[PP];
+        load_params<EPC>(p.g2, p.param_elem, col(j) < p.D ? col(j) : 0, f);
+        unpack_word<ELEM>(lds16(at + j * WB), q);
+        normal(1, j, rs2, mu2, xh);
+        if constexpr (FULL) add_sums(0, j, q);
+#pragma unroll
+        for (int k = 0; k < PP; ++k) {
+          acc[0][j][k] = fma_2(q[k], xh[k], acc[0][j][k]);
+          q[k] = mul_2(q[k], f[k]);  // zero past D
+          if constexpr (FULL) a1 = add_2(a1, q[k]);
+          a2 = fma_2(q[k], xh[k], a2);
+        }
+      }
+    }
+    if constexpr (FULL) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        dhw[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (p.dh && col(j) < p.D) dhw[j] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.dh) + row * p.lddh + col(j));
+      }
+    }
+    if (p.g2) means(a1, a2, rsb, m1, m2);
+    cp_wait<0>();
+    uint64_t d[NV][PP];
+    a1 = a2 = 0;
+    uint16_t* dr = static_cast<uint16_t*>(p.dres) + row * p.lddres;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const bool in = col(j) < p.D;
+      const int c = in ? col(j) : 0;
+      uint64_t xh[PP], f[PP], g[PP];
+      unpack_word<ELEM>(lds16(at + j * WB), d[j]);
+      normal(1, j, rs2, mu2, xh);
+      params_or<EPC>(p.g2, p.param_elem, c, 0.f, f);
+      if constexpr (FULL) unpack_word<ELEM>(dhw[j], g);
+      else unpack_word<ELEM>(lds16(at + 3 * TB + j * WB), g);
+#pragma unroll
+      for (int k = 0; k < PP; ++k) {  // dH
+        if constexpr (FULL) g[k] = add_2(g[k], m1);
+        d[j][k] = fma_2(xh[k], m2, fma_2(mul_2(d[j][k], f[k]), rs2, g[k]));
+      }
+      if (p.dres && in) *reinterpret_cast<uint4*>(dr + c) = pack_word<ELEM>(d[j]);
+      if (p.drop.cut) {
+        uint32_t draws[PP];
+        word_draws<EPC>(key, c, (uint32_t)row, draws);
+#pragma unroll
+        for (int k = 0; k < PP; ++k) d[j][k] = drop_pair(d[j][k], draws[k], key.cutw);
+      }
+      normal(2, j, rs1, mu1, xh);
+#pragma unroll
+      for (int k = 0; k < PP; ++k) acc[1][j][k] = fma_2(d[j][k], xh[k], acc[1][j][k]);
+      if constexpr (FULL) add_sums(1, j, d[j]);
+      params_or<EPC>(p.gate, p.param_elem, c, 1.f, f);
+      params_or<EPC>(p.g1, p.param_elem, c, 1.f, g);
+#pragma unroll
+      for (int k = 0; k < PP; ++k) {
+        d[j][k] = in ? mul_2(d[j][k], mul_2(mul_2(f[k], pk(p.scale, p.scale)), g[k])) : 0;
+        if constexpr (FULL) a1 = add_2(a1, d[j][k]);
+        a2 = fma_2(d[j][k], xh[k], a2);
+      }
+    }
+    copy_first(row + gridDim.x);
+    if (p.g1) means(a1, a2, rsa, m1, m2);
+    uint16_t* o = static_cast<uint16_t*>(p.dx) + row * p.lddx;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (p.g1) {
+        uint64_t xh[PP];
+        normal(2, j, rs1, mu1, xh);
+#pragma unroll
+        for (int k = 0; k < PP; ++k) {
+          uint64_t v = mul_2(xh[k], m2);
+          if constexpr (FULL) v = add_2(v, m1);
+          d[j][k] = fma_2(d[j][k], rs1, v);
+        }
+      }
+      if (col(j) < p.D) *reinterpret_cast<uint4*>(o + col(j)) = pack_word<ELEM>(d[j]);
+    }
+    copy_second(row + gridDim.x);
+  }
+  cp_wait<0>();
+  // a column is one thread's: its sums are the block's
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {  // the places of `part`: dy hhat, dy, dt xhat, dt
+    if (!(p.sums >> i & 1)) continue;
+    float* part = p.part + ((int64_t)blockIdx.x * 4 + i) * p.D;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (col(j) >= p.D) continue;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        float4 v;
+        if (i == 0 || i == 2) {
+          const float2 a = upk(acc[i / 2][j][2 * q]), b = upk(acc[i / 2][j][2 * q + 1]);
+          v = make_float4(a.x, a.y, b.x, b.y);
+        } else {
+          v = FULL ? sums[((i / 2) * 2 * NV + 2 * j + q) * T] : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        *reinterpret_cast<float4*>(part + col(j) + 4 * q) = v;
+      }
+    }
+  }
+}
+
 // The column sums of n partial rows in a fixed order (32 columns a block, warp w adds rows w, w + 32, ..., then the warps'
 // sums are added over the lanes), and what the gradients make of them: blocks y = 0 those of the second norm, y = 1 of the first
 // and the gate. A few hundred rows are all latency: both sums' loads of five rows a warp, all that an SM's one block leaves, are on
@@ -631,6 +847,17 @@ lnfp8_status bwd_vec(const JoinBwdParams& p, int* blocks_out, cudaStream_t st) {
   if (p.D <= 256 * W) return bwd_vec_launch<ELEM, 256, 2, FULL>(p, blocks_out, st);
   return bwd_vec_launch<ELEM, 512, 2, FULL>(p, blocks_out, st);
 }
+template <int ELEM, bool FULL>
+lnfp8_status bwd_wide(const JoinBwdParams& p, int* blocks_out, cudaStream_t st) {
+  using S = JoinBwdWide<ELEM, FULL>;
+  constexpr auto kernel = join_bwd_wide_kernel<ELEM, FULL>;
+  const lnfp8_status s = kernel_setup<kernel>(S::T, S::SMEM, nullptr, "block_join_bwd: kernel set-up");
+  if (s != LNFP8_OK) return s;
+  const int64_t blocks = min64(p.M, num_sms());
+  *blocks_out = (int)blocks;
+  if (launch_pdl(kernel, dim3((unsigned)blocks), dim3(S::T), S::SMEM, st, p) != cudaSuccess) return check_launch("block_join_bwd launch");
+  return check_launch("block_join_bwd");
+}
 template <int ELEM>
 lnfp8_status bwd_shift(const JoinBwdParams& p, int* blocks_out, cudaStream_t st) {
   if (p.D <= 128) return bwd_vec_launch<ELEM, 8, 2, true, true>(p, blocks_out, st);
@@ -645,15 +872,17 @@ lnfp8_status bwd_shift(const JoinBwdParams& p, int* blocks_out, cudaStream_t st)
 template <int ELEM>
 lnfp8_status bwd(const JoinBwdParams& p, int* blocks_out, cudaStream_t st) {
   constexpr int es = ElemSize<ELEM>::value;
-  if (p.D > 1024 * Word<ELEM>::EPC) return bwd_any<ELEM>(p, blocks_out, st);
+  const bool wide = p.D > 1024 * Word<ELEM>::EPC;
   const bool vec = p.D % 8 == 0 && row_aligned(p.dx, p.lddx, es) && (!p.dres || row_aligned(p.dres, p.lddres, es)) &&
                    (!p.dh || row_aligned(p.dh, p.lddh, es)) && (!p.g2 || (row_aligned(p.dy, p.lddy, es) && row_aligned(p.h, p.ldh, es))) &&
-                   (!(p.g1 || p.gate) || row_aligned(p.x, p.ldx, es));
-  if (!vec) {
-    if constexpr (ELEM == LNFP8_FP32) return bwd_any<ELEM>(p, blocks_out, st);
-    else return bwd_shift<ELEM>(p, blocks_out, st);
-  }
+                   (!(p.g1 || p.gate) || row_aligned(p.x, p.ldx, es)) && (!wide || vectors_aligned({p.g1, p.gate, p.g2}));
   const bool full = (p.layer && (p.g1 || p.g2)) || (p.sums & 10);
+  if constexpr (ELEM == LNFP8_FP32) {
+    if (!vec || wide) return bwd_any<ELEM>(p, blocks_out, st);
+  } else {
+    if (!vec) return wide ? bwd_any<ELEM>(p, blocks_out, st) : bwd_shift<ELEM>(p, blocks_out, st);
+    if (wide) return full ? bwd_wide<ELEM, true>(p, blocks_out, st) : bwd_wide<ELEM, false>(p, blocks_out, st);
+  }
   return full ? bwd_vec<ELEM, true>(p, blocks_out, st) : bwd_vec<ELEM, false>(p, blocks_out, st);
 }
 

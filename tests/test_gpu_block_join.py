@@ -189,6 +189,13 @@ def test_shapes(L, M, C, dtype, norm, names, p):
     run_both(L, M, C, dtype, norm, SETS[names], p, 0.5 if names == "full" else 1.0)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("C", [250, 1001, 4104, 8200, 12000, 16384])
+@pytest.mark.parametrize("norm,names,p", [("rms", "rms_block", 0.1), ("layer", "full", 0.0), ("rms", "gate_post", 0.2)])
+def test_several_rows_to_a_block(L, C, dtype, norm, names, p):
+    run_both(L, 470, C, dtype, norm, SETS[names], p, 1.0)
+
+
 @pytest.mark.parametrize("C", [96, 1001, 2048, 8200])
 @pytest.mark.parametrize("names", list(SETS))
 @pytest.mark.parametrize("norm,p,residual", list(itertools.product(("rms", "layer"), (0.0, 0.2), (True, False))))
