@@ -233,6 +233,9 @@ __global__ void __launch_bounds__(T, 1) join_bwd_vec_kernel(const JoinBwdParams 
   using S = JoinBwdShape<ELEM, TPR, NV, FULL, T, SHIFT>;
   constexpr int GPB = T / TPR, RING = S::RING, P = RING - 1;
   constexpr int EPC = Word<ELEM>::EPC, PP = EPC / 2, ES = ElemSize<ELEM>::value;
+  // with four sums of 16 columns in 512 threads the normalised values are made again from the row's words wherever they are used
+  // (8192 x 4096 bf16 with layer norms, betas and a gate 127 -> 119 us, 4096 x 8192 131 -> 117)
+  constexpr bool REMAKE = FULL && !SHIFT && ELEM != LNFP8_FP32 && TPR >= 256;
   __shared__ float2 xch[2 * T / 32];
   extern __shared__ uint4 ring[];  // [RING][SLOT bytes], then the factors pre_gamma, scale gate post_gamma
   const int g = threadIdx.x / TPR, t = threadIdx.x % TPR;
@@ -346,6 +349,15 @@ __global__ void __launch_bounds__(T, 1) join_bwd_vec_kernel(const JoinBwdParams 
       for (int k = 0; k < PP; ++k) v[k] = 0;
     }
   };
+  // a normalised word, tensor 1 (h) or 3 (x)
+  auto normal = [&](uint32_t slot, int i, int j, uint64_t rs2, uint64_t mu2, uint64_t* v) {
+    take(slot, i, j, i == 1 ? p.h : p.x, i == 1 ? p.ldh : p.ldx, v);
+#pragma unroll
+    for (int k = 0; k < PP; ++k) {
+      if constexpr (FULL) v[k] = sub_2(v[k], mu2);
+      v[k] = mul_2(v[k], rs2);
+    }
+  };
   // groups of whole warps leave when they have no more rows; narrower ones go on while another of their warp has
   constexpr bool LEAVE = TPR >= 32;
   for (int64_t row0 = blockIdx.x; LEAVE ? row < p.M : row0 < p.M; row0 += p.step, row += p.step) {
@@ -358,35 +370,36 @@ __global__ void __launch_bounds__(T, 1) join_bwd_vec_kernel(const JoinBwdParams 
       cp_wait<P>();
     }
     const bool active = LEAVE || row < p.M;
-    uint64_t d[NV][PP], xh[NV][PP];
+    uint64_t d[NV][PP], xh[REMAKE ? 1 : NV][PP];
     uint32_t draws[NV][PP];  // drawn ahead of the sums, beside whose exchanges they cost least
     if (p.drop.cut) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) word_draws<EPC>(key, (t + TPR * j) * EPC, (uint32_t)row, draws[j]);
     }
-    uint64_t rs2 = 0, m1 = 0, m2 = 0;
+    uint64_t rs2 = 0, mu2 = 0, m1 = 0, m2 = 0;
     if (p.g2) {
       const float rs = __uint_as_float(lds4(slot + t4)), mu = FULL ? __uint_as_float(lds4(slot + t4 + 8 * T)) : 0.f;
       rs2 = pk(rs, rs);
-      const uint64_t mu2 = pk(mu, mu);
+      mu2 = pk(mu, mu);
       uint64_t a1 = 0, a2 = 0;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         uint64_t f[PP];
         get_factors<TPR, NV, EPC>(fac, 0, j, f);
+        uint64_t* v = xh[REMAKE ? 0 : j];
         take(slot, 0, j, p.dy, p.lddy, d[j]);
-        take(slot, 1, j, p.h, p.ldh, xh[j]);
+        take(slot, 1, j, p.h, p.ldh, v);
 #pragma unroll
         for (int k = 0; k < PP; ++k) {
-          if constexpr (FULL) xh[j][k] = sub_2(xh[j][k], mu2);
-          xh[j][k] = mul_2(xh[j][k], rs2);
+          if constexpr (FULL) v[k] = sub_2(v[k], mu2);
+          v[k] = mul_2(v[k], rs2);
           if (active) {
-            acc[0][j][k] = fma_2(d[j][k], xh[j][k], acc[0][j][k]);
+            acc[0][j][k] = fma_2(d[j][k], v[k], acc[0][j][k]);
             if constexpr (FULL) acc[2][j][k] = add_2(acc[2][j][k], d[j][k]);
           }
           d[j][k] = mul_2(d[j][k], f[k]);  // zero past D
           if constexpr (FULL) a1 = add_2(a1, d[j][k]);
-          a2 = fma_2(d[j][k], xh[j][k], a2);
+          a2 = fma_2(d[j][k], v[k], a2);
         }
       }
       means(a1, a2, rs, m1, m2);
@@ -394,19 +407,20 @@ __global__ void __launch_bounds__(T, 1) join_bwd_vec_kernel(const JoinBwdParams 
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int k = 0; k < PP; ++k) d[j][k] = xh[j][k] = 0;
+        for (int k = 0; k < PP; ++k) d[j][k] = xh[REMAKE ? 0 : j][k] = 0;
     }
     const float rs = __uint_as_float(lds4(slot + t4 + 4 * T)), mu = FULL ? __uint_as_float(lds4(slot + t4 + 12 * T)) : 0.f;
     const uint64_t rs1 = p.g1 ? pk(rs, rs) : pk(1.f, 1.f), mu1 = pk(mu, mu);
     uint64_t a1 = 0, a2 = 0;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      uint64_t r[PP];
+      uint64_t r[PP], *v = xh[REMAKE ? 0 : j];
       take(slot, 2, j, p.dh, p.lddh, r);
+      if constexpr (REMAKE) normal(slot, 1, j, rs2, mu2, v);
 #pragma unroll
       for (int k = 0; k < PP; ++k) {  // dH
         if constexpr (FULL) r[k] = add_2(r[k], m1);
-        d[j][k] = fma_2(xh[j][k], m2, fma_2(d[j][k], rs2, r[k]));
+        d[j][k] = fma_2(v[k], m2, fma_2(d[j][k], rs2, r[k]));
       }
       if constexpr (SHIFT) {
         if (p.dres) write_shifted<ELEM, TPR>(drp - t * 16, (t + TPR * j) * EPC, p.D, t, active, pack_word<ELEM>(d[j]));
@@ -420,13 +434,13 @@ __global__ void __launch_bounds__(T, 1) join_bwd_vec_kernel(const JoinBwdParams 
       uint64_t f[PP];
       get_factors<TPR, NV, EPC>(fac, 1, j, f);  // zeros past D
       if (has_x) {
-        take(slot, 3, j, p.x, p.ldx, xh[j]);
+        take(slot, 3, j, p.x, p.ldx, v);
 #pragma unroll
         for (int k = 0; k < PP; ++k) {
-          if constexpr (FULL) xh[j][k] = sub_2(xh[j][k], mu1);
-          xh[j][k] = mul_2(xh[j][k], rs1);
+          if constexpr (FULL) v[k] = sub_2(v[k], mu1);
+          v[k] = mul_2(v[k], rs1);
           if (active) {
-            acc[1][j][k] = fma_2(d[j][k], xh[j][k], acc[1][j][k]);
+            acc[1][j][k] = fma_2(d[j][k], v[k], acc[1][j][k]);
             if constexpr (FULL) acc[3][j][k] = add_2(acc[3][j][k], d[j][k]);
           }
         }
@@ -435,19 +449,22 @@ __global__ void __launch_bounds__(T, 1) join_bwd_vec_kernel(const JoinBwdParams 
       for (int k = 0; k < PP; ++k) {
         d[j][k] = mul_2(d[j][k], f[k]);
         if constexpr (FULL) a1 = add_2(a1, d[j][k]);
-        a2 = fma_2(d[j][k], xh[j][k], a2);
+        a2 = fma_2(d[j][k], v[k], a2);
       }
     }
     if (p.g1) {
       means(a1, a2, rs, m1, m2);
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
+      for (int j = 0; j < NV; ++j) {
+        uint64_t* v = xh[REMAKE ? 0 : j];
+        if constexpr (REMAKE) normal(slot, 3, j, rs1, mu1, v);
 #pragma unroll
         for (int k = 0; k < PP; ++k) {
-          uint64_t o = mul_2(xh[j][k], m2);
+          uint64_t o = mul_2(v[k], m2);
           if constexpr (FULL) o = add_2(o, m1);
           d[j][k] = fma_2(d[j][k], rs1, o);
         }
+      }
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -504,7 +521,8 @@ __global__ void __launch_bounds__(T, 1) join_bwd_vec_kernel(const JoinBwdParams 
 // A block's 512 threads share a row, 32 columns each. The registers hold the sums of dy hhat and dt xhat and the gradient on its
 // way down; the normalised values are made again from the row's words in shared memory for each pass over them, and the sums for the betas
 // (FULL) live in shared memory too, where dh then has no place and is loaded behind the first pass. A tensor's words of the next row
-// are copied once the last pass over them is done. 2048 x 16384 bf16: XXX.
+// are copied once the last pass over them is done. 2048 x 16384 bf16 119 us, 51% of a copy
+// (by single elements 348), with layer norms, betas and a gate 155 (371).
 template <int ELEM, bool FULL>
 struct JoinBwdWide {
   static constexpr int T = 512, NV = 4, EPC = Word<ELEM>::EPC, TENSOR = NV * T * 16, TENSORS = FULL ? 3 : 4;  // dy, h, x, dh
@@ -804,7 +822,8 @@ lnfp8_status bwd_any(const JoinBwdParams& p, int* blocks_out, cudaStream_t st) {
   return bwd_any_launch<ELEM, 1024, 16>(p, blocks_out, st);
 }
 
-// Threads of a block (one an SM): as many as leave each the registers of its sums and its row.
+// Threads of a block (one an SM): as many as leave each the registers of its sums and its row. 16384 x 2048 bf16 with layer norms,
+// betas and a gate 99 us in 384 threads, 107 to 112 in 512, which spill (four groups of 8 columns a thread: 145).
 constexpr int bwd_threads(int elem, int tpr, int nv, bool full) {
   if (nv == 3) return full ? 256 : 384;
   return full && elem != LNFP8_FP32 && tpr <= 128 ? 384 : 512;
