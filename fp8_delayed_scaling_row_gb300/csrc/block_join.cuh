@@ -61,7 +61,7 @@ __device__ __forceinline__ void any_draws(uint16_t* bits, const DropKey& key, in
 
 // ------------------------------------------------------------ 16-byte rows
 // D a multiple of 8 and rows on 16-byte boundaries: thread t of a row's TPR holds its 16-byte words t, t + TPR, ... (EPC
-// columns each), 16 columns in all, and copies (cp.async) the words of its next RING - 1 rows into its own slots of a ring in
+// columns each), 8 to 32 columns in all, and copies (cp.async) the words of its next RING - 1 rows into its own slots of a ring in
 // shared memory, so that the bytes in flight cost no registers. Bound by HBM: 16384 x 2048 bf16 with two RMS norms and dropout
 // forward 45 us (89% of what a copy of the bytes takes), backward 75 (80%; 71 without dropout). With layer norms, betas and a gate
 // 56 and 99 us (72%, 61%): four reductions a row and four column sums, whose registers leave 12 warps an SM.
@@ -86,8 +86,8 @@ __device__ __forceinline__ void word_draws(const DropKey& key, int c, uint32_t r
 }
 // SHIFT: rows of any width on any boundary, the same words of eight columns. A row's aligned words go through the ring (from the
 // word that holds its first byte to its last byte, and no further), the group meets before it reads them, and a thread cuts its
-// columns out of two neighbours. On the way out a thread joins the last columns of the lane below to its first ones, so that all but a warp's
-// and a row's ends leave as aligned words.
+// columns out of two neighbours. On the way out a thread joins the last columns of the lane below to its first ones, so that
+// all but a warp's and a row's ends leave as aligned words.
 __device__ __forceinline__ void shift_words(uint32_t* w, uint32_t bytes) {  // the 16 bytes of 32 from `bytes` < 16 on
 #pragma unroll
   for (int k = 0; k < 6; ++k) w[k] = bytes & 8 ? w[k + 2] : w[k];
