@@ -40,7 +40,7 @@ struct PairCfg {
   static constexpr int BAR_OFF = STAGES * STAGE;
   static constexpr int BIAS_OFF = BAR_OFF + 256;  // a chunk's 32 columns of the bias for each epilogue warp
   static constexpr int SMEM = 1024 + BIAS_OFF + 64 * kPairEpiWarps;
-  static constexpr int TMEM_COLS = 2 * BN;
+  static constexpr int TMEM_COLS = 2 * BN <= 128 ? 128 : 2 * BN <= 256 ? 256 : 512;  // a power of two
   static_assert(STAGES >= 4 && SMEM <= 232448, "shared memory budget");
 };
 

@@ -319,3 +319,21 @@ def test_refusals(L):
     g.workspace = g.workspace[:64]
     with pytest.raises(L.LnFp8Error, match="workspace"):
         L.linear_glu_bwd(draw(8, 32, torch.bfloat16, 3), x, w, L.LinearGluCtx(h=draw(8, 64, torch.bfloat16, 4)), grads=g)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,K,N", [(66, 512, 5504), (256, 2048, 5504), (333, 1024, 2736), (700, 768, 2048), (1536, 768, 1024), (1000, 1032, 2744), (300, 264, 5512)])
+def test_tiles_that_are_no_power_of_two(L, M, K, N, dtype):
+    """Sizes whose tiles hold 96 outputs, the last ones in part; rows behind and beside y stay as they were."""
+    x, w, b = whole(M, K, dtype, 1), whole(2 * N, K, dtype, 2), whole(1, 2 * N, dtype, 3)[0]
+    out = torch.full((M + 3, N + 8), 7.0, dtype=dtype, device="cuda")
+    y, ctx = L.linear_glu_fwd(x, w, b, act="none", save="h", y=out[:M, :N])
+    z = x.double() @ w.double().t() + b.double()
+    assert torch.equal(ctx.h, z.to(dtype))
+    assert torch.equal(y, (z[:, :N] * z[:, N:]).to(torch.float32).to(dtype))
+    assert bool((out[M:] == 7).all()) and bool((out[:, N:] == 7).all())
+    xr, wr, br = draw(M, K, dtype, 4), draw(2 * N, K, dtype, 5, 1.5 / math.sqrt(K)), draw(1, 2 * N, dtype, 6, 0.1)[0]
+    for act in ACTS:
+        y, ctx = L.linear_glu_fwd(xr, wr, br, act=act, save="h")
+        check_fwd(y, ctx.h, xr, wr, br, act)
+    L.sync_status()
