@@ -233,9 +233,8 @@ __global__ void __launch_bounds__(T, 1) join_bwd_vec_kernel(const JoinBwdParams 
   using S = JoinBwdShape<ELEM, TPR, NV, FULL, T, SHIFT>;
   constexpr int GPB = T / TPR, RING = S::RING, P = RING - 1;
   constexpr int EPC = Word<ELEM>::EPC, PP = EPC / 2, ES = ElemSize<ELEM>::value;
-  // with four sums of 16 columns in 512 threads the normalised values are made again from the row's words wherever they are used
-  // (8192 x 4096 bf16 with layer norms, betas and a gate 127 -> 119 us, 4096 x 8192 131 -> 117)
-  constexpr bool REMAKE = FULL && !SHIFT && ELEM != LNFP8_FP32 && TPR >= 256;
+  // with four sums of 32 columns the normalised values are made again from the row's words wherever they are used
+  constexpr bool REMAKE = NV == 4;
   __shared__ float2 xch[2 * T / 32];
   extern __shared__ uint4 ring[];  // [RING][SLOT bytes], then the factors pre_gamma, scale gate post_gamma
   const int g = threadIdx.x / TPR, t = threadIdx.x % TPR;
@@ -822,10 +821,12 @@ lnfp8_status bwd_any(const JoinBwdParams& p, int* blocks_out, cudaStream_t st) {
   return bwd_any_launch<ELEM, 1024, 16>(p, blocks_out, st);
 }
 
-// Threads of a block (one an SM): as many as leave each the registers of its sums and its row. 16384 x 2048 bf16 with layer norms,
-// betas and a gate 99 us in 384 threads, 107 to 112 in 512, which spill (four groups of 8 columns a thread: 145).
+// Threads of a block (one an SM): as many as leave each the registers of its sums and its row: 256 for 24 columns of four sums or
+// 32 whose normalised values are made again, 384 for 16 of four or 24 of two, 512 for less; groups of 96, 192 and 384 threads
+// fill 384.
 constexpr int bwd_threads(int elem, int tpr, int nv, bool full) {
-  if (nv == 3) return full ? 256 : 384;
+  if (nv >= 3) return full || tpr == 256 ? 256 : 384;
+  if (tpr % 96 == 0) return 384;
   return full && elem != LNFP8_FP32 && tpr <= 128 ? 384 : 512;
 }
 template <int ELEM, int TPR, int NV, bool FULL, bool SHIFT = false>
@@ -849,22 +850,41 @@ lnfp8_status bwd_vec_launch(const JoinBwdParams& p, int* blocks_out, cudaStream_
   if (launch_pdl(kernel, dim3((unsigned)blocks), dim3(T), S::SMEM, st, q) != cudaSuccess) return check_launch("block_join_bwd launch");
   return check_launch("block_join_bwd");
 }
-// Columns a thread: 16 of a 16-bit type (24 where those would leave a quarter of the threads or more without any: 16384 x 768
-// 45.6 -> 38 us), 8 of fp32, whose words of four tensors fill the ring sooner.
+// Columns a thread: 16 of a 16-bit type; 24 where those would leave a quarter of the threads or more without any (us, bf16:
+// 16384 x 768 46 -> 38, 16384 x 2560 with two RMS norms and dropout 137 -> 103, with two layer norms, betas and a gate 218 -> 127, 8192 x
+// 5120 148 -> 113 and 200 -> 128; groups of 192 and 384 threads of 16 columns 121, 150, 124 and 154); 32 with four sums, whose
+// row then costs each SM fewer exchanges and whose registers hold nothing twice (two layer norms, betas and a gate, 32 and 16 columns:
+// 65536 x 512 75 and 85, 16384 x 1024 44 and 53, 16384 x 2048 87 and 99, 8192 x 4096 91 and 119, 4096 x 8192 96 and 117; of two sums
+// 32 columns gain up to 7% at 4096 and lose a fifth at 8192).
 template <int ELEM, bool FULL>
-lnfp8_status bwd_vec(const JoinBwdParams& p, int* blocks_out, cudaStream_t st) {
-  constexpr int W = 2 * Word<ELEM>::EPC;
-  if (p.D <= 8 * W) return bwd_vec_launch<ELEM, 8, 2, FULL>(p, blocks_out, st);
-  if (p.D <= 16 * W) return bwd_vec_launch<ELEM, 16, 2, FULL>(p, blocks_out, st);
-  if (p.D <= 32 * W) return bwd_vec_launch<ELEM, 32, 2, FULL>(p, blocks_out, st);
-  if constexpr (ELEM != LNFP8_FP32)
-    if (p.D <= 48 * W) return bwd_vec_launch<ELEM, 32, 3, FULL>(p, blocks_out, st);
-  if (p.D <= 64 * W) return bwd_vec_launch<ELEM, 64, 2, FULL>(p, blocks_out, st);
-  if constexpr (ELEM != LNFP8_FP32)
-    if (p.D <= 96 * W) return bwd_vec_launch<ELEM, 64, 3, FULL>(p, blocks_out, st);
-  if (p.D <= 128 * W) return bwd_vec_launch<ELEM, 128, 2, FULL>(p, blocks_out, st);
-  if (p.D <= 256 * W) return bwd_vec_launch<ELEM, 256, 2, FULL>(p, blocks_out, st);
-  return bwd_vec_launch<ELEM, 512, 2, FULL>(p, blocks_out, st);
+lnfp8_status bwd_vec16(const JoinBwdParams& p, int* blocks_out, cudaStream_t st) {
+  if (p.D <= 128) return bwd_vec_launch<ELEM, 8, 2, FULL>(p, blocks_out, st);
+  if (p.D <= 256) return bwd_vec_launch<ELEM, 16, 2, FULL>(p, blocks_out, st);
+  if (p.D <= 512) return bwd_vec_launch<ELEM, FULL ? 16 : 32, FULL ? 4 : 2, FULL>(p, blocks_out, st);
+  if (p.D <= 32 * 24) return bwd_vec_launch<ELEM, 32, 3, FULL>(p, blocks_out, st);
+  if (p.D <= 1024) return bwd_vec_launch<ELEM, FULL ? 32 : 64, FULL ? 4 : 2, FULL>(p, blocks_out, st);
+  if (p.D <= 64 * 24) return bwd_vec_launch<ELEM, 64, 3, FULL>(p, blocks_out, st);
+  if (p.D <= 2048) return bwd_vec_launch<ELEM, FULL ? 64 : 128, FULL ? 4 : 2, FULL>(p, blocks_out, st);
+  if (p.D <= 128 * 24) return bwd_vec_launch<ELEM, 128, 3, FULL>(p, blocks_out, st);
+  if (p.D <= 4096) return bwd_vec_launch<ELEM, FULL ? 128 : 256, FULL ? 4 : 2, FULL>(p, blocks_out, st);
+  if (p.D <= 256 * 24) return bwd_vec_launch<ELEM, 256, 3, FULL>(p, blocks_out, st);
+  return bwd_vec_launch<ELEM, FULL ? 256 : 512, FULL ? 4 : 2, FULL>(p, blocks_out, st);
+}
+// Of fp32 8 columns, whose words of four tensors fill the ring sooner, with groups of 96, 192 and 384 threads too (two layer norms
+// and a gate: 8191 x 768 42 -> 37 us; with betas 8191 x 1280 75 -> 65, 8191 x 2560 154 -> 129).
+template <bool FULL>
+lnfp8_status bwd_vec32(const JoinBwdParams& p, int* blocks_out, cudaStream_t st) {
+  constexpr int E = LNFP8_FP32;
+  if (p.D <= 64) return bwd_vec_launch<E, 8, 2, FULL>(p, blocks_out, st);
+  if (p.D <= 128) return bwd_vec_launch<E, 16, 2, FULL>(p, blocks_out, st);
+  if (p.D <= 256) return bwd_vec_launch<E, 32, 2, FULL>(p, blocks_out, st);
+  if (p.D <= 512) return bwd_vec_launch<E, 64, 2, FULL>(p, blocks_out, st);
+  if (p.D <= 768) return bwd_vec_launch<E, 96, 2, FULL>(p, blocks_out, st);
+  if (p.D <= 1024) return bwd_vec_launch<E, 128, 2, FULL>(p, blocks_out, st);
+  if (p.D <= 1536) return bwd_vec_launch<E, 192, 2, FULL>(p, blocks_out, st);
+  if (p.D <= 2048) return bwd_vec_launch<E, 256, 2, FULL>(p, blocks_out, st);
+  if (p.D <= 384 * 8) return bwd_vec_launch<E, 384, 2, FULL>(p, blocks_out, st);
+  return bwd_vec_launch<E, 512, 2, FULL>(p, blocks_out, st);
 }
 template <int ELEM, bool FULL>
 lnfp8_status bwd_wide(const JoinBwdParams& p, int* blocks_out, cudaStream_t st) {
@@ -902,7 +922,8 @@ lnfp8_status bwd(const JoinBwdParams& p, int* blocks_out, cudaStream_t st) {
     if (!vec) return wide ? bwd_any<ELEM>(p, blocks_out, st) : bwd_shift<ELEM>(p, blocks_out, st);
     if (wide) return full ? bwd_wide<ELEM, true>(p, blocks_out, st) : bwd_wide<ELEM, false>(p, blocks_out, st);
   }
-  return full ? bwd_vec<ELEM, true>(p, blocks_out, st) : bwd_vec<ELEM, false>(p, blocks_out, st);
+  if constexpr (ELEM == LNFP8_FP32) return full ? bwd_vec32<true>(p, blocks_out, st) : bwd_vec32<false>(p, blocks_out, st);
+  else return full ? bwd_vec16<ELEM, true>(p, blocks_out, st) : bwd_vec16<ELEM, false>(p, blocks_out, st);
 }
 
 }  // namespace

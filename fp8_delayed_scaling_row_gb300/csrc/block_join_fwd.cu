@@ -465,10 +465,19 @@ lnfp8_status fwd_vec(const JoinFwdParams& p, cudaStream_t st) {
     if (p.D <= 1536) return fwd_vec_launch<ELEM, 64, 3, FULL>(p, st);
   if (p.D <= 2048) return fwd_vec_launch<ELEM, 128, NV, FULL>(p, st);
   if constexpr (ELEM == LNFP8_FP32) return p.D <= 4096 ? fwd_vec_launch<ELEM, 256, NV, FULL>(p, st) : fwd_any<ELEM>(p, st);
-  else
+  else {
+    // 24 columns a thread there too, where 16 would leave a quarter of the threads or more without any, but for rows whose work
+    // is one RMS norm and no draws at most, which wait for memory alone. us, 24 and 16 columns: 16384 x 2560 bf16 with two layer norms,
+    // betas and a gate 73 and 108, two RMS norms and dropout 61 and 84, one layer norm with betas and dropout 68 and 91, one RMS
+    // norm 61 and 53; 8192 x 5120 80 and 120, 66 and 97, 71 and 99, 60 and 56
+    if (FULL || p.g1 || p.drop.cut) {
+      if (p.D > 2048 && p.D <= 128 * 24) return fwd_vec_launch<ELEM, 128, 3, FULL>(p, st);
+      if (p.D > 4096 && p.D <= 256 * 24) return fwd_vec_launch<ELEM, 256, 3, FULL>(p, st);
+    }
     return p.D <= 4096   ? fwd_vec_launch<ELEM, 256, NV, FULL>(p, st)
            : p.D <= 8192 ? fwd_vec_launch<ELEM, 512, NV, FULL>(p, st)
                          : fwd_vec_launch<ELEM, 512, 2 * NV, FULL>(p, st);
+  }
 }
 template <int ELEM>
 lnfp8_status fwd_shift(const JoinFwdParams& p, cudaStream_t st) {

@@ -196,6 +196,14 @@ def test_several_rows_to_a_block(L, C, dtype, norm, names, p):
     run_both(L, 470, C, dtype, norm, SETS[names], p, 1.0)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("C", [520, 640, 776, 1032, 1280, 2056, 2560, 3064, 4104, 5120, 6136, 6152])
+@pytest.mark.parametrize("norm,names,p", [("rms", "rms_block", 0.1), ("layer", "full", 0.0), ("layer", "gate_pre", 0.2)])
+def test_rows_shared_by_threads_that_are_no_power_of_two(L, C, dtype, norm, names, p):
+    """Both borders of the widths between powers of two, several rows to a group of threads and one group without any."""
+    run_both(L, 701, C, dtype, norm, SETS[names], p, 1.0)
+
+
 @pytest.mark.parametrize("C", [96, 1001, 2048, 8200])
 @pytest.mark.parametrize("names", list(SETS))
 @pytest.mark.parametrize("norm,p,residual", list(itertools.product(("rms", "layer"), (0.0, 0.2), (True, False))))
