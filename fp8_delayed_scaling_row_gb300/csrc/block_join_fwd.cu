@@ -452,32 +452,48 @@ lnfp8_status fwd_vec_launch(const JoinFwdParams& p, cudaStream_t st) {
   if (launch_pdl(kernel, dim3((unsigned)blocks), dim3(kVecThreads), S::SMEM, st, q) != cudaSuccess) return check_launch("block_join_fwd launch");
   return check_launch("block_join_fwd");
 }
+// Columns a thread: 16; 24 (16-bit types) where those would leave a quarter of the threads or more without any; 32 where a row is
+// much work, whose exchanges then cost an SM less. Rows of one RMS norm without draws wait for memory alone and keep 16 from 2048
+// columns on. us, bf16, 16 columns and the ones taken:
+//                                           16384 x 1024  16384 x 2048  16384 x 2560  8192 x 4096  8192 x 5120  4096 x 8192
+//   two layer norms, betas and a gate       31 and 27     56 and 47     108 and 72    64 and 50    120 and 80   71 (16)
+//   one layer norm with betas, dropout      27 and 26     50 and 47     91 and 68     54 and 48    99 and 70    57 (16)
+//   two RMS norms, dropout                  24 (16)       45 (16; 48)   84 and 60     48 (16; 47)  97 and 66    57 and 49
+//   two RMS norms                           24 (16)       47 (16; 48)   65 and 62     46 (16; 49)  75 and 60    45 (16; 51)
+//   one RMS norm                            23 (16)       46 (16; 47)   53 (16; 61)   47 (16; 47)  56 (16; 60)  47 (16; 48)
+// (in brackets the columns taken, then the time of the others). One layer norm without draws keeps 16 too (2048 columns 44, 48).
 template <int ELEM, bool FULL>
-lnfp8_status fwd_vec(const JoinFwdParams& p, cudaStream_t st) {
-  constexpr int NV = 16 / Word<ELEM>::EPC;
-  if (p.D <= 128) return fwd_vec_launch<ELEM, 8, NV, FULL>(p, st);
-  if (p.D <= 256) return fwd_vec_launch<ELEM, 16, NV, FULL>(p, st);
-  if (p.D <= 512) return fwd_vec_launch<ELEM, 32, NV, FULL>(p, st);
-  if constexpr (ELEM != LNFP8_FP32)
-    if (p.D <= 768) return fwd_vec_launch<ELEM, 32, 3, FULL>(p, st);
-  if (p.D <= 1024) return fwd_vec_launch<ELEM, 64, NV, FULL>(p, st);
-  if constexpr (ELEM != LNFP8_FP32)
-    if (p.D <= 1536) return fwd_vec_launch<ELEM, 64, 3, FULL>(p, st);
-  if (p.D <= 2048) return fwd_vec_launch<ELEM, 128, NV, FULL>(p, st);
-  if constexpr (ELEM == LNFP8_FP32) return p.D <= 4096 ? fwd_vec_launch<ELEM, 256, NV, FULL>(p, st) : fwd_any<ELEM>(p, st);
-  else {
-    // 24 columns a thread there too, where 16 would leave a quarter of the threads or more without any, but for rows whose work
-    // is one RMS norm and no draws at most, which wait for memory alone. us, 24 and 16 columns: 16384 x 2560 bf16 with two layer norms,
-    // betas and a gate 73 and 108, two RMS norms and dropout 61 and 84, one layer norm with betas and dropout 68 and 91, one RMS
-    // norm 61 and 53; 8192 x 5120 80 and 120, 66 and 97, 71 and 99, 60 and 56
-    if (FULL || p.g1 || p.drop.cut) {
-      if (p.D > 2048 && p.D <= 128 * 24) return fwd_vec_launch<ELEM, 128, 3, FULL>(p, st);
-      if (p.D > 4096 && p.D <= 256 * 24) return fwd_vec_launch<ELEM, 256, 3, FULL>(p, st);
-    }
-    return p.D <= 4096   ? fwd_vec_launch<ELEM, 256, NV, FULL>(p, st)
-           : p.D <= 8192 ? fwd_vec_launch<ELEM, 512, NV, FULL>(p, st)
-                         : fwd_vec_launch<ELEM, 512, 2 * NV, FULL>(p, st);
-  }
+lnfp8_status fwd_vec16(const JoinFwdParams& p, cudaStream_t st) {
+  const bool some = FULL || p.g1 || p.drop.cut, much = (p.g1 && p.drop.cut) || (FULL && (p.g1 || p.drop.cut));
+  if (p.D <= 128) return fwd_vec_launch<ELEM, 8, 2, FULL>(p, st);
+  if (p.D <= 256) return fwd_vec_launch<ELEM, 16, 2, FULL>(p, st);
+  if (p.D <= 512) return fwd_vec_launch<ELEM, 32, 2, FULL>(p, st);
+  if (p.D <= 32 * 24) return fwd_vec_launch<ELEM, 32, 3, FULL>(p, st);
+  if constexpr (FULL)
+    if (much && p.D <= 1024) return fwd_vec_launch<ELEM, 32, 4, FULL>(p, st);
+  if (p.D <= 1024) return fwd_vec_launch<ELEM, 64, 2, FULL>(p, st);
+  if (p.D <= 64 * 24) return fwd_vec_launch<ELEM, 64, 3, FULL>(p, st);
+  if constexpr (FULL)
+    if (much && p.D <= 2048) return fwd_vec_launch<ELEM, 64, 4, FULL>(p, st);
+  if (p.D <= 2048) return fwd_vec_launch<ELEM, 128, 2, FULL>(p, st);
+  if (some && p.D <= 128 * 24) return fwd_vec_launch<ELEM, 128, 3, FULL>(p, st);
+  if constexpr (FULL)
+    if (much && p.D <= 4096) return fwd_vec_launch<ELEM, 128, 4, FULL>(p, st);
+  if (p.D <= 4096) return fwd_vec_launch<ELEM, 256, 2, FULL>(p, st);
+  if (some && p.D <= 256 * 24) return fwd_vec_launch<ELEM, 256, 3, FULL>(p, st);
+  if constexpr (!FULL)  // (four factors a column would not fit beside two rows)
+    if (much && p.D <= 8192) return fwd_vec_launch<ELEM, 256, 4, FULL>(p, st);
+  return p.D <= 8192 ? fwd_vec_launch<ELEM, 512, 2, FULL>(p, st) : fwd_vec_launch<ELEM, 512, 4, FULL>(p, st);
+}
+template <bool FULL>
+lnfp8_status fwd_vec32(const JoinFwdParams& p, cudaStream_t st) {
+  constexpr int E = LNFP8_FP32;
+  if (p.D <= 128) return fwd_vec_launch<E, 8, 4, FULL>(p, st);
+  if (p.D <= 256) return fwd_vec_launch<E, 16, 4, FULL>(p, st);
+  if (p.D <= 512) return fwd_vec_launch<E, 32, 4, FULL>(p, st);
+  if (p.D <= 1024) return fwd_vec_launch<E, 64, 4, FULL>(p, st);
+  if (p.D <= 2048) return fwd_vec_launch<E, 128, 4, FULL>(p, st);
+  return p.D <= 4096 ? fwd_vec_launch<E, 256, 4, FULL>(p, st) : fwd_any<E>(p, st);
 }
 template <int ELEM>
 lnfp8_status fwd_shift(const JoinFwdParams& p, cudaStream_t st) {
@@ -504,7 +520,8 @@ lnfp8_status fwd(const JoinFwdParams& p, cudaStream_t st) {
     return fwd_any<ELEM>(p, st);
   }
   const bool full = (p.layer && (p.g1 || p.g2)) || p.b1 || p.b2;
-  return full ? fwd_vec<ELEM, true>(p, st) : fwd_vec<ELEM, false>(p, st);
+  if constexpr (ELEM == LNFP8_FP32) return full ? fwd_vec32<true>(p, st) : fwd_vec32<false>(p, st);
+  else return full ? fwd_vec16<ELEM, true>(p, st) : fwd_vec16<ELEM, false>(p, st);
 }
 
 }  // namespace

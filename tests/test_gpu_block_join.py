@@ -197,6 +197,14 @@ def test_several_rows_to_a_block(L, C, dtype, norm, names, p):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("C", [264, 512, 776, 1024, 1544, 2048, 3080, 4096, 6152, 7168, 8192])
+@pytest.mark.parametrize("norm,names,p", [("rms", "rms_block", 0.1), ("layer", "full", 0.0), ("layer", "full", 0.1), ("layer", "gate_pre", 0.0)])
+def test_columns_a_thread(L, C, dtype, norm, names, p):
+    """Both borders of the widths with 32 columns a thread where a row is much work, and parts with which it is not."""
+    run_both(L, 701, C, dtype, norm, SETS[names], p, 1.0)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("C", [520, 640, 776, 1032, 1280, 2056, 2560, 3064, 4104, 5120, 6136, 6152])
 @pytest.mark.parametrize("norm,names,p", [("rms", "rms_block", 0.1), ("layer", "full", 0.0), ("layer", "gate_pre", 0.2)])
 def test_rows_shared_by_threads_that_are_no_power_of_two(L, C, dtype, norm, names, p):
