@@ -186,8 +186,8 @@ __global__ void __launch_bounds__(kVecThreads, 1) join_fwd_vec_kernel(const Join
   constexpr int T = kVecThreads, RING = S::RING, P = RING - 1;
   constexpr int EPC = Word<ELEM>::EPC, PP = EPC / 2, ES = ElemSize<ELEM>::value;
   __shared__ float2 xch[2 * T / 32];
-  // [RING][2 tensors][NV][T] (SHIFT: [2 tensors][groups][words of a row]), then the factors: scale gate post_gamma, pre_gamma,
-  // scale gate post_beta, pre_beta
+  // [RING][2 tensors][NV][T] (SHIFT: [2 tensors][groups][words of a row]), then the factors: gate post_gamma, pre_gamma,
+  // gate post_beta, pre_beta (the scale is left to the sum with the residual, which then rounds once)
   extern __shared__ uint4 ring[];
   const int g = threadIdx.x / TPR, t = threadIdx.x % TPR;
   pdl_wait();
@@ -234,10 +234,10 @@ __global__ void __launch_bounds__(kVecThreads, 1) join_fwd_vec_kernel(const Join
   const DropKey key = drop_key(p.drop);
   if constexpr (!S::MAKE) {
     uint4* fput = ring + RING * SB / 16;
-    put_factors<T, TPR, NV, EPC>(fput, 0, p.gate, p.g1, p.param_elem, p.scale, 1.f, p.D);
+    put_factors<T, TPR, NV, EPC>(fput, 0, p.gate, p.g1, p.param_elem, 1.f, 1.f, p.D);
     if (p.g2) put_factors<T, TPR, NV, EPC>(fput, 1, p.g2, nullptr, p.param_elem, 1.f, 0.f, p.D);
     if constexpr (FULL) {
-      put_factors<T, TPR, NV, EPC>(fput, 2, p.b1, p.gate, p.param_elem, p.scale, 0.f, p.D);
+      put_factors<T, TPR, NV, EPC>(fput, 2, p.b1, p.gate, p.param_elem, 1.f, 0.f, p.D);
       put_factors<T, TPR, NV, EPC>(fput, 3, p.b2, nullptr, p.param_elem, 1.f, 0.f, p.D);
     }
     __syncthreads();
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kVecThreads, 1) join_fwd_vec_kernel(const Join
         uint64_t a[PP];
         params_or<EPC>(p.gate, p.param_elem, cc, 1.f, a);
 #pragma unroll
-        for (int i = 0; i < PP; ++i) f[i] = mul_2(mul_2(a[i], pk(p.scale, p.scale)), f[i]);
+        for (int i = 0; i < PP; ++i) f[i] = mul_2(a[i], f[i]);
       }
       if (c >= p.D) {
 #pragma unroll
@@ -262,6 +262,7 @@ __global__ void __launch_bounds__(kVecThreads, 1) join_fwd_vec_kernel(const Join
     }
   };
   const float inv_d = 1.0f / (float)p.D;
+  const uint64_t scale2 = pk(p.scale, p.scale);
   int turn = 0;
   uint32_t slot = mine, last = mine + P * SB;  // the row's slot; the one read before it, filled next
   uint8_t* hp = static_cast<uint8_t*>(p.h) + row * p.ldh * ES + t * 16;
@@ -368,7 +369,7 @@ __global__ void __launch_bounds__(kVecThreads, 1) join_fwd_vec_kernel(const Join
         unpack_word<ELEM>(lds16(slot + TB + j * WB), r);
       }
 #pragma unroll
-      for (int k = 0; k < PP; ++k) v[j][k] = add_2(v[j][k], r[k]);  // zeros past D
+      for (int k = 0; k < PP; ++k) v[j][k] = fma_2(v[j][k], scale2, r[k]);  // zeros past D
       const uint4 u = pack_word<ELEM>(v[j]);
       unpack_word<ELEM>(u, v[j]);  // normalised as it is kept
       if constexpr (SHIFT) write_shifted<ELEM, TPR>(hp - t * 16, (t + TPR * j) * EPC, p.D, t, active, u);
