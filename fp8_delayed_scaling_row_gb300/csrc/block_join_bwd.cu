@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(T, 1) join_bwd_vec_kernel(const JoinBwdParams 
     uint32_t draws[NV][PP];  // drawn ahead of the sums, beside whose exchanges they cost least
     if (p.drop.cut) {
 #pragma unroll
-      for (int j = 0; j < NV; ++j) word_draws<EPC>(key, (t + TPR * j) * EPC, (uint32_t)row, draws[j]);
+      for (int j = 0; j < NV; ++j) word_draws<EPC, SHIFT>(key, (t + TPR * j) * EPC, p.D, (uint32_t)row, draws[j]);
     }
     uint64_t rs2 = 0, mu2 = 0, m1 = 0, m2 = 0;
     if (p.g2) {
@@ -673,7 +673,7 @@ __global__ void __launch_bounds__(512, 1) join_bwd_wide_kernel(const JoinBwdPara
       if (p.dres && in) *reinterpret_cast<uint4*>(dr + c) = pack_word<ELEM>(d[j]);
       if (p.drop.cut) {
         uint32_t draws[PP];
-        word_draws<EPC>(key, c, (uint32_t)row, draws);
+        word_draws<EPC>(key, c, p.D, (uint32_t)row, draws);
 #pragma unroll
         for (int k = 0; k < PP; ++k) d[j][k] = drop_pair(d[j][k], draws[k], key.cutw);
       }

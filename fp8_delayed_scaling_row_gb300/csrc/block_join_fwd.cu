@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kVecThreads, 1) join_fwd_vec_kernel(const Join
     uint32_t draws[NV][PP];  // drawn ahead of the sums, beside whose exchanges they cost least
     if (p.drop.cut) {
 #pragma unroll
-      for (int j = 0; j < NV; ++j) word_draws<EPC>(key, (t + TPR * j) * EPC, (uint32_t)row, draws[j]);
+      for (int j = 0; j < NV; ++j) word_draws<EPC, SHIFT>(key, (t + TPR * j) * EPC, p.D, (uint32_t)row, draws[j]);
     }
     uint64_t rs2 = pk(1.f, 1.f);
     if (p.g1) {

@@ -1,0 +1,58 @@
+"""block_join and dropout where they can go wrong at the edges (GPU). Bounds as in test_gpu_block_join.py."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+import draws64 as D  # noqa: E402
+import plain64 as P  # noqa: E402
+from test_gpu_block_join import ALL, DTYPES, EPS, U, draw, normed, rounded, vectors  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def L():
+    from fp8_delayed_scaling_row_gb300 import lnfp8
+    return lnfp8
+
+
+ROWS_DROPPED = [pytest.param(dt, C, norm, names, id=f"{str(dt)[6:]}-{C}-{norm}") for dt in DTYPES for C in (1, 7, 8, 24, 40)
+                for norm, names in (("rms", ("post_gamma", "pre_gamma")), ("layer", ALL))]
+
+
+def dropped_rows(M, C, p, seed):
+    none = ~D.keep(M, C, p, seed, 0, 0).any(1).cuda()
+    assert 4 <= int(none.sum()) < M
+    return none
+
+
+@pytest.mark.parametrize("dtype,C,norm,names", ROWS_DROPPED)
+def test_a_row_whose_elements_are_all_dropped_is_the_residual(L, dtype, C, norm, names):
+    """x's rows are NaN throughout once normalised, and count for nothing where they are dropped."""
+    M, p, layer = 600, 0.9, norm == "layer"
+    x, r = draw(M, C, dtype, 1), draw(M, C, dtype, 2)
+    x[:, C // 2] = math.nan
+    vec, none = vectors(C, names, dtype), dropped_rows(M, C, p, 13)
+    h, y, ctx = L.block_join_fwd(x, r, norm=norm, p=p, rng=L.dropout_rng(13), eps=EPS, **vec)
+    assert torch.equal(h[none], r[none]) and h[~none].isnan().any(1).all() and y[~none].isnan().all()
+    hh, rs, mu, ehh, ers, emu = normed(h[none].double(), torch.zeros_like(h[none], dtype=torch.float64), layer)
+    P.assert_within(ctx.pre_rsigma[none][:, None], rs, ers + U * rs, "pre_rsigma")
+    if layer:
+        P.assert_within(ctx.pre_mu[none][:, None], mu, emu + U * mu.abs(), "pre_mu")
+    g2, b2 = vec["pre_gamma"].double(), vec.get("pre_beta", 0 * vec["pre_gamma"]).double()
+    want = hh * g2 + b2
+    P.assert_within(y[none], want, rounded(want, ehh * g2.abs() + 2 * U * ((hh * g2).abs() + b2.abs()), dtype), "y")
+
+
+@pytest.mark.parametrize("dtype,C,norm,names", ROWS_DROPPED)
+def test_a_row_whose_elements_are_all_dropped_has_no_gradient(L, dtype, C, norm, names):
+    """The gradient of h is NaN throughout, and dx of a row that is dropped is exactly zero."""
+    M, p = 600, 0.9
+    x, r, dh, dy = (draw(M, C, dtype, s) for s in (1, 2, 3, 4))
+    vec, none = vectors(C, names, dtype), dropped_rows(M, C, p, 13)
+    ctx = L.block_join_fwd(x, r, norm=norm, p=p, rng=L.dropout_rng(13), eps=EPS, **vec)[2]
+    dy[:, C // 2] = math.nan
+    g = L.block_join_bwd(dh, dy, ctx, **vec)
+    assert g.dresidual.isnan().all()
+    assert (g.dx[none] == 0).all() and g.dx[~none].isnan().all()
