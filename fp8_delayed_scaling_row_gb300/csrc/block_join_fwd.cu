@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 ? 2 : 1) joi
       const int c = tc + (i < n ? TPR * i : 0);
       const float f = p.scale * param_or(p.gate, p.param_elem, c, 1.f);
       fa[i] = f * param_or(p.g1, p.param_elem, c, 1.f);
-      fc[i] = f * param_or(p.b1, p.param_elem, c, 0.f);
+      fc[i] = p.b1 ? f * param_or(p.b1, p.param_elem, c, 0.f) : 0.f;  // no beta: none of a gate that may be infinite
       fg[i] = param_or(p.g2, p.param_elem, c, 0.f);
       fb[i] = param_or(p.b2, p.param_elem, c, 0.f);
     }
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kVecThreads, 1) join_fwd_vec_kernel(const Join
     put_factors<T, TPR, NV, EPC>(fput, 0, p.gate, p.g1, p.param_elem, 1.f, 1.f, p.D);
     if (p.g2) put_factors<T, TPR, NV, EPC>(fput, 1, p.g2, nullptr, p.param_elem, 1.f, 0.f, p.D);
     if constexpr (FULL) {
-      put_factors<T, TPR, NV, EPC>(fput, 2, p.b1, p.gate, p.param_elem, 1.f, 0.f, p.D);
+      put_factors<T, TPR, NV, EPC>(fput, 2, p.b1, p.b1 ? p.gate : nullptr, p.param_elem, 1.f, 0.f, p.D);  // no beta: none of a gate that may be infinite
       put_factors<T, TPR, NV, EPC>(fput, 3, p.b2, nullptr, p.param_elem, 1.f, 0.f, p.D);
     }
     __syncthreads();
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kVecThreads, 1) join_fwd_vec_kernel(const Join
     } else {
       const int c = (t + TPR * j) * EPC, cc = c < p.D ? c : 0;
       params_or<EPC>(k == 0 ? p.g1 : k == 1 ? p.g2 : k == 2 ? p.b1 : p.b2, p.param_elem, cc, k == 0 ? 1.f : 0.f, f);
-      if (k == 0 || k == 2) {
+      if (k == 0 || (k == 2 && p.b1)) {
         uint64_t a[PP];
         params_or<EPC>(p.gate, p.param_elem, cc, 1.f, a);
 #pragma unroll

@@ -56,3 +56,20 @@ def test_a_row_whose_elements_are_all_dropped_has_no_gradient(L, dtype, C, norm,
     g = L.block_join_bwd(dh, dy, ctx, **vec)
     assert g.dresidual.isnan().all()
     assert (g.dx[none] == 0).all() and g.dx[~none].isnan().all()
+
+
+@pytest.mark.parametrize("dtype,C", [(torch.bfloat16, 64), (torch.float16, 65), (torch.bfloat16, 8200), (torch.bfloat16, 8201),
+                                     (torch.float32, 64), (torch.float32, 65), (torch.float32, 8196)])
+@pytest.mark.parametrize("post", [False, True])
+def test_an_infinite_gate_without_a_beta(L, dtype, C, post):
+    """gate x is infinite in that column with the sign of x, and nothing else of h changes."""
+    M, at = 20, C // 2
+    x, r = draw(M, C, dtype, 1), draw(M, C, dtype, 2)
+    x[:, at] = torch.where(torch.arange(M, device="cuda") % 2 == 0, 2.0, -3.0).to(dtype)
+    vec = vectors(C, ("gate", "pre_gamma", "pre_beta") + (("post_gamma",) if post else ()), dtype)
+    vec["gate"][at] = 1.0
+    want = L.block_join_fwd(x, r, norm="layer", **vec)[0]
+    vec["gate"][at] = math.inf
+    h = L.block_join_fwd(x, r, norm="layer", **vec)[0]
+    assert torch.equal(h[:, at], torch.where(x[:, at] > 0, math.inf, -math.inf).to(dtype))
+    assert torch.equal(h[:, :at], want[:, :at]) and torch.equal(h[:, at + 1 :], want[:, at + 1 :])
