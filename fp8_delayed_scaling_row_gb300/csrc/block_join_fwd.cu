@@ -528,7 +528,7 @@ lnfp8_status fwd(const JoinFwdParams& p, cudaStream_t st) {
 }  // namespace
 
 lnfp8_status block_join_fwd_launch(const lnfp8_block_join_fwd_args* a, cudaStream_t st) {
-  if (a->M == 0) return LNFP8_OK;
+  if (a->M == 0) return drop_save_launch(a->drop, "block_join_fwd", st);
   JoinFwdParams p = {};
   p.x = a->x;
   p.resid = a->residual;

@@ -186,9 +186,15 @@ lnfp8_status dropout(const DropoutParams& p, cudaStream_t st) {
 
 }  // namespace
 
+lnfp8_status drop_save_launch(const lnfp8_dropout& d, const char* who, cudaStream_t st) {
+  if (!d.rng || !d.rng_saved) return LNFP8_OK;
+  if (cudaMemcpyAsync(d.rng_saved, d.rng, 2 * sizeof(int64_t), cudaMemcpyDeviceToDevice, st) != cudaSuccess) return check_launch(who);
+  return LNFP8_OK;
+}
+
 lnfp8_status dropout_launch(const void* x, int elem, int64_t rows, int64_t cols, int64_t ldx, const lnfp8_dropout& d, void* y,
                             int64_t ldy, cudaStream_t st) {
-  if (rows == 0) return LNFP8_OK;
+  if (rows == 0) return drop_save_launch(d, "dropout_apply", st);
   DropoutParams p = {};
   p.x = x;
   p.y = y;

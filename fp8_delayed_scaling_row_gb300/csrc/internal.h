@@ -187,6 +187,8 @@ lnfp8_status colsum_launch(const float* part, int n, int cols, int split, float*
 
 // Of 65536 draws, how many drop an element.
 inline uint32_t drop_threshold(double p) { return (uint32_t)(p * 65536.0 + 0.5); }
+// The backward's copy of rng of a call without rows, which launches no kernel that could make it.
+lnfp8_status drop_save_launch(const lnfp8_dropout& d, const char* who, cudaStream_t st);
 lnfp8_status dropout_launch(const void* x, int elem, int64_t rows, int64_t cols, int64_t ldx, const lnfp8_dropout& d, void* y,
                             int64_t ldy, cudaStream_t st);
 lnfp8_status block_join_fwd_launch(const lnfp8_block_join_fwd_args* a, cudaStream_t st);

@@ -73,3 +73,25 @@ def test_an_infinite_gate_without_a_beta(L, dtype, C, post):
     h = L.block_join_fwd(x, r, norm="layer", **vec)[0]
     assert torch.equal(h[:, at], torch.where(x[:, at] > 0, math.inf, -math.inf).to(dtype))
     assert torch.equal(h[:, :at], want[:, :at]) and torch.equal(h[:, at + 1 :], want[:, at + 1 :])
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_without_rows_keep_a_copy_of_rng(L, captured):
+    """The context's copy is what the call read, whatever its memory held before."""
+    x = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
+    rng = L.dropout_rng(1234, step=5)
+
+    def calls():
+        junk = [torch.full((2,), -7, dtype=torch.int64, device="cuda") for _ in range(8)]
+        del junk
+        return L.dropout_fwd(x, 0.5, rng)[1].rng, L.block_join_fwd(x, x, p=0.5, rng=rng)[2].rng
+
+    if not captured:
+        got = calls()
+    else:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = calls()
+        rng[1] += 1
+        graph.replay()
+    assert all(torch.equal(g, rng) for g in got)
