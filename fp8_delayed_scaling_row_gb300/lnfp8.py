@@ -1285,7 +1285,8 @@ NORMS = {"rms": 0, "layer": 1}
 @dataclass
 class BlockJoinCtx:
     """What block_join_bwd needs of its forward: x (with a norm of it, or a gate), h (with the norm behind it), their
-    statistics, and the dropout's probability, (seed, step) and site."""
+    statistics, the dropout's probability, (seed, step) and site, and whether there was a post_beta and a gate (None: not known,
+    and the backward takes the vectors that it is given)."""
     x: torch.Tensor | None = None
     h: torch.Tensor | None = None
     norm: str = "rms"
@@ -1297,6 +1298,8 @@ class BlockJoinCtx:
     post_rsigma: torch.Tensor | None = None
     pre_mu: torch.Tensor | None = None
     pre_rsigma: torch.Tensor | None = None
+    post_beta: bool | None = None
+    gate: bool | None = None
 
 
 def _norm(norm) -> int:
@@ -1369,7 +1372,7 @@ def block_join_fwd(x, residual=None, *, norm="rms", post_gamma=None, post_beta=N
                       b2, drop, h.data_ptr(), yp, m1p, r1p, m2p, r2p, ldx, ldr, ldh, ldy)
     _check(_c_block_join_fwd(C.byref(a), _raw_stream(dev)))
     return h, y, BlockJoinCtx(x if g1 is not None or gt is not None else None, h if g2 is not None else None, norm, scale, p, kept, site,
-                              m1, r1, m2, r2)
+                              m1, r1, m2, r2, b1 is not None, gt is not None)
 
 
 @dataclass
@@ -1420,7 +1423,8 @@ def _kept_rows(name, row, M, D, dt, dev):
 def block_join_bwd(dh, dy, ctx: BlockJoinCtx, *, post_gamma=None, post_beta=None, gate=None, pre_gamma=None, pre_beta=None,
                    grads: BlockJoinGrads | None = None, stream=None) -> BlockJoinGrads:
     """Gradients of block_join_fwd from those of h (dh, None: zero) and of y (dy, with pre_gamma): dx, dresidual, and in fp32,
-    summed in a fixed order, those of the vectors given, which are the forward's (pre_beta: for its gradient alone)."""
+    summed in a fixed order, those of the vectors given, which are the forward's (pre_beta, and post_beta without a gate: for their
+    gradients alone)."""
     first, name = (dh, "dh") if dh is not None else (dy, "dy")
     if first is None:
         raise ValueError("neither dh nor dy")
@@ -1443,8 +1447,14 @@ def block_join_bwd(dh, dy, ctx: BlockJoinCtx, *, post_gamma=None, post_beta=None
     ldx = ldh = 0
     if g1 is not None:
         m1, r1 = _kept_stats("post", ctx.post_mu, ctx.post_rsigma, kind, M, dev)
+    elif ctx.post_rsigma is not None:
+        raise ValueError("the forward had a post_gamma")
     if g1 is not None or gt is not None:
         xp, ldx = _kept_rows("x", ctx.x, M, D, dt, dev)
+    if ctx.gate is not None and ctx.gate != (gt is not None):
+        raise ValueError("the forward had a gate" if ctx.gate else "the forward had no gate")
+    if gt is not None and ctx.post_beta is not None and ctx.post_beta != (b1 is not None):
+        raise ValueError("dgate needs the forward's post_beta" if ctx.post_beta else "the forward had no post_beta, which would change dgate")
     if g2 is not None:
         m2, r2 = _kept_stats("pre", ctx.pre_mu, ctx.pre_rsigma, kind, M, dev)
         hp, ldh = _kept_rows("h", ctx.h, M, D, dt, dev)

@@ -95,3 +95,34 @@ def test_calls_without_rows_keep_a_copy_of_rng(L, captured):
         rng[1] += 1
         graph.replay()
     assert all(torch.equal(g, rng) for g in got)
+
+
+def test_a_backward_call_takes_the_vectors_of_its_forward(L):
+    """What would give another operator's gradients is refused; a beta's own gradient may be left out where no other needs it, and so
+    may y's part. A context made by hand that does not say which vectors there were is taken as it is."""
+    M, C, dt = 6, 64, torch.bfloat16
+    x, r, dh, dy = (draw(M, C, dt, s) for s in (1, 2, 3, 4))
+    v = vectors(C, ALL, dt)
+    post = {k: v[k] for k in ("post_gamma", "post_beta", "gate")}
+    _, _, ctx = L.block_join_fwd(x, r, norm="layer", **post)
+    want = L.block_join_bwd(dh, None, ctx, **post)
+    for left_out, match in (("post_gamma", "post_gamma"), ("gate", "gate"), ("post_beta", "post_beta")):
+        given = {k: t for k, t in post.items() if k != left_out}
+        if left_out == "post_gamma":
+            del given["post_beta"]
+        with pytest.raises(ValueError, match=match):
+            L.block_join_bwd(dh, None, ctx, **given)
+    by_hand = L.BlockJoinCtx(x, None, "layer", 1.0, 0.0, None, 0, ctx.post_mu, ctx.post_rsigma)
+    got = L.block_join_bwd(dh, None, by_hand, **post)
+    assert torch.equal(got.dx, want.dx) and torch.equal(got.dgate, want.dgate)
+    _, _, ctx = L.block_join_fwd(x, r, post_gamma=v["post_gamma"])
+    with pytest.raises(ValueError, match="gate"):
+        L.block_join_bwd(dh, None, ctx, post_gamma=v["post_gamma"], gate=v["gate"])
+    _, _, ctx = L.block_join_fwd(x, r, post_gamma=v["post_gamma"], gate=v["gate"])
+    with pytest.raises(ValueError, match="post_beta"):
+        L.block_join_bwd(dh, None, ctx, **post)
+    _, _, ctx = L.block_join_fwd(x, r, post_gamma=v["post_gamma"], post_beta=v["post_beta"], pre_gamma=v["pre_gamma"], pre_beta=v["pre_beta"])
+    g = L.block_join_bwd(dh, dy, ctx, post_gamma=v["post_gamma"], pre_gamma=v["pre_gamma"])
+    assert g.dpost_beta is None and g.dpre_beta is None and g.dpost_gamma is not None
+    g = L.block_join_bwd(dh, None, ctx, post_gamma=v["post_gamma"])
+    assert g.dpre_gamma is None and torch.equal(g.dresidual, dh)
