@@ -6,7 +6,7 @@ import pytest
 torch = pytest.importorskip("torch")
 import draws64 as D  # noqa: E402
 import plain64 as P  # noqa: E402
-from test_gpu_block_join import ALL, DTYPES, EPS, U, draw, normed, rounded, vectors  # noqa: E402
+from test_gpu_block_join import ALL, DTYPES, EPS, U, check_bwd, draw, keep_of, normed, rounded, vectors  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -126,3 +126,22 @@ def test_a_backward_call_takes_the_vectors_of_its_forward(L):
     assert g.dpost_beta is None and g.dpre_beta is None and g.dpost_gamma is not None
     g = L.block_join_bwd(dh, None, ctx, post_gamma=v["post_gamma"])
     assert g.dpre_gamma is None and torch.equal(g.dresidual, dh)
+
+
+@pytest.mark.parametrize("dtype,C", [(torch.bfloat16, 64), (torch.bfloat16, 65), (torch.bfloat16, 2048), (torch.bfloat16, 8192), (torch.float32, 768)])
+@pytest.mark.parametrize("M", [1, 700])
+def test_statistics_that_are_not_there_count_as_none(L, M, C, dtype):
+    """The calls without means, or without one of the norms, directly behind one whose rows have means far from zero, which its kernel
+    leaves in the shared memory that theirs takes over."""
+    x, r, dh, dy = (draw(M, C, dtype, s, 1.0, mean) for s, mean in ((1, 20.0), (2, 30.0), (3, 0.0), (4, 0.0)))
+    vec, keep = vectors(C, ALL, dtype), keep_of((M, C), 0.0, 0, 0, 0)
+    before = L.block_join_fwd(x, r, norm="layer", eps=EPS, **vec)[2]
+    calls = [(norm, names) for names in (ALL, ("post_gamma", "post_beta"), ("pre_gamma", "pre_beta"), ("gate", "pre_gamma", "pre_beta"), ("gate",))
+             for norm in ("rms", "layer")]
+    for norm, names in calls:
+        some = {k: v for k, v in vec.items() if k in names}
+        ctx = L.block_join_fwd(x, r, norm=norm, eps=EPS, **some)[2]
+        e = dy if "pre_gamma" in names else None
+        L.block_join_bwd(dh, dy, before, **vec)
+        g = L.block_join_bwd(dh, e, ctx, **some)
+        check_bwd(g, dh, e, ctx, some, keep)
