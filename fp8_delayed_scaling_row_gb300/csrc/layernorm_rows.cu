@@ -494,11 +494,14 @@ ln_bwd_vec_kernel(const LnBwdParams p) {
     }
     cp_commit();
   };
-  // words past D, and the slots of a group that gets no row at all, are read but never filled
+  // words past D, and the slots of a group that gets no row at all, are read but never filled (and only they are zeroed: nothing
+  // orders a copy behind a store of the same thread)
 #pragma unroll
   for (int k = 0; k < RING; ++k) {
-    sts4(base + k * SB + t4, 0u);
-    sts4(base + k * SB + t4 + 4 * T, 0u);
+    if (row >= p.M) {
+      sts4(base + k * SB + t4, 0u);
+      sts4(base + k * SB + t4 + 4 * T, 0u);
+    }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       if ((t + TPR * j) * EPC < p.D && row < p.M) continue;
