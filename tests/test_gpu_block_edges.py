@@ -6,7 +6,7 @@ import pytest
 torch = pytest.importorskip("torch")
 import draws64 as D  # noqa: E402
 import plain64 as P  # noqa: E402
-from test_gpu_block_join import ALL, DTYPES, EPS, U, check_bwd, draw, keep_of, normed, rounded, vectors  # noqa: E402
+from test_gpu_block_join import ALL, DTYPES, EPS, U, back, check_bwd, draw, keep_of, normed, rounded, vectors  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -145,3 +145,54 @@ def test_statistics_that_are_not_there_count_as_none(L, M, C, dtype):
         L.block_join_bwd(dh, dy, before, **vec)
         g = L.block_join_bwd(dh, e, ctx, **some)
         check_bwd(g, dh, e, ctx, some, keep)
+
+
+@pytest.mark.parametrize("C,norm,names", [(8192, "rms", ("post_gamma", "pre_gamma")), (1001, "layer", ALL)])
+def test_column_sums_past_32_bits(L, C, norm, names):
+    """Every row's part in the column sums of more than 2^31 elements: all rows differ, the terms have one sign on average, and the
+    gradients of the rows past 2^31 elements are 2^14 times the others', so that one of these rows (0.5% of the terms' magnitudes at least,
+    a third of it of one sign), or a block's of the others (1 in 152), shows beside the bound (0.09% at most) if it is left out or counted
+    twice."""
+    M, dt, layer = (1 << 31) // C + 70, torch.bfloat16, norm == "layer"
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.empty(M, C, dtype=dt, device="cuda").normal_(1.0, 1.0, generator=gen)
+    vec = vectors(C, names, dt)
+    h, e, ctx = L.block_join_fwd(x, x, norm=norm, eps=EPS, **vec)
+    e.copy_(h)
+    e[(1 << 31) // C :] *= 2.0 ** 14
+    g = L.block_join_bwd(e, e, ctx, **vec)
+    v = {k: t.double() for k, t in vec.items()}
+    n_sum = (M / 152 + 60) * U
+    gate, b1 = v.get("gate", torch.ones(C, dtype=torch.float64, device="cuda")), v.get("post_beta", torch.zeros(C, dtype=torch.float64, device="cuda"))
+    total = {}
+
+    def add(name, t, et, mag=None):
+        part = torch.stack((t.sum(0), (et + n_sum * (t.abs() if mag is None else mag)).sum(0)))
+        total[name] = total[name] + part if name in total else part
+
+    rows = (1 << 25) // C
+    for lo in range(0, M, rows):
+        part = slice(lo, min(M, lo + rows))
+
+        def given(name, t):
+            rs = getattr(ctx, name + "_rsigma")[part][:, None].double()
+            xh = (t[part].double() - (getattr(ctx, name + "_mu")[part][:, None].double() if layer else 0.0)) * rs
+            return xh, 3 * U * xh.abs(), rs
+
+        dy = e[part].double()
+        hh, ehh, rs = given("pre", h)
+        add("dpre_gamma", dy * hh, dy.abs() * ehh)
+        q = dy * v["pre_gamma"]
+        o, eo = back(q, U * q.abs(), hh, ehh, rs, layer)
+        d, ed = dy + o, eo + U * (dy.abs() + o.abs())
+        xh, exh, _ = given("post", x)
+        add("dpost_gamma", d * gate * xh, gate.abs() * (ed * (xh.abs() + exh) + d.abs() * exh) + 2 * U * (d * gate * xh).abs())
+        if layer:
+            add("dpre_beta", dy, 0 * dy)
+            add("dpost_beta", d * gate, ed * gate.abs() + 2 * U * (d * gate).abs())
+            n, en = xh * v["post_gamma"] + b1, exh * v["post_gamma"].abs()
+            pieces = (d * xh * v["post_gamma"]).abs() + (d * b1).abs()  # two sums are added
+            add("dgate", d * n, ed * (n.abs() + en) + d.abs() * en + ed * b1.abs() + 4 * U * pieces, pieces)
+    for name, (want, tol) in total.items():
+        P.assert_within(getattr(g, name), want, tol, name)
+    assert {"d" + n for n in names} == set(total)
