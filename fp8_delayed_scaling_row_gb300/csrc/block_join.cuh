@@ -4,8 +4,9 @@
 //   backward  dH = dh + rs2 (q - [mean(q)] - hhat mean(q hhat)), q = dy g2; dt = s drop'(dH), dn = gate dt,
 //             dx = T(rs1 (u - [mean(u)] - xhat mean(u xhat))), u = dn g1; dr = T(dH)
 //             ([mean]: layer norms only)
-// Each part is optional. All arithmetic is fp32. The forward folds s, gate, 1 / (1 - p), g1 and b1 into one factor and one
-// summand a column: t = xhat a + c where kept. Of column sums the backward needs four at most, since
+// Each part is optional. All arithmetic is fp32. The forward folds gate, g1 and b1 into one factor and one summand a column,
+// gate n = xhat a + c, and s / (1 - p) enters in the sum with r, which then rounds once. (join_fwd_any_kernel folds it into the factor and
+// the summand too, or multiplies vector by vector: its h may be the other neighbour of the vector kernel's for the same row.) Of column sums the backward needs four at most, since
 // dgate = sum dt n = g1 A + b1 B, dg1 = gate A, db1 = gate B with A = sum dt xhat, B = sum dt.
 // This header: what the two kernels of each direction (block_join_fwd.cu, block_join_bwd.cu) share.
 #pragma once
@@ -63,8 +64,8 @@ __device__ __forceinline__ void any_draws(uint16_t* bits, const DropKey& key, in
 // D a multiple of 8 and rows on 16-byte boundaries: thread t of a row's TPR holds its 16-byte words t, t + TPR, ... (EPC
 // columns each), 8 to 32 columns in all, and copies (cp.async) the words of its next RING - 1 rows into its own slots of a ring in
 // shared memory, so that the bytes in flight cost no registers. Bound by HBM: 16384 x 2048 bf16 with two RMS norms and dropout
-// forward 45 us (89% of what a copy of the bytes takes), backward 75 (80%; 71 without dropout). With layer norms, betas and a gate
-// 47 and 87 us (85%, 69%): four reductions a row and four column sums, whose registers leave 8 warps an SM.
+// forward 45 us (90% of what a copy of the bytes takes), backward 76 (79%; 71 without dropout). With layer norms, betas and a gate
+// 47 and 86 us (85%, 70%): four reductions a row and four column sums, whose registers leave 8 warps an SM.
 template <int ELEM>
 struct Word {
   static constexpr int EPC = ELEM == LNFP8_FP32 ? 4 : 8;
@@ -166,9 +167,10 @@ __device__ __forceinline__ void group_meet() {
   else group_sync<TPR>();
 }
 
-// A block has 512 threads, one to an SM, whose row groups share the columns' factors: in fp32 in shared memory, 16 bytes of
-// neighbouring lanes side by side, ready to be used (in registers they cost a block's worth of occupancy, read again as
-// parameters 60 instructions a row). FULL: with means (layer norms) and betas; without them (RMS) rows cost half the instructions.
+// One block to an SM, of 512 threads (backward 256, 384 or 512: bwd_threads), whose row groups share the columns' factors: in fp32
+// in shared memory, 16 bytes of neighbouring lanes side by side, ready to be used (in registers they cost a block's worth of
+// occupancy, read again as parameters 60 instructions a row). FULL: with means (layer norms) and betas; without them (RMS) rows cost
+// half the instructions. Rows on odd boundaries always run as FULL.
 constexpr int kVecThreads = 512;
 constexpr int kVecSmem = 226 * 1024;
 

@@ -1194,7 +1194,10 @@ lnfp8_status linear_act_bwd_launch(const lnfp8_linear_act_bwd_args* a, cudaStrea
 // ------------------------------------------------------------ the gated linear layer
 //   forward   z = x w^T + b (w [2N, K], gate rows first), y = T(act(z_gate) z_up), T(z) kept if asked for
 //   backward  dz_gate = dy z_up act'(z_gate), dz_up = dy act(z_gate), db = sum_rows dz, dx = T(dz w), dw = T(dz^T x)
-// Behind dz the backward is the plain layer's with 2N features.
+// Behind dz the backward is the plain layer's with 2N features. dz goes to the products in the tensors' type, which their instructions
+// ask of both operands: of the error of dx and dw against 64 bits, 2.3e-3 in bf16 and 2.9e-4 in fp16, the roundings of dx and dw
+// alone are 1.7e-3 and 2.1e-4. In fp16 a dz above 65504 is infinite, and one below 2^-14 keeps steps of 2^-24 only, also where dx
+// and dw would be in range; db, summed before, is not affected.
 lnfp8_status linear_glu_fwd_launch(const lnfp8_linear_glu_fwd_args* a, cudaStream_t st) {
   LinGemm g = {};
   g.M = a->M;

@@ -1173,7 +1173,8 @@ def linear_glu_grads(M, K, N, *, dx=True, dw=True, bias=True, dtype=torch.bfloat
 
 def linear_glu_bwd(dy, x, w, ctx: LinearGluCtx, *, dbias=True, grads: LinearGluGrads | None = None, stream=None) -> LinearGluGrads:
     """Gradients of linear_glu_fwd with save="h". Gradients that `grads` leaves None are not computed; without `grads`
-    dbias=False leaves the bias's out; x may be None without dw."""
+    dbias=False leaves the bias's out; x may be None without dw. The gradient of z, dy z_up act'(z_gate) and dy act(z_gate), is rounded to
+    the type for dx and dw: in fp16 it becomes infinite above 65504 and loses bits below 2^-14."""
     elem, ia = _elem(dy, "dy", _ELEM16), _act(ctx.act)
     if dy.dim() != 2 or w.dim() != 2:
         raise ValueError(f"dy and w have shapes {tuple(dy.shape)} and {tuple(w.shape)}: expected two dimensions")
@@ -1377,8 +1378,9 @@ def block_join_fwd(x, residual=None, *, norm="rms", post_gamma=None, post_beta=N
 
 @dataclass
 class BlockJoinGrads:
-    """Gradients of block_join_bwd; those of parts that the forward left out are None. workspace: scratch that the caller
-    keeps from call to call; None: each call takes its own from the current stream's memory and gives it back."""
+    """Gradients of block_join_bwd; those of vectors that the forward left out are None. dresidual, the gradient of the sum h, is
+    computed with or without a residual unless it is None here (block_join_grads(..., dresidual=False)). workspace: scratch that the
+    caller keeps from call to call; None: each call takes its own from the current stream's memory and gives it back."""
     dx: torch.Tensor
     dresidual: torch.Tensor | None = None
     dpost_gamma: torch.Tensor | None = None

@@ -722,6 +722,8 @@ typedef struct {
 /* Backward of linear_glu_fwd, from h: dz_gate = dy * h_up * act'(h_gate), dz_up = dy * act(h_gate)
  * (fp32; rounded to the type for the products, as linear_act_bwd's dz), dbias = sum_rows dz (before that
  * rounding, in a fixed order), dx = T(dz . w), dw = T(dz^T . x). With M = 0, dw and dbias are zero.
+ * dz is a product of three: in fp16 it becomes infinite above 65504 and loses bits below 2^-14, also where dx
+ * and dw themselves would be in range. Scale the gradients so that dy * h_up stays between.
  * The same call gives the same bits. The workspace need not be initialised. */
 lnfp8_status linear_glu_bwd(const lnfp8_linear_glu_bwd_args* args, lnfp8_stream stream);
 
